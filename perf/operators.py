@@ -4,10 +4,10 @@ Operators (q query heads, Hkv KV heads, d = head_dim, P = page_size, gs = group 
 
   tables   qskv.extend_tables      page tables, slot map, positions and touched-page list of one
                                    scheduler step, from the requests' lengths and a list of free pages
-  append   qskv.kv4_append         new tokens' keys and values quantised to 4 bits and stored by slot
-  gather   qskv.kv4_gather         cached tokens read back as values, by slot
-  meta     qskv.kv4_meta_build     element-wise min / max of a page's cached keys (bf16, rounded outwards)
-  decode   qskv.kv4_paged_decode   attention of one query token a sequence over its cached pages, all of
+  append   qskv.kvq_append         new tokens' keys and values quantised to 4 bits and stored by slot
+  gather   qskv.kvq_gather         cached tokens read back as values, by slot
+  meta     qskv.kvq_meta_build     element-wise min / max of a page's cached keys (bf16, rounded outwards)
+  decode   qskv.kvq_paged_decode   attention of one query token a sequence over its cached pages, all of
                                    them or a selected list
 
 Numbers held in 4 bits.  A group of gs neighbouring dims of one token and head, x_0..x_{gs-1}, is stored as
@@ -379,7 +379,7 @@ def prepare(case, seed):
     if "pool" in st:  # the cache as a user holds it: bytes
         st["pool"] = st["pool"].view(torch.uint8)
     if own:
-        size = _qskv().kv4_workspace_size(st["shape"]) if c["op"] == "decode" else 256
+        size = _qskv().kvq_workspace_size(st["shape"]) if c["op"] == "decode" else 256
         if c["op"] == "tables":
             size = _qskv().tables_workspace_size(st["shape"])
         st["workspace"] = torch.zeros(size, dtype=torch.uint8, device="cuda")
@@ -449,8 +449,8 @@ def _run_append(st):
     """Tokens stored, and read back as the values that the cache then stands for."""
     c = st["case"]
     if own:
-        _qskv().kv4_append(st["k"], st["v"], st["slots"], st["pool"], st["shape"], c["gs"], st["workspace"])
-        _qskv().kv4_gather(st["pool"], st["slots"], st["k_out"], st["v_out"], st["shape"], c["gs"], st["workspace"])
+        _qskv().kvq_append(st["k"], st["v"], st["slots"], st["pool"], st["shape"], c["gs"], st["workspace"])
+        _qskv().kvq_gather(st["pool"], st["slots"], st["k_out"], st["v_out"], st["shape"], c["gs"], st["workspace"])
         return {"k": st["k_out"], "v": st["v_out"]}
     _store(c, st["pool"].view(torch.int32), st["slots"], st["k"], st["v"])
     return _run_gather(st)
@@ -459,7 +459,7 @@ def _run_append(st):
 def _run_gather(st):
     c = st["case"]
     if own:
-        _qskv().kv4_gather(st["pool"], st["slots"], st["k_out"], st["v_out"], st["shape"], c["gs"], st["workspace"])
+        _qskv().kvq_gather(st["pool"], st["slots"], st["k_out"], st["v_out"], st["shape"], c["gs"], st["workspace"])
         return {"k": st["k_out"], "v": st["v_out"]}
     pool = st["pool"].view(torch.int32)
     return {"k": _read(c, pool, st["slots"], 0, _dtype(c)), "v": _read(c, pool, st["slots"], 1, _dtype(c))}
@@ -468,7 +468,7 @@ def _run_gather(st):
 def _run_meta(st):
     c = st["case"]
     if own:
-        _qskv().kv4_meta_build(st["pool"], st["page_ids"], st["valid"], st["meta"], st["shape"], c["gs"],
+        _qskv().kvq_meta_build(st["pool"], st["page_ids"], st["valid"], st["meta"], st["shape"], c["gs"],
                                st["workspace"])
         return {"meta": st["meta"]}
     ids = st["page_ids"].long()
@@ -482,7 +482,7 @@ def _run_meta(st):
 def _run_decode(st):
     c = st["case"]
     if own:
-        _qskv().kv4_paged_decode(st["q"], st["pool"], st["page_table"], st["seq_lens"], st["out"], st["shape"], c["gs"],
+        _qskv().kvq_paged_decode(st["q"], st["pool"], st["page_table"], st["seq_lens"], st["out"], st["shape"], c["gs"],
                                  st["workspace"], selected=st.get("selected"), n_selected=st.get("n_selected"),
                                  top_k=c["top_k"], lse=st["lse"])
         return {"out": st["out"], "lse": st["lse"]}
