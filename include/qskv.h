@@ -375,6 +375,133 @@ qskv_status qskv_cascade_paged_decode(const void *q, qskv_dtype q_dtype, const v
                                       float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * The 4-bit paged KV cache: keys and values of a page held as 4-bit codes
+ * with a bf16 scale and minimum per group of dims.  Layout of the pool:
+ *   pool  [num_pool_pages][num_kv_heads][block bytes]   (16-byte aligned)
+ * where a block of P = page_size tokens, d = head_dim, NG = d / group_size
+ * groups and W = d / 8 code words a token is, in 32-bit little-endian words,
+ *   [P][W] key codes | [P][W] value codes | [NG][P] key params | [NG][P] value params
+ * A group x_0 .. x_{group_size-1} of neighbouring dims of one token and head
+ * is held as  m = bf16(min x),  s = bf16((max x - m) / 15) (0 if the quotient
+ * is below 2^-100),  u = clamp(rint((x - m) / s), 0, 15) (0 if s = 0), each
+ * the exact value rounded once (to nearest, ties to even), and stands for
+ * m + s u.  A param word holds s in its low half and m in its high half.
+ * Code word w of a token holds dims 8w..8w+7, dim 8w+k in bits 4k..4k+3.  A
+ * key's word w = 4i + t is stored at place t * (d / 32) + i of its row; a
+ * value's word w = 4c + j of token t at place 4 (c ^ x) + j with
+ * x = (t / 2) % 4 for d = 128, (t / 4) % 2 for d = 64.
+ * group_size: 32, 64 or 128, at most head_dim.  Values must be finite and
+ * below 2^60 in magnitude.
+ *
+ * qskv_kvq_block_bytes: bytes of one block, page_size * (d + 8 NG)
+ * (0 for an unsupported shape or group size).
+ */
+size_t qskv_kvq_block_bytes(const qskv_shape *shape, int32_t group_size);
+
+/*
+ * Stores n_tokens new tokens into the 4-bit cache: key and value i
+ * ([num_kv_heads][head_dim] at k + i * k_stride, v + i * v_stride elements)
+ * quantised into slot slots[i] = page * page_size + place in page.  A
+ * negative slot (a padded place) is skipped.  Slots must differ from one
+ * another: of two tokens with the same slot, which one a word of the slot
+ * holds is unspecified.  Nothing else of the pool is written.
+ *   k, v      bf16 or fp32, 16-byte aligned; strides in elements, multiples of
+ *             16 bytes, so views of a fused projection's output can be passed
+ *   workspace 256 bytes (the error word), as for qskv_kv_meta_build
+ *   shape     num_kv_heads, head_dim, page_size and num_pool_pages are used
+ * Device errors: a slot past the pool is skipped, QSKV_ERR_DEVICE_INDEX.
+ */
+qskv_status qskv_kvq_append(const void *k, const void *v, qskv_dtype kv_dtype, int64_t k_stride, int64_t v_stride,
+                            const int32_t *slots, int32_t n_tokens, void *pool, const qskv_shape *shape,
+                            int32_t group_size, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Reads n_tokens cached tokens back as values: k_out[i], v_out[i]
+ * ([num_kv_heads][head_dim], contiguous, fp32 or bf16) = m + s u of slot
+ * slots[i], computed in fp32 (one rounding) and rounded to out_dtype; zeros
+ * for a negative slot.  Any slots, repeated ones too.
+ * Device errors: a slot past the pool gives zeros, QSKV_ERR_DEVICE_INDEX.
+ */
+qskv_status qskv_kvq_gather(const void *pool, const int32_t *slots, int32_t n_tokens, void *k_out, void *v_out,
+                            qskv_dtype out_dtype, const qskv_shape *shape, int32_t group_size, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/*
+ * Page metadata of the 4-bit cache, for qskv_page_select and
+ * qskv_page_select_approx (bound scorer): as qskv_kv_meta_build, the
+ * element-wise min and max over a page's valid tokens of the cached key
+ * values fp32(m + s u).  meta_dtype fp32: exactly those; bf16: the min
+ * rounded down and the max rounded up, so the bound still holds.
+ * List semantics and device errors of qskv_kv_meta_build, but a negative
+ * page id is a padded entry and skipped silently.
+ */
+qskv_status qskv_kvq_meta_build(const void *pool, const int32_t *page_ids, const int32_t *valid_tokens,
+                                int32_t n_pages, void *meta, qskv_dtype meta_dtype, const qskv_shape *shape,
+                                int32_t group_size, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of qskv_kvq_paged_decode (the other qskv_kvq calls need
+ * 256 and may share it); same rules as qskv_workspace_size. */
+size_t qskv_kvq_workspace_size(const qskv_shape *shape);
+
+/*
+ * Paged decode attention over the 4-bit cache: what qskv_sparse_paged_decode
+ * computes, with keys and values m + s u: all pages when selected is NULL,
+ * else the listed ones.  Same q, page_table, seq_lens, selected, n_selected,
+ * sm_scale, out (fp32) and lse, same device errors; params in slots past
+ * seq_len may hold anything.  Logits, softmax sums and outputs are kept in
+ * fp32 precision (queries and weights enter the matrix instructions as two
+ * fp16 halves each).
+ * batch * num_kv_heads * (top_k or max_pages) must be below 2^31.
+ */
+qskv_status qskv_kvq_paged_decode(const void *q, qskv_dtype q_dtype, const void *pool, const int32_t *page_table,
+                                  const int32_t *seq_lens, const qskv_shape *shape, int32_t group_size,
+                                  const int32_t *selected, const int32_t *n_selected, int32_t top_k, float sm_scale,
+                                  float *out, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Page tables and slot map of one scheduler step.  Request b holds
+ * seq_lens[b] tokens, whose pages page_table names, and brings new_lens[b]
+ * more.  Requests are admitted in order: request b with new_lens[b] > 0 fits
+ * if the new tokens of requests 0..b are at most max_tokens and the pages
+ * they need beyond those they hold are at most n_free.  (So once one does not
+ * fit, no later one that adds tokens does.)  For an admitted request:
+ *   page_table[b][j] = the next of free_pages, in order, for every new page j
+ *   seq_lens_out[b]  = seq_lens[b] + new_lens[b]     (else seq_lens[b])
+ *   slot_map[i], positions[i] of its tokens, i from cu_new[b]: the slot
+ *                      page * page_size + place and the position
+ *   touched_ids[e], touched_valid[e]: every page its new tokens fall into and
+ *                      the tokens that page then holds, by request and page:
+ *                      the list qskv_kv_meta_build or qskv_kvq_meta_build takes
+ * A refused request gets none of these: its page_table row and length stay,
+ * its tokens' slots and positions are -1, and the call flags
+ * QSKV_ERR_DEVICE_INDEX.  Entries of slot_map and positions past the last
+ * token are -1, those of touched_ids past the last page -1 and of
+ * touched_valid 0, so a captured step can run with padded lists.
+ *   cu_new       [batch + 1] prefix sums of the new_lens (negative ones count
+ *                as 0), at most max_tokens
+ *   counts       [4] or NULL: tokens (cu_new[batch]), pages taken from the
+ *                head of free_pages, touched pages, refused requests
+ *   positions, touched_ids and touched_valid may be NULL
+ *   max_tokens   length of slot_map and positions
+ *   max_touched  length of touched_ids and touched_valid, at least
+ *                min(max_tokens, max_tokens / page_size + 2 batch)
+ * Uses batch, page_size, max_pages and num_pool_pages of the shape.  No
+ * output may overlap an input or another output.
+ * Device errors: a length outside [0, max_pages * page_size] (before or after)
+ * refuses that request; a page id outside the pool (in the free list or the
+ * table) gives its tokens slot -1 and its touched entry -1; both flag
+ * QSKV_ERR_DEVICE_INDEX.
+ * Workspace: qskv_tables_workspace_size bytes, 256-byte aligned, zeroed once.
+ */
+size_t qskv_tables_workspace_size(const qskv_shape *shape);
+
+qskv_status qskv_extend_tables(const int32_t *seq_lens, const int32_t *new_lens, const int32_t *free_pages,
+                               int32_t n_free, int32_t *page_table, const qskv_shape *shape, int32_t *seq_lens_out,
+                               int32_t *cu_new, int32_t *slot_map, int32_t *positions, int32_t max_tokens,
+                               int32_t *touched_ids, int32_t *touched_valid, int32_t max_touched, int32_t *counts,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Synchronises `stream`, reads and clears the workspace's device error flags,
  * and returns QSKV_OK, QSKV_ERR_DEVICE_INDEX, QSKV_ERR_DEVICE_TIMEOUT or
  * QSKV_ERR_CUDA.  The only call that blocks the host.

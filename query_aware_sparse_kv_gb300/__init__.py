@@ -18,14 +18,23 @@ in include/qskv.h); this package is its binding:
                        prefix once per KV head on the tensor cores, the rest
                        paged, LSE merge
 
+  extend_tables        page tables, slot map and touched pages of a
+                       scheduler step, from lengths and a free-page list
+  kvq_append,          the KV cache in 4 bits (bf16 scale and minimum per
+  kvq_gather,            group of dims): tokens stored by slot, read back as
+  kvq_meta_build,        values, page metadata for the selection calls, and
+  kvq_paged_decode       the decode over it (all pages or selected ones)
+
 plus ``PagedDecoder`` (buffer plumbing for a whole step) and ``workloads``
 (seeded synthetic inputs).  Nothing here computes on the CPU: without the
 built library every call raises.
 """
 from .binding import (QSKV_BF16, QSKV_F32, QskvError, QskvLibraryMissing, Shape, cascade_paged_decode,
-                      cascade_workspace_size, get_error, kv_centroid_build, kv_meta_build, last_error_message, load,
-                      make_shape, page_select, page_select_approx, page_select_refresh, page_select_centroid,
-                      select_decode, sparse_paged_decode, sparse_paged_decode_noalloc, workspace_size)
+                      cascade_workspace_size, extend_tables, get_error, kv_centroid_build, kv_meta_build,
+                      kvq_append, kvq_block_bytes, kvq_gather, kvq_meta_build, kvq_paged_decode, kvq_workspace_size,
+                      last_error_message, load, make_shape, page_select, page_select_approx, page_select_refresh, page_select_centroid,
+                      select_decode, sparse_paged_decode, sparse_paged_decode_noalloc, tables_workspace_size,
+                      workspace_size)
 from .engine import PagedDecoder, from_inputs
 
 __all__ = ["QSKV_BF16", "QSKV_F32", "QskvError", "QskvLibraryMissing", "Shape", "cascade_paged_decode",
@@ -33,4 +42,6 @@ __all__ = ["QSKV_BF16", "QSKV_F32", "QskvError", "QskvLibraryMissing", "Shape", 
            "last_error_message", "load", "make_shape", "page_select", "page_select_refresh", "select_decode",
            "sparse_paged_decode",
            "sparse_paged_decode_noalloc", "workspace_size",
+           "extend_tables", "kvq_append", "kvq_block_bytes", "kvq_gather", "kvq_meta_build", "kvq_paged_decode",
+           "kvq_workspace_size", "tables_workspace_size",
            "PagedDecoder", "from_inputs"]

@@ -25,7 +25,9 @@ STATUS = {0: "QSKV_OK", 1: "QSKV_ERR_INVALID_ARG", 2: "QSKV_ERR_UNSUPPORTED", 3:
 EXPORTS = ("qskv_workspace_size", "qskv_kv_meta_build", "qskv_page_select", "qskv_page_select_refresh",
            "qskv_kv_centroid_build", "qskv_page_select_centroid", "qskv_page_select_approx",
            "qskv_sparse_paged_decode", "qskv_select_decode", "qskv_sparse_paged_decode_noalloc",
-           "qskv_cascade_workspace_size", "qskv_cascade_paged_decode", "qskv_get_error", "qskv_status_string",
+           "qskv_cascade_workspace_size", "qskv_cascade_paged_decode", "qskv_kvq_block_bytes", "qskv_kvq_append",
+           "qskv_kvq_gather", "qskv_kvq_meta_build", "qskv_kvq_workspace_size", "qskv_kvq_paged_decode",
+           "qskv_tables_workspace_size", "qskv_extend_tables", "qskv_get_error", "qskv_status_string",
            "qskv_last_error_message")
 
 
@@ -93,6 +95,25 @@ def load(path: str = LIB_PATH):
     lib.qskv_cascade_paged_decode.restype = ctypes.c_int
     lib.qskv_cascade_paged_decode.argtypes = [vp, ctypes.c_int, vp, vp, ctypes.c_int, i32p, i32p, sp, i32,
                                               ctypes.c_float, f32p, f32p, vp, sz, vp]
+    i64 = ctypes.c_int64
+    lib.qskv_kvq_block_bytes.restype = sz
+    lib.qskv_kvq_block_bytes.argtypes = [sp, i32]
+    lib.qskv_kvq_append.restype = ctypes.c_int
+    lib.qskv_kvq_append.argtypes = [vp, vp, ctypes.c_int, i64, i64, i32p, i32, vp, sp, i32, vp, sz, vp]
+    lib.qskv_kvq_gather.restype = ctypes.c_int
+    lib.qskv_kvq_gather.argtypes = [vp, i32p, i32, vp, vp, ctypes.c_int, sp, i32, vp, sz, vp]
+    lib.qskv_kvq_meta_build.restype = ctypes.c_int
+    lib.qskv_kvq_meta_build.argtypes = [vp, i32p, i32p, i32, vp, ctypes.c_int, sp, i32, vp, sz, vp]
+    lib.qskv_kvq_workspace_size.restype = sz
+    lib.qskv_kvq_workspace_size.argtypes = [sp]
+    lib.qskv_kvq_paged_decode.restype = ctypes.c_int
+    lib.qskv_kvq_paged_decode.argtypes = [vp, ctypes.c_int, vp, i32p, i32p, sp, i32, i32p, i32p, i32, ctypes.c_float,
+                                          f32p, f32p, vp, sz, vp]
+    lib.qskv_tables_workspace_size.restype = sz
+    lib.qskv_tables_workspace_size.argtypes = [sp]
+    lib.qskv_extend_tables.restype = ctypes.c_int
+    lib.qskv_extend_tables.argtypes = [i32p, i32p, i32p, i32, i32p, sp, i32p, i32p, i32p, i32p, i32, i32p, i32p, i32,
+                                       i32p, vp, sz, vp]
     lib.qskv_get_error.restype = ctypes.c_int
     lib.qskv_get_error.argtypes = [vp, vp]
     lib.qskv_status_string.restype = ctypes.c_char_p
@@ -267,6 +288,178 @@ def cascade_paged_decode(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Te
                                             _ptr(page_table), _ptr(seq_lens), ctypes.byref(shape), int(prefix_pages),
                                             float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace),
                                             workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# -- the 4-bit paged KV cache and the page tables -------------------------------
+# These calls check what a raw pointer cannot show (device, type, shape, layout)
+# and run on the tensors' own device.
+
+_I32 = torch.int32
+
+
+def _tensor(name: str, t, dtype, shape, device: torch.device):
+    """Pointer of a contiguous tensor of the given type and shape on `device`
+    (None: an optional one left out); q, out and lse may also be pinned host
+    memory."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} (got {t.dtype} {tuple(t.shape)})")
+    if t.device != device and (device.type != "cuda" or name not in ("q", "out", "lse") or not t.is_pinned()):
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device(name: str, t: torch.Tensor) -> torch.device:
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
+    return t.device
+
+
+def _workspace(t: torch.Tensor, device: torch.device):
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous and on {device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _run(fn, device: torch.device, args, stream):
+    """The call on `device`, on its current stream unless one is given."""
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(stream))
+    if st != 0:
+        raise QskvError(st, _lib.qskv_last_error_message().decode())
+
+
+def _pool_ptr(pool: torch.Tensor, shape: Shape, group_size: int, device: torch.device):
+    P, d = shape.page_size, shape.head_dim
+    block = P * (d + 8 * (d // max(int(group_size), 1)))
+    return _tensor("pool", pool, torch.uint8, (shape.num_pool_pages, shape.num_kv_heads, block), device)
+
+
+def kvq_block_bytes(shape: Shape, group_size: int) -> int:
+    """Bytes of one (page, KV head) block of the 4-bit cache: the pool is
+    uint8 [num_pool_pages][num_kv_heads][kvq_block_bytes]."""
+    n = load().qskv_kvq_block_bytes(ctypes.byref(shape), int(group_size))
+    if n == 0:
+        raise QskvError(2, load().qskv_last_error_message().decode())
+    return int(n)
+
+
+def kvq_workspace_size(shape: Shape) -> int:
+    n = load().qskv_kvq_workspace_size(ctypes.byref(shape))
+    if n == 0:
+        raise QskvError(1, load().qskv_last_error_message().decode())
+    return int(n)
+
+
+def tables_workspace_size(shape: Shape) -> int:
+    n = load().qskv_tables_workspace_size(ctypes.byref(shape))
+    if n == 0:
+        raise QskvError(1, load().qskv_last_error_message().decode())
+    return int(n)
+
+
+def _rows(name: str, t: torch.Tensor, dtype, n: int, heads: int, d: int, device: torch.device) -> int:
+    if t.dtype != dtype or t.shape != (n, heads, d):
+        raise ValueError(f"{name} must be {dtype} {(n, heads, d)} (got {t.dtype} {tuple(t.shape)})")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    sn, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and heads > 1):
+        raise ValueError(f"the heads and dims of {name} must be contiguous (strides {t.stride()})")
+    return t.data_ptr()
+
+
+def kvq_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor, shape: Shape,
+               group_size: int, workspace: torch.Tensor, stream=None):
+    """Quantise the tokens k, v [n][Hkv][d] (bf16 or fp32, any token stride of
+    whole 16 bytes) into the 4-bit pool's slots [n] int32 (negative: skipped)."""
+    lib = _lib or load()
+    dev = _device("pool", pool)
+    n, heads, d = slots.numel(), shape.num_kv_heads, shape.head_dim
+    args = (_rows("k", k, k.dtype, n, heads, d, dev), _rows("v", v, k.dtype, n, heads, d, dev), _dtype(k),
+            k.stride(0), v.stride(0), _tensor("slots", slots, _I32, (n,), dev), n,
+            _pool_ptr(pool, shape, group_size, dev), ctypes.byref(shape), group_size, *_workspace(workspace, dev))
+    _run(lib.qskv_kvq_append, dev, args, stream)
+
+
+def kvq_gather(pool: torch.Tensor, slots: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, shape: Shape,
+               group_size: int, workspace: torch.Tensor, stream=None):
+    """The cached tokens of `slots` [n] int32 as values, into k_out, v_out
+    [n][Hkv][d] (bf16 or fp32; zeros for a negative slot)."""
+    lib = _lib or load()
+    dev = _device("pool", pool)
+    n = slots.numel()
+    full = (n, shape.num_kv_heads, shape.head_dim)
+    args = (_pool_ptr(pool, shape, group_size, dev), _tensor("slots", slots, _I32, (n,), dev), n,
+            _tensor("k_out", k_out, k_out.dtype, full, dev), _tensor("v_out", v_out, k_out.dtype, full, dev),
+            _dtype(k_out), ctypes.byref(shape), group_size, *_workspace(workspace, dev))
+    _run(lib.qskv_kvq_gather, dev, args, stream)
+
+
+def kvq_meta_build(pool: torch.Tensor, page_ids: torch.Tensor, valid_tokens: torch.Tensor, meta: torch.Tensor,
+                   shape: Shape, group_size: int, workspace: torch.Tensor, stream=None):
+    """Min / max of the cached keys of the listed pages into meta
+    [Npool][Hkv][2][d] (fp32, or bf16 rounded outwards); negative ids are
+    skipped."""
+    lib = _lib or load()
+    dev = _device("pool", pool)
+    n = page_ids.numel()
+    full = (shape.num_pool_pages, shape.num_kv_heads, 2, shape.head_dim)
+    args = (_pool_ptr(pool, shape, group_size, dev), _tensor("page_ids", page_ids, _I32, (n,), dev),
+            _tensor("valid_tokens", valid_tokens, _I32, (n,), dev), n, _tensor("meta", meta, meta.dtype, full, dev),
+            _dtype(meta), ctypes.byref(shape), group_size, *_workspace(workspace, dev))
+    _run(lib.qskv_kvq_meta_build, dev, args, stream)
+
+
+def kvq_paged_decode(q: torch.Tensor, pool: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                     out: torch.Tensor, shape: Shape, group_size: int, workspace: torch.Tensor,
+                     selected: Optional[torch.Tensor] = None, n_selected: Optional[torch.Tensor] = None,
+                     top_k: int = 0, lse: Optional[torch.Tensor] = None, sm_scale: float = 0.0, stream=None):
+    """sparse_paged_decode over the 4-bit cache (kvq_workspace_size bytes of
+    workspace)."""
+    lib = _lib or load()
+    dev = _device("pool", pool)
+    B, Hq, Hkv, d = shape.batch, shape.num_q_heads, shape.num_kv_heads, shape.head_dim
+    if selected is not None and n_selected is None:
+        raise ValueError("with a selected list, n_selected must be given")
+    args = (_tensor("q", q, q.dtype, (B, Hq, d), dev), _dtype(q), _pool_ptr(pool, shape, group_size, dev),
+            _tensor("page_table", page_table, _I32, (B, shape.max_pages), dev),
+            _tensor("seq_lens", seq_lens, _I32, (B,), dev), ctypes.byref(shape), group_size,
+            _tensor("selected", selected, _I32, (B, Hkv, top_k), dev),
+            _tensor("n_selected", n_selected, _I32, (B, Hkv), dev), top_k, sm_scale,
+            _tensor("out", out, torch.float32, (B, Hq, d), dev), _tensor("lse", lse, torch.float32, (B, Hq), dev),
+            *_workspace(workspace, dev))
+    _run(lib.qskv_kvq_paged_decode, dev, args, stream)
+
+
+def extend_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, page_table: torch.Tensor,
+                  seq_lens_out: torch.Tensor, cu_new: torch.Tensor, slot_map: torch.Tensor, shape: Shape,
+                  workspace: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                  touched_ids: Optional[torch.Tensor] = None, touched_valid: Optional[torch.Tensor] = None,
+                  counts: Optional[torch.Tensor] = None, stream=None):
+    """Page tables, slot map, positions and touched pages of one scheduler
+    step (int32 tensors; see qskv_extend_tables in include/qskv.h).
+    len(slot_map) is the token capacity, len(touched_ids) the page capacity."""
+    lib = _lib or load()
+    dev = _device("page_table", page_table)
+    B, T = shape.batch, slot_map.numel()
+    E = 0 if touched_ids is None else touched_ids.numel()
+    n_free = free_pages.numel()
+    args = (_tensor("seq_lens", seq_lens, _I32, (B,), dev), _tensor("new_lens", new_lens, _I32, (B,), dev),
+            _tensor("free_pages", free_pages, _I32, (n_free,), dev), n_free,
+            _tensor("page_table", page_table, _I32, (B, shape.max_pages), dev), ctypes.byref(shape),
+            _tensor("seq_lens_out", seq_lens_out, _I32, (B,), dev), _tensor("cu_new", cu_new, _I32, (B + 1,), dev),
+            _tensor("slot_map", slot_map, _I32, (T,), dev), _tensor("positions", positions, _I32, (T,), dev), T,
+            _tensor("touched_ids", touched_ids, _I32, (E,), dev),
+            _tensor("touched_valid", touched_valid, _I32, (E,), dev), E, _tensor("counts", counts, _I32, (4,), dev),
+            *_workspace(workspace, dev))
+    _run(lib.qskv_extend_tables, dev, args, stream)
 
 
 def get_error(workspace: torch.Tensor, stream=None) -> int:

@@ -12,6 +12,7 @@
 #include "qskv.h"
 #include "qskv_device.cuh"
 #include "qskv_internal.h"
+#include "qskv_kvq.cuh"
 
 namespace qskv {
 
@@ -871,6 +872,224 @@ qskv_status qskv_cascade_paged_decode(const void *q, qskv_dtype q_dtype, const v
                     "cascade_paged_decode launch");
 }
 
+// ------------------------------------------------ the 4-bit paged KV cache --
+static qskv_status check_group_size(const qskv_shape *s, int32_t gs) {
+    if ((gs != 32 && gs != 64 && gs != 128) || gs > s->head_dim)
+        return fail(QSKV_ERR_UNSUPPORTED, "group_size must be 32, 64 or 128 and at most head_dim (got %d)", gs);
+    return QSKV_OK;
+}
+
+size_t qskv_kvq_block_bytes(const qskv_shape *shape, int32_t group_size) {
+    if (check_shape(shape) != QSKV_OK || check_group_size(shape, group_size) != QSKV_OK) return 0;
+    return size_t(kvq_block_words(shape->head_dim, shape->page_size, shape->head_dim / group_size)) * 4;
+}
+
+qskv_status qskv_kvq_append(const void *k, const void *v, qskv_dtype kv_dtype, int64_t k_stride, int64_t v_stride,
+                            const int32_t *slots, int32_t n_tokens, void *pool, const qskv_shape *shape,
+                            int32_t group_size, void *workspace, size_t workspace_bytes, void *stream) {
+    QSKV_TRY(check_shape(shape));
+    QSKV_TRY(check_group_size(shape, group_size));
+    QSKV_TRY(check_dtype(kv_dtype, "kv"));
+    if (n_tokens < 0) return fail(QSKV_ERR_INVALID_ARG, "n_tokens must be >= 0 (got %d)", n_tokens);
+    QSKV_TRY(check_workspace(workspace, workspace_bytes, 256));
+    if (n_tokens == 0) return ok();
+    if (!k || !v || !slots || !pool) return fail(QSKV_ERR_INVALID_ARG, "k, v, slots and pool must be non-NULL");
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(pool, 16))
+        return fail(QSKV_ERR_INVALID_ARG, "k, v and pool must be 16-byte aligned");
+    if (!aligned(slots, 4)) return fail(QSKV_ERR_INVALID_ARG, "slots must be 4-byte aligned");
+    const int64_t row = int64_t(shape->num_kv_heads) * shape->head_dim;
+    const int64_t vec = kv_dtype == QSKV_BF16 ? 8 : 4;
+    if (n_tokens > 1 && (k_stride < row || v_stride < row || k_stride % vec || v_stride % vec))
+        return fail(QSKV_ERR_INVALID_ARG,
+                    "k_stride and v_stride must be at least num_kv_heads * head_dim and multiples of 16 bytes");
+    KvqStoreArgs a = {};
+    a.k = k;
+    a.v = v;
+    a.pool = static_cast<uint32_t *>(pool);
+    a.slots = slots;
+    a.flags = static_cast<uint32_t *>(workspace);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.n_tokens = n_tokens;
+    a.num_kv_heads = shape->num_kv_heads;
+    a.page_size = shape->page_size;
+    a.num_pool_pages = shape->num_pool_pages;
+    a.group_size = group_size;
+    return launched(launch_kvq_append(a, kv_dtype, shape->head_dim, static_cast<cudaStream_t>(stream)),
+                    "kvq_append launch");
+}
+
+qskv_status qskv_kvq_gather(const void *pool, const int32_t *slots, int32_t n_tokens, void *k_out, void *v_out,
+                            qskv_dtype out_dtype, const qskv_shape *shape, int32_t group_size, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    QSKV_TRY(check_shape(shape));
+    QSKV_TRY(check_group_size(shape, group_size));
+    QSKV_TRY(check_dtype(out_dtype, "out"));
+    if (n_tokens < 0) return fail(QSKV_ERR_INVALID_ARG, "n_tokens must be >= 0 (got %d)", n_tokens);
+    QSKV_TRY(check_workspace(workspace, workspace_bytes, 256));
+    if (n_tokens == 0) return ok();
+    if (!pool || !slots || !k_out || !v_out)
+        return fail(QSKV_ERR_INVALID_ARG, "pool, slots, k_out and v_out must be non-NULL");
+    if (!aligned(pool, 16) || !aligned(k_out, 16) || !aligned(v_out, 16))
+        return fail(QSKV_ERR_INVALID_ARG, "pool, k_out and v_out must be 16-byte aligned");
+    if (!aligned(slots, 4)) return fail(QSKV_ERR_INVALID_ARG, "slots must be 4-byte aligned");
+    KvqStoreArgs a = {};
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.pool = static_cast<uint32_t *>(const_cast<void *>(pool));
+    a.slots = slots;
+    a.flags = static_cast<uint32_t *>(workspace);
+    a.n_tokens = n_tokens;
+    a.num_kv_heads = shape->num_kv_heads;
+    a.page_size = shape->page_size;
+    a.num_pool_pages = shape->num_pool_pages;
+    a.group_size = group_size;
+    return launched(launch_kvq_gather(a, out_dtype, shape->head_dim, static_cast<cudaStream_t>(stream)),
+                    "kvq_gather launch");
+}
+
+qskv_status qskv_kvq_meta_build(const void *pool, const int32_t *page_ids, const int32_t *valid_tokens,
+                                int32_t n_pages, void *meta, qskv_dtype meta_dtype, const qskv_shape *shape,
+                                int32_t group_size, void *workspace, size_t workspace_bytes, void *stream) {
+    QSKV_TRY(check_shape(shape));
+    QSKV_TRY(check_group_size(shape, group_size));
+    QSKV_TRY(check_dtype(meta_dtype, "meta"));
+    if (n_pages < 0) return fail(QSKV_ERR_INVALID_ARG, "n_pages must be >= 0 (got %d)", n_pages);
+    QSKV_TRY(check_workspace(workspace, workspace_bytes, 256));
+    if (n_pages == 0) return ok();
+    if (!pool || !page_ids || !valid_tokens || !meta)
+        return fail(QSKV_ERR_INVALID_ARG, "pool, page_ids, valid_tokens and meta must be non-NULL");
+    if (!aligned(pool, 16) || !aligned(meta, 16))
+        return fail(QSKV_ERR_INVALID_ARG, "pool and meta must be 16-byte aligned");
+    if (!aligned(page_ids, 4) || !aligned(valid_tokens, 4))
+        return fail(QSKV_ERR_INVALID_ARG, "page_ids and valid_tokens must be 4-byte aligned");
+    KvqMetaArgs a = {};
+    a.pool = static_cast<const uint32_t *>(pool);
+    a.page_ids = page_ids;
+    a.valid_tokens = valid_tokens;
+    a.meta = meta;
+    a.flags = static_cast<uint32_t *>(workspace);
+    a.n_list = n_pages;
+    a.num_kv_heads = shape->num_kv_heads;
+    a.page_size = shape->page_size;
+    a.num_pool_pages = shape->num_pool_pages;
+    a.group_size = group_size;
+    return launched(launch_kvq_meta(a, meta_dtype, shape->head_dim, static_cast<cudaStream_t>(stream)),
+                    "kvq_meta_build launch");
+}
+
+size_t qskv_kvq_workspace_size(const qskv_shape *shape) {
+    if (check_shape(shape) != QSKV_OK) return 0;
+    return 256;
+}
+
+qskv_status qskv_kvq_paged_decode(const void *q, qskv_dtype q_dtype, const void *pool, const int32_t *page_table,
+                                  const int32_t *seq_lens, const qskv_shape *shape, int32_t group_size,
+                                  const int32_t *selected, const int32_t *n_selected, int32_t top_k, float sm_scale,
+                                  float *out, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    QSKV_TRY(check_shape(shape));
+    QSKV_TRY(check_group_size(shape, group_size));
+    QSKV_TRY(check_dtype(q_dtype, "q"));
+    if (!q || !pool || !page_table || !seq_lens || !out)
+        return fail(QSKV_ERR_INVALID_ARG, "q, pool, page_table, seq_lens and out must be non-NULL");
+    if (selected && (!n_selected || top_k < 1))
+        return fail(QSKV_ERR_INVALID_ARG, "with a selected list, n_selected must be non-NULL and top_k >= 1");
+    if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16))
+        return fail(QSKV_ERR_INVALID_ARG, "q, pool and out must be 16-byte aligned");
+    if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(selected, 4) || !aligned(n_selected, 4) ||
+        !aligned(lse, 4))
+        return fail(QSKV_ERR_INVALID_ARG, "index and lse arrays must be 4-byte aligned");
+    if (!(sm_scale >= 0.f) || isinf(sm_scale)) return fail(QSKV_ERR_INVALID_ARG, "sm_scale must be finite and >= 0");
+    const int64_t rows = int64_t(shape->batch) * shape->num_kv_heads;
+    if (rows * (selected ? top_k : shape->max_pages) >= (int64_t(1) << 31))
+        return fail(QSKV_ERR_UNSUPPORTED, "batch * num_kv_heads * %s must be < 2^31", selected ? "top_k" : "max_pages");
+    QSKV_TRY(check_workspace(workspace, workspace_bytes, qskv_kvq_workspace_size(shape)));
+    KvqDecodeArgs a = {};
+    a.q = q;
+    a.pool = static_cast<const uint32_t *>(pool);
+    a.page_table = page_table;
+    a.seq_lens = seq_lens;
+    a.selected = selected;
+    a.n_selected = n_selected;
+    a.out = out;
+    a.lse = lse;
+    a.flags = static_cast<uint32_t *>(workspace);
+    a.batch = shape->batch;
+    a.num_q_heads = shape->num_q_heads;
+    a.num_kv_heads = shape->num_kv_heads;
+    a.group = shape->num_q_heads / shape->num_kv_heads;
+    a.page_size = shape->page_size;
+    a.max_pages = shape->max_pages;
+    a.num_pool_pages = shape->num_pool_pages;
+    a.top_k = selected ? top_k : 0;
+    a.group_size = group_size;
+    a.q_is_bf16 = q_dtype == QSKV_BF16;
+    const float scale = sm_scale > 0.f ? sm_scale : 1.f / sqrtf(float(shape->head_dim));
+    a.scale_log2 = scale * 1.4426950408889634f;
+    return launched(launch_kvq_decode(a, shape->head_dim, static_cast<cudaStream_t>(stream)),
+                    "kvq_paged_decode launch");
+}
+
+// ------------------------------------------------------------- page tables --
+size_t qskv_tables_workspace_size(const qskv_shape *shape) {
+    if (check_shape(shape) != QSKV_OK) return 0;
+    const size_t prefixes = shape->batch > kTablesScanRequests ? size_t(3) * (size_t(shape->batch) + 1) * 4 : 0;
+    return 256 + align256(prefixes);
+}
+
+qskv_status qskv_extend_tables(const int32_t *seq_lens, const int32_t *new_lens, const int32_t *free_pages,
+                               int32_t n_free, int32_t *page_table, const qskv_shape *shape, int32_t *seq_lens_out,
+                               int32_t *cu_new, int32_t *slot_map, int32_t *positions, int32_t max_tokens,
+                               int32_t *touched_ids, int32_t *touched_valid, int32_t max_touched, int32_t *counts,
+                               void *workspace, size_t workspace_bytes, void *stream) {
+    QSKV_TRY(check_shape(shape));
+    if (n_free < 0 || n_free == INT32_MAX) return fail(QSKV_ERR_INVALID_ARG, "n_free must be in [0, 2^31 - 1) (got %d)", n_free);
+    if (max_tokens < 1 || max_tokens == INT32_MAX)
+        return fail(QSKV_ERR_INVALID_ARG, "max_tokens must be in [1, 2^31 - 1) (got %d)", max_tokens);
+    if (!seq_lens || !new_lens || (!free_pages && n_free > 0) || !page_table || !seq_lens_out || !cu_new || !slot_map)
+        return fail(QSKV_ERR_INVALID_ARG,
+                    "seq_lens, new_lens, free_pages, page_table, seq_lens_out, cu_new and slot_map must be non-NULL");
+    if (!touched_ids != !touched_valid)
+        return fail(QSKV_ERR_INVALID_ARG, "touched_ids and touched_valid must both be given or both be NULL");
+    if (seq_lens_out == seq_lens || seq_lens_out == new_lens)
+        return fail(QSKV_ERR_INVALID_ARG, "seq_lens_out must not be the buffer of seq_lens or new_lens");
+    const int32_t *all[] = {seq_lens, new_lens, free_pages, page_table, seq_lens_out, cu_new, slot_map, positions,
+                            touched_ids, touched_valid, counts};
+    for (const int32_t *p : all)
+        if (!aligned(p, 4)) return fail(QSKV_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+    // every admitted request touches at most new / page_size + 2 pages, and at most one a token
+    const int64_t bound = int64_t(max_tokens) / shape->page_size + 2 * int64_t(shape->batch);
+    const int32_t most = int32_t(bound < max_tokens ? bound : max_tokens);
+    if (touched_ids && max_touched < most)
+        return fail(QSKV_ERR_INVALID_ARG, "max_touched must be at least %d for these sizes (got %d)", most, max_touched);
+    const int sms = current_sm_count(nullptr);
+    if (sms <= 0) return fail(QSKV_ERR_CUDA, "cannot query the current CUDA device");
+    QSKV_TRY(check_workspace(workspace, workspace_bytes, qskv_tables_workspace_size(shape)));
+    TablesArgs a = {};
+    a.seq_lens = seq_lens;
+    a.new_lens = new_lens;
+    a.free_pages = free_pages;
+    a.page_table = page_table;
+    a.seq_lens_out = seq_lens_out;
+    a.cu_new = cu_new;
+    a.slot_map = slot_map;
+    a.positions = positions;
+    a.touched_ids = touched_ids;
+    a.touched_valid = touched_valid;
+    a.counts = counts;
+    a.flags = static_cast<uint32_t *>(workspace);
+    a.batch = shape->batch;
+    a.page_size = shape->page_size;
+    a.max_pages = shape->max_pages;
+    a.num_pool_pages = shape->num_pool_pages;
+    a.n_free = n_free;
+    a.max_tokens = max_tokens;
+    a.max_touched = touched_ids ? max_touched : most;
+    return launched(launch_extend_tables(a, reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + 256), sms,
+                                         static_cast<cudaStream_t>(stream)),
+                    "extend_tables launch");
+}
+
 qskv_status qskv_get_error(void *workspace, void *stream) {
     if (!workspace) return fail(QSKV_ERR_WORKSPACE, "workspace is NULL");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -888,6 +1107,7 @@ qskv_status qskv_get_error(void *workspace, void *stream) {
     if (flags & kErrValid) what += " valid-tokens-out-of-range";
     if (flags & kErrTimeout) what += " wait-timeout";
     if (flags & kErrPrefix) what += " shared-prefix-contract-broken";
+    if (flags & kErrCapacity) what += " request-refused-for-capacity";
     if (flags & kErrTimeout) return fail(QSKV_ERR_DEVICE_TIMEOUT, "device flags:%s", what.c_str());
     return fail(QSKV_ERR_DEVICE_INDEX, "device flags:%s", what.c_str());
 }

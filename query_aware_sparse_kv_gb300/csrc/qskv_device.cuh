@@ -19,6 +19,7 @@ enum : uint32_t {
     kErrValid = 8u,     // valid-token count outside [1, page_size]
     kErrTimeout = 16u,  // a bounded mbarrier wait gave up
     kErrPrefix = 32u,   // a row breaks the shared-prefix contract of the cascade decode
+    kErrCapacity = 64u, // a request did not fit the free pages or the token capacity (page-table builder)
 };
 
 // A wait on a TMA transfer that has not completed after this long is treated
