@@ -3,7 +3,45 @@
 //
 // With k = m + s u per group j of dims, the logit of token t is
 //     l_t = scale * sum_j (s_tj (q_j . u_tj) + m_tj sum(q_j)),
-// and the output sum_t p_t (m_tj + s_tj u_t) over softmax weights p.
+// and the output sum_t p_t (m_tj + s_tj u_t) over softmax weights p, so the
+// matrix products run on the codes u themselves and scales and minima are
+// applied per token and group, outside them.
+//
+// Bound: HBM.  A token and head is d + 8 NG bytes; the arithmetic on it has
+// to fit the time those take (23 bytes a clock and SM), which is what shapes
+// the inner loop:
+//   * a code is a fp16 number as it stands: the bits 0x000u are the subnormal
+//     u 2^-24 and 0x00u0 is 16 u 2^-24, both exact operands of the tensor
+//     cores.  A word of 8 codes becomes four fp16 pairs with four ANDs and one
+//     shift; the 16 is taken off the query (keys) or the output (values).
+//   * S (16 tokens x 8 columns) = K_tile Q^T and O^T (dims x 8) += V_tile^T P^T
+//     as mma.sync m16n8k16 with fp32 accumulators; at most 8 query heads share
+//     a cache row, so there is no 128-row tile to feed tcgen05 with.
+//   * fp32 precision from fp16 operands: queries (scaled by a power of two
+//     into fp16's range) and weights enter as two halves hi + lo.  With at
+//     most 4 heads (HC = 4) the halves share the 8 columns: column 2h is head
+//     h's hi, 2h + 1 its lo; with 8 heads they are two products.
+//   * a key's words lie so that a lane's operands are one vector load; values
+//     come through ldmatrix.trans, whose 16-bit elements are four codes of one
+//     token: the pair of a register is two tokens, as the product needs.
+//
+// Softmax.  Running references per head: M for the exponent and sg for the
+// weights times value scales (p s sg is what becomes fp16).  Both are moved
+// only when a weight would pass 2^12, or p s sg 2^14 (rare after the first
+// tile), so the usual tile has no rescaling and one vote.  Sums of weights
+// and of p m stay per lane until the row ends.
+//
+// Work split.  A unit is one page of one (sequence, KV head) row; all units
+// in row order are cut into equal ranges, one per warp of a grid of two CTAs
+// an SM.  Every CTA finds its range from a scan of the lengths (or selection
+// counts) in shared memory, so ragged batches balance exactly.  A warp keeps
+// its own ring of stages, one bulk copy a page, and its own running state; a
+// row that lies within a warp is finished by it, pieces of a row within a CTA
+// are folded in shared memory, and pieces of several CTAs by the CTA that
+// draws the row's last ticket, always in unit order: results do not depend on
+// timing.
+#include <cuda_fp16.h>
+
 #include "qskv_internal.h"
 #include "qskv_kvq.cuh"
 
@@ -11,77 +49,705 @@ namespace qskv {
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kEntries = 1024;     // entries of the unit prefix held in shared memory
+constexpr int kMaxRing = 8;        // stages a warp
+constexpr float kNoRef = -1e30f;   // M before the first token
+constexpr float kTopP = 4096.f, kTopW = 16384.f;
 
-// One CTA per (sequence, KV head), one thread per dim, one head and token at
-// a time with a running maximum and sum.
-template <int D>
-__global__ void __launch_bounds__(D) kvq_decode_kernel(KvqDecodeArgs a) {
-    __shared__ float part[D / 32];
-    pdl_trigger();
-    pdl_wait();
-    const int row = blockIdx.x, b = row / a.num_kv_heads, g = row % a.num_kv_heads, c = threadIdx.x;
-    const int P = a.page_size, ng = D / a.group_size, w = c / 8, j = c / a.group_size;
-    int seq = a.seq_lens[b];
-    if (seq < 0 || seq > a.max_pages * P) {
-        if (c == 0) raise_error(a.flags, kErrSeqLen);
-        seq = seq < 0 ? 0 : a.max_pages * P;
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// x - (x rounded to fp16)
+__device__ __forceinline__ float half_rest(float x) { return x - __half2float(__float2half_rn(x)); }
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ float max_over_tokens(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float sum_over_tokens(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// ------------------------------------------------------------------ units --
+__device__ __forceinline__ int seq_of(const KvqDecodeArgs &a, int b) {
+    const int s = __ldg(a.seq_lens + b), cap = a.max_pages * a.page_size;
+    if (s < 0 || s > cap) {
+        raise_error(a.flags, kErrSeqLen);
+        return s < 0 ? 0 : cap;
     }
-    const int n_b = (seq + P - 1) / P;
-    int n = n_b;
+    return s;
+}
+__device__ __forceinline__ int pages_of(const KvqDecodeArgs &a, int b) {
+    return (seq_of(a, b) + a.page_size - 1) / a.page_size;
+}
+// Units of list item i: a row's selected pages, or all pages of a sequence
+// (all its KV heads).
+__device__ __forceinline__ int units_of(const KvqDecodeArgs &a, int i) {
+    if (!a.selected) return pages_of(a, i) * a.num_kv_heads;
+    const int n = __ldg(a.n_selected + i), lim = min(a.top_k, pages_of(a, i / a.num_kv_heads));
+    if (n < 0 || n > lim) {
+        raise_error(a.flags, kErrSelected);
+        return max(0, min(n, lim));
+    }
+    return n;
+}
+
+struct Unit {
+    int code;   // page << 6 | valid tokens; -1: skipped
+    int row, slot, count;
+};
+
+struct Shared {
+    int prefix[kEntries + 1];
+    int warp_sum[kWarps];
+    Unit desc[kWarps][64];
+    uint64_t bar[kWarps][kMaxRing];
+    // pieces of rows that no warp owns whole: 2w ends in, 2w + 1 runs on from, warp w's range
+    int piece_row[2 * kWarps], piece_begin[2 * kWarps], piece_end[2 * kWarps];
+    float piece_m[2 * kWarps][8], piece_l[2 * kWarps][8];
+    int fold_row[2], fold_first[2], fold_n[2], folds;
+    int last;
+    float row_m[8], row_l[8];
+};
+
+// The unit with global index u.
+__device__ __forceinline__ Unit unit_at(const KvqDecodeArgs &a, const Shared &s, int entries, int per, int u) {
+    int lo = 0, hi = entries;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s.prefix[mid] <= u)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    int i = lo * per, off = u - s.prefix[lo];
+    if (per > 1)
+        for (int n = units_of(a, i); off >= n; n = units_of(a, i)) off -= n, i++;
+    Unit r;
+    int b, j, seq;
     if (a.selected) {
-        n = a.n_selected[row];
-        const int lim = min(a.top_k, n_b);
-        if (n < 0 || n > lim) {
-            if (c == 0) raise_error(a.flags, kErrSelected);
-            n = max(0, min(n, lim));
+        b = i / a.num_kv_heads;
+        r.row = i, r.slot = off, r.count = units_of(a, i);
+        j = __ldg(a.selected + int64_t(i) * a.top_k + off);
+        seq = seq_of(a, b);
+    } else {
+        b = i;
+        seq = seq_of(a, b);
+        r.count = (seq + a.page_size - 1) / a.page_size;
+        const int g = off / r.count;
+        r.slot = j = off - g * r.count;
+        r.row = b * a.num_kv_heads + g;
+    }
+    r.code = -1;
+    if (j < 0 || j * int64_t(a.page_size) >= seq) {
+        raise_error(a.flags, kErrSelected);
+        return r;
+    }
+    const int p = __ldg(a.page_table + int64_t(b) * a.max_pages + j);
+    if (p < 0 || p >= a.num_pool_pages) {
+        raise_error(a.flags, kErrPageId);
+        return r;
+    }
+    r.code = (p << 6) | min(a.page_size, seq - j * a.page_size);
+    return r;
+}
+
+// ----------------------------------------------------- one row in a warp --
+// Lane 4g + t of a warp works, for every 16-token tile, on tokens g and g + 8
+// and on head t (HC = 4) or heads 2t and 2t + 1 (HC = 8).
+template <int D, int NG, int HC>
+struct RowState {
+    static constexpr int NW = D / 32;     // 32-dim chunks of a row; code words a lane holds of a token's key
+    static constexpr int GW = NW / NG;    // chunks a group
+    static constexpr int NH = HC / 4;     // heads a lane
+    uint32_t qh[NW][4], ql[HC == 8 ? NW : 1][4];
+    float qa[NH], qb[NH][NG];
+    float m[NH], l[NH], sg[NH], pm[NH][NG];
+    float o[NW][2][4];
+
+    __device__ __forceinline__ void load_query(const KvqDecodeArgs &a, int row) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const int h = HC == 4 ? g >> 1 : g;
+        const int b = row / a.num_kv_heads, kh = row % a.num_kv_heads;
+        const int64_t at = (int64_t(b) * a.num_q_heads + kh * a.group + h) * D + 8 * t;
+        float q[NW][8];
+#pragma unroll
+        for (int i = 0; i < NW; i++) {
+            uint4 x = make_uint4(0, 0, 0, 0), y = x;
+            if (h < a.group) {
+                if (a.q_is_bf16) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at + 32 * i);
+                    x = make_uint4(w.x << 16, w.x & 0xffff0000u, w.y << 16, w.y & 0xffff0000u);
+                    y = make_uint4(w.z << 16, w.z & 0xffff0000u, w.w << 16, w.w & 0xffff0000u);
+                } else {
+                    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q) + at + 32 * i);
+                    x = p[0], y = p[1];
+                }
+            }
+            q[i][0] = __uint_as_float(x.x), q[i][1] = __uint_as_float(x.y), q[i][2] = __uint_as_float(x.z);
+            q[i][3] = __uint_as_float(x.w), q[i][4] = __uint_as_float(y.x), q[i][5] = __uint_as_float(y.y);
+            q[i][6] = __uint_as_float(y.z), q[i][7] = __uint_as_float(y.w);
+        }
+        float top = 0.f, sum[NG];
+#pragma unroll
+        for (int j = 0; j < NG; j++) sum[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NW; i++)
+#pragma unroll
+            for (int k = 0; k < 8; k++) top = fmaxf(top, fabsf(q[i][k])), sum[i / GW] += q[i][k];
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll
+        for (int j = 0; j < NG; j++) {
+            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
+            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
+            sum[j] *= a.scale_log2;
+        }
+        // q 2^(13 - e) has its largest entry in [2^13, 2^14); its lo half is held times 2^11
+        const int e = min(max(int(__float_as_uint(top) >> 23) - 127, -100), 100);
+        const float up = __uint_as_float(uint32_t(140 - e) << 23);
+        const float back = __uint_as_float(uint32_t(127 + e + 11) << 23) * a.scale_log2;  // 2^24 / up
+#pragma unroll
+        for (int i = 0; i < NW; i++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {  // codes r and r + 4; odd r meets codes times 16
+                const float f = r & 1 ? up * 0.0625f : up;
+                const float x = q[i][r] * f, y = q[i][r + 4] * f;
+                const uint32_t hi = pack_half2(x, y), lo = pack_half2(half_rest(x) * 2048.f, half_rest(y) * 2048.f);
+                if constexpr (HC == 4) {
+                    qh[i][r] = g & 1 ? lo : hi;
+                } else {
+                    qh[i][r] = hi;
+                    ql[i][r] = lo;
+                }
+            }
+#pragma unroll
+        for (int h2 = 0; h2 < NH; h2++) {
+            const int from = HC == 4 ? 8 * t : 8 * t + 4 * h2;
+            qa[h2] = __shfl_sync(0xffffffffu, back, from);
+#pragma unroll
+            for (int j = 0; j < NG; j++) qb[h2][j] = __shfl_sync(0xffffffffu, sum[j], from);
         }
     }
-    for (int h = 0; h < a.group; h++) {
-        const int64_t at = (int64_t(b) * a.num_q_heads + g * a.group + h) * D + c;
-        const float q = a.q_is_bf16 ? __uint_as_float(uint32_t(static_cast<const uint16_t *>(a.q)[at]) << 16)
-                                    : static_cast<const float *>(a.q)[at];
-        float top = -1e30f, sum = 0.f, o = 0.f;
-        for (int i = 0; i < n; i++) {
-            const int page = a.selected ? a.selected[int64_t(row) * a.top_k + i] : i;
-            if (page < 0 || page >= n_b) {
-                if (c == 0) raise_error(a.flags, kErrSelected);
-                continue;
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int h = 0; h < NH; h++) {
+            m[h] = kNoRef, l[h] = 0.f, sg[h] = 1.f;
+#pragma unroll
+            for (int j = 0; j < NG; j++) pm[h][j] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < NW; c++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) o[c][0][r] = o[c][1][r] = 0.f;
+    }
+
+    // One 16-token tile: `tile` of the block at `st`, of which the first nv
+    // (1..16) tokens count.
+    __device__ __forceinline__ void tile(const uint8_t *st, int P, int tile, int nv) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const int ta = tile * 16 + g;
+        // ---- keys: codes of tokens g and g + 8, logits
+        uint32_t ka[NW], kb[NW];
+        const uint8_t *kp = st + ta * (D / 2) + t * (D / 8);
+        if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(kp), y = *reinterpret_cast<const uint4 *>(kp + 4 * D);
+            ka[0] = x.x, ka[1] = x.y, ka[2] = x.z, ka[3] = x.w;
+            kb[0] = y.x, kb[1] = y.y, kb[2] = y.z, kb[3] = y.w;
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(kp), y = *reinterpret_cast<const uint2 *>(kp + 4 * D);
+            ka[0] = x.x, ka[1] = x.y, kb[0] = y.x, kb[1] = y.y;
+        }
+        const uint32_t *par = reinterpret_cast<const uint32_t *>(st + P * D) + ta;
+        uint32_t va[NG], vb[NG];
+        float x[2][NH], xm[2][NH];
+#pragma unroll
+        for (int h = 0; h < NH; h++) x[0][h] = x[1][h] = xm[0][h] = xm[1][h] = 0.f;
+#pragma unroll
+        for (int j = 0; j < NG; j++) {
+            const uint32_t pa = par[j * P], pb = par[j * P + 8];
+            va[j] = par[(NG + j) * P], vb[j] = par[(NG + j) * P + 8];
+            float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = j * GW; i < (j + 1) * GW; i++) {
+                const uint32_t a = ka[i], b = kb[i], a8 = a >> 8, b8 = b >> 8;
+                constexpr uint32_t lo = 0x000f000fu, hi = 0x00f000f0u;
+                mma_f16(c0, a & lo, b & lo, a & hi, b & hi, qh[i][0], qh[i][1]);
+                if constexpr (HC == 4) {
+                    mma_f16(c1, a8 & lo, b8 & lo, a8 & hi, b8 & hi, qh[i][2], qh[i][3]);
+                } else {
+                    mma_f16(c1, a & lo, b & lo, a & hi, b & hi, ql[i][0], ql[i][1]);
+                    mma_f16(c0, a8 & lo, b8 & lo, a8 & hi, b8 & hi, qh[i][2], qh[i][3]);
+                    mma_f16(c1, a8 & lo, b8 & lo, a8 & hi, b8 & hi, ql[i][2], ql[i][3]);
+                }
             }
-            const int id = a.page_table[int64_t(b) * a.max_pages + page];
-            if (id < 0 || id >= a.num_pool_pages) {
-                if (c == 0) raise_error(a.flags, kErrPageId);
-                continue;
+            constexpr float lo_unit = 1.f / 2048.f;
+            const float sa = bf16_lo_to_float(pa), ma = bf16_hi_to_float(pa);
+            const float sb = bf16_lo_to_float(pb), mb = bf16_hi_to_float(pb);
+            float ua[NH], ub[NH];
+            if constexpr (HC == 4) {
+                ua[0] = fmaf(c0[1] + c1[1], lo_unit, c0[0] + c1[0]);
+                ub[0] = fmaf(c0[3] + c1[3], lo_unit, c0[2] + c1[2]);
+            } else {
+                ua[0] = fmaf(c1[0], lo_unit, c0[0]), ua[NH - 1] = fmaf(c1[1], lo_unit, c0[1]);
+                ub[0] = fmaf(c1[2], lo_unit, c0[2]), ub[NH - 1] = fmaf(c1[3], lo_unit, c0[3]);
             }
-            const uint32_t *block = a.pool + (int64_t(id) * a.num_kv_heads + g) * kvq_block_words(D, P, ng);
-            for (int t = 0; t < min(P, seq - page * P); t++) {
-                const uint32_t kw = block[t * (D / 8) + kvq_key_place<D>(w)];
-                const uint32_t vw = block[(P + t) * (D / 8) + kvq_value_place<D>(w, t)];
-                const uint32_t kp = block[2 * P * (D / 8) + j * P + t], vp = block[2 * P * (D / 8) + (ng + j) * P + t];
-                const float k = fmaf(float((kw >> (c % 8 * 4)) & 15u), bf16_lo_to_float(kp), bf16_hi_to_float(kp));
-                const float v = fmaf(float((vw >> (c % 8 * 4)) & 15u), bf16_lo_to_float(vp), bf16_hi_to_float(vp));
-                float x = q * k;
-                for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                __syncthreads();
-                if (c % 32 == 0) part[c / 32] = x;
-                __syncthreads();
-                x = 0.f;
-                for (int d = 0; d < D / 32; d++) x += part[d];
-                x *= a.scale_log2;
-                const float m = fmaxf(top, x), f = exp2f(top - m), p = exp2f(x - m);
-                sum = sum * f + p, o = o * f + p * v, top = m;
+#pragma unroll
+            for (int h = 0; h < NH; h++) {
+                x[0][h] = fmaf(sa, ua[h], x[0][h]), xm[0][h] = fmaf(ma, qb[h][j], xm[0][h]);
+                x[1][h] = fmaf(sb, ub[h], x[1][h]), xm[1][h] = fmaf(mb, qb[h][j], xm[1][h]);
             }
         }
-        a.out[at] = sum > 0.f ? o / sum : 0.f;
-        if (c == 0 && a.lse) a.lse[at / D] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+#pragma unroll
+        for (int h = 0; h < NH; h++) x[0][h] = fmaf(qa[h], x[0][h], xm[0][h]), x[1][h] = fmaf(qa[h], x[1][h], xm[1][h]);
+        if (nv < 16) {  // places past the end: no weight, and nothing of their params
+            const bool off_a = g >= nv, off_b = g + 8 >= nv;
+#pragma unroll
+            for (int h = 0; h < NH; h++) {
+                if (off_a) x[0][h] = -INFINITY;
+                if (off_b) x[1][h] = -INFINITY;
+            }
+#pragma unroll
+            for (int j = 0; j < NG; j++) {
+                if (off_a) va[j] = 0;
+                if (off_b) vb[j] = 0;
+            }
+        }
+        // ---- weights
+        float p[2][NH], w[2][NH][NG];
+        float most_p = 0.f, most_w = 0.f;
+        bool calm = true;
+#pragma unroll
+        for (int h = 0; h < NH; h++) {
+            p[0][h] = ex2(x[0][h] - m[h]), p[1][h] = ex2(x[1][h] - m[h]);
+            most_p = fmaxf(most_p, fmaxf(p[0][h], p[1][h]));
+#pragma unroll
+            for (int j = 0; j < NG; j++) {
+                w[0][h][j] = p[0][h] * (bf16_lo_to_float(va[j]) * sg[h]);
+                w[1][h][j] = p[1][h] * (bf16_lo_to_float(vb[j]) * sg[h]);
+                most_w = fmaxf(most_w, fmaxf(w[0][h][j], w[1][h][j]));
+            }
+        }
+        calm = most_p <= kTopP && most_w <= kTopW;
+        if (!__all_sync(0xffffffffu, calm)) {
+#pragma unroll
+            for (int h = 0; h < NH; h++) {
+                const float mn = fmaxf(m[h], max_over_tokens(fmaxf(x[0][h], x[1][h])));
+                const float f = ex2(m[h] - mn);
+                p[0][h] = ex2(x[0][h] - mn), p[1][h] = ex2(x[1][h] - mn);
+                float top = 0.f;
+#pragma unroll
+                for (int j = 0; j < NG; j++)
+                    top = fmaxf(top, fmaxf(p[0][h] * bf16_lo_to_float(va[j]), p[1][h] * bf16_lo_to_float(vb[j])));
+                top = max_over_tokens(top);
+                // sg such that the tile's largest p s sg lies in [2^8, 2^9); what is summed already may grow by 2^30
+                float s = sg[h];
+                if (top >= 7.888609052210118e-31f) {  // 2^-100
+                    s = __uint_as_float((262u << 23) - (__float_as_uint(top) & 0x7f800000u));
+                    if (m[h] != kNoRef) s = fminf(s, sg[h] * 1073741824.f);
+                }
+                const float r = f * (s / sg[h]);
+                m[h] = mn, sg[h] = s, l[h] *= f;
+#pragma unroll
+                for (int j = 0; j < NG; j++) {
+                    pm[h][j] *= f;
+                    w[0][h][j] = p[0][h] * (bf16_lo_to_float(va[j]) * s);
+                    w[1][h][j] = p[1][h] * (bf16_lo_to_float(vb[j]) * s);
+                }
+#pragma unroll
+                for (int c = 0; c < NW; c++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        if (HC == 4 || (k & 1) == h) o[c][0][k] *= r, o[c][1][k] *= r;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < NH; h++) {
+            l[h] += p[0][h] + p[1][h];
+#pragma unroll
+            for (int j = 0; j < NG; j++)
+                pm[h][j] = fmaf(p[1][h], bf16_hi_to_float(vb[j]), fmaf(p[0][h], bf16_hi_to_float(va[j]), pm[h][j]));
+        }
+        // ---- values
+        const int mat = lane >> 3, r = lane & 7;
+        const int token = tile * 16 + (mat & 1) * 8 + r;
+        const int sw = D == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
+        const uint32_t vrow = smem_u32(st) + P * (D / 2) + token * (D / 2);
+        uint32_t bh[2], bl[2];
+#pragma unroll
+        for (int c2 = 0; c2 < NW / 2; c2++) {
+            uint32_t v[4];
+            ldmatrix_x4_trans(v, vrow + (((2 * c2 + (mat >> 1)) ^ sw) << 4));
+#pragma unroll
+            for (int cc = 0; cc < 2; cc++) {
+                const int c = 2 * c2 + cc;
+                if (c % GW == 0) {
+                    const int j = c / GW;
+                    if constexpr (HC == 4) {
+                        bh[0] = movmatrix_trans(pack_half2(w[0][0][j], half_rest(w[0][0][j])));
+                        bh[1] = movmatrix_trans(pack_half2(w[1][0][j], half_rest(w[1][0][j])));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            bh[k] = movmatrix_trans(pack_half2(w[k][0][j], w[k][NH - 1][j]));
+                            bl[k] = movmatrix_trans(pack_half2(half_rest(w[k][0][j]), half_rest(w[k][NH - 1][j])));
+                        }
+                    }
+                }
+                const uint32_t v0 = v[2 * cc], v1 = v[2 * cc + 1];
+                constexpr uint32_t lo = 0x000f000fu, hi = 0x00f000f0u;
+                const uint32_t w0 = v0 >> 8, w1 = v1 >> 8;
+                mma_f16(o[c][0], v0 & lo, v0 & hi, v1 & lo, v1 & hi, bh[0], bh[1]);
+                mma_f16(o[c][1], w0 & lo, w0 & hi, w1 & lo, w1 & hi, bh[0], bh[1]);
+                if constexpr (HC == 8) {
+                    mma_f16(o[c][0], v0 & lo, v0 & hi, v1 & lo, v1 & hi, bl[0], bl[1]);
+                    mma_f16(o[c][1], w0 & lo, w0 & hi, w1 & lo, w1 & hi, bl[0], bl[1]);
+                }
+            }
+        }
     }
+
+    // Sums over the lanes; the row's outputs (final) or its piece's reference,
+    // weight sum and unnormalised output.
+    __device__ __forceinline__ void finish(const KvqDecodeArgs &a, int row, bool final, float *piece_o, float *piece_m,
+                                           float *piece_l) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const int64_t head0 = int64_t(row / a.num_kv_heads) * a.num_q_heads + int64_t(row % a.num_kv_heads) * a.group;
+#pragma unroll
+        for (int h = 0; h < NH; h++) {
+            l[h] = sum_over_tokens(l[h]);
+#pragma unroll
+            for (int j = 0; j < NG; j++) pm[h][j] = sum_over_tokens(pm[h][j]);
+            const int head = NH * t + h;
+            if (head >= a.group) continue;
+            const float unit = 16777216.f / sg[h];
+            const float inv = !final ? 1.f : l[h] > 0.f ? 1.f / l[h] : 0.f;
+            float *dst = final ? a.out + (head0 + head) * D : piece_o + head * D;
+#pragma unroll
+            for (int c = 0; c < NW; c++) {
+                const float base = pm[h][c / GW];
+                float v[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const float *q = o[c][k >> 1] + 2 * (k & 1);
+                    const float sum = HC == 4 ? q[0] + q[1] : q[h];
+                    v[k] = fmaf(sum, k & 1 ? unit * 0.0625f : unit, base) * inv;
+                }
+                *reinterpret_cast<float4 *>(dst + 32 * c + 4 * g) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+            if (g == 0) {
+                if (final) {
+                    if (a.lse) a.lse[head0 + head] = l[h] > 0.f ? (m[h] + log2f(l[h])) * kLn2 : -INFINITY;
+                } else {
+                    piece_m[head] = m[h], piece_l[head] = l[h];
+                }
+            }
+        }
+    }
+};
+
+// --------------------------------------------------------- the kernel --
+template <int D, int NG, int HC>
+__global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a) {
+    extern __shared__ __align__(128) uint8_t ring_mem[];
+    __shared__ Shared s;
+    pdl_trigger();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int P = a.page_size, G = a.group;
+    const uint32_t block_bytes = kvq_block_words(D, P, NG) * 4;
+    uint8_t *ring = ring_mem + size_t(warp) * a.stages * block_bytes;
+    if (lane < a.stages) mbar_init(&s.bar[warp][lane], 1);
+    if (tid < 2 * kWarps) s.piece_row[tid] = -1;
+    if (tid == 0) s.folds = 0;
+    mbar_fence_init();
+    if (a.selected) pdl_wait();  // the lengths may be read earlier, the selection not
+
+    // ---- prefix of the units over the list (rows, or sequences)
+    const int items = a.selected ? a.batch * a.num_kv_heads : a.batch;
+    const int per = (items + kEntries - 1) / kEntries, entries = (items + per - 1) / per;
+    const int ept = (entries + kThreads - 1) / kThreads;
+    int mine = 0;
+    for (int e = tid * ept; e < min((tid + 1) * ept, entries); e++) {
+        int n = 0;
+        for (int i = e * per; i < min((e + 1) * per, items); i++) n += units_of(a, i);
+        s.prefix[e] = n;
+        mine += n;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) s.warp_sum[warp] = incl;
+    __syncthreads();
+    int before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+        if (w < warp) before += s.warp_sum[w];
+        total += s.warp_sum[w];
+    }
+    for (int e = tid * ept; e < min((tid + 1) * ept, entries); e++) {
+        const int n = s.prefix[e];
+        s.prefix[e] = before;
+        before += n;
+    }
+    __syncthreads();
+    if (!a.selected) pdl_wait();
+
+    // ---- rows without a token or a selected page
+    const int all_warps = gridDim.x * kWarps;
+    for (int base = blockIdx.x * kWarps + warp; base < items; base += 32 * all_warps) {
+        const int64_t i = base + int64_t(lane) * all_warps;
+        uint32_t none = __ballot_sync(0xffffffffu, i < items && units_of(a, int(i)) == 0);
+        while (none) {
+            const int k = __ffs(none) - 1;
+            none &= none - 1;
+            const int item = base + k * all_warps;
+            const int heads = a.selected ? G : a.num_q_heads;
+            const int64_t h0 = int64_t(item) * heads;  // a row's heads, or a sequence's, lie together
+            for (int c = lane; c < heads * D / 4; c += 32)
+                reinterpret_cast<float4 *>(a.out + h0 * D)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (a.lse)
+                for (int h = lane; h < heads; h += 32) a.lse[h0 + h] = -INFINITY;
+        }
+    }
+
+    // ---- this warp's range
+    const int upw = max(int((uint32_t(total) + all_warps - 1) / all_warps), a.min_units);
+    const int64_t upc = int64_t(upw) * kWarps, c0 = blockIdx.x * upc;
+    const int u0 = int(min(c0 + int64_t(warp) * upw, int64_t(total))), u1 = int(min(int64_t(u0) + upw, int64_t(total)));
+    const int n = u1 - u0;
+    const int cta_begin = int(min(c0, int64_t(total))), cta_end = int(min(c0 + upc, int64_t(total)));
+
+    RowState<D, NG, HC> st;
+    int issued = 0, row = -1, row_begin = 0, row_end = 0;
+    float *piece_first = a.first_o + (int64_t(blockIdx.x) * kWarps + warp) * (G * D);
+    auto close = [&](bool at_end) {
+        const bool final = row_begin >= u0 && row_end <= u1;
+        const int k = 2 * warp + (at_end ? 1 : 0);
+        st.finish(a, row, final, at_end ? reinterpret_cast<float *>(ring) : piece_first, s.piece_m[k], s.piece_l[k]);
+        if (!final && lane == 0) s.piece_row[k] = row, s.piece_begin[k] = row_begin, s.piece_end[k] = row_end;
+    };
+    for (int it = 0; it < n; it++) {
+        for (; issued < n && issued < it + a.stages; issued++) {
+            if ((issued & 31) == 0) {  // describe the next 32 units
+                __syncwarp();
+                if (u0 + issued + lane < u1)
+                    s.desc[warp][(issued + lane) & 63] = unit_at(a, s, entries, per, u0 + issued + lane);
+                __syncwarp();
+            }
+            if (lane == 0) {
+                const Unit &u = s.desc[warp][issued & 63];
+                const int k = issued % a.stages;
+                uint64_t *bar = &s.bar[warp][k];
+                if (u.code >= 0) {
+                    const uint8_t *src = reinterpret_cast<const uint8_t *>(a.pool) +
+                                         (int64_t(u.code >> 6) * a.num_kv_heads + u.row % a.num_kv_heads) * block_bytes;
+                    mbar_arrive_expect_tx(bar, block_bytes);
+                    bulk_load(ring + k * block_bytes, src, block_bytes, bar);
+                } else {
+                    mbar_arrive(bar);
+                }
+            }
+        }
+        const Unit u = s.desc[warp][it & 63];
+        if (u.row != row) {
+            if (row >= 0) close(false);
+            row = u.row, row_begin = u0 + it - u.slot, row_end = row_begin + u.count;
+            st.load_query(a, row);
+            st.clear();
+        }
+        const int k = it % a.stages;
+        if (!mbar_wait_bounded(&s.bar[warp][k], (it / a.stages) & 1, kWaitLimitNs)) {
+            // a lost copy: flagged, the rest of the range is given up once the copies in flight had their time
+            if (lane == 0) raise_error(a.flags, kErrTimeout);
+            for (int i = it + 1; i < issued; i++)
+                mbar_wait_bounded(&s.bar[warp][i % a.stages], (i / a.stages) & 1, kWaitLimitNs);
+            break;
+        }
+        if (u.code >= 0) {
+            const int valid = u.code & 63;
+            for (int tile = 0; tile * 16 < valid; tile++) st.tile(ring + k * block_bytes, P, tile, valid - tile * 16);
+        }
+        __syncwarp();
+    }
+    if (row >= 0) close(true);
+    __syncthreads();
+
+    // ---- pieces of one row within the CTA, in unit order
+    const int elems = G * D / 4;
+    for (int i = 0; i < 2 * kWarps;) {
+        const int r = s.piece_row[i];
+        if (r < 0) {
+            i++;
+            continue;
+        }
+        int end = i + 1;
+        while (end < 2 * kWarps && (s.piece_row[end] < 0 || s.piece_row[end] == r)) end++;
+        const int begin_u = s.piece_begin[i], end_u = s.piece_end[i];
+        const bool whole = begin_u >= cta_begin && end_u <= cta_end;
+        const int slot = 2 * blockIdx.x + (begin_u < cta_begin ? 0 : 1);
+        const int64_t head0 = int64_t(r / a.num_kv_heads) * a.num_q_heads + int64_t(r % a.num_kv_heads) * G;
+        for (int e = tid; e < elems; e += kThreads) {
+            const int h = e * 4 / D;
+            float m = kNoRef, l = 0.f;
+            for (int k = i; k < end; k++)
+                if (s.piece_row[k] == r) m = fmaxf(m, s.piece_m[k][h]);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = i; k < end; k++) {
+                if (s.piece_row[k] != r) continue;
+                const float f = ex2(s.piece_m[k][h] - m);
+                const float *src = k & 1 ? reinterpret_cast<const float *>(ring_mem + size_t(k >> 1) * a.stages * block_bytes)
+                                         : a.first_o + (int64_t(blockIdx.x) * kWarps + (k >> 1)) * (G * D);
+                const float4 v = reinterpret_cast<const float4 *>(src)[e];
+                l = fmaf(f, s.piece_l[k][h], l);
+                o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+            }
+            if (whole) {
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                reinterpret_cast<float4 *>(a.out + head0 * D)[e] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                if (a.lse && e * 4 % D == 0) a.lse[head0 + h] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            } else {
+                reinterpret_cast<float4 *>(a.part_o)[int64_t(slot) * elems + e] = o;
+                if (e * 4 % D == 0) a.part_ml[slot * 16 + h] = m, a.part_ml[slot * 16 + 8 + h] = l;
+            }
+        }
+        if (!whole) {
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const int first = int(begin_u / upc), pieces = int((end_u - 1) / upc) - first + 1;
+                if (atomicAdd(a.tickets + r, 1u) == uint32_t(pieces - 1)) {
+                    a.tickets[r] = 0;
+                    s.fold_row[s.folds] = r, s.fold_first[s.folds] = first, s.fold_n[s.folds] = pieces;
+                    s.folds++;
+                }
+            }
+        }
+        i = end;
+    }
+    __syncthreads();
+
+    // ---- rows whose last ticket this CTA drew: pieces of several CTAs, in unit order
+    for (int f = 0; f < s.folds; f++) {
+        const int r = s.fold_row[f], first = s.fold_first[f], np = s.fold_n[f];
+        float *pw = reinterpret_cast<float *>(ring_mem);  // [np][G] weights, then [kThreads] float4
+        float4 *red = reinterpret_cast<float4 *>(ring_mem + (size_t(np) * G * 4 + 15) / 16 * 16);
+        __threadfence();
+        // piece k of the row: the CTA where it begins wrote slot 1, the others slot 0
+        if (warp < G) {
+            float m = kNoRef, l = 0.f;
+            for (int k = lane; k < np; k += 32) {
+                const int slot = 2 * (first + k) + (k == 0 ? 1 : 0);
+                const float x = __ldcg(a.part_ml + slot * 16 + warp);
+                pw[k * G + warp] = x;
+                m = fmaxf(m, x);
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int k = lane; k < np; k += 32) {
+                const int slot = 2 * (first + k) + (k == 0 ? 1 : 0);
+                const float x = ex2(pw[k * G + warp] - m);
+                pw[k * G + warp] = x;
+                l = fmaf(x, __ldcg(a.part_ml + slot * 16 + 8 + warp), l);
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (lane == 0) s.row_m[warp] = m, s.row_l[warp] = l;
+        }
+        __syncthreads();
+        const int groups = kThreads / elems, grp = tid / elems, e = tid % elems, h = e * 4 / D;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = grp; k < np; k += groups) {
+            const int slot = 2 * (first + k) + (k == 0 ? 1 : 0);
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o) + int64_t(slot) * elems + e);
+            const float x = pw[k * G + h];
+            o.x = fmaf(x, v.x, o.x), o.y = fmaf(x, v.y, o.y), o.z = fmaf(x, v.z, o.z), o.w = fmaf(x, v.w, o.w);
+        }
+        red[tid] = o;
+        __syncthreads();
+        if (grp == 0) {
+            for (int k = 1; k < groups; k++) {
+                const float4 v = red[k * elems + e];
+                o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+            }
+            const float l = s.row_l[h], inv = l > 0.f ? 1.f / l : 0.f;
+            const int64_t head0 = int64_t(r / a.num_kv_heads) * a.num_q_heads + int64_t(r % a.num_kv_heads) * G;
+            reinterpret_cast<float4 *>(a.out + head0 * D)[e] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+            if (a.lse && e * 4 % D == 0) a.lse[head0 + h] = l > 0.f ? (s.row_m[h] + log2f(l)) * kLn2 : -INFINITY;
+        }
+        __syncthreads();
+    }
+}
+
+// Shared memory a CTA may take beside its static part with two CTAs an SM
+// (228 KB an SM, 1 KB of each CTA's reserved).
+constexpr int kRingBudget = 113 * 1024 - int(sizeof(Shared));
+
+template <int D, int NG, int HC>
+cudaError_t launch_one(KvqDecodeArgs &a, int num_sms, int64_t max_units, cudaStream_t stream) {
+    const int stage = kWarps * kvq_block_words(D, a.page_size, NG) * 4;
+    a.stages = kRingBudget / stage < kMaxRing ? kRingBudget / stage : kMaxRing;
+    a.min_units = 1;
+    const int64_t want = (max_units + kWarps * a.min_units - 1) / (kWarps * a.min_units);
+    const int64_t most = int64_t(kvq_decode_ctas(num_sms));
+    const int bytes = a.stages * stage;
+    const cudaError_t e = cudaFuncSetAttribute(kvq_decode_kernel<D, NG, HC>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kvq_decode_kernel<D, NG, HC>, dim3(unsigned(want < most ? want : most)), dim3(kThreads), bytes, stream, a);
+}
+
+template <int D, int NG>
+cudaError_t launch_heads(KvqDecodeArgs &a, int num_sms, int64_t max_units, cudaStream_t stream) {
+    return a.group <= 4 ? launch_one<D, NG, 4>(a, num_sms, max_units, stream)
+                        : launch_one<D, NG, 8>(a, num_sms, max_units, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_kvq_decode(const KvqDecodeArgs &a, int head_dim, cudaStream_t stream) {
-    const dim3 grid(unsigned(a.batch * a.num_kv_heads));
-    return head_dim == 128 ? launch_pdl(kvq_decode_kernel<128>, grid, dim3(128), 0, stream, a)
-                           : launch_pdl(kvq_decode_kernel<64>, grid, dim3(64), 0, stream, a);
+int kvq_decode_ctas(int num_sms) { return 2 * num_sms; }
+int kvq_decode_warps() { return kWarps; }
+
+cudaError_t launch_kvq_decode(KvqDecodeArgs a, int head_dim, int num_sms, cudaStream_t stream) {
+    const int64_t max_units = int64_t(a.batch) * a.num_kv_heads * (a.selected ? a.top_k : a.max_pages);
+    const int ng = head_dim / a.group_size;
+    if (head_dim == 128)
+        return ng == 1   ? launch_heads<128, 1>(a, num_sms, max_units, stream)
+               : ng == 2 ? launch_heads<128, 2>(a, num_sms, max_units, stream)
+                         : launch_heads<128, 4>(a, num_sms, max_units, stream);
+    return ng == 1 ? launch_heads<64, 1>(a, num_sms, max_units, stream)
+                   : launch_heads<64, 2>(a, num_sms, max_units, stream);
 }
 
 }  // namespace qskv

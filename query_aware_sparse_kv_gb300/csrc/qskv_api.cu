@@ -978,9 +978,29 @@ qskv_status qskv_kvq_meta_build(const void *pool, const int32_t *page_ids, const
                     "kvq_meta_build launch");
 }
 
+namespace {
+struct KvqWorkspace {
+    size_t tickets, part_ml, part_o, first_o, total;
+    KvqWorkspace(const qskv_shape *s, int num_sms) {
+        const size_t ctas = size_t(kvq_decode_ctas(num_sms));
+        const size_t piece = size_t(s->num_q_heads / s->num_kv_heads) * s->head_dim * 4;
+        tickets = 256;
+        part_ml = align256(tickets + size_t(s->batch) * s->num_kv_heads * 4);
+        part_o = part_ml + ctas * 2 * 16 * 4;
+        first_o = part_o + ctas * 2 * piece;
+        total = first_o + ctas * kvq_decode_warps() * piece;
+    }
+};
+}  // namespace
+
 size_t qskv_kvq_workspace_size(const qskv_shape *shape) {
     if (check_shape(shape) != QSKV_OK) return 0;
-    return 256;
+    const int sms = current_sm_count(nullptr);
+    if (sms <= 0) {
+        fail(QSKV_ERR_CUDA, "cannot query the current CUDA device");
+        return 0;
+    }
+    return KvqWorkspace(shape, sms).total;
 }
 
 qskv_status qskv_kvq_paged_decode(const void *q, qskv_dtype q_dtype, const void *pool, const int32_t *page_table,
@@ -1003,8 +1023,16 @@ qskv_status qskv_kvq_paged_decode(const void *q, qskv_dtype q_dtype, const void 
     const int64_t rows = int64_t(shape->batch) * shape->num_kv_heads;
     if (rows * (selected ? top_k : shape->max_pages) >= (int64_t(1) << 31))
         return fail(QSKV_ERR_UNSUPPORTED, "batch * num_kv_heads * %s must be < 2^31", selected ? "top_k" : "max_pages");
-    QSKV_TRY(check_workspace(workspace, workspace_bytes, qskv_kvq_workspace_size(shape)));
+    const int sms = current_sm_count(nullptr);
+    if (sms <= 0) return fail(QSKV_ERR_CUDA, "cannot query the current CUDA device");
+    const KvqWorkspace L(shape, sms);
+    QSKV_TRY(check_workspace(workspace, workspace_bytes, L.total));
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     KvqDecodeArgs a = {};
+    a.tickets = reinterpret_cast<uint32_t *>(ws + L.tickets);
+    a.part_ml = reinterpret_cast<float *>(ws + L.part_ml);
+    a.part_o = reinterpret_cast<float *>(ws + L.part_o);
+    a.first_o = reinterpret_cast<float *>(ws + L.first_o);
     a.q = q;
     a.pool = static_cast<const uint32_t *>(pool);
     a.page_table = page_table;
@@ -1026,7 +1054,7 @@ qskv_status qskv_kvq_paged_decode(const void *q, qskv_dtype q_dtype, const void 
     a.q_is_bf16 = q_dtype == QSKV_BF16;
     const float scale = sm_scale > 0.f ? sm_scale : 1.f / sqrtf(float(shape->head_dim));
     a.scale_log2 = scale * 1.4426950408889634f;
-    return launched(launch_kvq_decode(a, shape->head_dim, static_cast<cudaStream_t>(stream)),
+    return launched(launch_kvq_decode(a, shape->head_dim, sms, static_cast<cudaStream_t>(stream)),
                     "kvq_paged_decode launch");
 }
 

@@ -75,6 +75,11 @@ struct KvqDecodeArgs {
     int32_t batch, num_q_heads, num_kv_heads, group, page_size, max_pages, num_pool_pages, top_k, group_size;
     int32_t q_is_bf16;
     float scale_log2;                      // sm_scale * log2(e)
+    uint32_t *tickets;                     // [rows], zero between calls
+    float *part_ml;                        // [2 CTAs][2][8]: reference and weight sum of a CTA's open rows
+    float *part_o;                         // [2 CTAs][G][d]: their unnormalised outputs
+    float *first_o;                        // [CTAs][warps][G][d]: a warp's piece of a row that ends in its range
+    int32_t stages, min_units;             // ring stages a warp; fewest units a warp (set by the launcher)
 };
 
 struct TablesArgs {
@@ -87,7 +92,10 @@ struct TablesArgs {
 cudaError_t launch_kvq_append(const KvqStoreArgs &a, int dtype, int head_dim, cudaStream_t stream);
 cudaError_t launch_kvq_gather(const KvqStoreArgs &a, int dtype, int head_dim, cudaStream_t stream);
 cudaError_t launch_kvq_meta(const KvqMetaArgs &a, int meta_dtype, int head_dim, cudaStream_t stream);
-cudaError_t launch_kvq_decode(const KvqDecodeArgs &a, int head_dim, cudaStream_t stream);
+// Largest decode grid on a device with num_sms SMs, and its warps a CTA (for the workspace).
+int kvq_decode_ctas(int num_sms);
+int kvq_decode_warps();
+cudaError_t launch_kvq_decode(KvqDecodeArgs a, int head_dim, int num_sms, cudaStream_t stream);
 // Requests that one CTA of the page-table builder scans in shared memory.
 constexpr int kTablesScanRequests = 2048;
 // scratch: 3 (batch + 1) int32, used beyond kTablesScanRequests requests.
