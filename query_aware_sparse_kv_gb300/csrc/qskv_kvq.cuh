@@ -79,7 +79,8 @@ struct KvqDecodeArgs {
     float *part_ml;                        // [2 CTAs][2][8]: reference and weight sum of a CTA's open rows
     float *part_o;                         // [2 CTAs][G][d]: their unnormalised outputs
     float *first_o;                        // [CTAs][warps][G][d]: a warp's piece of a row that ends in its range
-    int32_t stages, min_units;             // ring stages a warp; fewest units a warp (set by the launcher)
+    int32_t stages, stage_units;           // ring stages a warp, pages a stage (set by the launcher)
+    int32_t row_ctas;                      // CTAs a row; 0: even split of all rows' units (set by the launcher)
 };
 
 struct TablesArgs {
