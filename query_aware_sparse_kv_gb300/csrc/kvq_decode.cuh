@@ -1,0 +1,914 @@
+// Attention of one query token a sequence over the 4-bit paged cache (format:
+// qskv_kvq.cuh).
+//
+// With k = m + s u per group j of dims, the logit of token t is
+//     l_t = scale * sum_j (s_tj (q_j . u_tj) + m_tj sum(q_j)),
+// and the output sum_t p_t (m_tj + s_tj u_t) over softmax weights p, so the
+// matrix products run on the codes u themselves and scales and minima are
+// applied per token and group, outside them.
+//
+// Bound: HBM.  A token and head is d + 8 NG bytes; the arithmetic on it has
+// to fit the time those take (23 bytes a clock and SM), which is what shapes
+// the inner loop:
+//   * a code is a fp16 number as it stands: the bits 0x000u are the subnormal
+//     u 2^-24 and 0x00u0 is 16 u 2^-24, both exact operands of the tensor
+//     cores.  A word of 8 codes becomes four fp16 pairs with four ANDs and one
+//     shift; the 16 is taken off the query (keys) or the output (values).
+//   * S (16 tokens x 8 columns) = K_tile Q^T and O^T (dims x 8) += V_tile^T P^T
+//     as mma.sync m16n8k16 with fp32 accumulators; at most 8 query heads share
+//     a cache row, so there is no 128-row tile to feed tcgen05 with.
+//   * fp32 precision from fp16 operands: queries (scaled by a power of two
+//     into fp16's range) and weights enter as two halves hi + lo.  With at
+//     most 4 heads (HC = 4) the halves share the 8 columns: column 2h is head
+//     h's hi, 2h + 1 its lo; with 8 heads they are two products.
+//   * a key's words lie so that a lane's operands are one vector load; values
+//     come through ldmatrix.trans, whose 16-bit elements are four codes of one
+//     token: the pair of a register is two tokens, as the product needs.
+//
+// Softmax.  Running references per head: M for the exponent and sg for the
+// weights times value scales (p s sg is what becomes fp16).  Both are moved
+// only when a weight would pass 2^12, or p s sg 2^9 (rare after the first
+// tile), so the usual tile has no rescaling and one vote.  Sums of weights
+// and of p m stay per lane until the row ends.
+//
+// Work split.  A unit is one page of one (sequence, KV head) row; all units
+// in row order are cut into equal ranges, one per warp of a grid of two CTAs
+// an SM.  Every CTA finds its range from a scan of the lengths (or selection
+// counts) in shared memory, so ragged batches balance exactly.  A warp keeps
+// its own ring of stages, one bulk copy a page, and its own running state; a
+// row that lies within a warp is finished by it, pieces of a row within a CTA
+// are folded in shared memory, and pieces of several CTAs by the CTA that
+// draws the row's last ticket, always in unit order: results do not depend on
+// timing.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "qskv_internal.h"
+#include "qskv_kvq.cuh"
+
+namespace qskv {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kEntries = 512;      // entries of the unit prefix held in shared memory
+constexpr int kFill = 16;          // units a warp describes at once (a multiple of the units a stage)
+constexpr int kRowModePages = 64, kRowCtas = 16;
+constexpr int kMaxRing = 8;        // stages a warp
+constexpr float kNoRef = -1e30f;   // M before the first token
+// Largest weight, and largest weight times value scale, in the references' units; the grid of the latter's hi half.
+constexpr float kTopP = 4096.f, kTopW = 511.f, kGridW = 0.25f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with a zero accumulator in.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Codes 0 and 4 of a word less 8, and codes 1 and 5 less 8 times 16: 0x6400 | x
+// is 1024 + x, exactly.  `k1024` holds 0x64006400 in a register the compiler
+// cannot see through, so that mask and magic are one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+    return r;
+}
+__device__ __forceinline__ uint32_t less8(uint32_t w, uint32_t k1024) {
+    return add_half2(and_or(w, 0x000f000fu, k1024), 0xe408e408u);
+}
+__device__ __forceinline__ uint32_t less8_16(uint32_t w, uint32_t k1024) {
+    return add_half2(and_or(w, 0x00f000f0u, k1024), 0xe480e480u);
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// x rounded to a multiple of `grid`, a power of two.  The hi halves of
+// queries and weights are multiples of one grid with at most 11 bits, so a
+// hi half times a code is exact and so are sums of them up to 2^24 grid
+// units: the tensor cores, which cut each product to the scale of the
+// largest, then cut nothing.
+__device__ __forceinline__ float on_grid(float x, float grid) {
+    const float c = 12582912.f * grid;  // 1.5 * 2^23 units
+    return (x + c) - c;
+}
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ float max_over_tokens(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float sum_over_tokens(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// ------------------------------------------------------------------ units --
+__device__ __forceinline__ int seq_of(const KvqDecodeArgs &a, int b) {
+    const int s = __ldg(a.seq_lens + b), cap = a.max_pages * a.page_size;
+    if (s < 0 || s > cap) {
+        raise_error(a.flags, kErrSeqLen);
+        return s < 0 ? 0 : cap;
+    }
+    return s;
+}
+__device__ __forceinline__ int pages_of(const KvqDecodeArgs &a, int b) {
+    return (seq_of(a, b) + a.page_size - 1) / a.page_size;
+}
+// Units of list item i: a row's selected pages, or all pages of a sequence
+// (of one of its KV heads).
+__device__ __forceinline__ int units_of(const KvqDecodeArgs &a, int i) {
+    if (!a.selected) return pages_of(a, i);
+    const int n = __ldg(a.n_selected + i), lim = min(a.top_k, pages_of(a, i / a.num_kv_heads));
+    if (n < 0 || n > lim) {
+        raise_error(a.flags, kErrSelected);
+        return max(0, min(n, lim));
+    }
+    return n;
+}
+
+struct Unit {
+    const uint8_t *src;  // its block; nullptr: skipped
+    int row_valid;       // row << 6 | valid tokens
+    int slot, count;     // its place among the row's units, and how many those are
+};
+
+struct Shared {
+    int prefix[kEntries + 1];
+    int warp_sum[kWarps];
+    Unit desc[kWarps][2 * kFill];
+    uint64_t bar[kWarps][kMaxRing];
+    // pieces of rows that no warp owns whole: 2w ends in, 2w + 1 runs on from, warp w's range
+    int piece_row[2 * kWarps], piece_begin[2 * kWarps], piece_end[2 * kWarps];
+    float piece_m[2 * kWarps][8], piece_l[2 * kWarps][8], piece_f[2 * kWarps][8];
+    // rows that other CTAs hold pieces of
+    int open, open_row[2], open_slot0[2], open_slot1[2], open_n[2], open_last[2];
+    float row_m[8], row_l[8];
+};
+
+// The unit of row `row` at place `slot` of `count`.
+__device__ __forceinline__ Unit unit_of(const KvqDecodeArgs &a, int row, int slot, int count, uint32_t block_bytes) {
+    const int b = row / a.num_kv_heads, seq = seq_of(a, b);
+    const int j = a.selected ? __ldg(a.selected + int64_t(row) * a.top_k + slot) : slot;
+    Unit r;
+    r.src = nullptr, r.row_valid = row << 6, r.slot = slot, r.count = count;
+    if (j < 0 || j * int64_t(a.page_size) >= seq) {
+        raise_error(a.flags, kErrSelected);
+        return r;
+    }
+    const int p = __ldg(a.page_table + int64_t(b) * a.max_pages + j);
+    if (p < 0 || p >= a.num_pool_pages) {
+        raise_error(a.flags, kErrPageId);
+        return r;
+    }
+    r.src = reinterpret_cast<const uint8_t *>(a.pool) + (int64_t(p) * a.num_kv_heads + row % a.num_kv_heads) * block_bytes;
+    r.row_valid |= min(a.page_size, seq - j * a.page_size);
+    return r;
+}
+
+// The unit with global index u (even split).
+__device__ __forceinline__ Unit unit_at(const KvqDecodeArgs &a, const Shared &s, int entries, int per, int u,
+                                        uint32_t block_bytes) {
+    int lo = 0, hi = entries;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s.prefix[mid] <= u)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int heads = a.selected ? 1 : a.num_kv_heads;  // rows of a list item
+    int i = lo * per, off = u - s.prefix[lo], n = units_of(a, i);
+    for (; off >= n * heads; n = units_of(a, i)) off -= n * heads, i++;
+    const int g = off / n;
+    return unit_of(a, i * heads + g, off - g * n, n, block_bytes);
+}
+
+// ----------------------------------------------------- one row in a warp --
+// Lane 4g + t of a warp works, for every 16-token tile, on tokens g and g + 8
+// and on head t (HC = 4) or heads 2t and 2t + 1 (HC = 8).
+template <int D, int NG, int HC, int P>
+struct RowState {
+    static constexpr int NW = D / 32;     // 32-dim chunks of a row; code words a lane holds of a token's key
+    static constexpr int GW = NW / NG;    // chunks a group
+    static constexpr int NH = HC / 4;     // heads a lane
+    uint32_t qh[NW][4], ql[HC == 8 ? NW : 1][4];
+    float qa[NH], qb[NH][NG];
+    float m[NH], l[NH], sg[NH], pm[NH][NG];
+    bool q_lo;  // HC = 8: the queries have lo halves (fp32 ones; bf16 fits fp16 as it is, half the products)
+    float o[NW][2][4];
+
+    __device__ __forceinline__ void load_query(const KvqDecodeArgs &a, int row) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const int h = HC == 4 ? g >> 1 : g;
+        q_lo = !a.q_is_bf16;
+        const int b = row / a.num_kv_heads, kh = row % a.num_kv_heads;
+        const int64_t at = (int64_t(b) * a.num_q_heads + kh * a.group + h) * D + 8 * t;
+        float q[NW][8];
+#pragma unroll
+        for (int i = 0; i < NW; i++) {
+            uint4 x = make_uint4(0, 0, 0, 0), y = x;
+            if (h < a.group) {
+                if (a.q_is_bf16) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at + 32 * i);
+                    x = make_uint4(w.x << 16, w.x & 0xffff0000u, w.y << 16, w.y & 0xffff0000u);
+                    y = make_uint4(w.z << 16, w.z & 0xffff0000u, w.w << 16, w.w & 0xffff0000u);
+                } else {
+                    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q) + at + 32 * i);
+                    x = p[0], y = p[1];
+                }
+            }
+            q[i][0] = __uint_as_float(x.x), q[i][1] = __uint_as_float(x.y), q[i][2] = __uint_as_float(x.z);
+            q[i][3] = __uint_as_float(x.w), q[i][4] = __uint_as_float(y.x), q[i][5] = __uint_as_float(y.y);
+            q[i][6] = __uint_as_float(y.z), q[i][7] = __uint_as_float(y.w);
+        }
+        float top = 0.f, sum[NG];
+#pragma unroll
+        for (int j = 0; j < NG; j++) sum[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NW; i++)
+#pragma unroll
+            for (int k = 0; k < 8; k++) top = fmaxf(top, fabsf(q[i][k])), sum[i / GW] += q[i][k];
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll
+        for (int j = 0; j < NG; j++) {
+            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
+            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
+            sum[j] *= a.scale_log2;
+        }
+        // q 2^(13 - e) has its largest entry in [2^13, 2^14): hi in multiples of 2^3, lo (at most 2^2) held times 2^11
+        const int e = min(max(int(__float_as_uint(top) >> 23) - 127, -100), 100);
+        const float up = __uint_as_float(uint32_t(140 - e) << 23);
+        const float back = __uint_as_float(uint32_t(127 + e + 11) << 23) * a.scale_log2;  // 2^24 / up
+#pragma unroll
+        for (int i = 0; i < NW; i++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {  // codes r and r + 4; odd r meets codes times 16
+                const float f = r & 1 ? up * 0.0625f : up;
+                const float x = q[i][r] * f, y = q[i][r + 4] * f;
+                float gx = on_grid(x, r & 1 ? 0.5f : 8.f), gy = on_grid(y, r & 1 ? 0.5f : 8.f);
+                if (HC == 8 && !q_lo) gx = x, gy = y;
+                const uint32_t hi = pack_half2(gx, gy), lo = pack_half2((x - gx) * 2048.f, (y - gy) * 2048.f);
+                if constexpr (HC == 4) {
+                    qh[i][r] = g & 1 ? lo : hi;
+                } else {
+                    qh[i][r] = hi;
+                    ql[i][r] = lo;
+                }
+            }
+#pragma unroll
+        for (int h2 = 0; h2 < NH; h2++) {
+            const int from = HC == 4 ? 8 * t : 8 * t + 4 * h2;
+            qa[h2] = __shfl_sync(0xffffffffu, back, from);
+#pragma unroll
+            for (int j = 0; j < NG; j++) qb[h2][j] = __shfl_sync(0xffffffffu, sum[j], from);
+        }
+    }
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int h = 0; h < NH; h++) {
+            m[h] = kNoRef, l[h] = 0.f, sg[h] = 1.f;
+#pragma unroll
+            for (int j = 0; j < NG; j++) pm[h][j] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < NW; c++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) o[c][0][r] = o[c][1][r] = 0.f;
+    }
+
+    // One 16-token tile: `tile` of the block at `st`, of which the first nv
+    // (1..16) tokens count.
+    __device__ __forceinline__ void tile(const uint8_t *st, int tile, int nv) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const int ta = tile * 16 + g;
+        // ---- keys: codes of tokens g and g + 8, logits
+        uint32_t ka[NW], kb[NW];
+        const uint8_t *kp = st + ta * (D / 2) + t * (D / 8);
+        if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(kp), y = *reinterpret_cast<const uint4 *>(kp + 4 * D);
+            ka[0] = x.x, ka[1] = x.y, ka[2] = x.z, ka[3] = x.w;
+            kb[0] = y.x, kb[1] = y.y, kb[2] = y.z, kb[3] = y.w;
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(kp), y = *reinterpret_cast<const uint2 *>(kp + 4 * D);
+            ka[0] = x.x, ka[1] = x.y, kb[0] = y.x, kb[1] = y.y;
+        }
+        const uint32_t *par = reinterpret_cast<const uint32_t *>(st + P * D) + ta;
+        uint32_t va[NG], vb[NG];
+        float x[2][NH], xm[2][NH];
+#pragma unroll
+        for (int h = 0; h < NH; h++) x[0][h] = x[1][h] = xm[0][h] = xm[1][h] = 0.f;
+#pragma unroll
+        for (int j = 0; j < NG; j++) {
+            const uint32_t pa = par[j * P], pb = par[j * P + 8];
+            va[j] = par[(NG + j) * P], vb[j] = par[(NG + j) * P + 8];
+            float c0[4], c1[4];
+            constexpr uint32_t lo = 0x000f000fu, hi = 0x00f000f0u;
+            constexpr float lo_unit = 1.f / 2048.f;
+            float ua[NH], ub[NH];
+            if constexpr (HC == 4) {  // two chains where a group has more than one chunk
+#pragma unroll
+                for (int i = 0; i < GW; i++) {
+                    const uint32_t a = ka[j * GW + i], b = kb[j * GW + i], a8 = a >> 8, b8 = b >> 8;
+                    const uint32_t(&q)[4] = qh[j * GW + i];
+                    if (i == 0) {
+                        mma_f16_first(c0, a & lo, b & lo, a & hi, b & hi, q[0], q[1]);
+                        if (GW > 1)
+                            mma_f16_first(c1, a8 & lo, b8 & lo, a8 & hi, b8 & hi, q[2], q[3]);
+                        else
+                            mma_f16(c0, a8 & lo, b8 & lo, a8 & hi, b8 & hi, q[2], q[3]);
+                    } else {
+                        mma_f16(c0, a & lo, b & lo, a & hi, b & hi, q[0], q[1]);
+                        mma_f16(c1, a8 & lo, b8 & lo, a8 & hi, b8 & hi, q[2], q[3]);
+                    }
+                }
+                if (GW > 1) c0[0] += c1[0], c0[1] += c1[1], c0[2] += c1[2], c0[3] += c1[3];
+                ua[0] = fmaf(c0[1], lo_unit, c0[0]);
+                ub[0] = fmaf(c0[3], lo_unit, c0[2]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < GW; i++) {
+                    const uint32_t a = ka[j * GW + i], b = kb[j * GW + i], a8 = a >> 8, b8 = b >> 8;
+                    if (i == 0)
+                        mma_f16_first(c0, a & lo, b & lo, a & hi, b & hi, qh[j * GW + i][0], qh[j * GW + i][1]);
+                    else
+                        mma_f16(c0, a & lo, b & lo, a & hi, b & hi, qh[j * GW + i][0], qh[j * GW + i][1]);
+                    mma_f16(c0, a8 & lo, b8 & lo, a8 & hi, b8 & hi, qh[j * GW + i][2], qh[j * GW + i][3]);
+                }
+                if (q_lo) {
+#pragma unroll
+                    for (int i = 0; i < GW; i++) {
+                        const uint32_t a = ka[j * GW + i], b = kb[j * GW + i], a8 = a >> 8, b8 = b >> 8;
+                        if (i == 0)
+                            mma_f16_first(c1, a & lo, b & lo, a & hi, b & hi, ql[j * GW + i][0], ql[j * GW + i][1]);
+                        else
+                            mma_f16(c1, a & lo, b & lo, a & hi, b & hi, ql[j * GW + i][0], ql[j * GW + i][1]);
+                        mma_f16(c1, a8 & lo, b8 & lo, a8 & hi, b8 & hi, ql[j * GW + i][2], ql[j * GW + i][3]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; k++) c0[k] = fmaf(c1[k], lo_unit, c0[k]);
+                }
+                ua[0] = c0[0], ua[NH - 1] = c0[1];
+                ub[0] = c0[2], ub[NH - 1] = c0[3];
+            }
+            const float sa = bf16_lo_to_float(pa), ma = bf16_hi_to_float(pa);
+            const float sb = bf16_lo_to_float(pb), mb = bf16_hi_to_float(pb);
+#pragma unroll
+            for (int h = 0; h < NH; h++) {
+                x[0][h] = fmaf(sa, ua[h], x[0][h]), xm[0][h] = fmaf(ma, qb[h][j], xm[0][h]);
+                x[1][h] = fmaf(sb, ub[h], x[1][h]), xm[1][h] = fmaf(mb, qb[h][j], xm[1][h]);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < NH; h++) x[0][h] = fmaf(qa[h], x[0][h], xm[0][h]), x[1][h] = fmaf(qa[h], x[1][h], xm[1][h]);
+        if (nv < 16) {  // places past the end: no weight, and nothing of their params
+            const bool off_a = g >= nv, off_b = g + 8 >= nv;
+#pragma unroll
+            for (int h = 0; h < NH; h++) {
+                if (off_a) x[0][h] = -INFINITY;
+                if (off_b) x[1][h] = -INFINITY;
+            }
+#pragma unroll
+            for (int j = 0; j < NG; j++) {
+                if (off_a) va[j] = 0;
+                if (off_b) vb[j] = 0;
+            }
+        }
+        // ---- weights
+        float p[2][NH], w[2][NH][NG];
+        float most_p = 0.f, most_w = 0.f;
+        bool calm = true;
+#pragma unroll
+        for (int h = 0; h < NH; h++) {
+            p[0][h] = ex2(x[0][h] - m[h]), p[1][h] = ex2(x[1][h] - m[h]);
+            most_p = fmaxf(most_p, fmaxf(p[0][h], p[1][h]));
+            const float ps0 = p[0][h] * sg[h], ps1 = p[1][h] * sg[h];
+#pragma unroll
+            for (int j = 0; j < NG; j++) {
+                w[0][h][j] = ps0 * bf16_lo_to_float(va[j]);
+                w[1][h][j] = ps1 * bf16_lo_to_float(vb[j]);
+                most_w = fmaxf(most_w, fmaxf(w[0][h][j], w[1][h][j]));
+            }
+        }
+        calm = most_p <= kTopP && most_w <= kTopW;
+        if (!__all_sync(0xffffffffu, calm)) {
+#pragma unroll
+            for (int h = 0; h < NH; h++) {
+                const float mn = fmaxf(m[h], max_over_tokens(fmaxf(x[0][h], x[1][h])));
+                const float f = ex2(m[h] - mn);
+                p[0][h] = ex2(x[0][h] - mn), p[1][h] = ex2(x[1][h] - mn);
+                float top = 0.f;
+#pragma unroll
+                for (int j = 0; j < NG; j++)
+                    top = fmaxf(top, fmaxf(p[0][h] * bf16_lo_to_float(va[j]), p[1][h] * bf16_lo_to_float(vb[j])));
+                top = max_over_tokens(top);
+                // sg such that the tile's largest p s sg lies in [2^6, 2^7); what is summed already may grow by 2^30
+                float s = sg[h];
+                if (top >= 7.888609052210118e-31f) {  // 2^-100
+                    s = __uint_as_float((260u << 23) - (__float_as_uint(top) & 0x7f800000u));
+                    if (m[h] != kNoRef) s = fminf(s, sg[h] * 1073741824.f);
+                }
+                const float r = f * (s / sg[h]);
+                m[h] = mn, sg[h] = s, l[h] *= f;
+#pragma unroll
+                for (int j = 0; j < NG; j++) {
+                    pm[h][j] *= f;
+                    w[0][h][j] = p[0][h] * (bf16_lo_to_float(va[j]) * s);
+                    w[1][h][j] = p[1][h] * (bf16_lo_to_float(vb[j]) * s);
+                }
+#pragma unroll
+                for (int c = 0; c < NW; c++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        if (HC == 4 || (k & 1) == h) o[c][0][k] *= r, o[c][1][k] *= r;
+            }
+        }
+        // the value codes enter their product less 8 (sums of signed numbers: the tensor cores cut what they add
+        // towards zero, which on 0..15 is a bias), so pm takes the middle m + 8 s of each group
+#pragma unroll
+        for (int h = 0; h < NH; h++) l[h] += p[0][h] + p[1][h];
+#pragma unroll
+        for (int j = 0; j < NG; j++) {
+            const float mida = fmaf(8.f, bf16_lo_to_float(va[j]), bf16_hi_to_float(va[j]));
+            const float midb = fmaf(8.f, bf16_lo_to_float(vb[j]), bf16_hi_to_float(vb[j]));
+#pragma unroll
+            for (int h = 0; h < NH; h++) pm[h][j] = fmaf(p[1][h], midb, fmaf(p[0][h], mida, pm[h][j]));
+        }
+        // ---- values
+        const int mat = lane >> 3, r = lane & 7;
+        const int token = tile * 16 + (mat & 1) * 8 + r;
+        const int sw = D == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
+        const uint32_t vrow = smem_u32(st) + P * (D / 2) + token * (D / 2);
+        uint32_t bh[2], bl[2], k1024;
+        asm("mov.b32 %0, 0x64006400;" : "=r"(k1024));
+#pragma unroll
+        for (int c2 = 0; c2 < NW / 2; c2++) {
+            uint32_t v[4];
+            ldmatrix_x4_trans(v, vrow + (((2 * c2 + (mat >> 1)) ^ sw) << 4));
+#pragma unroll
+            for (int cc = 0; cc < 2; cc++) {
+                const int c = 2 * c2 + cc;
+                if (c % GW == 0) {
+                    const int j = c / GW;
+                    if constexpr (HC == 4) {
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            const float x = on_grid(w[k][0][j], kGridW);
+                            bh[k] = movmatrix_trans(pack_half2(x, w[k][0][j] - x));
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            const float x = on_grid(w[k][0][j], kGridW), y = on_grid(w[k][NH - 1][j], kGridW);
+                            bh[k] = movmatrix_trans(pack_half2(x, y));
+                            bl[k] = movmatrix_trans(pack_half2(w[k][0][j] - x, w[k][NH - 1][j] - y));
+                        }
+                    }
+                }
+                const uint32_t v0 = v[2 * cc], v1 = v[2 * cc + 1];
+                const uint32_t w0 = v0 >> 8, w1 = v1 >> 8;
+                const uint32_t a[4] = {less8(v0, k1024), less8_16(v0, k1024), less8(v1, k1024), less8_16(v1, k1024)};
+                const uint32_t b[4] = {less8(w0, k1024), less8_16(w0, k1024), less8(w1, k1024), less8_16(w1, k1024)};
+                mma_f16(o[c][0], a[0], a[1], a[2], a[3], bh[0], bh[1]);
+                mma_f16(o[c][1], b[0], b[1], b[2], b[3], bh[0], bh[1]);
+                if constexpr (HC == 8) {
+                    mma_f16(o[c][0], a[0], a[1], a[2], a[3], bl[0], bl[1]);
+                    mma_f16(o[c][1], b[0], b[1], b[2], b[3], bl[0], bl[1]);
+                }
+            }
+        }
+    }
+
+    // Sums over the lanes; the row's outputs (final) or its piece's reference,
+    // weight sum and unnormalised output.
+    __device__ __forceinline__ void finish(const KvqDecodeArgs &a, int row, bool final, float *piece_o, float *piece_m,
+                                           float *piece_l) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const int64_t head0 = int64_t(row / a.num_kv_heads) * a.num_q_heads + int64_t(row % a.num_kv_heads) * a.group;
+#pragma unroll
+        for (int h = 0; h < NH; h++) {
+            l[h] = sum_over_tokens(l[h]);
+#pragma unroll
+            for (int j = 0; j < NG; j++) pm[h][j] = sum_over_tokens(pm[h][j]);
+            const int head = NH * t + h;
+            if (head >= a.group) continue;
+            const float unit = 1.f / sg[h];
+            const float inv = !final ? 1.f : l[h] > 0.f ? 1.f / l[h] : 0.f;
+            float *dst = final ? a.out + (head0 + head) * D : piece_o + head * D;
+#pragma unroll
+            for (int c = 0; c < NW; c++) {
+                const float base = pm[h][c / GW];
+                float v[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const float *q = o[c][k >> 1] + 2 * (k & 1);
+                    const float sum = HC == 4 ? q[0] + q[1] : q[h];
+                    v[k] = fmaf(sum, k & 1 ? unit * 0.0625f : unit, base) * inv;
+                }
+                *reinterpret_cast<float4 *>(dst + 32 * c + 4 * g) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+            if (g == 0) {
+                if (final) {
+                    if (a.lse) a.lse[head0 + head] = l[h] > 0.f ? (m[h] + log2f(l[h])) * kLn2 : -INFINITY;
+                } else {
+                    piece_m[head] = m[h], piece_l[head] = l[h];
+                }
+            }
+        }
+    }
+};
+
+// --------------------------------------------------------- the kernel --
+template <int D, int NG, int HC, int P>
+__global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a) {
+    extern __shared__ __align__(128) uint8_t ring_mem[];
+    __shared__ Shared s;
+    pdl_trigger();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int U = 4096 / (P * D), kPageTiles = P / 16, kTiles = U * kPageTiles;
+    constexpr uint32_t block_bytes = kvq_block_words(D, P, NG) * 4;
+    static_assert(U >= 1 && kFill % U == 0, "a stage is a whole number of pages, a fill of stages");
+    const int G = a.group, S = a.stages;
+    uint8_t *ring = ring_mem + warp * (S * U * block_bytes);
+    if (lane < S) mbar_init(&s.bar[warp][lane], 1);
+    if (tid < 2 * kWarps) s.piece_row[tid] = -1;
+    if (tid == 0) s.open = 0;
+    mbar_fence_init();
+    if (a.selected) pdl_wait();  // the lengths may be read earlier, the selection not
+
+    // ---- this warp's units [u0, u1): of its CTA's row, or of all rows in order
+    int u0, u1, cta_begin, cta_end;
+    int entries = 0, per = 1, upc;
+    const int row0 = a.row_ctas ? blockIdx.x / a.row_ctas : 0;
+    int count0 = 0;
+    if (a.row_ctas) {
+        count0 = units_of(a, a.selected ? row0 : row0 / a.num_kv_heads);
+        upc = (count0 + a.row_ctas - 1) / a.row_ctas;
+        const int part = blockIdx.x - row0 * a.row_ctas;
+        cta_begin = min(part * upc, count0), cta_end = min(cta_begin + upc, count0);
+        const int n = cta_end - cta_begin;
+        u0 = cta_begin + n * warp / kWarps, u1 = cta_begin + n * (warp + 1) / kWarps;
+        __syncwarp();
+        if (!a.selected) pdl_wait();
+        if (count0 == 0 && part == 0) {
+            const int64_t h0 = int64_t(row0 / a.num_kv_heads) * a.num_q_heads + int64_t(row0 % a.num_kv_heads) * G;
+            for (int c = tid; c < G * D / 4; c += kThreads)
+                reinterpret_cast<float4 *>(a.out + h0 * D)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (a.lse && tid < G) a.lse[h0 + tid] = -INFINITY;
+        }
+    } else {
+        // prefix of the units over the list (rows, or sequences)
+        const int heads = a.selected ? 1 : a.num_kv_heads;
+        const int items = a.selected ? a.batch * a.num_kv_heads : a.batch;
+        per = (items + kEntries - 1) / kEntries, entries = (items + per - 1) / per;
+        const int ept = (entries + kThreads - 1) / kThreads;
+        int mine = 0;
+        for (int e = tid * ept; e < min((tid + 1) * ept, entries); e++) {
+            int n = 0;
+            for (int i = e * per; i < min((e + 1) * per, items); i++) n += units_of(a, i) * heads;
+            s.prefix[e] = n;
+            mine += n;
+        }
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31) s.warp_sum[warp] = incl;
+        __syncthreads();
+        int before = incl - mine, total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            if (w < warp) before += s.warp_sum[w];
+            total += s.warp_sum[w];
+        }
+        for (int e = tid * ept; e < min((tid + 1) * ept, entries); e++) {
+            const int n = s.prefix[e];
+            s.prefix[e] = before;
+            before += n;
+        }
+        __syncthreads();
+        const int all_warps = gridDim.x * kWarps;
+        const int upw = max(int((uint32_t(total) + all_warps - 1) / all_warps), 1);
+        upc = upw * kWarps;
+        const int64_t c0 = int64_t(blockIdx.x) * upc;
+        u0 = int(min(c0 + int64_t(warp) * upw, int64_t(total))), u1 = int(min(int64_t(u0) + upw, int64_t(total)));
+        cta_begin = int(min(c0, int64_t(total))), cta_end = int(min(c0 + upc, int64_t(total)));
+        if (!a.selected) pdl_wait();
+        // rows without a token or a selected page
+        for (int base = blockIdx.x * kWarps + warp; base < items; base += 32 * all_warps) {
+            const int64_t i = base + int64_t(lane) * all_warps;
+            uint32_t none = __ballot_sync(0xffffffffu, i < items && units_of(a, int(i)) == 0);
+            while (none) {
+                const int k = __ffs(none) - 1;
+                none &= none - 1;
+                const int item_heads = a.selected ? G : a.num_q_heads;
+                const int64_t h0 = int64_t(base + k * all_warps) * item_heads;  // a row's, or a sequence's, lie together
+                for (int c = lane; c < item_heads * D / 4; c += 32)
+                    reinterpret_cast<float4 *>(a.out + h0 * D)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (a.lse)
+                    for (int h = lane; h < item_heads; h += 32) a.lse[h0 + h] = -INFINITY;
+            }
+        }
+    }
+    __syncthreads();  // piece_row, open
+
+    // ---- the warp's pipeline: stage k holds units kU .. kU + U - 1 of its range
+    const int n = u1 - u0, stages = (n + U - 1) / U;
+    int put = 0, got = 0, parity = 0;
+    uint32_t plain = 0;  // bit per ring stage: all its units are whole pages of the row before them
+    auto issue = [&](int k) {
+        if (k >= stages) return;
+        const int first = k * U;
+        if (first % kFill == 0) {  // describe the next kFill units
+            __syncwarp();
+            const int u = u0 + first + lane;
+            if (lane < kFill && u < u1)
+                s.desc[warp][(first + lane) % (2 * kFill)] = a.row_ctas ? unit_of(a, row0, u, count0, block_bytes)
+                                                                        : unit_at(a, s, entries, per, u, block_bytes);
+            __syncwarp();
+        }
+        const uint8_t *src = nullptr;
+        bool same = true;
+        if (lane < U) {
+            same = first + lane < n;
+            if (same) {
+                const Unit &d = s.desc[warp][(first + lane) % (2 * kFill)];
+                src = d.src;
+                same = src && first > 0 &&
+                       d.row_valid == ((s.desc[warp][(first + lane - 1) % (2 * kFill)].row_valid & ~63) | P);
+            }
+        }
+        const uint32_t live = __ballot_sync(0xffffffffu, src != nullptr);
+        same = __all_sync(0xffffffffu, same);
+        plain = (plain & ~(1u << put)) | (uint32_t(same) << put);
+        uint64_t *bar = &s.bar[warp][put];
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(live) * block_bytes);
+        __syncwarp();
+        if (src) bulk_load(ring + (put * U + lane) * block_bytes, src, block_bytes, bar);
+        if (++put == S) put = 0;
+    };
+    RowState<D, NG, HC, P> st;
+    int row = -1, row_begin = 0, row_end = 0;
+    float *piece_first = a.first_o + (int64_t(blockIdx.x) * kWarps + warp) * (G * D);
+    auto close = [&](bool at_end) {
+        const bool final = row_begin >= u0 && row_end <= u1;
+        const int k = 2 * warp + (at_end ? 1 : 0);
+        st.finish(a, row, final, at_end ? reinterpret_cast<float *>(ring) : piece_first, s.piece_m[k], s.piece_l[k]);
+        if (!final && lane == 0) s.piece_row[k] = row, s.piece_begin[k] = row_begin, s.piece_end[k] = row_end;
+    };
+    auto enter = [&](const Unit &u, int it) {  // the state moves to the row of the warp's unit `it`
+        if ((u.row_valid >> 6) == row) return;
+        if (row >= 0) close(false);
+        row = u.row_valid >> 6, row_begin = u0 + it - u.slot, row_end = row_begin + u.count;
+        st.load_query(a, row);
+        st.clear();
+    };
+    for (int k = 0; k < S; k++) issue(k);
+    for (int k = 0; k < stages; k++) {
+        const bool same = (plain >> got) & 1;
+        if (!same) enter(s.desc[warp][k * U % (2 * kFill)], k * U);  // its query loads while the pages are on their way
+        if (!mbar_wait_bounded(&s.bar[warp][got], parity, kWaitLimitNs)) {
+            // a lost copy: flagged, the rest is given up once the copies in flight had their time
+            if (lane == 0) raise_error(a.flags, kErrTimeout);
+            for (int i = k + 1; i < min(k + S, stages); i++) {
+                if (++got == S) got = 0, parity ^= 1;
+                mbar_wait_bounded(&s.bar[warp][got], parity, kWaitLimitNs);
+            }
+            break;
+        }
+        const uint8_t *stage = ring + got * (U * block_bytes);
+#pragma unroll 1
+        for (int t = 0; t < kTiles; t++) {
+            int nv = 16;
+            if (!same) {
+                const int it = k * U + t / kPageTiles;
+                if (it >= n) break;
+                const Unit u = s.desc[warp][it % (2 * kFill)];
+                enter(u, it);
+                nv = min((u.row_valid & 63) - t % kPageTiles * 16, 16);
+                if (!u.src || nv <= 0) continue;
+            }
+            st.tile(stage + t / kPageTiles * block_bytes, t % kPageTiles, nv);
+        }
+        if (++got == S) got = 0, parity ^= 1;
+        __syncwarp();
+        issue(k + S);
+    }
+    if (row >= 0) close(true);
+    __syncthreads();
+
+    // ---- pieces of one row within the CTA, in unit order
+    const int elems = G * D / 4;
+    if (tid < 16 * kWarps) {  // weight of each piece for each head
+        const int k = tid >> 3, h = tid & 7, r = s.piece_row[k];
+        if (r >= 0 && h < G) {
+            float m = kNoRef;
+#pragma unroll
+            for (int i = 0; i < 2 * kWarps; i++)
+                if (s.piece_row[i] == r) m = fmaxf(m, s.piece_m[i][h]);
+            s.piece_f[k][h] = ex2(s.piece_m[k][h] - m);
+        }
+    }
+    __syncthreads();
+    for (int i = 0; i < 2 * kWarps;) {
+        const int r = s.piece_row[i];
+        if (r < 0) {
+            i++;
+            continue;
+        }
+        int end = i + 1;
+        while (end < 2 * kWarps && (s.piece_row[end] < 0 || s.piece_row[end] == r)) end++;
+        const int begin_u = s.piece_begin[i], end_u = s.piece_end[i];
+        const bool whole = begin_u >= cta_begin && end_u <= cta_end;
+        const int slot = a.row_ctas ? blockIdx.x : 2 * blockIdx.x + (begin_u < cta_begin ? 0 : 1);
+        const int64_t head0 = int64_t(r / a.num_kv_heads) * a.num_q_heads + int64_t(r % a.num_kv_heads) * G;
+        for (int e = tid; e < elems; e += kThreads) {
+            const int h = e * 4 / D;
+            float m = kNoRef, l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = i; k < end; k++) {
+                if (s.piece_row[k] < 0) continue;
+                const float f = s.piece_f[k][h];
+                const float *src = k & 1 ? reinterpret_cast<const float *>(ring_mem + (k >> 1) * (S * U * block_bytes))
+                                         : a.first_o + (int64_t(blockIdx.x) * kWarps + (k >> 1)) * (G * D);
+                const float4 v = reinterpret_cast<const float4 *>(src)[e];
+                l = fmaf(f, s.piece_l[k][h], l), m = fmaxf(m, s.piece_m[k][h]);
+                o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+            }
+            if (whole) {
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                reinterpret_cast<float4 *>(a.out + head0 * D)[e] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                if (a.lse && e * 4 % D == 0) a.lse[head0 + h] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            } else {
+                reinterpret_cast<float4 *>(a.part_o)[int64_t(slot) * elems + e] = o;
+                if (e * 4 % D == 0) a.part_ml[slot * 16 + h] = m, a.part_ml[slot * 16 + 8 + h] = l;
+            }
+        }
+        if (!whole && tid == 0) {  // at most two: one that begins before, one that ends after the CTA's range
+            const int x = s.open++;
+            s.open_row[x] = r;
+            if (a.row_ctas) {
+                s.open_slot0[x] = s.open_slot1[x] = row0 * a.row_ctas;
+                s.open_n[x] = (count0 + upc - 1) / upc;
+            } else {  // the CTA where a row begins wrote its slot 1, the later ones their slot 0
+                const int c = begin_u / upc;
+                s.open_slot0[x] = 2 * c + 1, s.open_slot1[x] = 2 * c;
+                s.open_n[x] = (end_u - 1) / upc - c + 1;
+            }
+        }
+        i = end;
+    }
+    __threadfence();
+    __syncthreads();
+    if (s.open == 0) return;
+    if (tid < s.open) {
+        const bool last = atomicAdd(a.tickets + s.open_row[tid], 1u) == uint32_t(s.open_n[tid] - 1);
+        if (last) a.tickets[s.open_row[tid]] = 0;
+        s.open_last[tid] = last;
+    }
+    __syncthreads();
+
+    // ---- rows whose last ticket this CTA drew: pieces of several CTAs, in unit order
+    for (int f = 0; f < s.open; f++) {
+        if (!s.open_last[f]) continue;
+        const int r = s.open_row[f], np = s.open_n[f], slot0 = s.open_slot0[f], slot1 = s.open_slot1[f];
+        const int step = a.row_ctas ? 1 : 2;
+        float *pw = reinterpret_cast<float *>(ring_mem);  // [np][G] weights, then [kThreads] float4
+        float4 *red = reinterpret_cast<float4 *>(ring_mem + (size_t(np) * G * 4 + 15) / 16 * 16);
+        __threadfence();
+        const int groups = kThreads / elems, grp = tid / elems, e = tid % elems, h = e * 4 / D;
+        auto piece = [&](int k) {
+            const int slot = k == 0 ? slot0 : slot1 + k * step;
+            return __ldcg(reinterpret_cast<const float4 *>(a.part_o) + int64_t(slot) * elems + e);
+        };
+        float4 early[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (grp + i * groups < np) early[i] = piece(grp + i * groups);
+        if (warp < G) {
+            float m = kNoRef, l = 0.f;
+            for (int k = lane; k < np; k += 32) {
+                const int slot = k == 0 ? slot0 : slot1 + k * step;
+                const float x = __ldcg(a.part_ml + slot * 16 + warp), y = __ldcg(a.part_ml + slot * 16 + 8 + warp);
+                const float mn = fmaxf(m, x);
+                l = fmaf(l, ex2(m - mn), y * ex2(x - mn));
+                pw[k * G + warp] = x;
+                m = mn;
+            }
+            float top = m;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            l *= ex2(m - top);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            for (int k = lane; k < np; k += 32) pw[k * G + warp] = ex2(pw[k * G + warp] - top);
+            if (lane == 0) s.row_m[warp] = top, s.row_l[warp] = l;
+        }
+        __syncthreads();
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](const float4 &v, int k) {
+            const float x = pw[k * G + h];
+            o.x = fmaf(x, v.x, o.x), o.y = fmaf(x, v.y, o.y), o.z = fmaf(x, v.z, o.z), o.w = fmaf(x, v.w, o.w);
+        };
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (grp + i * groups < np) add(early[i], grp + i * groups);
+#pragma unroll 4
+        for (int k = grp + 4 * groups; k < np; k += groups) add(piece(k), k);
+        red[tid] = o;
+        __syncthreads();
+        if (grp == 0) {
+            for (int k = 1; k < groups; k++) {
+                const float4 v = red[k * elems + e];
+                o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+            }
+            const float l = s.row_l[h], inv = l > 0.f ? 1.f / l : 0.f;
+            const int64_t head0 = int64_t(r / a.num_kv_heads) * a.num_q_heads + int64_t(r % a.num_kv_heads) * G;
+            reinterpret_cast<float4 *>(a.out + head0 * D)[e] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+            if (a.lse && e * 4 % D == 0) a.lse[head0 + h] = l > 0.f ? (s.row_m[h] + log2f(l)) * kLn2 : -INFINITY;
+        }
+        __syncthreads();
+    }
+}
+
+// Shared memory a CTA may take beside its static part with two CTAs an SM
+// (228 KB an SM, 1 KB of each CTA's reserved).
+constexpr int kRingBudget = 113 * 1024 - int(sizeof(Shared));
+
+template <int D, int NG, int HC, int P>
+cudaError_t launch_one(KvqDecodeArgs &a, int num_sms, cudaStream_t stream) {
+    // a stage is about 4 KB: with fewer pages its fixed cost shows, with more the ring has too few stages
+    constexpr int stage = kWarps * (4096 / (P * D)) * kvq_block_words(D, P, NG) * 4;
+    constexpr int stages = kRingBudget / stage < kMaxRing ? kRingBudget / stage : kMaxRing;
+    static_assert(stages >= 2, "the ring needs two stages");
+    a.stages = stages;
+    const int rows = a.batch * a.num_kv_heads, slots = kvq_decode_ctas(num_sms);
+    const int row_units = a.selected ? a.top_k : a.max_pages;
+    a.row_ctas = 0;
+    if (rows <= slots && (a.selected || row_units <= kRowModePages)) {
+        const int most = slots / rows, want = (row_units + kWarps - 1) / kWarps;
+        a.row_ctas = want < most ? want : most;
+        if (a.row_ctas > kRowCtas) a.row_ctas = kRowCtas;
+    }
+    const int64_t even = (int64_t(rows) * row_units + kWarps - 1) / kWarps;
+    const unsigned grid = a.row_ctas ? unsigned(rows * a.row_ctas) : unsigned(even < slots ? even : slots);
+    const cudaError_t e = cudaFuncSetAttribute(kvq_decode_kernel<D, NG, HC, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               stages * stage);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kvq_decode_kernel<D, NG, HC, P>, dim3(grid), dim3(kThreads), stages * stage, stream, a);
+}
+
+template <int P>
+cudaError_t launch_page(KvqDecodeArgs &a, int head_dim, int num_sms, cudaStream_t stream) {
+    const int ng = head_dim / a.group_size;
+    const bool few = a.group <= 4;
+    if (head_dim == 128) {
+        if (ng == 1) return few ? launch_one<128, 1, 4, P>(a, num_sms, stream) : launch_one<128, 1, 8, P>(a, num_sms, stream);
+        if (ng == 2) return few ? launch_one<128, 2, 4, P>(a, num_sms, stream) : launch_one<128, 2, 8, P>(a, num_sms, stream);
+        return few ? launch_one<128, 4, 4, P>(a, num_sms, stream) : launch_one<128, 4, 8, P>(a, num_sms, stream);
+    }
+    if (ng == 1) return few ? launch_one<64, 1, 4, P>(a, num_sms, stream) : launch_one<64, 1, 8, P>(a, num_sms, stream);
+    return few ? launch_one<64, 2, 4, P>(a, num_sms, stream) : launch_one<64, 2, 8, P>(a, num_sms, stream);
+}
+
+}  // namespace
+}  // namespace qskv

@@ -79,7 +79,7 @@ struct KvqDecodeArgs {
     float *part_ml;                        // [2 CTAs][2][8]: reference and weight sum of a CTA's open rows
     float *part_o;                         // [2 CTAs][G][d]: their unnormalised outputs
     float *first_o;                        // [CTAs][warps][G][d]: a warp's piece of a row that ends in its range
-    int32_t stages, stage_units;           // ring stages a warp, pages a stage (set by the launcher)
+    int32_t stages;                        // ring stages a warp (set by the launcher)
     int32_t row_ctas;                      // CTAs a row; 0: even split of all rows' units (set by the launcher)
 };
 
@@ -96,6 +96,7 @@ cudaError_t launch_kvq_meta(const KvqMetaArgs &a, int meta_dtype, int head_dim, 
 // Largest decode grid on a device with num_sms SMs, and its warps a CTA (for the workspace).
 int kvq_decode_ctas(int num_sms);
 int kvq_decode_warps();
+cudaError_t launch_kvq_decode_page32(KvqDecodeArgs a, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_kvq_decode(KvqDecodeArgs a, int head_dim, int num_sms, cudaStream_t stream);
 // Requests that one CTA of the page-table builder scans in shared memory.
 constexpr int kTablesScanRequests = 2048;
