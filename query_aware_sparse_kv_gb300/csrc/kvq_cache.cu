@@ -36,137 +36,211 @@ __device__ __forceinline__ float kvq_scale(float mx, float m) {
 }
 
 // rint((x - m) / s) clamped to [0, 15], ties to even, of the exact quotient.
-// d * (1 / s) is within 3 ulp of it (15.5 * 3 * 2^-24 < 2^-18), so rounding
-// it is right unless it lies within 2^-16 of a half; there the sign of the
-// exact remainder against that half decides.
-__device__ __forceinline__ uint32_t kvq_code(float x, float m, float s, float inv) {
-    const float d = x - m;
-    const float q = fminf(fmaxf(d * inv, -1.f), 17.f);
-    float u = rintf(q);
-    if (fabsf(q - u) > 0.5f - 1.52587890625e-5f) {
-        const float k = floorf(q);
-        float dd, err;
-        exact_diff(x, m, dd, err);
-        const float rem = fmaf(-(k + 0.5f), s, dd) + err;
-        u = rem > 0.f ? k + 1.f : (rem < 0.f ? k : 2.f * rintf(0.5f * k + 0.25f));
-    }
-    u = fminf(fmaxf(u, 0.f), 15.f);
-    return __float_as_uint(u + 8388608.f) & 15u;
+__device__ __noinline__ uint32_t kvq_code_exact(float x, float m, float s) {
+    float d, err;
+    exact_diff(x, m, d, err);
+    const float k = fminf(fmaxf(floorf(d / s), -1.f), 16.f);
+    // the quotient is within 2^-18 of d / s: k is its floor unless it lies that close to a whole number, where
+    // the comparison with k + 1/2 still rounds it right
+    const float rem = fmaf(-(k + 0.5f), s, d) + err;
+    const float u = rem > 0.f ? k + 1.f : (rem < 0.f ? k : 2.f * rintf(0.5f * k + 0.25f));
+    return uint32_t(fminf(fmaxf(u, 0.f), 15.f));
 }
 
-template <bool BF16>
-__device__ __forceinline__ void load8(const void *base, int64_t at, float (&x)[8]) {
-    if constexpr (BF16) {
-        const uint4 w = ldg_stream_v4(static_cast<const uint16_t *>(base) + at);
-        const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+// Code word of 8 values.  d * (1 / s) is within 2^-18 of the exact quotient
+// (three roundings of 2^-23 of at most 15.1), so adding it to 1.5 2^23 rounds
+// it right unless it lies within 2^-16 of a half; a word with such a value is
+// done again on exact remainders.  The rounded quotient's bits are the code
+// plus a constant; `acc * 16 + bits` packs them and the constants' sum is
+// taken off at the end.  CLAMP: m may lie above the smallest value (fp32
+// inputs, whose minimum is rounded); a bf16 minimum is exact, and then the
+// quotients are 0 to 15.06 and round into range by themselves.
+template <bool CLAMP>
+__device__ __forceinline__ uint32_t kvq_word(const float (&x)[8], float m, float s) {
+    constexpr float magic = 12582912.f;  // 1.5 * 2^23, bits 0x4b400000
+    constexpr uint32_t sum16 = 0x11111111u * 0x4b400000u;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    uint32_t acc = 0;
+    float off = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            x[2 * i] = bf16_lo_to_float(r[i]);
-            x[2 * i + 1] = bf16_hi_to_float(r[i]);
-        }
-    } else {
-        const uint4 a = ldg_stream_v4(static_cast<const float *>(base) + at);
-        const uint4 b = ldg_stream_v4(static_cast<const float *>(base) + at + 4);
-        x[0] = bits_f(a.x), x[1] = bits_f(a.y), x[2] = bits_f(a.z), x[3] = bits_f(a.w);
-        x[4] = bits_f(b.x), x[5] = bits_f(b.y), x[6] = bits_f(b.z), x[7] = bits_f(b.w);
+    for (int k = 7; k >= 0; k--) {
+        const float d = x[k] - m;
+        float t = fmaf(d, inv, magic);
+        if (CLAMP) t = fminf(fmaxf(t, magic), magic + 15.f);
+        off = fmaxf(off, fabsf(fmaf(d, inv, magic - t)));
+        acc = acc * 16 + __float_as_uint(t);
     }
+    uint32_t word = acc - sum16;
+    if (off > 0.5f - 1.52587890625e-5f) {
+        word = 0;
+#pragma unroll
+        for (int k = 0; k < 8; k++) word |= kvq_code_exact(x[k], m, s) << (4 * k);
+    }
+    return word;
 }
 
-// Thread -> (token, key or value, head, code word), words fastest.
-template <int D>
-struct WordIndex {
-    int token, which, head, word;
-    __device__ __forceinline__ WordIndex(int64_t i, int heads) {
-        constexpr int W = D / 8;
-        word = int(i % W);
-        int64_t r = i / W;
-        head = int(r % heads);
-        r /= heads;
-        which = int(r & 1);
-        token = int(r >> 1);
+// The 8 raw 16-bit pairs or the 8 floats of a word as loaded.
+template <bool BF16>
+struct Raw8 {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const void *base, int64_t at) {
+        if constexpr (BF16) {
+            a = ldg_stream_v4(static_cast<const uint16_t *>(base) + at);
+        } else {
+            a = ldg_stream_v4(static_cast<const float *>(base) + at);
+            b = ldg_stream_v4(static_cast<const float *>(base) + at + 4);
+        }
+    }
+    __device__ __forceinline__ void floats(float (&x)[8]) const {
+        if constexpr (BF16) {
+            const uint32_t r[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) x[2 * i] = bf16_lo_to_float(r[i]), x[2 * i + 1] = bf16_hi_to_float(r[i]);
+        } else {
+            x[0] = bits_f(a.x), x[1] = bits_f(a.y), x[2] = bits_f(a.z), x[3] = bits_f(a.w);
+            x[4] = bits_f(b.x), x[5] = bits_f(b.y), x[6] = bits_f(b.z), x[7] = bits_f(b.w);
+        }
     }
 };
 
-template <bool BF16, int D>
-__global__ void __launch_bounds__(256) kvq_append_kernel(KvqStoreArgs a) {
-    constexpr int W = D / 8;
-    pdl_trigger();
-    pdl_wait();
-    const int64_t total = int64_t(a.n_tokens) * 2 * a.num_kv_heads * W;
-    const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-    const bool in = i < total;
-    const WordIndex<D> ix(in ? i : 0, a.num_kv_heads);
-    const int slot = in ? a.slots[ix.token] : -1;
-    const int page = slot / a.page_size;
-    bool live = slot >= 0;
-    if (live && page >= a.num_pool_pages) {
-        live = false;
-        if (ix.word == 0) raise_error(a.flags, kErrPageId);
-    }
-    float x[8];
-    const int64_t row = int64_t(ix.token) * (ix.which ? a.v_stride : a.k_stride) + ix.head * D + ix.word * 8;
-    load8<BF16>(ix.which ? a.v : a.k, row, x);
-    float mn = x[0], mx = x[0];
+// Smallest and largest value of the group a lane's word belongs to; LANES
+// neighbouring lanes hold the group.
+template <bool BF16, int LANES>
+__device__ __forceinline__ void group_range(const Raw8<BF16> &raw, const float (&x)[8], float &mn, float &mx) {
+    if constexpr (BF16) {
+        // as pairs of bf16, exactly: (min, -max) of the word, then one shuffle a round for both
+        const uint32_t lo = Bf16Ops::vmin(Bf16Ops::vmin(raw.a.x, raw.a.y), Bf16Ops::vmin(raw.a.z, raw.a.w));
+        const uint32_t hi = Bf16Ops::vmax(Bf16Ops::vmax(raw.a.x, raw.a.y), Bf16Ops::vmax(raw.a.z, raw.a.w)) ^ 0x80008000u;
+        uint32_t r = Bf16Ops::vmin(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
 #pragma unroll
-    for (int k = 1; k < 8; k++) mn = fminf(mn, x[k]), mx = fmaxf(mx, x[k]);
-    const int lanes = a.group_size / 8;  // lanes of one group: 4, 8 or 16
-    for (int o = 1; o < lanes; o <<= 1) {
-        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    }
-    const uint32_t mbits = __bfloat16_as_ushort(__float2bfloat16_rn(mn));
-    const float m = bits_f(mbits << 16);
-    const float s = kvq_scale(mx, m);
-    uint32_t word = 0;
-    if (s > 0.f) {
-        const float inv = 1.f / s;
+        for (int o = 1; o < LANES; o <<= 1) r = Bf16Ops::vmin(r, __shfl_xor_sync(0xffffffffu, r, o));
+        mn = bf16_lo_to_float(r), mx = bf16_hi_to_float(r ^ 0x80000000u);
+    } else {
+        mn = x[0], mx = x[0];
 #pragma unroll
-        for (int k = 0; k < 8; k++) word |= kvq_code(x[k], m, s, inv) << (4 * k);
+        for (int k = 1; k < 8; k++) mn = fminf(mn, x[k]), mx = fmaxf(mx, x[k]);
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) {
+            mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        }
     }
-    if (!live) return;
-    const int P = a.page_size, t = slot % P, ng = D / a.group_size;
-    uint32_t *block = a.pool + (int64_t(page) * a.num_kv_heads + ix.head) * kvq_block_words(D, P, ng);
-    const int place = ix.which ? kvq_value_place<D>(ix.word, t) : kvq_key_place<D>(ix.word);
-    block[ix.which * P * W + t * W + place] = word;
-    if (ix.word % lanes == 0)
-        block[2 * P * W + (ix.which * ng + ix.word / lanes) * P + t] = (__float_as_uint(s) >> 16) | (mbits << 16);
 }
 
-template <bool BF16, int D>
-__global__ void __launch_bounds__(256) kvq_gather_kernel(KvqStoreArgs a) {
-    constexpr int W = D / 8;
+// A CTA takes kTokens neighbouring tokens of one head's keys or values (the
+// heads of a token run in neighbouring CTAs, so whole rows are read at about
+// the same time); a thread one code word of kItems tokens, all loaded before
+// the first is used.
+constexpr int kCacheThreads = 256, kItems = 4;
+template <int D>
+constexpr int kTokens = kCacheThreads / (D / 8) * kItems;
+
+template <bool BF16, int D, int GS>
+__global__ void __launch_bounds__(kCacheThreads) kvq_append_kernel(KvqStoreArgs a) {
+    constexpr int W = D / 8, LANES = GS / 8, NG = D / GS, TPB = kCacheThreads / W;
     pdl_trigger();
     pdl_wait();
-    const int64_t total = int64_t(a.n_tokens) * 2 * a.num_kv_heads * W;
-    const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i >= total) return;
-    const WordIndex<D> ix(i, a.num_kv_heads);
-    const int slot = a.slots[ix.token];
-    const int P = a.page_size, page = slot / P;
-    uint32_t word = 0, par = 0;
-    if (slot >= 0 && page >= a.num_pool_pages) {
-        if (ix.word == 0) raise_error(a.flags, kErrPageId);
-    } else if (slot >= 0) {
-        const int t = slot % P, ng = D / a.group_size;
-        const uint32_t *block = a.pool + (int64_t(page) * a.num_kv_heads + ix.head) * kvq_block_words(D, P, ng);
-        const int place = ix.which ? kvq_value_place<D>(ix.word, t) : kvq_key_place<D>(ix.word);
-        word = block[ix.which * P * W + t * W + place];
-        par = block[2 * P * W + (ix.which * ng + ix.word * 8 / a.group_size) * P + t];
-    }
-    const float s = bf16_lo_to_float(par), m = bf16_hi_to_float(par);
-    float x[8];
+    const int per_chunk = 2 * a.num_kv_heads;
+    const int chunk = blockIdx.x / per_chunk, y = blockIdx.x % per_chunk;
+    const int which = y >= a.num_kv_heads, head = which ? y - a.num_kv_heads : y;
+    const int w = threadIdx.x % W, token0 = chunk * kTokens<D> + threadIdx.x / W;
+    const void *src = which ? a.v : a.k;
+    const int64_t stride = which ? a.v_stride : a.k_stride, col = head * D + w * 8;
+    Raw8<BF16> raw[kItems];
+    int slot[kItems];
 #pragma unroll
-    for (int k = 0; k < 8; k++) x[k] = fmaf(float((word >> (4 * k)) & 15u), s, m);
-    const int64_t at = (int64_t(ix.token) * a.num_kv_heads + ix.head) * D + ix.word * 8;
-    void *out = ix.which ? a.v_out : a.k_out;
-    if constexpr (BF16) {
-        uint4 w = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                             pack_bf16x2(x[6], x[7]));
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) = w;
-    } else {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
-        o[0] = make_float4(x[0], x[1], x[2], x[3]);
-        o[1] = make_float4(x[4], x[5], x[6], x[7]);
+    for (int i = 0; i < kItems; i++) {
+        const int t = token0 + i * TPB, in = min(t, a.n_tokens - 1);
+        slot[i] = t < a.n_tokens ? __ldg(a.slots + in) : -1;
+        raw[i].load(src, in * stride + col);
+    }
+    const int P = a.page_size, shift = P == 16 ? 4 : 5;
+    const int words = kvq_block_words(D, P, NG);
+#pragma unroll
+    for (int i = 0; i < kItems; i++) {
+        float x[8], mn, mx;
+        raw[i].floats(x);
+        group_range<BF16, LANES>(raw[i], x, mn, mx);
+        const uint32_t mbits = BF16 ? __float_as_uint(mn) >> 16 : __bfloat16_as_ushort(__float2bfloat16_rn(mn));
+        const float m = bits_f(mbits << 16), s = kvq_scale(mx, m);
+        const uint32_t word = s > 0.f ? kvq_word<!BF16>(x, m, s) : 0u;
+        const int page = slot[i] >> shift, t = slot[i] & (P - 1);
+        if (slot[i] < 0) continue;
+        if (page >= a.num_pool_pages) {
+            if (w == 0) raise_error(a.flags, kErrPageId);
+            continue;
+        }
+        uint32_t *block = a.pool + (int64_t(page) * a.num_kv_heads + head) * words;
+        block[(which * P + t) * W + (which ? kvq_value_place<D>(w, t) : kvq_key_place<D>(w))] = word;
+        if (w % LANES == 0)
+            block[2 * P * W + (which * NG + w / LANES) * P + t] = (__float_as_uint(s) >> 16) | (mbits << 16);
+    }
+}
+
+// m + s u of the 8 codes of a word, each with fp32's one rounding.  A code is
+// cut out in place under the exponent of 2^23, so the float is 2^23 + 16^k u;
+// the 2^23 comes off exactly and the scale carries 16^-k.
+__device__ __forceinline__ void kvq_values(uint32_t word, uint32_t par, float (&x)[8]) {
+    const float s = bf16_lo_to_float(par), m = bf16_hi_to_float(par);
+    const float sk[4] = {s, s * 0.0625f, s * 0.00390625f, s * 0.000244140625f};
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const uint32_t w = h ? word >> 16 : word;
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            x[4 * h + k] = fmaf(bits_f((w & (15u << (4 * k))) | 0x4b000000u) - 8388608.f, sk[k], m);
+    }
+}
+
+template <bool BF16, int D, int GS>
+__global__ void __launch_bounds__(kCacheThreads) kvq_gather_kernel(KvqStoreArgs a) {
+    constexpr int W = D / 8, NG = D / GS, TPB = kCacheThreads / W;
+    pdl_trigger();
+    pdl_wait();
+    const int per_chunk = 2 * a.num_kv_heads;
+    const int chunk = blockIdx.x / per_chunk, y = blockIdx.x % per_chunk;
+    const int which = y >= a.num_kv_heads, head = which ? y - a.num_kv_heads : y;
+    const int w = threadIdx.x % W, token0 = chunk * kTokens<D> + threadIdx.x / W;
+    const int P = a.page_size, shift = P == 16 ? 4 : 5;
+    const int words = kvq_block_words(D, P, NG);
+    int slot[kItems];
+    uint32_t word[kItems], par[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; i++) {
+        const int t = token0 + i * TPB;
+        slot[i] = t < a.n_tokens ? __ldg(a.slots + t) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; i++) {
+        const int page = slot[i] >> shift, t = slot[i] & (P - 1);
+        word[i] = par[i] = 0;
+        if (slot[i] < 0) continue;
+        if (page >= a.num_pool_pages) {
+            if (w == 0) raise_error(a.flags, kErrPageId);
+            continue;
+        }
+        const uint32_t *block = a.pool + (int64_t(page) * a.num_kv_heads + head) * words;
+        word[i] = __ldg(block + (which * P + t) * W + (which ? kvq_value_place<D>(w, t) : kvq_key_place<D>(w)));
+        par[i] = __ldg(block + 2 * P * W + (which * NG + w / (GS / 8)) * P + t);
+    }
+    void *out = which ? a.v_out : a.k_out;
+#pragma unroll
+    for (int i = 0; i < kItems; i++) {
+        const int t = token0 + i * TPB;
+        if (t >= a.n_tokens) break;
+        float x[8];
+        kvq_values(word[i], par[i], x);
+        const int64_t at = (int64_t(t) * a.num_kv_heads + head) * D + w * 8;
+        if constexpr (BF16) {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) =
+                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                           pack_bf16x2(x[6], x[7]));
+        } else {
+            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
+            o[0] = make_float4(x[0], x[1], x[2], x[3]);
+            o[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
     }
 }
 
@@ -177,19 +251,59 @@ __device__ __forceinline__ uint32_t bf16_down(float x) {
 }
 __device__ __forceinline__ uint32_t bf16_up(float x) { return __bfloat16_as_ushort(__float2bfloat16_ru(x)); }
 
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float &lo, float &hi) {
+    uint32_t a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(p));
+    lo = bits_f(a), hi = bits_f(b);
+}
+
+// kvq_values, two codes an instruction.
+__device__ __forceinline__ void kvq_values2(uint32_t word, uint32_t par, float (&x)[8]) {
+    const float s = bf16_lo_to_float(par);
+    const uint32_t m = par & 0xffff0000u;
+    const uint64_t mm = pair(m, m), off = pair(0xcb000000u, 0xcb000000u);  // -2^23
+    const uint64_t s01 = pair(__float_as_uint(s), __float_as_uint(s * 0.0625f));
+    const uint64_t s23 = pair(__float_as_uint(s * 0.00390625f), __float_as_uint(s * 0.000244140625f));
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const uint32_t w = h ? word >> 16 : word;
+        const uint64_t a = pair((w & 0xfu) | 0x4b000000u, (w & 0xf0u) | 0x4b000000u);
+        const uint64_t b = pair((w & 0xf00u) | 0x4b000000u, (w & 0xf000u) | 0x4b000000u);
+        unpair(pair_fma(pair_add(a, off), s01, mm), x[4 * h], x[4 * h + 1]);
+        unpair(pair_fma(pair_add(b, off), s23, mm), x[4 * h + 2], x[4 * h + 3]);
+    }
+}
+
 // One warp per (listed page, KV head): D / 8 lanes cover a token's code
-// words, 32 / (D / 8) tokens at a time; lanes of the same word combine by
-// shuffles.
-template <bool BF16, int D>
-__global__ void __launch_bounds__(256) kvq_meta_kernel(KvqMetaArgs a) {
-    constexpr int W = D / 8, TP = 32 / W;
+// words, TP = 32 / (D / 8) tokens at a time; lanes of the same word combine
+// by shuffles.  All of a lane's codes and params (16 tokens' worth) are
+// loaded before the first is used.
+template <bool BF16, int D, int GS>
+__global__ void __launch_bounds__(kCacheThreads) kvq_meta_kernel(KvqMetaArgs a) {
+    constexpr int W = D / 8, TP = 32 / W, NT = 16 / TP, NG = D / GS;
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t tile = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int64_t tile = int64_t(blockIdx.x) * (kCacheThreads / 32) + (threadIdx.x >> 5);
     if (tile >= int64_t(a.n_list) * a.num_kv_heads) return;
-    const int e = int(tile / a.num_kv_heads), g = int(tile % a.num_kv_heads);
-    const int p = a.page_ids[e], valid = a.valid_tokens[e];
+    const int e = int(tile / a.num_kv_heads), g = int(tile - int64_t(e) * a.num_kv_heads);
+    const int p = __ldg(a.page_ids + e), valid = __ldg(a.valid_tokens + e);
     if (p < 0) return;
     if (p >= a.num_pool_pages) {
         if (lane == 0) raise_error(a.flags, kErrPageId);
@@ -199,20 +313,30 @@ __global__ void __launch_bounds__(256) kvq_meta_kernel(KvqMetaArgs a) {
         if (lane == 0) raise_error(a.flags, kErrValid);
         return;
     }
-    const int P = a.page_size, ng = D / a.group_size;
-    const uint32_t *block = a.pool + (int64_t(p) * a.num_kv_heads + g) * kvq_block_words(D, P, ng);
+    const int P = a.page_size;
+    const uint32_t *block = a.pool + (int64_t(p) * a.num_kv_heads + g) * kvq_block_words(D, P, NG);
     const int place = lane % W, t0 = lane / W, w = kvq_key_word<D>(place);
-    const uint32_t *params = block + 2 * P * W + (w * 8 / a.group_size) * P;
+    const uint32_t *params = block + 2 * P * W + w / (GS / 8) * P;
     float mn[8], mx[8];
 #pragma unroll
     for (int k = 0; k < 8; k++) mn[k] = INFINITY, mx[k] = -INFINITY;
-    for (int t = t0; t < valid; t += TP) {
-        const uint32_t word = block[t * W + place], par = params[t];
-        const float s = bf16_lo_to_float(par), m = bf16_hi_to_float(par);
+    for (int first = 0; first < valid; first += 16) {
+        uint32_t word[NT], par[NT];
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-            const float x = fmaf(float((word >> (4 * k)) & 15u), s, m);
-            mn[k] = fminf(mn[k], x), mx[k] = fmaxf(mx[k], x);
+        for (int i = 0; i < NT; i++) {  // a token past the end repeats the last one
+            const int t = min(first + t0 + i * TP, valid - 1);
+            word[i] = __ldg(block + t * W + place), par[i] = __ldg(params + t);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; i += 2) {
+            float x[8], y[8];
+            kvq_values2(word[i], par[i], x);
+            kvq_values2(word[i + 1], par[i + 1], y);
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                mn[k] = fminf(fminf(x[k], y[k]), mn[k]);
+                mx[k] = fmaxf(fmaxf(x[k], y[k]), mx[k]);
+            }
         }
     }
 #pragma unroll
@@ -222,52 +346,60 @@ __global__ void __launch_bounds__(256) kvq_meta_kernel(KvqMetaArgs a) {
             mn[k] = fminf(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], o));
             mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
         }
-    if (t0 > 0) return;
-    const int64_t at = (int64_t(p) * a.num_kv_heads + g) * 2 * D + w * 8;
+    // the first lanes of a word write the minima, the next ones the maxima
+    if (t0 > 1) return;
+    const int64_t at = ((int64_t(p) * a.num_kv_heads + g) * 2 + t0) * D + w * 8;
     if constexpr (BF16) {
-        uint32_t lo[4], hi[4];
+        uint32_t r[4];
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-            lo[k] = bf16_down(mn[2 * k]) | (bf16_down(mn[2 * k + 1]) << 16);
-            hi[k] = bf16_up(mx[2 * k]) | (bf16_up(mx[2 * k + 1]) << 16);
-        }
-        uint16_t *meta = static_cast<uint16_t *>(a.meta);
-        *reinterpret_cast<uint4 *>(meta + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<uint4 *>(meta + at + D) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        for (int k = 0; k < 4; k++)
+            r[k] = t0 == 0 ? bf16_down(mn[2 * k]) | (bf16_down(mn[2 * k + 1]) << 16)
+                           : bf16_up(mx[2 * k]) | (bf16_up(mx[2 * k + 1]) << 16);
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.meta) + at) = make_uint4(r[0], r[1], r[2], r[3]);
     } else {
         float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.meta) + at);
-        o[0] = make_float4(mn[0], mn[1], mn[2], mn[3]);
-        o[1] = make_float4(mn[4], mn[5], mn[6], mn[7]);
-        o = reinterpret_cast<float4 *>(static_cast<float *>(a.meta) + at + D);
-        o[0] = make_float4(mx[0], mx[1], mx[2], mx[3]);
-        o[1] = make_float4(mx[4], mx[5], mx[6], mx[7]);
+        o[0] = t0 == 0 ? make_float4(mn[0], mn[1], mn[2], mn[3]) : make_float4(mx[0], mx[1], mx[2], mx[3]);
+        o[1] = t0 == 0 ? make_float4(mn[4], mn[5], mn[6], mn[7]) : make_float4(mx[4], mx[5], mx[6], mx[7]);
     }
+}
+
+// One launch of kernel<bf16, head_dim, group_size>.
+#define KVQ_CASE(kernel, d, gs)                                                              \
+    if (head_dim == d && a.group_size == gs)                                                 \
+        return bf16 ? launch_pdl(kernel<true, d, gs>, grid, dim3(kCacheThreads), 0, stream, a) \
+                    : launch_pdl(kernel<false, d, gs>, grid, dim3(kCacheThreads), 0, stream, a);
+#define KVQ_LAUNCH(kernel)      \
+    KVQ_CASE(kernel, 128, 128)  \
+    KVQ_CASE(kernel, 128, 64)   \
+    KVQ_CASE(kernel, 128, 32)   \
+    KVQ_CASE(kernel, 64, 64)    \
+    KVQ_CASE(kernel, 64, 32)    \
+    return cudaErrorInvalidValue;
+
+dim3 token_grid(const KvqStoreArgs &a, int head_dim) {
+    const int per_cta = head_dim == 128 ? kTokens<128> : kTokens<64>;
+    return dim3(unsigned((int64_t(a.n_tokens) + per_cta - 1) / per_cta * 2 * a.num_kv_heads));
 }
 
 }  // namespace
 
-#define KVQ_DISPATCH(kernel, bf16, d, grid, stream, args)                                            \
-    ((d) == 128 ? ((bf16) ? launch_pdl(kernel<true, 128>, grid, dim3(256), 0, stream, args)          \
-                          : launch_pdl(kernel<false, 128>, grid, dim3(256), 0, stream, args))        \
-                : ((bf16) ? launch_pdl(kernel<true, 64>, grid, dim3(256), 0, stream, args)           \
-                          : launch_pdl(kernel<false, 64>, grid, dim3(256), 0, stream, args)))
-
 cudaError_t launch_kvq_append(const KvqStoreArgs &a, int dtype, int head_dim, cudaStream_t stream) {
-    const int64_t n = int64_t(a.n_tokens) * 2 * a.num_kv_heads * (head_dim / 8);
-    const dim3 grid(unsigned((n + 255) / 256));
-    return KVQ_DISPATCH(kvq_append_kernel, dtype == kDtypeBf16, head_dim, grid, stream, a);
+    const bool bf16 = dtype == kDtypeBf16;
+    const dim3 grid = token_grid(a, head_dim);
+    KVQ_LAUNCH(kvq_append_kernel)
 }
 
 cudaError_t launch_kvq_gather(const KvqStoreArgs &a, int dtype, int head_dim, cudaStream_t stream) {
-    const int64_t n = int64_t(a.n_tokens) * 2 * a.num_kv_heads * (head_dim / 8);
-    const dim3 grid(unsigned((n + 255) / 256));
-    return KVQ_DISPATCH(kvq_gather_kernel, dtype == kDtypeBf16, head_dim, grid, stream, a);
+    const bool bf16 = dtype == kDtypeBf16;
+    const dim3 grid = token_grid(a, head_dim);
+    KVQ_LAUNCH(kvq_gather_kernel)
 }
 
 cudaError_t launch_kvq_meta(const KvqMetaArgs &a, int meta_dtype, int head_dim, cudaStream_t stream) {
+    const bool bf16 = meta_dtype == kDtypeBf16;
     const int64_t n = int64_t(a.n_list) * a.num_kv_heads;
-    const dim3 grid(unsigned((n + 7) / 8));
-    return KVQ_DISPATCH(kvq_meta_kernel, meta_dtype == kDtypeBf16, head_dim, grid, stream, a);
+    const dim3 grid(unsigned((n + kCacheThreads / 32 - 1) / (kCacheThreads / 32)));
+    KVQ_LAUNCH(kvq_meta_kernel)
 }
 
 }  // namespace qskv
