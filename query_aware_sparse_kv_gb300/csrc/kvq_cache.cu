@@ -35,24 +35,14 @@ __device__ __forceinline__ float kvq_scale(float mx, float m) {
     return bits_f(up ? lo + 0x10000u : lo);
 }
 
-// rint((x - m) / s) clamped to [0, 15], ties to even, of the exact quotient.
-__device__ __noinline__ uint32_t kvq_code_exact(float x, float m, float s) {
-    float d, err;
-    exact_diff(x, m, d, err);
-    const float k = fminf(fmaxf(floorf(d / s), -1.f), 16.f);
-    // the quotient is within 2^-18 of d / s: k is its floor unless it lies that close to a whole number, where
-    // the comparison with k + 1/2 still rounds it right
-    const float rem = fmaf(-(k + 0.5f), s, d) + err;
-    const float u = rem > 0.f ? k + 1.f : (rem < 0.f ? k : 2.f * rintf(0.5f * k + 0.25f));
-    return uint32_t(fminf(fmaxf(u, 0.f), 15.f));
-}
-
-// Code word of 8 values.  d * (1 / s) is within 2^-18 of the exact quotient
-// (three roundings of 2^-23 of at most 15.1), so adding it to 1.5 2^23 rounds
-// it right unless it lies within 2^-16 of a half; a word with such a value is
-// done again on exact remainders.  The rounded quotient's bits are the code
-// plus a constant; `acc * 16 + bits` packs them and the constants' sum is
-// taken off at the end.  CLAMP: m may lie above the smallest value (fp32
+// Code word of 8 values: rint((x - m) / s) clamped to [0, 15], ties to even,
+// of the exact quotients.  Adding d * (1 / s) to 1.5 2^23 rounds to a
+// candidate u within one of the right one; d - u s is exact and says whether
+// it is: below s / 2 in magnitude it is.  A word with a remainder at s / 2
+// (a tie, or d itself rounded: 2^-19 s covers that) is looked at once more,
+// value by value, with the rounding error of d.  The candidates' bits are the
+// codes plus a constant; `acc * 16 + bits` packs them and the constants' sum
+// is taken off at the end.  CLAMP: m may lie above the smallest value (fp32
 // inputs, whose minimum is rounded); a bf16 minimum is exact, and then the
 // quotients are 0 to 15.06 and round into range by themselves.
 template <bool CLAMP>
@@ -67,17 +57,26 @@ __device__ __forceinline__ uint32_t kvq_word(const float (&x)[8], float m, float
     for (int k = 7; k >= 0; k--) {
         const float d = x[k] - m;
         float t = fmaf(d, inv, magic);
+        off = fmaxf(off, fabsf(fmaf(magic - t, s, d)));
         if (CLAMP) t = fminf(fmaxf(t, magic), magic + 15.f);
-        off = fmaxf(off, fabsf(fmaf(d, inv, magic - t)));
         acc = acc * 16 + __float_as_uint(t);
     }
-    uint32_t word = acc - sum16;
-    if (off > 0.5f - 1.52587890625e-5f) {
-        word = 0;
+    const float half = 0.5f * s;
+    if (off > half - s * 1.9073486328125e-6f) {
+        acc = 0;
 #pragma unroll
-        for (int k = 0; k < 8; k++) word |= kvq_code_exact(x[k], m, s) << (4 * k);
+        for (int k = 7; k >= 0; k--) {
+            float d, err;
+            exact_diff(x[k], m, d, err);
+            float t = fmaf(d, inv, magic);
+            const float r = fmaf(magic - t, s, d);
+            const float over = (fabsf(r) - half) + (r > 0.f ? err : -err);
+            if (over > 0.f || (over == 0.f && (__float_as_uint(t) & 1u))) t += r > 0.f ? 1.f : -1.f;
+            if (CLAMP) t = fminf(fmaxf(t, magic), magic + 15.f);
+            acc = acc * 16 + __float_as_uint(t);
+        }
     }
-    return word;
+    return acc - sum16;
 }
 
 // The 8 raw 16-bit pairs or the 8 floats of a word as loaded.
@@ -128,15 +127,13 @@ __device__ __forceinline__ void group_range(const Raw8<BF16> &raw, const float (
     }
 }
 
-// A CTA takes kTokens neighbouring tokens of one head's keys or values (the
-// heads of a token run in neighbouring CTAs, so whole rows are read at about
-// the same time); a thread one code word of kItems tokens, all loaded before
-// the first is used.
-constexpr int kCacheThreads = 256, kItems = 4;
-template <int D>
-constexpr int kTokens = kCacheThreads / (D / 8) * kItems;
+// A CTA takes neighbouring tokens of one head's keys or values (the heads of
+// a token run in neighbouring CTAs, so whole rows are read at about the same
+// time); a thread one code word of ITEMS tokens, all loaded before the first
+// is used: 4 where that still fills the GPU, 1 below (a decode step's tokens).
+constexpr int kCacheThreads = 256;
 
-template <bool BF16, int D, int GS>
+template <bool BF16, int D, int GS, int ITEMS>
 __global__ void __launch_bounds__(kCacheThreads) kvq_append_kernel(KvqStoreArgs a) {
     constexpr int W = D / 8, LANES = GS / 8, NG = D / GS, TPB = kCacheThreads / W;
     pdl_trigger();
@@ -144,13 +141,13 @@ __global__ void __launch_bounds__(kCacheThreads) kvq_append_kernel(KvqStoreArgs 
     const int per_chunk = 2 * a.num_kv_heads;
     const int chunk = blockIdx.x / per_chunk, y = blockIdx.x % per_chunk;
     const int which = y >= a.num_kv_heads, head = which ? y - a.num_kv_heads : y;
-    const int w = threadIdx.x % W, token0 = chunk * kTokens<D> + threadIdx.x / W;
+    const int w = threadIdx.x % W, token0 = chunk * (TPB * ITEMS) + threadIdx.x / W;
     const void *src = which ? a.v : a.k;
     const int64_t stride = which ? a.v_stride : a.k_stride, col = head * D + w * 8;
-    Raw8<BF16> raw[kItems];
-    int slot[kItems];
+    Raw8<BF16> raw[ITEMS];
+    int slot[ITEMS];
 #pragma unroll
-    for (int i = 0; i < kItems; i++) {
+    for (int i = 0; i < ITEMS; i++) {
         const int t = token0 + i * TPB, in = min(t, a.n_tokens - 1);
         slot[i] = t < a.n_tokens ? __ldg(a.slots + in) : -1;
         raw[i].load(src, in * stride + col);
@@ -158,7 +155,7 @@ __global__ void __launch_bounds__(kCacheThreads) kvq_append_kernel(KvqStoreArgs 
     const int P = a.page_size, shift = P == 16 ? 4 : 5;
     const int words = kvq_block_words(D, P, NG);
 #pragma unroll
-    for (int i = 0; i < kItems; i++) {
+    for (int i = 0; i < ITEMS; i++) {
         float x[8], mn, mx;
         raw[i].floats(x);
         group_range<BF16, LANES>(raw[i], x, mn, mx);
@@ -193,7 +190,7 @@ __device__ __forceinline__ void kvq_values(uint32_t word, uint32_t par, float (&
     }
 }
 
-template <bool BF16, int D, int GS>
+template <bool BF16, int D, int GS, int ITEMS>
 __global__ void __launch_bounds__(kCacheThreads) kvq_gather_kernel(KvqStoreArgs a) {
     constexpr int W = D / 8, NG = D / GS, TPB = kCacheThreads / W;
     pdl_trigger();
@@ -201,18 +198,18 @@ __global__ void __launch_bounds__(kCacheThreads) kvq_gather_kernel(KvqStoreArgs 
     const int per_chunk = 2 * a.num_kv_heads;
     const int chunk = blockIdx.x / per_chunk, y = blockIdx.x % per_chunk;
     const int which = y >= a.num_kv_heads, head = which ? y - a.num_kv_heads : y;
-    const int w = threadIdx.x % W, token0 = chunk * kTokens<D> + threadIdx.x / W;
+    const int w = threadIdx.x % W, token0 = chunk * (TPB * ITEMS) + threadIdx.x / W;
     const int P = a.page_size, shift = P == 16 ? 4 : 5;
     const int words = kvq_block_words(D, P, NG);
-    int slot[kItems];
-    uint32_t word[kItems], par[kItems];
+    int slot[ITEMS];
+    uint32_t word[ITEMS], par[ITEMS];
 #pragma unroll
-    for (int i = 0; i < kItems; i++) {
+    for (int i = 0; i < ITEMS; i++) {
         const int t = token0 + i * TPB;
         slot[i] = t < a.n_tokens ? __ldg(a.slots + t) : -1;
     }
 #pragma unroll
-    for (int i = 0; i < kItems; i++) {
+    for (int i = 0; i < ITEMS; i++) {
         const int page = slot[i] >> shift, t = slot[i] & (P - 1);
         word[i] = par[i] = 0;
         if (slot[i] < 0) continue;
@@ -226,7 +223,7 @@ __global__ void __launch_bounds__(kCacheThreads) kvq_gather_kernel(KvqStoreArgs 
     }
     void *out = which ? a.v_out : a.k_out;
 #pragma unroll
-    for (int i = 0; i < kItems; i++) {
+    for (int i = 0; i < ITEMS; i++) {
         const int t = token0 + i * TPB;
         if (t >= a.n_tokens) break;
         float x[8];
@@ -273,8 +270,10 @@ __device__ __forceinline__ void unpair(uint64_t p, float &lo, float &hi) {
     lo = bits_f(a), hi = bits_f(b);
 }
 
-// kvq_values, two codes an instruction.
-__device__ __forceinline__ void kvq_values2(uint32_t word, uint32_t par, float (&x)[8]) {
+// kvq_values, two codes an instruction.  `k23` holds 0x4b000000 in a register
+// the compiler cannot see through, so that mask and exponent are one
+// instruction.
+__device__ __forceinline__ void kvq_values2(uint32_t word, uint32_t par, uint32_t k23, float (&x)[8]) {
     const float s = bf16_lo_to_float(par);
     const uint32_t m = par & 0xffff0000u;
     const uint64_t mm = pair(m, m), off = pair(0xcb000000u, 0xcb000000u);  // -2^23
@@ -283,123 +282,196 @@ __device__ __forceinline__ void kvq_values2(uint32_t word, uint32_t par, float (
 #pragma unroll
     for (int h = 0; h < 2; h++) {
         const uint32_t w = h ? word >> 16 : word;
-        const uint64_t a = pair((w & 0xfu) | 0x4b000000u, (w & 0xf0u) | 0x4b000000u);
-        const uint64_t b = pair((w & 0xf00u) | 0x4b000000u, (w & 0xf000u) | 0x4b000000u);
+        const uint64_t a = pair(and_or(w, 0xfu, k23), and_or(w, 0xf0u, k23));
+        const uint64_t b = pair(and_or(w, 0xf00u, k23), and_or(w, 0xf000u, k23));
         unpair(pair_fma(pair_add(a, off), s01, mm), x[4 * h], x[4 * h + 1]);
         unpair(pair_fma(pair_add(b, off), s23, mm), x[4 * h + 2], x[4 * h + 3]);
     }
 }
 
-// One warp per (listed page, KV head): D / 8 lanes cover a token's code
-// words, TP = 32 / (D / 8) tokens at a time; lanes of the same word combine
-// by shuffles.  All of a lane's codes and params (16 tokens' worth) are
-// loaded before the first is used.
+// A warp takes (listed page, KV head) tiles in turn through a ring of bulk
+// copies of its own (a tile's key codes and key params are 1.1 KB a page of
+// 16 tokens; the ring keeps about 80 KB an SM on their way, where direct
+// loads of one tile a warp left the kernel waiting: 262 us for 36864 pages).
+// D / 8 lanes cover a token's code words, 32 / (D / 8) tokens at a time;
+// lanes of the same word combine by shuffles at the end.
+constexpr int kMetaWarps = 8, kMetaStages = 4;
+
 template <bool BF16, int D, int GS>
-__global__ void __launch_bounds__(kCacheThreads) kvq_meta_kernel(KvqMetaArgs a) {
-    constexpr int W = D / 8, TP = 32 / W, NT = 16 / TP, NG = D / GS;
+__global__ void __launch_bounds__(kMetaWarps * 32, 4) kvq_meta_kernel(KvqMetaArgs a) {
+    constexpr int W = D / 8, TP = 32 / W, NG = D / GS;
+    extern __shared__ __align__(128) uint32_t ring_mem[];
+    __shared__ uint64_t bars[kMetaWarps][kMetaStages];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int P = a.page_size, S = P == 16 ? kMetaStages : kMetaStages / 2;
+    const int code_words = P * W, stage_words = code_words + NG * P;
+    uint32_t *ring = ring_mem + warp * (S * stage_words);
+    if (lane < S) mbar_init(&bars[warp][lane], 1);
+    mbar_fence_init();
+    __syncwarp();
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t tile = int64_t(blockIdx.x) * (kCacheThreads / 32) + (threadIdx.x >> 5);
-    if (tile >= int64_t(a.n_list) * a.num_kv_heads) return;
-    const int e = int(tile / a.num_kv_heads), g = int(tile - int64_t(e) * a.num_kv_heads);
-    const int p = __ldg(a.page_ids + e), valid = __ldg(a.valid_tokens + e);
-    if (p < 0) return;
-    if (p >= a.num_pool_pages) {
-        if (lane == 0) raise_error(a.flags, kErrPageId);
-        return;
-    }
-    if (valid < 1 || valid > a.page_size) {
-        if (lane == 0) raise_error(a.flags, kErrValid);
-        return;
-    }
-    const int P = a.page_size;
-    const uint32_t *block = a.pool + (int64_t(p) * a.num_kv_heads + g) * kvq_block_words(D, P, NG);
-    const int place = lane % W, t0 = lane / W, w = kvq_key_word<D>(place);
-    const uint32_t *params = block + 2 * P * W + w / (GS / 8) * P;
-    float mn[8], mx[8];
-#pragma unroll
-    for (int k = 0; k < 8; k++) mn[k] = INFINITY, mx[k] = -INFINITY;
-    for (int first = 0; first < valid; first += 16) {
-        uint32_t word[NT], par[NT];
-#pragma unroll
-        for (int i = 0; i < NT; i++) {  // a token past the end repeats the last one
-            const int t = min(first + t0 + i * TP, valid - 1);
-            word[i] = __ldg(block + t * W + place), par[i] = __ldg(params + t);
+    const int64_t tiles = int64_t(a.n_list) * a.num_kv_heads;
+    const int64_t first = int64_t(blockIdx.x) * kMetaWarps + warp, step = int64_t(gridDim.x) * kMetaWarps;
+    const int n = first < tiles ? int((tiles - first + step - 1) / step) : 0;
+    // lane i of the warp describes the warp's tiles i, 32 + i, ..: (page, head) block and valid tokens
+    int64_t at = 0;
+    int valid = 0;
+    auto describe = [&](int i) {
+        valid = 0;
+        const int64_t tile = first + (i + lane) * step;
+        if (i + lane >= n) return;
+        const int e = int(tile / a.num_kv_heads), g = int(tile - int64_t(e) * a.num_kv_heads);
+        const int p = __ldg(a.page_ids + e), v = __ldg(a.valid_tokens + e);
+        if (p < 0) return;
+        if (p >= a.num_pool_pages) {
+            raise_error(a.flags, kErrPageId);
+            return;
         }
-#pragma unroll
-        for (int i = 0; i < NT; i += 2) {
-            float x[8], y[8];
-            kvq_values2(word[i], par[i], x);
-            kvq_values2(word[i + 1], par[i + 1], y);
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                mn[k] = fminf(fminf(x[k], y[k]), mn[k]);
-                mx[k] = fmaxf(fmaxf(x[k], y[k]), mx[k]);
+        if (v < 1 || v > P) {
+            raise_error(a.flags, kErrValid);
+            return;
+        }
+        at = int64_t(p) * a.num_kv_heads + g, valid = v;
+    };
+    int put = 0, got = 0, parity = 0;
+    auto issue = [&](int i) {
+        if (i >= n) return;
+        const int v = __shfl_sync(0xffffffffu, valid, i & 31);
+        const int64_t b = __shfl_sync(0xffffffffu, at, i & 31);
+        if (lane == 0) {
+            const uint32_t *block = a.pool + b * kvq_block_words(D, P, NG);
+            uint64_t *bar = &bars[warp][put];
+            uint32_t *dst = ring + put * stage_words;
+            if (v > 0) {
+                mbar_arrive_expect_tx(bar, stage_words * 4);
+                bulk_load(dst, block, code_words * 4, bar);
+                bulk_load(dst + code_words, block + 2 * code_words, NG * P * 4, bar);
+            } else {
+                mbar_arrive(bar);
             }
         }
-    }
-#pragma unroll
-    for (int o = W; o < 32; o <<= 1)
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-            mn[k] = fminf(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], o));
-            mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
+        if (++put == S) put = 0;
+    };
+    const int place = lane % W, t0 = lane / W, w = kvq_key_word<D>(place);
+    uint32_t k23;
+    asm("mov.b32 %0, 0x4b000000;" : "=r"(k23));
+    describe(0);
+    for (int i = 0; i < S - 1; i++) issue(i);
+    // a description is replaced once its 32 tiles are under way, so what the loop needs of the older ones is kept
+    int64_t kept_at = 0;
+    int kept_valid = 0;
+    for (int i = 0; i < n; i++) {
+        if ((i & 31) == 0) kept_at = at, kept_valid = valid;
+        if (((i + S - 1) & 31) == 0) describe(i + S - 1);
+        issue(i + S - 1);
+        const int v = __shfl_sync(0xffffffffu, kept_valid, i & 31);
+        const int64_t b = __shfl_sync(0xffffffffu, kept_at, i & 31);
+        if (!mbar_wait_bounded(&bars[warp][got], parity, kWaitLimitNs)) {
+            // a lost copy: flagged, the rest is given up once the copies in flight had their time
+            if (lane == 0) raise_error(a.flags, kErrTimeout);
+            for (int k = i + 1; k < min(i + S, n); k++) {
+                if (++got == S) got = 0, parity ^= 1;
+                mbar_wait_bounded(&bars[warp][got], parity, kWaitLimitNs);
+            }
+            return;
         }
-    // the first lanes of a word write the minima, the next ones the maxima
-    if (t0 > 1) return;
-    const int64_t at = ((int64_t(p) * a.num_kv_heads + g) * 2 + t0) * D + w * 8;
-    if constexpr (BF16) {
-        uint32_t r[4];
+        if (v > 0) {
+            const uint32_t *codes = ring + got * stage_words, *params = codes + code_words + w / (GS / 8) * P;
+            float mn[8], mx[8];
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-            r[k] = t0 == 0 ? bf16_down(mn[2 * k]) | (bf16_down(mn[2 * k + 1]) << 16)
-                           : bf16_up(mx[2 * k]) | (bf16_up(mx[2 * k + 1]) << 16);
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.meta) + at) = make_uint4(r[0], r[1], r[2], r[3]);
-    } else {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.meta) + at);
-        o[0] = t0 == 0 ? make_float4(mn[0], mn[1], mn[2], mn[3]) : make_float4(mx[0], mx[1], mx[2], mx[3]);
-        o[1] = t0 == 0 ? make_float4(mn[4], mn[5], mn[6], mn[7]) : make_float4(mx[4], mx[5], mx[6], mx[7]);
+            for (int k = 0; k < 8; k++) mn[k] = INFINITY, mx[k] = -INFINITY;
+#pragma unroll 2
+            for (int t = t0; t - t0 < v; t += 2 * TP) {  // a token past the end repeats the last one
+                const int ta = min(t, v - 1), tb = min(t + TP, v - 1);
+                float x[8], y[8];
+                kvq_values2(codes[ta * W + place], params[ta], k23, x);
+                kvq_values2(codes[tb * W + place], params[tb], k23, y);
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    mn[k] = fminf(fminf(x[k], y[k]), mn[k]);
+                    mx[k] = fmaxf(fmaxf(x[k], y[k]), mx[k]);
+                }
+            }
+#pragma unroll
+            for (int o = W; o < 32; o <<= 1)
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    mn[k] = fminf(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], o));
+                    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
+                }
+            // the first lanes of a word write the minima, the next ones the maxima
+            if (t0 < 2) {
+                const int64_t to = (b * 2 + t0) * D + w * 8;
+                if constexpr (BF16) {
+                    uint32_t r[4];
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        r[k] = t0 == 0 ? bf16_down(mn[2 * k]) | (bf16_down(mn[2 * k + 1]) << 16)
+                                       : bf16_up(mx[2 * k]) | (bf16_up(mx[2 * k + 1]) << 16);
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.meta) + to) = make_uint4(r[0], r[1], r[2], r[3]);
+                } else {
+                    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.meta) + to);
+                    o[0] = t0 == 0 ? make_float4(mn[0], mn[1], mn[2], mn[3]) : make_float4(mx[0], mx[1], mx[2], mx[3]);
+                    o[1] = t0 == 0 ? make_float4(mn[4], mn[5], mn[6], mn[7]) : make_float4(mx[4], mx[5], mx[6], mx[7]);
+                }
+            }
+        }
+        if (++got == S) got = 0, parity ^= 1;
+        __syncwarp();
     }
 }
 
-// One launch of kernel<bf16, head_dim, group_size>.
-#define KVQ_CASE(kernel, d, gs)                                                              \
-    if (head_dim == d && a.group_size == gs)                                                 \
-        return bf16 ? launch_pdl(kernel<true, d, gs>, grid, dim3(kCacheThreads), 0, stream, a) \
-                    : launch_pdl(kernel<false, d, gs>, grid, dim3(kCacheThreads), 0, stream, a);
-#define KVQ_LAUNCH(kernel)      \
-    KVQ_CASE(kernel, 128, 128)  \
-    KVQ_CASE(kernel, 128, 64)   \
-    KVQ_CASE(kernel, 128, 32)   \
-    KVQ_CASE(kernel, 64, 64)    \
-    KVQ_CASE(kernel, 64, 32)    \
-    return cudaErrorInvalidValue;
+// Launches of kernel<bf16, head_dim, group_size, ..>.
+#define KVQ_FORMATS(CASE) CASE(128, 128) CASE(128, 64) CASE(128, 32) CASE(64, 64) CASE(64, 32)
 
-dim3 token_grid(const KvqStoreArgs &a, int head_dim) {
-    const int per_cta = head_dim == 128 ? kTokens<128> : kTokens<64>;
-    return dim3(unsigned((int64_t(a.n_tokens) + per_cta - 1) / per_cta * 2 * a.num_kv_heads));
+// Tokens a CTA takes with `items` a thread, and its CTAs.
+int64_t token_ctas(const KvqStoreArgs &a, int head_dim, int items) {
+    const int per_cta = kCacheThreads / (head_dim / 8) * items;
+    return (int64_t(a.n_tokens) + per_cta - 1) / per_cta * 2 * a.num_kv_heads;
 }
+// 4 tokens a thread from four CTAs an SM on (one GB300 has 152): below, the loads of one token a thread already cover
+// what few CTAs there are, and the other three would only follow one another.
+constexpr int64_t kManyCtas = 608;
 
 }  // namespace
 
+#define KVQ_TOKENS(kernel, d, gs)                                                                              \
+    if (head_dim == d && a.group_size == gs) {                                                                 \
+        if (many) return bf16 ? launch_pdl(kernel<true, d, gs, 4>, grid, dim3(kCacheThreads), 0, stream, a)    \
+                              : launch_pdl(kernel<false, d, gs, 4>, grid, dim3(kCacheThreads), 0, stream, a);  \
+        return bf16 ? launch_pdl(kernel<true, d, gs, 1>, grid, dim3(kCacheThreads), 0, stream, a)              \
+                    : launch_pdl(kernel<false, d, gs, 1>, grid, dim3(kCacheThreads), 0, stream, a);            \
+    }
+
 cudaError_t launch_kvq_append(const KvqStoreArgs &a, int dtype, int head_dim, cudaStream_t stream) {
-    const bool bf16 = dtype == kDtypeBf16;
-    const dim3 grid = token_grid(a, head_dim);
-    KVQ_LAUNCH(kvq_append_kernel)
+    const bool bf16 = dtype == kDtypeBf16, many = token_ctas(a, head_dim, 4) >= kManyCtas;
+    const dim3 grid(unsigned(token_ctas(a, head_dim, many ? 4 : 1)));
+#define KVQ_APPEND(d, gs) KVQ_TOKENS(kvq_append_kernel, d, gs)
+    KVQ_FORMATS(KVQ_APPEND)
+    return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_kvq_gather(const KvqStoreArgs &a, int dtype, int head_dim, cudaStream_t stream) {
-    const bool bf16 = dtype == kDtypeBf16;
-    const dim3 grid = token_grid(a, head_dim);
-    KVQ_LAUNCH(kvq_gather_kernel)
+    const bool bf16 = dtype == kDtypeBf16, many = token_ctas(a, head_dim, 4) >= kManyCtas;
+    const dim3 grid(unsigned(token_ctas(a, head_dim, many ? 4 : 1)));
+#define KVQ_GATHER(d, gs) KVQ_TOKENS(kvq_gather_kernel, d, gs)
+    KVQ_FORMATS(KVQ_GATHER)
+    return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_kvq_meta(const KvqMetaArgs &a, int meta_dtype, int head_dim, cudaStream_t stream) {
+cudaError_t launch_kvq_meta(const KvqMetaArgs &a, int meta_dtype, int head_dim, int num_sms, cudaStream_t stream) {
     const bool bf16 = meta_dtype == kDtypeBf16;
-    const int64_t n = int64_t(a.n_list) * a.num_kv_heads;
-    const dim3 grid(unsigned((n + kCacheThreads / 32 - 1) / (kCacheThreads / 32)));
-    KVQ_LAUNCH(kvq_meta_kernel)
+    const int64_t ctas = (int64_t(a.n_list) * a.num_kv_heads + kMetaWarps - 1) / kMetaWarps;
+    const dim3 grid(unsigned(ctas < 4 * num_sms ? ctas : 4 * num_sms));
+    const int stages = a.page_size == 16 ? kMetaStages : kMetaStages / 2;
+    const int bytes = kMetaWarps * stages * a.page_size * (head_dim / 8 + head_dim / a.group_size) * 4;  // at most 40 KB
+#define KVQ_META(d, gs)                                                                                                 \
+    if (head_dim == d && a.group_size == gs)                                                                            \
+        return bf16 ? launch_pdl(kvq_meta_kernel<true, d, gs>, grid, dim3(kMetaWarps * 32), bytes, stream, a)           \
+                    : launch_pdl(kvq_meta_kernel<false, d, gs>, grid, dim3(kMetaWarps * 32), bytes, stream, a);
+    KVQ_FORMATS(KVQ_META)
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace qskv

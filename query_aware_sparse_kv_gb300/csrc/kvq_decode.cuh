@@ -93,11 +93,6 @@ __device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
 // Codes 0 and 4 of a word less 8, and codes 1 and 5 less 8 times 16: 0x6400 | x
 // is 1024 + x, exactly.  `k1024` holds 0x64006400 in a register the compiler
 // cannot see through, so that mask and magic are one instruction.
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
-    return r;
-}
 __device__ __forceinline__ uint32_t less8(uint32_t w, uint32_t k1024) {
     return add_half2(and_or(w, 0x000f000fu, k1024), 0xe408e408u);
 }
@@ -118,13 +113,6 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 __device__ __forceinline__ float on_grid(float x, float grid) {
     const float c = 12582912.f * grid;  // 1.5 * 2^23 units
     return (x + c) - c;
-}
-
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
 }
 
 __device__ __forceinline__ float max_over_tokens(float x) {

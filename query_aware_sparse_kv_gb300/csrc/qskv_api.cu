@@ -963,6 +963,8 @@ qskv_status qskv_kvq_meta_build(const void *pool, const int32_t *page_ids, const
         return fail(QSKV_ERR_INVALID_ARG, "pool and meta must be 16-byte aligned");
     if (!aligned(page_ids, 4) || !aligned(valid_tokens, 4))
         return fail(QSKV_ERR_INVALID_ARG, "page_ids and valid_tokens must be 4-byte aligned");
+    const int sms = current_sm_count(nullptr);
+    if (sms <= 0) return fail(QSKV_ERR_CUDA, "cannot query the current CUDA device");
     KvqMetaArgs a = {};
     a.pool = static_cast<const uint32_t *>(pool);
     a.page_ids = page_ids;
@@ -974,7 +976,7 @@ qskv_status qskv_kvq_meta_build(const void *pool, const int32_t *page_ids, const
     a.page_size = shape->page_size;
     a.num_pool_pages = shape->num_pool_pages;
     a.group_size = group_size;
-    return launched(launch_kvq_meta(a, meta_dtype, shape->head_dim, static_cast<cudaStream_t>(stream)),
+    return launched(launch_kvq_meta(a, meta_dtype, shape->head_dim, sms, static_cast<cudaStream_t>(stream)),
                     "kvq_meta_build launch");
 }
 

@@ -47,6 +47,21 @@ __device__ __forceinline__ int kvq_value_place(int w, int token) {
     return (((w >> 2) ^ x) << 2) | (w & 3);
 }
 
+// (w & mask) | magic in one instruction, if `magic` is in a register.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+    return r;
+}
+
+// Untiled bulk copy global -> shared (16-byte aligned, whole 16 bytes) that completes on `bar`.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 struct KvqStoreArgs {
     const void *k, *v;         // append: [n][Hkv][d], rows k_stride / v_stride elements apart
     void *k_out, *v_out;       // gather: [n][Hkv][d]
@@ -92,7 +107,7 @@ struct TablesArgs {
 
 cudaError_t launch_kvq_append(const KvqStoreArgs &a, int dtype, int head_dim, cudaStream_t stream);
 cudaError_t launch_kvq_gather(const KvqStoreArgs &a, int dtype, int head_dim, cudaStream_t stream);
-cudaError_t launch_kvq_meta(const KvqMetaArgs &a, int meta_dtype, int head_dim, cudaStream_t stream);
+cudaError_t launch_kvq_meta(const KvqMetaArgs &a, int meta_dtype, int head_dim, int num_sms, cudaStream_t stream);
 // Largest decode grid on a device with num_sms SMs, and its warps a CTA (for the workspace).
 int kvq_decode_ctas(int num_sms);
 int kvq_decode_warps();
