@@ -297,48 +297,48 @@ def cascade_paged_decode(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Te
 _I32 = torch.int32
 
 
-def _tensor(name: str, t, dtype, shape, device: torch.device):
-    """Pointer of a contiguous tensor of the given type and shape on `device`
-    (None: an optional one left out); q, out and lse may also be pinned host
-    memory."""
+def _tensor(name: str, t, dtype, shape, index: int):
+    """Address of a contiguous tensor of the given type and shape on CUDA
+    device `index` (None: an optional one left out); q, out and lse may also
+    be pinned host memory."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)} (got {t.dtype} {tuple(t.shape)})")
-    if t.device != device and (device.type != "cuda" or name not in ("q", "out", "lse") or not t.is_pinned()):
-        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if t.get_device() != index and (name not in ("q", "out", "lse") or t.is_cuda or not t.is_pinned()):
+        raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _device(name: str, t: torch.Tensor) -> torch.device:
-    if t.device.type != "cuda":
+def _device(name: str, t: torch.Tensor) -> int:
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
-    return t.device
+    return t.get_device()
 
 
-def _workspace(t: torch.Tensor, device: torch.device):
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"the workspace must be contiguous and on {device}")
-    return t.data_ptr(), t.numel() * t.element_size()
+def _workspace(t: torch.Tensor, index: int):
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous and on cuda:{index}")
+    return t.data_ptr(), t.nbytes
 
 
-def _run(fn, device: torch.device, args, stream):
-    """The call on `device`, on its current stream unless one is given."""
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, _stream(stream))
+def _run(fn, index: int, args, stream):
+    """The call on device `index`, on its current stream unless one is given."""
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             st = fn(*args, _stream(stream))
     if st != 0:
         raise QskvError(st, _lib.qskv_last_error_message().decode())
 
 
-def _pool_ptr(pool: torch.Tensor, shape: Shape, group_size: int, device: torch.device):
+def _pool_ptr(pool: torch.Tensor, shape: Shape, group_size: int, index: int):
     P, d = shape.page_size, shape.head_dim
     block = P * (d + 8 * (d // max(int(group_size), 1)))
-    return _tensor("pool", pool, torch.uint8, (shape.num_pool_pages, shape.num_kv_heads, block), device)
+    return _tensor("pool", pool, torch.uint8, (shape.num_pool_pages, shape.num_kv_heads, block), index)
 
 
 def kvq_block_bytes(shape: Shape, group_size: int) -> int:
@@ -364,15 +364,16 @@ def tables_workspace_size(shape: Shape) -> int:
     return int(n)
 
 
-def _rows(name: str, t: torch.Tensor, dtype, n: int, heads: int, d: int, device: torch.device) -> int:
-    if t.dtype != dtype or t.shape != (n, heads, d):
+def _rows(name: str, t: torch.Tensor, dtype, n: int, heads: int, d: int, index: int):
+    """Address and token stride of a [n][heads][d] tensor with contiguous heads and dims."""
+    if t.dtype is not dtype or t.shape != (n, heads, d):
         raise ValueError(f"{name} must be {dtype} {(n, heads, d)} (got {t.dtype} {tuple(t.shape)})")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
     sn, sh, sd = t.stride()
-    if (sd != 1 and d > 1) or (sh != d and heads > 1):
+    if sd != 1 or (sh != d and heads > 1):
         raise ValueError(f"the heads and dims of {name} must be contiguous (strides {t.stride()})")
-    return t.data_ptr()
+    return t.data_ptr(), sn
 
 
 def kvq_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor, shape: Shape,
@@ -382,8 +383,9 @@ def kvq_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool: torc
     lib = _lib or load()
     dev = _device("pool", pool)
     n, heads, d = slots.numel(), shape.num_kv_heads, shape.head_dim
-    args = (_rows("k", k, k.dtype, n, heads, d, dev), _rows("v", v, k.dtype, n, heads, d, dev), _dtype(k),
-            k.stride(0), v.stride(0), _tensor("slots", slots, _I32, (n,), dev), n,
+    kp, ks = _rows("k", k, k.dtype, n, heads, d, dev)
+    vp, vs = _rows("v", v, k.dtype, n, heads, d, dev)
+    args = (kp, vp, _dtype(k), ks, vs, _tensor("slots", slots, _I32, (n,), dev), n,
             _pool_ptr(pool, shape, group_size, dev), ctypes.byref(shape), group_size, *_workspace(workspace, dev))
     _run(lib.qskv_kvq_append, dev, args, stream)
 
