@@ -54,7 +54,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kEntries = 512;      // entries of the unit prefix held in shared memory
 constexpr int kFill = 16;          // units a warp describes at once (a multiple of the units a stage)
-constexpr int kRowModePages = 64, kRowCtas = 16;
+constexpr int kRowModePages = 64, kRowCtas = 16, kRowUnits = 32;
 constexpr int kMaxRing = 8;        // stages a warp
 constexpr float kNoRef = -1e30f;   // M before the first token
 // Largest weight, and largest weight times value scale, in the references' units; the grid of the latter's hi half.
@@ -164,8 +164,8 @@ struct Shared {
     // pieces of rows that no warp owns whole: 2w ends in, 2w + 1 runs on from, warp w's range
     int piece_row[2 * kWarps], piece_begin[2 * kWarps], piece_end[2 * kWarps];
     float piece_m[2 * kWarps][8], piece_l[2 * kWarps][8], piece_f[2 * kWarps][8];
-    // rows that other CTAs hold pieces of
-    int open, open_row[2], open_slot0[2], open_slot1[2], open_n[2], open_last[2];
+    // rows that other CTAs hold pieces of and whose last ticket this one drew
+    int open, open_row[2], open_slot0[2], open_slot1[2], open_n[2];
     float row_m[8], row_l[8];
 };
 
@@ -704,18 +704,23 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
             break;
         }
         const uint8_t *stage = ring + got * (U * block_bytes);
+        if (HC == 4 && same) {
+#pragma unroll
+            for (int t = 0; t < kTiles; t++) st.tile(stage + t / kPageTiles * block_bytes, t % kPageTiles, 16);
+        } else {
 #pragma unroll 1
-        for (int t = 0; t < kTiles; t++) {
-            int nv = 16;
-            if (!same) {
-                const int it = k * U + t / kPageTiles;
-                if (it >= n) break;
-                const Unit u = s.desc[warp][it % (2 * kFill)];
-                enter(u, it);
-                nv = min((u.row_valid & 63) - t % kPageTiles * 16, 16);
-                if (!u.src || nv <= 0) continue;
+            for (int t = 0; t < kTiles; t++) {
+                int nv = 16;
+                if (HC == 4 || !same) {
+                    const int it = k * U + t / kPageTiles;
+                    if (it >= n) break;
+                    const Unit u = s.desc[warp][it % (2 * kFill)];
+                    enter(u, it);
+                    nv = min((u.row_valid & 63) - t % kPageTiles * 16, 16);
+                    if (!u.src || nv <= 0) continue;
+                }
+                st.tile(stage + t / kPageTiles * block_bytes, t % kPageTiles, nv);
             }
-            st.tile(stage + t / kPageTiles * block_bytes, t % kPageTiles, nv);
         }
         if (++got == S) got = 0, parity ^= 1;
         __syncwarp();
@@ -724,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
     if (row >= 0) close(true);
     __syncthreads();
 
-    // ---- pieces of one row within the CTA, in unit order
+    // ---- pieces of one row within the CTA, in unit order: a run of pieces to a warp
     const int elems = G * D / 4;
     if (tid < 16 * kWarps) {  // weight of each piece for each head
         const int k = tid >> 3, h = tid & 7, r = s.piece_row[k];
@@ -737,24 +742,27 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
         }
     }
     __syncthreads();
-    for (int i = 0; i < 2 * kWarps;) {
-        const int r = s.piece_row[i];
-        if (r < 0) {
-            i++;
-            continue;
-        }
-        int end = i + 1;
-        while (end < 2 * kWarps && (s.piece_row[end] < 0 || s.piece_row[end] == r)) end++;
-        const int begin_u = s.piece_begin[i], end_u = s.piece_end[i];
+    const int piece_row = lane < 2 * kWarps ? s.piece_row[lane] : -1;
+    const uint32_t pieces = __ballot_sync(0xffffffffu, piece_row >= 0);
+    // a run starts at a piece whose row the piece before it (of those there are) does not have
+    const uint32_t earlier = pieces & ((1u << lane) - 1);
+    const int previous = __shfl_sync(0xffffffffu, piece_row, earlier ? 31 - __clz(earlier) : 0);
+    uint32_t runs = __ballot_sync(0xffffffffu, piece_row >= 0 && (!earlier || previous != piece_row));
+    for (int i = 0; runs; i++, runs &= runs - 1) {
+        if (i % kWarps != warp) continue;
+        const int first = __ffs(runs) - 1;
+        const int r = __shfl_sync(0xffffffffu, piece_row, first);
+        const uint32_t members = __ballot_sync(0xffffffffu, piece_row == r);
+        const int begin_u = s.piece_begin[first], end_u = s.piece_end[first];
         const bool whole = begin_u >= cta_begin && end_u <= cta_end;
         const int slot = a.row_ctas ? blockIdx.x : 2 * blockIdx.x + (begin_u < cta_begin ? 0 : 1);
         const int64_t head0 = int64_t(r / a.num_kv_heads) * a.num_q_heads + int64_t(r % a.num_kv_heads) * G;
-        for (int e = tid; e < elems; e += kThreads) {
+        for (int e = lane; e < elems; e += 32) {
             const int h = e * 4 / D;
             float m = kNoRef, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = i; k < end; k++) {
-                if (s.piece_row[k] < 0) continue;
+            for (uint32_t left = members; left; left &= left - 1) {
+                const int k = __ffs(left) - 1;
                 const float f = s.piece_f[k][h];
                 const float *src = k & 1 ? reinterpret_cast<const float *>(ring_mem + (k >> 1) * (S * U * block_bytes))
                                          : a.first_o + (int64_t(blockIdx.x) * kWarps + (k >> 1)) * (G * D);
@@ -771,33 +779,26 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
                 if (e * 4 % D == 0) a.part_ml[slot * 16 + h] = m, a.part_ml[slot * 16 + 8 + h] = l;
             }
         }
-        if (!whole && tid == 0) {  // at most two: one that begins before, one that ends after the CTA's range
-            const int x = s.open++;
-            s.open_row[x] = r;
-            if (a.row_ctas) {
-                s.open_slot0[x] = s.open_slot1[x] = row0 * a.row_ctas;
-                s.open_n[x] = (count0 + upc - 1) / upc;
-            } else {  // the CTA where a row begins wrote its slot 1, the later ones their slot 0
-                const int c = begin_u / upc;
-                s.open_slot0[x] = 2 * c + 1, s.open_slot1[x] = 2 * c;
-                s.open_n[x] = (end_u - 1) / upc - c + 1;
+        if (whole) continue;
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) {
+            // pieces of the row: one for each CTA its units fall into
+            int c = row0 * a.row_ctas, np = (count0 + upc - 1) / upc;
+            if (!a.row_ctas) c = begin_u / upc, np = (end_u - 1) / upc - c + 1;
+            if (atomicAdd(a.tickets + r, 1u) == uint32_t(np - 1)) {
+                a.tickets[r] = 0;
+                const int x = atomicAdd(&s.open, 1);  // at most two: one from before, one beyond the CTA's range
+                s.open_row[x] = r, s.open_n[x] = np;
+                // the CTA where a row begins wrote its slot 1, the later ones their slot 0
+                s.open_slot0[x] = a.row_ctas ? c : 2 * c + 1, s.open_slot1[x] = a.row_ctas ? c : 2 * c;
             }
         }
-        i = end;
-    }
-    __threadfence();
-    __syncthreads();
-    if (s.open == 0) return;
-    if (tid < s.open) {
-        const bool last = atomicAdd(a.tickets + s.open_row[tid], 1u) == uint32_t(s.open_n[tid] - 1);
-        if (last) a.tickets[s.open_row[tid]] = 0;
-        s.open_last[tid] = last;
     }
     __syncthreads();
 
     // ---- rows whose last ticket this CTA drew: pieces of several CTAs, in unit order
     for (int f = 0; f < s.open; f++) {
-        if (!s.open_last[f]) continue;
         const int r = s.open_row[f], np = s.open_n[f], slot0 = s.open_slot0[f], slot1 = s.open_slot1[f];
         const int step = a.row_ctas ? 1 : 2;
         float *pw = reinterpret_cast<float *>(ring_mem);  // [np][G] weights, then [kThreads] float4
@@ -873,7 +874,7 @@ cudaError_t launch_one(KvqDecodeArgs &a, int num_sms, cudaStream_t stream) {
     const int row_units = a.selected ? a.top_k : a.max_pages;
     a.row_ctas = 0;
     if (rows <= slots && (a.selected || row_units <= kRowModePages)) {
-        const int most = slots / rows, want = (row_units + kWarps - 1) / kWarps;
+        const int most = slots / rows, want = (row_units + kRowUnits - 1) / kRowUnits;
         a.row_ctas = want < most ? want : most;
         if (a.row_ctas > kRowCtas) a.row_ctas = kRowCtas;
     }
