@@ -27,7 +27,7 @@
 //
 // Softmax.  Running references per head: M for the exponent and sg for the
 // weights times value scales (p s sg is what becomes fp16).  Both are moved
-// only when a weight would pass 2^12, or p s sg 2^9 (rare after the first
+// only when a weight would pass 2^12, or p s sg 2^14 (rare after the first
 // tile), so the usual tile has no rescaling and one vote.  Sums of weights
 // and of p m stay per lane until the row ends.
 //
@@ -57,8 +57,8 @@ constexpr int kFill = 16;          // units a warp describes at once (a multiple
 constexpr int kRowModePages = 64, kRowCtas = 16, kRowUnits = 32;
 constexpr int kMaxRing = 8;        // stages a warp
 constexpr float kNoRef = -1e30f;   // M before the first token
-// Largest weight, and largest weight times value scale, in the references' units; the grid of the latter's hi half.
-constexpr float kTopP = 4096.f, kTopW = 511.f, kGridW = 0.25f;
+// Largest weight, and largest weight times value scale, in the references' units.
+constexpr float kTopP = 4096.f, kTopW = 16383.f;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -105,11 +105,15 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// x rounded to a multiple of `grid`, a power of two.  The hi halves of
-// queries and weights are multiples of one grid with at most 11 bits, so a
-// hi half times a code is exact and so are sums of them up to 2^24 grid
-// units: the tensor cores, which cut each product to the scale of the
-// largest, then cut nothing.
+// x rounded to fp16, as a float.
+__device__ __forceinline__ float to_half(float x) { return __half2float(__float2half_rn(x)); }
+
+// x rounded to a multiple of `grid`, a power of two.  The hi halves of fp32
+// queries are multiples of one grid with at most 11 bits.  Key codes are
+// subnormal operands, which the tensor cores line up 7 bits lower than their
+// value; on a grid a hi half times a code, and sums of them up to 2^24 grid
+// units, lose nothing by that.  (Value codes are normal numbers, and the
+// weights' hi halves simply rounded.)
 __device__ __forceinline__ float on_grid(float x, float grid) {
     const float c = 12582912.f * grid;  // 1.5 * 2^23 units
     return (x + c) - c;
@@ -164,8 +168,8 @@ struct Shared {
     // pieces of rows that no warp owns whole: 2w ends in, 2w + 1 runs on from, warp w's range
     int piece_row[2 * kWarps], piece_begin[2 * kWarps], piece_end[2 * kWarps];
     float piece_m[2 * kWarps][8], piece_l[2 * kWarps][8], piece_f[2 * kWarps][8];
-    // rows that other CTAs hold pieces of and whose last ticket this one drew
-    int open, open_row[2], open_slot0[2], open_slot1[2], open_n[2];
+    // rows that other CTAs hold pieces of
+    int open, open_row[2], open_slot0[2], open_slot1[2], open_n[2], open_last[2];
     float row_m[8], row_l[8];
 };
 
@@ -427,10 +431,10 @@ struct RowState {
                 for (int j = 0; j < NG; j++)
                     top = fmaxf(top, fmaxf(p[0][h] * bf16_lo_to_float(va[j]), p[1][h] * bf16_lo_to_float(vb[j])));
                 top = max_over_tokens(top);
-                // sg such that the tile's largest p s sg lies in [2^6, 2^7); what is summed already may grow by 2^30
+                // sg such that the tile's largest p s sg lies in [2^8, 2^9); what is summed already may grow by 2^30
                 float s = sg[h];
                 if (top >= 7.888609052210118e-31f) {  // 2^-100
-                    s = __uint_as_float((260u << 23) - (__float_as_uint(top) & 0x7f800000u));
+                    s = __uint_as_float((262u << 23) - (__float_as_uint(top) & 0x7f800000u));
                     if (m[h] != kNoRef) s = fminf(s, sg[h] * 1073741824.f);
                 }
                 const float r = f * (s / sg[h]);
@@ -478,13 +482,13 @@ struct RowState {
                     if constexpr (HC == 4) {
 #pragma unroll
                         for (int k = 0; k < 2; k++) {
-                            const float x = on_grid(w[k][0][j], kGridW);
+                            const float x = to_half(w[k][0][j]);
                             bh[k] = movmatrix_trans(pack_half2(x, w[k][0][j] - x));
                         }
                     } else {
 #pragma unroll
                         for (int k = 0; k < 2; k++) {
-                            const float x = on_grid(w[k][0][j], kGridW), y = on_grid(w[k][NH - 1][j], kGridW);
+                            const float x = to_half(w[k][0][j]), y = to_half(w[k][NH - 1][j]);
                             bh[k] = movmatrix_trans(pack_half2(x, y));
                             bl[k] = movmatrix_trans(pack_half2(w[k][0][j] - x, w[k][NH - 1][j] - y));
                         }
@@ -729,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
     if (row >= 0) close(true);
     __syncthreads();
 
-    // ---- pieces of one row within the CTA, in unit order: a run of pieces to a warp
+    // ---- pieces of one row within the CTA, in unit order
     const int elems = G * D / 4;
     if (tid < 16 * kWarps) {  // weight of each piece for each head
         const int k = tid >> 3, h = tid & 7, r = s.piece_row[k];
@@ -747,29 +751,34 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
     // a run starts at a piece whose row the piece before it (of those there are) does not have
     const uint32_t earlier = pieces & ((1u << lane) - 1);
     const int previous = __shfl_sync(0xffffffffu, piece_row, earlier ? 31 - __clz(earlier) : 0);
-    uint32_t runs = __ballot_sync(0xffffffffu, piece_row >= 0 && (!earlier || previous != piece_row));
-    for (int i = 0; runs; i++, runs &= runs - 1) {
-        if (i % kWarps != warp) continue;
-        const int first = __ffs(runs) - 1;
+    const uint32_t runs = __ballot_sync(0xffffffffu, piece_row >= 0 && (!earlier || previous != piece_row));
+    const int chunks = (elems + 31) / 32, items = __popc(runs) * chunks;  // an item: 32 float4 of a run
+    for (int i = warp; i < items; i += kWarps) {
+        uint32_t left = runs;
+        for (int k = i / chunks; k > 0; k--) left &= left - 1;
+        const int first = __ffs(left) - 1, e = i % chunks * 32 + lane;
         const int r = __shfl_sync(0xffffffffu, piece_row, first);
         const uint32_t members = __ballot_sync(0xffffffffu, piece_row == r);
         const int begin_u = s.piece_begin[first], end_u = s.piece_end[first];
         const bool whole = begin_u >= cta_begin && end_u <= cta_end;
         const int slot = a.row_ctas ? blockIdx.x : 2 * blockIdx.x + (begin_u < cta_begin ? 0 : 1);
-        const int64_t head0 = int64_t(r / a.num_kv_heads) * a.num_q_heads + int64_t(r % a.num_kv_heads) * G;
-        for (int e = lane; e < elems; e += 32) {
+        if (e < elems) {
             const int h = e * 4 / D;
             float m = kNoRef, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (uint32_t left = members; left; left &= left - 1) {
-                const int k = __ffs(left) - 1;
+            auto add = [&](int k, const float *src) {
                 const float f = s.piece_f[k][h];
-                const float *src = k & 1 ? reinterpret_cast<const float *>(ring_mem + (k >> 1) * (S * U * block_bytes))
-                                         : a.first_o + (int64_t(blockIdx.x) * kWarps + (k >> 1)) * (G * D);
                 const float4 v = reinterpret_cast<const float4 *>(src)[e];
                 l = fmaf(f, s.piece_l[k][h], l), m = fmaxf(m, s.piece_m[k][h]);
                 o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+            };
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) {
+                if (members >> (2 * w) & 1) add(2 * w, a.first_o + (int64_t(blockIdx.x) * kWarps + w) * (G * D));
+                if (members >> (2 * w + 1) & 1)
+                    add(2 * w + 1, reinterpret_cast<const float *>(ring_mem + w * (S * U * block_bytes)));
             }
+            const int64_t head0 = int64_t(r / a.num_kv_heads) * a.num_q_heads + int64_t(r % a.num_kv_heads) * G;
             if (whole) {
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 reinterpret_cast<float4 *>(a.out + head0 * D)[e] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
@@ -779,16 +788,13 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
                 if (e * 4 % D == 0) a.part_ml[slot * 16 + h] = m, a.part_ml[slot * 16 + 8 + h] = l;
             }
         }
-        if (whole) continue;
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) {
-            // pieces of the row: one for each CTA its units fall into
-            int c = row0 * a.row_ctas, np = (count0 + upc - 1) / upc;
-            if (!a.row_ctas) c = begin_u / upc, np = (end_u - 1) / upc - c + 1;
-            if (atomicAdd(a.tickets + r, 1u) == uint32_t(np - 1)) {
-                a.tickets[r] = 0;
-                const int x = atomicAdd(&s.open, 1);  // at most two: one from before, one beyond the CTA's range
+        if (!whole) {
+            __threadfence();
+            if (lane == 0 && i % chunks == 0) {  // at most two: a row from before, a row beyond the CTA's range
+                // pieces of the row: one for each CTA its units fall into
+                int c = row0 * a.row_ctas, np = (count0 + upc - 1) / upc;
+                if (!a.row_ctas) c = begin_u / upc, np = (end_u - 1) / upc - c + 1;
+                const int x = atomicAdd(&s.open, 1);
                 s.open_row[x] = r, s.open_n[x] = np;
                 // the CTA where a row begins wrote its slot 1, the later ones their slot 0
                 s.open_slot0[x] = a.row_ctas ? c : 2 * c + 1, s.open_slot1[x] = a.row_ctas ? c : 2 * c;
@@ -796,9 +802,17 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
         }
     }
     __syncthreads();
+    if (s.open == 0) return;
+    if (tid < s.open) {
+        const bool last = atomicAdd(a.tickets + s.open_row[tid], 1u) == uint32_t(s.open_n[tid] - 1);
+        if (last) a.tickets[s.open_row[tid]] = 0;
+        s.open_last[tid] = last;
+    }
+    __syncthreads();
 
     // ---- rows whose last ticket this CTA drew: pieces of several CTAs, in unit order
     for (int f = 0; f < s.open; f++) {
+        if (!s.open_last[f]) continue;
         const int r = s.open_row[f], np = s.open_n[f], slot0 = s.open_slot0[f], slot1 = s.open_slot1[f];
         const int step = a.row_ctas ? 1 : 2;
         float *pw = reinterpret_cast<float *>(ring_mem);  // [np][G] weights, then [kThreads] float4
