@@ -25,7 +25,8 @@ in include/qskv.h); this package is its binding:
   kvq_meta_build,        values, page metadata for the selection calls, and
   kvq_paged_decode       the decode over it (all pages or selected ones)
 
-plus ``PagedDecoder`` (buffer plumbing for a whole step) and ``workloads``
+plus ``PagedDecoder`` and ``QuantizedPagedDecoder`` (buffer plumbing for a
+whole step over a bf16 / fp32 and over a 4-bit cache) and ``workloads``
 (seeded synthetic inputs).  Nothing here computes on the CPU: without the
 built library every call raises.
 """
@@ -35,7 +36,7 @@ from .binding import (QSKV_BF16, QSKV_F32, QskvError, QskvLibraryMissing, Shape,
                       last_error_message, load, make_shape, page_select, page_select_approx, page_select_refresh, page_select_centroid,
                       select_decode, sparse_paged_decode, sparse_paged_decode_noalloc, tables_workspace_size,
                       workspace_size)
-from .engine import PagedDecoder, from_inputs
+from .engine import PagedDecoder, QuantizedPagedDecoder, from_inputs
 
 __all__ = ["QSKV_BF16", "QSKV_F32", "QskvError", "QskvLibraryMissing", "Shape", "cascade_paged_decode",
            "cascade_workspace_size", "get_error", "kv_centroid_build", "kv_meta_build", "page_select_approx", "page_select_centroid",
@@ -44,4 +45,4 @@ __all__ = ["QSKV_BF16", "QSKV_F32", "QskvError", "QskvLibraryMissing", "Shape", 
            "sparse_paged_decode_noalloc", "workspace_size",
            "extend_tables", "kvq_append", "kvq_block_bytes", "kvq_gather", "kvq_meta_build", "kvq_paged_decode",
            "kvq_workspace_size", "tables_workspace_size",
-           "PagedDecoder", "from_inputs"]
+           "PagedDecoder", "QuantizedPagedDecoder", "from_inputs"]

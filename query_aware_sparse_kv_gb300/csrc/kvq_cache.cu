@@ -6,6 +6,8 @@
 // half a block and writes 2 d bf16.  A thread owns one 32-bit code word
 // (8 dims), so a bf16 row is read (or written) 16 bytes a lane and the
 // reductions over a group run over 4, 8 or 16 neighbouring lanes.
+#include <cuda_fp16.h>
+
 #include "qskv_internal.h"
 #include "qskv_kvq.cuh"
 
@@ -79,6 +81,28 @@ __device__ __forceinline__ uint32_t kvq_word(const float (&x)[8], float m, float
     return acc - sum16;
 }
 
+// The same for bf16 values with an exact minimum: the quotients are 0 to 15.06,
+// nothing to clamp, and unless a value is tiny against s they are rational
+// numbers with few bits: rounded to fp32 correctly (one residual step does
+// that), none but an exact tie lands on a tie, and adding 1.5 2^23 then rounds
+// it to even.  A quotient is (whole multiple of the smallest unit of x and m)
+// / s with an 8-bit s, so one that is no tie is at least that unit / 2^9 s
+// away from one; with x and m zero or above s / 2^10 that is 2^-19 or more,
+// beyond fp32's rounding at 15.
+__device__ __forceinline__ uint32_t kvq_word_plain(const float (&x)[8], float m, float s) {
+    constexpr float magic = 12582912.f;
+    constexpr uint32_t sum16 = 0x11111111u * 0x4b400000u;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    uint32_t acc = 0;
+#pragma unroll
+    for (int k = 7; k >= 0; k--) {
+        const float d = x[k] - m, q0 = d * inv, q = fmaf(fmaf(-q0, s, d), inv, q0);
+        acc = acc * 16 + __float_as_uint(q + magic);
+    }
+    return acc - sum16;
+}
+
 // The 8 raw 16-bit pairs or the 8 floats of a word as loaded.
 template <bool BF16>
 struct Raw8 {
@@ -90,6 +114,12 @@ struct Raw8 {
             a = ldg_stream_v4(static_cast<const float *>(base) + at);
             b = ldg_stream_v4(static_cast<const float *>(base) + at + 4);
         }
+    }
+    // Smallest magnitude among the word's values and m (bf16).
+    __device__ __forceinline__ float smallest(float m) const {
+        constexpr uint32_t abs2 = 0x7fff7fffu;
+        uint32_t r = Bf16Ops::vmin(Bf16Ops::vmin(a.x & abs2, a.y & abs2), Bf16Ops::vmin(a.z & abs2, a.w & abs2));
+        return fminf(fminf(bf16_lo_to_float(r), bf16_hi_to_float(r)), fabsf(m));
     }
     __device__ __forceinline__ void floats(float (&x)[8]) const {
         if constexpr (BF16) {
@@ -161,7 +191,13 @@ __global__ void __launch_bounds__(kCacheThreads) kvq_append_kernel(KvqStoreArgs 
         group_range<BF16, LANES>(raw[i], x, mn, mx);
         const uint32_t mbits = BF16 ? __float_as_uint(mn) >> 16 : __bfloat16_as_ushort(__float2bfloat16_rn(mn));
         const float m = bits_f(mbits << 16), s = kvq_scale(mx, m);
-        const uint32_t word = s > 0.f ? kvq_word<!BF16>(x, m, s) : 0u;
+        uint32_t word = 0;
+        if (s > 0.f) {
+            if (BF16 && raw[i].smallest(m) * 1024.f >= s)
+                word = kvq_word_plain(x, m, s);
+            else
+                word = kvq_word<!BF16>(x, m, s);
+        }
         const int page = slot[i] >> shift, t = slot[i] & (P - 1);
         if (slot[i] < 0) continue;
         if (page >= a.num_pool_pages) {
@@ -175,18 +211,19 @@ __global__ void __launch_bounds__(kCacheThreads) kvq_append_kernel(KvqStoreArgs 
     }
 }
 
-// m + s u of the 8 codes of a word, each with fp32's one rounding.  A code is
-// cut out in place under the exponent of 2^23, so the float is 2^23 + 16^k u;
-// the 2^23 comes off exactly and the scale carries 16^-k.
+// m + s u of the 8 codes of a word, each with fp32's one rounding.  A pair of
+// codes cut out in place is a pair of fp16 subnormals u 2^-24 (or 16 u 2^-24),
+// which one conversion each makes floats; the scale carries the 2^24 back.
 __device__ __forceinline__ void kvq_values(uint32_t word, uint32_t par, float (&x)[8]) {
-    const float s = bf16_lo_to_float(par), m = bf16_hi_to_float(par);
-    const float sk[4] = {s, s * 0.0625f, s * 0.00390625f, s * 0.000244140625f};
+    const float m = bf16_hi_to_float(par), s = bf16_lo_to_float(par) * 16777216.f, s16 = s * 0.0625f;
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-        const uint32_t w = h ? word >> 16 : word;
-#pragma unroll
-        for (int k = 0; k < 4; k++)
-            x[4 * h + k] = fmaf(bits_f((w & (15u << (4 * k))) | 0x4b000000u) - 8388608.f, sk[k], m);
+        const uint32_t w = h ? word >> 8 : word;
+        const uint32_t even = w & 0x000f000fu, odd = w & 0x00f000f0u;
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&even));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&odd));
+        x[2 * h] = fmaf(a.x, s, m), x[2 * h + 4] = fmaf(a.y, s, m);
+        x[2 * h + 1] = fmaf(b.x, s16, m), x[2 * h + 5] = fmaf(b.y, s16, m);
     }
 }
 
@@ -241,52 +278,11 @@ __global__ void __launch_bounds__(kCacheThreads) kvq_gather_kernel(KvqStoreArgs 
     }
 }
 
-// fp32 -> bf16 bits, rounded towards -inf or +inf: the metadata stays a bound
-// of every cached key after the rounding.
-__device__ __forceinline__ uint32_t bf16_down(float x) {
-    return __bfloat16_as_ushort(__float2bfloat16_rd(x));
-}
-__device__ __forceinline__ uint32_t bf16_up(float x) { return __bfloat16_as_ushort(__float2bfloat16_ru(x)); }
-
-// Pairs of fp32 in one instruction.
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t p, float &lo, float &hi) {
-    uint32_t a, b;
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(p));
-    lo = bits_f(a), hi = bits_f(b);
-}
-
-// kvq_values, two codes an instruction.  `k23` holds 0x4b000000 in a register
-// the compiler cannot see through, so that mask and exponent are one
-// instruction.
-__device__ __forceinline__ void kvq_values2(uint32_t word, uint32_t par, uint32_t k23, float (&x)[8]) {
-    const float s = bf16_lo_to_float(par);
-    const uint32_t m = par & 0xffff0000u;
-    const uint64_t mm = pair(m, m), off = pair(0xcb000000u, 0xcb000000u);  // -2^23
-    const uint64_t s01 = pair(__float_as_uint(s), __float_as_uint(s * 0.0625f));
-    const uint64_t s23 = pair(__float_as_uint(s * 0.00390625f), __float_as_uint(s * 0.000244140625f));
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-        const uint32_t w = h ? word >> 16 : word;
-        const uint64_t a = pair(and_or(w, 0xfu, k23), and_or(w, 0xf0u, k23));
-        const uint64_t b = pair(and_or(w, 0xf00u, k23), and_or(w, 0xf000u, k23));
-        unpair(pair_fma(pair_add(a, off), s01, mm), x[4 * h], x[4 * h + 1]);
-        unpair(pair_fma(pair_add(b, off), s23, mm), x[4 * h + 2], x[4 * h + 3]);
-    }
+// Two floats -> bf16x2, rounded down.
+__device__ __forceinline__ uint32_t pack_bf16x2_down(float lo, float hi) {
+    // truncation rounds towards zero: a negative value goes up by one if anything is cut off
+    const uint32_t a = __float_as_uint(lo), b = __float_as_uint(hi);
+    return __byte_perm(a + (uint32_t(int32_t(a) >> 31) & 0xffffu), b + (uint32_t(int32_t(b) >> 31) & 0xffffu), 0x7632);
 }
 
 // A warp takes (listed page, KV head) tiles in turn through a ring of bulk
@@ -354,8 +350,6 @@ __global__ void __launch_bounds__(kMetaWarps * 32, 4) kvq_meta_kernel(KvqMetaArg
         if (++put == S) put = 0;
     };
     const int place = lane % W, t0 = lane / W, w = kvq_key_word<D>(place);
-    uint32_t k23;
-    asm("mov.b32 %0, 0x4b000000;" : "=r"(k23));
     describe(0);
     for (int i = 0; i < S - 1; i++) issue(i);
     // a description is replaced once its 32 tiles are under way, so what the loop needs of the older ones is kept
@@ -381,39 +375,48 @@ __global__ void __launch_bounds__(kMetaWarps * 32, 4) kvq_meta_kernel(KvqMetaArg
             float mn[8], mx[8];
 #pragma unroll
             for (int k = 0; k < 8; k++) mn[k] = INFINITY, mx[k] = -INFINITY;
-#pragma unroll 2
-            for (int t = t0; t - t0 < v; t += 2 * TP) {  // a token past the end repeats the last one
-                const int ta = min(t, v - 1), tb = min(t + TP, v - 1);
+            auto take = [&](int ta, int tb) {
                 float x[8], y[8];
-                kvq_values2(codes[ta * W + place], params[ta], k23, x);
-                kvq_values2(codes[tb * W + place], params[tb], k23, y);
+                kvq_values(codes[ta * W + place], params[ta], x);
+                kvq_values(codes[tb * W + place], params[tb], y);
 #pragma unroll
                 for (int k = 0; k < 8; k++) {
                     mn[k] = fminf(fminf(x[k], y[k]), mn[k]);
                     mx[k] = fmaxf(fmaxf(x[k], y[k]), mx[k]);
                 }
+            };
+            if (v == P) {
+                for (int c = 0; c < P; c += 16)
+#pragma unroll
+                    for (int t = 0; t < 16; t += 2 * TP) take(c + t + t0, c + t + t0 + TP);
+            } else {
+#pragma unroll 1
+                for (int t = 0; t < v; t += 2 * TP)  // a token past the end repeats the last one
+                    take(min(t + t0, v - 1), min(t + t0 + TP, v - 1));
             }
+            // even lane groups (of W lanes) end up with the minima, odd ones with the negated maxima
+            const bool odd = t0 & 1;
+            float r[8];
 #pragma unroll
-            for (int o = W; o < 32; o <<= 1)
-#pragma unroll
-                for (int k = 0; k < 8; k++) {
-                    mn[k] = fminf(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], o));
-                    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
-                }
-            // the first lanes of a word write the minima, the next ones the maxima
+            for (int k = 0; k < 8; k++) {
+                const float other = __shfl_xor_sync(0xffffffffu, odd ? mn[k] : -mx[k], W);
+                r[k] = fminf(odd ? -mx[k] : mn[k], other);
+                if (TP == 4) r[k] = fminf(r[k], __shfl_xor_sync(0xffffffffu, r[k], 2 * W));
+            }
             if (t0 < 2) {
                 const int64_t to = (b * 2 + t0) * D + w * 8;
+                const uint32_t sign = odd ? 0x80000000u : 0u;
                 if constexpr (BF16) {
-                    uint32_t r[4];
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        r[k] = t0 == 0 ? bf16_down(mn[2 * k]) | (bf16_down(mn[2 * k + 1]) << 16)
-                                       : bf16_up(mx[2 * k]) | (bf16_up(mx[2 * k + 1]) << 16);
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.meta) + to) = make_uint4(r[0], r[1], r[2], r[3]);
+                    const uint32_t sign2 = sign | sign >> 16;
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.meta) + to) =
+                        make_uint4(pack_bf16x2_down(r[0], r[1]) ^ sign2, pack_bf16x2_down(r[2], r[3]) ^ sign2,
+                                   pack_bf16x2_down(r[4], r[5]) ^ sign2, pack_bf16x2_down(r[6], r[7]) ^ sign2);
                 } else {
+#pragma unroll
+                    for (int k = 0; k < 8; k++) r[k] = bits_f(__float_as_uint(r[k]) ^ sign);
                     float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.meta) + to);
-                    o[0] = t0 == 0 ? make_float4(mn[0], mn[1], mn[2], mn[3]) : make_float4(mx[0], mx[1], mx[2], mx[3]);
-                    o[1] = t0 == 0 ? make_float4(mn[4], mn[5], mn[6], mn[7]) : make_float4(mx[4], mx[5], mx[6], mx[7]);
+                    o[0] = make_float4(r[0], r[1], r[2], r[3]);
+                    o[1] = make_float4(r[4], r[5], r[6], r[7]);
                 }
             }
         }

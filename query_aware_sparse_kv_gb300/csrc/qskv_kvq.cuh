@@ -113,8 +113,8 @@ int kvq_decode_ctas(int num_sms);
 int kvq_decode_warps();
 cudaError_t launch_kvq_decode_page32(KvqDecodeArgs a, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_kvq_decode(KvqDecodeArgs a, int head_dim, int num_sms, cudaStream_t stream);
-// Requests that one CTA of the page-table builder scans in shared memory.
-constexpr int kTablesScanRequests = 2048;
+// Requests that one CTA of the page-table builder scans in shared memory (three prefixes, below 48 KB).
+constexpr int kTablesScanRequests = 4032;
 // scratch: 3 (batch + 1) int32, used beyond kTablesScanRequests requests.
 cudaError_t launch_extend_tables(const TablesArgs &a, int32_t *scratch, int num_sms, cudaStream_t stream);
 

@@ -30,7 +30,7 @@
 namespace qskv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kScanRequests = kTablesScanRequests;
 
 struct Need {
@@ -51,24 +51,28 @@ struct Prefix {
     }
 };
 
+// Pages hold 16 or 32 tokens.
+__device__ __forceinline__ int page_shift(const TablesArgs &a) { return a.page_size == 16 ? 4 : 5; }
+
 struct Request {
     int32_t old, add;
     bool valid;
     int32_t have, now;  // pages before and after (valid requests)
-    __device__ __forceinline__ Request(const TablesArgs &a, int b) {
-        old = a.seq_lens[b];
-        add = a.new_lens[b];
+    __device__ __forceinline__ Request(const TablesArgs &a, int b) : Request(a, a.seq_lens[b], a.new_lens[b]) {}
+    __device__ __forceinline__ Request(const TablesArgs &a, int32_t length, int32_t more) {
+        old = length;
+        add = more;
         const int64_t cap = int64_t(a.max_pages) * a.page_size;
         valid = old >= 0 && add >= 0 && int64_t(old) + add <= cap;
         const uint32_t P = a.page_size;  // unsigned: the sums may pass 2^31 - 1 by P - 1
-        have = valid ? int32_t((uint32_t(old) + P - 1) / P) : 0;
-        now = valid ? int32_t((uint32_t(old) + uint32_t(add) + P - 1) / P) : 0;
+        have = valid ? int32_t((uint32_t(old) + P - 1) >> page_shift(a)) : 0;
+        now = valid ? int32_t((uint32_t(old) + uint32_t(add) + P - 1) >> page_shift(a)) : 0;
     }
     __device__ __forceinline__ Need need(const TablesArgs &a) const {
         Need n;
         n.tok = max(add, 0);
         n.need = now - have;
-        n.touch = valid && add > 0 ? now - old / a.page_size : 0;
+        n.touch = valid && add > 0 ? now - (old >> page_shift(a)) : 0;
         return n;
     }
 };
@@ -106,18 +110,30 @@ __device__ __forceinline__ Need block_scan(const Need &mine, const Need &base, N
     return before;
 }
 
-// Prefixes of requests [r0, r1), r1 - r0 <= kScanRequests, into p[r0 - shift ..].
-__device__ void scan_requests(const TablesArgs &a, int r0, int r1, int shift, const Need &base, const Prefix &p) {
+// Prefixes of requests [r0, r1), r1 - r0 <= kScanRequests, into p[r0 ..]; a
+// thread's lengths are all loaded before the first is used.
+__device__ void scan_requests(const TablesArgs &a, int r0, int r1, const Need &base, const Prefix &p) {
+    constexpr int kEach = (kScanRequests + kThreads - 1) / kThreads;
     const int per = (r1 - r0 + kThreads - 1) / kThreads;
-    const int b0 = min(r0 + int(threadIdx.x) * per, r1), b1 = min(b0 + per, r1);
-    Need mine = {0, 0, 0};
-    for (int b = b0; b < b1; b++) mine += Request(a, b).need(a);
-    Need total, run = block_scan(mine, base, &total);
-    for (int b = b0; b < b1; b++) {
-        p.set(b - shift, run);
-        run += Request(a, b).need(a);
+    const int b0 = r0 + int(threadIdx.x) * per, n = max(0, min(per, r1 - b0));
+    int32_t old[kEach], add[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+        old[i] = add[i] = 0;
+        if (i < n) old[i] = a.seq_lens[b0 + i], add[i] = a.new_lens[b0 + i];
     }
-    if (threadIdx.x == 0 && r1 == a.batch) p.set(r1 - shift, total);
+    Need mine = {0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kEach; i++)
+        if (i < n) mine += Request(a, old[i], add[i]).need(a);
+    Need total, run = block_scan(mine, base, &total);
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+        if (i >= n) break;
+        p.set(b0 + i, run);
+        run += Request(a, old[i], add[i]).need(a);
+    }
+    if (threadIdx.x == 0 && r1 == a.batch) p.set(r1, total);
 }
 
 // Last index i of prefix[0..n] with prefix[i] <= x (prefix[0] = 0 <= x).
@@ -147,10 +163,59 @@ __device__ __forceinline__ int page_of(const TablesArgs &a, const Prefix &p, con
     return -1;
 }
 
-__device__ void write_tables(const TablesArgs &a, const Prefix &p) {
+// n <= 4 values at dst[i], i a multiple of 4: one store where the buffer allows it.
+__device__ __forceinline__ void store4(int32_t *dst, int64_t i, int n, const int (&v)[4]) {
+    if (n == 4 && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+        *reinterpret_cast<int4 *>(dst + i) = make_int4(v[0], v[1], v[2], v[3]);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        if (k < n) dst[i + k] = v[k];
+}
+
+// Slots and positions of the tokens from i on, SPAN (1 or 4) of them.
+template <int SPAN>
+__device__ __forceinline__ void write_tokens(const TablesArgs &a, const Prefix &p, int64_t i) {
+    const int P = a.page_size, B = a.batch, n = int(min(int64_t(SPAN), a.max_tokens - i));
+    int slot[4], pos[4], b = find(p.tok, B, int(i)), last = -1, page = -1, id = -1;
+    bool fits = false;
+    Request r(a, 0, 0);
+#pragma unroll 1
+    for (int k = 0; k < SPAN; k++) {
+        slot[k] = pos[k] = -1;
+        if (k >= n) continue;
+        while (b < B && p.tok[b + 1] <= int(i) + k) b++;
+        if (b >= B) continue;
+        if (b != last) r = Request(a, b), fits = admitted(a, p, r, b), last = b, page = -1;
+        if (!fits) continue;
+        pos[k] = r.old + int(i) + k - p.tok[b];
+        const int j = pos[k] >> page_shift(a);
+        if (j != page) page = j, id = page_of(a, p, r, b, j);
+        if (id >= 0) slot[k] = id * P + (pos[k] - j * P);
+    }
+    if (SPAN == 1) {
+        a.slot_map[i] = slot[0];
+        if (a.positions) a.positions[i] = pos[0];
+        return;
+    }
+    store4(a.slot_map, i, n, slot);
+    if (a.positions) store4(a.positions, i, n, pos);
+}
+
+// The CTAs below `token_ctas` write the tokens' outputs, the others those of
+// the requests and of the touched pages; the last one also the counts.
+template <int SPAN>
+__device__ void write_tables(const TablesArgs &a, const Prefix &p, int token_ctas) {
     const int P = a.page_size, B = a.batch;
-    const int64_t step = int64_t(gridDim.x) * blockDim.x;
-    const int64_t first = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    const int cta = blockIdx.x, others = gridDim.x - token_ctas;
+    if (cta < token_ctas) {
+        const int64_t step = int64_t(token_ctas) * kThreads * SPAN;
+        for (int64_t i = (int64_t(cta) * kThreads + threadIdx.x) * SPAN; i < a.max_tokens; i += step)
+            write_tokens<SPAN>(a, p, i);
+        return;
+    }
+    const int64_t first = int64_t(cta - token_ctas) * kThreads + threadIdx.x, step = int64_t(others) * kThreads;
     for (int64_t b = first; b < B; b += step) {
         const Request r(a, int(b));
         const bool ok = admitted(a, p, r, int(b));
@@ -160,27 +225,13 @@ __device__ void write_tables(const TablesArgs &a, const Prefix &p) {
         if (r.valid && r.add > 0 && !ok) raise_error(a.flags, kErrCapacity);
     }
     if (first == 0) a.cu_new[B] = min(p.tok[B], a.max_tokens);
-    for (int64_t i = first; i < a.max_tokens; i += step) {
-        int slot = -1, pos = -1;
-        const int b = find(p.tok, B, int(i));
-        if (b < B) {
-            const Request r(a, b);
-            if (admitted(a, p, r, b)) {
-                pos = r.old + int(i) - p.tok[b];
-                const int id = page_of(a, p, r, b, pos / P);
-                if (id >= 0) slot = id * P + pos % P;
-            }
-        }
-        a.slot_map[i] = slot;
-        if (a.positions) a.positions[i] = pos;
-    }
     for (int64_t e = first; e < a.max_touched; e += step) {
         int id = -1, valid = 0;
         const int b = find(p.touch, B, int(e));
         if (b < B) {
             const Request r(a, b);
             if (admitted(a, p, r, b)) {
-                const int j = r.old / P + int(e) - p.touch[b];
+                const int j = (r.old >> page_shift(a)) + int(e) - p.touch[b];
                 id = page_of(a, p, r, b, j);
                 if (j >= r.have) a.page_table[int64_t(b) * a.max_pages + j] = id;
                 if (id >= 0) valid = min(P, r.old + r.add - j * P);
@@ -188,7 +239,7 @@ __device__ void write_tables(const TablesArgs &a, const Prefix &p) {
         }
         if (a.touched_ids) a.touched_ids[e] = id, a.touched_valid[e] = valid;
     }
-    if (a.counts && blockIdx.x == 0) {
+    if (a.counts && cta == gridDim.x - 1) {
         Need mine = {0, 0, 0};
         int64_t refused = 0;
         for (int b = threadIdx.x; b < B; b += kThreads) {
@@ -208,16 +259,17 @@ __device__ void write_tables(const TablesArgs &a, const Prefix &p) {
             a.counts[1] = int32_t(total.need), a.counts[2] = int32_t(total.touch), a.counts[3] = int32_t(total.tok);
         }
     }
-    __threadfence();
 }
 
-__global__ void __launch_bounds__(kThreads) tables_kernel(TablesArgs a) {
+template <int SPAN>
+__global__ void __launch_bounds__(kThreads) tables_kernel(TablesArgs a, int token_ctas) {
     __shared__ int32_t s[3][kScanRequests + 1];
     pdl_wait();
     const Prefix p{s[0], s[1], s[2]};
-    scan_requests(a, 0, a.batch, 0, Need{0, 0, 0}, p);
+    scan_requests(a, 0, a.batch, Need{0, 0, 0}, p);
     __syncthreads();
-    write_tables(a, p);
+    write_tables<SPAN>(a, p, token_ctas);
+    __threadfence();
 }
 
 __global__ void __launch_bounds__(kThreads) tables_scan_kernel(TablesArgs a, Prefix p) {
@@ -226,27 +278,38 @@ __global__ void __launch_bounds__(kThreads) tables_scan_kernel(TablesArgs a, Pre
     Need mine = {0, 0, 0}, base;
     for (int b = threadIdx.x; b < r0; b += kThreads) mine += Request(a, b).need(a);
     block_scan(mine, Need{0, 0, 0}, &base);
-    scan_requests(a, r0, r1, 0, base, p);
+    scan_requests(a, r0, r1, base, p);
     __threadfence();
 }
 
-__global__ void __launch_bounds__(kThreads) tables_write_kernel(TablesArgs a, Prefix p) {
+template <int SPAN>
+__global__ void __launch_bounds__(kThreads) tables_write_kernel(TablesArgs a, Prefix p, int token_ctas) {
     pdl_wait();
-    write_tables(a, p);
+    write_tables<SPAN>(a, p, token_ctas);
+    __threadfence();
 }
 
 }  // namespace
 
 cudaError_t launch_extend_tables(const TablesArgs &a, int32_t *scratch, int num_sms, cudaStream_t stream) {
-    const int64_t items = int64_t(a.max_tokens) + a.max_touched + a.batch;
-    int64_t ctas = (items + kThreads * 2 - 1) / (kThreads * 2);
-    ctas = ctas < 1 ? 1 : (ctas > 4 * num_sms ? 4 * num_sms : ctas);
-    if (a.batch <= kScanRequests) return launch_pdl(tables_kernel, dim3(unsigned(ctas)), dim3(kThreads), 0, stream, a);
+    // One token a thread while that fits one CTA an SM (a step's latency is one chain of loads then), else four
+    // neighbouring ones, which mostly share their request and page, up to two CTAs an SM.
+    const bool few = (int64_t(a.max_tokens) + kThreads - 1) / kThreads <= num_sms;
+    const int64_t per_cta = few ? kThreads : 4 * kThreads;
+    int64_t tok = (int64_t(a.max_tokens) + per_cta - 1) / per_cta;
+    if (tok > 2 * num_sms) tok = 2 * num_sms;
+    int64_t rest = (int64_t(a.max_touched > a.batch ? a.max_touched : a.batch) + kThreads - 1) / kThreads;
+    if (rest > num_sms) rest = num_sms;
+    const dim3 grid(unsigned(tok + rest)), block(kThreads);
+    if (a.batch <= kScanRequests)
+        return few ? launch_pdl(tables_kernel<1>, grid, block, 0, stream, a, int(tok))
+                   : launch_pdl(tables_kernel<4>, grid, block, 0, stream, a, int(tok));
     const Prefix p{scratch, scratch + (a.batch + 1), scratch + 2 * (a.batch + 1)};
     const cudaError_t e = launch_pdl(tables_scan_kernel, dim3(unsigned((a.batch + kScanRequests - 1) / kScanRequests)),
-                                     dim3(kThreads), 0, stream, a, p);
+                                     block, 0, stream, a, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(tables_write_kernel, dim3(unsigned(ctas)), dim3(kThreads), 0, stream, a, p);
+    return few ? launch_pdl(tables_write_kernel<1>, grid, block, 0, stream, a, p, int(tok))
+               : launch_pdl(tables_write_kernel<4>, grid, block, 0, stream, a, p, int(tok));
 }
 
 }  // namespace qskv

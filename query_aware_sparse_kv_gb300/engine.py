@@ -206,6 +206,132 @@ class PagedDecoder:
             raise B.QskvError(st, B.last_error_message())
 
 
+class QuantizedPagedDecoder:
+    """A decode batch over a KV cache held in 4 bits, from lengths to outputs.
+
+    Owns the pool (codes with a bf16 scale and minimum per group of
+    ``group_size`` dims), its page metadata, the page table and the free
+    pages.  A step is: ``extend`` (tables and slots of the new tokens),
+    ``append`` (their keys and values quantised into the pool, the touched
+    pages' metadata rebuilt), ``select`` (with top_k: the pages each query
+    attends to) and ``decode``; ``step`` does all of it.  Row lengths are
+    also kept on the host, so a step never waits for the GPU.
+
+    batch       rows (requests); a row of length 0 is free
+    max_pages   pages a row may hold
+    max_tokens  new tokens a step may bring, all rows together
+    top_k       pages kept per (row, KV head); None = all
+    """
+
+    def __init__(self, batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int, max_pages: int,
+                 num_pool_pages: int, group_size: int = 64, top_k: Optional[int] = None, max_tokens: int = 8192,
+                 sm_scale: float = 0.0, device="cuda"):
+        self.shape = B.make_shape(batch, num_q_heads, num_kv_heads, head_dim, page_size, max_pages, num_pool_pages)
+        self.group_size, self.top_k, self.sm_scale, self.max_tokens = group_size, top_k, sm_scale, max_tokens
+        block = B.kvq_block_bytes(self.shape, group_size)
+        i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device=device)  # noqa: E731
+        self.pool = torch.zeros((num_pool_pages, num_kv_heads, block), dtype=torch.uint8, device=device)
+        self.page_table = torch.full((batch, max_pages), -1, dtype=torch.int32, device=device)
+        self.seq_lens, self._lens_out = i32(batch), i32(batch)
+        self.free_pages = torch.arange(num_pool_pages, dtype=torch.int32, device=device)
+        self.cu_new, self.slot_map, self.positions = i32(batch + 1), i32(max_tokens), i32(max_tokens)
+        touched = min(max_tokens, max_tokens // page_size + 2 * batch)
+        self.touched_ids, self.touched_valid = i32(touched), i32(touched)
+        with torch.cuda.device(self.pool.device):
+            size = max(B.kvq_workspace_size(self.shape), B.tables_workspace_size(self.shape),
+                       B.workspace_size(self.shape) if top_k is not None else 0)
+        self.workspace = torch.zeros(size, dtype=torch.uint8, device=device)
+        if top_k is not None:
+            self.meta = torch.zeros((num_pool_pages, num_kv_heads, 2, head_dim), dtype=torch.bfloat16, device=device)
+            self.selected, self.n_selected = i32(batch, num_kv_heads, top_k), i32(batch, num_kv_heads)
+        self.out = torch.zeros((batch, num_q_heads, head_dim), dtype=torch.float32, device=device)
+        self.lse = torch.zeros((batch, num_q_heads), dtype=torch.float32, device=device)
+        self.lengths = [0] * batch  # as of the last extend
+
+    def _pages(self, tokens: int) -> int:
+        return -(-tokens // self.shape.page_size)
+
+    def extend(self, new_lens, stream=None):
+        """Make room for new_lens[b] more tokens of every row b: page table,
+        ``slot_map`` and ``positions`` of the new tokens (rows in order),
+        ``touched_ids`` / ``touched_valid`` and the new ``seq_lens``.  Raises
+        ValueError, changing nothing, if they do not fit."""
+        new = [int(n) for n in new_lens]
+        if len(new) != self.shape.batch or min(new) < 0:
+            raise ValueError(f"new_lens must be {self.shape.batch} counts >= 0")
+        if sum(new) > self.max_tokens:
+            raise ValueError(f"{sum(new)} new tokens, at most {self.max_tokens} a step")
+        grown = [a + n for a, n in zip(self.lengths, new)]
+        for b, n in enumerate(grown):
+            if n > self.shape.max_pages * self.shape.page_size:
+                raise ValueError(f"row {b} would hold {n} tokens, more than its {self.shape.max_pages} pages")
+        need = sum(self._pages(n) - self._pages(a) for a, n in zip(self.lengths, grown))
+        if need > self.free_pages.numel():
+            raise ValueError(f"{need} pages needed, {self.free_pages.numel()} free")
+        added = torch.tensor(new, dtype=torch.int32).to(self.pool.device, non_blocking=True)
+        B.extend_tables(self.seq_lens, added, self.free_pages, self.page_table, self._lens_out, self.cu_new,
+                        self.slot_map, self.shape, self.workspace, positions=self.positions,
+                        touched_ids=self.touched_ids, touched_valid=self.touched_valid, stream=stream)
+        self.seq_lens, self._lens_out = self._lens_out, self.seq_lens
+        self.free_pages = self.free_pages[need:]
+        self.lengths = grown
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, stream=None):
+        """Store the keys and values [n][Hkv][d] of the tokens of the last
+        ``extend`` (rows in order) and, with top_k, rebuild the metadata of
+        the pages they fall into."""
+        B.kvq_append(k, v, self.slot_map[:k.shape[0]], self.pool, self.shape, self.group_size, self.workspace, stream)
+        if self.top_k is not None:
+            B.kvq_meta_build(self.pool, self.touched_ids, self.touched_valid, self.meta, self.shape, self.group_size,
+                             self.workspace, stream)
+
+    def select(self, q: torch.Tensor, stream=None):
+        """The top_k pages of every (row, KV head) by their score bound."""
+        B.page_select(q, self.meta, self.page_table, self.seq_lens, self.top_k, self.selected, self.n_selected,
+                      self.shape, self.workspace, None, stream)
+
+    def decode(self, q: torch.Tensor, out=None, lse=None, stream=None):
+        """Attention of q [batch][Hq][d] over the selected (or all) pages,
+        into ``out`` / ``lse``."""
+        sparse = self.top_k is not None
+        B.kvq_paged_decode(q, self.pool, self.page_table, self.seq_lens, self.out if out is None else out, self.shape,
+                           self.group_size, self.workspace, selected=self.selected if sparse else None,
+                           n_selected=self.n_selected if sparse else None, top_k=self.top_k or 0,
+                           lse=self.lse if lse is None else lse, sm_scale=self.sm_scale, stream=stream)
+
+    def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, new_lens=None, stream=None):
+        """One step: the rows' new tokens (one each by default) stored, then
+        the queries' attention over what the rows hold with them."""
+        self.extend([1] * self.shape.batch if new_lens is None else new_lens, stream)
+        self.append(k, v, stream)
+        if self.top_k is not None:
+            self.select(q, stream)
+        self.decode(q, stream=stream)
+
+    def gather(self, row: int, dtype=torch.float32, stream=None):
+        """The cached keys and values [length][Hkv][d] of a row."""
+        P, n = self.shape.page_size, self.lengths[row]
+        t = torch.arange(n, device=self.pool.device)
+        slots = (self.page_table[row].long()[t // P] * P + t % P).to(torch.int32)
+        k, v = (torch.empty((n, self.shape.num_kv_heads, self.shape.head_dim), dtype=dtype, device=self.pool.device)
+                for _ in range(2))
+        B.kvq_gather(self.pool, slots, k, v, self.shape, self.group_size, self.workspace, stream)
+        return k, v
+
+    def release(self, row: int):
+        """Give a row's pages back; its length is 0 afterwards."""
+        n = self._pages(self.lengths[row])
+        self.free_pages = torch.cat([self.free_pages, self.page_table[row, :n]])
+        self.seq_lens[row] = 0
+        self.lengths[row] = 0
+
+    def check(self, stream=None):
+        """Raise if the device flagged an out-of-range index or a timeout."""
+        st = B.get_error(self.workspace, stream)
+        if st != 0:
+            raise B.QskvError(st, B.last_error_message())
+
+
 def from_inputs(inputs: dict, device="cuda", top_k="spec", prefix_pages: int = 0,
                 scorer: str = "bound", approx_epsilon: Optional[float] = None, approx_seed: int = 0) -> PagedDecoder:
     """A PagedDecoder over a workloads.make_inputs() batch copied to `device`."""

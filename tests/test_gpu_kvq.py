@@ -481,7 +481,7 @@ def _requests(seed, B, P, mp, most):
 
 @pytest.mark.parametrize("P", [16, 32])
 @pytest.mark.parametrize("B,mp,most", [(1, 1, 16), (1, 40, 600), (5, 7, 100), (300, 20, 40), (2048, 6, 30),
-                                       (2049, 6, 30), (5000, 4, 20)])
+                                       (2049, 6, 30), (4032, 4, 20), (4033, 4, 20), (5000, 4, 20)])
 def test_tables(P, B, mp, most):
     seq, new, free, table, N = _requests(B + P, B, P, mp, most)
     T = max(1, sum(new))
@@ -489,7 +489,7 @@ def test_tables(P, B, mp, most):
     assert _run_tables(seq, new, free, table, P, N, T + 33)[0] == 0  # padded places
 
 
-@pytest.mark.parametrize("B", [40, 2100])
+@pytest.mark.parametrize("B", [40, 2100, 4100])
 def test_tables_refuse_in_order(B):
     seq, new, free, table, N = _requests(B, B, 16, 8, 60)
     err, want = _run_tables(seq, new, free[:len(free) // 2], table, 16, N, sum(new))  # pages run out
@@ -580,3 +580,47 @@ def test_a_serving_run_together():
                     continue
                 tol, _ = R.attend_bounds(qs, kf[2][rows], kf[1][rows], vf[2][rows], vf[1][rows], d ** -0.5, len(rows))
                 assert float((got - o).abs().max()) <= tol
+
+
+def test_quantized_decoder_runs_a_batch():
+    """The engine's class over prefill, steps, a row given back and taken again: every output against the reference."""
+    g = torch.Generator().manual_seed(7)
+    B, hq, hkv, d, P, gs = 3, 8, 2, 128, 16, 64
+    for top_k in (None, 2):
+        dec = qskv.QuantizedPagedDecoder(B, hq, hkv, d, P, max_pages=9, num_pool_pages=20, group_size=gs, top_k=top_k,
+                                         max_tokens=400)
+        kept = [[torch.zeros((0, hkv, d))] * 2 for _ in range(B)]
+        for new in ([40, 0, 90], [1, 1, 1], [1, 17, 0], None, [0, 1, 1]):
+            if new is None:
+                dec.release(0)
+                kept[0] = [torch.zeros((0, hkv, d))] * 2
+                continue
+            n = sum(new)
+            k, v = (torch.randn((n, hkv, d), generator=g).bfloat16() for _ in range(2))
+            q = torch.randn((B, hq, d), generator=g).bfloat16()
+            dec.step(q.cuda(), k.cuda(), v.cuda(), new)
+            dec.check()
+            at = 0
+            for b in range(B):
+                kept[b] = [torch.cat([x, y[at:at + new[b]].float()]) for x, y in zip(kept[b], (k, v))]
+                at += new[b]
+                n_b = -(-len(kept[b][0]) // P)
+                for h in range(hkv):
+                    kf, vf = (R.quantise(x[:, h], gs) for x in kept[b])
+                    pages = list(range(n_b)) if top_k is None else dec.selected[b, h, :min(top_k, n_b)].tolist()
+                    rows = [t for j in pages for t in range(j * P, min(len(kept[b][0]), (j + 1) * P))]
+                    qs = q[b, h * 4:h * 4 + 4]
+                    o, l = R.attend(qs, R.values(*kf)[rows], R.values(*vf)[rows], d ** -0.5)
+                    if not rows:
+                        assert bool((dec.out[b] == 0).all()) and bool(torch.isinf(dec.lse[b]).all())
+                        continue
+                    tol, _ = R.attend_bounds(qs, kf[2][rows], kf[1][rows], vf[2][rows], vf[1][rows], d ** -0.5, len(rows))
+                    assert float((dec.out[b, h * 4:h * 4 + 4].cpu().double() - o).abs().max()) <= tol
+        assert dec.lengths == [0, 19, 92]
+        with pytest.raises(ValueError, match="14 pages needed, 12 free"):  # 2 + 6 of 20 are held
+            dec.extend([144, 80, 0])
+        with pytest.raises(ValueError, match="401 new tokens"):
+            dec.extend([300, 101, 0])
+        with pytest.raises(ValueError, match="row 2"):
+            dec.extend([0, 0, 53])
+        assert dec.lengths == [0, 19, 92]

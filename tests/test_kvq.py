@@ -136,10 +136,10 @@ def test_extend_tables_refusals(lib, mem):
                dict(E=3)):  # min(8 tokens, 8 / 16 + 2 * 2) = 4 pages may be touched
         assert call(**kw) == INVALID, kw
     assert call(shape=ctypes.byref(qskv.make_shape(2, 8, 2, 128, 24, 8, 16))) == UNSUPPORTED
-    small = qskv.make_shape(2048, 8, 2, 128, 16, 8, 16)
-    large = qskv.make_shape(2049, 8, 2, 128, 16, 8, 16)
+    small = qskv.make_shape(4032, 8, 2, 128, 16, 8, 16)
+    large = qskv.make_shape(4033, 8, 2, 128, 16, 8, 16)
     assert lib.qskv_tables_workspace_size(ctypes.byref(small)) == 256
-    assert lib.qskv_tables_workspace_size(ctypes.byref(large)) >= 256 + 3 * 2050 * 4
+    assert lib.qskv_tables_workspace_size(ctypes.byref(large)) >= 256 + 3 * 4034 * 4
     assert lib.qskv_tables_workspace_size(ctypes.byref(qskv.make_shape(0, 8, 2, 128, 16, 8, 16))) == 0
 
 
