@@ -54,7 +54,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kEntries = 512;      // entries of the unit prefix held in shared memory
 constexpr int kFill = 16;          // units a warp describes at once (a multiple of the units a stage)
-constexpr int kRowModePages = 64, kRowCtas = 16, kRowUnits = 32;
+constexpr int kRowModePages = 64, kRowCtas = 16, kRowUnits = 32, kWarpUnits = 12, kWarpUnitsMany = 32;
 constexpr int kMaxRing = 8;        // stages a warp
 constexpr float kNoRef = -1e30f;   // M before the first token
 // Largest weight, and largest weight times value scale, in the references' units.
@@ -193,6 +193,15 @@ __device__ __forceinline__ Unit unit_of(const KvqDecodeArgs &a, int row, int slo
     return r;
 }
 
+// The unit of row `row` at place `slot` of the `row_units` places a row has at
+// most (rows to warps): empty past the row's end.
+__device__ __forceinline__ Unit place_of(const KvqDecodeArgs &a, int row, int slot, int row_units, uint32_t block_bytes) {
+    if (slot < units_of(a, a.selected ? row : row / a.num_kv_heads)) return unit_of(a, row, slot, row_units, block_bytes);
+    Unit r;
+    r.src = nullptr, r.row_valid = row << 6, r.slot = slot, r.count = row_units;
+    return r;
+}
+
 // The unit with global index u (even split).
 __device__ __forceinline__ Unit unit_at(const KvqDecodeArgs &a, const Shared &s, int entries, int per, int u,
                                         uint32_t block_bytes) {
@@ -219,7 +228,8 @@ struct RowState {
     static constexpr int NW = D / 32;     // 32-dim chunks of a row; code words a lane holds of a token's key
     static constexpr int GW = NW / NG;    // chunks a group
     static constexpr int NH = HC / 4;     // heads a lane
-    uint32_t qh[NW][4], ql[HC == 8 ? NW : 1][4];
+    uint32_t qh[NW][4];
+    uint4 *ql;  // HC = 8: the lo halves' fragments, in the warp's shared memory ([NW][32 lanes]): registers are short
     float qa[NH], qb[NH][NG];
     float m[NH], l[NH], sg[NH], pm[NH][NG];
     bool q_lo;  // HC = 8: the queries have lo halves (fp32 ones; bf16 fits fp16 as it is, half the products)
@@ -281,7 +291,7 @@ struct RowState {
                     qh[i][r] = g & 1 ? lo : hi;
                 } else {
                     qh[i][r] = hi;
-                    ql[i][r] = lo;
+                    if (q_lo) reinterpret_cast<uint32_t *>(ql + i * 32 + lane)[r] = lo;  // read by this lane alone
                 }
             }
 #pragma unroll
@@ -368,11 +378,12 @@ struct RowState {
 #pragma unroll
                     for (int i = 0; i < GW; i++) {
                         const uint32_t a = ka[j * GW + i], b = kb[j * GW + i], a8 = a >> 8, b8 = b >> 8;
+                        const uint4 q = ql[(j * GW + i) * 32 + lane];
                         if (i == 0)
-                            mma_f16_first(c1, a & lo, b & lo, a & hi, b & hi, ql[j * GW + i][0], ql[j * GW + i][1]);
+                            mma_f16_first(c1, a & lo, b & lo, a & hi, b & hi, q.x, q.y);
                         else
-                            mma_f16(c1, a & lo, b & lo, a & hi, b & hi, ql[j * GW + i][0], ql[j * GW + i][1]);
-                        mma_f16(c1, a8 & lo, b8 & lo, a8 & hi, b8 & hi, ql[j * GW + i][2], ql[j * GW + i][3]);
+                            mma_f16(c1, a & lo, b & lo, a & hi, b & hi, q.x, q.y);
+                        mma_f16(c1, a8 & lo, b8 & lo, a8 & hi, b8 & hi, q.z, q.w);
                     }
 #pragma unroll
                     for (int k = 0; k < 4; k++) c0[k] = fmaf(c1[k], lo_unit, c0[k]);
@@ -567,10 +578,16 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
 
     // ---- this warp's units [u0, u1): of its CTA's row, or of all rows in order
     int u0, u1, cta_begin, cta_end;
-    int entries = 0, per = 1, upc;
+    int entries = 0, per = 1, upc = 0;
+    const int warp_index = blockIdx.x * kWarps + warp, all_warps = gridDim.x * kWarps;
     const int row0 = a.row_ctas ? blockIdx.x / a.row_ctas : 0;
     int count0 = 0;
-    if (a.row_ctas) {
+    if (a.warp_units) {  // rows to warps in turn: this warp's rows, warp_units places each
+        const int rows = a.batch * a.num_kv_heads;
+        u0 = 0, u1 = warp_index < rows ? (rows - warp_index + all_warps - 1) / all_warps * a.warp_units : 0;
+        cta_begin = cta_end = 0;
+        if (!a.selected) pdl_wait();
+    } else if (a.row_ctas) {
         count0 = units_of(a, a.selected ? row0 : row0 / a.num_kv_heads);
         upc = (count0 + a.row_ctas - 1) / a.row_ctas;
         const int part = blockIdx.x - row0 * a.row_ctas;
@@ -618,7 +635,6 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
             before += n;
         }
         __syncthreads();
-        const int all_warps = gridDim.x * kWarps;
         const int upw = max(int((uint32_t(total) + all_warps - 1) / all_warps), 1);
         upc = upw * kWarps;
         const int64_t c0 = int64_t(blockIdx.x) * upc;
@@ -646,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
     // ---- the warp's pipeline: stage k holds units kU .. kU + U - 1 of its range
     const int n = u1 - u0, stages = (n + U - 1) / U;
     int put = 0, got = 0, parity = 0;
+    const uint64_t policy = l2_evict_first_policy();
     uint32_t plain = 0;  // bit per ring stage: all its units are whole pages of the row before them
     auto issue = [&](int k) {
         if (k >= stages) return;
@@ -654,8 +671,10 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
             __syncwarp();
             const int u = u0 + first + lane;
             if (lane < kFill && u < u1)
-                s.desc[warp][(first + lane) % (2 * kFill)] = a.row_ctas ? unit_of(a, row0, u, count0, block_bytes)
-                                                                        : unit_at(a, s, entries, per, u, block_bytes);
+                s.desc[warp][(first + lane) % (2 * kFill)] =
+                    a.warp_units ? place_of(a, warp_index + u / a.warp_units * all_warps, u % a.warp_units, a.warp_units, block_bytes)
+                    : a.row_ctas ? unit_of(a, row0, u, count0, block_bytes)
+                                 : unit_at(a, s, entries, per, u, block_bytes);
             __syncwarp();
         }
         const uint8_t *src = nullptr;
@@ -675,10 +694,16 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
         uint64_t *bar = &s.bar[warp][put];
         if (lane == 0) mbar_arrive_expect_tx(bar, __popc(live) * block_bytes);
         __syncwarp();
-        if (src) bulk_load(ring + (put * U + lane) * block_bytes, src, block_bytes, bar);
+        if (src) {
+            if (a.evict_first)
+                bulk_load_hint(ring + (put * U + lane) * block_bytes, src, block_bytes, bar, policy);
+            else
+                bulk_load(ring + (put * U + lane) * block_bytes, src, block_bytes, bar);
+        }
         if (++put == S) put = 0;
     };
     RowState<D, NG, HC, P> st;
+    st.ql = reinterpret_cast<uint4 *>(ring_mem + kWarps * (S * U * block_bytes)) + warp * (D / 32 * 32);
     int row = -1, row_begin = 0, row_end = 0;
     float *piece_first = a.first_o + (int64_t(blockIdx.x) * kWarps + warp) * (G * D);
     auto close = [&](bool at_end) {
@@ -731,6 +756,7 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
         issue(k + S);
     }
     if (row >= 0) close(true);
+    if (a.warp_units) return;  // every row was one warp's
     __syncthreads();
 
     // ---- pieces of one row within the CTA, in unit order
@@ -876,28 +902,41 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
 // Shared memory a CTA may take beside its static part with two CTAs an SM
 // (228 KB an SM, 1 KB of each CTA's reserved).
 constexpr int kRingBudget = 113 * 1024 - int(sizeof(Shared));
+template <int D, int HC>
+constexpr int kQueryBytes = HC == 8 ? kWarps * D * 16 : 0;  // the lo halves of 8 heads
 
 template <int D, int NG, int HC, int P>
 cudaError_t launch_one(KvqDecodeArgs &a, int num_sms, cudaStream_t stream) {
     // a stage is about 4 KB: with fewer pages its fixed cost shows, with more the ring has too few stages
     constexpr int stage = kWarps * (4096 / (P * D)) * kvq_block_words(D, P, NG) * 4;
-    constexpr int stages = kRingBudget / stage < kMaxRing ? kRingBudget / stage : kMaxRing;
+    constexpr int fit = (kRingBudget - kQueryBytes<D, HC>) / stage, stages = fit < kMaxRing ? fit : kMaxRing;
+    constexpr int bytes = stages * stage + kQueryBytes<D, HC>;
     static_assert(stages >= 2, "the ring needs two stages");
     a.stages = stages;
     const int rows = a.batch * a.num_kv_heads, slots = kvq_decode_ctas(num_sms);
-    const int row_units = a.selected ? a.top_k : a.max_pages;
-    a.row_ctas = 0;
+    const int row_units = a.selected && a.top_k < a.max_pages ? a.top_k : a.max_pages;
+    // Rows of few pages, more of them than CTAs: whole rows to warps, nothing to join (2048 rows of 7 pages: 15.3 us,
+    // 28.7 split evenly; 512 rows of 1 to 32 pages: 28.0 and 19.6, so longer rows only if every warp gets one).  Rows
+    // that fit one wave of CTAs and are cut about alike (selections, short tables): a group of CTAs each, which need
+    // no prefix over the lengths.  Else the even split.
+    const bool whole = rows > slots && (row_units <= kWarpUnits || (row_units <= kWarpUnitsMany && rows >= slots * kWarps));
+    a.row_ctas = 0, a.warp_units = whole ? row_units : 0;
     if (rows <= slots && (a.selected || row_units <= kRowModePages)) {
         const int most = slots / rows, want = (row_units + kRowUnits - 1) / kRowUnits;
         a.row_ctas = want < most ? want : most;
         if (a.row_ctas > kRowCtas) a.row_ctas = kRowCtas;
     }
+    // The pages are read once a call.  Above half of L2 they are marked to leave it first, which keeps queries, tables
+    // and partial outputs in it: 24.8 -> 23.7 us at 71 MB; below, pages that stay serve the next call: 10.1 us at
+    // 19 MB with the plain policy, 11.2 with the other.
+    a.evict_first = int64_t(rows) * row_units * (stage / kWarps / (4096 / (P * D))) * 2 > l2_cache_bytes();
     const int64_t even = (int64_t(rows) * row_units + kWarps - 1) / kWarps;
-    const unsigned grid = a.row_ctas ? unsigned(rows * a.row_ctas) : unsigned(even < slots ? even : slots);
+    const unsigned grid = a.warp_units ? unsigned(slots < (rows + kWarps - 1) / kWarps ? slots : (rows + kWarps - 1) / kWarps)
+                          : a.row_ctas ? unsigned(rows * a.row_ctas) : unsigned(even < slots ? even : slots);
     const cudaError_t e = cudaFuncSetAttribute(kvq_decode_kernel<D, NG, HC, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               stages * stage);
+                                               bytes);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kvq_decode_kernel<D, NG, HC, P>, dim3(grid), dim3(kThreads), stages * stage, stream, a);
+    return launch_pdl(kvq_decode_kernel<D, NG, HC, P>, dim3(grid), dim3(kThreads), bytes, stream, a);
 }
 
 template <int P>

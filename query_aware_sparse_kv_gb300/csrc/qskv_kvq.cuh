@@ -62,6 +62,15 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  : "memory");
 }
 
+__device__ __forceinline__ void bulk_load_hint(void *dst, const void *src, uint32_t bytes, uint64_t *bar,
+                                               uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
 struct KvqStoreArgs {
     const void *k, *v;         // append: [n][Hkv][d], rows k_stride / v_stride elements apart
     void *k_out, *v_out;       // gather: [n][Hkv][d]
@@ -96,6 +105,8 @@ struct KvqDecodeArgs {
     float *first_o;                        // [CTAs][warps][G][d]: a warp's piece of a row that ends in its range
     int32_t stages;                        // ring stages a warp (set by the launcher)
     int32_t row_ctas;                      // CTAs a row; 0: even split of all rows' units (set by the launcher)
+    int32_t warp_units;                    // places a row where rows go to warps whole, 0 elsewhere (set by the launcher)
+    int32_t evict_first;                   // 1: the pages are read with L2's evict-first policy (set by the launcher)
 };
 
 struct TablesArgs {
