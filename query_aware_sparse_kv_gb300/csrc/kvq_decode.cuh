@@ -316,9 +316,9 @@ struct RowState {
             for (int r = 0; r < 4; r++) o[c][0][r] = o[c][1][r] = 0.f;
     }
 
-    // One 16-token tile: `tile` of the block at `st`, of which the first nv
-    // (1..16) tokens count.
-    __device__ __forceinline__ void tile(const uint8_t *st, int tile, int nv) {
+    // Logits of one 16-token tile (`tile` of the block at `st`) in x, and its value params in va, vb.
+    __device__ __forceinline__ void logits(const uint8_t *st, int tile, float (&x)[2][NH], uint32_t (&va)[NG],
+                                           uint32_t (&vb)[NG]) const {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         const int ta = tile * 16 + g;
         // ---- keys: codes of tokens g and g + 8, logits
@@ -333,8 +333,7 @@ struct RowState {
             ka[0] = x.x, ka[1] = x.y, kb[0] = y.x, kb[1] = y.y;
         }
         const uint32_t *par = reinterpret_cast<const uint32_t *>(st + P * D) + ta;
-        uint32_t va[NG], vb[NG];
-        float x[2][NH], xm[2][NH];
+        float xm[2][NH];
 #pragma unroll
         for (int h = 0; h < NH; h++) x[0][h] = x[1][h] = xm[0][h] = xm[1][h] = 0.f;
 #pragma unroll
@@ -401,48 +400,67 @@ struct RowState {
         }
 #pragma unroll
         for (int h = 0; h < NH; h++) x[0][h] = fmaf(qa[h], x[0][h], xm[0][h]), x[1][h] = fmaf(qa[h], x[1][h], xm[1][h]);
-        if (nv < 16) {  // places past the end: no weight, and nothing of their params
+    }
+
+    // NT tiles, tile i of them number tile0 + i of the blocks from st on.  The first nv (1..16) tokens of the last one
+    // count, all of the others.
+    template <int NT>
+    __device__ __forceinline__ void tiles(const uint8_t *st, int tile0, int nv) {
+        constexpr int PT = P / 16;
+        constexpr uint32_t block_bytes = kvq_block_words(D, P, NG) * 4;
+        const int lane = threadIdx.x & 31, g = lane >> 2;
+        uint32_t va[NT][NG], vb[NT][NG];
+        float x[NT][2][NH];
+#pragma unroll
+        for (int i = 0; i < NT; i++) logits(st + (tile0 + i) / PT * block_bytes, (tile0 + i) % PT, x[i], va[i], vb[i]);
+        if (NT == 1 && nv < 16) {  // places past the end: no weight, and nothing of their params
             const bool off_a = g >= nv, off_b = g + 8 >= nv;
 #pragma unroll
             for (int h = 0; h < NH; h++) {
-                if (off_a) x[0][h] = -INFINITY;
-                if (off_b) x[1][h] = -INFINITY;
+                if (off_a) x[0][0][h] = -INFINITY;
+                if (off_b) x[0][1][h] = -INFINITY;
             }
 #pragma unroll
             for (int j = 0; j < NG; j++) {
-                if (off_a) va[j] = 0;
-                if (off_b) vb[j] = 0;
+                if (off_a) va[0][j] = 0;
+                if (off_b) vb[0][j] = 0;
             }
         }
         // ---- weights
-        float p[2][NH], w[2][NH][NG];
+        float p[NT][2][NH], w[NT][2][NH][NG];
         float most_p = 0.f, most_w = 0.f;
-        bool calm = true;
 #pragma unroll
-        for (int h = 0; h < NH; h++) {
-            p[0][h] = ex2(x[0][h] - m[h]), p[1][h] = ex2(x[1][h] - m[h]);
-            most_p = fmaxf(most_p, fmaxf(p[0][h], p[1][h]));
-            const float ps0 = p[0][h] * sg[h], ps1 = p[1][h] * sg[h];
-#pragma unroll
-            for (int j = 0; j < NG; j++) {
-                w[0][h][j] = ps0 * bf16_lo_to_float(va[j]);
-                w[1][h][j] = ps1 * bf16_lo_to_float(vb[j]);
-                most_w = fmaxf(most_w, fmaxf(w[0][h][j], w[1][h][j]));
-            }
-        }
-        calm = most_p <= kTopP && most_w <= kTopW;
-        if (!__all_sync(0xffffffffu, calm)) {
+        for (int i = 0; i < NT; i++)
 #pragma unroll
             for (int h = 0; h < NH; h++) {
-                const float mn = fmaxf(m[h], max_over_tokens(fmaxf(x[0][h], x[1][h])));
+                p[i][0][h] = ex2(x[i][0][h] - m[h]), p[i][1][h] = ex2(x[i][1][h] - m[h]);
+                most_p = fmaxf(most_p, fmaxf(p[i][0][h], p[i][1][h]));
+                const float ps0 = p[i][0][h] * sg[h], ps1 = p[i][1][h] * sg[h];
+#pragma unroll
+                for (int j = 0; j < NG; j++) {
+                    w[i][0][h][j] = ps0 * bf16_lo_to_float(va[i][j]);
+                    w[i][1][h][j] = ps1 * bf16_lo_to_float(vb[i][j]);
+                    most_w = fmaxf(most_w, fmaxf(w[i][0][h][j], w[i][1][h][j]));
+                }
+            }
+        if (!__all_sync(0xffffffffu, most_p <= kTopP && most_w <= kTopW)) {
+#pragma unroll
+            for (int h = 0; h < NH; h++) {
+                float mn = m[h];
+#pragma unroll
+                for (int i = 0; i < NT; i++) mn = fmaxf(mn, fmaxf(x[i][0][h], x[i][1][h]));
+                mn = max_over_tokens(mn);
                 const float f = ex2(m[h] - mn);
-                p[0][h] = ex2(x[0][h] - mn), p[1][h] = ex2(x[1][h] - mn);
                 float top = 0.f;
 #pragma unroll
-                for (int j = 0; j < NG; j++)
-                    top = fmaxf(top, fmaxf(p[0][h] * bf16_lo_to_float(va[j]), p[1][h] * bf16_lo_to_float(vb[j])));
+                for (int i = 0; i < NT; i++) {
+                    p[i][0][h] = ex2(x[i][0][h] - mn), p[i][1][h] = ex2(x[i][1][h] - mn);
+#pragma unroll
+                    for (int j = 0; j < NG; j++)
+                        top = fmaxf(top, fmaxf(p[i][0][h] * bf16_lo_to_float(va[i][j]), p[i][1][h] * bf16_lo_to_float(vb[i][j])));
+                }
                 top = max_over_tokens(top);
-                // sg such that the tile's largest p s sg lies in [2^8, 2^9); what is summed already may grow by 2^30
+                // sg such that the tiles' largest p s sg lies in [2^8, 2^9); what is summed already may grow by 2^30
                 float s = sg[h];
                 if (top >= 7.888609052210118e-31f) {  // 2^-100
                     s = __uint_as_float((262u << 23) - (__float_as_uint(top) & 0x7f800000u));
@@ -453,8 +471,11 @@ struct RowState {
 #pragma unroll
                 for (int j = 0; j < NG; j++) {
                     pm[h][j] *= f;
-                    w[0][h][j] = p[0][h] * (bf16_lo_to_float(va[j]) * s);
-                    w[1][h][j] = p[1][h] * (bf16_lo_to_float(vb[j]) * s);
+#pragma unroll
+                    for (int i = 0; i < NT; i++) {
+                        w[i][0][h][j] = p[i][0][h] * (bf16_lo_to_float(va[i][j]) * s);
+                        w[i][1][h][j] = p[i][1][h] * (bf16_lo_to_float(vb[i][j]) * s);
+                    }
                 }
 #pragma unroll
                 for (int c = 0; c < NW; c++)
@@ -466,15 +487,24 @@ struct RowState {
         // the value codes enter their product less 8 (sums of signed numbers: the tensor cores cut what they add
         // towards zero, which on 0..15 is a bias), so pm takes the middle m + 8 s of each group
 #pragma unroll
-        for (int h = 0; h < NH; h++) l[h] += p[0][h] + p[1][h];
+        for (int i = 0; i < NT; i++) {
 #pragma unroll
-        for (int j = 0; j < NG; j++) {
-            const float mida = fmaf(8.f, bf16_lo_to_float(va[j]), bf16_hi_to_float(va[j]));
-            const float midb = fmaf(8.f, bf16_lo_to_float(vb[j]), bf16_hi_to_float(vb[j]));
+            for (int h = 0; h < NH; h++) l[h] += p[i][0][h] + p[i][1][h];
 #pragma unroll
-            for (int h = 0; h < NH; h++) pm[h][j] = fmaf(p[1][h], midb, fmaf(p[0][h], mida, pm[h][j]));
+            for (int j = 0; j < NG; j++) {
+                const float mida = fmaf(8.f, bf16_lo_to_float(va[i][j]), bf16_hi_to_float(va[i][j]));
+                const float midb = fmaf(8.f, bf16_lo_to_float(vb[i][j]), bf16_hi_to_float(vb[i][j]));
+#pragma unroll
+                for (int h = 0; h < NH; h++) pm[h][j] = fmaf(p[i][1][h], midb, fmaf(p[i][0][h], mida, pm[h][j]));
+            }
         }
-        // ---- values
+#pragma unroll
+        for (int i = 0; i < NT; i++) values(st + (tile0 + i) / PT * block_bytes, (tile0 + i) % PT, w[i]);
+    }
+
+    // The outputs' sums take one tile's values with weights w.
+    __device__ __forceinline__ void values(const uint8_t *st, int tile, const float (&w)[2][NH][NG]) {
+        const int lane = threadIdx.x & 31;
         const int mat = lane >> 3, r = lane & 7;
         const int token = tile * 16 + (mat & 1) * 8 + r;
         const int sw = D == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
@@ -735,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
         const uint8_t *stage = ring + got * (U * block_bytes);
         if (HC == 4 && same) {
 #pragma unroll
-            for (int t = 0; t < kTiles; t++) st.tile(stage + t / kPageTiles * block_bytes, t % kPageTiles, 16);
+            for (int t = 0; t < kTiles; t += 2) st.template tiles<2>(stage, t, 16);
         } else {
 #pragma unroll 1
             for (int t = 0; t < kTiles; t++) {
@@ -748,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
                     nv = min((u.row_valid & 63) - t % kPageTiles * 16, 16);
                     if (!u.src || nv <= 0) continue;
                 }
-                st.tile(stage + t / kPageTiles * block_bytes, t % kPageTiles, nv);
+                st.template tiles<1>(stage, t, nv);
             }
         }
         if (++got == S) got = 0, parity ^= 1;
