@@ -90,15 +90,19 @@ __device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// Codes 0 and 4 of a word less 8, and codes 1 and 5 less 8 times 16: 0x6400 | x
-// is 1024 + x, exactly.  `k1024` holds 0x64006400 in a register the compiler
-// cannot see through, so that mask and magic are one instruction.
-__device__ __forceinline__ uint32_t less8(uint32_t w, uint32_t k1024) {
-    return add_half2(and_or(w, 0x000f000fu, k1024), 0xe408e408u);
+// Bytes 0 and 2 (BYTE 0) or 1 and 3 (BYTE 1) of a word as a pair of fp16
+// numbers under the high byte `top`: two codes c0 + 16 c1 each, with top 0x64
+// on 1024 and exact, with 0 times 2^-24.
+template <int BYTE>
+__device__ __forceinline__ uint32_t byte_pair(uint32_t w, uint32_t top) {
+    return __byte_perm(w, top, BYTE ? 0x4341 : 0x4240);
 }
-__device__ __forceinline__ uint32_t less8_16(uint32_t w, uint32_t k1024) {
-    return add_half2(and_or(w, 0x00f000f0u, k1024), 0xe480e480u);
-}
+constexpr uint32_t kTop = 0x64646464u;
+// Of such a pair the lower codes alone, the top byte kept.
+__device__ __forceinline__ uint32_t low_code(uint32_t x) { return x & 0xff0fff0fu; }
+// Off 1024 and less the middle: 8, and 8 + 16 * 8 for two codes.
+__device__ __forceinline__ uint32_t less8(uint32_t x) { return add_half2(x, 0xe408e408u); }
+__device__ __forceinline__ uint32_t less136(uint32_t x) { return add_half2(x, 0xe488e488u); }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
@@ -274,16 +278,23 @@ struct RowState {
             sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
             sum[j] *= a.scale_log2;
         }
-        // q 2^(13 - e) has its largest entry in [2^13, 2^14): hi in multiples of 2^3, lo (at most 2^2) held times 2^11
-        const int e = min(max(int(__float_as_uint(top) >> 23) - 127, -100), 100);
+        // q 2^(13 - e) has its largest entry, and a sixteenth more of it, below 2^14: hi in multiples of 2^3 (exact up
+        // to there), lo (at most 2^2) held times 2^11
+        const int e = min(max(int(__float_as_uint(top * 1.0625f) >> 23) - 127, -100), 100);
         const float up = __uint_as_float(uint32_t(140 - e) << 23);
         const float back = __uint_as_float(uint32_t(127 + e + 11) << 23) * a.scale_log2;  // 2^24 / up
 #pragma unroll
         for (int i = 0; i < NW; i++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) {  // codes r and r + 4; odd r meets codes times 16
+            for (int r = 0; r < 4; r++) {  // codes r and r + 4
+                // odd r meets codes times 16 (HC = 8) or, times 16, with the code before added (HC = 4); the latter's
+                // query then loses what that code has got there already
                 const float f = r & 1 ? up * 0.0625f : up;
-                const float x = q[i][r] * f, y = q[i][r + 4] * f;
+                float x = q[i][r] * f, y = q[i][r + 4] * f;
+                if (HC == 4 && !(r & 1)) {
+                    x = fmaf(q[i][r + 1], -0.0625f * up, x);
+                    y = fmaf(q[i][r + 5], -0.0625f * up, y);
+                }
                 float gx = on_grid(x, r & 1 ? 0.5f : 8.f), gy = on_grid(y, r & 1 ? 0.5f : 8.f);
                 if (HC == 8 && !q_lo) gx = x, gy = y;
                 const uint32_t hi = pack_half2(gx, gy), lo = pack_half2((x - gx) * 2048.f, (y - gy) * 2048.f);
@@ -347,17 +358,19 @@ struct RowState {
             if constexpr (HC == 4) {  // two chains where a group has more than one chunk
 #pragma unroll
                 for (int i = 0; i < GW; i++) {
-                    const uint32_t a = ka[j * GW + i], b = kb[j * GW + i], a8 = a >> 8, b8 = b >> 8;
+                    const uint32_t a = ka[j * GW + i], b = kb[j * GW + i];
+                    const uint32_t x = byte_pair<0>(a, 0), y = byte_pair<0>(b, 0);
+                    const uint32_t x2 = byte_pair<1>(a, 0), y2 = byte_pair<1>(b, 0);
                     const uint32_t(&q)[4] = qh[j * GW + i];
                     if (i == 0) {
-                        mma_f16_first(c0, a & lo, b & lo, a & hi, b & hi, q[0], q[1]);
+                        mma_f16_first(c0, a & lo, b & lo, x, y, q[0], q[1]);
                         if (GW > 1)
-                            mma_f16_first(c1, a8 & lo, b8 & lo, a8 & hi, b8 & hi, q[2], q[3]);
+                            mma_f16_first(c1, x2 & lo, y2 & lo, x2, y2, q[2], q[3]);
                         else
-                            mma_f16(c0, a8 & lo, b8 & lo, a8 & hi, b8 & hi, q[2], q[3]);
+                            mma_f16(c0, x2 & lo, y2 & lo, x2, y2, q[2], q[3]);
                     } else {
-                        mma_f16(c0, a & lo, b & lo, a & hi, b & hi, q[0], q[1]);
-                        mma_f16(c1, a8 & lo, b8 & lo, a8 & hi, b8 & hi, q[2], q[3]);
+                        mma_f16(c0, a & lo, b & lo, x, y, q[0], q[1]);
+                        mma_f16(c1, x2 & lo, y2 & lo, x2, y2, q[2], q[3]);
                     }
                 }
                 if (GW > 1) c0[0] += c1[0], c0[1] += c1[1], c0[2] += c1[2], c0[3] += c1[3];
@@ -509,8 +522,7 @@ struct RowState {
         const int token = tile * 16 + (mat & 1) * 8 + r;
         const int sw = D == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
         const uint32_t vrow = smem_u32(st) + P * (D / 2) + token * (D / 2);
-        uint32_t bh[2], bl[2], k1024;
-        asm("mov.b32 %0, 0x64006400;" : "=r"(k1024));
+        uint32_t bh[2], bl[2];
 #pragma unroll
         for (int c2 = 0; c2 < NW / 2; c2++) {
             uint32_t v[4];
@@ -536,9 +548,10 @@ struct RowState {
                     }
                 }
                 const uint32_t v0 = v[2 * cc], v1 = v[2 * cc + 1];
-                const uint32_t w0 = v0 >> 8, w1 = v1 >> 8;
-                const uint32_t a[4] = {less8(v0, k1024), less8_16(v0, k1024), less8(v1, k1024), less8_16(v1, k1024)};
-                const uint32_t b[4] = {less8(w0, k1024), less8_16(w0, k1024), less8(w1, k1024), less8_16(w1, k1024)};
+                const uint32_t x0 = byte_pair<0>(v0, kTop), x1 = byte_pair<0>(v1, kTop);
+                const uint32_t y0 = byte_pair<1>(v0, kTop), y1 = byte_pair<1>(v1, kTop);
+                const uint32_t a[4] = {less8(low_code(x0)), less136(x0), less8(low_code(x1)), less136(x1)};
+                const uint32_t b[4] = {less8(low_code(y0)), less136(y0), less8(low_code(y1)), less136(y1)};
                 mma_f16(o[c][0], a[0], a[1], a[2], a[3], bh[0], bh[1]);
                 mma_f16(o[c][1], b[0], b[1], b[2], b[3], bh[0], bh[1]);
                 if constexpr (HC == 8) {
@@ -570,10 +583,11 @@ struct RowState {
                 const float base = pm[h][c / GW];
                 float v[4];
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const float *q = o[c][k >> 1] + 2 * (k & 1);
-                    const float sum = HC == 4 ? q[0] + q[1] : q[h];
-                    v[k] = fmaf(sum, k & 1 ? unit * 0.0625f : unit, base) * inv;
+                for (int k = 0; k < 4; k += 2) {  // sums of codes c0, and of c0 + 16 c1
+                    const float *q = o[c][k >> 1];
+                    const float even = HC == 4 ? q[0] + q[1] : q[h], both = HC == 4 ? q[2] + q[3] : q[2 + h];
+                    v[k] = fmaf(even, unit, base) * inv;
+                    v[k + 1] = fmaf(both - even, unit * 0.0625f, base) * inv;
                 }
                 *reinterpret_cast<float4 *>(dst + 32 * c + 4 * g) = make_float4(v[0], v[1], v[2], v[3]);
             }
@@ -694,35 +708,38 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
     int put = 0, got = 0, parity = 0;
     const uint64_t policy = l2_evict_first_policy();
     uint32_t plain = 0;  // bit per ring stage: all its units are whole pages of the row before them
+    uint32_t live = 0, whole = 0;
+    int fill_last = -64;  // the unit before the first has no row
     auto issue = [&](int k) {
         if (k >= stages) return;
         const int first = k * U;
         if (first % kFill == 0) {  // describe the next kFill units
             __syncwarp();
             const int u = u0 + first + lane;
-            if (lane < kFill && u < u1)
-                s.desc[warp][(first + lane) % (2 * kFill)] =
-                    a.warp_units ? place_of(a, warp_index + u / a.warp_units * all_warps, u % a.warp_units, a.warp_units, block_bytes)
+            Unit d;
+            d.src = nullptr, d.row_valid = -1;
+            if (lane < kFill && u < u1) {
+                d = a.warp_units ? place_of(a, warp_index + u / a.warp_units * all_warps, u % a.warp_units, a.warp_units, block_bytes)
                     : a.row_ctas ? unit_of(a, row0, u, count0, block_bytes)
                                  : unit_at(a, s, entries, per, u, block_bytes);
+                s.desc[warp][(first + lane) % (2 * kFill)] = d;
+            }
+            // bit i: unit i is there; it is a whole page of the row before it
+            int before = __shfl_up_sync(0xffffffffu, d.row_valid, 1);
+            if (lane == 0) before = fill_last;
+            live = __ballot_sync(0xffffffffu, d.src != nullptr);
+            whole = __ballot_sync(0xffffffffu, d.src != nullptr && d.row_valid == ((before & ~63) | P));
+            fill_last = __shfl_sync(0xffffffffu, d.row_valid, kFill - 1);
             __syncwarp();
         }
-        const uint8_t *src = nullptr;
-        bool same = true;
-        if (lane < U) {
-            same = first + lane < n;
-            if (same) {
-                const Unit &d = s.desc[warp][(first + lane) % (2 * kFill)];
-                src = d.src;
-                same = src && first > 0 &&
-                       d.row_valid == ((s.desc[warp][(first + lane - 1) % (2 * kFill)].row_valid & ~63) | P);
-            }
-        }
-        const uint32_t live = __ballot_sync(0xffffffffu, src != nullptr);
-        same = __all_sync(0xffffffffu, same);
+        constexpr uint32_t stage_mask = (1u << U) - 1;
+        const uint32_t here = live >> (first % kFill) & stage_mask;
+        const bool same = (whole >> (first % kFill) & stage_mask) == stage_mask;
         plain = (plain & ~(1u << put)) | (uint32_t(same) << put);
+        const uint8_t *src = nullptr;
+        if (lane < U && (here >> lane & 1)) src = s.desc[warp][(first + lane) % (2 * kFill)].src;
         uint64_t *bar = &s.bar[warp][put];
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(live) * block_bytes);
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(here) * block_bytes);
         __syncwarp();
         if (src) {
             if (a.evict_first)

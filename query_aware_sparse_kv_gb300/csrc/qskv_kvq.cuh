@@ -47,13 +47,6 @@ __device__ __forceinline__ int kvq_value_place(int w, int token) {
     return (((w >> 2) ^ x) << 2) | (w & 3);
 }
 
-// (w & mask) | magic in one instruction, if `magic` is in a register.
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
-    return r;
-}
-
 // Untiled bulk copy global -> shared (16-byte aligned, whole 16 bytes) that completes on `bar`.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
