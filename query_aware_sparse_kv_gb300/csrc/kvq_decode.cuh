@@ -90,19 +90,27 @@ __device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// Bytes 0 and 2 (BYTE 0) or 1 and 3 (BYTE 1) of a word as a pair of fp16
-// numbers under the high byte `top`: two codes c0 + 16 c1 each, with top 0x64
-// on 1024 and exact, with 0 times 2^-24.
-template <int BYTE>
-__device__ __forceinline__ uint32_t byte_pair(uint32_t w, uint32_t top) {
-    return __byte_perm(w, top, BYTE ? 0x4341 : 0x4240);
+// Value codes 0 and 4 of a word less 8, and codes 1 and 5 less 8 times 16:
+// 0x6400 | x is 1024 + x, exactly.  `k1024` holds 0x64006400 in a register the
+// compiler cannot see through, so that mask and offset are one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+    return r;
 }
-constexpr uint32_t kTop = 0x64646464u;
-// Of such a pair the lower codes alone, the top byte kept.
-__device__ __forceinline__ uint32_t low_code(uint32_t x) { return x & 0xff0fff0fu; }
-// Off 1024 and less the middle: 8, and 8 + 16 * 8 for two codes.
-__device__ __forceinline__ uint32_t less8(uint32_t x) { return add_half2(x, 0xe408e408u); }
-__device__ __forceinline__ uint32_t less136(uint32_t x) { return add_half2(x, 0xe488e488u); }
+__device__ __forceinline__ uint32_t less8(uint32_t w, uint32_t k1024) {
+    return add_half2(and_or(w, 0x000f000fu, k1024), 0xe408e408u);
+}
+__device__ __forceinline__ uint32_t less8_16(uint32_t w, uint32_t k1024) {
+    return add_half2(and_or(w, 0x00f000f0u, k1024), 0xe480e480u);
+}
+
+// Bytes 0 and 2 (BYTE 0) or 1 and 3 (BYTE 1) of a word of key codes as a pair
+// of fp16 subnormals: two codes, (c0 + 16 c1) 2^-24 each.
+template <int BYTE>
+__device__ __forceinline__ uint32_t byte_pair(uint32_t w) {
+    return __byte_perm(w, 0, BYTE ? 0x4341 : 0x4240);
+}
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
@@ -359,8 +367,8 @@ struct RowState {
 #pragma unroll
                 for (int i = 0; i < GW; i++) {
                     const uint32_t a = ka[j * GW + i], b = kb[j * GW + i];
-                    const uint32_t x = byte_pair<0>(a, 0), y = byte_pair<0>(b, 0);
-                    const uint32_t x2 = byte_pair<1>(a, 0), y2 = byte_pair<1>(b, 0);
+                    const uint32_t x = byte_pair<0>(a), y = byte_pair<0>(b);
+                    const uint32_t x2 = byte_pair<1>(a), y2 = byte_pair<1>(b);
                     const uint32_t(&q)[4] = qh[j * GW + i];
                     if (i == 0) {
                         mma_f16_first(c0, a & lo, b & lo, x, y, q[0], q[1]);
@@ -522,7 +530,8 @@ struct RowState {
         const int token = tile * 16 + (mat & 1) * 8 + r;
         const int sw = D == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
         const uint32_t vrow = smem_u32(st) + P * (D / 2) + token * (D / 2);
-        uint32_t bh[2], bl[2];
+        uint32_t bh[2], bl[2], k1024;
+        asm("mov.b32 %0, 0x64006400;" : "=r"(k1024));
 #pragma unroll
         for (int c2 = 0; c2 < NW / 2; c2++) {
             uint32_t v[4];
@@ -548,10 +557,9 @@ struct RowState {
                     }
                 }
                 const uint32_t v0 = v[2 * cc], v1 = v[2 * cc + 1];
-                const uint32_t x0 = byte_pair<0>(v0, kTop), x1 = byte_pair<0>(v1, kTop);
-                const uint32_t y0 = byte_pair<1>(v0, kTop), y1 = byte_pair<1>(v1, kTop);
-                const uint32_t a[4] = {less8(low_code(x0)), less136(x0), less8(low_code(x1)), less136(x1)};
-                const uint32_t b[4] = {less8(low_code(y0)), less136(y0), less8(low_code(y1)), less136(y1)};
+                const uint32_t w0 = v0 >> 8, w1 = v1 >> 8;
+                const uint32_t a[4] = {less8(v0, k1024), less8_16(v0, k1024), less8(v1, k1024), less8_16(v1, k1024)};
+                const uint32_t b[4] = {less8(w0, k1024), less8_16(w0, k1024), less8(w1, k1024), less8_16(w1, k1024)};
                 mma_f16(o[c][0], a[0], a[1], a[2], a[3], bh[0], bh[1]);
                 mma_f16(o[c][1], b[0], b[1], b[2], b[3], bh[0], bh[1]);
                 if constexpr (HC == 8) {
@@ -583,11 +591,10 @@ struct RowState {
                 const float base = pm[h][c / GW];
                 float v[4];
 #pragma unroll
-                for (int k = 0; k < 4; k += 2) {  // sums of codes c0, and of c0 + 16 c1
-                    const float *q = o[c][k >> 1];
-                    const float even = HC == 4 ? q[0] + q[1] : q[h], both = HC == 4 ? q[2] + q[3] : q[2 + h];
-                    v[k] = fmaf(even, unit, base) * inv;
-                    v[k + 1] = fmaf(both - even, unit * 0.0625f, base) * inv;
+                for (int k = 0; k < 4; k++) {
+                    const float *q = o[c][k >> 1] + 2 * (k & 1);
+                    const float sum = HC == 4 ? q[0] + q[1] : q[h];
+                    v[k] = fmaf(sum, k & 1 ? unit * 0.0625f : unit, base) * inv;
                 }
                 *reinterpret_cast<float4 *>(dst + 32 * c + 4 * g) = make_float4(v[0], v[1], v[2], v[3]);
             }
