@@ -245,7 +245,8 @@ struct RowState {
     float qa[NH], qb[NH][NG];
     float m[NH], l[NH], sg[NH], pm[NH][NG];
     bool q_lo;  // HC = 8: the queries have lo halves (fp32 ones; bf16 fits fp16 as it is, half the products)
-    float o[NW][2][4];
+    // of a lane: dims 4g, 4g + 1 (rows g, g + 8 of [0]) and 4g + 2, 4g + 3 (of [1]) of each chunk, for each of its heads
+    float o[NW][2][2 * NH];
 
     __device__ __forceinline__ void load_query(const KvqDecodeArgs &a, int row) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -332,7 +333,7 @@ struct RowState {
 #pragma unroll
         for (int c = 0; c < NW; c++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) o[c][0][r] = o[c][1][r] = 0.f;
+            for (int r = 0; r < 2 * NH; r++) o[c][0][r] = o[c][1][r] = 0.f;
     }
 
     // Logits of one 16-token tile (`tile` of the block at `st`) in x, and its value params in va, vb.
@@ -501,8 +502,7 @@ struct RowState {
 #pragma unroll
                 for (int c = 0; c < NW; c++)
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        if (HC == 4 || (k & 1) == h) o[c][0][k] *= r, o[c][1][k] *= r;
+                    for (int k = h; k < 2 * NH; k += NH) o[c][0][k] *= r, o[c][1][k] *= r;
             }
         }
         // the value codes enter their product less 8 (sums of signed numbers: the tensor cores cut what they add
@@ -519,52 +519,71 @@ struct RowState {
                 for (int h = 0; h < NH; h++) pm[h][j] = fmaf(p[i][1][h], midb, fmaf(p[i][0][h], mida, pm[h][j]));
             }
         }
-#pragma unroll
-        for (int i = 0; i < NT; i++) values(st + (tile0 + i) / PT * block_bytes, (tile0 + i) % PT, w[i]);
+        values<NT>(st, tile0, w);
     }
 
-    // The outputs' sums take one tile's values with weights w.
-    __device__ __forceinline__ void values(const uint8_t *st, int tile, const float (&w)[2][NH][NG]) {
-        const int lane = threadIdx.x & 31;
-        const int mat = lane >> 3, r = lane & 7;
-        const int token = tile * 16 + (mat & 1) * 8 + r;
+    // The outputs' sums take NT tiles' values with weights w.  A chunk of 32 dims at a time goes through accumulators
+    // that start at zero and are added to the sums in fp32: the tensor cores cut what they add towards zero, which
+    // along a whole row would shrink the sums (1.1e-6 of them over 82 tiles); and with hi and lo columns (HC = 4) one
+    // sum of both is all that is kept.
+    template <int NT>
+    __device__ __forceinline__ void values(const uint8_t *st, int tile0, const float (&w)[NT][2][NH][NG]) {
+        constexpr int PT = P / 16;
+        constexpr uint32_t block_bytes = kvq_block_words(D, P, NG) * 4;
+        const int lane = threadIdx.x & 31, mat = lane >> 3, r = lane & 7;
         const int sw = D == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
-        const uint32_t vrow = smem_u32(st) + P * (D / 2) + token * (D / 2);
-        uint32_t bh[2], bl[2], k1024;
+        const uint32_t vrow = smem_u32(st) + P * (D / 2) + ((mat & 1) * 8 + r) * (D / 2);
+        uint32_t bh[NT][2], bl[NT][2], k1024;
         asm("mov.b32 %0, 0x64006400;" : "=r"(k1024));
 #pragma unroll
         for (int c2 = 0; c2 < NW / 2; c2++) {
-            uint32_t v[4];
-            ldmatrix_x4_trans(v, vrow + (((2 * c2 + (mat >> 1)) ^ sw) << 4));
+            uint32_t v[NT][4];
+#pragma unroll
+            for (int i = 0; i < NT; i++)
+                ldmatrix_x4_trans(v[i], vrow + (tile0 + i) / PT * block_bytes + (tile0 + i) % PT * 16 * (D / 2) +
+                                            (((2 * c2 + (mat >> 1)) ^ sw) << 4));
 #pragma unroll
             for (int cc = 0; cc < 2; cc++) {
                 const int c = 2 * c2 + cc;
-                if (c % GW == 0) {
-                    const int j = c / GW;
-                    if constexpr (HC == 4) {
+                float x0[4], x1[4];
+#pragma unroll
+                for (int i = 0; i < NT; i++) {
+                    if (c % GW == 0) {
+                        const int j = c / GW;
 #pragma unroll
                         for (int k = 0; k < 2; k++) {
-                            const float x = to_half(w[k][0][j]);
-                            bh[k] = movmatrix_trans(pack_half2(x, w[k][0][j] - x));
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 2; k++) {
-                            const float x = to_half(w[k][0][j]), y = to_half(w[k][NH - 1][j]);
-                            bh[k] = movmatrix_trans(pack_half2(x, y));
-                            bl[k] = movmatrix_trans(pack_half2(w[k][0][j] - x, w[k][NH - 1][j] - y));
+                            const float x = to_half(w[i][k][0][j]), y = to_half(w[i][k][NH - 1][j]);
+                            if constexpr (HC == 4) {
+                                bh[i][k] = movmatrix_trans(pack_half2(x, w[i][k][0][j] - x));
+                            } else {
+                                bh[i][k] = movmatrix_trans(pack_half2(x, y));
+                                bl[i][k] = movmatrix_trans(pack_half2(w[i][k][0][j] - x, w[i][k][NH - 1][j] - y));
+                            }
                         }
                     }
+                    const uint32_t v0 = v[i][2 * cc], v1 = v[i][2 * cc + 1], w0 = v0 >> 8, w1 = v1 >> 8;
+                    const uint32_t a[4] = {less8(v0, k1024), less8_16(v0, k1024), less8(v1, k1024), less8_16(v1, k1024)};
+                    const uint32_t b[4] = {less8(w0, k1024), less8_16(w0, k1024), less8(w1, k1024), less8_16(w1, k1024)};
+                    if (i == 0) {
+                        mma_f16_first(x0, a[0], a[1], a[2], a[3], bh[i][0], bh[i][1]);
+                        mma_f16_first(x1, b[0], b[1], b[2], b[3], bh[i][0], bh[i][1]);
+                    } else {
+                        mma_f16(x0, a[0], a[1], a[2], a[3], bh[i][0], bh[i][1]);
+                        mma_f16(x1, b[0], b[1], b[2], b[3], bh[i][0], bh[i][1]);
+                    }
+                    if constexpr (HC == 8) {
+                        mma_f16(x0, a[0], a[1], a[2], a[3], bl[i][0], bl[i][1]);
+                        mma_f16(x1, b[0], b[1], b[2], b[3], bl[i][0], bl[i][1]);
+                    }
                 }
-                const uint32_t v0 = v[2 * cc], v1 = v[2 * cc + 1];
-                const uint32_t w0 = v0 >> 8, w1 = v1 >> 8;
-                const uint32_t a[4] = {less8(v0, k1024), less8_16(v0, k1024), less8(v1, k1024), less8_16(v1, k1024)};
-                const uint32_t b[4] = {less8(w0, k1024), less8_16(w0, k1024), less8(w1, k1024), less8_16(w1, k1024)};
-                mma_f16(o[c][0], a[0], a[1], a[2], a[3], bh[0], bh[1]);
-                mma_f16(o[c][1], b[0], b[1], b[2], b[3], bh[0], bh[1]);
-                if constexpr (HC == 8) {
-                    mma_f16(o[c][0], a[0], a[1], a[2], a[3], bl[0], bl[1]);
-                    mma_f16(o[c][1], b[0], b[1], b[2], b[3], bl[0], bl[1]);
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    if constexpr (HC == 4) {
+                        o[c][0][k] += x0[2 * k] + x0[2 * k + 1], o[c][1][k] += x1[2 * k] + x1[2 * k + 1];
+                    } else {
+                        o[c][0][2 * k] += x0[2 * k], o[c][0][2 * k + 1] += x0[2 * k + 1];
+                        o[c][1][2 * k] += x1[2 * k], o[c][1][2 * k + 1] += x1[2 * k + 1];
+                    }
                 }
             }
         }
@@ -592,9 +611,7 @@ struct RowState {
                 float v[4];
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
-                    const float *q = o[c][k >> 1] + 2 * (k & 1);
-                    const float sum = HC == 4 ? q[0] + q[1] : q[h];
-                    v[k] = fmaf(sum, k & 1 ? unit * 0.0625f : unit, base) * inv;
+                    v[k] = fmaf(o[c][k >> 1][NH * (k & 1) + h], k & 1 ? unit * 0.0625f : unit, base) * inv;
                 }
                 *reinterpret_cast<float4 *>(dst + 32 * c + 4 * g) = make_float4(v[0], v[1], v[2], v[3]);
             }
