@@ -90,27 +90,18 @@ __device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// Value codes 0 and 4 of a word less 8, and codes 1 and 5 less 8 times 16:
-// 0x6400 | x is 1024 + x, exactly.  `k1024` holds 0x64006400 in a register the
-// compiler cannot see through, so that mask and offset are one instruction.
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
-    return r;
-}
-__device__ __forceinline__ uint32_t less8(uint32_t w, uint32_t k1024) {
-    return add_half2(and_or(w, 0x000f000fu, k1024), 0xe408e408u);
-}
-__device__ __forceinline__ uint32_t less8_16(uint32_t w, uint32_t k1024) {
-    return add_half2(and_or(w, 0x00f000f0u, k1024), 0xe480e480u);
-}
-
-// Bytes 0 and 2 (BYTE 0) or 1 and 3 (BYTE 1) of a word of key codes as a pair
-// of fp16 subnormals: two codes, (c0 + 16 c1) 2^-24 each.
+// Bytes 0 and 2 (BYTE 0) or 1 and 3 (BYTE 1) of a word as a pair of fp16
+// numbers under the high byte `top`: two codes c0 + 16 c1 each, on 1024 and
+// exact with top 0x64 (normal numbers), times 2^-24 with 0 (subnormals).
 template <int BYTE>
-__device__ __forceinline__ uint32_t byte_pair(uint32_t w) {
-    return __byte_perm(w, 0, BYTE ? 0x4341 : 0x4240);
+__device__ __forceinline__ uint32_t byte_pair(uint32_t w, uint32_t top) {
+    return __byte_perm(w, top, BYTE ? 0x4341 : 0x4240);
 }
+constexpr uint32_t kTop = 0x64646464u;
+// The lower code alone of such a pair on 1024, less 8; and both less their
+// middles, 8 + 16 * 8.
+__device__ __forceinline__ uint32_t less8(uint32_t x) { return add_half2(x & 0xff0fff0fu, 0xe408e408u); }
+__device__ __forceinline__ uint32_t less136(uint32_t x) { return add_half2(x, 0xe488e488u); }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
@@ -245,7 +236,8 @@ struct RowState {
     float qa[NH], qb[NH][NG];
     float m[NH], l[NH], sg[NH], pm[NH][NG];
     bool q_lo;  // HC = 8: the queries have lo halves (fp32 ones; bf16 fits fp16 as it is, half the products)
-    // of a lane: dims 4g, 4g + 1 (rows g, g + 8 of [0]) and 4g + 2, 4g + 3 (of [1]) of each chunk, for each of its heads
+    // of a lane, for each of its heads and each chunk: the sums of dim 4g's codes and of those plus 16 times dim 4g + 1's
+    // (rows g and g + 8 of [0]), and the same of dims 4g + 2 and 4g + 3 ([1])
     float o[NW][2][2 * NH];
 
     __device__ __forceinline__ void load_query(const KvqDecodeArgs &a, int row) {
@@ -368,8 +360,8 @@ struct RowState {
 #pragma unroll
                 for (int i = 0; i < GW; i++) {
                     const uint32_t a = ka[j * GW + i], b = kb[j * GW + i];
-                    const uint32_t x = byte_pair<0>(a), y = byte_pair<0>(b);
-                    const uint32_t x2 = byte_pair<1>(a), y2 = byte_pair<1>(b);
+                    const uint32_t x = byte_pair<0>(a, 0), y = byte_pair<0>(b, 0);
+                    const uint32_t x2 = byte_pair<1>(a, 0), y2 = byte_pair<1>(b, 0);
                     const uint32_t(&q)[4] = qh[j * GW + i];
                     if (i == 0) {
                         mma_f16_first(c0, a & lo, b & lo, x, y, q[0], q[1]);
@@ -533,8 +525,7 @@ struct RowState {
         const int lane = threadIdx.x & 31, mat = lane >> 3, r = lane & 7;
         const int sw = D == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
         const uint32_t vrow = smem_u32(st) + P * (D / 2) + ((mat & 1) * 8 + r) * (D / 2);
-        uint32_t bh[NT][2], bl[NT][2], k1024;
-        asm("mov.b32 %0, 0x64006400;" : "=r"(k1024));
+        uint32_t bh[NT][2], bl[NT][2];
 #pragma unroll
         for (int c2 = 0; c2 < NW / 2; c2++) {
             uint32_t v[NT][4];
@@ -561,9 +552,12 @@ struct RowState {
                             }
                         }
                     }
-                    const uint32_t v0 = v[i][2 * cc], v1 = v[i][2 * cc + 1], w0 = v0 >> 8, w1 = v1 >> 8;
-                    const uint32_t a[4] = {less8(v0, k1024), less8_16(v0, k1024), less8(v1, k1024), less8_16(v1, k1024)};
-                    const uint32_t b[4] = {less8(w0, k1024), less8_16(w0, k1024), less8(w1, k1024), less8_16(w1, k1024)};
+                    // rows g: the lower code of each byte; rows g + 8: both, lower + 16 * upper
+                    const uint32_t v0 = v[i][2 * cc], v1 = v[i][2 * cc + 1];
+                    const uint32_t e0 = byte_pair<0>(v0, kTop), e1 = byte_pair<0>(v1, kTop);
+                    const uint32_t f0 = byte_pair<1>(v0, kTop), f1 = byte_pair<1>(v1, kTop);
+                    const uint32_t a[4] = {less8(e0), less136(e0), less8(e1), less136(e1)};
+                    const uint32_t b[4] = {less8(f0), less136(f0), less8(f1), less136(f1)};
                     if (i == 0) {
                         mma_f16_first(x0, a[0], a[1], a[2], a[3], bh[i][0], bh[i][1]);
                         mma_f16_first(x1, b[0], b[1], b[2], b[3], bh[i][0], bh[i][1]);
@@ -610,8 +604,10 @@ struct RowState {
                 const float base = pm[h][c / GW];
                 float v[4];
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    v[k] = fmaf(o[c][k >> 1][NH * (k & 1) + h], k & 1 ? unit * 0.0625f : unit, base) * inv;
+                for (int k = 0; k < 4; k += 2) {
+                    const float lower = o[c][k >> 1][h], both = o[c][k >> 1][NH + h];
+                    v[k] = fmaf(lower, unit, base) * inv;
+                    v[k + 1] = fmaf(both - lower, unit * 0.0625f, base) * inv;
                 }
                 *reinterpret_cast<float4 *>(dst + 32 * c + 4 * g) = make_float4(v[0], v[1], v[2], v[3]);
             }
