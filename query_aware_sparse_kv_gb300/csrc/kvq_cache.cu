@@ -1,11 +1,15 @@
 // Writing to, reading from and summarising the 4-bit paged KV cache (format:
 // qskv_kvq.cuh).
 //
-// All three are bound by HBM: append reads 2 d elements a token and head and
-// writes d + 8 NG bytes, gather does the reverse, the metadata build reads
-// half a block and writes 2 d bf16.  A thread owns one 32-bit code word
-// (8 dims), so a bf16 row is read (or written) 16 bytes a lane and the
-// reductions over a group run over 4, 8 or 16 neighbouring lanes.
+// Append reads 2 d elements a token and head and writes d + 8 NG bytes, gather
+// does the reverse, the metadata build reads half a block and writes 2 d bf16.
+// A thread owns one 32-bit code word (8 dims), so a bf16 row is read (or
+// written) 16 bytes a lane and the reductions over a group run over 4, 8 or 16
+// neighbouring lanes.  One GB300: 131072 tokens x 8 heads of 128 dims read
+// back to bf16 in 119 us (5.9 TB/s of 6.76 copied: HBM); 32768 tokens stored
+// in 52 us (3.3 TB/s) and the metadata of 36864 pages x 8 heads made in 157 us
+// (3.1 TB/s), both at 75 to 80 % of the issue slots with the ALU pipe at 65 to
+// 70 %: bound by the instructions a code costs.
 #include <cuda_fp16.h>
 
 #include "qskv_internal.h"

@@ -7,20 +7,25 @@
 // matrix products run on the codes u themselves and scales and minima are
 // applied per token and group, outside them.
 //
-// Bound: HBM.  A token and head is d + 8 NG bytes; the arithmetic on it has
-// to fit the time those take (23 bytes a clock and SM), which is what shapes
-// the inner loop:
-//   * a code is a fp16 number as it stands: the bits 0x000u are the subnormal
-//     u 2^-24 and 0x00u0 is 16 u 2^-24, both exact operands of the tensor
-//     cores.  A word of 8 codes becomes four fp16 pairs with four ANDs and one
-//     shift; the 16 is taken off the query (keys) or the output (values).
+// Bound: the SMs' instruction issue (with all pages in L2 the kernel takes as
+// long as from HBM), then HBM.  A token and head is d + 8 NG bytes, 23 bytes a
+// clock and SM at the copy rate; the arithmetic on it should fit that time,
+// which shapes the inner loop:
+//   * a code is a fp16 number almost as it stands.  Keys: one byte permutation
+//     puts a byte, two codes c0 + 16 c1, under a zero byte, the subnormal
+//     (c0 + 16 c1) 2^-24; masking the upper code off gives c0 2^-24.  The
+//     query of c1 is taken a sixteenth, and that much off c0's.  Values: the
+//     same under 0x64 (1024 + x, exact), less the middle of the codes, so that
+//     sums of signed, normal numbers are made.
 //   * S (16 tokens x 8 columns) = K_tile Q^T and O^T (dims x 8) += V_tile^T P^T
 //     as mma.sync m16n8k16 with fp32 accumulators; at most 8 query heads share
-//     a cache row, so there is no 128-row tile to feed tcgen05 with.
+//     a cache row, so there is no 128-row tile to feed tcgen05 with, and the
+//     codes would have to be widened into shared memory for it.
 //   * fp32 precision from fp16 operands: queries (scaled by a power of two
 //     into fp16's range) and weights enter as two halves hi + lo.  With at
 //     most 4 heads (HC = 4) the halves share the 8 columns: column 2h is head
-//     h's hi, 2h + 1 its lo; with 8 heads they are two products.
+//     h's hi, 2h + 1 its lo; with 8 heads they are two products.  Outputs are
+//     within 2e-7 of fp64 over the measured cases.
 //   * a key's words lie so that a lane's operands are one vector load; values
 //     come through ldmatrix.trans, whose 16-bit elements are four codes of one
 //     token: the pair of a register is two tokens, as the product needs.
@@ -28,18 +33,27 @@
 // Softmax.  Running references per head: M for the exponent and sg for the
 // weights times value scales (p s sg is what becomes fp16).  Both are moved
 // only when a weight would pass 2^12, or p s sg 2^14 (rare after the first
-// tile), so the usual tile has no rescaling and one vote.  Sums of weights
+// tile), so the usual step has no rescaling and one vote.  Sums of weights
 // and of p m stay per lane until the row ends.
 //
-// Work split.  A unit is one page of one (sequence, KV head) row; all units
-// in row order are cut into equal ranges, one per warp of a grid of two CTAs
-// an SM.  Every CTA finds its range from a scan of the lengths (or selection
-// counts) in shared memory, so ragged batches balance exactly.  A warp keeps
-// its own ring of stages, one bulk copy a page, and its own running state; a
-// row that lies within a warp is finished by it, pieces of a row within a CTA
-// are folded in shared memory, and pieces of several CTAs by the CTA that
-// draws the row's last ticket, always in unit order: results do not depend on
-// timing.
+// Work split.  A unit is one page of one (sequence, KV head) row.  A warp has
+// its own ring of stages of about 4 KB (one bulk copy a page, one mbarrier a
+// stage) and its own running state, and takes a range of units:
+//   * many rows of few pages: rows to warps in turn, whole;
+//   * rows that fit one wave of CTAs and are cut alike (selections, short
+//     tables): a group of CTAs a row, whose warps share its units;
+//   * else all units in row order in equal ranges, one a warp, for a grid of
+//     two CTAs an SM; every CTA finds its ranges from a scan of the lengths
+//     (or selection counts) in shared memory, so ragged batches balance.
+// A row that lies within a warp is finished by it, pieces of a row within a
+// CTA are folded there, and pieces of several CTAs by the CTA that draws the
+// row's last ticket, always in unit order: results do not depend on timing.
+//
+// One GB300, GPU time: 32 sequences x 8 KV heads x 128 pages of 16 tokens, 4
+// heads a group: 22.8 us (3.2 TB/s); 4 x 65536..131072 tokens, groups of 32
+// dims: 105 us (4.8 TB/s, 71 % of the copy rate); 64 ragged sequences up to
+// 4095 tokens with 8 heads a group, fp32 queries: 74 us (2.1 TB/s); two short
+// rows: 5.3 us.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -800,14 +814,17 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
             break;
         }
         const uint8_t *stage = ring + got * (U * block_bytes);
-        if (HC == 4 && same) {
+        // Two tiles a step share the vote and hide each other's latencies, where the registers suffice: with 8 heads only
+        // for one group a row (32 x 8 rows of 8192 tokens: 84 us, 89 tile by tile; a ragged batch with two groups 77 and 74).
+        constexpr bool kPairs = HC == 4 || NG == 1;
+        if (kPairs && same) {
 #pragma unroll
             for (int t = 0; t < kTiles; t += 2) st.template tiles<2>(stage, t, 16);
         } else {
 #pragma unroll 1
             for (int t = 0; t < kTiles; t++) {
                 int nv = 16;
-                if (HC == 4 || !same) {
+                if (kPairs || !same) {
                     const int it = k * U + t / kPageTiles;
                     if (it >= n) break;
                     const Unit u = s.desc[warp][it % (2 * kFill)];

