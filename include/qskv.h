@@ -390,8 +390,8 @@ qskv_status qskv_cascade_paged_decode(const void *q, qskv_dtype q_dtype, const v
  * key's word w = 4i + t is stored at place t * (d / 32) + i of its row; a
  * value's word w = 4c + j of token t at place 4 (c ^ x) + j with
  * x = (t / 2) % 4 for d = 128, (t / 4) % 2 for d = 64.
- * group_size: 32, 64 or 128, at most head_dim.  Values must be finite and
- * below 2^60 in magnitude.
+ * group_size: 32, 64 or 128, at most head_dim.  Keys, values and queries must
+ * be finite and below 2^60 in magnitude.
  *
  * qskv_kvq_block_bytes: bytes of one block, page_size * (d + 8 NG)
  * (0 for an unsupported shape or group size).
@@ -439,8 +439,9 @@ qskv_status qskv_kvq_meta_build(const void *pool, const int32_t *page_ids, const
                                 int32_t n_pages, void *meta, qskv_dtype meta_dtype, const qskv_shape *shape,
                                 int32_t group_size, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of workspace of qskv_kvq_paged_decode (the other qskv_kvq calls need
- * 256 and may share it); same rules as qskv_workspace_size. */
+/* Bytes of workspace of qskv_kvq_paged_decode; same rules as
+ * qskv_workspace_size.  The other qskv_kvq calls need 256; all calls of one
+ * shape may share one buffer of the largest size. */
 size_t qskv_kvq_workspace_size(const qskv_shape *shape);
 
 /*
@@ -485,13 +486,14 @@ qskv_status qskv_kvq_paged_decode(const void *q, qskv_dtype q_dtype, const void 
  *   max_tokens   length of slot_map and positions
  *   max_touched  length of touched_ids and touched_valid, at least
  *                min(max_tokens, max_tokens / page_size + 2 batch)
- * Uses batch, page_size, max_pages and num_pool_pages of the shape.  No
- * output may overlap an input or another output.
+ * Uses batch, num_kv_heads, page_size, max_pages and num_pool_pages of the
+ * shape.  No output may overlap an input or another output.
  * Device errors: a length outside [0, max_pages * page_size] (before or after)
  * refuses that request; a page id outside the pool (in the free list or the
  * table) gives its tokens slot -1 and its touched entry -1; both flag
  * QSKV_ERR_DEVICE_INDEX.
- * Workspace: qskv_tables_workspace_size bytes, 256-byte aligned, zeroed once.
+ * Workspace: qskv_tables_workspace_size bytes, 256-byte aligned, zeroed once;
+ * it may be shared with the other calls (of the same batch and num_kv_heads).
  */
 size_t qskv_tables_workspace_size(const qskv_shape *shape);
 

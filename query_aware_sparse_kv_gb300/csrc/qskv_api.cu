@@ -1061,10 +1061,13 @@ qskv_status qskv_kvq_paged_decode(const void *q, qskv_dtype q_dtype, const void 
 }
 
 // ------------------------------------------------------------- page tables --
+// The prefixes lie behind the row counters of the other calls, which stay zero in a shared workspace.
+static size_t tables_scratch(const qskv_shape *s) { return align256(256 + size_t(s->batch) * s->num_kv_heads * 4); }
+
 size_t qskv_tables_workspace_size(const qskv_shape *shape) {
     if (check_shape(shape) != QSKV_OK) return 0;
-    const size_t prefixes = shape->batch > kTablesScanRequests ? size_t(3) * (size_t(shape->batch) + 1) * 4 : 0;
-    return 256 + align256(prefixes);
+    if (shape->batch <= kTablesScanRequests) return 256;
+    return tables_scratch(shape) + align256(size_t(3) * (size_t(shape->batch) + 1) * 4);
 }
 
 qskv_status qskv_extend_tables(const int32_t *seq_lens, const int32_t *new_lens, const int32_t *free_pages,
@@ -1115,7 +1118,7 @@ qskv_status qskv_extend_tables(const int32_t *seq_lens, const int32_t *new_lens,
     a.n_free = n_free;
     a.max_tokens = max_tokens;
     a.max_touched = touched_ids ? max_touched : most;
-    return launched(launch_extend_tables(a, reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + 256), sms,
+    return launched(launch_extend_tables(a, reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + tables_scratch(shape)), sms,
                                          static_cast<cudaStream_t>(stream)),
                     "extend_tables launch");
 }

@@ -215,7 +215,9 @@ class QuantizedPagedDecoder:
     ``append`` (their keys and values quantised into the pool, the touched
     pages' metadata rebuilt), ``select`` (with top_k: the pages each query
     attends to) and ``decode``; ``step`` does all of it.  Row lengths are
-    also kept on the host, so a step never waits for the GPU.
+    also kept on the host, so a step never waits for the GPU.  (The lengths
+    come from the host: ``extend`` cannot be captured into a graph; the calls
+    it makes can, see binding.extend_tables.)
 
     batch       rows (requests); a row of length 0 is free
     max_pages   pages a row may hold
@@ -247,6 +249,7 @@ class QuantizedPagedDecoder:
         self.out = torch.zeros((batch, num_q_heads, head_dim), dtype=torch.float32, device=device)
         self.lse = torch.zeros((batch, num_q_heads), dtype=torch.float32, device=device)
         self.lengths = [0] * batch  # as of the last extend
+        self._new = 0  # tokens of the last extend that append has not stored yet
 
     def _pages(self, tokens: int) -> int:
         return -(-tokens // self.shape.page_size)
@@ -259,6 +262,8 @@ class QuantizedPagedDecoder:
         new = [int(n) for n in new_lens]
         if len(new) != self.shape.batch or min(new) < 0:
             raise ValueError(f"new_lens must be {self.shape.batch} counts >= 0")
+        if self._new:
+            raise ValueError(f"{self._new} tokens of the last extend are not stored yet")
         if sum(new) > self.max_tokens:
             raise ValueError(f"{sum(new)} new tokens, at most {self.max_tokens} a step")
         grown = [a + n for a, n in zip(self.lengths, new)]
@@ -268,22 +273,26 @@ class QuantizedPagedDecoder:
         need = sum(self._pages(n) - self._pages(a) for a, n in zip(self.lengths, grown))
         if need > self.free_pages.numel():
             raise ValueError(f"{need} pages needed, {self.free_pages.numel()} free")
-        added = torch.tensor(new, dtype=torch.int32).to(self.pool.device, non_blocking=True)
+        with torch.cuda.device(self.pool.device), torch.cuda.stream(stream):  # (stream None: the current one)
+            added = torch.tensor(new, dtype=torch.int32).to(self.pool.device, non_blocking=True)
         B.extend_tables(self.seq_lens, added, self.free_pages, self.page_table, self._lens_out, self.cu_new,
                         self.slot_map, self.shape, self.workspace, positions=self.positions,
                         touched_ids=self.touched_ids, touched_valid=self.touched_valid, stream=stream)
         self.seq_lens, self._lens_out = self._lens_out, self.seq_lens
         self.free_pages = self.free_pages[need:]
-        self.lengths = grown
+        self.lengths, self._new = grown, sum(new)
 
     def append(self, k: torch.Tensor, v: torch.Tensor, stream=None):
         """Store the keys and values [n][Hkv][d] of the tokens of the last
         ``extend`` (rows in order) and, with top_k, rebuild the metadata of
         the pages they fall into."""
+        if k.shape[0] != self._new:
+            raise ValueError(f"{k.shape[0]} keys for the {self._new} tokens of the last extend")
         B.kvq_append(k, v, self.slot_map[:k.shape[0]], self.pool, self.shape, self.group_size, self.workspace, stream)
         if self.top_k is not None:
             B.kvq_meta_build(self.pool, self.touched_ids, self.touched_valid, self.meta, self.shape, self.group_size,
                              self.workspace, stream)
+        self._new = 0
 
     def select(self, q: torch.Tensor, stream=None):
         """The top_k pages of every (row, KV head) by their score bound."""
@@ -311,18 +320,20 @@ class QuantizedPagedDecoder:
     def gather(self, row: int, dtype=torch.float32, stream=None):
         """The cached keys and values [length][Hkv][d] of a row."""
         P, n = self.shape.page_size, self.lengths[row]
-        t = torch.arange(n, device=self.pool.device)
-        slots = (self.page_table[row].long()[t // P] * P + t % P).to(torch.int32)
-        k, v = (torch.empty((n, self.shape.num_kv_heads, self.shape.head_dim), dtype=dtype, device=self.pool.device)
-                for _ in range(2))
+        with torch.cuda.device(self.pool.device), torch.cuda.stream(stream):
+            t = torch.arange(n, device=self.pool.device)
+            slots = (self.page_table[row].long()[t // P] * P + t % P).to(torch.int32)
+            k, v = (torch.empty((n, self.shape.num_kv_heads, self.shape.head_dim), dtype=dtype,
+                                device=self.pool.device) for _ in range(2))
         B.kvq_gather(self.pool, slots, k, v, self.shape, self.group_size, self.workspace, stream)
         return k, v
 
-    def release(self, row: int):
+    def release(self, row: int, stream=None):
         """Give a row's pages back; its length is 0 afterwards."""
         n = self._pages(self.lengths[row])
-        self.free_pages = torch.cat([self.free_pages, self.page_table[row, :n]])
-        self.seq_lens[row] = 0
+        with torch.cuda.device(self.pool.device), torch.cuda.stream(stream):
+            self.free_pages = torch.cat([self.free_pages, self.page_table[row, :n]])
+            self.seq_lens[row] = 0
         self.lengths[row] = 0
 
     def check(self, stream=None):

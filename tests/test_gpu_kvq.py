@@ -302,6 +302,9 @@ def test_decode_over_selected_pages(d, gs, P, hq, hkv):
     ([3000, 1, 20_000, 0, 7], 4, 2, 128, 32, 64),
     ([1] * 700, 2, 2, 64, 16, 64),       # more rows than warps, one token each
     ([37] * 300 + [0] * 100 + [2000], 4, 4, 64, 16, 32),
+    ([i * 7 % 41 for i in range(900)] + [500], 1, 1, 64, 16, 32),  # more sequences than the prefix has entries
+    ([i * 13 % 190 for i in range(170)], 16, 2, 64, 16, 64),     # whole rows to warps, 8 heads, empty ones
+    ([i * 29 % 350 for i in range(110)], 4, 4, 128, 32, 128),    # the same, pages of 32
 ])
 def test_decode_splits_and_joins(lens, hq, hkv, d, P, gs):
     b = Batch(17, lens, hq, hkv, d, P, gs, torch.float32)
@@ -312,6 +315,19 @@ def test_decode_splits_and_joins(lens, hq, hkv, d, P, gs):
     for _ in range(3):  # no order of arrival shows
         b.decode()
         assert torch.equal(b.out, first)
+
+
+@pytest.mark.parametrize("P,top_k,most", [(16, 5, 190), (16, 20, 700), (32, 40, 900)])
+def test_decode_over_selected_pages_of_many_rows(P, top_k, most):
+    """More rows than a wave of CTAs: short selections to warps whole, longer ones split evenly; some rows empty, some
+    selecting nothing."""
+    g = torch.Generator().manual_seed(top_k)
+    lens = [0 if i % 17 == 0 else i * 37 % most for i in range(200)]
+    b = Batch(31, lens, 4, 2, 64, P, 64, torch.bfloat16)
+    sel = [[sorted(torch.randperm(n, generator=g)[:min(n, (i * 3 + h) % (top_k + 1))].tolist()) for h in range(2)]
+           for i, n in enumerate(b.n)]
+    b.decode(selected=sel, top_k=top_k)
+    b.check(selected=sel)
 
 
 def test_decode_with_a_wider_table_and_without_lse():
@@ -521,6 +537,34 @@ def test_tables_of_long_prompts():
     assert err == 0
 
 
+def test_tables_share_the_decodes_workspace():
+    """More requests than one CTA scans: the tables' scratch leaves the decode's row counters alone."""
+    B, P, mp, N = 4100, 16, 200, 800
+    shape = qskv.make_shape(B, 1, 1, 64, P, mp, N)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = _ws(max(qskv.kvq_workspace_size(shape), qskv.tables_workspace_size(shape)))
+    g = torch.Generator().manual_seed(2)
+    f = [R.quantise(torch.randn((N, 1, P, 64), generator=g), 64) for _ in range(2)]
+    pool = R.pack(*f[0], *f[1]).cuda()
+    new = i32(B)
+    new[0], new[7], new[4099] = 3000, 2900, 3100
+    table, lens, cu, slots = torch.full((B, mp), -1, dtype=torch.int32, device="cuda"), i32(B), i32(B + 1), i32(9000)
+    q, outs = torch.randn((B, 1, 64), device="cuda"), []
+    for _ in range(3):
+        qskv.extend_tables(i32(B), new, torch.arange(N, dtype=torch.int32, device="cuda"), table, lens, cu, slots, shape, ws)
+        outs.append(torch.empty((B, 1, 64), device="cuda"))
+        qskv.kvq_paged_decode(q, pool, table, lens, outs[-1], shape, 64, ws)
+        assert qskv.get_error(ws) == 0
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2]) and bool((outs[0][[0, 7, 4099]] != 0).any())
+    kx, vx = R.values(*f[0]), R.values(*f[1])
+    at = [(j // P, j % P) for j in range(3000)]
+    p, t = ([x[i] for x in at] for i in (0, 1))
+    o, _ = R.attend(q[0].cpu(), kx[p, 0, t], vx[p, 0, t], 64 ** -0.5)
+    tol, _ = R.attend_bounds(q[0].cpu(), f[0][2][p, 0, t], f[0][1][p, 0, t], f[1][2][p, 0, t], f[1][1][p, 0, t], 64 ** -0.5,
+                             3000)
+    assert float((outs[0][0].cpu().double() - o).abs().max()) <= tol
+
+
 # ------------------------------------------------------------- in a run --
 def test_a_serving_run_together():
     """Prefill of two requests and four decode steps: tables, append, metadata, selection and decode in turn, against
@@ -623,4 +667,16 @@ def test_quantized_decoder_runs_a_batch():
             dec.extend([300, 101, 0])
         with pytest.raises(ValueError, match="row 2"):
             dec.extend([0, 0, 53])
+        with pytest.raises(ValueError, match="1 keys for the 0 tokens"):
+            dec.append(k.cuda()[:1], v.cuda()[:1])
         assert dec.lengths == [0, 19, 92]
+        side = torch.cuda.Stream()  # the same on a stream that is not the current one
+        side.wait_stream(torch.cuda.current_stream())
+        dec.extend([0, 2, 0], stream=side)
+        with pytest.raises(ValueError, match="2 tokens of the last extend"):
+            dec.extend([1, 0, 0])
+        dec.append(k.cuda()[:2], v.cuda()[:2], stream=side)
+        got = dec.gather(1, stream=side)
+        side.synchronize()
+        for x, y in zip(got, (k, v)):
+            assert torch.equal(x[-2:].cpu(), R.values(*R.quantise(y[:2], gs)).float())
