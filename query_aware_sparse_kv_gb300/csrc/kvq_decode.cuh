@@ -24,8 +24,12 @@
 //   * fp32 precision from fp16 operands: queries (scaled by a power of two
 //     into fp16's range) and weights enter as two halves hi + lo.  With at
 //     most 4 heads (HC = 4) the halves share the 8 columns: column 2h is head
-//     h's hi, 2h + 1 its lo; with 8 heads they are two products.  Outputs are
-//     within 2e-7 of fp64 over the measured cases.
+//     h's hi, 2h + 1 its lo; with 8 heads they are two products.  bf16 queries
+//     of 8 heads need no lo half as long as a code's query stays as it is, so
+//     their keys' upper codes are masked out instead (one product; permuted
+//     ones with the lo half take 119 instead of 110 us at 32 x 8 rows of 8192
+//     tokens in groups of 32; fp32 queries gain: 87 instead of 92 us in groups
+//     of 128).  Outputs are within 2e-7 of fp64 over the measured cases.
 //   * a key's words lie so that a lane's operands are one vector load; values
 //     come through ldmatrix.trans, whose 16-bit elements are four codes of one
 //     token: the pair of a register is two tokens, as the product needs.
@@ -52,8 +56,8 @@
 // One GB300, GPU time: 32 sequences x 8 KV heads x 128 pages of 16 tokens, 4
 // heads a group: 22.8 us (3.2 TB/s); 4 x 65536..131072 tokens, groups of 32
 // dims: 105 us (4.8 TB/s, 71 % of the copy rate); 64 ragged sequences up to
-// 4095 tokens with 8 heads a group, fp32 queries: 74 us (2.1 TB/s); two short
-// rows: 5.3 us.
+// 4095 tokens with 8 heads a group, fp32 queries: 69.8 us (2.2 TB/s); two
+// short rows: 5.3 us.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -116,6 +120,15 @@ constexpr uint32_t kTop = 0x64646464u;
 // middles, 8 + 16 * 8.
 __device__ __forceinline__ uint32_t less8(uint32_t x) { return add_half2(x & 0xff0fff0fu, 0xe408e408u); }
 __device__ __forceinline__ uint32_t less136(uint32_t x) { return add_half2(x, 0xe488e488u); }
+
+// a0 += b0, a1 += b1 as one instruction.
+__device__ __forceinline__ void add_pair(float &a0, float &a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1));
+}
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
@@ -302,11 +315,11 @@ struct RowState {
         for (int i = 0; i < NW; i++)
 #pragma unroll
             for (int r = 0; r < 4; r++) {  // codes r and r + 4
-                // odd r meets codes times 16 (HC = 8) or, times 16, with the code before added (HC = 4); the latter's
-                // query then loses what that code has got there already
+                // odd r meets 16 times its code, alone (HC = 8, bf16 queries) or with the code before added, whose query
+                // then loses what that code has got there already
                 const float f = r & 1 ? up * 0.0625f : up;
                 float x = q[i][r] * f, y = q[i][r + 4] * f;
-                if (HC == 4 && !(r & 1)) {
+                if ((HC == 4 || q_lo) && !(r & 1)) {
                     x = fmaf(q[i][r + 1], -0.0625f * up, x);
                     y = fmaf(q[i][r + 5], -0.0625f * up, y);
                 }
@@ -392,28 +405,37 @@ struct RowState {
                 ua[0] = fmaf(c0[1], lo_unit, c0[0]);
                 ub[0] = fmaf(c0[3], lo_unit, c0[2]);
             } else {
-#pragma unroll
-                for (int i = 0; i < GW; i++) {
-                    const uint32_t a = ka[j * GW + i], b = kb[j * GW + i], a8 = a >> 8, b8 = b >> 8;
-                    if (i == 0)
-                        mma_f16_first(c0, a & lo, b & lo, a & hi, b & hi, qh[j * GW + i][0], qh[j * GW + i][1]);
-                    else
-                        mma_f16(c0, a & lo, b & lo, a & hi, b & hi, qh[j * GW + i][0], qh[j * GW + i][1]);
-                    mma_f16(c0, a8 & lo, b8 & lo, a8 & hi, b8 & hi, qh[j * GW + i][2], qh[j * GW + i][3]);
-                }
-                if (q_lo) {
+                if (q_lo) {  // one product's operands for both halves: a permutation saves the masks of the upper codes
 #pragma unroll
                     for (int i = 0; i < GW; i++) {
-                        const uint32_t a = ka[j * GW + i], b = kb[j * GW + i], a8 = a >> 8, b8 = b >> 8;
-                        const uint4 q = ql[(j * GW + i) * 32 + lane];
-                        if (i == 0)
-                            mma_f16_first(c1, a & lo, b & lo, a & hi, b & hi, q.x, q.y);
-                        else
-                            mma_f16(c1, a & lo, b & lo, a & hi, b & hi, q.x, q.y);
-                        mma_f16(c1, a8 & lo, b8 & lo, a8 & hi, b8 & hi, q.z, q.w);
+                        const uint32_t a = ka[j * GW + i], b = kb[j * GW + i];
+                        const uint32_t x = byte_pair<0>(a, 0), y = byte_pair<0>(b, 0);
+                        const uint32_t x2 = byte_pair<1>(a, 0), y2 = byte_pair<1>(b, 0);
+                        const uint32_t(&q)[4] = qh[j * GW + i];
+                        const uint4 ql4 = ql[(j * GW + i) * 32 + lane];
+                        if (i == 0) {
+                            mma_f16_first(c0, a & lo, b & lo, x, y, q[0], q[1]);
+                            mma_f16_first(c1, a & lo, b & lo, x, y, ql4.x, ql4.y);
+                        } else {
+                            mma_f16(c0, a & lo, b & lo, x, y, q[0], q[1]);
+                            mma_f16(c1, a & lo, b & lo, x, y, ql4.x, ql4.y);
+                        }
+                        mma_f16(c0, x2 & lo, y2 & lo, x2, y2, q[2], q[3]);
+                        mma_f16(c1, x2 & lo, y2 & lo, x2, y2, ql4.z, ql4.w);
                     }
 #pragma unroll
                     for (int k = 0; k < 4; k++) c0[k] = fmaf(c1[k], lo_unit, c0[k]);
+                } else {  // masked: a code's query stays the bf16 value, which fp16 holds whole, and no lo half is needed
+#pragma unroll
+                    for (int i = 0; i < GW; i++) {
+                        const uint32_t a = ka[j * GW + i], b = kb[j * GW + i], a8 = a >> 8, b8 = b >> 8;
+                        const uint32_t(&q)[4] = qh[j * GW + i];
+                        if (i == 0)
+                            mma_f16_first(c0, a & lo, b & lo, a & hi, b & hi, q[0], q[1]);
+                        else
+                            mma_f16(c0, a & lo, b & lo, a & hi, b & hi, q[0], q[1]);
+                        mma_f16(c0, a8 & lo, b8 & lo, a8 & hi, b8 & hi, q[2], q[3]);
+                    }
                 }
                 ua[0] = c0[0], ua[NH - 1] = c0[1];
                 ub[0] = c0[2], ub[NH - 1] = c0[3];
@@ -589,8 +611,8 @@ struct RowState {
                     if constexpr (HC == 4) {
                         o[c][0][k] += x0[2 * k] + x0[2 * k + 1], o[c][1][k] += x1[2 * k] + x1[2 * k + 1];
                     } else {
-                        o[c][0][2 * k] += x0[2 * k], o[c][0][2 * k + 1] += x0[2 * k + 1];
-                        o[c][1][2 * k] += x1[2 * k], o[c][1][2 * k + 1] += x1[2 * k + 1];
+                        add_pair(o[c][0][2 * k], o[c][0][2 * k + 1], x0[2 * k], x0[2 * k + 1]);
+                        add_pair(o[c][1][2 * k], o[c][1][2 * k + 1], x1[2 * k], x1[2 * k + 1]);
                     }
                 }
             }
