@@ -289,38 +289,47 @@ __device__ __forceinline__ uint32_t pack_bf16x2_down(float lo, float hi) {
     return __byte_perm(a + (uint32_t(int32_t(a) >> 31) & 0xffffu), b + (uint32_t(int32_t(b) >> 31) & 0xffffu), 0x7632);
 }
 
-// A warp takes (listed page, KV head) tiles in turn through a ring of bulk
-// copies of its own (a tile's key codes and key params are 1.1 KB a page of
-// 16 tokens; the ring keeps about 80 KB an SM on their way, where direct
-// loads of one tile a warp left the kernel waiting: 262 us for 36864 pages).
-// D / 8 lanes cover a token's code words, 32 / (D / 8) tokens at a time;
-// lanes of the same word combine by shuffles at the end.
-constexpr int kMetaWarps = 8, kMetaStages = 4;
+// A lane group of D / 8 lanes, one a code word of a token, takes whole (listed
+// page, KV head) tiles: a warp 2 or 4 at a time, so that nothing is combined
+// across lanes.  The tiles come through a ring of bulk copies, a warp's own (a
+// tile's key codes and key params are 1.1 KB a page of 16 tokens; direct loads
+// of one tile a warp left the kernel waiting: 262 us for 36864 pages x 8
+// heads).  One tile a warp, its tokens on two lane groups joined by shuffles,
+// took 157 us there against 125 now (3.9 TB/s; 64-dim heads 123 against 69):
+// the mask, conversion, fma, min and max of each code bound it, not HBM.
+// CTAs of 4 warps: 300 to 600 pages take 3.7 and 4.4 us, with 8 warps 4.2 and
+// 4.7 (36864 pages 123); pages of 32 tokens leave room for 5 CTAs an SM.
+constexpr int kMetaWarps = 4, kMetaStages = 2;
+
+// Words of a tile in the ring: D / 8 more than a multiple of the banks, so that the lane groups meet different ones.
+__host__ __device__ constexpr int kvq_meta_tile_words(int words, int page_size, int groups) {
+    return page_size * (words + groups) + ((words - page_size * (words + groups)) & 31);
+}
 
 template <bool BF16, int D, int GS>
-__global__ void __launch_bounds__(kMetaWarps * 32, 4) kvq_meta_kernel(KvqMetaArgs a) {
-    constexpr int W = D / 8, TP = 32 / W, NG = D / GS;
+__global__ void __launch_bounds__(kMetaWarps * 32, 8) kvq_meta_kernel(KvqMetaArgs a) {
+    constexpr int W = D / 8, T = 32 / W, NG = D / GS, S = kMetaStages, R = 32 / T;
     extern __shared__ __align__(128) uint32_t ring_mem[];
-    __shared__ uint64_t bars[kMetaWarps][kMetaStages];
+    __shared__ uint64_t bars[kMetaWarps][S];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int P = a.page_size, S = P == 16 ? kMetaStages : kMetaStages / 2;
-    const int code_words = P * W, stage_words = code_words + NG * P;
+    const int P = a.page_size, warps = blockDim.x >> 5;  // at most kMetaWarps
+    const int code_words = P * W, tile_words = kvq_meta_tile_words(W, P, NG), stage_words = T * tile_words;
     uint32_t *ring = ring_mem + warp * (S * stage_words);
-    if (lane < S) mbar_init(&bars[warp][lane], 1);
+    if (lane < S) mbar_init(&bars[warp][lane], T);
     mbar_fence_init();
     __syncwarp();
     pdl_trigger();
     pdl_wait();
-    const int64_t tiles = int64_t(a.n_list) * a.num_kv_heads;
-    const int64_t first = int64_t(blockIdx.x) * kMetaWarps + warp, step = int64_t(gridDim.x) * kMetaWarps;
-    const int n = first < tiles ? int((tiles - first + step - 1) / step) : 0;
-    // lane i of the warp describes the warp's tiles i, 32 + i, ..: (page, head) block and valid tokens
+    const int64_t tiles = int64_t(a.n_list) * a.num_kv_heads, steps = (tiles + T - 1) / T;
+    const int64_t first = int64_t(blockIdx.x) * warps + warp, stride = int64_t(gridDim.x) * warps;
+    const int n = first < steps ? int((steps - first + stride - 1) / stride) : 0;
+    // lane T i + k describes tile k of the warp's steps i, R + i, ..: (page, head) block and valid tokens
     int64_t at = 0;
     int valid = 0;
     auto describe = [&](int i) {
         valid = 0;
-        const int64_t tile = first + (i + lane) * step;
-        if (i + lane >= n) return;
+        const int64_t tile = (first + (i + lane / T) * stride) * T + lane % T;
+        if (i + lane / T >= n || tile >= tiles) return;
         const int e = int(tile / a.num_kv_heads), g = int(tile - int64_t(e) * a.num_kv_heads);
         const int p = __ldg(a.page_ids + e), v = __ldg(a.valid_tokens + e);
         if (p < 0) return;
@@ -335,16 +344,17 @@ __global__ void __launch_bounds__(kMetaWarps * 32, 4) kvq_meta_kernel(KvqMetaArg
         at = int64_t(p) * a.num_kv_heads + g, valid = v;
     };
     int put = 0, got = 0, parity = 0;
-    auto issue = [&](int i) {
+    auto issue = [&](int i) {  // lane k copies tile k
         if (i >= n) return;
-        const int v = __shfl_sync(0xffffffffu, valid, i & 31);
-        const int64_t b = __shfl_sync(0xffffffffu, at, i & 31);
-        if (lane == 0) {
+        const int from = i % R * T + lane % T;
+        const int v = __shfl_sync(0xffffffffu, valid, from);
+        const int64_t b = __shfl_sync(0xffffffffu, at, from);
+        if (lane < T) {
             const uint32_t *block = a.pool + b * kvq_block_words(D, P, NG);
             uint64_t *bar = &bars[warp][put];
-            uint32_t *dst = ring + put * stage_words;
+            uint32_t *dst = ring + put * stage_words + lane * tile_words;
             if (v > 0) {
-                mbar_arrive_expect_tx(bar, stage_words * 4);
+                mbar_arrive_expect_tx(bar, (code_words + NG * P) * 4);
                 bulk_load(dst, block, code_words * 4, bar);
                 bulk_load(dst + code_words, block + 2 * code_words, NG * P * 4, bar);
             } else {
@@ -353,18 +363,18 @@ __global__ void __launch_bounds__(kMetaWarps * 32, 4) kvq_meta_kernel(KvqMetaArg
         }
         if (++put == S) put = 0;
     };
-    const int place = lane % W, t0 = lane / W, w = kvq_key_word<D>(place);
+    const int place = lane % W, tile = lane / W, w = kvq_key_word<D>(place);
     describe(0);
     for (int i = 0; i < S - 1; i++) issue(i);
-    // a description is replaced once its 32 tiles are under way, so what the loop needs of the older ones is kept
+    // a description is replaced once its steps are under way, so what the loop needs of the older ones is kept
     int64_t kept_at = 0;
     int kept_valid = 0;
     for (int i = 0; i < n; i++) {
-        if ((i & 31) == 0) kept_at = at, kept_valid = valid;
-        if (((i + S - 1) & 31) == 0) describe(i + S - 1);
+        if (i % R == 0) kept_at = at, kept_valid = valid;
+        if ((i + S - 1) % R == 0) describe(i + S - 1);
         issue(i + S - 1);
-        const int v = __shfl_sync(0xffffffffu, kept_valid, i & 31);
-        const int64_t b = __shfl_sync(0xffffffffu, kept_at, i & 31);
+        const int v = __shfl_sync(0xffffffffu, kept_valid, i % R * T + tile);
+        const int64_t b = __shfl_sync(0xffffffffu, kept_at, i % R * T + tile);
         if (!mbar_wait_bounded(&bars[warp][got], parity, kWaitLimitNs)) {
             // a lost copy: flagged, the rest is given up once the copies in flight had their time
             if (lane == 0) raise_error(a.flags, kErrTimeout);
@@ -374,54 +384,54 @@ __global__ void __launch_bounds__(kMetaWarps * 32, 4) kvq_meta_kernel(KvqMetaArg
             }
             return;
         }
-        if (v > 0) {
-            const uint32_t *codes = ring + got * stage_words, *params = codes + code_words + w / (GS / 8) * P;
-            float mn[8], mx[8];
+        const uint32_t *codes = ring + got * stage_words + tile * tile_words + place;
+        const uint32_t *params = codes - place + code_words + w / (GS / 8) * P;
+        float mn[8], mx[8];
 #pragma unroll
-            for (int k = 0; k < 8; k++) mn[k] = INFINITY, mx[k] = -INFINITY;
-            auto take = [&](int ta, int tb) {
-                float x[8], y[8];
-                kvq_values(codes[ta * W + place], params[ta], x);
-                kvq_values(codes[tb * W + place], params[tb], y);
-#pragma unroll
-                for (int k = 0; k < 8; k++) {
-                    mn[k] = fminf(fminf(x[k], y[k]), mn[k]);
-                    mx[k] = fmaxf(fmaxf(x[k], y[k]), mx[k]);
-                }
-            };
-            if (v == P) {
-                for (int c = 0; c < P; c += 16)
-#pragma unroll
-                    for (int t = 0; t < 16; t += 2 * TP) take(c + t + t0, c + t + t0 + TP);
-            } else {
-#pragma unroll 1
-                for (int t = 0; t < v; t += 2 * TP)  // a token past the end repeats the last one
-                    take(min(t + t0, v - 1), min(t + t0 + TP, v - 1));
-            }
-            // even lane groups (of W lanes) end up with the minima, odd ones with the negated maxima
-            const bool odd = t0 & 1;
-            float r[8];
+        for (int k = 0; k < 8; k++) mn[k] = INFINITY, mx[k] = -INFINITY;
+        auto take = [&](int ta, int tb, uint32_t pa, uint32_t pb) {
+            float x[8], y[8];
+            kvq_values(codes[ta * W], pa, x);
+            kvq_values(codes[tb * W], pb, y);
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-                const float other = __shfl_xor_sync(0xffffffffu, odd ? mn[k] : -mx[k], W);
-                r[k] = fminf(odd ? -mx[k] : mn[k], other);
-                if (TP == 4) r[k] = fminf(r[k], __shfl_xor_sync(0xffffffffu, r[k], 2 * W));
+                mn[k] = fminf(fminf(x[k], y[k]), mn[k]);
+                mx[k] = fmaxf(fmaxf(x[k], y[k]), mx[k]);
             }
-            if (t0 < 2) {
-                const int64_t to = (b * 2 + t0) * D + w * 8;
-                const uint32_t sign = odd ? 0x80000000u : 0u;
-                if constexpr (BF16) {
-                    const uint32_t sign2 = sign | sign >> 16;
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.meta) + to) =
-                        make_uint4(pack_bf16x2_down(r[0], r[1]) ^ sign2, pack_bf16x2_down(r[2], r[3]) ^ sign2,
-                                   pack_bf16x2_down(r[4], r[5]) ^ sign2, pack_bf16x2_down(r[6], r[7]) ^ sign2);
-                } else {
+        };
+        if (__all_sync(0xffffffffu, v == P)) {
+            for (int c = 0; c < P; c += 16)
 #pragma unroll
-                    for (int k = 0; k < 8; k++) r[k] = bits_f(__float_as_uint(r[k]) ^ sign);
-                    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.meta) + to);
-                    o[0] = make_float4(r[0], r[1], r[2], r[3]);
-                    o[1] = make_float4(r[4], r[5], r[6], r[7]);
+                for (int t = 0; t < 16; t += 4) {
+                    const uint4 p = *reinterpret_cast<const uint4 *>(params + c + t);
+                    take(c + t, c + t + 1, p.x, p.y);
+                    take(c + t + 2, c + t + 3, p.z, p.w);
                 }
+        } else {  // a token past the end repeats the last one
+            const int last = max(v - 1, 0), most = __reduce_max_sync(0xffffffffu, v);
+#pragma unroll 1
+            for (int t = 0; t < most; t += 2) {
+                const int ta = min(t, last), tb = min(t + 1, last);
+                take(ta, tb, params[ta], params[tb]);
+            }
+        }
+        if (v > 0) {
+            const int64_t to = b * 2 * D + w * 8;
+            if constexpr (BF16) {  // the maximum up: the negated one down
+                uint16_t *o = static_cast<uint16_t *>(a.meta) + to;
+                constexpr uint32_t sign = 0x80008000u;
+                *reinterpret_cast<uint4 *>(o) =
+                    make_uint4(pack_bf16x2_down(mn[0], mn[1]), pack_bf16x2_down(mn[2], mn[3]),
+                               pack_bf16x2_down(mn[4], mn[5]), pack_bf16x2_down(mn[6], mn[7]));
+                *reinterpret_cast<uint4 *>(o + D) =
+                    make_uint4(pack_bf16x2_down(-mx[0], -mx[1]) ^ sign, pack_bf16x2_down(-mx[2], -mx[3]) ^ sign,
+                               pack_bf16x2_down(-mx[4], -mx[5]) ^ sign, pack_bf16x2_down(-mx[6], -mx[7]) ^ sign);
+            } else {
+                float *o = static_cast<float *>(a.meta) + to;
+                reinterpret_cast<float4 *>(o)[0] = make_float4(mn[0], mn[1], mn[2], mn[3]);
+                reinterpret_cast<float4 *>(o)[1] = make_float4(mn[4], mn[5], mn[6], mn[7]);
+                reinterpret_cast<float4 *>(o + D)[0] = make_float4(mx[0], mx[1], mx[2], mx[3]);
+                reinterpret_cast<float4 *>(o + D)[1] = make_float4(mx[4], mx[5], mx[6], mx[7]);
             }
         }
         if (++got == S) got = 0, parity ^= 1;
@@ -469,14 +479,18 @@ cudaError_t launch_kvq_gather(const KvqStoreArgs &a, int dtype, int head_dim, cu
 
 cudaError_t launch_kvq_meta(const KvqMetaArgs &a, int meta_dtype, int head_dim, int num_sms, cudaStream_t stream) {
     const bool bf16 = meta_dtype == kDtypeBf16;
-    const int64_t ctas = (int64_t(a.n_list) * a.num_kv_heads + kMetaWarps - 1) / kMetaWarps;
-    const dim3 grid(unsigned(ctas < 4 * num_sms ? ctas : 4 * num_sms));
-    const int stages = a.page_size == 16 ? kMetaStages : kMetaStages / 2;
-    const int bytes = kMetaWarps * stages * a.page_size * (head_dim / 8 + head_dim / a.group_size) * 4;  // at most 40 KB
+    const int words = head_dim / 8, groups = head_dim / a.group_size, per_warp = 32 / words;
+    const int64_t tiles = int64_t(a.n_list) * a.num_kv_heads;
+    int warps = kMetaWarps;
+    while (warps > 1 && tiles <= int64_t(warps / 2) * per_warp * num_sms) warps /= 2;  // few tiles: all SMs take a share
+    const int per_cta = warps * per_warp;
+    const int64_t ctas = (tiles + per_cta - 1) / per_cta;
+    const dim3 grid(unsigned(ctas < 8 * num_sms ? ctas : 8 * num_sms));
+    const int bytes = per_cta * kMetaStages * kvq_meta_tile_words(words, a.page_size, groups) * 4;  // at most 41 KB
 #define KVQ_META(d, gs)                                                                                                 \
     if (head_dim == d && a.group_size == gs)                                                                            \
-        return bf16 ? launch_pdl(kvq_meta_kernel<true, d, gs>, grid, dim3(kMetaWarps * 32), bytes, stream, a)           \
-                    : launch_pdl(kvq_meta_kernel<false, d, gs>, grid, dim3(kMetaWarps * 32), bytes, stream, a);
+        return bf16 ? launch_pdl(kvq_meta_kernel<true, d, gs>, grid, dim3(warps * 32), bytes, stream, a)                \
+                    : launch_pdl(kvq_meta_kernel<false, d, gs>, grid, dim3(warps * 32), bytes, stream, a);
     KVQ_FORMATS(KVQ_META)
     return cudaErrorInvalidValue;
 }

@@ -192,6 +192,35 @@ def test_metadata_of_bad_entries_is_flagged_and_left():
     assert bool((meta == 5).all())
 
 
+@pytest.mark.parametrize("d, gs, P, entries", [(64, 32, 16, 90000), (64, 64, 32, 3001), (128, 128, 16, 80000),
+                                               (128, 32, 32, 20000)])
+def test_metadata_of_long_lists(d, gs, P, entries):
+    """Many tiles a warp, odd numbers of heads; full, part filled, skipped and bad entries next to one another."""
+    g = torch.Generator().manual_seed(entries)
+    N, H = 61, 3
+    shape = qskv.make_shape(1, H, H, d, P, 1, N)
+    f = [R.quantise(torch.randn((N, H, P, d), generator=g), gs) for _ in range(2)]
+    pool, ws = R.pack(*f[0], *f[1]).cuda(), _ws()
+    filled = torch.randint(1, P + 1, (N,), generator=g)
+    filled[::2] = P
+    k = R.values(*f[0]).float()
+    want = torch.full((N, H, 2, d), 123.0)
+    for bad in (False, True):
+        ids = torch.randint(0, N - 1, (entries,), generator=g)  # a page listed again is given the same count again
+        valid = filled[ids]
+        ids[5::7] = -1
+        if bad:
+            ids[3::1001], valid[4::1009] = N, P + 1
+        meta = torch.full((N, H, 2, d), 123.0, device="cuda")
+        qskv.kvq_meta_build(pool, ids.int().cuda(), valid.int().cuda(), meta, shape, gs, ws)
+        assert qskv.get_error(ws) == (5 if bad else 0)
+        for p in range(N):
+            listed = bool(((ids == p) & (valid <= P)).any())
+            x = k[p, :, :int(filled[p])]
+            want[p] = torch.stack([x.amin(1), x.amax(1)], 1) if listed else 123.0
+        assert torch.equal(meta.cpu(), want)
+
+
 # --------------------------------------------------------------- decode --
 def _garbage(pool, page, first, d, P, gs):
     """The params of a page's places from `first` on become NaN, infinities and the type's extremes."""
