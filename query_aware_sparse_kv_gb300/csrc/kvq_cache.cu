@@ -7,8 +7,8 @@
 // written) 16 bytes a lane and the reductions over a group run over 4, 8 or 16
 // neighbouring lanes.  One GB300: 131072 tokens x 8 heads of 128 dims read
 // back to bf16 in 119 us (5.9 TB/s of 6.76 copied: HBM); 32768 tokens stored
-// in 52 us (3.3 TB/s) and the metadata of 36864 pages x 8 heads made in 157 us
-// (3.1 TB/s), both at 75 to 80 % of the issue slots with the ALU pipe at 65 to
+// in 47 us (3.7 TB/s) and the metadata of 36864 pages x 8 heads made in 125 us
+// (3.9 TB/s), both at 75 to 80 % of the issue slots with the ALU pipe at 65 to
 // 70 %: bound by the instructions a code costs.
 #include <cuda_fp16.h>
 
@@ -19,6 +19,31 @@ namespace qskv {
 namespace {
 
 __device__ __forceinline__ float bits_f(uint32_t b) { return __uint_as_float(b); }
+
+// Two floats in one 64-bit register, an instruction for both.
+struct Float2 {
+    uint64_t r;
+    __device__ __forceinline__ Float2() {}
+    __device__ __forceinline__ Float2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ void get(float &a, float &b) const {
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+    }
+};
+__device__ __forceinline__ Float2 operator+(Float2 a, Float2 b) {
+    Float2 c;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(c.r) : "l"(a.r), "l"(b.r));
+    return c;
+}
+__device__ __forceinline__ Float2 operator*(Float2 a, Float2 b) {
+    Float2 c;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(c.r) : "l"(a.r), "l"(b.r));
+    return c;
+}
+__device__ __forceinline__ Float2 fma(Float2 a, Float2 b, Float2 c) {
+    Float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.r) : "l"(a.r), "l"(b.r), "l"(c.r));
+    return d;
+}
 
 // x - m and the rounding error of that difference: their sum is exact.
 __device__ __forceinline__ void exact_diff(float x, float m, float &d, float &err) {
@@ -98,11 +123,14 @@ __device__ __forceinline__ uint32_t kvq_word_plain(const float (&x)[8], float m,
     constexpr uint32_t sum16 = 0x11111111u * 0x4b400000u;
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const Float2 inv2(inv, inv), minus_s(-s, -s), minus_m(-m, -m), magic2(magic, magic);
     uint32_t acc = 0;
 #pragma unroll
-    for (int k = 7; k >= 0; k--) {
-        const float d = x[k] - m, q0 = d * inv, q = fmaf(fmaf(-q0, s, d), inv, q0);
-        acc = acc * 16 + __float_as_uint(q + magic);
+    for (int k = 6; k >= 0; k -= 2) {
+        const Float2 d = Float2(x[k], x[k + 1]) + minus_m, q0 = d * inv2, q = fma(fma(q0, minus_s, d), inv2, q0);
+        float a, b;
+        (q + magic2).get(a, b);
+        acc = (acc * 16 + __float_as_uint(b)) * 16 + __float_as_uint(a);
     }
     return acc - sum16;
 }
