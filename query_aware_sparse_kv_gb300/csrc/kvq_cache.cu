@@ -7,8 +7,8 @@
 // written) 16 bytes a lane and the reductions over a group run over 4, 8 or 16
 // neighbouring lanes.  One GB300: 131072 tokens x 8 heads of 128 dims read
 // back to bf16 in 119 us (5.9 TB/s of 6.76 copied: HBM); 32768 tokens stored
-// in 47 us (3.7 TB/s) and the metadata of 36864 pages x 8 heads made in 125 us
-// (3.9 TB/s), both at 75 to 80 % of the issue slots with the ALU pipe at 65 to
+// in 45 us (3.8 TB/s) and the metadata of 36864 pages x 8 heads made in 115 us
+// (4.3 TB/s), both at 75 to 80 % of the issue slots with the ALU pipe at 65 to
 // 70 %: bound by the instructions a code costs.
 #include <cuda_fp16.h>
 
@@ -84,13 +84,16 @@ __device__ __forceinline__ uint32_t kvq_word(const float (&x)[8], float m, float
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
     uint32_t acc = 0;
     float off = 0.f;
+    const Float2 inv2(inv, inv), s2(s, s), minus_m(-m, -m), magic2(magic, magic), minus1(-1.f, -1.f);
 #pragma unroll
-    for (int k = 7; k >= 0; k--) {
-        const float d = x[k] - m;
-        float t = fmaf(d, inv, magic);
-        off = fmaxf(off, fabsf(fmaf(magic - t, s, d)));
-        if (CLAMP) t = fminf(fmaxf(t, magic), magic + 15.f);
-        acc = acc * 16 + __float_as_uint(t);
+    for (int k = 6; k >= 0; k -= 2) {
+        const Float2 d = Float2(x[k], x[k + 1]) + minus_m, t = fma(d, inv2, magic2);
+        const Float2 r = fma(fma(t, minus1, magic2), s2, d);
+        float a, b, ra, rb;
+        t.get(a, b), r.get(ra, rb);
+        off = fmaxf(fmaxf(fabsf(ra), fabsf(rb)), off);
+        if (CLAMP) a = fminf(fmaxf(a, magic), magic + 15.f), b = fminf(fmaxf(b, magic), magic + 15.f);
+        acc = (acc * 16 + __float_as_uint(b)) * 16 + __float_as_uint(a);
     }
     const float half = 0.5f * s;
     if (off > half - s * 1.9073486328125e-6f) {
@@ -254,8 +257,8 @@ __device__ __forceinline__ void kvq_values(uint32_t word, uint32_t par, float (&
         const uint32_t even = w & 0x000f000fu, odd = w & 0x00f000f0u;
         const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&even));
         const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&odd));
-        x[2 * h] = fmaf(a.x, s, m), x[2 * h + 4] = fmaf(a.y, s, m);
-        x[2 * h + 1] = fmaf(b.x, s16, m), x[2 * h + 5] = fmaf(b.y, s16, m);
+        fma(Float2(a.x, a.y), Float2(s, s), Float2(m, m)).get(x[2 * h], x[2 * h + 4]);
+        fma(Float2(b.x, b.y), Float2(s16, s16), Float2(m, m)).get(x[2 * h + 1], x[2 * h + 5]);
     }
 }
 
@@ -323,10 +326,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2_down(float lo, float hi) {
 // tile's key codes and key params are 1.1 KB a page of 16 tokens; direct loads
 // of one tile a warp left the kernel waiting: 262 us for 36864 pages x 8
 // heads).  One tile a warp, its tokens on two lane groups joined by shuffles,
-// took 157 us there against 125 now (3.9 TB/s; 64-dim heads 123 against 69):
-// the mask, conversion, fma, min and max of each code bound it, not HBM.
-// CTAs of 4 warps: 300 to 600 pages take 3.7 and 4.4 us, with 8 warps 4.2 and
-// 4.7 (36864 pages 123); pages of 32 tokens leave room for 5 CTAs an SM.
+// took 157 us there, whole tiles 125 (64-dim heads 123 and 69), and with two
+// values an fma 115 (4.3 TB/s; 63): the mask, conversion, min and max of each
+// code bound it (ALU 73 %, issue 80 %), not HBM.
+// CTAs of 4 warps: 300 and 600 pages take 3.6 and 4.3 us, with 8 warps 4.2 and
+// 4.7 (36864 pages: 125 against 123, before the pairs); pages of 32 tokens leave room for 5 CTAs an SM.
 constexpr int kMetaWarps = 4, kMetaStages = 2;
 
 // Words of a tile in the ring: D / 8 more than a multiple of the banks, so that the lane groups meet different ones.
