@@ -56,7 +56,7 @@
 // One GB300, GPU time: 32 sequences x 8 KV heads x 128 pages of 16 tokens, 4
 // heads a group: 22.8 us (3.2 TB/s); 4 x 65536..131072 tokens, groups of 32
 // dims: 105 us (4.8 TB/s, 71 % of the copy rate); 64 ragged sequences up to
-// 4095 tokens with 8 heads a group, fp32 queries: 69.8 us (2.2 TB/s); two
+// 4095 tokens with 8 heads a group, fp32 queries: 69.4 us (2.2 TB/s); two
 // short rows: 5.3 us.
 #pragma once
 
@@ -128,6 +128,15 @@ __device__ __forceinline__ void add_pair(float &a0, float &a1, float b0, float b
         "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
         : "+f"(a0), "+f"(a1)
         : "f"(b0), "f"(b1));
+}
+
+// c0 += a0 * b0, c1 += a1 * b1 likewise.
+__device__ __forceinline__ void fma_pair(float &c0, float &c1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%0, %1};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "+f"(c0), "+f"(c1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -424,7 +433,7 @@ struct RowState {
                         mma_f16(c1, x2 & lo, y2 & lo, x2, y2, ql4.z, ql4.w);
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; k++) c0[k] = fmaf(c1[k], lo_unit, c0[k]);
+                    for (int k = 0; k < 4; k += 2) fma_pair(c0[k], c0[k + 1], c1[k], c1[k + 1], lo_unit, lo_unit);
                 } else {  // masked: a code's query stays the bf16 value, which fp16 holds whole, and no lo half is needed
 #pragma unroll
                     for (int i = 0; i < GW; i++) {
@@ -442,10 +451,12 @@ struct RowState {
             }
             const float sa = bf16_lo_to_float(pa), ma = bf16_hi_to_float(pa);
             const float sb = bf16_lo_to_float(pb), mb = bf16_hi_to_float(pb);
-#pragma unroll
-            for (int h = 0; h < NH; h++) {
-                x[0][h] = fmaf(sa, ua[h], x[0][h]), xm[0][h] = fmaf(ma, qb[h][j], xm[0][h]);
-                x[1][h] = fmaf(sb, ub[h], x[1][h]), xm[1][h] = fmaf(mb, qb[h][j], xm[1][h]);
+            if constexpr (NH == 2) {  // in pairs: 32 x 8 rows of 8192 tokens, fp32, in 85.4 against 87.5 us
+                fma_pair(x[0][0], x[0][1], sa, sa, ua[0], ua[1]), fma_pair(xm[0][0], xm[0][1], ma, ma, qb[0][j], qb[1][j]);
+                fma_pair(x[1][0], x[1][1], sb, sb, ub[0], ub[1]), fma_pair(xm[1][0], xm[1][1], mb, mb, qb[0][j], qb[1][j]);
+            } else {
+                x[0][0] = fmaf(sa, ua[0], x[0][0]), xm[0][0] = fmaf(ma, qb[0][j], xm[0][0]);
+                x[1][0] = fmaf(sb, ub[0], x[1][0]), xm[1][0] = fmaf(mb, qb[0][j], xm[1][0]);
             }
         }
 #pragma unroll
