@@ -521,13 +521,15 @@ struct RowState {
                         top = fmaxf(top, fmaxf(p[i][0][h] * bf16_lo_to_float(va[i][j]), p[i][1][h] * bf16_lo_to_float(vb[i][j])));
                 }
                 top = max_over_tokens(top);
-                // sg such that the tiles' largest p s sg lies in [2^8, 2^9); what is summed already may grow by 2^30
+                // sg such that the tiles' largest p s sg lies in [2^8, 2^9), but no higher than the references' move f lets
+                // what is summed already stay where it is: sums never grow by being rescaled (a head whose reference
+                // stands still, rescaled because another one's moves, would take its sums up to infinity step by step).
+                // The powers of two keep r exact but for f itself; f of zero (the first tile, or sums far below) clears.
                 float s = sg[h];
-                if (top >= 7.888609052210118e-31f) {  // 2^-100
-                    s = __uint_as_float((262u << 23) - (__float_as_uint(top) & 0x7f800000u));
-                    if (m[h] != kNoRef) s = fminf(s, sg[h] * 1073741824.f);
-                }
-                const float r = f * (s / sg[h]);
+                if (top >= 7.888609052210118e-31f)  // 2^-100
+                    s = fminf(__uint_as_float((262u << 23) - (__float_as_uint(top) & 0x7f800000u)),
+                              __uint_as_float(__float_as_uint(sg[h] / f) & 0x7f800000u));
+                const float r = f * s / sg[h];
                 m[h] = mn, sg[h] = s, l[h] *= f;
 #pragma unroll
                 for (int j = 0; j < NG; j++) {

@@ -1,0 +1,84 @@
+"""What the 4-bit decode's sums and references have to stand: logits and values of every order."""
+import math
+
+import pytest
+import torch
+
+import kvq_ref as R
+import query_aware_sparse_kv_gb300 as qskv
+
+gpu = pytest.mark.gpu
+P = 32
+ROWS = 320  # more rows than CTAs, of at most 12 pages: a warp takes whole rows, tile after tile
+
+
+class Case:
+    """`rows` sequences over the same cached tokens k, v [T][hkv][d] (their pages are shared); q [hq][d] of all of them,
+    or [rows][hq][d]."""
+
+    def __init__(self, q, k, v, gs, rows=ROWS, dtype=torch.float32):
+        T, hkv, d = k.shape
+        self.T, self.hkv, self.d, self.gs, self.rows = T, hkv, d, gs, rows
+        n = -(-T // P)
+        pad = torch.zeros((n * P - T, hkv, d), dtype=k.dtype)
+        f = [R.quantise(torch.cat([x, pad]).unflatten(0, (n, P)).transpose(1, 2), gs) for x in (k, v)]
+        self.pool = R.pack(*f[0], *f[1])
+        # the cached values, [T][hkv][d] in 64 bits
+        self.k, self.v = (R.values(*x).transpose(1, 2).flatten(0, 1)[:T] for x in f)
+        self.q = q.expand((rows,) + q.shape[-2:]).contiguous().to(dtype)
+        self.shape = qskv.make_shape(rows, q.shape[-2], hkv, d, P, n, n)
+
+    def run(self, scale):
+        B, hq, d = self.q.shape
+        n = self.shape.max_pages
+        ws = torch.zeros(qskv.kvq_workspace_size(self.shape), dtype=torch.uint8, device="cuda")
+        out, lse = torch.full((B, hq, d), math.nan, device="cuda"), torch.full((B, hq), math.nan, device="cuda")
+        table = torch.arange(n, dtype=torch.int32).repeat(B, 1).cuda()
+        qskv.kvq_paged_decode(self.q.cuda(), self.pool.cuda(), table,
+                              torch.full((B,), self.T, dtype=torch.int32, device="cuda"), out, self.shape, self.gs, ws,
+                              lse=lse, sm_scale=scale)
+        assert qskv.get_error(ws) == 0
+        return out.cpu().double(), lse.cpu().double()
+
+    def exact(self, scale, row=0):
+        G = self.q.shape[1] // self.hkv
+        r = [R.attend(self.q[row, h * G:(h + 1) * G], self.k[:, h], self.v[:, h], scale) for h in range(self.hkv)]
+        return torch.cat([x[0] for x in r]), torch.cat([x[1] for x in r])
+
+
+def _steps(T, heads, d, logits):
+    """Queries and keys of `heads` heads of one group whose logits, in binary orders with a scale of 1, are
+    logits [heads][T]: head h reads 32 dims of d, the last 32 from head d / 32 - 1 on, which hold its logit (a bf16
+    number) in every place."""
+    q, k = torch.zeros((heads, d)), torch.zeros((T, 1, d))
+    for h in range(heads):
+        at = 32 * min(h, d // 32 - 1)
+        q[h, at:at + 32] = math.log(2) / 32
+        k[:, 0, at:at + 32] = logits[h][:, None]
+    return q, k
+
+
+@gpu
+@pytest.mark.parametrize("heads,gap,strong,late", [(2, 100, 15000.0, 30.0), (4, 100, 15000.0, 30.0), (8, 100, 15000.0, 30.0),
+                                                  (2, 105, 4e5, 1000.0), (2, 60, 30.0, 3e-5), (8, 4, 1.0, 1.0)])
+def test_a_head_keeps_its_sums_while_another_ones_logits_rise(heads, gap, strong, late):
+    """The first head has 64 tokens of values 0 and `strong`, then ones of `gap` binary orders less weight and values up to
+    `late`; the last head's logits rise by 14 orders a tile, so that the references move at every step.  The strong tokens'
+    logits are zeros, hence their weights equal."""
+    T = 12 * P
+    g = torch.Generator().manual_seed(heads + gap)
+    t = torch.arange(T)
+    logits = [torch.where(t < 64, 0, -gap).float()] + [(t // 16 * 14.0)] * (heads - 1)
+    q, k = _steps(T, heads, 128, logits)
+    v = torch.rand((T, 1, 128), generator=g)
+    v = torch.where(t[:, None, None] < 64, (v > 0.1).float() * strong, v * late)
+    c = Case(q, k, v, 32)
+    out, lse = c.run(1.0)
+    o, l = c.exact(1.0)
+    # weights of powers of two of logits that are sums of 32 equal products (off by 2^-22 of them at most), 384 tokens' sums
+    # of 2^-24 each, two fp16 halves 2^-22: all below 2^-14 of the largest value where logits reach 336, 2^-18 for the first
+    top = float(c.v.abs().max())
+    assert bool(torch.isfinite(out).all())
+    assert float((out[:, 0] - o[0]).abs().max()) <= 2.0 ** -18 * top
+    assert float((out - o).abs().max()) <= 2.0 ** -14 * top
+    assert float((lse - l).abs().max()) <= 2.0 ** -14
