@@ -75,6 +75,9 @@ constexpr int kFill = 16;          // units a warp describes at once (a multiple
 constexpr int kRowModePages = 64, kRowCtas = 16, kRowUnits = 32, kWarpUnits = 12, kWarpUnitsMany = 32;
 constexpr int kMaxRing = 8;        // stages a warp
 constexpr float kNoRef = -1e30f;   // M before the first token
+// sg before the first token whose share p s is 2^-100 or more: tokens of one value have a scale of zero and say nothing of
+// the scales to come, and on this reference any share above 2^-86 passes kTopW, so that it is fitted then.
+constexpr float kNoScale = 1.2676506002282294e30f;  // 2^100
 // Largest weight, and largest weight times value scale, in the references' units.
 constexpr float kTopP = 4096.f, kTopW = 16383.f;
 
@@ -354,7 +357,7 @@ struct RowState {
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int h = 0; h < NH; h++) {
-            m[h] = kNoRef, l[h] = 0.f, sg[h] = 1.f;
+            m[h] = kNoRef, l[h] = 0.f, sg[h] = kNoScale;
 #pragma unroll
             for (int j = 0; j < NG; j++) pm[h][j] = 0.f;
         }

@@ -82,3 +82,35 @@ def test_a_head_keeps_its_sums_while_another_ones_logits_rise(heads, gap, strong
     assert float((out[:, 0] - o[0]).abs().max()) <= 2.0 ** -18 * top
     assert float((out - o).abs().max()) <= 2.0 ** -14 * top
     assert float((lse - l).abs().max()) <= 2.0 ** -14
+
+
+def _relative(out, o):
+    """Root mean square of the errors over that of the outputs."""
+    return float((out - o).pow(2).mean().sqrt() / o.pow(2).mean().sqrt())
+
+
+# The bound on it.  A logit of order 1 is a sum of a few parts of up to about 8 (a group's scale times its codes, its minimum
+# times the query's sum) with some 24 roundings of half a step, 2^-24: 8 sqrt(24) 2^-24 = 2.3e-6 by their root mean square.
+# Weights carry that and their two halves' 2^-22; tokens' errors are independent and add up as the outputs themselves do.
+PRECISION = 2.0 ** -18
+
+
+@gpu
+@pytest.mark.parametrize("lead", [0.0, 0.5])
+@pytest.mark.parametrize("small", [1e-3, 1e-6, 1e-9])
+@pytest.mark.parametrize("d,gs,hq", [(64, 32, 2), (128, 128, 4), (128, 64, 8)])
+def test_small_values_after_tokens_of_one_value(lead, small, d, gs, hq):
+    """The first 40 tokens' values are all zero (or all a half) over the head, scales of zero; the others' are small.  With a
+    lead of a half the small values are looked at as what the outputs hold beside its share."""
+    g = torch.Generator().manual_seed(hq)
+    T = 300
+    v = torch.randn((T, 1, d), generator=g) * small
+    v[:40] = lead
+    c = Case(torch.randn((hq, d), generator=g), torch.randn((T, 1, d), generator=g), v, gs)
+    out, _ = c.run(d ** -0.5)
+    o, _ = c.exact(d ** -0.5)
+    if lead:  # an output is rounded against that share: no more than PRECISION of it
+        assert float((out - o).abs().max()) <= PRECISION * 8 * float(o.abs().max())
+    else:
+        for r in (0, ROWS // 2, ROWS - 1):
+            assert _relative(out[r], o) <= PRECISION
