@@ -391,7 +391,8 @@ qskv_status qskv_cascade_paged_decode(const void *q, qskv_dtype q_dtype, const v
  * value's word w = 4c + j of token t at place 4 (c ^ x) + j with
  * x = (t / 2) % 4 for d = 128, (t / 4) % 2 for d = 64.
  * group_size: 32, 64 or 128, at most head_dim.  Keys, values and queries must
- * be finite and below 2^60 in magnitude.
+ * be finite and below 2^60 in magnitude, and so that every logit is below
+ * 2^126 (with the default sm_scale it is).
  *
  * qskv_kvq_block_bytes: bytes of one block, page_size * (d + 8 NG)
  * (0 for an unsupported shape or group size).

@@ -74,7 +74,7 @@ constexpr int kEntries = 512;      // entries of the unit prefix held in shared 
 constexpr int kFill = 16;          // units a warp describes at once (a multiple of the units a stage)
 constexpr int kRowModePages = 64, kRowCtas = 16, kRowUnits = 32, kWarpUnits = 12, kWarpUnitsMany = 32;
 constexpr int kMaxRing = 8;        // stages a warp
-constexpr float kNoRef = -1e30f;   // M before the first token
+constexpr float kNoRef = -3e38f;   // M before the first token: below any finite logit, so that the first token moves it
 // sg before the first token whose share p s is 2^-100 or more: tokens of one value have a scale of zero and say nothing of
 // the scales to come, and on this reference any share above 2^-86 passes kTopW, so that it is fitted then.
 constexpr float kNoScale = 1.2676506002282294e30f;  // 2^100

@@ -114,3 +114,20 @@ def test_small_values_after_tokens_of_one_value(lead, small, d, gs, hq):
     else:
         for r in (0, ROWS // 2, ROWS - 1):
             assert _relative(out[r], o) <= PRECISION
+
+
+@gpu
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("power", [40, 52, 58])
+@pytest.mark.parametrize("rows,hq", [(3, 4), (ROWS, 8)])
+def test_logits_of_any_finite_size(sign, power, rows, hq):
+    """Equal keys and queries of up to 2^58: every logit the same, up to 2^122 in magnitude; the outputs are the mean."""
+    g = torch.Generator().manual_seed(power)
+    big = 2.0 ** power
+    T = 100
+    c = Case(torch.full((hq, 64), big), torch.full((T, 1, 64), sign * big), torch.randn((T, 1, 64), generator=g), 64, rows=rows)
+    out, lse = c.run(0.0)
+    o = c.v[:, 0].mean(0)
+    assert float((out - o).abs().max()) <= 2.0 ** -18 * float(c.v.abs().max())
+    l = sign * big * big * 64 / 8
+    assert float((lse - l).abs().max()) <= 2.0 ** -20 * abs(l)
