@@ -451,8 +451,11 @@ size_t qskv_kvq_workspace_size(const qskv_shape *shape);
  * else the listed ones.  Same q, page_table, seq_lens, selected, n_selected,
  * sm_scale, out (fp32) and lse, same device errors; params in slots past
  * seq_len may hold anything.  Logits, softmax sums and outputs are kept in
- * fp32 precision (queries and weights enter the matrix instructions as two
- * fp16 halves each).
+ * fp32.  Queries, and weights times value scales, enter the matrix
+ * instructions as two fp16 halves each: a query's entries are held within
+ * 2^-21 of its head's largest one, weights times scales within 2^-22 of
+ * themselves or 2^-33 of their head's largest, whichever is more (so what is
+ * small beside those has fewer bits than fp32).
  * batch * num_kv_heads * (top_k or max_pages) must be below 2^31.
  */
 qskv_status qskv_kvq_paged_decode(const void *q, qskv_dtype q_dtype, const void *pool, const int32_t *page_table,

@@ -29,7 +29,11 @@
 //     their keys' upper codes are masked out instead (one product; permuted
 //     ones with the lo half take 119 instead of 110 us at 32 x 8 rows of 8192
 //     tokens in groups of 32; fp32 queries gain: 87 instead of 92 us in groups
-//     of 128).  Outputs are within 2e-7 of fp64 over the measured cases.
+//     of 128).  Root mean square error of the outputs against fp64, as a share
+//     of theirs, over all formats, 300 and 3000 tokens: 1.4e-7 to 2.8e-7, with
+//     8 heads up to 3.4e-7 (fp32 queries) and 5.0e-7 (bf16).  What a half drops
+//     is measured against the largest entry of its head: a query with one entry
+//     4096 times the others has logits within 1.5e-6 of sum |q| (|m| + s u).
 //   * a key's words lie so that a lane's operands are one vector load; values
 //     come through ldmatrix.trans, whose 16-bit elements are four codes of one
 //     token: the pair of a register is two tokens, as the product needs.

@@ -1,4 +1,5 @@
-"""What the 4-bit decode's sums and references have to stand: logits and values of every order."""
+"""What the 4-bit decode's sums and references have to stand: logits and values of every order, and fp32 precision that a
+lost fp16 half would break."""
 import math
 
 import pytest
@@ -95,6 +96,52 @@ def _relative(out, o):
 PRECISION = 2.0 ** -18
 
 
+def _fp32(c, scale, halve_q=None, halve_w=None):
+    """The rows' outputs by plain fp32 torch; queries or weights rounded to a shorter type where one is given."""
+    G = c.q.shape[1] // c.hkv
+    outs = []
+    for h in range(c.hkv):
+        q = c.q[:, h * G:(h + 1) * G].float()
+        if halve_q is not None:
+            q = q.to(halve_q).float()
+        x = q @ c.k[:, h].float().T * scale
+        p = torch.exp(x - x.amax(-1, keepdim=True))
+        w = p if halve_w is None else p.to(halve_w).float()
+        outs.append(w @ c.v[:, h].float() / p.sum(-1, keepdim=True))
+    return torch.cat(outs, 1).double()
+
+
+def _plain_case(seed, d, gs, hq, hkv, dtype, rows=4, T=300):
+    g = torch.Generator().manual_seed(seed)
+    return Case(torch.randn((rows, hq, d), generator=g), torch.randn((T, hkv, d), generator=g),
+                torch.randn((T, hkv, d), generator=g), gs, rows=rows, dtype=dtype)
+
+
+def test_the_precision_bound_takes_fp32_and_refuses_a_lost_half():
+    c = _plain_case(1, 128, 64, 8, 2, torch.float32)
+    o = torch.stack([c.exact(128 ** -0.5, r)[0] for r in range(c.rows)])
+    assert _relative(_fp32(c, 128 ** -0.5), o) < PRECISION / 4
+    for kw in (dict(halve_q=torch.float16), dict(halve_q=torch.bfloat16), dict(halve_w=torch.float16),
+               dict(halve_w=torch.bfloat16)):
+        assert _relative(_fp32(c, 128 ** -0.5, **kw), o) > PRECISION * 8, kw
+
+
+FORMATS = [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,gs", FORMATS)
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 2), (16, 2)])
+@pytest.mark.parametrize("rows", [4, ROWS])
+def test_outputs_have_fp32_precision(dtype, d, gs, hq, hkv, rows):
+    c = _plain_case(d + gs + hq, d, gs, hq, hkv, dtype, rows=rows)
+    out, _ = c.run(d ** -0.5)
+    some = range(0, rows, max(1, rows // 8))
+    o = torch.stack([c.exact(d ** -0.5, r)[0] for r in some])
+    assert _relative(out[list(some)], o) <= PRECISION
+
+
 @gpu
 @pytest.mark.parametrize("lead", [0.0, 0.5])
 @pytest.mark.parametrize("small", [1e-3, 1e-6, 1e-9])
@@ -131,3 +178,28 @@ def test_logits_of_any_finite_size(sign, power, rows, hq):
     assert float((out - o).abs().max()) <= 2.0 ** -18 * float(c.v.abs().max())
     l = sign * big * big * 64 / 8
     assert float((lse - l).abs().max()) <= 2.0 ** -20 * abs(l)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,gs", FORMATS)
+@pytest.mark.parametrize("hq", [1, 4, 8])
+@pytest.mark.parametrize("outlier", [1, 2 ** 4, 2 ** 8, 2 ** 12])
+def test_logits_with_one_outlying_query_dim(dtype, d, gs, hq, outlier):
+    """Rows of one token: the lse is the logit itself.  One query entry is `outlier` times the others.
+
+    The largest entry is at least 2^13 / 1.07 units, every entry held as two fp16 halves within 2^-9 and 2^-14 of them (its
+    own and the one it shares a product with): 2^-21.8 of the largest.  The tensor cores cut the 16 products and the sum of
+    an instruction to 2^-23 of the largest product, at most 15 of the largest entry.  Both on codes of up to 15:
+    2^-21 max |q| sum 15 s.  The rest is fp32: 20 roundings, on partial sums of at most A = sum |q| (|m| + s u)."""
+    g = torch.Generator().manual_seed(d + gs + hq)
+    q = torch.randn((ROWS, hq, d), generator=g)
+    q[:, :, 5] *= outlier
+    k = torch.randn((1, 1, d), generator=g)
+    c = Case(q, k, torch.randn((1, 1, d), generator=g), gs, dtype=dtype)
+    _, lse = c.run(1.0)
+    u, s, m = R.quantise(k[0, 0], gs)
+    s, m = (x.repeat_interleave(gs, -1) for x in (s, m))
+    q = c.q.double()
+    tol = 2.0 ** -21 * q.abs().amax(-1) * 15 * s.sum() + 20 * 2.0 ** -24 * (q.abs() @ (m.abs() + s * u))
+    assert bool(((lse - q @ c.k[0, 0]).abs() <= tol).all())
