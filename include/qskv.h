@@ -270,8 +270,11 @@ qskv_status qskv_page_select_approx(qskv_scorer scorer, const void *q, qskv_dtyp
  * warp's single round of loads) or by a second kernel.  The per-row
  * counters are zero between calls (a zeroed workspace starts them so).
  * q, page_table and seq_lens may be read before the previous kernel in the
- * stream has completed when that kernel is one of this library's (which
- * never writes them); a kernel of the caller's is always waited for.
+ * stream has completed when that kernel lets its dependents start early, as
+ * most of this library's do.  None of those writes them; qskv_extend_tables,
+ * which writes page_table and lengths, never does so.  A kernel of the
+ * caller's that writes them must not either (griddepcontrol.launch_dependents
+ * or cudaTriggerProgrammaticLaunchCompletion); any other is waited for.
  * A sequence with no token gives out = 0 and lse = -inf.  lse may be NULL.
  * Device errors: a bad page id or selected index skips that page and flags
  * QSKV_ERR_DEVICE_INDEX.
@@ -449,7 +452,8 @@ size_t qskv_kvq_workspace_size(const qskv_shape *shape);
  * Paged decode attention over the 4-bit cache: what qskv_sparse_paged_decode
  * computes, with keys and values m + s u: all pages when selected is NULL,
  * else the listed ones.  Same q, page_table, seq_lens, selected, n_selected,
- * sm_scale, out (fp32) and lse, same device errors; params in slots past
+ * sm_scale, out (fp32) and lse, same device errors; nothing is read before
+ * the previous kernel in the stream has completed.  Params in slots past
  * seq_len may hold anything.  Logits, softmax sums and outputs are kept in
  * fp32.  Queries, and weights times value scales, enter the matrix
  * instructions as two fp16 halves each: a query's entries are held within

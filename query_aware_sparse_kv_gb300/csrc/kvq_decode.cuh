@@ -260,8 +260,15 @@ __device__ __forceinline__ Unit unit_at(const KvqDecodeArgs &a, const Shared &s,
             hi = mid;
     }
     const int heads = a.selected ? 1 : a.num_kv_heads;  // rows of a list item
+    const int last = (a.selected ? a.batch * a.num_kv_heads : a.batch) - 1;
     int i = lo * per, off = u - s.prefix[lo], n = units_of(a, i);
-    for (; off >= n * heads; n = units_of(a, i)) off -= n * heads, i++;
+    while (off >= n * heads && i < last) off -= n * heads, n = units_of(a, ++i);
+    if (off >= n * heads) {  // the lengths (or counts) became shorter while the kernel ran
+        raise_error(a.flags, a.selected ? kErrSelected : kErrSeqLen);
+        Unit r;
+        r.src = nullptr, r.row_valid = (i * heads) << 6, r.slot = 0, r.count = 1;
+        return r;
+    }
     const int g = off / n;
     return unit_of(a, i * heads + g, off - g * n, n, block_bytes);
 }
@@ -694,7 +701,8 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
     if (tid < 2 * kWarps) s.piece_row[tid] = -1;
     if (tid == 0) s.open = 0;
     mbar_fence_init();
-    if (a.selected) pdl_wait();  // the lengths may be read earlier, the selection not
+    // Nothing is read before this, the lengths neither: whoever wrote them may have let this kernel start early.
+    pdl_wait();
 
     // ---- this warp's units [u0, u1): of its CTA's row, or of all rows in order
     int u0, u1, cta_begin, cta_end;
@@ -706,7 +714,6 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
         const int rows = a.batch * a.num_kv_heads;
         u0 = 0, u1 = warp_index < rows ? (rows - warp_index + all_warps - 1) / all_warps * a.warp_units : 0;
         cta_begin = cta_end = 0;
-        if (!a.selected) pdl_wait();
     } else if (a.row_ctas) {
         count0 = units_of(a, a.selected ? row0 : row0 / a.num_kv_heads);
         upc = (count0 + a.row_ctas - 1) / a.row_ctas;
@@ -714,8 +721,6 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
         cta_begin = min(part * upc, count0), cta_end = min(cta_begin + upc, count0);
         const int n = cta_end - cta_begin;
         u0 = cta_begin + n * warp / kWarps, u1 = cta_begin + n * (warp + 1) / kWarps;
-        __syncwarp();
-        if (!a.selected) pdl_wait();
         if (count0 == 0 && part == 0) {
             const int64_t h0 = int64_t(row0 / a.num_kv_heads) * a.num_q_heads + int64_t(row0 % a.num_kv_heads) * G;
             for (int c = tid; c < G * D / 4; c += kThreads)
@@ -760,7 +765,6 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
         const int64_t c0 = int64_t(blockIdx.x) * upc;
         u0 = int(min(c0 + int64_t(warp) * upw, int64_t(total))), u1 = int(min(int64_t(u0) + upw, int64_t(total)));
         cta_begin = int(min(c0, int64_t(total))), cta_end = int(min(c0 + upc, int64_t(total)));
-        if (!a.selected) pdl_wait();
         // rows without a token or a selected page
         for (int base = blockIdx.x * kWarps + warp; base < items; base += 32 * all_warps) {
             const int64_t i = base + int64_t(lane) * all_warps;

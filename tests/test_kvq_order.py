@@ -1,0 +1,72 @@
+"""What the kernels of the 4-bit cache and the page tables read, and when: nothing before the kernel ahead has completed."""
+import glob
+import os
+import re
+
+import pytest
+import torch
+
+import query_aware_sparse_kv_gb300 as qskv
+
+CSRC = os.path.join(os.path.dirname(qskv.__file__), "csrc")
+
+
+def _kernels(path):
+    """(name, body) of every kernel of a source file, comments left out."""
+    text = re.sub(r"//[^\n]*", "", open(path).read())
+    for m in re.finditer(r"__global__[^{;]*?(\w+)\s*\([^{;]*\)\s*\{", text):
+        yield m.group(1), text[m.end():text.index("\n}", m.end())]
+
+
+@pytest.mark.parametrize("path", sorted(glob.glob(os.path.join(CSRC, "kvq_*.cu*")) + [os.path.join(CSRC, "tables.cu")]))
+def test_a_kernel_waits_before_it_reads(path):
+    for name, body in _kernels(path):
+        waits = [line.strip() for line in body.split("\n") if "pdl_wait" in line]
+        assert waits == ["pdl_wait();"], name  # one, on no condition
+        before = body[:body.index("pdl_wait();")]
+        assert not re.search(r"__ld|units_of|pages_of|seq_of|a\.\w+\s*\[|scan_requests|Request\(", before), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,pages,top_k", [(3, 200, 0), (40, 9, 0), (500, 7, 0), (2, 30, 0), (6, 300, 40)])
+def test_decode_right_behind_a_change_of_lengths_and_tables(rows, pages, top_k):
+    """Lengths and page tables (and selections) written by an ordinary kernel, the decode next in the stream: it reads the
+    new ones, longer and shorter."""
+    g = torch.Generator().manual_seed(rows)
+    d, gs, P, N = 64, 64, 16, 64
+    shape = qskv.make_shape(rows, 2, 1, d, P, pages, N)
+    pool = torch.zeros((N, 1, qskv.kvq_block_bytes(shape, gs)), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(qskv.kvq_workspace_size(shape), dtype=torch.uint8, device="cuda")
+    kv = torch.randn((N * P, 1, d), generator=g).cuda()
+    qskv.kvq_append(kv, kv, torch.arange(N * P, dtype=torch.int32, device="cuda"), pool, shape, gs, ws)
+    q = torch.randn((rows, 2, d), generator=g).cuda()
+    steps = [torch.randint(0, hi + 1, (rows,), generator=g).int().cuda() for hi in (pages * P, 16, pages * P, 1, pages * P)]
+    tables = [torch.randint(0, N, (rows, pages), generator=g).int().cuda() for _ in steps]
+    sel = torch.arange(max(top_k, 1), dtype=torch.int32, device="cuda").repeat(rows, 1, 1)
+
+    def run(lens, table, out, counts):
+        kw = dict(selected=sel, n_selected=counts, top_k=top_k) if top_k else {}
+        qskv.kvq_paged_decode(q, pool, table, lens, out, shape, gs, ws, **kw)
+
+    def counts_of(lens):
+        return ((lens + P - 1) // P).clamp(max=top_k).int()[:, None].contiguous()
+
+    want = []
+    for lens, table in zip(steps, tables):
+        n = counts_of(lens) if top_k else None
+        torch.cuda.synchronize()
+        want.append(torch.empty((rows, 2, d), device="cuda"))
+        run(lens, table, want[-1], n)
+    torch.cuda.synchronize()
+    lens, table = torch.zeros_like(steps[0]), torch.zeros_like(tables[0])
+    counts = torch.zeros((rows, 1), dtype=torch.int32, device="cuda")
+    got = [torch.empty_like(want[0]) for _ in range(4 * len(steps))]
+    for i, out in enumerate(got):
+        table.copy_(tables[i % len(steps)])
+        lens.copy_(steps[i % len(steps)])
+        if top_k:
+            counts.copy_(counts_of(lens))
+        run(lens, table, out, counts)
+    assert qskv.get_error(ws) == 0
+    for i, out in enumerate(got):
+        assert torch.equal(out, want[i % len(steps)]), i
