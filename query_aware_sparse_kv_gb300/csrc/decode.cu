@@ -426,9 +426,10 @@ __global__ void __launch_bounds__(WPC * 32, kDecodeCtasPerSm)
     }
     __syncwarp();
     if constexpr (ROWCTA) {
-        // The page table is an input no kernel of this library writes, so the
-        // row's entries are staged before the wait for the previous kernel
-        // (which ends the selection), leaving one dependent round trip
+        // No kernel that writes the page table lets this one start early (the
+        // page-table builder does not, a caller's must not), so the row's
+        // entries are staged before the wait for the previous kernel (which
+        // ends the selection), leaving one dependent round trip
         // (selected -> code) after it.
         if (a.pt_in_smem) {
             const int32_t *pt = a.page_table + int64_t(rc_row / a.num_kv_heads) * a.max_pages;

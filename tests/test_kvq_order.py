@@ -70,3 +70,46 @@ def test_decode_right_behind_a_change_of_lengths_and_tables(rows, pages, top_k):
     assert qskv.get_error(ws) == 0
     for i, out in enumerate(got):
         assert torch.equal(out, want[i % len(steps)]), i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,pages,top_k", [(2, 40, 6), (16, 40, 6), (2, 400, 16), (300, 12, 0), (4, 300, 0)])
+def test_tables_and_the_decodes_that_read_them_early(rows, pages, top_k):
+    """extend_tables and, next in the stream, a step over a bf16 cache, whose kernels may read table and lengths ahead of
+    their wait: as with the host waiting in between."""
+    g = torch.Generator().manual_seed(pages)
+    d, P, hkv = 64, 16, 2
+    N = rows * pages
+    shape = qskv.make_shape(rows, 2 * hkv, hkv, d, P, pages, N)
+    k, v = (torch.randn((N, hkv, P, d), generator=g).bfloat16().cuda() for _ in range(2))
+    q = torch.randn((rows, 2 * hkv, d), generator=g).bfloat16().cuda()
+    order = torch.randperm(N, generator=g).int()
+    new = [torch.randint(0, pages * P // 6 + 1, (rows,), generator=g).int() for _ in range(5)]
+    T = max(int(n.sum()) for n in new) + 1
+    size = max(qskv.workspace_size(shape), qskv.tables_workspace_size(shape))
+    full = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def run(wait):
+        ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+        meta = torch.zeros((N, hkv, 2, d), dtype=torch.bfloat16, device="cuda")
+        qskv.kv_meta_build(k, torch.arange(N, dtype=torch.int32, device="cuda"), full(N) + P, meta, shape, ws)
+        table, lens, other, cu, slots = torch.full_like(full(rows, pages), -1), full(rows), full(rows), full(rows + 1), full(T)
+        sel, n_sel, outs, taken, held = full(rows, hkv, max(top_k, 1)), full(rows, hkv), [], 0, torch.zeros(rows).long()
+        free, added = order.cuda(), [n.cuda() for n in new]
+        for n, a in zip(new, added):
+            qskv.extend_tables(lens, a, free[taken:], table, other, cu, slots, shape, ws)
+            lens, other = other, lens
+            if wait:
+                torch.cuda.synchronize()
+            outs.append(torch.empty((rows, 2 * hkv, d), device="cuda"))
+            if top_k:
+                qskv.select_decode(q, k, v, meta, table, lens, top_k, sel, n_sel, outs[-1], shape, ws)
+            else:
+                qskv.sparse_paged_decode(q, k, v, table, lens, outs[-1], shape, ws)
+            taken += int(((held + n + P - 1) // P - (held + P - 1) // P).sum())
+            held = held + n
+        assert qskv.get_error(ws) == 0
+        return outs
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
