@@ -217,7 +217,8 @@ class QuantizedPagedDecoder:
     attends to) and ``decode``; ``step`` does all of it.  Row lengths are
     also kept on the host, so a step never waits for the GPU.  (The lengths
     come from the host: ``extend`` cannot be captured into a graph; the calls
-    it makes can, see binding.extend_tables.)
+    it makes can, see binding.extend_tables.)  Calls may go to any streams, as
+    long as each waits for the work of the call before it.
 
     batch       rows (requests); a row of length 0 is free
     max_pages   pages a row may hold
@@ -235,7 +236,8 @@ class QuantizedPagedDecoder:
         self.pool = torch.zeros((num_pool_pages, num_kv_heads, block), dtype=torch.uint8, device=device)
         self.page_table = torch.full((batch, max_pages), -1, dtype=torch.int32, device=device)
         self.seq_lens, self._lens_out = i32(batch), i32(batch)
-        self.free_pages = torch.arange(num_pool_pages, dtype=torch.int32, device=device)
+        # ids from _taken on are free; written in place, so that no storage goes back while a stream may still read it
+        self._free, self._taken = torch.arange(num_pool_pages, dtype=torch.int32, device=device), 0
         self.cu_new, self.slot_map, self.positions = i32(batch + 1), i32(max_tokens), i32(max_tokens)
         touched = min(max_tokens, max_tokens // page_size + 2 * batch)
         self.touched_ids, self.touched_valid = i32(touched), i32(touched)
@@ -253,6 +255,11 @@ class QuantizedPagedDecoder:
 
     def _pages(self, tokens: int) -> int:
         return -(-tokens // self.shape.page_size)
+
+    @property
+    def free_pages(self) -> torch.Tensor:
+        """The pages that no row holds (a view of the list, of which ``extend`` takes the first)."""
+        return self._free[self._taken:]
 
     def extend(self, new_lens, stream=None):
         """Make room for new_lens[b] more tokens of every row b: page table,
@@ -279,7 +286,7 @@ class QuantizedPagedDecoder:
                         self.slot_map, self.shape, self.workspace, positions=self.positions,
                         touched_ids=self.touched_ids, touched_valid=self.touched_valid, stream=stream)
         self.seq_lens, self._lens_out = self._lens_out, self.seq_lens
-        self.free_pages = self.free_pages[need:]
+        self._taken += need
         self.lengths, self._new = grown, sum(new)
 
     def append(self, k: torch.Tensor, v: torch.Tensor, stream=None):
@@ -332,8 +339,9 @@ class QuantizedPagedDecoder:
         """Give a row's pages back; its length is 0 afterwards."""
         n = self._pages(self.lengths[row])
         with torch.cuda.device(self.pool.device), torch.cuda.stream(stream):
-            self.free_pages = torch.cat([self.free_pages, self.page_table[row, :n]])
+            self._free[self._taken - n:self._taken].copy_(self.page_table[row, :n])
             self.seq_lens[row] = 0
+        self._taken -= n
         self.lengths[row] = 0
 
     def check(self, stream=None):

@@ -1,0 +1,120 @@
+"""QuantizedPagedDecoder's own work, on the CPU: the library's calls replaced by records and 64-bit statements."""
+import contextlib
+
+import pytest
+import torch
+
+import kvq_ref as R
+import query_aware_sparse_kv_gb300 as qskv
+from query_aware_sparse_kv_gb300 import build, engine
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The calls a decoder makes, in order: (name, device entered, stream entered, arguments)."""
+    build.build()
+    made, device, stream = [], [], []
+
+    @contextlib.contextmanager
+    def enter(stack, what):
+        stack.append(what)
+        yield
+        stack.pop()
+
+    def record(name, fn=None):
+        def call(*args, **kw):
+            made.append((name, device[-1] if device else None, stream[-1] if stream else None, args, kw))
+            return fn(*args, **kw) if fn else None
+
+        monkeypatch.setattr(engine.B, name, call)
+
+    def tables(seq_lens, new_lens, free_pages, page_table, seq_lens_out, cu_new, slot_map, shape, workspace, positions,
+               touched_ids, touched_valid, stream=None):
+        r = R.tables(seq_lens.tolist(), new_lens.tolist(), free_pages.tolist(), page_table.tolist(), shape.page_size,
+                     shape.num_pool_pages, slot_map.numel(), touched_ids.numel())
+        for t, name in ((page_table, "page_table"), (seq_lens_out, "seq_lens_out"), (cu_new, "cu_new"),
+                        (slot_map, "slot_map"), (positions, "positions"), (touched_ids, "touched_ids"),
+                        (touched_valid, "touched_valid")):
+            t.copy_(torch.tensor(r[name], dtype=torch.int32).view(t.shape))
+
+    monkeypatch.setattr(torch.cuda, "device", lambda d: enter(device, d))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: enter(stream, s))
+    for name in ("kvq_workspace_size", "tables_workspace_size", "workspace_size"):
+        record(name, lambda shape: 256)
+    record("extend_tables", tables)
+    record("get_error", lambda *a: 0)
+    for name in ("kvq_append", "kvq_gather", "kvq_meta_build", "page_select", "kvq_paged_decode"):
+        record(name)
+    return made
+
+
+def _decoder(**kw):
+    args = dict(batch=3, num_q_heads=4, num_kv_heads=2, head_dim=64, page_size=16, max_pages=6, num_pool_pages=14,
+                max_tokens=200, device="cpu")
+    args.update(kw)
+    return qskv.QuantizedPagedDecoder(**args)
+
+
+def _tokens(n, hkv=2, d=64):
+    return torch.zeros((n, hkv, d))
+
+
+def _held(dec):
+    return [int(p) for b, n in enumerate(dec.lengths) for p in dec.page_table[b, :-(-n // 16)]]
+
+
+def test_free_pages_stay_in_one_buffer(calls):
+    """Pages given back and taken again, in many orders: always each page once, and always in the storage the decoder
+    began with (none goes back to the allocator while another stream may read it)."""
+    dec = _decoder()
+    g = torch.Generator().manual_seed(0)
+    at = dec.free_pages.untyped_storage().data_ptr()
+    for _ in range(200):
+        row = int(torch.randint(0, 3, (1,), generator=g))
+        if torch.rand((), generator=g) < 0.4:
+            dec.release(row)
+            assert dec.lengths[row] == 0 and int(dec.seq_lens[row]) == 0
+        else:
+            new = [0, 0, 0]
+            new[row] = min(int(torch.randint(0, 60, (1,), generator=g)), 96 - dec.lengths[row])
+            before = list(dec.lengths)
+            try:
+                dec.extend(new)
+            except ValueError:
+                assert dec.lengths == before
+                continue
+            dec.append(_tokens(sum(new)), _tokens(sum(new)))
+        assert dec.seq_lens.tolist() == dec.lengths
+        assert sorted(_held(dec) + dec.free_pages.tolist()) == list(range(14))
+        assert dec.free_pages.untyped_storage().data_ptr() == at
+
+
+@gpu
+def test_pages_given_back_on_a_stream_that_is_behind():
+    """release on a stream with work before it; other tensors of the list's size are made and filled on the default stream
+    meanwhile, and the pages handed out afterwards are still each another one."""
+    build.build()
+    dec = _decoder(batch=40, max_pages=2, num_pool_pages=70, device="cuda")
+    k = torch.zeros((35 * 20, 2, 64), device="cuda")
+    x = torch.randn((2048, 2048), device="cuda")
+    side = torch.cuda.Stream()
+    for rows in range(0, 35, 5):
+        new = [20 if rows <= b < rows + 5 else 0 for b in range(40)]
+        dec.extend(new)
+        dec.append(k[:100], k[:100])
+    for _ in range(3):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                x = x @ x * 1e-3
+        for b in range(5, 10):
+            dec.release(b, stream=side)
+            fill = [torch.full((n,), -5, dtype=torch.int32, device="cuda") for n in (2, 10, 60, 62, 64, 66, 70, 128)]
+        torch.cuda.current_stream().wait_stream(side)
+        assert sorted(_held(dec) + dec.free_pages.tolist()) == list(range(70))
+        dec.extend([20 if 5 <= b < 10 else 0 for b in range(40)])
+        dec.append(k[:100], k[:100])
+        dec.check()
+        assert sorted(_held(dec) + dec.free_pages.tolist()) == list(range(70)) and len(fill) == 8
