@@ -303,8 +303,9 @@ class QuantizedPagedDecoder:
 
     def select(self, q: torch.Tensor, stream=None):
         """The top_k pages of every (row, KV head) by their score bound."""
-        B.page_select(q, self.meta, self.page_table, self.seq_lens, self.top_k, self.selected, self.n_selected,
-                      self.shape, self.workspace, None, stream)
+        with torch.cuda.device(self.pool.device):
+            B.page_select(q, self.meta, self.page_table, self.seq_lens, self.top_k, self.selected, self.n_selected,
+                          self.shape, self.workspace, None, stream)
 
     def decode(self, q: torch.Tensor, out=None, lse=None, stream=None):
         """Attention of q [batch][Hq][d] over the selected (or all) pages,
@@ -346,7 +347,8 @@ class QuantizedPagedDecoder:
 
     def check(self, stream=None):
         """Raise if the device flagged an out-of-range index or a timeout."""
-        st = B.get_error(self.workspace, stream)
+        with torch.cuda.device(self.pool.device):
+            st = B.get_error(self.workspace, stream)
         if st != 0:
             raise B.QskvError(st, B.last_error_message())
 

@@ -91,6 +91,16 @@ def test_free_pages_stay_in_one_buffer(calls):
         assert dec.free_pages.untyped_storage().data_ptr() == at
 
 
+def test_calls_without_a_device_of_their_own_run_on_the_decoders(calls):
+    """The selection and the error check go to the current device: the decoder makes its own that."""
+    dec = _decoder(top_k=2)
+    dec.step(torch.zeros((3, 4, 64)), _tokens(5), _tokens(5), [2, 0, 3])
+    dec.check()
+    entered = {name: device for name, device, *_ in calls}
+    for name in ("workspace_size", "kvq_workspace_size", "tables_workspace_size", "page_select", "get_error"):
+        assert entered[name] == dec.pool.device, name
+
+
 @gpu
 def test_pages_given_back_on_a_stream_that_is_behind():
     """release on a stream with work before it; other tensors of the list's size are made and filled on the default stream
