@@ -7,6 +7,7 @@ libqskv.so's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
@@ -253,6 +254,17 @@ class QuantizedPagedDecoder:
         self.lengths = [0] * batch  # as of the last extend
         self._new = 0  # tokens of the last extend that append has not stored yet
 
+    @contextlib.contextmanager
+    def _on(self, stream):
+        """The decoder's device and `stream` (a stream object, a raw handle as the library's calls take it, or None: the
+        device's current one) for torch's own operations."""
+        device = self.pool.device
+        if stream is not None and not hasattr(stream, "cuda_stream"):
+            handle = int(stream)
+            stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+        with torch.cuda.device(device), torch.cuda.stream(stream):
+            yield
+
     def _pages(self, tokens: int) -> int:
         return -(-tokens // self.shape.page_size)
 
@@ -280,7 +292,7 @@ class QuantizedPagedDecoder:
         need = sum(self._pages(n) - self._pages(a) for a, n in zip(self.lengths, grown))
         if need > self.free_pages.numel():
             raise ValueError(f"{need} pages needed, {self.free_pages.numel()} free")
-        with torch.cuda.device(self.pool.device), torch.cuda.stream(stream):  # (stream None: the current one)
+        with self._on(stream):
             added = torch.tensor(new, dtype=torch.int32).to(self.pool.device, non_blocking=True)
         B.extend_tables(self.seq_lens, added, self.free_pages, self.page_table, self._lens_out, self.cu_new,
                         self.slot_map, self.shape, self.workspace, positions=self.positions,
@@ -328,7 +340,7 @@ class QuantizedPagedDecoder:
     def gather(self, row: int, dtype=torch.float32, stream=None):
         """The cached keys and values [length][Hkv][d] of a row."""
         P, n = self.shape.page_size, self.lengths[row]
-        with torch.cuda.device(self.pool.device), torch.cuda.stream(stream):
+        with self._on(stream):
             t = torch.arange(n, device=self.pool.device)
             slots = (self.page_table[row].long()[t // P] * P + t % P).to(torch.int32)
             k, v = (torch.empty((n, self.shape.num_kv_heads, self.shape.head_dim), dtype=dtype,
@@ -339,7 +351,7 @@ class QuantizedPagedDecoder:
     def release(self, row: int, stream=None):
         """Give a row's pages back; its length is 0 afterwards."""
         n = self._pages(self.lengths[row])
-        with torch.cuda.device(self.pool.device), torch.cuda.stream(stream):
+        with self._on(stream):
             self._free[self._taken - n:self._taken].copy_(self.page_table[row, :n])
             self.seq_lens[row] = 0
         self._taken -= n

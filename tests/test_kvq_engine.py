@@ -101,6 +101,23 @@ def test_calls_without_a_device_of_their_own_run_on_the_decoders(calls):
         assert entered[name] == dec.pool.device, name
 
 
+def test_raw_stream_handles(calls, monkeypatch):
+    """A stream as a number, as every call of the library takes it: torch's own work goes to that stream too."""
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: ("external", handle, device))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: ("default", device))
+    dec = _decoder()
+    entered = []
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: entered.append(s) or contextlib.nullcontext())
+    for handle, want in ((0x7100, ("external", 0x7100, dec.pool.device)), (0, ("default", dec.pool.device)), (None, None)):
+        del calls[:], entered[:]
+        dec.step(torch.zeros((3, 4, 64)), _tokens(5), _tokens(5), [2, 0, 3], stream=handle)
+        dec.gather(2, stream=handle)
+        dec.release(2, stream=handle)
+        assert entered == [want] * 3
+        for name, _, _, args, kw in calls:
+            assert kw.get("stream", args[-1]) == handle, name
+
+
 @gpu
 def test_pages_given_back_on_a_stream_that_is_behind():
     """release on a stream with work before it; other tensors of the list's size are made and filled on the default stream
@@ -128,3 +145,26 @@ def test_pages_given_back_on_a_stream_that_is_behind():
         dec.append(k[:100], k[:100])
         dec.check()
         assert sorted(_held(dec) + dec.free_pages.tolist()) == list(range(70)) and len(fill) == 8
+
+
+@gpu
+def test_raw_stream_handles_on_the_gpu():
+    build.build()
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn((40, 2, 64), generator=g).cuda() for _ in range(2))
+    q = torch.randn((3, 4, 64), generator=g).cuda()
+    side, outs = torch.cuda.Stream(), []
+    for stream in (None, side, side.cuda_stream, 0):
+        torch.cuda.synchronize()
+        dec = _decoder(device="cuda", top_k=2)
+        torch.cuda.synchronize()
+        dec.step(q, k, v, [25, 0, 15], stream=stream)
+        dec.release(0, stream=stream)
+        dec.step(q, k[:20], v[:20], [18, 0, 2], stream=stream)
+        got = dec.gather(0, stream=stream)
+        dec.check(stream=stream)
+        torch.cuda.synchronize()
+        outs.append((dec.out, dec.lse, *got))
+    for other in outs[1:]:
+        for x, y in zip(outs[0], other):
+            assert torch.equal(x, y)
