@@ -313,8 +313,17 @@ class QuantizedPagedDecoder:
                              self.workspace, stream)
         self._new = 0
 
+    def _check_query(self, q: torch.Tensor):
+        """Refuse what is not queries of every row, as the decode's own call does (the selection's takes any address)."""
+        B._dtype(q)
+        B._tensor("q", q, q.dtype, (self.shape.batch, self.shape.num_q_heads, self.shape.head_dim),
+                  self.pool.get_device())
+        if q.data_ptr() % 16:
+            raise ValueError("q must be 16-byte aligned")
+
     def select(self, q: torch.Tensor, stream=None):
         """The top_k pages of every (row, KV head) by their score bound."""
+        self._check_query(q)
         with torch.cuda.device(self.pool.device):
             B.page_select(q, self.meta, self.page_table, self.seq_lens, self.top_k, self.selected, self.n_selected,
                           self.shape, self.workspace, None, stream)

@@ -118,6 +118,29 @@ def test_raw_stream_handles(calls, monkeypatch):
             assert kw.get("stream", args[-1]) == handle, name
 
 
+def _bad_queries(dtype=torch.float32):
+    """Queries that a decoder of 3 rows, 4 heads of 64 dims refuses."""
+    flat = torch.zeros(3 * 4 * 64 + 1, dtype=dtype)
+    yield torch.zeros((2, 4, 64), dtype=dtype)  # not every row's
+    yield torch.zeros((3, 2, 64), dtype=dtype)
+    yield torch.zeros((3, 4, 128), dtype=dtype)
+    yield torch.zeros((3, 4, 64), dtype=torch.float16)
+    yield torch.zeros((3, 64, 4), dtype=dtype).transpose(1, 2)
+    yield flat[1:].view(3, 4, 64)  # not on 16 bytes
+    yield torch.zeros((3, 4, 64), dtype=dtype, device="meta")
+
+
+def test_the_selection_is_given_queries_of_every_row_only(calls):
+    """page_select is handed an address: shorter queries would be read past their end."""
+    dec = _decoder(top_k=2)
+    for q in _bad_queries():
+        with pytest.raises((ValueError, TypeError)):
+            dec.select(q)
+    assert "page_select" not in [c[0] for c in calls]
+    dec.select(torch.zeros((3, 4, 64), dtype=torch.bfloat16))
+    assert calls[-1][0] == "page_select"
+
+
 @gpu
 def test_pages_given_back_on_a_stream_that_is_behind():
     """release on a stream with work before it; other tensors of the list's size are made and filled on the default stream
