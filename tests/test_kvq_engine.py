@@ -127,7 +127,6 @@ def _bad_queries(dtype=torch.float32):
     yield torch.zeros((3, 4, 64), dtype=torch.float16)
     yield torch.zeros((3, 64, 4), dtype=dtype).transpose(1, 2)
     yield flat[1:].view(3, 4, 64)  # not on 16 bytes
-    yield torch.zeros((3, 4, 64), dtype=dtype, device="meta")
 
 
 def test_the_selection_is_given_queries_of_every_row_only(calls):
