@@ -339,9 +339,19 @@ class QuantizedPagedDecoder:
 
     def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, new_lens=None, stream=None):
         """One step: the rows' new tokens (one each by default) stored, then
-        the queries' attention over what the rows hold with them."""
+        the queries' attention over what the rows hold with them.  A step
+        that is refused (ValueError, TypeError, QskvError) leaves lengths,
+        pages and cache as they were."""
+        self._check_query(q)
+        lengths, taken = self.lengths, self._taken
         self.extend([1] * self.shape.batch if new_lens is None else new_lens, stream)
-        self.append(k, v, stream)
+        try:
+            self.append(k, v, stream)
+        except Exception:
+            # nothing is stored: the lengths as before, of the table only entries past them are new
+            self.seq_lens, self._lens_out = self._lens_out, self.seq_lens
+            self.lengths, self._taken, self._new = lengths, taken, 0
+            raise
         if self.top_k is not None:
             self.select(q, stream)
         self.decode(q, stream=stream)

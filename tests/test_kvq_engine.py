@@ -140,6 +140,34 @@ def test_the_selection_is_given_queries_of_every_row_only(calls):
     assert calls[-1][0] == "page_select"
 
 
+def _state(dec):
+    return (list(dec.lengths), dec.seq_lens.tolist(), dec.free_pages.tolist(),
+            [dec.page_table[b, :-(-n // 16)].tolist() for b, n in enumerate(dec.lengths)])
+
+
+def test_a_refused_step_changes_nothing(calls, monkeypatch):
+    dec = _decoder()
+    q = torch.zeros((3, 4, 64))
+    dec.step(q, _tokens(45), _tokens(45), [20, 5, 20])
+    before = _state(dec)
+    stored = len([c for c in calls if c[0] == "kvq_append"])
+    for bad in _bad_queries():
+        with pytest.raises((ValueError, TypeError)):
+            dec.step(bad, _tokens(3), _tokens(3))
+    for k, new in ((_tokens(2), None), (_tokens(4), None), (_tokens(3), [1, 1]), (_tokens(3), [-1, 1, 3]), (None, None),
+                   (_tokens(100), [100, 0, 0])):
+        with pytest.raises((ValueError, TypeError, AttributeError)):
+            dec.step(q, k, k, new)
+    with monkeypatch.context() as m:  # a refusal by the call that stores
+        m.setattr(engine.B, "kvq_append", lambda *a: (_ for _ in ()).throw(ValueError("k must be ..")))
+        with pytest.raises(ValueError, match="k must be"):
+            dec.step(q, _tokens(40), _tokens(40), [0, 30, 10])
+    assert _state(dec) == before and len([c for c in calls if c[0] == "kvq_append"]) == stored
+    dec.step(q, _tokens(40), _tokens(40), [0, 30, 10])
+    assert dec.lengths == dec.seq_lens.tolist() == [20, 35, 30]
+    assert sorted(_held(dec) + dec.free_pages.tolist()) == list(range(14))
+
+
 @gpu
 def test_pages_given_back_on_a_stream_that_is_behind():
     """release on a stream with work before it; other tensors of the list's size are made and filled on the default stream
@@ -190,3 +218,29 @@ def test_raw_stream_handles_on_the_gpu():
     for other in outs[1:]:
         for x, y in zip(outs[0], other):
             assert torch.equal(x, y)
+
+
+@gpu
+@pytest.mark.parametrize("top_k", [None, 2])
+def test_a_refused_step_changes_nothing_on_the_gpu(top_k):
+    """A decoder that was given bad steps between the good ones ends with the bits of one that was not."""
+    build.build()
+    outs = []
+    for bad in (False, True):
+        g = torch.Generator().manual_seed(4)
+        dec = _decoder(device="cuda", top_k=top_k)
+        for new in ([25, 0, 40], [1, 1, 1], [1, 17, 1]):
+            k, v = (torch.randn((sum(new), 2, 64), generator=g).cuda() for _ in range(2))
+            q = torch.randn((3, 4, 64), generator=g).cuda()
+            if bad:
+                for args in ((q[:2], k, v, new), (q.half(), k, v, new), (q, k.half(), v.half(), new), (q, k, v[:1], new),
+                             (q, k[:1], v[:1], new), (q, k.cpu(), v, new), (q, k[:, :1], v[:, :1], new),
+                             (q, k, v, [n + 200 for n in new]), (q.cpu(), k, v, new),
+                             (q, k.transpose(1, 2).contiguous().transpose(1, 2), v, new)):
+                    with pytest.raises((ValueError, TypeError)):
+                        dec.step(*args)
+            dec.step(q, k, v, new)
+            dec.check()
+        outs.append((dec.out, dec.lse, *dec.gather(0), *dec.gather(2)))
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
