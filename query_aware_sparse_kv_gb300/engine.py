@@ -230,6 +230,12 @@ class QuantizedPagedDecoder:
     def __init__(self, batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int, max_pages: int,
                  num_pool_pages: int, group_size: int = 64, top_k: Optional[int] = None, max_tokens: int = 8192,
                  sm_scale: float = 0.0, device="cuda"):
+        if top_k is not None and top_k < 1:
+            raise ValueError(f"top_k must be None (all pages) or >= 1 (got {top_k})")
+        if max_tokens < 1:
+            raise ValueError(f"max_tokens must be >= 1 (got {max_tokens})")
+        if not 0 <= sm_scale < float("inf"):
+            raise ValueError(f"sm_scale must be finite and >= 0 (got {sm_scale})")
         self.shape = B.make_shape(batch, num_q_heads, num_kv_heads, head_dim, page_size, max_pages, num_pool_pages)
         self.group_size, self.top_k, self.sm_scale, self.max_tokens = group_size, top_k, sm_scale, max_tokens
         block = B.kvq_block_bytes(self.shape, group_size)
@@ -323,6 +329,8 @@ class QuantizedPagedDecoder:
 
     def select(self, q: torch.Tensor, stream=None):
         """The top_k pages of every (row, KV head) by their score bound."""
+        if self.top_k is None:
+            raise ValueError("a decoder with top_k None attends to all pages and selects none")
         self._check_query(q)
         with torch.cuda.device(self.pool.device):
             B.page_select(q, self.meta, self.page_table, self.seq_lens, self.top_k, self.selected, self.n_selected,

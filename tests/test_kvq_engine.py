@@ -168,6 +168,19 @@ def test_a_refused_step_changes_nothing(calls, monkeypatch):
     assert sorted(_held(dec) + dec.free_pages.tolist()) == list(range(14))
 
 
+def test_arguments_that_no_step_could_run_with(calls):
+    """Refused when the decoder is made, not by a step that has stored its tokens."""
+    for bad in (dict(top_k=0), dict(top_k=-3), dict(max_tokens=0), dict(sm_scale=-1.0), dict(sm_scale=float("nan")),
+                dict(sm_scale=float("inf"))):
+        with pytest.raises(ValueError, match=list(bad)[0]):
+            _decoder(**bad)
+    for bad in (dict(group_size=48), dict(head_dim=96), dict(page_size=24), dict(batch=0), dict(num_q_heads=6)):
+        with pytest.raises(qskv.QskvError):
+            _decoder(**bad)
+    with pytest.raises(ValueError, match="selects none"):
+        _decoder(top_k=None).select(torch.zeros((3, 4, 64)))
+
+
 @gpu
 def test_pages_given_back_on_a_stream_that_is_behind():
     """release on a stream with work before it; other tensors of the list's size are made and filled on the default stream
