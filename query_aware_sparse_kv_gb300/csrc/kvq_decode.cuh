@@ -538,12 +538,14 @@ struct RowState {
                 // sg such that the tiles' largest p s sg lies in [2^8, 2^9), but no higher than the references' move f lets
                 // what is summed already stay where it is: sums never grow by being rescaled (a head whose reference
                 // stands still, rescaled because another one's moves, would take its sums up to infinity step by step).
-                // The powers of two keep r exact but for f itself; f of zero (the first tile, or sums far below) clears.
-                float s = sg[h];
+                // References are powers of two and handled by their exponents: two divisions a head here, at a row's start
+                // most of all, took 74.4 instead of 68.6 us in the ragged batch.  f is zero before 2^-126 is reached.
+                const int was = __float_as_int(sg[h]) >> 23;
+                int now = was;
                 if (top >= 7.888609052210118e-31f)  // 2^-100
-                    s = fminf(__uint_as_float((262u << 23) - (__float_as_uint(top) & 0x7f800000u)),
-                              __uint_as_float(__float_as_uint(sg[h] / f) & 0x7f800000u));
-                const float r = f * s / sg[h];
+                    now = min(262 - (__float_as_int(top) >> 23), was + int(fminf(mn - m[h], 300.f)));
+                const float s = __int_as_float(now << 23);
+                const float r = f * __int_as_float((127 + min(max(now - was, -126), 127)) << 23);
                 m[h] = mn, sg[h] = s, l[h] *= f;
 #pragma unroll
                 for (int j = 0; j < NG; j++) {
