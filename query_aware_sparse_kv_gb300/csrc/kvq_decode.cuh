@@ -77,7 +77,7 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kEntries = 512;      // entries of the unit prefix held in shared memory
 constexpr int kFill = 16;          // units a warp describes at once (a multiple of the units a stage)
 constexpr int kRowModePages = 64, kRowCtas = 16, kRowUnits = 32, kWarpUnits = 12, kWarpUnitsMany = 32;
-constexpr int kMaxRing = 8;        // stages a warp
+constexpr int kMaxRing = 3;        // stages a warp: 2 or 3 fit, by the format
 constexpr float kNoRef = -3e38f;   // M before the first token: below any finite logit, so that the first token moves it
 // sg before the first token whose share p s is 2^-100 or more: tokens of one value have a scale of zero and say nothing of
 // the scales to come, and on this reference any share above 2^-86 passes kTopW, so that it is fitted then.
@@ -1041,9 +1041,9 @@ template <int D, int NG, int HC, int P>
 cudaError_t launch_one(KvqDecodeArgs &a, int num_sms, cudaStream_t stream) {
     // a stage is about 4 KB: with fewer pages its fixed cost shows, with more the ring has too few stages
     constexpr int stage = kWarps * (4096 / (P * D)) * kvq_block_words(D, P, NG) * 4;
-    constexpr int fit = (kRingBudget - kQueryBytes<D, HC>) / stage, stages = fit < kMaxRing ? fit : kMaxRing;
+    constexpr int stages = (kRingBudget - kQueryBytes<D, HC>) / stage;
     constexpr int bytes = stages * stage + kQueryBytes<D, HC>;
-    static_assert(stages >= 2, "the ring needs two stages");
+    static_assert(stages >= 2 && stages <= kMaxRing, "the ring needs two stages, and a barrier each");
     a.stages = stages;
     const int rows = a.batch * a.num_kv_heads, slots = kvq_decode_ctas(num_sms);
     const int row_units = a.selected && a.top_k < a.max_pages ? a.top_k : a.max_pages;
