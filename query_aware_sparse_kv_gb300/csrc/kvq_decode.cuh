@@ -539,13 +539,12 @@ struct RowState {
                 // what is summed already stay where it is: sums never grow by being rescaled (a head whose reference
                 // stands still, rescaled because another one's moves, would take its sums up to infinity step by step).
                 // References are powers of two and handled by their exponents: two divisions a head here, at a row's start
-                // most of all, took 74.4 instead of 68.6 us in the ragged batch.  f is zero before 2^-126 is reached.
-                const int was = __float_as_int(sg[h]) >> 23;
-                int now = was;
-                if (top >= 7.888609052210118e-31f)  // 2^-100
-                    now = min(262 - (__float_as_int(top) >> 23), was + int(fminf(mn - m[h], 300.f)));
-                const float s = __int_as_float(now << 23);
-                const float r = f * __int_as_float((127 + min(max(now - was, -126), 127)) << 23);
+                // most of all, took 74.4 instead of 68.6 us in the ragged batch.
+                float s = sg[h];
+                if (top >= 7.888609052210118e-31f)  // 2^-100; a move of 2^128 or more sets no limit (infinity)
+                    s = fminf(__int_as_float((262 << 23) - (__float_as_int(top) & 0x7f800000)),
+                              s * __int_as_float((127 + int(fminf(mn - m[h], 128.f))) << 23));
+                const float r = f * s * __int_as_float((254 << 23) - __float_as_int(sg[h]));
                 m[h] = mn, sg[h] = s, l[h] *= f;
 #pragma unroll
                 for (int j = 0; j < NG; j++) {
@@ -1050,7 +1049,12 @@ cudaError_t launch_one(KvqDecodeArgs &a, int num_sms, cudaStream_t stream) {
     // Rows of few pages, more of them than CTAs: whole rows to warps, nothing to join (2048 rows of 7 pages: 15.3 us,
     // 28.7 split evenly; 512 rows of 1 to 32 pages: 28.0 and 19.6, so longer rows only if every warp gets one).  Rows
     // that fit one wave of CTAs and are cut about alike (selections, short tables): a group of CTAs each, which need
-    // no prefix over the lengths.  Else the even split.
+    // no prefix over the lengths (256 rows of 128 selected pages 22.7 us, 29.0 split evenly; 8 rows of 32 pages 8.5 and
+    // 10.6; longer tables are split evenly for their lengths' sake).  A CTA of the group for every 32 places: 8 rows of
+    // 32, 64, 128 pages take 8.6, 11.7, 11.7 us so, 10.6, 10.5, 10.9 with 16 places and 8.6, 10.8, 13.8 with 64; at most
+    // 16 CTAs: 8 rows of 1024 and 2048 pages take 17.0 and 24.5 us, 19.8 and 33.2 with 8, 15.0 and 21.4 with 64, which
+    // shorter rows and more of them do not tell apart.  The split goes by the table's width, the lengths being on the
+    // device: 32 rows of 7 pages take 13 us in a table of 2048 pages, 7 in one of 8.  Else the even split.
     const bool whole = rows > slots && (row_units <= kWarpUnits || (row_units <= kWarpUnitsMany && rows >= slots * kWarps));
     a.row_ctas = 0, a.warp_units = whole ? row_units : 0;
     if (rows <= slots && (a.selected || row_units <= kRowModePages)) {
