@@ -6,10 +6,11 @@
 // A thread owns one 32-bit code word (8 dims), so a bf16 row is read (or
 // written) 16 bytes a lane and the reductions over a group run over 4, 8 or 16
 // neighbouring lanes.  One GB300: 131072 tokens x 8 heads of 128 dims read
-// back to bf16 in 119 us (5.9 TB/s of 6.76 copied: HBM); 32768 tokens stored
-// in 45 us (3.8 TB/s) and the metadata of 36864 pages x 8 heads made in 115 us
-// (4.3 TB/s), both at 75 to 80 % of the issue slots with the ALU pipe at 65 to
-// 70 %: bound by the instructions a code costs.
+// back to bf16 in 118 us (6.0 TB/s of 6.76 copied: HBM); 32768 tokens stored
+// in 47 us (3.7 TB/s) and the metadata of 36864 pages x 8 heads made in 115 us
+// (4.3 TB/s), at 74 and 80 % of the issue slots with the ALU pipe at 73 %:
+// bound by the instructions a code costs, 20 in the append (about half of them
+// a word's or a group's: scale, shuffles, smallest magnitude, addresses).
 #include <cuda_fp16.h>
 
 #include "qskv_internal.h"
@@ -480,7 +481,9 @@ int64_t token_ctas(const KvqStoreArgs &a, int head_dim, int items) {
     return (int64_t(a.n_tokens) + per_cta - 1) / per_cta * 2 * a.num_kv_heads;
 }
 // 4 tokens a thread from four CTAs an SM on (one GB300 has 152): below, the loads of one token a thread already cover
-// what few CTAs there are, and the other three would only follow one another.
+// what few CTAs there are, and the other three would only follow one another.  Stored tokens of 8 heads of 128 dims, with
+// 1 and 4 a thread: 600 in 2.2 and 4.2 us, 1200 in 3.3 and 4.9, 2400 (the border) in 5.5 and 5.5, 4800 in 10.0 and 8.2,
+// 32768 in 62.7 and 46.9; read back, 600 in 1.9 and 2.4, 1200 in 2.6 and 2.3, 2400 in 3.9 and 3.0, 32768 in 49.1 and 30.9.
 constexpr int64_t kManyCtas = 608;
 
 }  // namespace

@@ -7,10 +7,13 @@
 // matrix products run on the codes u themselves and scales and minima are
 // applied per token and group, outside them.
 //
-// Bound: the SMs' instruction issue (with all pages in L2 the kernel takes as
-// long as from HBM), then HBM.  A token and head is d + 8 NG bytes, 23 bytes a
-// clock and SM at the copy rate; the arithmetic on it should fit that time,
-// which shapes the inner loop:
+// Bound: the latency of dependent instructions.  128 registers a thread leave
+// 16 warps an SM, of which 0.8 to 1.4 a scheduler can issue in a cycle: 40 to
+// 63 % of the issue slots are used, ALU 31 to 51 %, tensor cores 15 to 26 %,
+// DRAM 24 to 56 %, and waits of a fixed latency are the largest stall.  (With
+// all pages in L2 the kernel takes as long as from HBM.)  A token and head is
+// d + 8 NG bytes, 23 bytes a clock and SM at the copy rate; the arithmetic on
+// it should fit that time, which shapes the inner loop:
 //   * a code is a fp16 number almost as it stands.  Keys: one byte permutation
 //     puts a byte, two codes c0 + 16 c1, under a zero byte, the subnormal
 //     (c0 + 16 c1) 2^-24; masking the upper code off gives c0 2^-24.  The
@@ -59,9 +62,10 @@
 //
 // One GB300, GPU time: 32 sequences x 8 KV heads x 128 pages of 16 tokens, 4
 // heads a group: 22.8 us (3.2 TB/s); 4 x 65536..131072 tokens, groups of 32
-// dims: 105 us (4.8 TB/s, 71 % of the copy rate); 64 ragged sequences up to
-// 4095 tokens with 8 heads a group, fp32 queries: 69.4 us (2.2 TB/s); two
-// short rows: 5.3 us.
+// dims: 106 us (4.8 TB/s, 70 % of the copy rate); 64 ragged sequences up to
+// 4095 tokens with 8 heads a group, fp32 queries: 68.5 us (2.3 TB/s); 32 x 8
+// rows of 8192 tokens, 8 heads a group, one group of 128 dims: 80.6 us with
+// bf16 queries, 86.0 with fp32 ones (3.5 TB/s); two short rows: 5.8 us.
 #pragma once
 
 #include <cuda_fp16.h>
