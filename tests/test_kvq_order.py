@@ -14,13 +14,16 @@ CSRC = os.path.join(os.path.dirname(qskv.__file__), "csrc")
 def _kernels(path):
     """(name, body) of every kernel of a source file, comments left out."""
     text = re.sub(r"//[^\n]*", "", open(path).read())
-    for m in re.finditer(r"__global__[^{;]*?(\w+)\s*\([^{;]*\)\s*\{", text):
+    for m in re.finditer(r"__global__[^{;]*?(\w+_kernel)\s*\([^{;]*\)\s*\{", text):
         yield m.group(1), text[m.end():text.index("\n}", m.end())]
 
 
 @pytest.mark.parametrize("path", sorted(glob.glob(os.path.join(CSRC, "kvq_*.cu*")) + [os.path.join(CSRC, "tables.cu")]))
 def test_a_kernel_waits_before_it_reads(path):
-    for name, body in _kernels(path):
+    text = open(path).read()
+    kernels = list(_kernels(path))
+    assert len(kernels) == text.count("__global__")
+    for name, body in kernels:
         waits = [line.strip() for line in body.split("\n") if "pdl_wait" in line]
         assert waits == ["pdl_wait();"], name  # one, on no condition
         before = body[:body.index("pdl_wait();")]
