@@ -14,8 +14,8 @@ Numbers held in 8 bits.  The d dims x of one token and head (its key, or its val
     u = e4m3(x * 2^-e)     (to nearest, ties to even)
 and stand for u * 2^e, which bf16 and fp32 hold exactly.
 
-One (page, head) block of the pool, in bytes, P tokens:
-    [P][d] key codes | [P / 2][d][2] value codes | [P] key e + 127 | [P] value e + 127
+One (page, head) block of the pool is P / 16 parts of 16 tokens each, in bytes:
+    [16][d] key codes | [8][d][2] value codes | [16] key e + 127 | [16] value e + 127
 16-byte chunk c of a key's row t is stored at place c ^ 4 (t % 2) for d = 128, c for d = 64.  A value row holds two
 tokens, dim by dim; its 16-byte chunk c (8 dims) of token pair p is at place c ^ f, f = (p & 1) + 2 (p & 2) for d = 128
 and f = 2 (p % 4) for d = 64.
@@ -119,6 +119,11 @@ def _block_bytes(c):
     return c["page"] * (2 * c["d"] + 2)
 
 
+def _part(c, t):
+    """First byte of the part that token t of a page lies in."""
+    return t // 16 * (16 * (2 * c["d"] + 2))
+
+
 def _key_places(c, dev):
     """Byte of each dim of a key in its block: [P][d]."""
     t = torch.arange(c["page"], device=dev)[:, None]
@@ -126,16 +131,21 @@ def _key_places(c, dev):
     chunk = i // 16
     if c["d"] == 128:
         chunk = chunk ^ (4 * (t % 2))
-    return t * c["d"] + 16 * chunk + i % 16
+    return _part(c, t) + t % 16 * c["d"] + 16 * chunk + i % 16
 
 
 def _value_places(c, dev):
     """Byte of each dim of a value in its block: [P][d]."""
     t = torch.arange(c["page"], device=dev)[:, None]
     i = torch.arange(c["d"], device=dev)[None, :]
-    p = t // 2
+    p = t % 16 // 2
     f = (p & 1) + 2 * (p & 2) if c["d"] == 128 else 2 * (p % 4)
-    return c["page"] * c["d"] + p * 2 * c["d"] + 16 * ((i // 8) ^ f) + 2 * (i % 8) + t % 2
+    return _part(c, t) + 16 * c["d"] + p * 2 * c["d"] + 16 * ((i // 8) ^ f) + 2 * (i % 8) + t % 2
+
+
+def _power_places(c, t, which):
+    """Byte of the power of a key (0) or value (1) of token t of a page."""
+    return _part(c, t) + 32 * c["d"] + 16 * which + t % 16
 
 
 def _power(e):
@@ -161,7 +171,7 @@ def _values(codes, exps):
 
 def _store(c, pool, slots, k, v):
     """Tokens k, v [n][Hkv][d] into the slots of pool [Npool][Hkv][block bytes]."""
-    P, H, d = c["page"], c["hkv"], c["d"]
+    P, H = c["page"], c["hkv"]
     # a negative slot repeats the first token's store
     keep = torch.where(slots >= 0, torch.arange(len(slots), device=slots.device), 0)
     slot = slots[keep].long()
@@ -171,26 +181,25 @@ def _store(c, pool, slots, k, v):
     for which, (x, places) in enumerate(((k, _key_places), (v, _value_places))):
         codes, exps = _quantise(x[keep])
         flat[base[:, :, None] + places(c, slot.device)[t][:, None, :]] = codes
-        flat[base + (2 * P * d + which * P + t)[:, None]] = exps
+        flat[base + _power_places(c, t, which)[:, None]] = exps
 
 
 def _read(c, pool, slots, which, dtype):
     """Values [n][Hkv][d] of the slots (0 where a slot is negative)."""
-    P, H, d = c["page"], c["hkv"], c["d"]
+    P, H = c["page"], c["hkv"]
     slot = slots.clamp_min(0).long()
     t = slot % P
     base = ((slot // P * H)[:, None] + torch.arange(H, device=slot.device)) * _block_bytes(c)
     places = (_value_places if which else _key_places)(c, slot.device)
     flat = pool.view(-1)
-    x = _values(flat[base[:, :, None] + places[t][:, None, :]], flat[base + (2 * P * d + which * P + t)[:, None]])
+    x = _values(flat[base[:, :, None] + places[t][:, None, :]], flat[base + _power_places(c, t, which)[:, None]])
     return torch.where((slots >= 0)[:, None, None], x, torch.zeros_like(x)).to(dtype)
 
 
 def _unpack(c, blocks, which):
     """Blocks [..., block bytes] -> values fp32 [..., P, d] of the keys (0) or the values (1)."""
-    P, d = c["page"], c["d"]
     codes = blocks[..., (_value_places if which else _key_places)(c, blocks.device)]
-    return _values(codes, blocks[..., 2 * P * d + which * P:2 * P * d + (which + 1) * P])
+    return _values(codes, blocks[..., _power_places(c, torch.arange(c["page"], device=blocks.device), which)])
 
 
 # ------------------------------------------------------------------ inputs --
@@ -216,7 +225,7 @@ def _pool8(c, g, pages):
         for which in (0, 1):
             codes, exps = _quantise(_keys(g, n, H, P, d))
             pool[a:a + n, :, (_value_places if which else _key_places)(c, pool.device).flatten()] = codes.flatten(-2)
-            pool[a:a + n, :, 2 * P * d + which * P:2 * P * d + (which + 1) * P] = exps
+            pool[a:a + n, :, _power_places(c, torch.arange(P, device=pool.device), which)] = exps
     return pool
 
 
@@ -250,10 +259,11 @@ def _spoil(c, st, lens):
     bad = torch.arange(P, device="cuda")[None, :] >= (lens[last] % P)[:, None]  # [rows][P]
     if "pool" in st:
         b = st["pool"][page]
-        for places, at in ((_key_places, 2 * P * d), (_value_places, 2 * P * d + P)):
+        for which, places in enumerate((_key_places, _value_places)):
             x = places(c, b.device).flatten()
             b[:, :, x] = torch.where(bad[:, None, :, None], 0x7F, b[:, :, x].unflatten(-1, (P, d))).flatten(-2)
-            b[:, :, at:at + P] = torch.where(bad[:, None, :], 0xFF, b[:, :, at:at + P])
+            x = _power_places(c, torch.arange(P, device=b.device), which)
+            b[:, :, x] = torch.where(bad[:, None, :], 0xFF, b[:, :, x])
         st["pool"][page] = b
     else:
         for n in ("k_pool", "v_pool"):
@@ -514,16 +524,18 @@ def _exact_number(b):
 def _exact_block(c, raw):
     """Bytes of blocks [..., block bytes] -> keys and values, doubles [..., P, d], by the byte."""
     P, d = c["page"], c["d"]
-    dims, t = torch.arange(d, device=raw.device), torch.arange(P, device=raw.device)[:, None]
+    raw = raw.unflatten(-1, (P // 16, 32 * d + 32))  # parts of 16 tokens
+    dims, t = torch.arange(d, device=raw.device), torch.arange(16, device=raw.device)[:, None]
     if d == 128:
         key = dims % 16 + ((dims // 16 + 4 * (t % 2)) % 8) * 16
         turn = t // 2 % 2 + 4 * (t // 4 % 2)
     else:
-        key, turn = dims.expand(P, d), 2 * (t // 2 % 4)
+        key, turn = dims.expand(16, d), 2 * (t // 2 % 4)
     value = t // 2 * 2 * d + (dims // 8 ^ turn) * 16 + dims % 8 * 2 + t % 2
-    at = 2 * P * d
-    k = _exact_number(raw[..., t * d + key]) * torch.exp2(raw[..., at:at + P].double() - 127)[..., None]
-    v = _exact_number(raw[..., P * d + value]) * torch.exp2(raw[..., at + P:].double() - 127)[..., None]
+    power = torch.exp2(raw[..., 32 * d:].double() - 127)
+    k = _exact_number(raw[..., t * d + key]) * power[..., :16, None]
+    v = _exact_number(raw[..., 16 * d + value]) * power[..., 16:, None]
+    k, v = k.flatten(-3, -2), v.flatten(-3, -2)
     return k, v
 
 
