@@ -2,12 +2,12 @@
 
 Operators (Hq query heads, Hkv KV heads, G = Hq / Hkv, d = head_dim, P = page_size):
 
-  store    qskv.kv8_append, kv8_gather   new tokens' keys and values stored in 8 bits by slot, and read back as values
-  gather   qskv.kv8_gather               cached tokens read back by slot
-  meta     qskv.kv8_meta_build           element-wise min / max of a page's cached keys, for the page selection
-  decode   qskv.kv8_paged_decode         attention of one query token a sequence over its cached pages, all or a selection
+  store    qskv.kvf_append, kvf_gather   new tokens' keys and values stored in 8 bits by slot, and read back as values
+  gather   qskv.kvf_gather               cached tokens read back by slot
+  meta     qskv.kvf_meta_build           element-wise min / max of a page's cached keys, for the page selection
+  decode   qskv.kvf_paged_decode         attention of one query token a sequence over its cached pages, all or a selection
   prefill  qskv.paged_prefill,           causal attention of every sequence's newest tokens, packed one sequence after
-           qskv.kv8_paged_prefill        the other, over all that its pages hold (the new tokens among it)
+           qskv.kvf_paged_prefill        the other, over all that its pages hold (the new tokens among it)
 
 Numbers held in 8 bits.  The d dims x of one token and head (its key, or its value) are stored as
     e = the smallest whole number with max |x| <= 448 * 2^e, clamped to [-100, 119] (-100 where all are zero)
@@ -68,7 +68,7 @@ def listed():
         dict(name="prefill_long_prompt", op="prefill", cache="bf16", batch=1, hq=32, hkv=8, d=128, page=16,
              new_lo=16_384, new_hi=16_384, old_lo=0, old_hi=0, kind="prompts", dtype="bf16"),
         # prompts in chunks, over an 8-bit cache of what came before
-        dict(name="prefill_chunk_kv8", op="prefill", cache="kv8", batch=4, hq=32, hkv=8, d=128, page=32, new_lo=1024,
+        dict(name="prefill_chunk_kvf", op="prefill", cache="kvf", batch=4, hq=32, hkv=8, d=128, page=32, new_lo=1024,
              new_hi=2048, old_lo=0, old_hi=30_000, kind="prompts", dtype="bf16"),
         # a small model's prompts in fp32, no shared heads
         dict(name="prefill_mha_fp32", op="prefill", cache="fp32", batch=6, hq=16, hkv=16, d=64, page=16, new_lo=1,
@@ -103,7 +103,7 @@ def draw(rng):
         hi = _log(rng, 1, min(131_072, max(1, 2_000_000 // (batch * hkv))))
         return dict(op=op, batch=batch, hq=hkv * group, hkv=hkv, d=d, page=page, lo=rng.choice([0, 1, hi // 2]), hi=hi,
                     top_k=rng.choice([0, 0, 1, 7, 32, 128]), dtype=dtype)
-    cache = rng.choice(["bf16", "bf16", "kv8"]) if dtype == "bf16" else rng.choice(["fp32", "bf16", "kv8"])
+    cache = rng.choice(["bf16", "bf16", "kvf"]) if dtype == "bf16" else rng.choice(["fp32", "bf16", "kvf"])
     batch = _log(rng, 1, 64)
     # (query, token) pairs, all heads, that the padded batch has
     most = (3_000_000_000 if dtype == "bf16" else 400_000_000) // (batch * hkv * group)
@@ -340,7 +340,7 @@ def prepare(case, seed):
         st["page_table"], pages = _table(g, lens, P, mp)
         st["seq_lens"] = lens.to(torch.int32)
         st["cu_new"] = torch.cat([torch.zeros_like(new[:1]), torch.cumsum(new, 0)]).to(torch.int32)
-        if c["cache"] == "kv8":
+        if c["cache"] == "kvf":
             st["pool"] = _pool8(c, g, pages)
         else:
             st["k_pool"], st["v_pool"] = _pool16(c, g, pages), _pool16(c, g, pages)
@@ -356,7 +356,7 @@ def prepare(case, seed):
         st["shape"] = _qskv().make_shape(*shape)
         size = 256
         if c["op"] == "decode":
-            size = _qskv().kv8_workspace_size(st["shape"])
+            size = _qskv().kvf_workspace_size(st["shape"])
         elif c["op"] == "prefill":
             size = _qskv().prefill_workspace_size(st["shape"], len(st["q"]))
         st["workspace"] = torch.zeros(size, dtype=torch.uint8, device="cuda")
@@ -372,8 +372,8 @@ def _run_store(st):
     """Tokens stored, and read back as the values that the cache then stands for."""
     c = st["case"]
     if own:
-        _qskv().kv8_append(st["k"], st["v"], st["slots"], st["pool"], st["shape"], st["workspace"])
-        _qskv().kv8_gather(st["pool"], st["slots"], st["k_out"], st["v_out"], st["shape"], st["workspace"])
+        _qskv().kvf_append(st["k"], st["v"], st["slots"], st["pool"], st["shape"], st["workspace"])
+        _qskv().kvf_gather(st["pool"], st["slots"], st["k_out"], st["v_out"], st["shape"], st["workspace"])
         return {"k": st["k_out"], "v": st["v_out"]}
     _store(c, st["pool"], st["slots"], st["k"], st["v"])
     return _run_gather(st)
@@ -382,7 +382,7 @@ def _run_store(st):
 def _run_gather(st):
     c = st["case"]
     if own:
-        _qskv().kv8_gather(st["pool"], st["slots"], st["k_out"], st["v_out"], st["shape"], st["workspace"])
+        _qskv().kvf_gather(st["pool"], st["slots"], st["k_out"], st["v_out"], st["shape"], st["workspace"])
         return {"k": st["k_out"], "v": st["v_out"]}
     return {"k": _read(c, st["pool"], st["slots"], 0, _dtype(c)), "v": _read(c, st["pool"], st["slots"], 1, _dtype(c))}
 
@@ -390,7 +390,7 @@ def _run_gather(st):
 def _run_meta(st):
     c = st["case"]
     if own:
-        _qskv().kv8_meta_build(st["pool"], st["page_ids"], st["valid"], st["meta"], st["shape"], st["workspace"])
+        _qskv().kvf_meta_build(st["pool"], st["page_ids"], st["valid"], st["meta"], st["shape"], st["workspace"])
         return {"meta": st["meta"]}
     ids = st["page_ids"].long()
     k = _unpack(c, st["pool"][ids], 0)  # [n][Hkv][P][d]
@@ -411,7 +411,7 @@ def _softmax_times(x, v):
 def _run_decode(st):
     c = st["case"]
     if own:
-        _qskv().kv8_paged_decode(st["q"], st["pool"], st["page_table"], st["seq_lens"], st["out"], st["shape"],
+        _qskv().kvf_paged_decode(st["q"], st["pool"], st["page_table"], st["seq_lens"], st["out"], st["shape"],
                                  st["workspace"], selected=st.get("selected"), n_selected=st.get("n_selected"),
                                  top_k=c["top_k"], lse=st["lse"])
         return {"out": st["out"], "lse": st["lse"]}
@@ -439,8 +439,8 @@ def _run_decode(st):
 def _run_prefill(st):
     c = st["case"]
     if own:
-        if c["cache"] == "kv8":
-            _qskv().kv8_paged_prefill(st["q"], st["pool"], st["page_table"], st["seq_lens"], st["cu_new"], st["out"],
+        if c["cache"] == "kvf":
+            _qskv().kvf_paged_prefill(st["q"], st["pool"], st["page_table"], st["seq_lens"], st["cu_new"], st["out"],
                                       st["shape"], st["workspace"], lse=st["lse"])
         else:
             _qskv().paged_prefill(st["q"], st["k_pool"], st["v_pool"], st["page_table"], st["seq_lens"], st["cu_new"],
@@ -454,8 +454,8 @@ def _run_prefill(st):
     i = torch.arange(N, device=dev)[None, :]
     at = torch.where(cu[:-1, None] + i < cu[1:, None], cu[:-1, None] + i, T)  # T: none
     q = st["q"][at.clamp(max=T - 1)].float().view(B, N, H, G, d).transpose(1, 2).reshape(B, H, N * G, d)
-    pools = (st["pool"],) * 2 if c["cache"] == "kv8" else (st["k_pool"], st["v_pool"])
-    k, v = ((_unpack(c, p[page], w) if c["cache"] == "kv8" else p[page].float()).transpose(1, 2).flatten(2, 3)
+    pools = (st["pool"],) * 2 if c["cache"] == "kvf" else (st["k_pool"], st["v_pool"])
+    k, v = ((_unpack(c, p[page], w) if c["cache"] == "kvf" else p[page].float()).transpose(1, 2).flatten(2, 3)
             for w, p in enumerate(pools))
     t = torch.arange(k.shape[2], device=dev)
     v.masked_fill_((t >= lens[:, None])[:, None, :, None], 0.0)
@@ -494,7 +494,7 @@ def work(case):
         rows = c["batch"] * H
         return {"bytes": int(rows * read * cached + rows * 4 * (read / P) + c["batch"] * c["hq"] * (d * es + 4 * d + 4)),
                 "flops": int(4 * d * read * c["batch"] * c["hq"])}
-    if c["cache"] != "kv8":
+    if c["cache"] != "kvf":
         cached = 2 * d * (2 if c["cache"] == "bf16" else 4)
     # means over the rows' lengths (whole numbers of a range, independent of each other)
     lo, hi, old = c["new_lo"], c["new_hi"], _mean(c["old_lo"], c["old_hi"])
@@ -616,7 +616,7 @@ def _exact_prefill(c, st):
             continue
         pages = st["page_table"][b, :-(-lens[b] // P)].long()
         for h in range(H):
-            if c["cache"] == "kv8":
+            if c["cache"] == "kvf":
                 k, v = _exact_block(c, st["pool"][pages, h])
             else:
                 k, v = st["k_pool"][pages, h].double(), st["v_pool"][pages, h].double()
