@@ -468,6 +468,77 @@ qskv_status qskv_kvq_paged_decode(const void *q, qskv_dtype q_dtype, const void 
                                   float *out, float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * The 8-bit paged KV cache: keys and values of a page held as 8-bit floating
+ * point codes (e4m3: 4 exponent bits, 3 of fraction, largest value 448) with
+ * one power of two per token, head and key or value.  The dims x of a token's
+ * key (or value) of one head are held as
+ *   e = the smallest whole number with max |x| <= 448 * 2^e, clamped to
+ *       [-100, 119] (-100 where all are zero),
+ *   u = e4m3(x * 2^-e), to nearest, ties to even,
+ * and stand for u * 2^e, which fp32 and bf16 hold exactly.  Layout of the pool:
+ *   pool  [num_pool_pages][num_kv_heads][block bytes]   (16-byte aligned)
+ * where a block is page_size / 16 parts of 16 tokens each, in bytes
+ *   [16][d] key codes | [8][d][2] value codes | [16] key e + 127 | [16] value e + 127
+ * The 16-byte chunk c of the key of a part's token t is at place c ^ 4 (t % 2)
+ * of its row for d = 128, at c for d = 64.  A value row holds two tokens, dim
+ * by dim; chunk c (8 dims) of pair p = t / 2 is at place c ^ f with
+ * f = (p & 1) + 2 (p & 2) for d = 128 and f = 2 (p % 4) for d = 64.
+ * Keys, values and queries must be finite and below 2^60 in magnitude, and so
+ * that every logit is below 2^126.
+ *
+ * qskv_kvf_block_bytes: bytes of one block, page_size * (2 d + 2) (0 for an
+ * unsupported shape).
+ */
+size_t qskv_kvf_block_bytes(const qskv_shape *shape);
+
+/*
+ * Stores n_tokens new tokens into the 8-bit cache by slot: arguments, skipped
+ * places, device errors and what is unspecified as in qskv_kvq_append.
+ */
+qskv_status qskv_kvf_append(const void *k, const void *v, qskv_dtype kv_dtype, int64_t k_stride, int64_t v_stride,
+                            const int32_t *slots, int32_t n_tokens, void *pool, const qskv_shape *shape,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Reads n_tokens cached tokens back as values u * 2^e, exact in either
+ * out_dtype; zeros for a negative slot.  Otherwise as qskv_kvq_gather.
+ */
+qskv_status qskv_kvf_gather(const void *pool, const int32_t *slots, int32_t n_tokens, void *k_out, void *v_out,
+                            qskv_dtype out_dtype, const qskv_shape *shape, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/*
+ * Page metadata of the 8-bit cache, for qskv_page_select and
+ * qskv_page_select_approx (bound scorer): the element-wise min and max over a
+ * page's valid tokens of the cached key values, exact in either meta_dtype.
+ * Otherwise as qskv_kvq_meta_build.
+ */
+qskv_status qskv_kvf_meta_build(const void *pool, const int32_t *page_ids, const int32_t *valid_tokens,
+                                int32_t n_pages, void *meta, qskv_dtype meta_dtype, const qskv_shape *shape,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of qskv_kvf_paged_decode; the other qskv_kvf calls need
+ * 256, and the rules are those of qskv_kvq_workspace_size. */
+size_t qskv_kvf_workspace_size(const qskv_shape *shape);
+
+/*
+ * Paged decode attention over the 8-bit cache: what qskv_sparse_paged_decode
+ * computes, with the cached values, over all pages when selected is NULL, else
+ * the listed ones; the same arguments, device errors and order of reads as
+ * qskv_kvq_paged_decode.  What lies in slots past seq_len may be anything.
+ * Logits, softmax sums and outputs are kept in fp32.  Queries, and weights
+ * times the values' powers of two, enter the matrix instructions as two fp16
+ * halves each: a query's entries are held within 2^-22 of themselves or 2^-38
+ * of their head's largest one, weights times powers within 2^-22 of themselves
+ * or 2^-33 of their head's largest, whichever is more.
+ * batch * num_kv_heads * (top_k or max_pages) * (page_size / 16) must be below 2^31.
+ */
+qskv_status qskv_kvf_paged_decode(const void *q, qskv_dtype q_dtype, const void *pool, const int32_t *page_table,
+                                  const int32_t *seq_lens, const qskv_shape *shape, const int32_t *selected,
+                                  const int32_t *n_selected, int32_t top_k, float sm_scale, float *out, float *lse,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Page tables and slot map of one scheduler step.  Request b holds
  * seq_lens[b] tokens, whose pages page_table names, and brings new_lens[b]
  * more.  Requests are admitted in order: request b with new_lens[b] > 0 fits

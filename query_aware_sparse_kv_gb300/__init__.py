@@ -24,6 +24,9 @@ in include/qskv.h); this package is its binding:
   kvq_gather,            group of dims): tokens stored by slot, read back as
   kvq_meta_build,        values, page metadata for the selection calls, and
   kvq_paged_decode       the decode over it (all pages or selected ones)
+  kvf_append, kvf_gather,  the same for a cache in 8 bits (e4m3 codes, a
+  kvf_meta_build,            power of two per token and head)
+  kvf_paged_decode
 
 plus ``PagedDecoder`` and ``QuantizedPagedDecoder`` (buffer plumbing for a
 whole step over a bf16 / fp32 and over a 4-bit cache) and ``workloads``
@@ -31,7 +34,8 @@ whole step over a bf16 / fp32 and over a 4-bit cache) and ``workloads``
 built library every call raises.
 """
 from .binding import (QSKV_BF16, QSKV_F32, QskvError, QskvLibraryMissing, Shape, cascade_paged_decode,
-                      cascade_workspace_size, extend_tables, get_error, kv_centroid_build, kv_meta_build,
+                      cascade_workspace_size, extend_tables, get_error, kvf_append, kvf_block_bytes, kvf_gather,
+                      kvf_meta_build, kvf_paged_decode, kvf_workspace_size, kv_centroid_build, kv_meta_build,
                       kvq_append, kvq_block_bytes, kvq_gather, kvq_meta_build, kvq_paged_decode, kvq_workspace_size,
                       last_error_message, load, make_shape, page_select, page_select_approx, page_select_refresh, page_select_centroid,
                       select_decode, sparse_paged_decode, sparse_paged_decode_noalloc, tables_workspace_size,
@@ -45,4 +49,5 @@ __all__ = ["QSKV_BF16", "QSKV_F32", "QskvError", "QskvLibraryMissing", "Shape", 
            "sparse_paged_decode_noalloc", "workspace_size",
            "extend_tables", "kvq_append", "kvq_block_bytes", "kvq_gather", "kvq_meta_build", "kvq_paged_decode",
            "kvq_workspace_size", "tables_workspace_size",
+           "kvf_append", "kvf_block_bytes", "kvf_gather", "kvf_meta_build", "kvf_paged_decode", "kvf_workspace_size",
            "PagedDecoder", "QuantizedPagedDecoder", "from_inputs"]

@@ -27,8 +27,9 @@ EXPORTS = ("qskv_workspace_size", "qskv_kv_meta_build", "qskv_page_select", "qsk
            "qskv_sparse_paged_decode", "qskv_select_decode", "qskv_sparse_paged_decode_noalloc",
            "qskv_cascade_workspace_size", "qskv_cascade_paged_decode", "qskv_kvq_block_bytes", "qskv_kvq_append",
            "qskv_kvq_gather", "qskv_kvq_meta_build", "qskv_kvq_workspace_size", "qskv_kvq_paged_decode",
-           "qskv_tables_workspace_size", "qskv_extend_tables", "qskv_get_error", "qskv_status_string",
-           "qskv_last_error_message")
+           "qskv_kvf_block_bytes", "qskv_kvf_append", "qskv_kvf_gather", "qskv_kvf_meta_build",
+           "qskv_kvf_workspace_size", "qskv_kvf_paged_decode", "qskv_tables_workspace_size", "qskv_extend_tables",
+           "qskv_get_error", "qskv_status_string", "qskv_last_error_message")
 
 
 class QskvLibraryMissing(RuntimeError):
@@ -109,6 +110,19 @@ def load(path: str = LIB_PATH):
     lib.qskv_kvq_paged_decode.restype = ctypes.c_int
     lib.qskv_kvq_paged_decode.argtypes = [vp, ctypes.c_int, vp, i32p, i32p, sp, i32, i32p, i32p, i32, ctypes.c_float,
                                           f32p, f32p, vp, sz, vp]
+    lib.qskv_kvf_block_bytes.restype = sz
+    lib.qskv_kvf_block_bytes.argtypes = [sp]
+    lib.qskv_kvf_append.restype = ctypes.c_int
+    lib.qskv_kvf_append.argtypes = [vp, vp, ctypes.c_int, i64, i64, i32p, i32, vp, sp, vp, sz, vp]
+    lib.qskv_kvf_gather.restype = ctypes.c_int
+    lib.qskv_kvf_gather.argtypes = [vp, i32p, i32, vp, vp, ctypes.c_int, sp, vp, sz, vp]
+    lib.qskv_kvf_meta_build.restype = ctypes.c_int
+    lib.qskv_kvf_meta_build.argtypes = [vp, i32p, i32p, i32, vp, ctypes.c_int, sp, vp, sz, vp]
+    lib.qskv_kvf_workspace_size.restype = sz
+    lib.qskv_kvf_workspace_size.argtypes = [sp]
+    lib.qskv_kvf_paged_decode.restype = ctypes.c_int
+    lib.qskv_kvf_paged_decode.argtypes = [vp, ctypes.c_int, vp, i32p, i32p, sp, i32p, i32p, i32, ctypes.c_float, f32p,
+                                          f32p, vp, sz, vp]
     lib.qskv_tables_workspace_size.restype = sz
     lib.qskv_tables_workspace_size.argtypes = [sp]
     lib.qskv_extend_tables.restype = ctypes.c_int
@@ -290,7 +304,7 @@ def cascade_paged_decode(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Te
                                             workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
-# -- the 4-bit paged KV cache and the page tables -------------------------------
+# -- the quantised paged KV caches and the page tables --------------------------
 # These calls check what a raw pointer cannot show (device, type, shape, layout)
 # and run on the tensors' own device.
 
@@ -438,6 +452,92 @@ def kvq_paged_decode(q: torch.Tensor, pool: torch.Tensor, page_table: torch.Tens
             _tensor("out", out, torch.float32, (B, Hq, d), dev), _tensor("lse", lse, torch.float32, (B, Hq), dev),
             *_workspace(workspace, dev))
     _run(lib.qskv_kvq_paged_decode, dev, args, stream)
+
+
+def _pool8_ptr(pool: torch.Tensor, shape: Shape, index: int):
+    block = shape.page_size * (2 * shape.head_dim + 2)
+    return _tensor("pool", pool, torch.uint8, (shape.num_pool_pages, shape.num_kv_heads, block), index)
+
+
+def kvf_block_bytes(shape: Shape) -> int:
+    """Bytes of one (page, KV head) block of the 8-bit cache: the pool is
+    uint8 [num_pool_pages][num_kv_heads][kvf_block_bytes]."""
+    n = load().qskv_kvf_block_bytes(ctypes.byref(shape))
+    if n == 0:
+        raise QskvError(2, load().qskv_last_error_message().decode())
+    return int(n)
+
+
+def kvf_workspace_size(shape: Shape) -> int:
+    n = load().qskv_kvf_workspace_size(ctypes.byref(shape))
+    if n == 0:
+        raise QskvError(1, load().qskv_last_error_message().decode())
+    return int(n)
+
+
+def kvf_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor, shape: Shape,
+               workspace: torch.Tensor, stream=None):
+    """Store the tokens k, v [n][Hkv][d] (bf16 or fp32, any token stride of
+    whole 16 bytes) in 8 bits into the pool's slots [n] int32 (negative:
+    skipped)."""
+    lib = _lib or load()
+    dev = _device("pool", pool)
+    n, heads, d = slots.numel(), shape.num_kv_heads, shape.head_dim
+    kp, ks = _rows("k", k, k.dtype, n, heads, d, dev)
+    vp, vs = _rows("v", v, k.dtype, n, heads, d, dev)
+    args = (kp, vp, _dtype(k), ks, vs, _tensor("slots", slots, _I32, (n,), dev), n, _pool8_ptr(pool, shape, dev),
+            ctypes.byref(shape), *_workspace(workspace, dev))
+    _run(lib.qskv_kvf_append, dev, args, stream)
+
+
+def kvf_gather(pool: torch.Tensor, slots: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, shape: Shape,
+               workspace: torch.Tensor, stream=None):
+    """The cached tokens of `slots` [n] int32 as values, into k_out, v_out
+    [n][Hkv][d] (bf16 or fp32, exact in both; zeros for a negative slot)."""
+    lib = _lib or load()
+    dev = _device("pool", pool)
+    n = slots.numel()
+    full = (n, shape.num_kv_heads, shape.head_dim)
+    args = (_pool8_ptr(pool, shape, dev), _tensor("slots", slots, _I32, (n,), dev), n,
+            _tensor("k_out", k_out, k_out.dtype, full, dev), _tensor("v_out", v_out, k_out.dtype, full, dev),
+            _dtype(k_out), ctypes.byref(shape), *_workspace(workspace, dev))
+    _run(lib.qskv_kvf_gather, dev, args, stream)
+
+
+def kvf_meta_build(pool: torch.Tensor, page_ids: torch.Tensor, valid_tokens: torch.Tensor, meta: torch.Tensor,
+                   shape: Shape, workspace: torch.Tensor, stream=None):
+    """Min / max of the cached keys of the listed pages into meta
+    [Npool][Hkv][2][d] (fp32 or bf16, exact in both); negative ids are
+    skipped."""
+    lib = _lib or load()
+    dev = _device("pool", pool)
+    n = page_ids.numel()
+    full = (shape.num_pool_pages, shape.num_kv_heads, 2, shape.head_dim)
+    args = (_pool8_ptr(pool, shape, dev), _tensor("page_ids", page_ids, _I32, (n,), dev),
+            _tensor("valid_tokens", valid_tokens, _I32, (n,), dev), n, _tensor("meta", meta, meta.dtype, full, dev),
+            _dtype(meta), ctypes.byref(shape), *_workspace(workspace, dev))
+    _run(lib.qskv_kvf_meta_build, dev, args, stream)
+
+
+def kvf_paged_decode(q: torch.Tensor, pool: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                     out: torch.Tensor, shape: Shape, workspace: torch.Tensor,
+                     selected: Optional[torch.Tensor] = None, n_selected: Optional[torch.Tensor] = None,
+                     top_k: int = 0, lse: Optional[torch.Tensor] = None, sm_scale: float = 0.0, stream=None):
+    """sparse_paged_decode over the 8-bit cache (kvf_workspace_size bytes of
+    workspace)."""
+    lib = _lib or load()
+    dev = _device("pool", pool)
+    B, Hq, Hkv, d = shape.batch, shape.num_q_heads, shape.num_kv_heads, shape.head_dim
+    if selected is not None and n_selected is None:
+        raise ValueError("with a selected list, n_selected must be given")
+    args = (_tensor("q", q, q.dtype, (B, Hq, d), dev), _dtype(q), _pool8_ptr(pool, shape, dev),
+            _tensor("page_table", page_table, _I32, (B, shape.max_pages), dev),
+            _tensor("seq_lens", seq_lens, _I32, (B,), dev), ctypes.byref(shape),
+            _tensor("selected", selected, _I32, (B, Hkv, top_k), dev),
+            _tensor("n_selected", n_selected, _I32, (B, Hkv), dev), top_k, sm_scale,
+            _tensor("out", out, torch.float32, (B, Hq, d), dev), _tensor("lse", lse, torch.float32, (B, Hq), dev),
+            *_workspace(workspace, dev))
+    _run(lib.qskv_kvf_paged_decode, dev, args, stream)
 
 
 def extend_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, page_table: torch.Tensor,

@@ -1,0 +1,313 @@
+// Writing to, reading from and summarising the 8-bit paged KV cache (format:
+// qskv_kvf.cuh).
+//
+// All three move bytes: append reads 2 d elements a token and head and writes
+// 2 d + 2 bytes, gather does the reverse, the metadata build reads the keys'
+// d + 1 bytes a token and writes 2 d elements a page.  A thread of append and
+// gather owns 8 dims, so a bf16 row is read (or written) 16 bytes a lane and a
+// token's largest magnitude is found over d / 8 neighbouring lanes.
+#include "qskv_internal.h"
+#include "qskv_kvf.cuh"
+
+#include <cuda_fp16.h>
+
+namespace qskv {
+namespace {
+
+constexpr int kCacheThreads = 256;
+
+// The 8 values of a thread as loaded, and as floats.
+template <bool BF16>
+struct Raw8 {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const void *base, int64_t at) {
+        if constexpr (BF16) {
+            a = ldg_stream_v4(static_cast<const uint16_t *>(base) + at);
+        } else {
+            a = ldg_stream_v4(static_cast<const float *>(base) + at);
+            b = ldg_stream_v4(static_cast<const float *>(base) + at + 4);
+        }
+    }
+    // Largest magnitude, as the bits of a float.
+    __device__ __forceinline__ uint32_t top() const {
+        constexpr uint32_t abs2 = 0x7fff7fffu, abs1 = 0x7fffffffu;
+        if constexpr (BF16) {  // magnitudes order as their bits do
+            const uint32_t r = __vmaxu2(__vmaxu2(a.x & abs2, a.y & abs2), __vmaxu2(a.z & abs2, a.w & abs2));
+            return max(r & 0xffff0000u, r << 16);
+        } else {
+            return max(max(max(a.x & abs1, a.y & abs1), max(a.z & abs1, a.w & abs1)),
+                       max(max(b.x & abs1, b.y & abs1), max(b.z & abs1, b.w & abs1)));
+        }
+    }
+    __device__ __forceinline__ void floats(float (&x)[8]) const {
+        if constexpr (BF16) {
+            const uint32_t r[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) x[2 * i] = bf16_lo_to_float(r[i]), x[2 * i + 1] = bf16_hi_to_float(r[i]);
+        } else {
+            const uint32_t r[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 8; i++) x[i] = __uint_as_float(r[i]);
+        }
+    }
+};
+
+// e + 127 for the largest magnitude `top` (bits): 448 is 1.75 2^8.
+__device__ __forceinline__ int kvf_exponent(uint32_t top) {
+    const int e = int(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u);
+    return min(max(e, 127 + kKvfLowExp), 127 + kKvfHighExp);
+}
+
+// Four codes of x times `up` (a power of two), byte i from x[i].
+__device__ __forceinline__ uint32_t kvf_codes(const float *x, float up) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1] * up), "f"(x[0] * up));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3] * up), "f"(x[2] * up));
+    return uint32_t(lo) | uint32_t(hi) << 16;
+}
+
+// First byte of the part that a slot lies in, for one head.
+template <int D>
+__device__ __forceinline__ int64_t part_at(int slot, int page_size, int num_kv_heads, int head) {
+    const int shift = page_size == 16 ? 4 : 5, parts = page_size >> 4;
+    return ((int64_t(slot >> shift) * num_kv_heads + head) * parts + ((slot & (page_size - 1)) >> 4)) * kvf_part_bytes(D);
+}
+
+// A thread takes its 8 dims of ITEMS tokens that follow one another: where two
+// of them are a pair of the cache (a run of tokens goes to slots in order) the
+// value codes of both leave as one 16-byte store; a token without its other
+// one in the same thread is stored byte by byte.
+template <bool BF16, int D, int ITEMS>
+__global__ void __launch_bounds__(kCacheThreads) kvf_append_kernel(KvfStoreArgs a) {
+    constexpr int W = D / 8, TPB = kCacheThreads / W;
+    pdl_trigger();
+    pdl_wait();
+    const int per_chunk = 2 * a.num_kv_heads;
+    const int chunk = blockIdx.x / per_chunk, y = blockIdx.x % per_chunk;
+    const int which = y >= a.num_kv_heads, head = which ? y - a.num_kv_heads : y;
+    const int w = threadIdx.x % W, token0 = (chunk * TPB + threadIdx.x / W) * ITEMS;
+    const void *src = which ? a.v : a.k;
+    const int64_t stride = which ? a.v_stride : a.k_stride, col = head * D + w * 8;
+    Raw8<BF16> raw[ITEMS];
+    int slot[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; i++) {
+        const int t = token0 + i, in = min(t, a.n_tokens - 1);
+        slot[i] = t < a.n_tokens ? __ldg(a.slots + in) : -1;
+        raw[i].load(src, in * stride + col);
+    }
+    uint2 codes[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; i++) {
+        uint32_t top = raw[i].top();
+#pragma unroll
+        for (int o = 1; o < W; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int e = kvf_exponent(top);
+        const float up = kvf_power(254 - e);
+        float x[8];
+        raw[i].floats(x);
+        codes[i] = make_uint2(kvf_codes(x, up), kvf_codes(x + 4, up));
+        if (slot[i] >= a.num_pool_pages * int64_t(a.page_size)) {
+            if (w == 0) raise_error(a.flags, kErrPageId);
+            slot[i] = -1;
+        }
+        if (slot[i] < 0) continue;
+        uint8_t *part = a.pool + part_at<D>(slot[i], a.page_size, a.num_kv_heads, head);
+        const int t = slot[i] & 15;
+        if (w == 0) part[32 * D + 16 * which + t] = uint8_t(e);
+        if (!which)
+            *reinterpret_cast<uint2 *>(part + t * D + kvf_key_chunk<D>(w >> 1, t) * 16 + (w & 1) * 8) = codes[i];
+    }
+    if (!which) return;
+    bool taken = false;  // the token before this one was stored together with it
+#pragma unroll
+    for (int i = 0; i < ITEMS; i++) {
+        if (slot[i] < 0 || taken) {
+            taken = false;
+            continue;
+        }
+        const int t = slot[i] & 15, p = t >> 1;
+        uint8_t *to = a.pool + part_at<D>(slot[i], a.page_size, a.num_kv_heads, head) + 16 * D + p * 2 * D +
+                      kvf_value_chunk<D>(w, p) * 16;
+        if (i + 1 < ITEMS && !(t & 1) && slot[i + 1 < ITEMS ? i + 1 : i] == slot[i] + 1) {
+            const uint2 x = codes[i], y = codes[i + 1 < ITEMS ? i + 1 : i];
+            *reinterpret_cast<uint4 *>(to) = make_uint4(__byte_perm(x.x, y.x, 0x5140), __byte_perm(x.x, y.x, 0x7362),
+                                                        __byte_perm(x.y, y.y, 0x5140), __byte_perm(x.y, y.y, 0x7362));
+            taken = true;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                to[2 * k + (t & 1)] = uint8_t(codes[i].x >> (8 * k));
+                to[8 + 2 * k + (t & 1)] = uint8_t(codes[i].y >> (8 * k));
+            }
+        }
+    }
+}
+
+// The values u 2^e of 8 codes.
+__device__ __forceinline__ void kvf_values(uint2 codes, float power, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t h = kvf_half2((i & 2 ? codes.y : codes.x) >> (16 * (i & 1)));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        x[2 * i] = f.x * power, x[2 * i + 1] = f.y * power;
+    }
+}
+
+template <bool BF16, int D, int ITEMS>
+__global__ void __launch_bounds__(kCacheThreads) kvf_gather_kernel(KvfStoreArgs a) {
+    constexpr int W = D / 8, TPB = kCacheThreads / W;
+    pdl_trigger();
+    pdl_wait();
+    const int per_chunk = 2 * a.num_kv_heads;
+    const int chunk = blockIdx.x / per_chunk, y = blockIdx.x % per_chunk;
+    const int which = y >= a.num_kv_heads, head = which ? y - a.num_kv_heads : y;
+    const int w = threadIdx.x % W, token0 = (chunk * TPB + threadIdx.x / W) * ITEMS;
+    int slot[ITEMS];
+    uint2 codes[ITEMS];
+    uint32_t e[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; i++) slot[i] = token0 + i < a.n_tokens ? __ldg(a.slots + token0 + i) : -1;
+#pragma unroll
+    for (int i = 0; i < ITEMS; i++) {
+        codes[i] = make_uint2(0, 0), e[i] = 127;
+        if (slot[i] >= a.num_pool_pages * int64_t(a.page_size)) {
+            if (w == 0) raise_error(a.flags, kErrPageId);
+            continue;
+        }
+        if (slot[i] < 0) continue;
+        const uint8_t *part = a.pool + part_at<D>(slot[i], a.page_size, a.num_kv_heads, head);
+        const int t = slot[i] & 15, p = t >> 1;
+        e[i] = __ldg(part + 32 * D + 16 * which + t);
+        if (which) {
+            const uint4 x =
+                __ldg(reinterpret_cast<const uint4 *>(part + 16 * D + p * 2 * D + kvf_value_chunk<D>(w, p) * 16));
+            const uint32_t pick = t & 1 ? 0x7531 : 0x6420;
+            codes[i] = make_uint2(__byte_perm(x.x, x.y, pick), __byte_perm(x.z, x.w, pick));
+        } else {
+            codes[i] = __ldg(reinterpret_cast<const uint2 *>(part + t * D + kvf_key_chunk<D>(w >> 1, t) * 16 + (w & 1) * 8));
+        }
+    }
+    void *out = which ? a.v_out : a.k_out;
+#pragma unroll
+    for (int i = 0; i < ITEMS; i++) {
+        if (token0 + i >= a.n_tokens) break;
+        float x[8];
+        kvf_values(codes[i], kvf_power(e[i]), x);
+        const int64_t at = (int64_t(token0 + i) * a.num_kv_heads + head) * D + w * 8;
+        if constexpr (BF16) {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) =
+                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                           pack_bf16x2(x[6], x[7]));
+        } else {
+            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
+            o[0] = make_float4(x[0], x[1], x[2], x[3]);
+            o[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
+    }
+}
+
+// A lane group of D / 4 lanes takes a (listed page, KV head) tile, a lane four
+// dims of all its tokens: nothing is combined across lanes, and the loads of
+// 16 tokens are in flight together.
+constexpr int kMetaThreads = 128;
+
+template <bool BF16, int D>
+__global__ void __launch_bounds__(kMetaThreads) kvf_meta_kernel(KvfMetaArgs a) {
+    constexpr int L = D / 4;
+    pdl_trigger();
+    pdl_wait();
+    const int64_t tile = (int64_t(blockIdx.x) * kMetaThreads + threadIdx.x) / L;
+    const int w = threadIdx.x % L, P = a.page_size;
+    if (tile >= int64_t(a.n_list) * a.num_kv_heads) return;
+    const int e = int(tile / a.num_kv_heads), g = int(tile - int64_t(e) * a.num_kv_heads);
+    const int p = __ldg(a.page_ids + e), valid = __ldg(a.valid_tokens + e);
+    if (p < 0) return;
+    if (p >= a.num_pool_pages || valid < 1 || valid > P) {
+        if (w == 0) raise_error(a.flags, p >= a.num_pool_pages ? kErrPageId : kErrValid);
+        return;
+    }
+    const int64_t row = int64_t(p) * a.num_kv_heads + g;
+    const uint8_t *block = a.pool + row * (P >> 4) * kvf_part_bytes(D);
+    float mn[4], mx[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) mn[k] = INFINITY, mx[k] = -INFINITY;
+    for (int c = 0; c < valid; c += 16) {
+        const uint8_t *part = block + (c >> 4) * kvf_part_bytes(D);
+        const uint4 powers = __ldg(reinterpret_cast<const uint4 *>(part + 32 * D));
+        uint32_t codes[16];
+#pragma unroll
+        for (int t = 0; t < 16; t++)  // a token past the end repeats the first
+            codes[t] = __ldg(reinterpret_cast<const uint32_t *>(
+                part + (c + t < valid ? t * D + kvf_key_chunk<D>(w >> 2, t) * 16 : kvf_key_chunk<D>(w >> 2, 0) * 16) + (w & 3) * 4));
+#pragma unroll
+        for (int t = 0; t < 16; t++) {
+            const uint32_t four = t < 4 ? powers.x : t < 8 ? powers.y : t < 12 ? powers.z : powers.w;
+            const float power = kvf_power(c + t < valid ? (four >> (8 * (t & 3))) & 255 : powers.x & 255);
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint32_t x2 = kvf_half2(codes[t] >> (16 * h));
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x2));
+                const float x = f.x * power, y = f.y * power;
+                mn[2 * h] = fminf(mn[2 * h], x), mx[2 * h] = fmaxf(mx[2 * h], x);
+                mn[2 * h + 1] = fminf(mn[2 * h + 1], y), mx[2 * h + 1] = fmaxf(mx[2 * h + 1], y);
+            }
+        }
+    }
+    const int64_t to = row * 2 * D + w * 4;
+    if constexpr (BF16) {  // exact: a value has 4 significant bits
+        uint16_t *o = static_cast<uint16_t *>(a.meta) + to;
+        *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16x2(mn[0], mn[1]), pack_bf16x2(mn[2], mn[3]));
+        *reinterpret_cast<uint2 *>(o + D) = make_uint2(pack_bf16x2(mx[0], mx[1]), pack_bf16x2(mx[2], mx[3]));
+    } else {
+        float *o = static_cast<float *>(a.meta) + to;
+        *reinterpret_cast<float4 *>(o) = make_float4(mn[0], mn[1], mn[2], mn[3]);
+        *reinterpret_cast<float4 *>(o + D) = make_float4(mx[0], mx[1], mx[2], mx[3]);
+    }
+}
+
+// CTAs of `items` tokens a thread.
+int64_t token_ctas(const KvfStoreArgs &a, int head_dim, int items) {
+    const int per_cta = kCacheThreads / (head_dim / 8) * items;
+    return (int64_t(a.n_tokens) + per_cta - 1) / per_cta * 2 * a.num_kv_heads;
+}
+constexpr int kItems = 8;
+constexpr int64_t kManyCtas = 608;
+
+}  // namespace
+
+#define KVF_TOKENS(kernel)                                                                                      \
+    const bool bf16 = dtype == kDtypeBf16, many = token_ctas(a, head_dim, kItems) >= kManyCtas;                 \
+    const dim3 grid(unsigned(token_ctas(a, head_dim, many ? kItems : 1))), block(kCacheThreads);                \
+    if (head_dim == 128) {                                                                                      \
+        if (many) return bf16 ? launch_pdl(kernel<true, 128, kItems>, grid, block, 0, stream, a)                \
+                              : launch_pdl(kernel<false, 128, kItems>, grid, block, 0, stream, a);              \
+        return bf16 ? launch_pdl(kernel<true, 128, 1>, grid, block, 0, stream, a)                               \
+                    : launch_pdl(kernel<false, 128, 1>, grid, block, 0, stream, a);                             \
+    }                                                                                                           \
+    if (many) return bf16 ? launch_pdl(kernel<true, 64, kItems>, grid, block, 0, stream, a)                     \
+                          : launch_pdl(kernel<false, 64, kItems>, grid, block, 0, stream, a);                   \
+    return bf16 ? launch_pdl(kernel<true, 64, 1>, grid, block, 0, stream, a)                                    \
+                : launch_pdl(kernel<false, 64, 1>, grid, block, 0, stream, a);
+
+cudaError_t launch_kvf_append(const KvfStoreArgs &a, int dtype, int head_dim, cudaStream_t stream) {
+    KVF_TOKENS(kvf_append_kernel)
+}
+
+cudaError_t launch_kvf_gather(const KvfStoreArgs &a, int dtype, int head_dim, cudaStream_t stream) {
+    KVF_TOKENS(kvf_gather_kernel)
+}
+
+cudaError_t launch_kvf_meta(const KvfMetaArgs &a, int meta_dtype, int head_dim, int, cudaStream_t stream) {
+    const bool bf16 = meta_dtype == kDtypeBf16;
+    const int per_cta = kMetaThreads / (head_dim / 4);
+    const int64_t tiles = int64_t(a.n_list) * a.num_kv_heads;
+    const dim3 grid(unsigned((tiles + per_cta - 1) / per_cta)), block(kMetaThreads);
+    if (head_dim == 128)
+        return bf16 ? launch_pdl(kvf_meta_kernel<true, 128>, grid, block, 0, stream, a)
+                    : launch_pdl(kvf_meta_kernel<false, 128>, grid, block, 0, stream, a);
+    return bf16 ? launch_pdl(kvf_meta_kernel<true, 64>, grid, block, 0, stream, a)
+                : launch_pdl(kvf_meta_kernel<false, 64>, grid, block, 0, stream, a);
+}
+
+}  // namespace qskv

@@ -192,20 +192,21 @@ __device__ __forceinline__ int seq_of(const KvqDecodeArgs &a, int b) {
 __device__ __forceinline__ int pages_of(const KvqDecodeArgs &a, int b) {
     return (seq_of(a, b) + a.page_size - 1) / a.page_size;
 }
-// Units of list item i: a row's selected pages, or all pages of a sequence
-// (of one of its KV heads).
+// Units of list item i: those of a row's selected pages, or of all pages of a
+// sequence (of one of its KV heads).  A format F cuts a page into F::SUB units.
+template <class F>
 __device__ __forceinline__ int units_of(const KvqDecodeArgs &a, int i) {
-    if (!a.selected) return pages_of(a, i);
+    if (!a.selected) return pages_of(a, i) * F::SUB;
     const int n = __ldg(a.n_selected + i), lim = min(a.top_k, pages_of(a, i / a.num_kv_heads));
     if (n < 0 || n > lim) {
         raise_error(a.flags, kErrSelected);
-        return max(0, min(n, lim));
+        return max(0, min(n, lim)) * F::SUB;
     }
-    return n;
+    return n * F::SUB;
 }
 
 struct Unit {
-    const uint8_t *src;  // its block; nullptr: skipped
+    const uint8_t *src;  // its bytes; nullptr: skipped
     int row_valid;       // row << 6 | valid tokens
     int slot, count;     // its place among the row's units, and how many those are
 };
@@ -224,37 +225,42 @@ struct Shared {
 };
 
 // The unit of row `row` at place `slot` of `count`.
-__device__ __forceinline__ Unit unit_of(const KvqDecodeArgs &a, int row, int slot, int count, uint32_t block_bytes) {
+template <class F>
+__device__ __forceinline__ Unit unit_of(const KvqDecodeArgs &a, int row, int slot, int count) {
     const int b = row / a.num_kv_heads, seq = seq_of(a, b);
-    const int j = a.selected ? __ldg(a.selected + int64_t(row) * a.top_k + slot) : slot;
+    const int j = a.selected ? __ldg(a.selected + int64_t(row) * a.top_k + slot / F::SUB) : slot / F::SUB;
     Unit r;
     r.src = nullptr, r.row_valid = row << 6, r.slot = slot, r.count = count;
     if (j < 0 || j * int64_t(a.page_size) >= seq) {
         raise_error(a.flags, kErrSelected);
         return r;
     }
+    const int valid = min(F::TOKENS, seq - j * a.page_size - slot % F::SUB * F::TOKENS);
+    if (F::SUB > 1 && valid <= 0) return r;
     const int p = __ldg(a.page_table + int64_t(b) * a.max_pages + j);
     if (p < 0 || p >= a.num_pool_pages) {
         raise_error(a.flags, kErrPageId);
         return r;
     }
-    r.src = reinterpret_cast<const uint8_t *>(a.pool) + (int64_t(p) * a.num_kv_heads + row % a.num_kv_heads) * block_bytes;
-    r.row_valid |= min(a.page_size, seq - j * a.page_size);
+    r.src = reinterpret_cast<const uint8_t *>(a.pool) +
+            ((int64_t(p) * a.num_kv_heads + row % a.num_kv_heads) * F::SUB + slot % F::SUB) * F::BYTES;
+    r.row_valid |= valid;
     return r;
 }
 
 // The unit of row `row` at place `slot` of the `row_units` places a row has at
 // most (rows to warps): empty past the row's end.
-__device__ __forceinline__ Unit place_of(const KvqDecodeArgs &a, int row, int slot, int row_units, uint32_t block_bytes) {
-    if (slot < units_of(a, a.selected ? row : row / a.num_kv_heads)) return unit_of(a, row, slot, row_units, block_bytes);
+template <class F>
+__device__ __forceinline__ Unit place_of(const KvqDecodeArgs &a, int row, int slot, int row_units) {
+    if (slot < units_of<F>(a, a.selected ? row : row / a.num_kv_heads)) return unit_of<F>(a, row, slot, row_units);
     Unit r;
     r.src = nullptr, r.row_valid = row << 6, r.slot = slot, r.count = row_units;
     return r;
 }
 
 // The unit with global index u (even split).
-__device__ __forceinline__ Unit unit_at(const KvqDecodeArgs &a, const Shared &s, int entries, int per, int u,
-                                        uint32_t block_bytes) {
+template <class F>
+__device__ __forceinline__ Unit unit_at(const KvqDecodeArgs &a, const Shared &s, int entries, int per, int u) {
     int lo = 0, hi = entries;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -265,8 +271,8 @@ __device__ __forceinline__ Unit unit_at(const KvqDecodeArgs &a, const Shared &s,
     }
     const int heads = a.selected ? 1 : a.num_kv_heads;  // rows of a list item
     const int last = (a.selected ? a.batch * a.num_kv_heads : a.batch) - 1;
-    int i = lo * per, off = u - s.prefix[lo], n = units_of(a, i);
-    while (off >= n * heads && i < last) off -= n * heads, n = units_of(a, ++i);
+    int i = lo * per, off = u - s.prefix[lo], n = units_of<F>(a, i);
+    while (off >= n * heads && i < last) off -= n * heads, n = units_of<F>(a, ++i);
     if (off >= n * heads) {  // the lengths (or counts) became shorter while the kernel ran
         raise_error(a.flags, a.selected ? kErrSelected : kErrSeqLen);
         Unit r;
@@ -274,7 +280,7 @@ __device__ __forceinline__ Unit unit_at(const KvqDecodeArgs &a, const Shared &s,
         return r;
     }
     const int g = off / n;
-    return unit_of(a, i * heads + g, off - g * n, n, block_bytes);
+    return unit_of<F>(a, i * heads + g, off - g * n, n);
 }
 
 // ----------------------------------------------------- one row in a warp --
@@ -287,6 +293,7 @@ struct RowState {
     static constexpr int NH = HC / 4;     // heads a lane
     uint32_t qh[NW][4];
     uint4 *ql;  // HC = 8: the lo halves' fragments, in the warp's shared memory ([NW][32 lanes]): registers are short
+    __device__ __forceinline__ void attach(uint8_t *mem, int warp) { ql = reinterpret_cast<uint4 *>(mem) + warp * (NW * 32); }
     float qa[NH], qb[NH][NG];
     float m[NH], l[NH], sg[NH], pm[NH][NG];
     bool q_lo;  // HC = 8: the queries have lo halves (fp32 ones; bf16 fits fp16 as it is, half the products)
@@ -690,16 +697,31 @@ struct RowState {
     }
 };
 
+// What the kernel below has to know of a cache's format: its tokens and bytes
+// a unit, units a page and units a stage of the ring, the state of a row, that
+// state's own shared memory, whether two tiles of a stage may go through it
+// together, and from how many units a row the work is split which way.
+template <int D_, int NG, int HC, int P>
+struct KvqFormat {
+    using State = RowState<D_, NG, HC, P>;
+    static constexpr int D = D_, TOKENS = P, SUB = 1, BYTES = kvq_block_words(D, P, NG) * 4;
+    static constexpr int U = 4096 / (P * D);  // a stage is about 4 KB: with fewer pages its fixed cost shows, with more the ring has too few stages
+    static constexpr int STATE_BYTES = HC == 8 ? kWarps * D * 16 : 0;  // the lo halves of 8 heads
+    // Two tiles a step share the vote and hide each other's latencies, where the registers suffice: with 8 heads only
+    // for one group a row (32 x 8 rows of 8192 tokens: 84 us, 89 tile by tile; a ragged batch with two groups 77 and 74).
+    static constexpr bool PAIRS = HC == 4 || NG == 1;
+};
+
 // --------------------------------------------------------- the kernel --
-template <int D, int NG, int HC, int P>
+template <class F>
 __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a) {
     extern __shared__ __align__(128) uint8_t ring_mem[];
     __shared__ Shared s;
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int U = 4096 / (P * D), kPageTiles = P / 16, kTiles = U * kPageTiles;
-    constexpr uint32_t block_bytes = kvq_block_words(D, P, NG) * 4;
-    static_assert(U >= 1 && kFill % U == 0, "a stage is a whole number of pages, a fill of stages");
+    constexpr int D = F::D, U = F::U, kPageTiles = F::TOKENS / 16, kTiles = U * kPageTiles;
+    constexpr uint32_t block_bytes = F::BYTES;
+    static_assert(U >= 1 && kFill % U == 0, "a stage is a whole number of units, a fill of stages");
     const int G = a.group, S = a.stages;
     uint8_t *ring = ring_mem + warp * (S * U * block_bytes);
     if (lane < S) mbar_init(&s.bar[warp][lane], 1);
@@ -720,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
         u0 = 0, u1 = warp_index < rows ? (rows - warp_index + all_warps - 1) / all_warps * a.warp_units : 0;
         cta_begin = cta_end = 0;
     } else if (a.row_ctas) {
-        count0 = units_of(a, a.selected ? row0 : row0 / a.num_kv_heads);
+        count0 = units_of<F>(a, a.selected ? row0 : row0 / a.num_kv_heads);
         upc = (count0 + a.row_ctas - 1) / a.row_ctas;
         const int part = blockIdx.x - row0 * a.row_ctas;
         cta_begin = min(part * upc, count0), cta_end = min(cta_begin + upc, count0);
@@ -741,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
         int mine = 0;
         for (int e = tid * ept; e < min((tid + 1) * ept, entries); e++) {
             int n = 0;
-            for (int i = e * per; i < min((e + 1) * per, items); i++) n += units_of(a, i) * heads;
+            for (int i = e * per; i < min((e + 1) * per, items); i++) n += units_of<F>(a, i) * heads;
             s.prefix[e] = n;
             mine += n;
         }
@@ -773,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
         // rows without a token or a selected page
         for (int base = blockIdx.x * kWarps + warp; base < items; base += 32 * all_warps) {
             const int64_t i = base + int64_t(lane) * all_warps;
-            uint32_t none = __ballot_sync(0xffffffffu, i < items && units_of(a, int(i)) == 0);
+            uint32_t none = __ballot_sync(0xffffffffu, i < items && units_of<F>(a, int(i)) == 0);
             while (none) {
                 const int k = __ffs(none) - 1;
                 none &= none - 1;
@@ -792,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
     const int n = u1 - u0, stages = (n + U - 1) / U;
     int put = 0, got = 0, parity = 0;
     const uint64_t policy = l2_evict_first_policy();
-    uint32_t plain = 0;  // bit per ring stage: all its units are whole pages of the row before them
+    uint32_t plain = 0;  // bit per ring stage: all its units are whole ones of the row before them
     uint32_t live = 0, whole = 0;
     int fill_last = -64;  // the unit before the first has no row
     auto issue = [&](int k) {
@@ -804,16 +826,16 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
             Unit d;
             d.src = nullptr, d.row_valid = -1;
             if (lane < kFill && u < u1) {
-                d = a.warp_units ? place_of(a, warp_index + u / a.warp_units * all_warps, u % a.warp_units, a.warp_units, block_bytes)
-                    : a.row_ctas ? unit_of(a, row0, u, count0, block_bytes)
-                                 : unit_at(a, s, entries, per, u, block_bytes);
+                d = a.warp_units ? place_of<F>(a, warp_index + u / a.warp_units * all_warps, u % a.warp_units, a.warp_units)
+                    : a.row_ctas ? unit_of<F>(a, row0, u, count0)
+                                 : unit_at<F>(a, s, entries, per, u);
                 s.desc[warp][(first + lane) % (2 * kFill)] = d;
             }
-            // bit i: unit i is there; it is a whole page of the row before it
+            // bit i: unit i is there; it is a whole one of the row before it
             int before = __shfl_up_sync(0xffffffffu, d.row_valid, 1);
             if (lane == 0) before = fill_last;
             live = __ballot_sync(0xffffffffu, d.src != nullptr);
-            whole = __ballot_sync(0xffffffffu, d.src != nullptr && d.row_valid == ((before & ~63) | P));
+            whole = __ballot_sync(0xffffffffu, d.src != nullptr && d.row_valid == ((before & ~63) | F::TOKENS));
             fill_last = __shfl_sync(0xffffffffu, d.row_valid, kFill - 1);
             __syncwarp();
         }
@@ -834,8 +856,8 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
         }
         if (++put == S) put = 0;
     };
-    RowState<D, NG, HC, P> st;
-    st.ql = reinterpret_cast<uint4 *>(ring_mem + kWarps * (S * U * block_bytes)) + warp * (D / 32 * 32);
+    typename F::State st;
+    st.attach(ring_mem + kWarps * (S * U * block_bytes), warp);
     int row = -1, row_begin = 0, row_end = 0;
     float *piece_first = a.first_o + (int64_t(blockIdx.x) * kWarps + warp) * (G * D);
     auto close = [&](bool at_end) {
@@ -865,17 +887,14 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
             break;
         }
         const uint8_t *stage = ring + got * (U * block_bytes);
-        // Two tiles a step share the vote and hide each other's latencies, where the registers suffice: with 8 heads only
-        // for one group a row (32 x 8 rows of 8192 tokens: 84 us, 89 tile by tile; a ragged batch with two groups 77 and 74).
-        constexpr bool kPairs = HC == 4 || NG == 1;
-        if (kPairs && same) {
+        if (F::PAIRS && same) {
 #pragma unroll
-            for (int t = 0; t < kTiles; t += 2) st.template tiles<2>(stage, t, 16);
+            for (int t = 0; t < kTiles; t += 2) st.template tiles<F::PAIRS ? 2 : 1>(stage, t, 16);
         } else {
 #pragma unroll 1
             for (int t = 0; t < kTiles; t++) {
                 int nv = 16;
-                if (kPairs || !same) {
+                if (F::PAIRS || !same) {
                     const int it = k * U + t / kPageTiles;
                     if (it >= n) break;
                     const Unit u = s.desc[warp][it % (2 * kFill)];
@@ -1037,19 +1056,16 @@ __global__ void __launch_bounds__(kThreads, 2) kvq_decode_kernel(KvqDecodeArgs a
 // Shared memory a CTA may take beside its static part with two CTAs an SM
 // (228 KB an SM, 1 KB of each CTA's reserved).
 constexpr int kRingBudget = 113 * 1024 - int(sizeof(Shared));
-template <int D, int HC>
-constexpr int kQueryBytes = HC == 8 ? kWarps * D * 16 : 0;  // the lo halves of 8 heads
 
-template <int D, int NG, int HC, int P>
+template <class F>
 cudaError_t launch_one(KvqDecodeArgs &a, int num_sms, cudaStream_t stream) {
-    // a stage is about 4 KB: with fewer pages its fixed cost shows, with more the ring has too few stages
-    constexpr int stage = kWarps * (4096 / (P * D)) * kvq_block_words(D, P, NG) * 4;
-    constexpr int stages = (kRingBudget - kQueryBytes<D, HC>) / stage;
-    constexpr int bytes = stages * stage + kQueryBytes<D, HC>;
-    static_assert(stages >= 2 && stages <= kMaxRing, "the ring needs two stages, and a barrier each");
+    constexpr int stage = kWarps * F::U * F::BYTES;
+    constexpr int fit = (kRingBudget - F::STATE_BYTES) / stage, stages = fit < kMaxRing ? fit : kMaxRing;
+    constexpr int bytes = stages * stage + F::STATE_BYTES;
+    static_assert(stages >= 2, "the ring needs two stages");
     a.stages = stages;
     const int rows = a.batch * a.num_kv_heads, slots = kvq_decode_ctas(num_sms);
-    const int row_units = a.selected && a.top_k < a.max_pages ? a.top_k : a.max_pages;
+    const int row_units = (a.selected && a.top_k < a.max_pages ? a.top_k : a.max_pages) * F::SUB;
     // Rows of few pages, more of them than CTAs: whole rows to warps, nothing to join (2048 rows of 7 pages: 15.3 us,
     // 28.7 split evenly; 512 rows of 1 to 32 pages: 28.0 and 19.6, so longer rows only if every warp gets one).  Rows
     // that fit one wave of CTAs and are cut about alike (selections, short tables): a group of CTAs each, which need
@@ -1069,14 +1085,13 @@ cudaError_t launch_one(KvqDecodeArgs &a, int num_sms, cudaStream_t stream) {
     // The pages are read once a call.  Above half of L2 they are marked to leave it first, which keeps queries, tables
     // and partial outputs in it: 24.8 -> 23.7 us at 71 MB; below, pages that stay serve the next call: 10.1 us at
     // 19 MB with the plain policy, 11.2 with the other.
-    a.evict_first = int64_t(rows) * row_units * (stage / kWarps / (4096 / (P * D))) * 2 > l2_cache_bytes();
+    a.evict_first = int64_t(rows) * row_units * F::BYTES * 2 > l2_cache_bytes();
     const int64_t even = (int64_t(rows) * row_units + kWarps - 1) / kWarps;
     const unsigned grid = a.warp_units ? unsigned(slots < (rows + kWarps - 1) / kWarps ? slots : (rows + kWarps - 1) / kWarps)
                           : a.row_ctas ? unsigned(rows * a.row_ctas) : unsigned(even < slots ? even : slots);
-    const cudaError_t e = cudaFuncSetAttribute(kvq_decode_kernel<D, NG, HC, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               bytes);
+    const cudaError_t e = cudaFuncSetAttribute(kvq_decode_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kvq_decode_kernel<D, NG, HC, P>, dim3(grid), dim3(kThreads), bytes, stream, a);
+    return launch_pdl(kvq_decode_kernel<F>, dim3(grid), dim3(kThreads), bytes, stream, a);
 }
 
 template <int P>
@@ -1084,12 +1099,12 @@ cudaError_t launch_page(KvqDecodeArgs &a, int head_dim, int num_sms, cudaStream_
     const int ng = head_dim / a.group_size;
     const bool few = a.group <= 4;
     if (head_dim == 128) {
-        if (ng == 1) return few ? launch_one<128, 1, 4, P>(a, num_sms, stream) : launch_one<128, 1, 8, P>(a, num_sms, stream);
-        if (ng == 2) return few ? launch_one<128, 2, 4, P>(a, num_sms, stream) : launch_one<128, 2, 8, P>(a, num_sms, stream);
-        return few ? launch_one<128, 4, 4, P>(a, num_sms, stream) : launch_one<128, 4, 8, P>(a, num_sms, stream);
+        if (ng == 1) return few ? launch_one<KvqFormat<128, 1, 4, P>>(a, num_sms, stream) : launch_one<KvqFormat<128, 1, 8, P>>(a, num_sms, stream);
+        if (ng == 2) return few ? launch_one<KvqFormat<128, 2, 4, P>>(a, num_sms, stream) : launch_one<KvqFormat<128, 2, 8, P>>(a, num_sms, stream);
+        return few ? launch_one<KvqFormat<128, 4, 4, P>>(a, num_sms, stream) : launch_one<KvqFormat<128, 4, 8, P>>(a, num_sms, stream);
     }
-    if (ng == 1) return few ? launch_one<64, 1, 4, P>(a, num_sms, stream) : launch_one<64, 1, 8, P>(a, num_sms, stream);
-    return few ? launch_one<64, 2, 4, P>(a, num_sms, stream) : launch_one<64, 2, 8, P>(a, num_sms, stream);
+    if (ng == 1) return few ? launch_one<KvqFormat<64, 1, 4, P>>(a, num_sms, stream) : launch_one<KvqFormat<64, 1, 8, P>>(a, num_sms, stream);
+    return few ? launch_one<KvqFormat<64, 2, 4, P>>(a, num_sms, stream) : launch_one<KvqFormat<64, 2, 8, P>>(a, num_sms, stream);
 }
 
 }  // namespace

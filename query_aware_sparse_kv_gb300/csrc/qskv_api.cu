@@ -12,6 +12,7 @@
 #include "qskv.h"
 #include "qskv_device.cuh"
 #include "qskv_internal.h"
+#include "qskv_kvf.cuh"
 #include "qskv_kvq.cuh"
 
 namespace qskv {
@@ -1005,12 +1006,14 @@ size_t qskv_kvq_workspace_size(const qskv_shape *shape) {
     return KvqWorkspace(shape, sms).total;
 }
 
-qskv_status qskv_kvq_paged_decode(const void *q, qskv_dtype q_dtype, const void *pool, const int32_t *page_table,
-                                  const int32_t *seq_lens, const qskv_shape *shape, int32_t group_size,
+}  // extern "C"
+
+namespace {
+// Checks and arguments that the decodes over quantised caches share; `units` parts a page of the cache has.
+qskv_status quantised_decode_args(KvqDecodeArgs &a, const void *q, qskv_dtype q_dtype, const void *pool,
+                                  const int32_t *page_table, const int32_t *seq_lens, const qskv_shape *shape, int units,
                                   const int32_t *selected, const int32_t *n_selected, int32_t top_k, float sm_scale,
-                                  float *out, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
-    QSKV_TRY(check_shape(shape));
-    QSKV_TRY(check_group_size(shape, group_size));
+                                  float *out, float *lse, void *workspace, size_t workspace_bytes, int *num_sms) {
     QSKV_TRY(check_dtype(q_dtype, "q"));
     if (!q || !pool || !page_table || !seq_lens || !out)
         return fail(QSKV_ERR_INVALID_ARG, "q, pool, page_table, seq_lens and out must be non-NULL");
@@ -1023,14 +1026,15 @@ qskv_status qskv_kvq_paged_decode(const void *q, qskv_dtype q_dtype, const void 
         return fail(QSKV_ERR_INVALID_ARG, "index and lse arrays must be 4-byte aligned");
     if (!(sm_scale >= 0.f) || isinf(sm_scale)) return fail(QSKV_ERR_INVALID_ARG, "sm_scale must be finite and >= 0");
     const int64_t rows = int64_t(shape->batch) * shape->num_kv_heads;
-    if (rows * (selected ? top_k : shape->max_pages) >= (int64_t(1) << 31))
-        return fail(QSKV_ERR_UNSUPPORTED, "batch * num_kv_heads * %s must be < 2^31", selected ? "top_k" : "max_pages");
-    const int sms = current_sm_count(nullptr);
+    const int64_t most = (int64_t(1) << 31) / units;
+    if (rows * (selected ? top_k : shape->max_pages) >= most)
+        return fail(QSKV_ERR_UNSUPPORTED, "batch * num_kv_heads * %s must be < %lld", selected ? "top_k" : "max_pages",
+                    (long long)most);
+    const int sms = *num_sms = current_sm_count(nullptr);
     if (sms <= 0) return fail(QSKV_ERR_CUDA, "cannot query the current CUDA device");
     const KvqWorkspace L(shape, sms);
     QSKV_TRY(check_workspace(workspace, workspace_bytes, L.total));
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    KvqDecodeArgs a = {};
     a.tickets = reinterpret_cast<uint32_t *>(ws + L.tickets);
     a.part_ml = reinterpret_cast<float *>(ws + L.part_ml);
     a.part_o = reinterpret_cast<float *>(ws + L.part_o);
@@ -1052,12 +1056,139 @@ qskv_status qskv_kvq_paged_decode(const void *q, qskv_dtype q_dtype, const void 
     a.max_pages = shape->max_pages;
     a.num_pool_pages = shape->num_pool_pages;
     a.top_k = selected ? top_k : 0;
-    a.group_size = group_size;
     a.q_is_bf16 = q_dtype == QSKV_BF16;
     const float scale = sm_scale > 0.f ? sm_scale : 1.f / sqrtf(float(shape->head_dim));
     a.scale_log2 = scale * 1.4426950408889634f;
+    return QSKV_OK;
+}
+}  // namespace
+
+extern "C" {
+
+qskv_status qskv_kvq_paged_decode(const void *q, qskv_dtype q_dtype, const void *pool, const int32_t *page_table,
+                                  const int32_t *seq_lens, const qskv_shape *shape, int32_t group_size,
+                                  const int32_t *selected, const int32_t *n_selected, int32_t top_k, float sm_scale,
+                                  float *out, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    QSKV_TRY(check_shape(shape));
+    QSKV_TRY(check_group_size(shape, group_size));
+    KvqDecodeArgs a = {};
+    int sms = 0;
+    QSKV_TRY(quantised_decode_args(a, q, q_dtype, pool, page_table, seq_lens, shape, 1, selected, n_selected, top_k,
+                                   sm_scale, out, lse, workspace, workspace_bytes, &sms));
+    a.group_size = group_size;
     return launched(launch_kvq_decode(a, shape->head_dim, sms, static_cast<cudaStream_t>(stream)),
                     "kvq_paged_decode launch");
+}
+
+// ------------------------------------------------ the 8-bit paged KV cache --
+size_t qskv_kvf_block_bytes(const qskv_shape *shape) {
+    if (check_shape(shape) != QSKV_OK) return 0;
+    return size_t(shape->page_size / kKvfPartTokens) * kvf_part_bytes(shape->head_dim);
+}
+
+qskv_status qskv_kvf_append(const void *k, const void *v, qskv_dtype kv_dtype, int64_t k_stride, int64_t v_stride,
+                            const int32_t *slots, int32_t n_tokens, void *pool, const qskv_shape *shape,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+    QSKV_TRY(check_shape(shape));
+    QSKV_TRY(check_dtype(kv_dtype, "kv"));
+    if (n_tokens < 0) return fail(QSKV_ERR_INVALID_ARG, "n_tokens must be >= 0 (got %d)", n_tokens);
+    QSKV_TRY(check_workspace(workspace, workspace_bytes, 256));
+    if (n_tokens == 0) return ok();
+    if (!k || !v || !slots || !pool) return fail(QSKV_ERR_INVALID_ARG, "k, v, slots and pool must be non-NULL");
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(pool, 16))
+        return fail(QSKV_ERR_INVALID_ARG, "k, v and pool must be 16-byte aligned");
+    if (!aligned(slots, 4)) return fail(QSKV_ERR_INVALID_ARG, "slots must be 4-byte aligned");
+    const int64_t row = int64_t(shape->num_kv_heads) * shape->head_dim;
+    const int64_t vec = kv_dtype == QSKV_BF16 ? 8 : 4;
+    if (n_tokens > 1 && (k_stride < row || v_stride < row || k_stride % vec || v_stride % vec))
+        return fail(QSKV_ERR_INVALID_ARG,
+                    "k_stride and v_stride must be at least num_kv_heads * head_dim and multiples of 16 bytes");
+    KvfStoreArgs a = {};
+    a.k = k;
+    a.v = v;
+    a.pool = static_cast<uint8_t *>(pool);
+    a.slots = slots;
+    a.flags = static_cast<uint32_t *>(workspace);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.n_tokens = n_tokens;
+    a.num_kv_heads = shape->num_kv_heads;
+    a.page_size = shape->page_size;
+    a.num_pool_pages = shape->num_pool_pages;
+    return launched(launch_kvf_append(a, kv_dtype, shape->head_dim, static_cast<cudaStream_t>(stream)),
+                    "kvf_append launch");
+}
+
+qskv_status qskv_kvf_gather(const void *pool, const int32_t *slots, int32_t n_tokens, void *k_out, void *v_out,
+                            qskv_dtype out_dtype, const qskv_shape *shape, void *workspace, size_t workspace_bytes,
+                            void *stream) {
+    QSKV_TRY(check_shape(shape));
+    QSKV_TRY(check_dtype(out_dtype, "out"));
+    if (n_tokens < 0) return fail(QSKV_ERR_INVALID_ARG, "n_tokens must be >= 0 (got %d)", n_tokens);
+    QSKV_TRY(check_workspace(workspace, workspace_bytes, 256));
+    if (n_tokens == 0) return ok();
+    if (!pool || !slots || !k_out || !v_out)
+        return fail(QSKV_ERR_INVALID_ARG, "pool, slots, k_out and v_out must be non-NULL");
+    if (!aligned(pool, 16) || !aligned(k_out, 16) || !aligned(v_out, 16))
+        return fail(QSKV_ERR_INVALID_ARG, "pool, k_out and v_out must be 16-byte aligned");
+    if (!aligned(slots, 4)) return fail(QSKV_ERR_INVALID_ARG, "slots must be 4-byte aligned");
+    KvfStoreArgs a = {};
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.pool = static_cast<uint8_t *>(const_cast<void *>(pool));
+    a.slots = slots;
+    a.flags = static_cast<uint32_t *>(workspace);
+    a.n_tokens = n_tokens;
+    a.num_kv_heads = shape->num_kv_heads;
+    a.page_size = shape->page_size;
+    a.num_pool_pages = shape->num_pool_pages;
+    return launched(launch_kvf_gather(a, out_dtype, shape->head_dim, static_cast<cudaStream_t>(stream)),
+                    "kvf_gather launch");
+}
+
+qskv_status qskv_kvf_meta_build(const void *pool, const int32_t *page_ids, const int32_t *valid_tokens,
+                                int32_t n_pages, void *meta, qskv_dtype meta_dtype, const qskv_shape *shape,
+                                void *workspace, size_t workspace_bytes, void *stream) {
+    QSKV_TRY(check_shape(shape));
+    QSKV_TRY(check_dtype(meta_dtype, "meta"));
+    if (n_pages < 0) return fail(QSKV_ERR_INVALID_ARG, "n_pages must be >= 0 (got %d)", n_pages);
+    QSKV_TRY(check_workspace(workspace, workspace_bytes, 256));
+    if (n_pages == 0) return ok();
+    if (!pool || !page_ids || !valid_tokens || !meta)
+        return fail(QSKV_ERR_INVALID_ARG, "pool, page_ids, valid_tokens and meta must be non-NULL");
+    if (!aligned(pool, 16) || !aligned(meta, 16))
+        return fail(QSKV_ERR_INVALID_ARG, "pool and meta must be 16-byte aligned");
+    if (!aligned(page_ids, 4) || !aligned(valid_tokens, 4))
+        return fail(QSKV_ERR_INVALID_ARG, "page_ids and valid_tokens must be 4-byte aligned");
+    const int sms = current_sm_count(nullptr);
+    if (sms <= 0) return fail(QSKV_ERR_CUDA, "cannot query the current CUDA device");
+    KvfMetaArgs a = {};
+    a.pool = static_cast<const uint8_t *>(pool);
+    a.page_ids = page_ids;
+    a.valid_tokens = valid_tokens;
+    a.meta = meta;
+    a.flags = static_cast<uint32_t *>(workspace);
+    a.n_list = n_pages;
+    a.num_kv_heads = shape->num_kv_heads;
+    a.page_size = shape->page_size;
+    a.num_pool_pages = shape->num_pool_pages;
+    return launched(launch_kvf_meta(a, meta_dtype, shape->head_dim, sms, static_cast<cudaStream_t>(stream)),
+                    "kvf_meta_build launch");
+}
+
+size_t qskv_kvf_workspace_size(const qskv_shape *shape) { return qskv_kvq_workspace_size(shape); }
+
+qskv_status qskv_kvf_paged_decode(const void *q, qskv_dtype q_dtype, const void *pool, const int32_t *page_table,
+                                  const int32_t *seq_lens, const qskv_shape *shape, const int32_t *selected,
+                                  const int32_t *n_selected, int32_t top_k, float sm_scale, float *out, float *lse,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    QSKV_TRY(check_shape(shape));
+    KvqDecodeArgs a = {};
+    int sms = 0;
+    QSKV_TRY(quantised_decode_args(a, q, q_dtype, pool, page_table, seq_lens, shape, shape->page_size / kKvfPartTokens,
+                                   selected, n_selected, top_k, sm_scale, out, lse, workspace, workspace_bytes, &sms));
+    return launched(launch_kvf_decode(a, shape->head_dim, sms, static_cast<cudaStream_t>(stream)),
+                    "kvf_paged_decode launch");
 }
 
 // ------------------------------------------------------------- page tables --

@@ -208,11 +208,11 @@ class PagedDecoder:
 
 
 class QuantizedPagedDecoder:
-    """A decode batch over a KV cache held in 4 bits, from lengths to outputs.
+    """A decode batch over a KV cache held in 4 or 8 bits, from lengths to outputs.
 
-    Owns the pool (codes with a bf16 scale and minimum per group of
-    ``group_size`` dims), its page metadata, the page table and the free
-    pages.  A step is: ``extend`` (tables and slots of the new tokens),
+    Owns the pool (4 bits: codes with a bf16 scale and minimum per group of
+    ``group_size`` dims; 8 bits: e4m3 codes with a power of two per token and
+    head), its page metadata, the page table and the free pages.  A step is: ``extend`` (tables and slots of the new tokens),
     ``append`` (their keys and values quantised into the pool, the touched
     pages' metadata rebuilt), ``select`` (with top_k: the pages each query
     attends to) and ``decode``; ``step`` does all of it.  Row lengths are
@@ -225,11 +225,14 @@ class QuantizedPagedDecoder:
     max_pages   pages a row may hold
     max_tokens  new tokens a step may bring, all rows together
     top_k       pages kept per (row, KV head); None = all
+    bits        4 or 8 (group_size says nothing for 8)
     """
 
     def __init__(self, batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int, max_pages: int,
                  num_pool_pages: int, group_size: int = 64, top_k: Optional[int] = None, max_tokens: int = 8192,
-                 sm_scale: float = 0.0, device="cuda"):
+                 sm_scale: float = 0.0, device="cuda", bits: int = 4):
+        if bits not in (4, 8):
+            raise ValueError(f"bits must be 4 or 8 (got {bits})")
         if top_k is not None and top_k < 1:
             raise ValueError(f"top_k must be None (all pages) or >= 1 (got {top_k})")
         if max_tokens < 1:
@@ -238,7 +241,10 @@ class QuantizedPagedDecoder:
             raise ValueError(f"sm_scale must be finite and >= 0 (got {sm_scale})")
         self.shape = B.make_shape(batch, num_q_heads, num_kv_heads, head_dim, page_size, max_pages, num_pool_pages)
         self.group_size, self.top_k, self.sm_scale, self.max_tokens = group_size, top_k, sm_scale, max_tokens
-        block = B.kvq_block_bytes(self.shape, group_size)
+        self.bits = bits
+        # the shape as the cache's calls take it, with the group size where there is one
+        self._format = (self.shape, group_size) if bits == 4 else (self.shape,)
+        block = B.kvq_block_bytes(*self._format) if bits == 4 else B.kvf_block_bytes(self.shape)
         i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device=device)  # noqa: E731
         self.pool = torch.zeros((num_pool_pages, num_kv_heads, block), dtype=torch.uint8, device=device)
         self.page_table = torch.full((batch, max_pages), -1, dtype=torch.int32, device=device)
@@ -249,7 +255,8 @@ class QuantizedPagedDecoder:
         touched = min(max_tokens, max_tokens // page_size + 2 * batch)
         self.touched_ids, self.touched_valid = i32(touched), i32(touched)
         with torch.cuda.device(self.pool.device):
-            size = max(B.kvq_workspace_size(self.shape), B.tables_workspace_size(self.shape),
+            size = max(B.kvq_workspace_size(self.shape) if bits == 4 else B.kvf_workspace_size(self.shape),
+                       B.tables_workspace_size(self.shape),
                        B.workspace_size(self.shape) if top_k is not None else 0)
         self.workspace = torch.zeros(size, dtype=torch.uint8, device=device)
         if top_k is not None:
@@ -313,10 +320,10 @@ class QuantizedPagedDecoder:
         the pages they fall into."""
         if k.shape[0] != self._new:
             raise ValueError(f"{k.shape[0]} keys for the {self._new} tokens of the last extend")
-        B.kvq_append(k, v, self.slot_map[:k.shape[0]], self.pool, self.shape, self.group_size, self.workspace, stream)
+        store, meta_build = (B.kvq_append, B.kvq_meta_build) if self.bits == 4 else (B.kvf_append, B.kvf_meta_build)
+        store(k, v, self.slot_map[:k.shape[0]], self.pool, *self._format, self.workspace, stream)
         if self.top_k is not None:
-            B.kvq_meta_build(self.pool, self.touched_ids, self.touched_valid, self.meta, self.shape, self.group_size,
-                             self.workspace, stream)
+            meta_build(self.pool, self.touched_ids, self.touched_valid, self.meta, *self._format, self.workspace, stream)
         self._new = 0
 
     def _check_query(self, q: torch.Tensor):
@@ -340,10 +347,11 @@ class QuantizedPagedDecoder:
         """Attention of q [batch][Hq][d] over the selected (or all) pages,
         into ``out`` / ``lse``."""
         sparse = self.top_k is not None
-        B.kvq_paged_decode(q, self.pool, self.page_table, self.seq_lens, self.out if out is None else out, self.shape,
-                           self.group_size, self.workspace, selected=self.selected if sparse else None,
-                           n_selected=self.n_selected if sparse else None, top_k=self.top_k or 0,
-                           lse=self.lse if lse is None else lse, sm_scale=self.sm_scale, stream=stream)
+        paged_decode = B.kvq_paged_decode if self.bits == 4 else B.kvf_paged_decode
+        paged_decode(q, self.pool, self.page_table, self.seq_lens, self.out if out is None else out, *self._format,
+                     self.workspace, selected=self.selected if sparse else None,
+                     n_selected=self.n_selected if sparse else None, top_k=self.top_k or 0,
+                     lse=self.lse if lse is None else lse, sm_scale=self.sm_scale, stream=stream)
 
     def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, new_lens=None, stream=None):
         """One step: the rows' new tokens (one each by default) stored, then
@@ -372,7 +380,7 @@ class QuantizedPagedDecoder:
             slots = (self.page_table[row].long()[t // P] * P + t % P).to(torch.int32)
             k, v = (torch.empty((n, self.shape.num_kv_heads, self.shape.head_dim), dtype=dtype,
                                 device=self.pool.device) for _ in range(2))
-        B.kvq_gather(self.pool, slots, k, v, self.shape, self.group_size, self.workspace, stream)
+        (B.kvq_gather if self.bits == 4 else B.kvf_gather)(self.pool, slots, k, v, *self._format, self.workspace, stream)
         return k, v
 
     def release(self, row: int, stream=None):
