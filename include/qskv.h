@@ -539,6 +539,55 @@ qskv_status qskv_kvf_paged_decode(const void *q, qskv_dtype q_dtype, const void 
                                   void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Prefill: causal attention of every sequence's newest tokens over all that
+ * its pages hold, for a prompt, a chunk of one behind what is cached, a few
+ * tokens checked at once, or any mixture of those in one batch.  The sequences'
+ * queries are packed: sequence b's are the rows cu_new[b] .. cu_new[b+1] - 1 of
+ * q, as qskv_extend_tables numbers them, n_b = cu_new[b+1] - cu_new[b] of them.
+ * seq_lens[b] counts the new tokens, whose keys and values are already in the
+ * cache.  Query i of the sequence stands at pos = seq_len - n_b + i, and for
+ * each query head h (KV head g = h / G), over the tokens t <= pos:
+ *   l_t = sm_scale * (q_h . k_t),  out[cu_new[b] + i][h] = sum_t softmax(l)_t v_t,
+ *   lse[cu_new[b] + i][h] = log sum_t exp(l_t).
+ *   q         [n_tokens][num_q_heads][head_dim] bf16 or fp32, 16-byte aligned,
+ *             rows q_stride elements apart (a multiple of 16 bytes, so a view
+ *             of a fused projection's output can be passed)
+ *   cu_new    [batch + 1] int32, non-decreasing, within [0, n_tokens]
+ *   out       [n_tokens][num_q_heads][head_dim], contiguous, q's type; must not
+ *             overlap an input
+ *   lse       [n_tokens][num_q_heads] fp32, or NULL
+ *   n_tokens  rows of q and out; rows behind cu_new[batch] (padding) are not
+ *             read, and out and lse there are left as they were.
+ *             n_tokens * num_q_heads must be below 2^31.
+ *   sm_scale  0 means 1/sqrt(d)
+ * Here q, out and lse are device memory.  The caches are those of
+ * qskv_sparse_paged_decode (k_pool, v_pool in kv_dtype) and of
+ * qskv_kvf_paged_decode (pool); what lies in slots past seq_len may be anything.
+ * With fp32 queries, and with an fp32 cache, everything is computed in fp32.
+ * With bf16 queries over a bf16 or 8-bit cache the products take bf16 operands
+ * (softmax weights are rounded to bf16) and sum in fp32.
+ * Nothing is read before the previous kernel in the stream has completed.
+ * Device errors: cu_new out of order or range, seq_len outside
+ * [0, max_pages * page_size] or below n_b: clamped to what there is (a query
+ * before position 0 attends to nothing: out 0, lse -inf), a page id outside the
+ * pool: its tokens are skipped; both flag QSKV_ERR_DEVICE_INDEX.
+ * Workspace: qskv_prefill_workspace_size bytes, 256-byte aligned, zeroed once;
+ * it may be shared with the other calls (of the same batch and num_kv_heads).
+ */
+size_t qskv_prefill_workspace_size(const qskv_shape *shape, int32_t n_tokens);
+
+qskv_status qskv_paged_prefill(const void *q, qskv_dtype q_dtype, int64_t q_stride, const void *k_pool,
+                               const void *v_pool, qskv_dtype kv_dtype, const int32_t *page_table,
+                               const int32_t *seq_lens, const int32_t *cu_new, int32_t n_tokens,
+                               const qskv_shape *shape, float sm_scale, void *out, float *lse, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+qskv_status qskv_kvf_paged_prefill(const void *q, qskv_dtype q_dtype, int64_t q_stride, const void *pool,
+                                   const int32_t *page_table, const int32_t *seq_lens, const int32_t *cu_new,
+                                   int32_t n_tokens, const qskv_shape *shape, float sm_scale, void *out, float *lse,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Page tables and slot map of one scheduler step.  Request b holds
  * seq_lens[b] tokens, whose pages page_table names, and brings new_lens[b]
  * more.  Requests are admitted in order: request b with new_lens[b] > 0 fits

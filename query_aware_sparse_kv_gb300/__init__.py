@@ -27,6 +27,8 @@ in include/qskv.h); this package is its binding:
   kvf_append, kvf_gather,  the same for a cache in 8 bits (e4m3 codes, a
   kvf_meta_build,            power of two per token and head)
   kvf_paged_decode
+  paged_prefill,         causal attention of every row's newest tokens (prompts,
+  kvf_paged_prefill        chunks of them, single tokens) over its pages
 
 plus ``PagedDecoder`` and ``QuantizedPagedDecoder`` (buffer plumbing for a
 whole step over a bf16 / fp32 and over a 4-bit cache) and ``workloads``
@@ -38,7 +40,7 @@ from .binding import (QSKV_BF16, QSKV_F32, QskvError, QskvLibraryMissing, Shape,
                       kvf_meta_build, kvf_paged_decode, kvf_workspace_size, kv_centroid_build, kv_meta_build,
                       kvq_append, kvq_block_bytes, kvq_gather, kvq_meta_build, kvq_paged_decode, kvq_workspace_size,
                       last_error_message, load, make_shape, page_select, page_select_approx, page_select_refresh, page_select_centroid,
-                      select_decode, sparse_paged_decode, sparse_paged_decode_noalloc, tables_workspace_size,
+                      kvf_paged_prefill, paged_prefill, prefill_workspace_size, select_decode, sparse_paged_decode, sparse_paged_decode_noalloc, tables_workspace_size,
                       workspace_size)
 from .engine import PagedDecoder, QuantizedPagedDecoder, from_inputs
 
@@ -50,4 +52,5 @@ __all__ = ["QSKV_BF16", "QSKV_F32", "QskvError", "QskvLibraryMissing", "Shape", 
            "extend_tables", "kvq_append", "kvq_block_bytes", "kvq_gather", "kvq_meta_build", "kvq_paged_decode",
            "kvq_workspace_size", "tables_workspace_size",
            "kvf_append", "kvf_block_bytes", "kvf_gather", "kvf_meta_build", "kvf_paged_decode", "kvf_workspace_size",
+           "kvf_paged_prefill", "paged_prefill", "prefill_workspace_size",
            "PagedDecoder", "QuantizedPagedDecoder", "from_inputs"]

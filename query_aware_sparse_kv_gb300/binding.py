@@ -28,7 +28,8 @@ EXPORTS = ("qskv_workspace_size", "qskv_kv_meta_build", "qskv_page_select", "qsk
            "qskv_cascade_workspace_size", "qskv_cascade_paged_decode", "qskv_kvq_block_bytes", "qskv_kvq_append",
            "qskv_kvq_gather", "qskv_kvq_meta_build", "qskv_kvq_workspace_size", "qskv_kvq_paged_decode",
            "qskv_kvf_block_bytes", "qskv_kvf_append", "qskv_kvf_gather", "qskv_kvf_meta_build",
-           "qskv_kvf_workspace_size", "qskv_kvf_paged_decode", "qskv_tables_workspace_size", "qskv_extend_tables",
+           "qskv_kvf_workspace_size", "qskv_kvf_paged_decode", "qskv_prefill_workspace_size", "qskv_paged_prefill",
+           "qskv_kvf_paged_prefill", "qskv_tables_workspace_size", "qskv_extend_tables",
            "qskv_get_error", "qskv_status_string", "qskv_last_error_message")
 
 
@@ -123,6 +124,14 @@ def load(path: str = LIB_PATH):
     lib.qskv_kvf_paged_decode.restype = ctypes.c_int
     lib.qskv_kvf_paged_decode.argtypes = [vp, ctypes.c_int, vp, i32p, i32p, sp, i32p, i32p, i32, ctypes.c_float, f32p,
                                           f32p, vp, sz, vp]
+    lib.qskv_prefill_workspace_size.restype = sz
+    lib.qskv_prefill_workspace_size.argtypes = [sp, i32]
+    lib.qskv_paged_prefill.restype = ctypes.c_int
+    lib.qskv_paged_prefill.argtypes = [vp, ctypes.c_int, i64, vp, vp, ctypes.c_int, i32p, i32p, i32p, i32, sp,
+                                       ctypes.c_float, vp, f32p, vp, sz, vp]
+    lib.qskv_kvf_paged_prefill.restype = ctypes.c_int
+    lib.qskv_kvf_paged_prefill.argtypes = [vp, ctypes.c_int, i64, vp, i32p, i32p, i32p, i32, sp, ctypes.c_float, vp,
+                                           f32p, vp, sz, vp]
     lib.qskv_tables_workspace_size.restype = sz
     lib.qskv_tables_workspace_size.argtypes = [sp]
     lib.qskv_extend_tables.restype = ctypes.c_int
@@ -538,6 +547,58 @@ def kvf_paged_decode(q: torch.Tensor, pool: torch.Tensor, page_table: torch.Tens
             _tensor("out", out, torch.float32, (B, Hq, d), dev), _tensor("lse", lse, torch.float32, (B, Hq), dev),
             *_workspace(workspace, dev))
     _run(lib.qskv_kvf_paged_decode, dev, args, stream)
+
+
+# -- prefill ----------------------------------------------------------------------
+
+def prefill_workspace_size(shape: Shape, n_tokens: int) -> int:
+    """Bytes of workspace of a prefill call of up to n_tokens queries."""
+    n = load().qskv_prefill_workspace_size(ctypes.byref(shape), int(n_tokens))
+    if n == 0:
+        raise QskvError(1, load().qskv_last_error_message().decode())
+    return int(n)
+
+
+def _prefill(fn, q, caches, page_table, seq_lens, cu_new, out, shape, workspace, lse, sm_scale, stream, dev):
+    B, Hq, d = shape.batch, shape.num_q_heads, shape.head_dim
+    T = q.shape[0]
+    qp, qs = _rows("q", q, q.dtype, T, Hq, d, dev)
+    if out.get_device() != dev:  # (pinned host memory is for the decode's one token a row)
+        raise ValueError(f"out must be on cuda:{dev} (got {out.device})")
+    if lse is not None and lse.get_device() != dev:
+        raise ValueError(f"lse must be on cuda:{dev} (got {lse.device})")
+    args = (qp, _dtype(q), qs, *caches, _tensor("page_table", page_table, _I32, (B, shape.max_pages), dev),
+            _tensor("seq_lens", seq_lens, _I32, (B,), dev), _tensor("cu_new", cu_new, _I32, (B + 1,), dev), T,
+            ctypes.byref(shape), sm_scale, _tensor("out", out, q.dtype, (T, Hq, d), dev),
+            _tensor("lse", lse, torch.float32, (T, Hq), dev), *_workspace(workspace, dev))
+    _run(fn, dev, args, stream)
+
+
+def paged_prefill(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, page_table: torch.Tensor,
+                  seq_lens: torch.Tensor, cu_new: torch.Tensor, out: torch.Tensor, shape: Shape,
+                  workspace: torch.Tensor, lse: Optional[torch.Tensor] = None, sm_scale: float = 0.0, stream=None):
+    """Causal attention of every row's newest tokens over its pages: row b's
+    queries are q[cu_new[b]:cu_new[b + 1]] ([T][Hq][d] packed, bf16 or fp32,
+    any token stride of whole 16 bytes), the last of its seq_lens[b] tokens.
+    out [T][Hq][d] has q's type; rows behind cu_new[-1] stay as they were.
+    The workspace must hold prefill_workspace_size(shape, T) bytes."""
+    lib = _lib or load()
+    dev = _device("k_pool", k_pool)
+    full = (shape.num_pool_pages, shape.num_kv_heads, shape.page_size, shape.head_dim)
+    caches = (_tensor("k_pool", k_pool, k_pool.dtype, full, dev), _tensor("v_pool", v_pool, k_pool.dtype, full, dev),
+              _dtype(k_pool))
+    _prefill(lib.qskv_paged_prefill, q, caches, page_table, seq_lens, cu_new, out, shape, workspace, lse, sm_scale,
+             stream, dev)
+
+
+def kvf_paged_prefill(q: torch.Tensor, pool: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                      cu_new: torch.Tensor, out: torch.Tensor, shape: Shape, workspace: torch.Tensor,
+                      lse: Optional[torch.Tensor] = None, sm_scale: float = 0.0, stream=None):
+    """paged_prefill over the 8-bit cache."""
+    lib = _lib or load()
+    dev = _device("pool", pool)
+    _prefill(lib.qskv_kvf_paged_prefill, q, (_pool8_ptr(pool, shape, dev),), page_table, seq_lens, cu_new, out, shape,
+             workspace, lse, sm_scale, stream, dev)
 
 
 def extend_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, page_table: torch.Tensor,

@@ -14,6 +14,7 @@
 #include "qskv_internal.h"
 #include "qskv_kvf.cuh"
 #include "qskv_kvq.cuh"
+#include "qskv_prefill.cuh"
 
 namespace qskv {
 
@@ -1189,6 +1190,139 @@ qskv_status qskv_kvf_paged_decode(const void *q, qskv_dtype q_dtype, const void 
                                    selected, n_selected, top_k, sm_scale, out, lse, workspace, workspace_bytes, &sms));
     return launched(launch_kvf_decode(a, shape->head_dim, sms, static_cast<cudaStream_t>(stream)),
                     "kvf_paged_decode launch");
+}
+
+// ------------------------------------------------------------------ prefill --
+}  // extern "C"
+
+namespace {
+// Behind the error word and the row counters of the other calls, which stay zero in a shared workspace.
+struct PrefillWorkspace {
+    size_t plan, tile_begin, items, tickets, part_o, part_lse, total;
+    int64_t max_items, max_slots;
+    // A call whose tiles have tile_rows rows, cut into parts for `waves` of them an SM.
+    PrefillWorkspace(const qskv_shape *s, int64_t n_tokens, int num_sms, int tile_rows, int waves) {
+        const int64_t per = tile_rows / (s->num_q_heads / s->num_kv_heads), heads = s->num_kv_heads;
+        // a cut tile has more blocks than the share of one of num_sms * waves parts, so there are fewer than twice as many parts
+        max_slots = waves > 0 ? (2 * int64_t(num_sms) * waves + heads - 1) / heads + 1 : 0;
+        max_items = n_tokens / per + s->batch + 1 + max_slots;
+        plan = align256(256 + size_t(s->batch) * heads * 4);
+        tile_begin = plan + sizeof(PrefillPlan);
+        items = align256(tile_begin + (size_t(s->batch) + 1) * 4);
+        tickets = align256(items + size_t(max_items) * sizeof(PrefillItem));
+        part_o = align256(tickets + size_t(max_slots * heads) * 4);
+        part_lse = part_o + size_t(max_slots * heads) * tile_rows * s->head_dim * 4;
+        total = part_lse + size_t(max_slots * heads) * tile_rows * 4;
+    }
+};
+
+size_t prefill_workspace(const qskv_shape *s, int64_t n_tokens, int num_sms) {
+    return PrefillWorkspace(s, n_tokens, num_sms, kPrefillSimtRows, 0).total;
+}
+
+qskv_status check_prefill_tokens(const qskv_shape *s, int64_t n_tokens) {
+    if (n_tokens < 0) return fail(QSKV_ERR_INVALID_ARG, "n_tokens must be >= 0 (got %lld)", (long long)n_tokens);
+    if (n_tokens * s->num_q_heads >= (int64_t(1) << 31))
+        return fail(QSKV_ERR_UNSUPPORTED, "n_tokens * num_q_heads must be < 2^31");
+    return QSKV_OK;
+}
+
+// pool: the 8-bit cache, else k_pool and v_pool in kv_dtype.
+qskv_status prefill(const void *q, qskv_dtype q_dtype, int64_t q_stride, const void *k_pool, const void *v_pool,
+                    qskv_dtype kv_dtype, const void *pool, const int32_t *page_table, const int32_t *seq_lens,
+                    const int32_t *cu_new, int32_t n_tokens, const qskv_shape *shape, float sm_scale, void *out, float *lse,
+                    void *workspace, size_t workspace_bytes, void *stream, const char *what) {
+    QSKV_TRY(check_shape(shape));
+    QSKV_TRY(check_dtype(q_dtype, "q"));
+    QSKV_TRY(check_dtype(kv_dtype, "kv"));
+    QSKV_TRY(check_prefill_tokens(shape, n_tokens));
+    if (n_tokens == 0) return ok();
+    const void *keys = pool ? pool : k_pool, *values = pool ? pool : v_pool;
+    if (!q || !keys || !values || !page_table || !seq_lens || !cu_new || !out)
+        return fail(QSKV_ERR_INVALID_ARG, "q, the pools, page_table, seq_lens, cu_new and out must be non-NULL");
+    if (!aligned(q, 16) || !aligned(keys, 16) || !aligned(values, 16) || !aligned(out, 16))
+        return fail(QSKV_ERR_INVALID_ARG, "q, the pools and out must be 16-byte aligned");
+    if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_new, 4) || !aligned(lse, 4))
+        return fail(QSKV_ERR_INVALID_ARG, "index and lse arrays must be 4-byte aligned");
+    const int64_t row = int64_t(shape->num_q_heads) * shape->head_dim, vec = q_dtype == QSKV_BF16 ? 8 : 4;
+    if (n_tokens == 1) q_stride = row;
+    if (q_stride < row || q_stride % vec)
+        return fail(QSKV_ERR_INVALID_ARG, "q_stride must be at least num_q_heads * head_dim and a multiple of 16 bytes");
+    if (!(sm_scale >= 0.f) || isinf(sm_scale)) return fail(QSKV_ERR_INVALID_ARG, "sm_scale must be finite and >= 0");
+    const int sms = current_sm_count(nullptr);
+    if (sms <= 0) return fail(QSKV_ERR_CUDA, "cannot query the current CUDA device");
+    QSKV_TRY(check_workspace(workspace, workspace_bytes, prefill_workspace(shape, n_tokens, sms)));
+    PrefillArgs a = {};
+    a.tile_rows = kPrefillSimtRows;
+    a.block_keys = kPrefillSimtKeys;
+    a.waves = 0;
+    const PrefillWorkspace L(shape, n_tokens, sms, a.tile_rows, a.waves);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.q = q;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.pool = static_cast<const uint8_t *>(pool);
+    a.page_table = page_table;
+    a.seq_lens = seq_lens;
+    a.cu_new = cu_new;
+    a.out = out;
+    a.lse = lse;
+    a.flags = static_cast<uint32_t *>(workspace);
+    a.plan = reinterpret_cast<PrefillPlan *>(ws + L.plan);
+    a.tile_begin = reinterpret_cast<int32_t *>(ws + L.tile_begin);
+    a.items = reinterpret_cast<PrefillItem *>(ws + L.items);
+    a.tickets = reinterpret_cast<uint32_t *>(ws + L.tickets);
+    a.part_o = reinterpret_cast<float *>(ws + L.part_o);
+    a.part_lse = reinterpret_cast<float *>(ws + L.part_lse);
+    a.q_stride = q_stride;
+    a.n_tokens = n_tokens;
+    a.batch = shape->batch;
+    a.num_q_heads = shape->num_q_heads;
+    a.num_kv_heads = shape->num_kv_heads;
+    a.group = shape->num_q_heads / shape->num_kv_heads;
+    a.page_size = shape->page_size;
+    a.max_pages = shape->max_pages;
+    a.num_pool_pages = shape->num_pool_pages;
+    a.max_items = int32_t(L.max_items);
+    a.max_slots = int32_t(L.max_slots);
+    a.num_sms = sms;
+    const float scale = sm_scale > 0.f ? sm_scale : 1.f / sqrtf(float(shape->head_dim));
+    a.scale_log2 = scale * 1.4426950408889634f;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_prefill_plan(a, st);
+    if (e == cudaSuccess) e = launch_prefill_simt(a, q_dtype, kv_dtype, shape->head_dim, st);
+    return launched(e, what);
+}
+}  // namespace
+
+extern "C" {
+
+size_t qskv_prefill_workspace_size(const qskv_shape *shape, int32_t n_tokens) {
+    if (check_shape(shape) != QSKV_OK || check_prefill_tokens(shape, n_tokens) != QSKV_OK) return 0;
+    const int sms = current_sm_count(nullptr);
+    if (sms <= 0) {
+        fail(QSKV_ERR_CUDA, "cannot query the current CUDA device");
+        return 0;
+    }
+    return prefill_workspace(shape, n_tokens, sms);
+}
+
+qskv_status qskv_paged_prefill(const void *q, qskv_dtype q_dtype, int64_t q_stride, const void *k_pool,
+                               const void *v_pool, qskv_dtype kv_dtype, const int32_t *page_table,
+                               const int32_t *seq_lens, const int32_t *cu_new, int32_t n_tokens,
+                               const qskv_shape *shape, float sm_scale, void *out, float *lse, void *workspace,
+                               size_t workspace_bytes, void *stream) {
+    return prefill(q, q_dtype, q_stride, k_pool, v_pool, kv_dtype, nullptr, page_table, seq_lens, cu_new, n_tokens, shape,
+                   sm_scale, out, lse, workspace, workspace_bytes, stream, "paged_prefill launch");
+}
+
+qskv_status qskv_kvf_paged_prefill(const void *q, qskv_dtype q_dtype, int64_t q_stride, const void *pool,
+                                   const int32_t *page_table, const int32_t *seq_lens, const int32_t *cu_new,
+                                   int32_t n_tokens, const qskv_shape *shape, float sm_scale, void *out, float *lse,
+                                   void *workspace, size_t workspace_bytes, void *stream) {
+    if (!pool && n_tokens > 0) return fail(QSKV_ERR_INVALID_ARG, "pool must be non-NULL");
+    return prefill(q, q_dtype, q_stride, nullptr, nullptr, QSKV_BF16, pool, page_table, seq_lens, cu_new, n_tokens, shape,
+                   sm_scale, out, lse, workspace, workspace_bytes, stream, "kvf_paged_prefill launch");
 }
 
 // ------------------------------------------------------------- page tables --

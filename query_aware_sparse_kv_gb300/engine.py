@@ -15,6 +15,17 @@ import torch
 from . import binding as B
 
 
+@contextlib.contextmanager
+def _on(device, stream):
+    """`device` and `stream` (a stream object, a raw handle as the library's calls take it, or None: the device's
+    current one) for torch's own operations."""
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
+
+
 class PagedDecoder:
     """One decode batch over a paged KV cache resident on the GPU.
 
@@ -31,11 +42,12 @@ class PagedDecoder:
     approx_epsilon  None: exact top-K; else the lossy top-K stops refining
                 once at most floor(epsilon * top_k) pages are undecided and
                 samples them from the threshold bucket (seed approx_seed)
+    prefill_tokens  queries that a ``prefill`` may bring (0: none)
     """
 
     def __init__(self, q, k_pool, v_pool, page_table, seq_lens, top_k: Optional[int], sm_scale: float = 0.0,
                  prefix_pages: int = 0, scorer: str = "bound", approx_epsilon: Optional[float] = None,
-                 approx_seed: int = 0):
+                 approx_seed: int = 0, prefill_tokens: int = 0):
         self.approx_epsilon, self.approx_seed = approx_epsilon, approx_seed
         if scorer not in ("bound", "centroid"):
             raise ValueError(f"unknown scorer {scorer!r}")
@@ -56,6 +68,9 @@ class PagedDecoder:
         ws = B.workspace_size(self.shape)
         if self.prefix_pages > 0:
             ws = max(ws, B.cascade_workspace_size(self.shape, self.prefix_pages))
+        self.prefill_tokens = int(prefill_tokens)
+        if self.prefill_tokens > 0:
+            ws = max(ws, B.prefill_workspace_size(self.shape, self.prefill_tokens))
         self.workspace = torch.zeros(ws, dtype=torch.uint8, device=dev)
         k = max(int(top_k or 1), 1)
         self.selected = torch.full((batch, hkv, k), -1, dtype=torch.int32, device=dev)
@@ -69,6 +84,21 @@ class PagedDecoder:
             B.kv_centroid_build(self.k_pool, page_ids, valid_tokens, self.meta, self.shape, self.workspace, stream)
         else:
             B.kv_meta_build(self.k_pool, page_ids, valid_tokens, self.meta, self.shape, self.workspace, stream)
+
+    def prefill(self, q: torch.Tensor, cu_new: torch.Tensor, out: Optional[torch.Tensor] = None,
+                lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Causal attention of the rows' newest tokens, whose keys and values
+        are in the pools and counted by ``seq_lens``: row b's queries are
+        q[cu_new[b]:cu_new[b + 1]] of q [T][Hq][d].  Into ``out`` (q's shape
+        and type; zeros to begin with if none is given), which is returned."""
+        if q.shape[0] > self.prefill_tokens:
+            raise ValueError(f"{q.shape[0]} queries, at most {self.prefill_tokens} a prefill (prefill_tokens)")
+        if out is None:
+            with _on(self.k_pool.device, stream):
+                out = torch.zeros(q.shape, dtype=q.dtype, device=self.k_pool.device)
+        B.paged_prefill(q, self.k_pool, self.v_pool, self.page_table, self.seq_lens, cu_new, out, self.shape,
+                        self.workspace, lse=lse, sm_scale=self.sm_scale, stream=stream)
+        return out
 
     # -- indexer phase -------------------------------------------------------
     @property
@@ -256,6 +286,7 @@ class QuantizedPagedDecoder:
         self.touched_ids, self.touched_valid = i32(touched), i32(touched)
         with torch.cuda.device(self.pool.device):
             size = max(B.kvq_workspace_size(self.shape) if bits == 4 else B.kvf_workspace_size(self.shape),
+                       B.prefill_workspace_size(self.shape, max_tokens) if bits == 8 else 0,
                        B.tables_workspace_size(self.shape),
                        B.workspace_size(self.shape) if top_k is not None else 0)
         self.workspace = torch.zeros(size, dtype=torch.uint8, device=device)
@@ -267,16 +298,9 @@ class QuantizedPagedDecoder:
         self.lengths = [0] * batch  # as of the last extend
         self._new = 0  # tokens of the last extend that append has not stored yet
 
-    @contextlib.contextmanager
     def _on(self, stream):
-        """The decoder's device and `stream` (a stream object, a raw handle as the library's calls take it, or None: the
-        device's current one) for torch's own operations."""
-        device = self.pool.device
-        if stream is not None and not hasattr(stream, "cuda_stream"):
-            handle = int(stream)
-            stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
-        with torch.cuda.device(device), torch.cuda.stream(stream):
-            yield
+        """The decoder's device and `stream` for torch's own operations."""
+        return _on(self.pool.device, stream)
 
     def _pages(self, tokens: int) -> int:
         return -(-tokens // self.shape.page_size)
@@ -359,8 +383,15 @@ class QuantizedPagedDecoder:
         that is refused (ValueError, TypeError, QskvError) leaves lengths,
         pages and cache as they were."""
         self._check_query(q)
+        self._extend_and_append(k, v, [1] * self.shape.batch if new_lens is None else new_lens, stream)
+        if self.top_k is not None:
+            self.select(q, stream)
+        self.decode(q, stream=stream)
+
+    def _extend_and_append(self, k, v, new_lens, stream):
+        """Both, or neither: lengths, pages and cache stay as they were if either is refused."""
         lengths, taken = self.lengths, self._taken
-        self.extend([1] * self.shape.batch if new_lens is None else new_lens, stream)
+        self.extend(new_lens, stream)
         try:
             self.append(k, v, stream)
         except Exception:
@@ -368,9 +399,34 @@ class QuantizedPagedDecoder:
             self.seq_lens, self._lens_out = self._lens_out, self.seq_lens
             self.lengths, self._taken, self._new = lengths, taken, 0
             raise
-        if self.top_k is not None:
-            self.select(q, stream)
-        self.decode(q, stream=stream)
+
+    def prefill(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, new_lens, out: Optional[torch.Tensor] = None,
+                lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Prompts, or chunks of them: the rows' new tokens stored, then the
+        causal attention of all of them, q [sum(new_lens)][Hq][d], over what
+        the rows hold (8-bit caches; all pages, whatever top_k).  Into ``out``
+        (q's shape and type), which is returned.  A call that is refused
+        leaves lengths, pages and cache as they were."""
+        if self.bits != 8:
+            raise ValueError("prefill attends to 8-bit caches (bits=8)")
+        new_lens = [int(x) for x in new_lens]
+        n, s = sum(new_lens), self.shape
+        B._dtype(q)
+        B._rows("q", q, q.dtype, n, s.num_q_heads, s.head_dim, self.pool.get_device())
+        if q.data_ptr() % 16 or (n > 1 and q.stride(0) * q.element_size() % 16):
+            raise ValueError("the rows of q must be 16-byte aligned")
+        for name, t, want in (("out", out, (q.dtype, q.shape)), ("lse", lse, (torch.float32, q.shape[:2]))):
+            if t is not None and ((t.dtype, t.shape) != want or t.get_device() != self.pool.get_device()
+                                  or not t.is_contiguous() or t.data_ptr() % 16):
+                raise ValueError(f"{name} must be {want[0]} {tuple(want[1])}, contiguous, 16-byte aligned and on the "
+                                 f"decoder's device")
+        if out is None:
+            with self._on(stream):
+                out = torch.empty(q.shape, dtype=q.dtype, device=self.pool.device)
+        self._extend_and_append(k, v, new_lens, stream)
+        B.kvf_paged_prefill(q, self.pool, self.page_table, self.seq_lens, self.cu_new, out, s, self.workspace, lse=lse,
+                            sm_scale=self.sm_scale, stream=stream)
+        return out
 
     def gather(self, row: int, dtype=torch.float32, stream=None):
         """The cached keys and values [length][Hkv][d] of a row."""
