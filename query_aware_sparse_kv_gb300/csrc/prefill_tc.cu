@@ -1,0 +1,621 @@
+// Prefill on the tensor cores (qskv_prefill.cuh): bf16 queries over a bf16
+// cache, tcgen05 products with accumulators and softmax weights in tensor
+// memory.
+//
+// A CTA works on a tile of 256 rows (queries x the heads that share a KV
+// head), as two halves of 128, against blocks of 128 keys:
+//   S = Q K^T (128 x 128 a half), P = softmax weights, O += P V (128 x d).
+// The halves take turns on the tensor cores: while one half's logits are being
+// turned into weights, the other's products run.  In tensor memory a half has
+// 128 columns of S, over whose first 64 its P is written as bf16 pairs, and d
+// columns of O.  Roles:
+//   8 softmax warps  one thread a row: reads its 128 logits, keeps the running
+//                    maximum and sum (fp32), writes P.  The maximum a row's
+//                    weights refer to moves only when one would pass 2^8; O
+//                    is then scaled in tensor memory, which its P V before
+//                    that has left by then (the products run in order and S of
+//                    this block was issued after it).  At the end the row's O
+//                    is divided by its sum and stored.
+//   1 MMA thread     issues all products; O += P V of block j, then S of block j + 1.
+//   1 load warp      gathers the pages' keys and values by TMA (boxes of 16
+//                    tokens x 64 dims) into one ring, K and V in turn.
+//   1 list warp      takes items from the list, one ahead, and loads Q.
+// Places without a token (past the row's end, a page that is not there) weigh
+// nothing: their logits are replaced, and the rows of V, which may hold
+// anything, are zeroed in shared memory before the product by the softmax
+// warps of the first half.
+//
+// Every wait is bounded; a wait that gives up flags a timeout and stops the
+// CTA's other roles; copies and products under way complete before the CTA
+// leaves.
+#include <mutex>
+
+#include "qskv_prefill.cuh"
+
+namespace qskv {
+namespace {
+
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kListWarp = 10;
+constexpr int kThreads = 384;
+constexpr int kGoodRing = 16;      // blocks whose page masks are kept (more than the ring's stages)
+constexpr int kItemReaders = kSoftmaxWarps + 2;
+constexpr float kLazy = 8.f;       // weights up to 2^8 before a row's reference moves
+
+template <int D>
+struct Cfg {
+    static constexpr int NB = D / 64;            // 64-dim (128-byte) column groups
+    static constexpr int ATOM = 128 * 128;       // 128 rows x 128 bytes
+    static constexpr int TILE = NB * ATOM;       // 128 rows of Q, K or V
+    static constexpr int STAGES = D == 128 ? 5 : 8;
+    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 1024;
+    static constexpr uint32_t S_COL = 0, O_COL = 256;  // half h: S (and P) at 128 h, O at 256 + 128 h
+};
+
+struct Slot {
+    PrefillItem item;
+    int head;  // KV head; -1: no more items
+};
+
+struct Shared {
+    uint64_t item_full[2], item_empty[2], q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2];
+    uint64_t parts_done, last_known, drain;
+    Slot slot[2];
+    uint32_t good[kGoodRing];  // pages of a block that are there
+    uint32_t tmem;
+    uint32_t last;
+    volatile uint32_t abort;
+};
+
+// Bounded wait that also gives up when another role of the CTA has.
+__device__ __forceinline__ bool wait_phase(Shared &s, uint64_t *bar, uint32_t parity, uint32_t *flags) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (s.abort) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            s.abort = 1u;
+            raise_error(flags, kErrTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+// The same for a whole warp.
+__device__ __forceinline__ bool warp_wait(Shared &s, uint64_t *bar, uint32_t parity, uint32_t *flags) {
+    return __all_sync(0xffffffffu, wait_phase(s, bar, parity, flags));
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// 128 columns of a thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&r)[128]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
+        "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, "
+        "%42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
+        "%62, %63, %64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, "
+        "%82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, "
+        "%101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, "
+        "%117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127"
+        "}, [%128];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
+          "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+          "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
+          "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
+          "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+          "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]),
+          "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]),
+          "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]),
+          "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]),
+          "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two floats in one 64-bit register, an instruction for both.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+template <int REGS>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+// The next item, copied out of its slot.
+struct ItemReader {
+    int slot = 0, phase = 0;
+    __device__ __forceinline__ bool next(Shared &s, Slot &x, uint32_t *flags) {
+        if (!warp_wait(s, &s.item_full[slot], phase, flags)) return false;
+        x = s.slot[slot];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&s.item_empty[slot]);
+        if ((slot ^= 1) == 0) phase ^= 1;
+        return x.head >= 0;
+    }
+};
+
+// ------------------------------------------------------------- softmax --
+template <int D>
+__device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uint32_t tmem) {
+    using C = Cfg<D>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane, tile_row = half * 128 + r;
+    const int G = a.group, shift = 31 - __clz(G), P = a.page_size;
+    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
+    const uint32_t s_at = lanes + C::S_COL + 128 * half, o_at = lanes + C::O_COL + 128 * half;
+    const float sc = a.scale_log2;
+    const uint64_t sc2 = pair(sc, sc);
+    ItemReader items;
+    Slot x;
+    uint32_t s_phase = 0, o_phase = 0, parts_phase = 0;
+    uint32_t stage0 = 0;   // ring stages of the items before this one
+    uint32_t blocks0 = 0;  // and their blocks
+    while (items.next(s, x, a.flags)) {
+        const PrefillItem &it = x.item;
+        const int n = it.block1 - it.block0, end = it.pos + it.tokens;  // keys the tile sees
+        const int token = tile_row >> shift;
+        const bool mine = token < it.tokens;
+        const int limit = mine ? it.pos + token + 1 : end;  // keys the row sees
+        const bool active = half == 0 || it.tokens * G > 128;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < n && ok && active; j++) {
+            ok = warp_wait(s, &s.s_full[half], s_phase, a.flags);
+            if (!ok) break;
+            s_phase ^= 1;
+            tc_fence_after();
+            uint32_t rr[128];
+            tmem_ld128(s_at, rr);
+            const int key0 = (it.block0 + j) * 128;
+            const uint32_t good = s.good[(blocks0 + j) % kGoodRing];
+            const uint32_t whole = (1u << (128 / P)) - 1;
+            const bool cut = good != whole;  // a page is not there, or behind the end
+            if (__any_sync(0xffffffffu, limit < key0 + 128) || cut) {
+                const int lim = limit - key0;
+#pragma unroll
+                for (int k = 0; k < 128; k++)
+                    if (k >= lim || !(good >> (P == 16 ? k / 16 : k / 32) & 1)) rr[k] = 0xff800000u;
+            }
+            float top = __uint_as_float(rr[0]);
+#pragma unroll
+            for (int k = 1; k + 1 < 128; k += 2)
+                top = fmaxf(fmaxf(top, __uint_as_float(rr[k])), __uint_as_float(rr[k + 1]));
+            top = fmaxf(top, __uint_as_float(rr[127])) * sc;
+            if (j == 0) {
+                m = top;
+            } else if (__any_sync(0xffffffffu, top > m + kLazy)) {
+                const float mn = top > m + kLazy ? top : m;
+                const float down = mn == m ? 1.f : ex2(m - mn);
+                m = mn, l *= down;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o_at + c, o);
+#pragma unroll
+                    for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * down);
+                    tmem_st32(o_at + c, o);
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            const uint64_t minus = pair(-base, -base);
+            uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int k = 0; k < 32; k++) {
+                    float u, v;
+                    unpair(fma2(pair(__uint_as_float(rr[64 * c + 2 * k]), __uint_as_float(rr[64 * c + 2 * k + 1])), sc2,
+                                minus),
+                           u, v);
+                    u = ex2(u), v = ex2(v);
+                    sum[k & 3] = add2(sum[k & 3], pair(u, v));
+                    pk[k] = pack_bf16x2(u, v);
+                }
+                tmem_st32(s_at + 32 * c, pk);
+            }
+            float u, v;
+            unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), u, v);
+            l += u + v;
+            if (half == 0 && (cut || key0 + 128 > end)) {  // rows of V without a token: zeros
+                const uint32_t at = stage0 + 2 * j + 1, stage = at % C::STAGES;
+                ok = warp_wait(s, &s.kv_full[stage], at / C::STAGES & 1, a.flags);
+                if (key0 + r >= end || !(good >> (r / P) & 1)) {
+                    uint4 *row = reinterpret_cast<uint4 *>(ring + stage * C::TILE + r * 128);
+#pragma unroll
+                    for (int b = 0; b < C::NB; b++)
+#pragma unroll
+                        for (int k = 0; k < 8; k++) row[b * (C::ATOM / 16) + k] = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            tc_fence_before();
+            mbar_arrive(&s.p_full[half]);
+        }
+        stage0 += 2 * n, blocks0 += n;
+        if (!ok) return;
+        if (active && n > 0) {
+            if (!warp_wait(s, &s.o_full[half], o_phase, a.flags)) return;
+            o_phase ^= 1;
+            tc_fence_after();
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+        const int64_t head = (int64_t(it.token + token) * a.num_q_heads) + x.head * G + (tile_row & (G - 1));
+        uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + head * D);
+        const int64_t slot0 = int64_t(it.slot) * a.num_kv_heads + x.head;  // part p: + p Hkv
+        // of a part: its row's outputs, 4 dims at [dim / 4][row]
+        float4 *part_o = reinterpret_cast<float4 *>(a.part_o) + tile_row;
+        constexpr int64_t kPart = int64_t(D / 4) * kPrefillTcRows;
+        if (active) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32(o_at + c, o);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; k++) o[k] = 0;
+                }
+                if (mine) {
+                    float f[32];
+#pragma unroll
+                    for (int k = 0; k < 32; k++) f[k] = l > 0.f ? __uint_as_float(o[k]) * inv : 0.f;
+                    if (it.parts == 1) {
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            out[c / 8 + k] =
+                                make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]), pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
+                                           pack_bf16x2(f[8 * k + 4], f[8 * k + 5]), pack_bf16x2(f[8 * k + 6], f[8 * k + 7]));
+                    } else {
+                        float4 *to = part_o + (slot0 + int64_t(it.part) * a.num_kv_heads) * kPart + c / 4 * kPrefillTcRows;
+#pragma unroll
+                        for (int k = 0; k < 8; k++)
+                            to[k * kPrefillTcRows] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        tc_fence_before();
+        if (it.parts == 1) {
+            if (mine && a.lse) a.lse[head] = lse2 * 0.6931471805599453f;
+            continue;
+        }
+        // ---- a part: the last one that is done joins them, in their order
+        if (mine) a.part_lse[(slot0 + int64_t(it.part) * a.num_kv_heads) * kPrefillTcRows + tile_row] = lse2;
+        __threadfence();
+        mbar_arrive(&s.parts_done);
+        if (threadIdx.x == 0) {
+            if (wait_phase(s, &s.parts_done, parts_phase, a.flags)) {
+                const uint32_t done = atomicAdd(a.tickets + slot0, 1u);
+                s.last = done == uint32_t(it.parts) - 1;
+                __threadfence();
+                mbar_arrive(&s.last_known);
+            }
+        }
+        __syncwarp();
+        if (!warp_wait(s, &s.last_known, parts_phase, a.flags)) return;
+        parts_phase ^= 1;
+        if (!s.last) continue;
+        __threadfence();
+        if (!mine) continue;
+        const float *part_lse = a.part_lse + slot0 * kPrefillTcRows + tile_row;
+        const int64_t step = int64_t(a.num_kv_heads) * kPrefillTcRows;
+        float most = -INFINITY, total = 0.f;
+        for (int p = 0; p < it.parts; p++) most = fmaxf(most, __ldcg(part_lse + p * step));
+        if (most > -INFINITY)
+            for (int p = 0; p < it.parts; p++) total += ex2(__ldcg(part_lse + p * step) - most);
+        const float share = total > 0.f ? 1.f / total : 0.f;
+        if (a.lse) a.lse[head] = total > 0.f ? (most + log2f(total)) * 0.6931471805599453f : -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < D / 8; c += 4) {
+            float4 f[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) f[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p = 0; p < it.parts; p++) {
+                const float w = most > -INFINITY ? ex2(__ldcg(part_lse + p * step) - most) * share : 0.f;
+                const float4 *from = part_o + (slot0 + int64_t(p) * a.num_kv_heads) * kPart + c * 2 * kPrefillTcRows;
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    const float4 o = __ldcg(from + k * kPrefillTcRows);
+                    f[k].x = fmaf(w, o.x, f[k].x), f[k].y = fmaf(w, o.y, f[k].y);
+                    f[k].z = fmaf(w, o.z, f[k].z), f[k].w = fmaf(w, o.w, f[k].w);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                out[c + k] = make_uint4(pack_bf16x2(f[2 * k].x, f[2 * k].y), pack_bf16x2(f[2 * k].z, f[2 * k].w),
+                                        pack_bf16x2(f[2 * k + 1].x, f[2 * k + 1].y), pack_bf16x2(f[2 * k + 1].z, f[2 * k + 1].w));
+        }
+    }
+}
+
+// ------------------------------------------------------------ products --
+template <int D>
+__device__ void mma_role(const PrefillArgs &a, Shared &s, uint32_t q_at, uint32_t ring_at, uint32_t tmem) {
+    using C = Cfg<D>;
+    constexpr uint32_t id_s = tc_idesc_bf16(128, 128, false, false), id_o = tc_idesc_bf16(128, D, false, true);
+    const bool issuer = (threadIdx.x & 31) == 0;
+    ItemReader items;
+    Slot x;
+    uint32_t q_phase = 0, p_phase = 0, at = 0;  // p_phase: bit h of half h; at: the ring's stage counter
+    bool issued = false;
+    auto logits = [&](int half, uint32_t stage) {
+        const uint32_t k = ring_at + stage * C::TILE, q = q_at + half * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; kk++) {
+            const uint32_t off = (kk >> 2) * C::ATOM + (kk & 3) * 32;
+            tc_mma_bf16(tmem + C::S_COL + 128 * half, tc_sdesc_sw128(q + off, 16, 1024), tc_sdesc_sw128(k + off, 16, 1024),
+                        id_s, kk > 0);
+        }
+        tc_commit(&s.s_full[half]);
+    };
+    while (items.next(s, x, a.flags)) {
+        const int n = x.item.block1 - x.item.block0, halves = x.item.tokens * a.group > 128 ? 2 : 1;
+        bool ok = true;
+        if (issuer && n > 0) {
+            ok = wait_phase(s, &s.q_full, q_phase, a.flags) &&
+                 wait_phase(s, &s.kv_full[at % C::STAGES], at / C::STAGES & 1, a.flags);
+            if (ok) {
+                tc_fence_after();
+                for (int h = 0; h < halves; h++) logits(h, at % C::STAGES);
+                tc_commit(&s.kv_empty[at % C::STAGES]);
+                if (n == 1) tc_commit(&s.q_empty);
+                issued = true;
+            }
+            for (int j = 0; j < n && ok; j++) {
+                const uint32_t v_at = at + 2 * j + 1, k_at = v_at + 1;
+                const uint32_t v = v_at % C::STAGES, k = k_at % C::STAGES;
+                ok = wait_phase(s, &s.kv_full[v], v_at / C::STAGES & 1, a.flags);
+                for (int h = 0; h < halves && ok; h++) {
+                    ok = wait_phase(s, &s.p_full[h], p_phase >> h & 1, a.flags);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t va = ring_at + v * C::TILE;
+#pragma unroll
+                    for (int ks = 0; ks < 8; ks++)  // A = P from tensor memory (8 columns: 16 keys); B = V, dims contiguous
+                        tc_mma_bf16_ts(tmem + C::O_COL + 128 * h, tmem + C::S_COL + 128 * h + ks * 8,
+                                       tc_sdesc_sw128(va + ks * 16 * 128, C::ATOM, 1024), id_o, j > 0 || ks > 0);
+                    if (j + 1 == n) {
+                        tc_commit(&s.o_full[h]);
+                        continue;
+                    }
+                    if (h == 0) ok = wait_phase(s, &s.kv_full[k], k_at / C::STAGES & 1, a.flags);
+                    if (!ok) break;
+                    logits(h, k);
+                }
+                if (!ok) break;
+                p_phase ^= (1u << halves) - 1;
+                tc_commit(&s.kv_empty[v]);
+                if (j + 1 < n) tc_commit(&s.kv_empty[k]);
+                if (j + 2 == n) tc_commit(&s.q_empty);
+            }
+            q_phase ^= 1, at += 2 * n;
+        }
+        if (!__all_sync(0xffffffffu, ok)) break;
+    }
+    if (issuer && issued) {  // every product has completed before the tensor memory is freed
+        tc_commit(&s.drain);
+        mbar_wait_bounded(&s.drain, 0, kWaitLimitNs);
+    }
+    __syncwarp();
+}
+
+// --------------------------------------------------------------- loads --
+template <int D>
+__device__ void load_role(const PrefillArgs &a, Shared &s, uint8_t *ring, const CUtensorMap *map_k, const CUtensorMap *map_v) {
+    using C = Cfg<D>;
+    const int lane = threadIdx.x & 31, P = a.page_size, ppb = 128 / P, boxes = P / 16;
+    ItemReader items;
+    Slot x;
+    uint32_t at = 0, blocks0 = 0;
+    bool ok = true;
+    while (ok && items.next(s, x, a.flags)) {
+        const PrefillItem &it = x.item;
+        const int n = it.block1 - it.block0, end = it.pos + it.tokens;
+        // lane j < ppb holds page j of a block, -1 where there is none; read a block ahead
+        auto page_of = [&](int j) {
+            const int page = (it.block0 + j) * ppb + lane;
+            if (lane >= ppb || j >= n || page * P >= end) return -1;
+            const int id = __ldg(a.page_table + int64_t(it.row) * a.max_pages + page);
+            if (id < 0 || id >= a.num_pool_pages) {
+                raise_error(a.flags, kErrPageId);
+                return -1;
+            }
+            return id;
+        };
+        int next = page_of(0);
+        for (int j = 0; j < n && ok; j++) {
+            const int id = next;
+            next = page_of(j + 1);
+            const uint32_t good = __ballot_sync(0xffffffffu, id >= 0);
+            for (int which = 0; which < 2 && ok; which++, at++) {
+                const uint32_t stage = at % C::STAGES;
+                if (at >= C::STAGES) ok = warp_wait(s, &s.kv_empty[stage], (at / C::STAGES - 1) & 1, a.flags);
+                if (!ok) break;
+                if (lane == 0) {
+                    if (which == 0) s.good[(blocks0 + j) % kGoodRing] = good;
+                    mbar_arrive_expect_tx(&s.kv_full[stage], __popc(good) * P * D * 2);
+                }
+                __syncwarp();
+                if (id >= 0) {
+                    uint8_t *to = ring + stage * C::TILE + lane * P * 128;
+                    const int y = (id * a.num_kv_heads + x.head) * P;
+                    for (int b = 0; b < boxes; b++)
+#pragma unroll
+                        for (int c = 0; c < C::NB; c++)
+                            tma_load_2d(to + b * 16 * 128 + c * C::ATOM, which ? map_v : map_k, c * 64, y + b * 16,
+                                        &s.kv_full[stage]);
+                }
+            }
+        }
+        blocks0 += n;
+    }
+    // copies under way land before the CTA's memory is released
+    const uint32_t first = at > C::STAGES ? at - C::STAGES : 0;
+    for (uint32_t i = first; i < at; i++) mbar_wait_bounded(&s.kv_full[i % C::STAGES], i / C::STAGES & 1, kWaitLimitNs);
+}
+
+// Takes items from the list, one ahead of the CTA's other roles, and loads their queries.
+template <int D>
+__device__ void list_role(const PrefillArgs &a, Shared &s, uint8_t *q, const CUtensorMap *map_q) {
+    using C = Cfg<D>;
+    if ((threadIdx.x & 31) != 0) return;
+    const int total = int(__ldcg(&a.plan->items)) * a.num_kv_heads, per = 128 / a.group;
+    int slot = 0, phase = 0, q_phase = 0;
+    bool q_used = false;
+    for (int i = 0;; i++) {
+        const int next = int(atomicAdd(&a.plan->next, 1u));
+        if (i >= 2 && !wait_phase(s, &s.item_empty[slot], phase ^ 1, a.flags)) break;
+        Slot x;
+        x.head = -1;
+        if (next < total) {
+            const int4 *from = reinterpret_cast<const int4 *>(a.items + next / a.num_kv_heads);
+            int4 *to = reinterpret_cast<int4 *>(&x.item);
+#pragma unroll
+            for (int k = 0; k < int(sizeof(PrefillItem) / 16); k++) to[k] = __ldcg(from + k);
+            x.head = next % a.num_kv_heads;
+        }
+        s.slot[slot] = x;
+        mbar_arrive(&s.item_full[slot]);
+        if (x.head < 0) break;
+        if ((slot ^= 1) == 0) phase ^= 1;
+        if (x.item.block1 == x.item.block0) continue;
+        if (q_used) {
+            if (!wait_phase(s, &s.q_empty, q_phase, a.flags)) break;
+            q_phase ^= 1;
+        }
+        q_used = true;
+        const int halves = x.item.tokens > per ? 2 : 1;
+        mbar_arrive_expect_tx(&s.q_full, halves * C::TILE);
+        for (int h = 0; h < halves; h++)
+#pragma unroll
+            for (int c = 0; c < C::NB; c++)
+                tma_load_3d(q + h * C::TILE + c * C::ATOM, map_q, c * 64, x.head * a.group, x.item.token + h * per, &s.q_full);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PrefillArgs a) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t raw[];
+    __shared__ Shared s;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *q = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *ring = q + 2 * C::TILE;
+    if (threadIdx.x == 0) {
+        s.abort = 0u;
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&s.item_full[i], 1);
+            mbar_init(&s.item_empty[i], kItemReaders);
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.p_full[i], 128);
+            mbar_init(&s.o_full[i], 1);
+        }
+        mbar_init(&s.q_full, 1);
+        mbar_init(&s.q_empty, 1);
+        for (int i = 0; i < C::STAGES; i++) {
+            mbar_init(&s.kv_full[i], 1);
+            mbar_init(&s.kv_empty[i], 1);
+        }
+        mbar_init(&s.parts_done, 32 * kSoftmaxWarps);
+        mbar_init(&s.last_known, 1);
+        mbar_init(&s.drain, 1);
+        mbar_fence_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(&s.tmem, 512);
+    if (warp == kListWarp && lane == 0) {
+        prefetch_tensormap(&map_q);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();
+    pdl_wait();
+    // registers a thread: 2 x 208 + 88, what the launch has (3 x 168)
+    if (warp < kSoftmaxWarps) {
+        regs_inc<208>();
+        softmax_role<D>(a, s, ring, s.tmem);
+    } else {
+        regs_dec<88>();
+        if (warp == kMmaWarp) {
+            mma_role<D>(a, s, smem_u32(q), smem_u32(ring), s.tmem);
+        } else if (warp == kLoadWarp) {
+            load_role<D>(a, s, ring, &map_k, &map_v);
+        } else if (warp == kListWarp) {
+            list_role<D>(a, s, q, &map_q);
+            __syncwarp();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(s.tmem, 512);
+}
+
+template <int D>
+cudaError_t launch_dim(const PrefillArgs &a, const CUtensorMap *q, const CUtensorMap *k, const CUtensorMap *v,
+                       cudaStream_t stream) {
+    auto kernel = prefill_tc_kernel<D>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t most = int64_t(a.max_items) * a.num_kv_heads;
+    return launch_pdl(kernel, dim3(unsigned(most < a.num_sms ? most : a.num_sms)), dim3(kThreads), size_t(Cfg<D>::SMEM), stream,
+                      *q, *k, *v, a);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_tc(const PrefillArgs &a, const CUtensorMap *q, const CUtensorMap *k, const CUtensorMap *v,
+                              int head_dim, cudaStream_t stream) {
+    return head_dim == 128 ? launch_dim<128>(a, q, k, v, stream) : launch_dim<64>(a, q, k, v, stream);
+}
+
+}  // namespace qskv

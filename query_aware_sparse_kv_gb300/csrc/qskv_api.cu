@@ -183,6 +183,24 @@ qskv_status make_pool_map(CUtensorMap *map, const void *pool, const qskv_shape *
     return QSKV_OK;
 }
 
+// Queries as a 3-D bf16 tensor [n_tokens][Hq][D] (tokens q_stride elements
+// apart), loaded as the 128 rows (token, head of the group) of half a prefill
+// tile: boxes of 64 dims x G heads x 128 / G tokens.
+qskv_status make_query_map(CUtensorMap *map, const void *q, int64_t q_stride, int64_t n_tokens, const qskv_shape *s) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(QSKV_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+    const cuuint32_t G = cuuint32_t(s->num_q_heads / s->num_kv_heads);
+    const cuuint64_t dims[3] = {cuuint64_t(s->head_dim), cuuint64_t(s->num_q_heads), cuuint64_t(n_tokens)};
+    const cuuint64_t strides[2] = {cuuint64_t(s->head_dim) * 2, cuuint64_t(q_stride) * 2};
+    const cuuint32_t box[3] = {64, G, 128 / G};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(QSKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+    return QSKV_OK;
+}
+
 qskv_status launched(cudaError_t e, const char *what) {
     if (e != cudaSuccess) return fail(QSKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
     return ok();
@@ -1217,7 +1235,9 @@ struct PrefillWorkspace {
 };
 
 size_t prefill_workspace(const qskv_shape *s, int64_t n_tokens, int num_sms) {
-    return PrefillWorkspace(s, n_tokens, num_sms, kPrefillSimtRows, 0).total;
+    const size_t x = PrefillWorkspace(s, n_tokens, num_sms, kPrefillSimtRows, 0).total;
+    const size_t y = PrefillWorkspace(s, n_tokens, num_sms, kPrefillTcRows, kPrefillWaves).total;
+    return x > y ? x : y;
 }
 
 qskv_status check_prefill_tokens(const qskv_shape *s, int64_t n_tokens) {
@@ -1253,9 +1273,10 @@ qskv_status prefill(const void *q, qskv_dtype q_dtype, int64_t q_stride, const v
     if (sms <= 0) return fail(QSKV_ERR_CUDA, "cannot query the current CUDA device");
     QSKV_TRY(check_workspace(workspace, workspace_bytes, prefill_workspace(shape, n_tokens, sms)));
     PrefillArgs a = {};
-    a.tile_rows = kPrefillSimtRows;
-    a.block_keys = kPrefillSimtKeys;
-    a.waves = 0;
+    const bool tensor_cores = q_dtype == QSKV_BF16 && kv_dtype == QSKV_BF16 && !pool;
+    a.tile_rows = tensor_cores ? kPrefillTcRows : kPrefillSimtRows;
+    a.block_keys = tensor_cores ? kPrefillTcKeys : kPrefillSimtKeys;
+    a.waves = tensor_cores ? kPrefillWaves : 0;
     const PrefillWorkspace L(shape, n_tokens, sms, a.tile_rows, a.waves);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.q = q;
@@ -1289,8 +1310,16 @@ qskv_status prefill(const void *q, qskv_dtype q_dtype, int64_t q_stride, const v
     const float scale = sm_scale > 0.f ? sm_scale : 1.f / sqrtf(float(shape->head_dim));
     a.scale_log2 = scale * 1.4426950408889634f;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    CUtensorMap tq, tk, tv;
+    if (tensor_cores) {
+        QSKV_TRY(make_query_map(&tq, q, q_stride, n_tokens, shape));
+        QSKV_TRY(make_pool_map(&tk, k_pool, shape));
+        QSKV_TRY(make_pool_map(&tv, v_pool, shape));
+    }
     cudaError_t e = launch_prefill_plan(a, st);
-    if (e == cudaSuccess) e = launch_prefill_simt(a, q_dtype, kv_dtype, shape->head_dim, st);
+    if (e == cudaSuccess)
+        e = tensor_cores ? launch_prefill_tc(a, &tq, &tk, &tv, shape->head_dim, st)
+                         : launch_prefill_simt(a, q_dtype, kv_dtype, shape->head_dim, st);
     return launched(e, what);
 }
 }  // namespace

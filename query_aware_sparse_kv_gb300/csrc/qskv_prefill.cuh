@@ -76,9 +76,13 @@ __device__ __forceinline__ void prefill_row(const PrefillArgs &a, int b, int &fi
 // Which kernel a call takes, and the sizes of its work: tiles of kPrefillTcRows rows on the tensor cores (bf16 queries
 // over bf16 or 8-bit caches), of kPrefillSimtRows in fp32 arithmetic.
 constexpr int kPrefillTcRows = 256, kPrefillTcKeys = 128;
+constexpr int kPrefillWaves = 2;
 constexpr int kPrefillSimtRows = 64, kPrefillSimtKeys = 64;
 
 cudaError_t launch_prefill_plan(const PrefillArgs &a, cudaStream_t stream);
+// q: the queries as [n_tokens][Hq][D], boxes of 64 dims x G heads x 128 / G tokens; k, v: the pools' 16 x 64 boxes.
+cudaError_t launch_prefill_tc(const PrefillArgs &a, const CUtensorMap *q, const CUtensorMap *k, const CUtensorMap *v,
+                              int head_dim, cudaStream_t stream);
 cudaError_t launch_prefill_simt(const PrefillArgs &a, int q_dtype, int kv_dtype, int head_dim, cudaStream_t stream);
 
 }  // namespace qskv
