@@ -1,6 +1,6 @@
-// Prefill on the tensor cores (qskv_prefill.cuh): bf16 queries over a bf16
-// cache, tcgen05 products with accumulators and softmax weights in tensor
-// memory.
+// Prefill on the tensor cores (qskv_prefill.cuh): bf16 queries over a bf16 or
+// an 8-bit cache, tcgen05 products with accumulators and softmax weights in
+// tensor memory.
 //
 // A CTA works on a tile of 256 rows (queries x the heads that share a KV
 // head), as two halves of 128, against blocks of 128 keys:
@@ -18,7 +18,12 @@
 //                    is divided by its sum and stored.
 //   1 MMA thread     issues all products; O += P V of block j, then S of block j + 1.
 //   1 load warp      gathers the pages' keys and values by TMA (boxes of 16
-//                    tokens x 64 dims) into one ring, K and V in turn.
+//                    tokens x 64 dims) into one ring, K and V in turn; for an
+//                    8-bit cache
+//   4 convert warps  do: a code times its power of two is a bf16 number, so
+//                    they fill the ring with the cached values as they are.
+//                    The codes of the next K or V are on their way while one is
+//                    converted.
 //   1 list warp      takes items from the list, one ahead, and loads Q.
 // Places without a token (past the row's end, a page that is not there) weigh
 // nothing: their logits are replaced, and the rows of V, which may hold
@@ -30,15 +35,20 @@
 // leaves.
 #include <mutex>
 
+#include <cuda_fp16.h>
+
+#include "qskv_kvf.cuh"
 #include "qskv_prefill.cuh"
 
 namespace qskv {
 namespace {
 
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kListWarp = 10;
-constexpr int kThreads = 384;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kListWarp = 10, kConvertWarp = 12;
+template <bool KVF>
+constexpr int kThreads = KVF ? 512 : 384;
 constexpr int kGoodRing = 16;      // blocks whose page masks are kept (more than the ring's stages)
-constexpr int kItemReaders = kSoftmaxWarps + 2;
+template <bool KVF>
+constexpr int kItemReaders = kSoftmaxWarps + 1 + (KVF ? 4 : 1);
 constexpr float kLazy = 8.f;       // weights up to 2^8 before a row's reference moves
 
 template <int D>
@@ -94,19 +104,15 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
-// 128 columns of a thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&r)[128]) {
+// 64 columns of a thread's TMEM lane, not waited for.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
         "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
         "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, "
         "%42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
-        "%62, %63, %64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, "
-        "%82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, "
-        "%101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, "
-        "%117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127"
-        "}, [%128];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "%62, %63"
+        "}, [%64];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
           "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
@@ -114,18 +120,22 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&r)[128]) {
           "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
           "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
           "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
-          "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
-          "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
-          "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
-          "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
-          "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]),
-          "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]),
-          "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]),
-          "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]),
-          "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
         : "r"(taddr)
         : "memory");
+}
+// Waits for the loads before it; nothing reads r earlier.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[64], bool wait) {
+    if (wait) asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    asm volatile(""
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+          "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+          "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]),
+          "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]),
+          "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]),
+          "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
+          "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63]));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -177,7 +187,7 @@ struct ItemReader {
 };
 
 // ------------------------------------------------------------- softmax --
-template <int D>
+template <int D, bool KVF>
 __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uint32_t tmem) {
     using C = Cfg<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2, quarter = warp & 3;
@@ -206,8 +216,11 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
             if (!ok) break;
             s_phase ^= 1;
             tc_fence_after();
-            uint32_t rr[128];
-            tmem_ld128(s_at, rr);
+            uint32_t rr[2][64];
+            tmem_ld64(s_at, rr[0]);
+            tmem_ld64(s_at + 64, rr[1]);
+            tmem_ld_wait(rr[0], true);
+            tmem_ld_wait(rr[1], false);
             const int key0 = (it.block0 + j) * 128;
             const uint32_t good = s.good[(blocks0 + j) % kGoodRing];
             const uint32_t whole = (1u << (128 / P)) - 1;
@@ -216,13 +229,16 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
                 const int lim = limit - key0;
 #pragma unroll
                 for (int k = 0; k < 128; k++)
-                    if (k >= lim || !(good >> (P == 16 ? k / 16 : k / 32) & 1)) rr[k] = 0xff800000u;
+                    if (k >= lim || !(good >> (P == 16 ? k / 16 : k / 32) & 1)) rr[k / 64][k % 64] = 0xff800000u;
             }
-            float top = __uint_as_float(rr[0]);
+            float most[4];
 #pragma unroll
-            for (int k = 1; k + 1 < 128; k += 2)
-                top = fmaxf(fmaxf(top, __uint_as_float(rr[k])), __uint_as_float(rr[k + 1]));
-            top = fmaxf(top, __uint_as_float(rr[127])) * sc;
+            for (int k = 0; k < 4; k++) most[k] = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 128; k += 2)
+                most[k / 2 & 3] = fmaxf(fmaxf(most[k / 2 & 3], __uint_as_float(rr[k / 64][k % 64])),
+                                        __uint_as_float(rr[k / 64][k % 64 + 1]));
+            const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * sc;
             if (j == 0) {
                 m = top;
             } else if (__any_sync(0xffffffffu, top > m + kLazy)) {
@@ -247,8 +263,7 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
 #pragma unroll
                 for (int k = 0; k < 32; k++) {
                     float u, v;
-                    unpair(fma2(pair(__uint_as_float(rr[64 * c + 2 * k]), __uint_as_float(rr[64 * c + 2 * k + 1])), sc2,
-                                minus),
+                    unpair(fma2(pair(__uint_as_float(rr[c][2 * k]), __uint_as_float(rr[c][2 * k + 1])), sc2, minus),
                            u, v);
                     u = ex2(u), v = ex2(v);
                     sum[k & 3] = add2(sum[k & 3], pair(u, v));
@@ -259,7 +274,7 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
             float u, v;
             unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), u, v);
             l += u + v;
-            if (half == 0 && (cut || key0 + 128 > end)) {  // rows of V without a token: zeros
+            if (!KVF && half == 0 && (cut || key0 + 128 > end)) {  // rows of V without a token: zeros
                 const uint32_t at = stage0 + 2 * j + 1, stage = at % C::STAGES;
                 ok = warp_wait(s, &s.kv_full[stage], at / C::STAGES & 1, a.flags);
                 if (key0 + r >= end || !(good >> (r / P) & 1)) {
@@ -499,6 +514,120 @@ __device__ void load_role(const PrefillArgs &a, Shared &s, uint8_t *ring, const 
     for (uint32_t i = first; i < at; i++) mbar_wait_bounded(&s.kv_full[i % C::STAGES], i / C::STAGES & 1, kWaitLimitNs);
 }
 
+// The same for an 8-bit cache.  A part of 16 tokens has D chunks of 16 bytes of keys and as many of values, a thread each.
+template <int D>
+__device__ void convert_role(const PrefillArgs &a, Shared &s, uint8_t *ring) {
+    using C = Cfg<D>;
+    constexpr int PARTS = 128 / D, LOADS = 8 / PARTS;  // parts the threads cover at once, and how often they do
+    const int lane = threadIdx.x & 31, tid = threadIdx.x - 32 * kConvertWarp;
+    const int P = a.page_size, per_page = P / 16, c = tid % D;
+    // keys: token and first 16-byte chunk (16 dims); values: pair of tokens and chunk (8 dims)
+    const int kt = c / (D / 16), kc = kvf_key_chunk<D>(c % (D / 16), kt);
+    const int vp = c / (D / 8), vc = kvf_value_chunk<D>(c % (D / 8), vp);
+    ItemReader items;
+    Slot x;
+    uint32_t at = 0, blocks0 = 0;
+    bool ok = true;
+    while (ok && items.next(s, x, a.flags)) {
+        const PrefillItem &it = x.item;
+        const int n = it.block1 - it.block0, end = it.pos + it.tokens;
+        auto page_of = [&](int j) {  // lane p < 8: the page of part p of a block, -1 where there is none
+            const int t = (it.block0 + j) * 128 + lane * 16;
+            if (lane >= 8 || j >= n || t >= end) return -1;
+            const int id = __ldg(a.page_table + int64_t(it.row) * a.max_pages + t / P);
+            if (id < 0 || id >= a.num_pool_pages) {
+                raise_error(a.flags, kErrPageId);
+                return -1;
+            }
+            return id;
+        };
+        uint4 codes[LOADS];
+        uint32_t powers[LOADS];
+        auto load = [&](int i, int which, int ids) {  // chunk i of the thread: its codes and their tokens' powers
+            const int part = i * PARTS + tid / D, id = __shfl_sync(0xffffffffu, ids, part);
+            codes[i] = make_uint4(0, 0, 0, 0), powers[i] = 0;
+            if (id < 0) return;
+            const uint8_t *from =
+                a.pool + ((int64_t(id) * a.num_kv_heads + x.head) * per_page + part % per_page) * kvf_part_bytes(D);
+            codes[i] = __ldg(reinterpret_cast<const uint4 *>(from + which * 16 * D + c * 16));
+            if (which)
+                powers[i] = __ldg(reinterpret_cast<const uint16_t *>(from + 32 * D + 16) + vp);
+            else
+                powers[i] = __ldg(from + 32 * D + kt);
+        };
+        int ids = page_of(0), next = -1;
+        if (n > 0) {
+#pragma unroll
+            for (int i = 0; i < LOADS; i++) load(i, 0, ids);
+        }
+        for (int j = 0; j < n && ok; j++) {
+            const int key0 = (it.block0 + j) * 128;
+            next = page_of(j + 1);
+            const int page = __shfl_sync(0xffffffffu, ids, lane * per_page & 7);
+            const uint32_t good = __ballot_sync(0xffffffffu, lane < 128 / P && page >= 0);
+#pragma unroll
+            for (int which = 0; which < 2; which++, at++) {
+                const uint32_t stage = at % C::STAGES;
+                if (at >= C::STAGES) ok = warp_wait(s, &s.kv_empty[stage], (at / C::STAGES - 1) & 1, a.flags);
+                if (!ok) break;
+                if (which == 0 && tid == 0) s.good[(blocks0 + j) % kGoodRing] = good;
+                uint8_t *to = ring + stage * C::TILE;
+#pragma unroll
+                for (int i = 0; i < LOADS; i++) {
+                    const uint4 w = codes[i];
+                    const uint32_t e = powers[i];
+                    load(i, which ^ 1, which ? next : ids);
+                    const int row0 = (i * PARTS + tid / D) * 16 + (which ? 2 * vp : kt);
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t y[2][4];
+                    if (which) {  // bytes in turn of both tokens
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            // what lies past the end may be no number
+                            const bool in = key0 + row0 + h < end;
+                            const float power = in ? kvf_power(e >> (8 * h) & 255) : 0.f;
+#pragma unroll
+                            for (int k = 0; k < 4; k++) {
+                                const uint32_t f = kvf_half2(__byte_perm(u[k], 0, h ? 0x0031 : 0x0020));
+                                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f));
+                                y[h][k] = in ? pack_bf16x2(v.x * power, v.y * power) : 0u;
+                            }
+                        }
+                        const int col = vc / 8 * C::ATOM;
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            const int row = row0 + h;
+                            *reinterpret_cast<uint4 *>(to + col + row * 128 + (((vc & 7) ^ (row & 7)) << 4)) =
+                                make_uint4(y[h][0], y[h][1], y[h][2], y[h][3]);
+                        }
+                    } else {
+                        const float power = kvf_power(e);
+#pragma unroll
+                        for (int k = 0; k < 8; k++) {
+                            const uint32_t f = kvf_half2(u[k / 2] >> (16 * (k & 1)));
+                            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f));
+                            y[k / 4][k % 4] = pack_bf16x2(v.x * power, v.y * power);
+                        }
+                        // the lanes of the upper half of the dims store theirs the other way round: all banks are met
+                        const int swap = D == 128 ? kc >> 2 & 1 : 0;
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            const int k = (kc & 3) * 2 + (h ^ swap);
+                            const uint4 v = swap ? make_uint4(y[h ^ 1][0], y[h ^ 1][1], y[h ^ 1][2], y[h ^ 1][3])
+                                                 : make_uint4(y[h][0], y[h][1], y[h][2], y[h][3]);
+                            *reinterpret_cast<uint4 *>(to + kc / 4 * C::ATOM + row0 * 128 + ((k ^ (row0 & 7)) << 4)) = v;
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&s.kv_full[stage]);
+            }
+            ids = next;
+        }
+        blocks0 += n;
+    }
+}
+
 // Takes items from the list, one ahead of the CTA's other roles, and loads their queries.
 template <int D>
 __device__ void list_role(const PrefillArgs &a, Shared &s, uint8_t *q, const CUtensorMap *map_q) {
@@ -538,8 +667,8 @@ __device__ void list_role(const PrefillArgs &a, Shared &s, uint8_t *q, const CUt
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool KVF>
+__global__ void __launch_bounds__(kThreads<KVF>, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PrefillArgs a) {
     using C = Cfg<D>;
@@ -552,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         s.abort = 0u;
         for (int i = 0; i < 2; i++) {
             mbar_init(&s.item_full[i], 1);
-            mbar_init(&s.item_empty[i], kItemReaders);
+            mbar_init(&s.item_empty[i], kItemReaders<KVF>);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_full[i], 128);
             mbar_init(&s.o_full[i], 1);
@@ -560,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&s.q_full, 1);
         mbar_init(&s.q_empty, 1);
         for (int i = 0; i < C::STAGES; i++) {
-            mbar_init(&s.kv_full[i], 1);
+            mbar_init(&s.kv_full[i], KVF ? 128 : 1);
             mbar_init(&s.kv_empty[i], 1);
         }
         mbar_init(&s.parts_done, 32 * kSoftmaxWarps);
@@ -571,28 +700,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tmem_alloc(&s.tmem, 512);
     if (warp == kListWarp && lane == 0) {
         prefetch_tensormap(&map_q);
-        prefetch_tensormap(&map_k);
-        prefetch_tensormap(&map_v);
+        if (!KVF) {
+            prefetch_tensormap(&map_k);
+            prefetch_tensormap(&map_v);
+        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     pdl_trigger();
     pdl_wait();
-    // registers a thread: 2 x 208 + 88, what the launch has (3 x 168)
+    // registers a thread: shares of what the launch has, 3 x 168 (2 x 208 + 88) or 4 x 128 (2 x 184 + 40 + 104)
     if (warp < kSoftmaxWarps) {
-        regs_inc<208>();
-        softmax_role<D>(a, s, ring, s.tmem);
-    } else {
-        regs_dec<88>();
+        regs_inc<KVF ? 184 : 208>();
+        softmax_role<D, KVF>(a, s, ring, s.tmem);
+    } else if (warp < kConvertWarp) {
+        regs_dec<KVF ? 40 : 88>();
         if (warp == kMmaWarp) {
             mma_role<D>(a, s, smem_u32(q), smem_u32(ring), s.tmem);
-        } else if (warp == kLoadWarp) {
+        } else if (!KVF && warp == kLoadWarp) {
             load_role<D>(a, s, ring, &map_k, &map_v);
         } else if (warp == kListWarp) {
             list_role<D>(a, s, q, &map_q);
             __syncwarp();
         }
+    } else if constexpr (KVF) {
+        regs_dec<104>();
+        convert_role<D>(a, s, ring);
     }
     tc_fence_before();
     __syncthreads();
@@ -600,22 +734,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tmem_dealloc(s.tmem, 512);
 }
 
-template <int D>
-cudaError_t launch_dim(const PrefillArgs &a, const CUtensorMap *q, const CUtensorMap *k, const CUtensorMap *v,
+template <int D, bool KVF>
+cudaError_t launch_one(const PrefillArgs &a, const CUtensorMap *q, const CUtensorMap *k, const CUtensorMap *v,
                        cudaStream_t stream) {
-    auto kernel = prefill_tc_kernel<D>;
+    auto kernel = prefill_tc_kernel<D, KVF>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t most = int64_t(a.max_items) * a.num_kv_heads;
-    return launch_pdl(kernel, dim3(unsigned(most < a.num_sms ? most : a.num_sms)), dim3(kThreads), size_t(Cfg<D>::SMEM), stream,
-                      *q, *k, *v, a);
+    return launch_pdl(kernel, dim3(unsigned(most < a.num_sms ? most : a.num_sms)), dim3(kThreads<KVF>),
+                      size_t(Cfg<D>::SMEM), stream, *q, *k, *v, a);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill_tc(const PrefillArgs &a, const CUtensorMap *q, const CUtensorMap *k, const CUtensorMap *v,
                               int head_dim, cudaStream_t stream) {
-    return head_dim == 128 ? launch_dim<128>(a, q, k, v, stream) : launch_dim<64>(a, q, k, v, stream);
+    if (a.pool) return head_dim == 128 ? launch_one<128, true>(a, q, k, v, stream) : launch_one<64, true>(a, q, k, v, stream);
+    return head_dim == 128 ? launch_one<128, false>(a, q, k, v, stream) : launch_one<64, false>(a, q, k, v, stream);
 }
 
 }  // namespace qskv

@@ -1273,7 +1273,7 @@ qskv_status prefill(const void *q, qskv_dtype q_dtype, int64_t q_stride, const v
     if (sms <= 0) return fail(QSKV_ERR_CUDA, "cannot query the current CUDA device");
     QSKV_TRY(check_workspace(workspace, workspace_bytes, prefill_workspace(shape, n_tokens, sms)));
     PrefillArgs a = {};
-    const bool tensor_cores = q_dtype == QSKV_BF16 && kv_dtype == QSKV_BF16 && !pool;
+    const bool tensor_cores = q_dtype == QSKV_BF16 && kv_dtype == QSKV_BF16;
     a.tile_rows = tensor_cores ? kPrefillTcRows : kPrefillSimtRows;
     a.block_keys = tensor_cores ? kPrefillTcKeys : kPrefillSimtKeys;
     a.waves = tensor_cores ? kPrefillWaves : 0;
@@ -1313,8 +1313,13 @@ qskv_status prefill(const void *q, qskv_dtype q_dtype, int64_t q_stride, const v
     CUtensorMap tq, tk, tv;
     if (tensor_cores) {
         QSKV_TRY(make_query_map(&tq, q, q_stride, n_tokens, shape));
-        QSKV_TRY(make_pool_map(&tk, k_pool, shape));
-        QSKV_TRY(make_pool_map(&tv, v_pool, shape));
+        if (pool) {
+            memset(&tk, 0, sizeof tk);  // not used
+            memset(&tv, 0, sizeof tv);
+        } else {
+            QSKV_TRY(make_pool_map(&tk, k_pool, shape));
+            QSKV_TRY(make_pool_map(&tv, v_pool, shape));
+        }
     }
     cudaError_t e = launch_prefill_plan(a, st);
     if (e == cudaSuccess)
