@@ -389,71 +389,103 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
 }
 
 // ------------------------------------------------------------ products --
+// One lane of the warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// The whole warp follows the pipeline, so that what a product is issued with is the same in all lanes and known to be:
+// with one lane in this code a product took the issuing thread 100 clocks, 470 with few registers, of which it runs 64.
 template <int D>
-__device__ void mma_role(const PrefillArgs &a, Shared &s, uint32_t q_at, uint32_t ring_at, uint32_t tmem) {
+__device__ __forceinline__ void mma_role(const PrefillArgs &a, Shared &s, uint32_t q_at, uint32_t ring_at) {
     using C = Cfg<D>;
     constexpr uint32_t id_s = tc_idesc_bf16(128, 128, false, false), id_o = tc_idesc_bf16(128, D, false, true);
-    const bool issuer = (threadIdx.x & 31) == 0;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
+    const uint64_t q_desc = tc_sdesc_sw128(q_at, 16, 1024), k_desc = tc_sdesc_sw128(ring_at, 16, 1024);
+    const uint64_t v_desc = tc_sdesc_sw128(ring_at, C::ATOM, 1024);  // dims contiguous
     ItemReader items;
     Slot x;
-    uint32_t q_phase = 0, p_phase = 0, at = 0;  // p_phase: bit h of half h; at: the ring's stage counter
+    uint32_t q_phase = 0, p_phase = 0;  // p_phase: bit h of half h
+    uint32_t stage = 0, phase = 0;      // of the ring
     bool issued = false;
-    auto logits = [&](int half, uint32_t stage) {
-        const uint32_t k = ring_at + stage * C::TILE, q = q_at + half * C::TILE;
+    auto advance = [&] {
+        if (++stage == C::STAGES) stage = 0, phase ^= 1;
+    };
+    auto logits = [&](int half, uint32_t k) {
+        if (elect_one()) {
+            const uint64_t qd = q_desc + half * (C::TILE >> 4), kd = k_desc + k * (C::TILE >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; kk++) {
-            const uint32_t off = (kk >> 2) * C::ATOM + (kk & 3) * 32;
-            tc_mma_bf16(tmem + C::S_COL + 128 * half, tc_sdesc_sw128(q + off, 16, 1024), tc_sdesc_sw128(k + off, 16, 1024),
-                        id_s, kk > 0);
+            for (int kk = 0; kk < D / 16; kk++) {
+                const uint32_t off = ((kk >> 2) * C::ATOM + (kk & 3) * 32) >> 4;
+                tc_mma_bf16(tmem + C::S_COL + 128 * half, qd + off, kd + off, id_s, kk > 0);
+            }
+            tc_commit(&s.s_full[half]);
         }
-        tc_commit(&s.s_full[half]);
+        __syncwarp();
+    };
+    auto outputs = [&](int half, uint32_t v, bool more) {
+        if (elect_one()) {
+            const uint64_t vd = v_desc + v * (C::TILE >> 4);
+#pragma unroll
+            for (int ks = 0; ks < 8; ks++)  // P from tensor memory, 8 columns: 16 keys
+                tc_mma_bf16_ts(tmem + C::O_COL + 128 * half, tmem + C::S_COL + 128 * half + ks * 8, vd + ks * (16 * 128 >> 4),
+                               id_o, more || ks > 0);
+        }
+        __syncwarp();
+    };
+    auto commit = [&](uint64_t *bar) {
+        if (elect_one()) tc_commit(bar);
+        __syncwarp();
     };
     while (items.next(s, x, a.flags)) {
-        const int n = x.item.block1 - x.item.block0, halves = x.item.tokens * a.group > 128 ? 2 : 1;
-        bool ok = true;
-        if (issuer && n > 0) {
-            ok = wait_phase(s, &s.q_full, q_phase, a.flags) &&
-                 wait_phase(s, &s.kv_full[at % C::STAGES], at / C::STAGES & 1, a.flags);
-            if (ok) {
+        const int n = __shfl_sync(0xffffffffu, x.item.block1 - x.item.block0, 0);
+        const int halves = __shfl_sync(0xffffffffu, x.item.tokens * a.group > 128 ? 2 : 1, 0);
+        if (n == 0) continue;
+        bool ok = warp_wait(s, &s.q_full, q_phase, a.flags) && warp_wait(s, &s.kv_full[stage], phase, a.flags);
+        if (!ok) break;
+        tc_fence_after();
+        for (int h = 0; h < halves; h++) logits(h, stage);
+        issued = true;
+        commit(&s.kv_empty[stage]);
+        if (n == 1) commit(&s.q_empty);
+        advance();
+        for (int j = 0; j < n; j++) {
+            const uint32_t v = stage;
+            ok = warp_wait(s, &s.kv_full[v], phase, a.flags);
+            if (!ok) break;
+            advance();
+            for (int h = 0; h < halves; h++) {
+                ok = warp_wait(s, &s.p_full[h], p_phase >> h & 1, a.flags);
+                if (!ok) break;
                 tc_fence_after();
-                for (int h = 0; h < halves; h++) logits(h, at % C::STAGES);
-                tc_commit(&s.kv_empty[at % C::STAGES]);
-                if (n == 1) tc_commit(&s.q_empty);
-                issued = true;
-            }
-            for (int j = 0; j < n && ok; j++) {
-                const uint32_t v_at = at + 2 * j + 1, k_at = v_at + 1;
-                const uint32_t v = v_at % C::STAGES, k = k_at % C::STAGES;
-                ok = wait_phase(s, &s.kv_full[v], v_at / C::STAGES & 1, a.flags);
-                for (int h = 0; h < halves && ok; h++) {
-                    ok = wait_phase(s, &s.p_full[h], p_phase >> h & 1, a.flags);
+                outputs(h, v, j > 0);
+                if (j + 1 == n) {
+                    commit(&s.o_full[h]);
+                    continue;
+                }
+                if (h == 0) {
+                    ok = warp_wait(s, &s.kv_full[stage], phase, a.flags);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t va = ring_at + v * C::TILE;
-#pragma unroll
-                    for (int ks = 0; ks < 8; ks++)  // A = P from tensor memory (8 columns: 16 keys); B = V, dims contiguous
-                        tc_mma_bf16_ts(tmem + C::O_COL + 128 * h, tmem + C::S_COL + 128 * h + ks * 8,
-                                       tc_sdesc_sw128(va + ks * 16 * 128, C::ATOM, 1024), id_o, j > 0 || ks > 0);
-                    if (j + 1 == n) {
-                        tc_commit(&s.o_full[h]);
-                        continue;
-                    }
-                    if (h == 0) ok = wait_phase(s, &s.kv_full[k], k_at / C::STAGES & 1, a.flags);
-                    if (!ok) break;
-                    logits(h, k);
                 }
-                if (!ok) break;
-                p_phase ^= (1u << halves) - 1;
-                tc_commit(&s.kv_empty[v]);
-                if (j + 1 < n) tc_commit(&s.kv_empty[k]);
-                if (j + 2 == n) tc_commit(&s.q_empty);
+                logits(h, stage);
             }
-            q_phase ^= 1, at += 2 * n;
+            if (!ok) break;
+            p_phase ^= (1u << halves) - 1;
+            commit(&s.kv_empty[v]);
+            if (j + 1 < n) {
+                commit(&s.kv_empty[stage]);
+                advance();
+            }
+            if (j + 2 == n) commit(&s.q_empty);
         }
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (!ok) break;
+        q_phase ^= 1;
     }
-    if (issuer && issued) {  // every product has completed before the tensor memory is freed
-        tc_commit(&s.drain);
+    if (issued) {  // every product has completed before the tensor memory is freed
+        commit(&s.drain);
         mbar_wait_bounded(&s.drain, 0, kWaitLimitNs);
     }
     __syncwarp();
@@ -717,7 +749,7 @@ __global__ void __launch_bounds__(kThreads<KVF>, 1)
     } else if (warp < kConvertWarp) {
         regs_dec<KVF ? 40 : 88>();
         if (warp == kMmaWarp) {
-            mma_role<D>(a, s, smem_u32(q), smem_u32(ring), s.tmem);
+            mma_role<D>(a, s, smem_u32(q), smem_u32(ring));
         } else if (!KVF && warp == kLoadWarp) {
             load_role<D>(a, s, ring, &map_k, &map_v);
         } else if (warp == kListWarp) {
