@@ -17,10 +17,10 @@
 //                    this block was issued after it).  At the end the row's O
 //                    is divided by its sum and stored.
 //   1 MMA thread     issues all products; O += P V of block j, then S of block j + 1.
-//   1 load warp      gathers the pages' keys and values by TMA (boxes of 16
+//   2 load warps     gather the pages' keys and values by TMA (boxes of 16
 //                    tokens x 64 dims) into one ring, K and V in turn; for an
 //                    8-bit cache
-//   4 convert warps  do: a code times its power of two is a bf16 number, so
+//   4 convert warps  do that: a code times its power of two is a bf16 number, so
 //                    they fill the ring with the cached values as they are.
 //                    The codes of the next K or V are on their way while one is
 //                    converted.
@@ -43,12 +43,12 @@
 namespace qskv {
 namespace {
 
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kListWarp = 10, kConvertWarp = 12;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kListWarp = 11, kConvertWarp = 12;
 template <bool KVF>
 constexpr int kThreads = KVF ? 512 : 384;
 constexpr int kGoodRing = 16;      // blocks whose page masks are kept (more than the ring's stages)
 template <bool KVF>
-constexpr int kItemReaders = kSoftmaxWarps + 1 + (KVF ? 4 : 1);
+constexpr int kItemReaders = kSoftmaxWarps + 1 + (KVF ? 4 : 2);
 constexpr float kLazy = 8.f;       // weights up to 2^8 before a row's reference moves
 
 template <int D>
@@ -138,10 +138,31 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[64], bool wait) {
           "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63]));
 }
 
+// Stores 32 columns; tmem_st_wait before anybody is told.
+__device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
+        "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22,"
+        " %23, %24, %25, %26, %27, %28, %29, %30, %31, %32"
+        "};" ::"r"(taddr),
+          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+          "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+          "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // Two floats in one 64-bit register, an instruction for both.
@@ -210,6 +231,7 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
         const int limit = mine ? it.pos + token + 1 : end;  // keys the row sees
         const bool active = half == 0 || it.tokens * G > 128;
         float m = -INFINITY, l = 0.f;
+        const int least = __reduce_min_sync(0xffffffffu, limit);  // of the warp's rows
         bool ok = true;
         for (int j = 0; j < n && ok && active; j++) {
             ok = warp_wait(s, &s.s_full[half], s_phase, a.flags);
@@ -225,7 +247,7 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
             const uint32_t good = s.good[(blocks0 + j) % kGoodRing];
             const uint32_t whole = (1u << (128 / P)) - 1;
             const bool cut = good != whole;  // a page is not there, or behind the end
-            if (__any_sync(0xffffffffu, limit < key0 + 128) || cut) {
+            if (least < key0 + 128 || cut) {
                 const int lim = limit - key0;
 #pragma unroll
                 for (int k = 0; k < 128; k++)
@@ -236,8 +258,8 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
             for (int k = 0; k < 4; k++) most[k] = -INFINITY;
 #pragma unroll
             for (int k = 0; k < 128; k += 2)
-                most[k / 2 & 3] = fmaxf(fmaxf(most[k / 2 & 3], __uint_as_float(rr[k / 64][k % 64])),
-                                        __uint_as_float(rr[k / 64][k % 64 + 1]));
+                most[k / 2 & 3] = max3(most[k / 2 & 3], __uint_as_float(rr[k / 64][k % 64]),
+                                       __uint_as_float(rr[k / 64][k % 64 + 1]));
             const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * sc;
             if (j == 0) {
                 m = top;
@@ -254,26 +276,6 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
                     tmem_st32(o_at + c, o);
                 }
             }
-            const float base = m == -INFINITY ? 0.f : m;
-            const uint64_t minus = pair(-base, -base);
-            uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int c = 0; c < 2; c++) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int k = 0; k < 32; k++) {
-                    float u, v;
-                    unpair(fma2(pair(__uint_as_float(rr[c][2 * k]), __uint_as_float(rr[c][2 * k + 1])), sc2, minus),
-                           u, v);
-                    u = ex2(u), v = ex2(v);
-                    sum[k & 3] = add2(sum[k & 3], pair(u, v));
-                    pk[k] = pack_bf16x2(u, v);
-                }
-                tmem_st32(s_at + 32 * c, pk);
-            }
-            float u, v;
-            unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), u, v);
-            l += u + v;
             if (!KVF && half == 0 && (cut || key0 + 128 > end)) {  // rows of V without a token: zeros
                 const uint32_t at = stage0 + 2 * j + 1, stage = at % C::STAGES;
                 ok = warp_wait(s, &s.kv_full[stage], at / C::STAGES & 1, a.flags);
@@ -286,8 +288,29 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
                 }
                 fence_proxy_async_smem();
             }
+            const float base = m == -INFINITY ? 0.f : m;
+            const uint64_t minus = pair(-base, -base);
+            uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int k = 0; k < 32; k++) {
+                    float u, v;
+                    unpair(fma2(pair(__uint_as_float(rr[c][2 * k]), __uint_as_float(rr[c][2 * k + 1])), sc2, minus), u, v);
+                    u = ex2(u), v = ex2(v);
+                    sum[k & 3] = add2(sum[k & 3], pair(u, v));
+                    pk[k] = pack_bf16x2(u, v);
+                }
+                tmem_st32_async(s_at + 32 * c, pk);
+            }
+            tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&s.p_full[half]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.p_full[half]);
+            float u, v;
+            unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), u, v);
+            l += u + v;
         }
         stage0 += 2 * n, blocks0 += n;
         if (!ok) return;
@@ -389,11 +412,38 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
 }
 
 // ------------------------------------------------------------ products --
-// One lane of the warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
+// Products and commits for the lane that `lead` is 1 in; a warp issues them together, with operands that are the same in
+// all lanes.
+__device__ __forceinline__ uint32_t elect_one() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
+    return r;
+}
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate)), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate)), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
 }
 
 // The whole warp follows the pipeline, so that what a product is issued with is the same in all lanes and known to be:
@@ -413,32 +463,24 @@ __device__ __forceinline__ void mma_role(const PrefillArgs &a, Shared &s, uint32
     auto advance = [&] {
         if (++stage == C::STAGES) stage = 0, phase ^= 1;
     };
+    const uint32_t lead = elect_one();
     auto logits = [&](int half, uint32_t k) {
-        if (elect_one()) {
-            const uint64_t qd = q_desc + half * (C::TILE >> 4), kd = k_desc + k * (C::TILE >> 4);
+        const uint64_t qd = q_desc + half * (C::TILE >> 4), kd = k_desc + k * (C::TILE >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; kk++) {
-                const uint32_t off = ((kk >> 2) * C::ATOM + (kk & 3) * 32) >> 4;
-                tc_mma_bf16(tmem + C::S_COL + 128 * half, qd + off, kd + off, id_s, kk > 0);
-            }
-            tc_commit(&s.s_full[half]);
+        for (int kk = 0; kk < D / 16; kk++) {
+            const uint32_t off = ((kk >> 2) * C::ATOM + (kk & 3) * 32) >> 4;
+            mma_ss(lead, tmem + C::S_COL + 128 * half, qd + off, kd + off, id_s, kk > 0);
         }
-        __syncwarp();
+        mma_commit(lead, &s.s_full[half]);
     };
     auto outputs = [&](int half, uint32_t v, bool more) {
-        if (elect_one()) {
-            const uint64_t vd = v_desc + v * (C::TILE >> 4);
+        const uint64_t vd = v_desc + v * (C::TILE >> 4);
 #pragma unroll
-            for (int ks = 0; ks < 8; ks++)  // P from tensor memory, 8 columns: 16 keys
-                tc_mma_bf16_ts(tmem + C::O_COL + 128 * half, tmem + C::S_COL + 128 * half + ks * 8, vd + ks * (16 * 128 >> 4),
-                               id_o, more || ks > 0);
-        }
-        __syncwarp();
+        for (int ks = 0; ks < 8; ks++)  // P from tensor memory, 8 columns: 16 keys
+            mma_ts(lead, tmem + C::O_COL + 128 * half, tmem + C::S_COL + 128 * half + ks * 8, vd + ks * (16 * 128 >> 4), id_o,
+                   more || ks > 0);
     };
-    auto commit = [&](uint64_t *bar) {
-        if (elect_one()) tc_commit(bar);
-        __syncwarp();
-    };
+    auto commit = [&](uint64_t *bar) { mma_commit(lead, bar); };
     while (items.next(s, x, a.flags)) {
         const int n = __shfl_sync(0xffffffffu, x.item.block1 - x.item.block0, 0);
         const int halves = __shfl_sync(0xffffffffu, x.item.tokens * a.group > 128 ? 2 : 1, 0);
@@ -468,7 +510,6 @@ __device__ __forceinline__ void mma_role(const PrefillArgs &a, Shared &s, uint32
                 if (h == 0) {
                     ok = warp_wait(s, &s.kv_full[stage], phase, a.flags);
                     if (!ok) break;
-                    tc_fence_after();
                 }
                 logits(h, stage);
             }
@@ -492,21 +533,23 @@ __device__ __forceinline__ void mma_role(const PrefillArgs &a, Shared &s, uint32
 }
 
 // --------------------------------------------------------------- loads --
+// Keys (which 0, the even stages of the ring) or values (1, the odd ones).
 template <int D>
-__device__ void load_role(const PrefillArgs &a, Shared &s, uint8_t *ring, const CUtensorMap *map_k, const CUtensorMap *map_v) {
+__device__ __forceinline__ void load_role(const PrefillArgs &a, Shared &s, uint8_t *ring, const CUtensorMap *map, int which) {
     using C = Cfg<D>;
-    const int lane = threadIdx.x & 31, P = a.page_size, ppb = 128 / P, boxes = P / 16;
+    const int lane = threadIdx.x & 31, P = a.page_size, ppb = 128 / P, per = P / 16;
+    const uint32_t lead = elect_one();
     ItemReader items;
     Slot x;
-    uint32_t at = 0, blocks0 = 0;
+    uint32_t at = which, blocks0 = 0;
     bool ok = true;
     while (ok && items.next(s, x, a.flags)) {
         const PrefillItem &it = x.item;
         const int n = it.block1 - it.block0, end = it.pos + it.tokens;
-        // lane j < ppb holds page j of a block, -1 where there is none; read a block ahead
+        // lane p < 8 holds the page of the 16 tokens of box p of a block, -1 where there is none; read a block ahead
         auto page_of = [&](int j) {
-            const int page = (it.block0 + j) * ppb + lane;
-            if (lane >= ppb || j >= n || page * P >= end) return -1;
+            const int t = (it.block0 + j) * 128 + lane * 16, page = t / P;
+            if (lane >= 8 || j >= n || page * P >= end) return -1;
             const int id = __ldg(a.page_table + int64_t(it.row) * a.max_pages + page);
             if (id < 0 || id >= a.num_pool_pages) {
                 raise_error(a.flags, kErrPageId);
@@ -515,35 +558,38 @@ __device__ void load_role(const PrefillArgs &a, Shared &s, uint8_t *ring, const 
             return id;
         };
         int next = page_of(0);
-        for (int j = 0; j < n && ok; j++) {
+        for (int j = 0; j < n; j++, at += 2) {
             const int id = next;
             next = page_of(j + 1);
-            const uint32_t good = __ballot_sync(0xffffffffu, id >= 0);
-            for (int which = 0; which < 2 && ok; which++, at++) {
-                const uint32_t stage = at % C::STAGES;
-                if (at >= C::STAGES) ok = warp_wait(s, &s.kv_empty[stage], (at / C::STAGES - 1) & 1, a.flags);
-                if (!ok) break;
-                if (lane == 0) {
-                    if (which == 0) s.good[(blocks0 + j) % kGoodRing] = good;
-                    mbar_arrive_expect_tx(&s.kv_full[stage], __popc(good) * P * D * 2);
-                }
-                __syncwarp();
-                if (id >= 0) {
-                    uint8_t *to = ring + stage * C::TILE + lane * P * 128;
-                    const int y = (id * a.num_kv_heads + x.head) * P;
-                    for (int b = 0; b < boxes; b++)
+            const uint32_t stage = at % C::STAGES, boxes = __ballot_sync(0xffffffffu, id >= 0);
+            if (at >= C::STAGES) ok = warp_wait(s, &s.kv_empty[stage], (at / C::STAGES - 1) & 1, a.flags);
+            if (!ok) break;
+            const int first = __shfl_sync(0xffffffffu, id, lane * per & 7);
+            const uint32_t good = __ballot_sync(0xffffffffu, lane < ppb && first >= 0);
+            if (lead) {
+                if (which == 0) s.good[(blocks0 + j) % kGoodRing] = good;
+                mbar_arrive_expect_tx(&s.kv_full[stage], __popc(boxes) * 16 * D * 2);
+            }
+            __syncwarp();
+            uint8_t *to = ring + stage * C::TILE;
 #pragma unroll
-                        for (int c = 0; c < C::NB; c++)
-                            tma_load_2d(to + b * 16 * 128 + c * C::ATOM, which ? map_v : map_k, c * 64, y + b * 16,
-                                        &s.kv_full[stage]);
+            for (int p = 0; p < 8; p++) {
+                const int y = (__shfl_sync(0xffffffffu, id, p) * a.num_kv_heads + x.head) * P + p % per * 16;
+                if ((boxes >> p & 1) && lead) {
+#pragma unroll
+                    for (int c = 0; c < C::NB; c++)
+                        tma_load_2d(to + p * 16 * 128 + c * C::ATOM, map, c * 64, y, &s.kv_full[stage]);
                 }
             }
+            __syncwarp();
         }
         blocks0 += n;
     }
-    // copies under way land before the CTA's memory is released
-    const uint32_t first = at > C::STAGES ? at - C::STAGES : 0;
-    for (uint32_t i = first; i < at; i++) mbar_wait_bounded(&s.kv_full[i % C::STAGES], i / C::STAGES & 1, kWaitLimitNs);
+    // copies under way land before the CTA's memory is released: this warp's among the last that fit the ring (the stages
+    // of those before were filled again, so their barriers have moved on)
+    const uint32_t all = at - which, low = all > C::STAGES ? all - C::STAGES : 0;
+    for (uint32_t i = low + ((low ^ which) & 1); i < at; i += 2)
+        mbar_wait_bounded(&s.kv_full[i % C::STAGES], i / C::STAGES & 1, kWaitLimitNs);
 }
 
 // The same for an 8-bit cache.  A part of 16 tokens has D chunks of 16 bytes of keys and as many of values, a thread each.
@@ -715,7 +761,7 @@ __global__ void __launch_bounds__(kThreads<KVF>, 1)
             mbar_init(&s.item_full[i], 1);
             mbar_init(&s.item_empty[i], kItemReaders<KVF>);
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.p_full[i], 128);
+            mbar_init(&s.p_full[i], 4);
             mbar_init(&s.o_full[i], 1);
         }
         mbar_init(&s.q_full, 1);
@@ -750,8 +796,8 @@ __global__ void __launch_bounds__(kThreads<KVF>, 1)
         regs_dec<KVF ? 40 : 88>();
         if (warp == kMmaWarp) {
             mma_role<D>(a, s, smem_u32(q), smem_u32(ring));
-        } else if (!KVF && warp == kLoadWarp) {
-            load_role<D>(a, s, ring, &map_k, &map_v);
+        } else if (!KVF && (warp == kLoadWarp || warp == kLoadWarp + 1)) {
+            load_role<D>(a, s, ring, warp == kLoadWarp ? &map_k : &map_v, warp - kLoadWarp);
         } else if (warp == kListWarp) {
             list_role<D>(a, s, q, &map_q);
             __syncwarp();
