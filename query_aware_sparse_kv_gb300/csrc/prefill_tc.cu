@@ -213,7 +213,8 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
     using C = Cfg<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane, tile_row = half * 128 + r;
-    const int G = a.group, shift = 31 - __clz(G), P = a.page_size;
+    const int G = a.group, shift = 31 - __clz(G), page_shift = a.page_size == 16 ? 4 : 5;
+    const uint32_t whole = a.page_size == 16 ? 0xff : 0xf;  // all pages of a block
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
     const uint32_t s_at = lanes + C::S_COL + 128 * half, o_at = lanes + C::O_COL + 128 * half;
     const float sc = a.scale_log2;
@@ -245,13 +246,12 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
             tmem_ld_wait(rr[1], false);
             const int key0 = (it.block0 + j) * 128;
             const uint32_t good = s.good[(blocks0 + j) % kGoodRing];
-            const uint32_t whole = (1u << (128 / P)) - 1;
             const bool cut = good != whole;  // a page is not there, or behind the end
             if (least < key0 + 128 || cut) {
                 const int lim = limit - key0;
 #pragma unroll
                 for (int k = 0; k < 128; k++)
-                    if (k >= lim || !(good >> (P == 16 ? k / 16 : k / 32) & 1)) rr[k / 64][k % 64] = 0xff800000u;
+                    if (k >= lim || !(good >> (k >> page_shift) & 1)) rr[k / 64][k % 64] = 0xff800000u;
             }
             float most[4];
 #pragma unroll
@@ -261,14 +261,12 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
                 most[k / 2 & 3] = max3(most[k / 2 & 3], __uint_as_float(rr[k / 64][k % 64]),
                                        __uint_as_float(rr[k / 64][k % 64 + 1]));
             const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * sc;
-            if (j == 0) {
-                m = top;
-            } else if (__any_sync(0xffffffffu, top > m + kLazy)) {
+            if (__any_sync(0xffffffffu, top > m + kLazy)) {
                 const float mn = top > m + kLazy ? top : m;
                 const float down = mn == m ? 1.f : ex2(m - mn);
                 m = mn, l *= down;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = 0; c < D && j > 0; c += 32) {
                     uint32_t o[32];
                     tmem_ld32(o_at + c, o);
 #pragma unroll
@@ -279,7 +277,7 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
             if (!KVF && half == 0 && (cut || key0 + 128 > end)) {  // rows of V without a token: zeros
                 const uint32_t at = stage0 + 2 * j + 1, stage = at % C::STAGES;
                 ok = warp_wait(s, &s.kv_full[stage], at / C::STAGES & 1, a.flags);
-                if (key0 + r >= end || !(good >> (r / P) & 1)) {
+                if (key0 + r >= end || !(good >> (r >> page_shift) & 1)) {
                     uint4 *row = reinterpret_cast<uint4 *>(ring + stage * C::TILE + r * 128);
 #pragma unroll
                     for (int b = 0; b < C::NB; b++)
@@ -537,7 +535,7 @@ __device__ __forceinline__ void mma_role(const PrefillArgs &a, Shared &s, uint32
 template <int D>
 __device__ __forceinline__ void load_role(const PrefillArgs &a, Shared &s, uint8_t *ring, const CUtensorMap *map, int which) {
     using C = Cfg<D>;
-    const int lane = threadIdx.x & 31, P = a.page_size, ppb = 128 / P, per = P / 16;
+    const int lane = threadIdx.x & 31, P = a.page_size, page_shift = P == 16 ? 4 : 5, ppb = P == 16 ? 8 : 4, per = P >> 4;
     const uint32_t lead = elect_one();
     ItemReader items;
     Slot x;
@@ -548,8 +546,8 @@ __device__ __forceinline__ void load_role(const PrefillArgs &a, Shared &s, uint8
         const int n = it.block1 - it.block0, end = it.pos + it.tokens;
         // lane p < 8 holds the page of the 16 tokens of box p of a block, -1 where there is none; read a block ahead
         auto page_of = [&](int j) {
-            const int t = (it.block0 + j) * 128 + lane * 16, page = t / P;
-            if (lane >= 8 || j >= n || page * P >= end) return -1;
+            const int t = (it.block0 + j) * 128 + lane * 16, page = t >> page_shift;
+            if (lane >= 8 || j >= n || page << page_shift >= end) return -1;
             const int id = __ldg(a.page_table + int64_t(it.row) * a.max_pages + page);
             if (id < 0 || id >= a.num_pool_pages) {
                 raise_error(a.flags, kErrPageId);
@@ -574,7 +572,7 @@ __device__ __forceinline__ void load_role(const PrefillArgs &a, Shared &s, uint8
             uint8_t *to = ring + stage * C::TILE;
 #pragma unroll
             for (int p = 0; p < 8; p++) {
-                const int y = (__shfl_sync(0xffffffffu, id, p) * a.num_kv_heads + x.head) * P + p % per * 16;
+                const int y = (__shfl_sync(0xffffffffu, id, p) * a.num_kv_heads + x.head) * P + (p & (per - 1)) * 16;
                 if ((boxes >> p & 1) && lead) {
 #pragma unroll
                     for (int c = 0; c < C::NB; c++)
@@ -598,7 +596,7 @@ __device__ void convert_role(const PrefillArgs &a, Shared &s, uint8_t *ring) {
     using C = Cfg<D>;
     constexpr int PARTS = 128 / D, LOADS = 8 / PARTS;  // parts the threads cover at once, and how often they do
     const int lane = threadIdx.x & 31, tid = threadIdx.x - 32 * kConvertWarp;
-    const int P = a.page_size, per_page = P / 16, c = tid % D;
+    const int page_shift = a.page_size == 16 ? 4 : 5, ppb = a.page_size == 16 ? 8 : 4, per_page = a.page_size >> 4, c = tid % D;
     // keys: token and first 16-byte chunk (16 dims); values: pair of tokens and chunk (8 dims)
     const int kt = c / (D / 16), kc = kvf_key_chunk<D>(c % (D / 16), kt);
     const int vp = c / (D / 8), vc = kvf_value_chunk<D>(c % (D / 8), vp);
@@ -612,7 +610,7 @@ __device__ void convert_role(const PrefillArgs &a, Shared &s, uint8_t *ring) {
         auto page_of = [&](int j) {  // lane p < 8: the page of part p of a block, -1 where there is none
             const int t = (it.block0 + j) * 128 + lane * 16;
             if (lane >= 8 || j >= n || t >= end) return -1;
-            const int id = __ldg(a.page_table + int64_t(it.row) * a.max_pages + t / P);
+            const int id = __ldg(a.page_table + int64_t(it.row) * a.max_pages + (t >> page_shift));
             if (id < 0 || id >= a.num_pool_pages) {
                 raise_error(a.flags, kErrPageId);
                 return -1;
@@ -626,7 +624,7 @@ __device__ void convert_role(const PrefillArgs &a, Shared &s, uint8_t *ring) {
             codes[i] = make_uint4(0, 0, 0, 0), powers[i] = 0;
             if (id < 0) return;
             const uint8_t *from =
-                a.pool + ((int64_t(id) * a.num_kv_heads + x.head) * per_page + part % per_page) * kvf_part_bytes(D);
+                a.pool + ((int64_t(id) * a.num_kv_heads + x.head) * per_page + (part & (per_page - 1))) * kvf_part_bytes(D);
             codes[i] = __ldg(reinterpret_cast<const uint4 *>(from + which * 16 * D + c * 16));
             if (which)
                 powers[i] = __ldg(reinterpret_cast<const uint16_t *>(from + 32 * D + 16) + vp);
@@ -642,7 +640,7 @@ __device__ void convert_role(const PrefillArgs &a, Shared &s, uint8_t *ring) {
             const int key0 = (it.block0 + j) * 128;
             next = page_of(j + 1);
             const int page = __shfl_sync(0xffffffffu, ids, lane * per_page & 7);
-            const uint32_t good = __ballot_sync(0xffffffffu, lane < 128 / P && page >= 0);
+            const uint32_t good = __ballot_sync(0xffffffffu, lane < ppb && page >= 0);
 #pragma unroll
             for (int which = 0; which < 2; which++, at++) {
                 const uint32_t stage = at % C::STAGES;
