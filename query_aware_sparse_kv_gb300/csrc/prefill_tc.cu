@@ -138,17 +138,26 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[64], bool wait) {
           "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63]));
 }
 
-// Stores 32 columns; tmem_st_wait before anybody is told.
-__device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t (&r)[32]) {
+// 16 columns of a thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
-        "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22,"
-        " %23, %24, %25, %26, %27, %28, %29, %30, %31, %32"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+        "}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+// Stores 16 columns; tmem_st_wait before anybody is told.
+__device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+        "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16"
         "};" ::"r"(taddr),
           "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-          "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-          "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -266,13 +275,14 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
                 const float down = mn == m ? 1.f : ex2(m - mn);
                 m = mn, l *= down;
 #pragma unroll 1
-                for (int c = 0; c < D && j > 0; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(o_at + c, o);
+                for (int c = 0; c < D && j > 0; c += 16) {  // 16 columns: the logits take up most registers
+                    uint32_t o[16];
+                    tmem_ld16(o_at + c, o);
 #pragma unroll
-                    for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * down);
-                    tmem_st32(o_at + c, o);
+                    for (int k = 0; k < 16; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * down);
+                    tmem_st16_async(o_at + c, o);
                 }
+                tmem_st_wait();
             }
             if (!KVF && half == 0 && (cut || key0 + 128 > end)) {  // rows of V without a token: zeros
                 const uint32_t at = stage0 + 2 * j + 1, stage = at % C::STAGES;
@@ -290,17 +300,18 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
             const uint64_t minus = pair(-base, -base);
             uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-                uint32_t pk[32];
+            for (int c = 0; c < 4; c++) {
+                uint32_t pk[16];
 #pragma unroll
-                for (int k = 0; k < 32; k++) {
+                for (int k = 0; k < 16; k++) {
+                    const int i = 32 * c + 2 * k;
                     float u, v;
-                    unpair(fma2(pair(__uint_as_float(rr[c][2 * k]), __uint_as_float(rr[c][2 * k + 1])), sc2, minus), u, v);
+                    unpair(fma2(pair(__uint_as_float(rr[i / 64][i % 64]), __uint_as_float(rr[i / 64][i % 64 + 1])), sc2, minus), u, v);
                     u = ex2(u), v = ex2(v);
                     sum[k & 3] = add2(sum[k & 3], pair(u, v));
                     pk[k] = pack_bf16x2(u, v);
                 }
-                tmem_st32_async(s_at + 32 * c, pk);
+                tmem_st16_async(s_at + 16 * c, pk);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -595,6 +606,7 @@ template <int D>
 __device__ void convert_role(const PrefillArgs &a, Shared &s, uint8_t *ring) {
     using C = Cfg<D>;
     constexpr int PARTS = 128 / D, LOADS = 8 / PARTS;  // parts the threads cover at once, and how often they do
+    constexpr int AHEAD = 4;  // of those, loaded ahead
     const int lane = threadIdx.x & 31, tid = threadIdx.x - 32 * kConvertWarp;
     const int page_shift = a.page_size == 16 ? 4 : 5, ppb = a.page_size == 16 ? 8 : 4, per_page = a.page_size >> 4, c = tid % D;
     // keys: token and first 16-byte chunk (16 dims); values: pair of tokens and chunk (8 dims)
@@ -617,24 +629,25 @@ __device__ void convert_role(const PrefillArgs &a, Shared &s, uint8_t *ring) {
             }
             return id;
         };
-        uint4 codes[LOADS];
-        uint32_t powers[LOADS];
+        uint4 codes[AHEAD];
+        uint32_t powers[AHEAD];
         auto load = [&](int i, int which, int ids) {  // chunk i of the thread: its codes and their tokens' powers
+            const int to = i % AHEAD;
             const int part = i * PARTS + tid / D, id = __shfl_sync(0xffffffffu, ids, part);
-            codes[i] = make_uint4(0, 0, 0, 0), powers[i] = 0;
+            codes[to] = make_uint4(0, 0, 0, 0), powers[to] = 0;
             if (id < 0) return;
             const uint8_t *from =
                 a.pool + ((int64_t(id) * a.num_kv_heads + x.head) * per_page + (part & (per_page - 1))) * kvf_part_bytes(D);
-            codes[i] = __ldg(reinterpret_cast<const uint4 *>(from + which * 16 * D + c * 16));
+            codes[to] = __ldg(reinterpret_cast<const uint4 *>(from + which * 16 * D + c * 16));
             if (which)
-                powers[i] = __ldg(reinterpret_cast<const uint16_t *>(from + 32 * D + 16) + vp);
+                powers[to] = __ldg(reinterpret_cast<const uint16_t *>(from + 32 * D + 16) + vp);
             else
-                powers[i] = __ldg(from + 32 * D + kt);
+                powers[to] = __ldg(from + 32 * D + kt);
         };
         int ids = page_of(0), next = -1;
         if (n > 0) {
 #pragma unroll
-            for (int i = 0; i < LOADS; i++) load(i, 0, ids);
+            for (int i = 0; i < AHEAD; i++) load(i, 0, ids);
         }
         for (int j = 0; j < n && ok; j++) {
             const int key0 = (it.block0 + j) * 128;
@@ -650,9 +663,12 @@ __device__ void convert_role(const PrefillArgs &a, Shared &s, uint8_t *ring) {
                 uint8_t *to = ring + stage * C::TILE;
 #pragma unroll
                 for (int i = 0; i < LOADS; i++) {
-                    const uint4 w = codes[i];
-                    const uint32_t e = powers[i];
-                    load(i, which ^ 1, which ? next : ids);
+                    const uint4 w = codes[i % AHEAD];
+                    const uint32_t e = powers[i % AHEAD];
+                    if (i + AHEAD < LOADS)
+                        load(i + AHEAD, which, ids);
+                    else
+                        load(i + AHEAD - LOADS, which ^ 1, which ? next : ids);
                     const int row0 = (i * PARTS + tid / D) * 16 + (which ? 2 * vp : kt);
                     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
                     uint32_t y[2][4];
@@ -786,12 +802,12 @@ __global__ void __launch_bounds__(kThreads<KVF>, 1)
     tc_fence_after();
     pdl_trigger();
     pdl_wait();
-    // registers a thread: shares of what the launch has, 3 x 168 (2 x 208 + 88) or 4 x 128 (2 x 184 + 40 + 104)
+    // registers a thread: shares of what the launch has, 3 x 168 (2 x 208 + 88) or 4 x 128 (2 x 176 + 64 + 96)
     if (warp < kSoftmaxWarps) {
-        regs_inc<KVF ? 184 : 208>();
+        regs_inc<KVF ? 176 : 208>();
         softmax_role<D, KVF>(a, s, ring, s.tmem);
     } else if (warp < kConvertWarp) {
-        regs_dec<KVF ? 40 : 88>();
+        regs_dec<KVF ? 64 : 88>();
         if (warp == kMmaWarp) {
             mma_role<D>(a, s, smem_u32(q), smem_u32(ring));
         } else if (!KVF && (warp == kLoadWarp || warp == kLoadWarp + 1)) {
@@ -801,7 +817,7 @@ __global__ void __launch_bounds__(kThreads<KVF>, 1)
             __syncwarp();
         }
     } else if constexpr (KVF) {
-        regs_dec<104>();
+        regs_dec<96>();
         convert_role<D>(a, s, ring);
     }
     tc_fence_before();
