@@ -20,10 +20,9 @@
 //   2 load warps     gather the pages' keys and values by TMA (boxes of 16
 //                    tokens x 64 dims) into one ring, K and V in turn; for an
 //                    8-bit cache
-//   4 convert warps  do that: a code times its power of two is a bf16 number, so
-//                    they fill the ring with the cached values as they are.
-//                    The codes of the next K or V are on their way while one is
-//                    converted.
+//   1 fetch warp     copies the codes into a ring of 16-token parts, from which
+//   4 convert warps  fill the other one: a code times its power of two is a bf16
+//                    number, so the products see the cached values as they are.
 //   1 list warp      takes items from the list, one ahead, and loads Q.
 // Places without a token (past the row's end, a page that is not there) weigh
 // nothing: their logits are replaced, and the rows of V, which may hold
@@ -48,16 +47,17 @@ template <bool KVF>
 constexpr int kThreads = KVF ? 512 : 384;
 constexpr int kGoodRing = 16;      // blocks whose page masks are kept (more than the ring's stages)
 template <bool KVF>
-constexpr int kItemReaders = kSoftmaxWarps + 1 + (KVF ? 4 : 2);
+constexpr int kItemReaders = kSoftmaxWarps + 1 + (KVF ? 1 + 4 : 2);
 constexpr float kLazy = 8.f;       // weights up to 2^8 before a row's reference moves
 
-template <int D>
+template <int D, bool KVF>
 struct Cfg {
     static constexpr int NB = D / 64;            // 64-dim (128-byte) column groups
     static constexpr int ATOM = 128 * 128;       // 128 rows x 128 bytes
     static constexpr int TILE = NB * ATOM;       // 128 rows of Q, K or V
-    static constexpr int STAGES = D == 128 ? 5 : 8;
-    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 1024;
+    static constexpr int STAGES = D == 128 ? (KVF ? 4 : 5) : 8;
+    static constexpr int PARTS = KVF ? 8 * kvf_part_bytes(D) : 0;  // codes of a block
+    static constexpr int SMEM = 2 * TILE + STAGES * TILE + PARTS + 1024;
     static constexpr uint32_t S_COL = 0, O_COL = 256;  // half h: S (and P) at 128 h, O at 256 + 128 h
 };
 
@@ -69,6 +69,7 @@ struct Slot {
 struct Shared {
     uint64_t item_full[2], item_empty[2], q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2];
     uint64_t parts_done, last_known, drain;
+    uint64_t part_full[8], part_empty[8];  // of the 8-bit codes
     Slot slot[2];
     uint32_t good[kGoodRing];  // pages of a block that are there
     uint32_t tmem;
@@ -219,7 +220,7 @@ struct ItemReader {
 // ------------------------------------------------------------- softmax --
 template <int D, bool KVF>
 __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uint32_t tmem) {
-    using C = Cfg<D>;
+    using C = Cfg<D, KVF>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane, tile_row = half * 128 + r;
     const int G = a.group, shift = 31 - __clz(G), page_shift = a.page_size == 16 ? 4 : 5;
@@ -457,9 +458,9 @@ __device__ __forceinline__ void mma_commit(uint32_t lead, uint64_t *bar) {
 
 // The whole warp follows the pipeline, so that what a product is issued with is the same in all lanes and known to be:
 // with one lane in this code a product took the issuing thread 100 clocks, 470 with few registers, of which it runs 64.
-template <int D>
+template <int D, bool KVF>
 __device__ __forceinline__ void mma_role(const PrefillArgs &a, Shared &s, uint32_t q_at, uint32_t ring_at) {
-    using C = Cfg<D>;
+    using C = Cfg<D, KVF>;
     constexpr uint32_t id_s = tc_idesc_bf16(128, 128, false, false), id_o = tc_idesc_bf16(128, D, false, true);
     const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
     const uint64_t q_desc = tc_sdesc_sw128(q_at, 16, 1024), k_desc = tc_sdesc_sw128(ring_at, 16, 1024);
@@ -545,7 +546,7 @@ __device__ __forceinline__ void mma_role(const PrefillArgs &a, Shared &s, uint32
 // Keys (which 0, the even stages of the ring) or values (1, the odd ones).
 template <int D>
 __device__ __forceinline__ void load_role(const PrefillArgs &a, Shared &s, uint8_t *ring, const CUtensorMap *map, int which) {
-    using C = Cfg<D>;
+    using C = Cfg<D, false>;
     const int lane = threadIdx.x & 31, P = a.page_size, page_shift = P == 16 ? 4 : 5, ppb = P == 16 ? 8 : 4, per = P >> 4;
     const uint32_t lead = elect_one();
     ItemReader items;
@@ -601,99 +602,114 @@ __device__ __forceinline__ void load_role(const PrefillArgs &a, Shared &s, uint8
         mbar_wait_bounded(&s.kv_full[i % C::STAGES], i / C::STAGES & 1, kWaitLimitNs);
 }
 
-// The same for an 8-bit cache.  A part of 16 tokens has D chunks of 16 bytes of keys and as many of values, a thread each.
+// The codes of an 8-bit cache, parts of 16 tokens: a block's 8 into a ring of as many.
 template <int D>
-__device__ void convert_role(const PrefillArgs &a, Shared &s, uint8_t *ring) {
-    using C = Cfg<D>;
-    constexpr int PARTS = 128 / D, LOADS = 8 / PARTS;  // parts the threads cover at once, and how often they do
-    constexpr int AHEAD = 4;  // of those, loaded ahead
-    const int lane = threadIdx.x & 31, tid = threadIdx.x - 32 * kConvertWarp;
-    const int page_shift = a.page_size == 16 ? 4 : 5, ppb = a.page_size == 16 ? 8 : 4, per_page = a.page_size >> 4, c = tid % D;
-    // keys: token and first 16-byte chunk (16 dims); values: pair of tokens and chunk (8 dims)
-    const int kt = c / (D / 16), kc = kvf_key_chunk<D>(c % (D / 16), kt);
-    const int vp = c / (D / 8), vc = kvf_value_chunk<D>(c % (D / 8), vp);
+__device__ __forceinline__ void fetch_role(const PrefillArgs &a, Shared &s, uint8_t *parts) {
+    constexpr uint32_t BYTES = kvf_part_bytes(D);
+    const int lane = threadIdx.x & 31, page_shift = a.page_size == 16 ? 4 : 5, ppb = a.page_size == 16 ? 8 : 4;
+    const int per = a.page_size >> 4;
     ItemReader items;
     Slot x;
-    uint32_t at = 0, blocks0 = 0;
+    uint32_t block = 0;
     bool ok = true;
     while (ok && items.next(s, x, a.flags)) {
         const PrefillItem &it = x.item;
         const int n = it.block1 - it.block0, end = it.pos + it.tokens;
         auto page_of = [&](int j) {  // lane p < 8: the page of part p of a block, -1 where there is none
-            const int t = (it.block0 + j) * 128 + lane * 16;
-            if (lane >= 8 || j >= n || t >= end) return -1;
-            const int id = __ldg(a.page_table + int64_t(it.row) * a.max_pages + (t >> page_shift));
+            const int t = (it.block0 + j) * 128 + lane * 16, page = t >> page_shift;
+            if (lane >= 8 || j >= n || page << page_shift >= end) return -1;
+            const int id = __ldg(a.page_table + int64_t(it.row) * a.max_pages + page);
             if (id < 0 || id >= a.num_pool_pages) {
                 raise_error(a.flags, kErrPageId);
                 return -1;
             }
             return id;
         };
-        uint4 codes[AHEAD];
-        uint32_t powers[AHEAD];
-        auto load = [&](int i, int which, int ids) {  // chunk i of the thread: its codes and their tokens' powers
-            const int to = i % AHEAD;
-            const int part = i * PARTS + tid / D, id = __shfl_sync(0xffffffffu, ids, part);
-            codes[to] = make_uint4(0, 0, 0, 0), powers[to] = 0;
-            if (id < 0) return;
-            const uint8_t *from =
-                a.pool + ((int64_t(id) * a.num_kv_heads + x.head) * per_page + (part & (per_page - 1))) * kvf_part_bytes(D);
-            codes[to] = __ldg(reinterpret_cast<const uint4 *>(from + which * 16 * D + c * 16));
-            if (which)
-                powers[to] = __ldg(reinterpret_cast<const uint16_t *>(from + 32 * D + 16) + vp);
-            else
-                powers[to] = __ldg(from + 32 * D + kt);
-        };
-        int ids = page_of(0), next = -1;
-        if (n > 0) {
-#pragma unroll
-            for (int i = 0; i < AHEAD; i++) load(i, 0, ids);
-        }
-        for (int j = 0; j < n && ok; j++) {
-            const int key0 = (it.block0 + j) * 128;
+        int next = page_of(0);
+        for (int j = 0; j < n; j++, block++) {
+            const int id = next;
             next = page_of(j + 1);
-            const int page = __shfl_sync(0xffffffffu, ids, lane * per_page & 7);
-            const uint32_t good = __ballot_sync(0xffffffffu, lane < ppb && page >= 0);
+            const int first = __shfl_sync(0xffffffffu, id, lane * per & 7);
+            const uint32_t good = __ballot_sync(0xffffffffu, lane < ppb && first >= 0);
+            if (lane == 0) s.good[block % kGoodRing] = good;
+            __syncwarp();
+            // a lane a part, as soon as its place is free
+            if (lane < 8) {
+                ok = block == 0 || wait_phase(s, &s.part_empty[lane], (block - 1) & 1, a.flags);
+                if (ok && id >= 0) {
+                    mbar_arrive_expect_tx(&s.part_full[lane], BYTES);
+                    bulk_load(parts + lane * BYTES,
+                              a.pool + ((int64_t(id) * a.num_kv_heads + x.head) * per + (lane & (per - 1))) * BYTES, BYTES,
+                              &s.part_full[lane]);
+                } else if (ok) {
+                    mbar_arrive(&s.part_full[lane]);
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+        }
+    }
+    // copies under way land before the CTA's memory is released
+    if (lane < 8 && block > 0) mbar_wait_bounded(&s.part_full[lane], (block - 1) & 1, kWaitLimitNs);
+    __syncwarp();
+}
+
+// Codes to bf16 numbers, K and V in turn.  A part has D chunks of 16 bytes of keys and as many of values, a thread each.
+template <int D>
+__device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, uint8_t *ring, const uint8_t *parts) {
+    using C = Cfg<D, true>;
+    constexpr int TOGETHER = 128 / D, STEPS = 8 / TOGETHER;  // parts the threads cover at once, and how often they do
+    const int tid = threadIdx.x - 32 * kConvertWarp, c = tid % D, lane = tid & 31;
+    const int page_shift = a.page_size == 16 ? 4 : 5;
+    // keys: token and first 16-byte chunk (16 dims); values: pair of tokens and chunk (8 dims)
+    const int kt = c / (D / 16), kc = kvf_key_chunk<D>(c % (D / 16), kt);
+    const int vp = c / (D / 8), vc = kvf_value_chunk<D>(c % (D / 8), vp);
+    ItemReader items;
+    Slot x;
+    uint32_t stage = 0, phase = 0, block = 0;  // of the ring; blocks of all items
+    bool ok = true, filled = false;            // filled: the ring has been, once
+    while (ok && items.next(s, x, a.flags)) {
+        const PrefillItem &it = x.item;
+        const int n = it.block1 - it.block0, end = it.pos + it.tokens;
+        for (int j = 0; j < n && ok; j++, block++) {
+            const int key0 = (it.block0 + j) * 128;
 #pragma unroll
-            for (int which = 0; which < 2; which++, at++) {
-                const uint32_t stage = at % C::STAGES;
-                if (at >= C::STAGES) ok = warp_wait(s, &s.kv_empty[stage], (at / C::STAGES - 1) & 1, a.flags);
+            for (int which = 0; which < 2; which++) {
+                if (filled) ok = warp_wait(s, &s.kv_empty[stage], phase ^ 1, a.flags);
                 if (!ok) break;
-                if (which == 0 && tid == 0) s.good[(blocks0 + j) % kGoodRing] = good;
                 uint8_t *to = ring + stage * C::TILE;
-#pragma unroll
-                for (int i = 0; i < LOADS; i++) {
-                    const uint4 w = codes[i % AHEAD];
-                    const uint32_t e = powers[i % AHEAD];
-                    if (i + AHEAD < LOADS)
-                        load(i + AHEAD, which, ids);
-                    else
-                        load(i + AHEAD - LOADS, which ^ 1, which ? next : ids);
-                    const int row0 = (i * PARTS + tid / D) * 16 + (which ? 2 * vp : kt);
+#pragma unroll 2
+                for (int i = 0; i < STEPS; i++) {
+                    const int part = i * TOGETHER + tid / D;
+                    if (which == 0) {
+                        ok = warp_wait(s, &s.part_full[part], block & 1, a.flags);
+                        if (!ok) break;
+                    }
+                    const uint8_t *from = parts + part * kvf_part_bytes(D);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(from + which * 16 * D + c * 16);
                     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t y[2][4];
+                    const int row0 = part * 16 + (which ? 2 * vp : kt);
                     if (which) {  // bytes in turn of both tokens
+                        const bool there = s.good[block % kGoodRing] >> (part * 16 >> page_shift) & 1;
+                        const uint32_t e = *reinterpret_cast<const uint16_t *>(from + 32 * D + 16 + 2 * vp);
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
-                            // what lies past the end may be no number
-                            const bool in = key0 + row0 + h < end;
-                            const float power = in ? kvf_power(e >> (8 * h) & 255) : 0.f;
+                            const int row = row0 + h;
+                            const bool in = there && key0 + row < end;  // what lies past the end may be no number
+                            const float power = kvf_power(e >> (8 * h) & 255);
+                            uint32_t y[4];
 #pragma unroll
                             for (int k = 0; k < 4; k++) {
                                 const uint32_t f = kvf_half2(__byte_perm(u[k], 0, h ? 0x0031 : 0x0020));
                                 const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f));
-                                y[h][k] = in ? pack_bf16x2(v.x * power, v.y * power) : 0u;
+                                y[k] = in ? pack_bf16x2(v.x * power, v.y * power) : 0u;
                             }
-                        }
-                        const int col = vc / 8 * C::ATOM;
-#pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const int row = row0 + h;
-                            *reinterpret_cast<uint4 *>(to + col + row * 128 + (((vc & 7) ^ (row & 7)) << 4)) =
-                                make_uint4(y[h][0], y[h][1], y[h][2], y[h][3]);
+                            *reinterpret_cast<uint4 *>(to + vc / 8 * C::ATOM + row * 128 + (((vc & 7) ^ (row & 7)) << 4)) =
+                                make_uint4(y[0], y[1], y[2], y[3]);
                         }
                     } else {
-                        const float power = kvf_power(e);
+                        const float power = kvf_power(from[32 * D + kt]);
+                        uint32_t y[2][4];
 #pragma unroll
                         for (int k = 0; k < 8; k++) {
                             const uint32_t f = kvf_half2(u[k / 2] >> (16 * (k & 1)));
@@ -710,20 +726,24 @@ __device__ void convert_role(const PrefillArgs &a, Shared &s, uint8_t *ring) {
                             *reinterpret_cast<uint4 *>(to + kc / 4 * C::ATOM + row0 * 128 + ((k ^ (row0 & 7)) << 4)) = v;
                         }
                     }
+                    if (which) {  // the part's place is free
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s.part_empty[part]);
+                    }
                 }
+                if (!ok) break;
                 fence_proxy_async_smem();
                 mbar_arrive(&s.kv_full[stage]);
+                if (++stage == C::STAGES) stage = 0, phase ^= 1, filled = true;
             }
-            ids = next;
         }
-        blocks0 += n;
     }
 }
 
 // Takes items from the list, one ahead of the CTA's other roles, and loads their queries.
 template <int D>
 __device__ void list_role(const PrefillArgs &a, Shared &s, uint8_t *q, const CUtensorMap *map_q) {
-    using C = Cfg<D>;
+    using C = Cfg<D, false>;  // its tiles are as large for both caches
     if ((threadIdx.x & 31) != 0) return;
     const int total = int(__ldcg(&a.plan->items)) * a.num_kv_heads, per = 128 / a.group;
     int slot = 0, phase = 0, q_phase = 0;
@@ -763,7 +783,7 @@ template <int D, bool KVF>
 __global__ void __launch_bounds__(kThreads<KVF>, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PrefillArgs a) {
-    using C = Cfg<D>;
+    using C = Cfg<D, KVF>;
     extern __shared__ uint8_t raw[];
     __shared__ Shared s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -783,6 +803,10 @@ __global__ void __launch_bounds__(kThreads<KVF>, 1)
         for (int i = 0; i < C::STAGES; i++) {
             mbar_init(&s.kv_full[i], KVF ? 128 : 1);
             mbar_init(&s.kv_empty[i], 1);
+        }
+        for (int i = 0; i < 8 && KVF; i++) {
+            mbar_init(&s.part_full[i], 1);
+            mbar_init(&s.part_empty[i], D / 32);  // the warps that convert a part
         }
         mbar_init(&s.parts_done, 32 * kSoftmaxWarps);
         mbar_init(&s.last_known, 1);
@@ -809,16 +833,18 @@ __global__ void __launch_bounds__(kThreads<KVF>, 1)
     } else if (warp < kConvertWarp) {
         regs_dec<KVF ? 64 : 88>();
         if (warp == kMmaWarp) {
-            mma_role<D>(a, s, smem_u32(q), smem_u32(ring));
+            mma_role<D, KVF>(a, s, smem_u32(q), smem_u32(ring));
         } else if (!KVF && (warp == kLoadWarp || warp == kLoadWarp + 1)) {
             load_role<D>(a, s, ring, warp == kLoadWarp ? &map_k : &map_v, warp - kLoadWarp);
+        } else if (KVF && warp == kLoadWarp) {
+            fetch_role<D>(a, s, ring + C::STAGES * C::TILE);
         } else if (warp == kListWarp) {
             list_role<D>(a, s, q, &map_q);
             __syncwarp();
         }
     } else if constexpr (KVF) {
         regs_dec<96>();
-        convert_role<D>(a, s, ring);
+        convert_role<D>(a, s, ring, ring + C::STAGES * C::TILE);
     }
     tc_fence_before();
     __syncthreads();
@@ -830,11 +856,11 @@ template <int D, bool KVF>
 cudaError_t launch_one(const PrefillArgs &a, const CUtensorMap *q, const CUtensorMap *k, const CUtensorMap *v,
                        cudaStream_t stream) {
     auto kernel = prefill_tc_kernel<D, KVF>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, KVF>::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t most = int64_t(a.max_items) * a.num_kv_heads;
     return launch_pdl(kernel, dim3(unsigned(most < a.num_sms ? most : a.num_sms)), dim3(kThreads<KVF>),
-                      size_t(Cfg<D>::SMEM), stream, *q, *k, *v, a);
+                      size_t(Cfg<D, KVF>::SMEM), stream, *q, *k, *v, a);
 }
 
 }  // namespace
