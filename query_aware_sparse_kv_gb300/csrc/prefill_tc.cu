@@ -69,7 +69,7 @@ struct Slot {
 struct Shared {
     uint64_t item_full[2], item_empty[2], q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2];
     uint64_t parts_done, last_known, drain;
-    uint64_t part_full[8], part_empty[8];  // of the 8-bit codes
+    uint64_t part_full, part_empty[8];  // of the 8-bit codes: a block's are there, a part's place is free
     Slot slot[2];
     uint32_t good[kGoodRing];  // pages of a block that are there
     uint32_t tmem;
@@ -637,12 +637,12 @@ __device__ __forceinline__ void fetch_role(const PrefillArgs &a, Shared &s, uint
             if (lane < 8) {
                 ok = block == 0 || wait_phase(s, &s.part_empty[lane], (block - 1) & 1, a.flags);
                 if (ok && id >= 0) {
-                    mbar_arrive_expect_tx(&s.part_full[lane], BYTES);
+                    mbar_arrive_expect_tx(&s.part_full, BYTES);
                     bulk_load(parts + lane * BYTES,
                               a.pool + ((int64_t(id) * a.num_kv_heads + x.head) * per + (lane & (per - 1))) * BYTES, BYTES,
-                              &s.part_full[lane]);
+                              &s.part_full);
                 } else if (ok) {
-                    mbar_arrive(&s.part_full[lane]);
+                    mbar_arrive(&s.part_full);
                 }
             }
             ok = __all_sync(0xffffffffu, ok);
@@ -650,92 +650,122 @@ __device__ __forceinline__ void fetch_role(const PrefillArgs &a, Shared &s, uint
         }
     }
     // copies under way land before the CTA's memory is released
-    if (lane < 8 && block > 0) mbar_wait_bounded(&s.part_full[lane], (block - 1) & 1, kWaitLimitNs);
+    if (block > 0) mbar_wait_bounded(&s.part_full, (block - 1) & 1, kWaitLimitNs);
     __syncwarp();
 }
 
-// Codes to bf16 numbers, K and V in turn.  A part has D chunks of 16 bytes of keys and as many of values, a thread each.
+// Two e4m3 codes, in the upper bytes of x's halves (what else is in x says nothing), as bf16 numbers less 2^120: sign,
+// exponent and fraction moved to their places.  Times 2^(120 + e) they are the cached values, exactly; a code's subnormals
+// are bf16's, which a product takes as they are.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t x, uint32_t x_up4) {
+    return (x & 0x80008000u) | (x_up4 & 0x07f007f0u);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// 2^(120 + e) in both halves, as far as bf16 goes; powers above (values from 2^16 on) leave the rest in `more`.
+__device__ __forceinline__ uint32_t power_bf16x2(uint32_t stored, uint32_t &more) {
+    const uint32_t f = min(stored + 120u, 254u);
+    more = stored + 120u - f;
+    return f << 7 | f << 23;
+}
+
+// Codes to bf16 numbers, K and V in turn.  A part has D chunks of 16 bytes of keys and as many of values, a thread each;
+// of a K or V its chunks are STEPS parts at the same places.
 template <int D>
 __device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, uint8_t *ring, const uint8_t *parts) {
     using C = Cfg<D, true>;
     constexpr int TOGETHER = 128 / D, STEPS = 8 / TOGETHER;  // parts the threads cover at once, and how often they do
-    const int tid = threadIdx.x - 32 * kConvertWarp, c = tid % D, lane = tid & 31;
+    constexpr int FROM = TOGETHER * kvf_part_bytes(D), TO = TOGETHER * 16 * 128;  // bytes from one to the next
+    const int tid = threadIdx.x - 32 * kConvertWarp, c = tid % D, part0 = tid / D, lane = tid & 31;
     const int page_shift = a.page_size == 16 ? 4 : 5;
+    const uint32_t whole = a.page_size == 16 ? 0xff : 0xf;
     // keys: token and first 16-byte chunk (16 dims); values: pair of tokens and chunk (8 dims)
     const int kt = c / (D / 16), kc = kvf_key_chunk<D>(c % (D / 16), kt);
     const int vp = c / (D / 8), vc = kvf_value_chunk<D>(c % (D / 8), vp);
+    const uint8_t *codes = parts + part0 * kvf_part_bytes(D) + c * 16, *powers = parts + part0 * kvf_part_bytes(D) + 32 * D;
+    // the lanes of the upper half of the dims store theirs the other way round: all banks are met
+    const int swap = D == 128 ? kc >> 2 & 1 : 0;
+    const int k_to = kc / 4 * C::ATOM + (part0 * 16 + kt) * 128;
+    const int k_first = k_to + ((((kc & 3) * 2 + swap) ^ (kt & 7)) << 4), k_second = k_to + ((((kc & 3) * 2 + (swap ^ 1)) ^ (kt & 7)) << 4);
+    const int v_to = vc / 8 * C::ATOM + (part0 * 16 + 2 * vp) * 128;
+    const int v_first = v_to + (((vc & 7) ^ (2 * vp & 7)) << 4), v_second = v_to + 128 + (((vc & 7) ^ ((2 * vp + 1) & 7)) << 4);
     ItemReader items;
     Slot x;
     uint32_t stage = 0, phase = 0, block = 0;  // of the ring; blocks of all items
     bool ok = true, filled = false;            // filled: the ring has been, once
+    auto advance = [&] {
+        fence_proxy_async_smem();
+        mbar_arrive(&s.kv_full[stage]);
+        if (++stage == C::STAGES) stage = 0, phase ^= 1, filled = true;
+    };
     while (ok && items.next(s, x, a.flags)) {
         const PrefillItem &it = x.item;
         const int n = it.block1 - it.block0, end = it.pos + it.tokens;
-        for (int j = 0; j < n && ok; j++, block++) {
-            const int key0 = (it.block0 + j) * 128;
+        for (int j = 0; j < n; j++, block++) {
+            const int left = end - (it.block0 + j) * 128;  // tokens of the row from the block on
+            ok = warp_wait(s, &s.part_full, block & 1, a.flags) && (!filled || warp_wait(s, &s.kv_empty[stage], phase ^ 1, a.flags));
+            if (!ok) break;
+            uint8_t *to = ring + stage * C::TILE;
+#pragma unroll 4
+            for (int i = 0; i < STEPS; i++) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(codes + i * FROM);
+                uint32_t more;
+                const uint32_t power = power_bf16x2(powers[i * FROM + kt], more);
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                uint32_t y[8];
 #pragma unroll
-            for (int which = 0; which < 2; which++) {
-                if (filled) ok = warp_wait(s, &s.kv_empty[stage], phase ^ 1, a.flags);
-                if (!ok) break;
-                uint8_t *to = ring + stage * C::TILE;
-#pragma unroll 2
-                for (int i = 0; i < STEPS; i++) {
-                    const int part = i * TOGETHER + tid / D;
-                    if (which == 0) {
-                        ok = warp_wait(s, &s.part_full[part], block & 1, a.flags);
-                        if (!ok) break;
-                    }
-                    const uint8_t *from = parts + part * kvf_part_bytes(D);
-                    const uint4 w = *reinterpret_cast<const uint4 *>(from + which * 16 * D + c * 16);
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                    const int row0 = part * 16 + (which ? 2 * vp : kt);
-                    if (which) {  // bytes in turn of both tokens
-                        const bool there = s.good[block % kGoodRing] >> (part * 16 >> page_shift) & 1;
-                        const uint32_t e = *reinterpret_cast<const uint16_t *>(from + 32 * D + 16 + 2 * vp);
-#pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const int row = row0 + h;
-                            const bool in = there && key0 + row < end;  // what lies past the end may be no number
-                            const float power = kvf_power(e >> (8 * h) & 255);
-                            uint32_t y[4];
-#pragma unroll
-                            for (int k = 0; k < 4; k++) {
-                                const uint32_t f = kvf_half2(__byte_perm(u[k], 0, h ? 0x0031 : 0x0020));
-                                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f));
-                                y[k] = in ? pack_bf16x2(v.x * power, v.y * power) : 0u;
-                            }
-                            *reinterpret_cast<uint4 *>(to + vc / 8 * C::ATOM + row * 128 + (((vc & 7) ^ (row & 7)) << 4)) =
-                                make_uint4(y[0], y[1], y[2], y[3]);
-                        }
-                    } else {
-                        const float power = kvf_power(from[32 * D + kt]);
-                        uint32_t y[2][4];
-#pragma unroll
-                        for (int k = 0; k < 8; k++) {
-                            const uint32_t f = kvf_half2(u[k / 2] >> (16 * (k & 1)));
-                            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f));
-                            y[k / 4][k % 4] = pack_bf16x2(v.x * power, v.y * power);
-                        }
-                        // the lanes of the upper half of the dims store theirs the other way round: all banks are met
-                        const int swap = D == 128 ? kc >> 2 & 1 : 0;
-#pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const int k = (kc & 3) * 2 + (h ^ swap);
-                            const uint4 v = swap ? make_uint4(y[h ^ 1][0], y[h ^ 1][1], y[h ^ 1][2], y[h ^ 1][3])
-                                                 : make_uint4(y[h][0], y[h][1], y[h][2], y[h][3]);
-                            *reinterpret_cast<uint4 *>(to + kc / 4 * C::ATOM + row0 * 128 + ((k ^ (row0 & 7)) << 4)) = v;
-                        }
-                    }
-                    if (which) {  // the part's place is free
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&s.part_empty[part]);
-                    }
+                for (int k = 0; k < 8; k++) {
+                    const uint32_t z = __byte_perm(u[k / 2], 0, k & 1 ? 0x3424 : 0x1404);
+                    y[k] = mul_bf16x2(codes_bf16(z, z >> 4), power);
                 }
-                if (!ok) break;
-                fence_proxy_async_smem();
-                mbar_arrive(&s.kv_full[stage]);
-                if (++stage == C::STAGES) stage = 0, phase ^= 1, filled = true;
+                if (more) {
+                    const uint32_t p = (127u + more) << 7 | (127u + more) << 23;
+#pragma unroll
+                    for (int k = 0; k < 8; k++) y[k] = mul_bf16x2(y[k], p);
+                }
+                const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+                *reinterpret_cast<uint4 *>(to + k_first + i * TO) = swap ? hi : lo;
+                *reinterpret_cast<uint4 *>(to + k_second + i * TO) = swap ? lo : hi;
             }
+            advance();
+            if (filled) ok = warp_wait(s, &s.kv_empty[stage], phase ^ 1, a.flags);
+            if (!ok) break;
+            to = ring + stage * C::TILE;
+            const uint32_t good = s.good[block % kGoodRing];
+            const bool full = good == whole && left >= 128;
+#pragma unroll 4
+            for (int i = 0; i < STEPS; i++) {
+                uint4 w = *reinterpret_cast<const uint4 *>(codes + 16 * D + i * FROM);
+                uint32_t e = *reinterpret_cast<const uint16_t *>(powers + 16 + 2 * vp + i * FROM);
+                const int part = i * TOGETHER + part0, row = part * 16 + 2 * vp;
+                if (!full) {  // what lies past the end may be no number
+                    const bool there = good >> (part * 16 >> page_shift) & 1;
+                    const uint32_t keep = (there && row < left ? 0x00ff00ffu : 0u) | (there && row + 1 < left ? 0xff00ff00u : 0u);
+                    w.x &= keep, w.y &= keep, w.z &= keep, w.w &= keep, e &= keep;
+                }
+                uint32_t more0, more1;
+                const uint32_t p0 = power_bf16x2(e & 255, more0), p1 = power_bf16x2(e >> 8, more1);
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                uint32_t y0[4], y1[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) {  // bytes in turn of both tokens
+                    y0[k] = mul_bf16x2(codes_bf16(u[k] << 8, u[k] << 4), p0);
+                    y1[k] = mul_bf16x2(codes_bf16(u[k], u[k] >> 4), p1);
+                }
+                if (more0 | more1) {
+                    const uint32_t q0 = (127u + more0) << 7 | (127u + more0) << 23, q1 = (127u + more1) << 7 | (127u + more1) << 23;
+#pragma unroll
+                    for (int k = 0; k < 4; k++) y0[k] = mul_bf16x2(y0[k], q0), y1[k] = mul_bf16x2(y1[k], q1);
+                }
+                *reinterpret_cast<uint4 *>(to + v_first + i * TO) = make_uint4(y0[0], y0[1], y0[2], y0[3]);
+                *reinterpret_cast<uint4 *>(to + v_second + i * TO) = make_uint4(y1[0], y1[1], y1[2], y1[3]);
+                __syncwarp();  // the part's place is free
+                if (lane == 0) mbar_arrive(&s.part_empty[part]);
+            }
+            advance();
         }
     }
 }
@@ -805,7 +835,7 @@ __global__ void __launch_bounds__(kThreads<KVF>, 1)
             mbar_init(&s.kv_empty[i], 1);
         }
         for (int i = 0; i < 8 && KVF; i++) {
-            mbar_init(&s.part_full[i], 1);
+            if (i == 0) mbar_init(&s.part_full, 8);
             mbar_init(&s.part_empty[i], D / 32);  // the warps that convert a part
         }
         mbar_init(&s.parts_done, 32 * kSoftmaxWarps);

@@ -291,6 +291,34 @@ def test_offsets_past_32_bits():
             assert bool(((out[:, h:h + 1].cpu().double() - o).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,P", [(64, 16), (64, 32), (128, 16), (128, 32)])
+def test_every_number_of_an_8_bit_cache(dtype, d, P):
+    """Rows of one token: the output is its value, whatever code and power, and the lse its key's dim that the query asks for."""
+    g = torch.Generator().manual_seed(d + P)
+    B, H, G = 96, 2, 8
+    codes = [torch.randint(0, 256, (B, H, P, d), generator=g) for _ in range(2)]
+    codes = [torch.where((u & 127) == 127, u - 1, u) for u in codes]
+    # (a logit of 2^20 keeps 2^-4 in fp32, which is as far as this asks for)
+    powers = [torch.randint(-100, 12, (B, H, P), generator=g), torch.randint(-100, 120, (B, H, P), generator=g)]
+    powers[1][::2] = torch.randint(-12, 14, powers[1][::2].shape, generator=g)
+    pool = F.pack(codes[0], powers[0], codes[1], powers[1]).cuda()
+    k, v = F.values(codes[0], powers[0])[:, :, 0], F.values(codes[1], powers[1])[:, :, 0]
+    shape = qskv.make_shape(B, H * G, H, d, P, 1, B)
+    table, lens, cu = _i32([[b] for b in range(B)]), _i32([1] * B), _i32(list(range(B + 1)))
+    ws = torch.zeros(qskv.prefill_workspace_size(shape, B), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty((B, H * G, d), dtype=dtype, device="cuda"), torch.empty((B, H * G), device="cuda")
+    dims = torch.randint(0, d, (B, H * G), generator=g)
+    q = torch.zeros((B, H * G, d), dtype=dtype).scatter_(2, dims[..., None], 1.0)
+    qskv.kvf_paged_prefill(torch.zeros_like(q).cuda(), pool, table, lens, cu, out, shape, ws, lse=lse, sm_scale=1.0)
+    assert torch.equal(out.cpu().double(), v.repeat_interleave(G, 1)) and bool((lse == 0).all())
+    qskv.kvf_paged_prefill(q.cuda(), pool, table, lens, cu, out, shape, ws, lse=lse, sm_scale=1.0)
+    assert qskv.get_error(ws) == 0
+    want = k.repeat_interleave(G, 1).gather(2, dims[..., None])[..., 0]
+    # scaled by log2 e and back by ln 2: two constants, two products and their sum, 2^-24 each; the weight's exponent 2^-22
+    assert bool(((lse.cpu().double() - want).abs() <= 5 * 2.0 ** -24 * want.abs() + 2.0 ** -22).all())
+
+
 # --------------------------------------------------- with what calls it --
 def test_paged_decoder_prefills_and_decodes():
     """PagedDecoder.prefill over bf16 pools; a decode step's output is the prefill's of the last token."""
