@@ -207,62 +207,124 @@ __global__ void __launch_bounds__(kCacheThreads) kvf_gather_kernel(KvfStoreArgs 
     }
 }
 
-// A lane group of D / 4 lanes takes a (listed page, KV head) tile, a lane four
-// dims of all its tokens: nothing is combined across lanes, and the loads of
-// 16 tokens are in flight together.
-constexpr int kMetaThreads = 128;
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_min(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_max(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A lane group of D / 4 lanes takes (listed page, KV head) tiles, a lane four
+// dims of all their tokens: nothing is combined across lanes, and the loads of
+// 16 tokens are in flight together.  The values of a part are compared as
+// pairs of fp16 less its largest power, which is exact unless its powers are
+// more than 14 apart (then as floats).  The page of the next tile is looked up
+// while one is summarised.
+constexpr int kMetaThreads = 128, kMetaCtas = 8;  // CTAs an SM
 
 template <bool BF16, int D>
-__global__ void __launch_bounds__(kMetaThreads) kvf_meta_kernel(KvfMetaArgs a) {
+__global__ void __launch_bounds__(kMetaThreads, kMetaCtas) kvf_meta_kernel(KvfMetaArgs a) {
     constexpr int L = D / 4;
     pdl_trigger();
     pdl_wait();
-    const int64_t tile = (int64_t(blockIdx.x) * kMetaThreads + threadIdx.x) / L;
     const int w = threadIdx.x % L, P = a.page_size;
-    if (tile >= int64_t(a.n_list) * a.num_kv_heads) return;
-    const int e = int(tile / a.num_kv_heads), g = int(tile - int64_t(e) * a.num_kv_heads);
-    const int p = __ldg(a.page_ids + e), valid = __ldg(a.valid_tokens + e);
-    if (p < 0) return;
-    if (p >= a.num_pool_pages || valid < 1 || valid > P) {
-        if (w == 0) raise_error(a.flags, p >= a.num_pool_pages ? kErrPageId : kErrValid);
-        return;
-    }
-    const int64_t row = int64_t(p) * a.num_kv_heads + g;
-    const uint8_t *block = a.pool + row * (P >> 4) * kvf_part_bytes(D);
-    float mn[4], mx[4];
+    const uint32_t group = L == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);  // lanes of this tile
+    const int64_t tiles = int64_t(a.n_list) * a.num_kv_heads, stride = int64_t(gridDim.x) * (kMetaThreads / L);
+    int64_t tile = (int64_t(blockIdx.x) * kMetaThreads + threadIdx.x) / L;
+    int p = -1, valid = 0;
+    auto look_up = [&] {
+        if (tile >= tiles) return;
+        const int e = int(tile / a.num_kv_heads);
+        p = __ldg(a.page_ids + e), valid = __ldg(a.valid_tokens + e);
+    };
+    look_up();
+    while (tile < tiles) {
+        const int64_t row = int64_t(p) * a.num_kv_heads + tile % a.num_kv_heads;
+        const int page = p, n = valid;
+        tile += stride;
+        look_up();
+        if (page < 0) continue;
+        if (page >= a.num_pool_pages || n < 1 || n > P) {
+            if (w == 0) raise_error(a.flags, page >= a.num_pool_pages ? kErrPageId : kErrValid);
+            continue;
+        }
+        const uint8_t *block = a.pool + row * (P >> 4) * kvf_part_bytes(D);
+        float mn[4], mx[4];
 #pragma unroll
-    for (int k = 0; k < 4; k++) mn[k] = INFINITY, mx[k] = -INFINITY;
-    for (int c = 0; c < valid; c += 16) {
-        const uint8_t *part = block + (c >> 4) * kvf_part_bytes(D);
-        const uint4 powers = __ldg(reinterpret_cast<const uint4 *>(part + 32 * D));
-        uint32_t codes[16];
+        for (int k = 0; k < 4; k++) mn[k] = INFINITY, mx[k] = -INFINITY;
+        for (int c = 0; c < n; c += 16) {
+            const uint8_t *part = block + (c >> 4) * kvf_part_bytes(D);
+            // lane t (of 16) holds the power of token t; a token past the end stands for the last one
+            const int last = min(n - c, 16) - 1, own = min(int(threadIdx.x & 15), last);
+            const uint32_t stored = __ldg(part + 32 * D + own);
+            const uint8_t *even = part + kvf_key_chunk<D>(w >> 2, 0) * 16 + (w & 3) * 4;
+            const uint8_t *odd = part + kvf_key_chunk<D>(w >> 2, 1) * 16 + (w & 3) * 4;
+            uint32_t codes[16];
+            if (last == 15) {
 #pragma unroll
-        for (int t = 0; t < 16; t++)  // a token past the end repeats the first
-            codes[t] = __ldg(reinterpret_cast<const uint32_t *>(
-                part + (c + t < valid ? t * D + kvf_key_chunk<D>(w >> 2, t) * 16 : kvf_key_chunk<D>(w >> 2, 0) * 16) + (w & 3) * 4));
+                for (int t = 0; t < 16; t++) codes[t] = __ldg(reinterpret_cast<const uint32_t *>((t & 1 ? odd : even) + t * D));
+            } else {
 #pragma unroll
-        for (int t = 0; t < 16; t++) {
-            const uint32_t four = t < 4 ? powers.x : t < 8 ? powers.y : t < 12 ? powers.z : powers.w;
-            const float power = kvf_power(c + t < valid ? (four >> (8 * (t & 3))) & 255 : powers.x & 255);
+                for (int t = 0; t < 16; t++) {
+                    const int u = min(t, last);
+                    codes[t] = __ldg(reinterpret_cast<const uint32_t *>((u & 1 ? odd : even) + u * D));
+                }
+            }
+            const uint32_t top = __reduce_max_sync(group, stored);
+            if (__reduce_min_sync(group, stored) + 14 >= top) {
+                // 2^(e - largest e) of the part is 2^-14 or more, so a code (a multiple of 2^-9) times it is a fp16 number
+                const uint32_t mine = (15 + stored - top) << 10, power = mine | mine << 16;
+                uint32_t lo[2] = {0x7c007c00u, 0x7c007c00u}, hi[2] = {0xfc00fc00u, 0xfc00fc00u};
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const uint32_t x2 = kvf_half2(codes[t] >> (16 * h));
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x2));
-                const float x = f.x * power, y = f.y * power;
-                mn[2 * h] = fminf(mn[2 * h], x), mx[2 * h] = fmaxf(mx[2 * h], x);
-                mn[2 * h + 1] = fminf(mn[2 * h + 1], y), mx[2 * h + 1] = fmaxf(mx[2 * h + 1], y);
+                for (int t = 0; t < 16; t++) {
+                    const uint32_t f = __shfl_sync(group, power, t, 16);
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const uint32_t x = half2_mul(kvf_half2(codes[t] >> (16 * h)), f);
+                        lo[h] = half2_min(lo[h], x), hi[h] = half2_max(hi[h], x);
+                    }
+                }
+                const float unit = kvf_power(top);
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&lo[h]));
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&hi[h]));
+                    mn[2 * h] = fminf(mn[2 * h], x.x * unit), mn[2 * h + 1] = fminf(mn[2 * h + 1], x.y * unit);
+                    mx[2 * h] = fmaxf(mx[2 * h], y.x * unit), mx[2 * h + 1] = fmaxf(mx[2 * h + 1], y.y * unit);
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < 16; t++) {
+                    const float power = kvf_power(__shfl_sync(group, stored, t, 16));
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const uint32_t x2 = kvf_half2(codes[t] >> (16 * h));
+                        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&x2));
+                        mn[2 * h] = fminf(mn[2 * h], x.x * power), mn[2 * h + 1] = fminf(mn[2 * h + 1], x.y * power);
+                        mx[2 * h] = fmaxf(mx[2 * h], x.x * power), mx[2 * h + 1] = fmaxf(mx[2 * h + 1], x.y * power);
+                    }
+                }
             }
         }
-    }
-    const int64_t to = row * 2 * D + w * 4;
-    if constexpr (BF16) {  // exact: a value has 4 significant bits
-        uint16_t *o = static_cast<uint16_t *>(a.meta) + to;
-        *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16x2(mn[0], mn[1]), pack_bf16x2(mn[2], mn[3]));
-        *reinterpret_cast<uint2 *>(o + D) = make_uint2(pack_bf16x2(mx[0], mx[1]), pack_bf16x2(mx[2], mx[3]));
-    } else {
-        float *o = static_cast<float *>(a.meta) + to;
-        *reinterpret_cast<float4 *>(o) = make_float4(mn[0], mn[1], mn[2], mn[3]);
-        *reinterpret_cast<float4 *>(o + D) = make_float4(mx[0], mx[1], mx[2], mx[3]);
+        const int64_t to = row * 2 * D + w * 4;
+        if constexpr (BF16) {  // exact: a value has 4 significant bits
+            uint16_t *o = static_cast<uint16_t *>(a.meta) + to;
+            *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16x2(mn[0], mn[1]), pack_bf16x2(mn[2], mn[3]));
+            *reinterpret_cast<uint2 *>(o + D) = make_uint2(pack_bf16x2(mx[0], mx[1]), pack_bf16x2(mx[2], mx[3]));
+        } else {
+            float *o = static_cast<float *>(a.meta) + to;
+            *reinterpret_cast<float4 *>(o) = make_float4(mn[0], mn[1], mn[2], mn[3]);
+            *reinterpret_cast<float4 *>(o + D) = make_float4(mx[0], mx[1], mx[2], mx[3]);
+        }
     }
 }
 
@@ -298,11 +360,11 @@ cudaError_t launch_kvf_gather(const KvfStoreArgs &a, int dtype, int head_dim, cu
     KVF_TOKENS(kvf_gather_kernel)
 }
 
-cudaError_t launch_kvf_meta(const KvfMetaArgs &a, int meta_dtype, int head_dim, int, cudaStream_t stream) {
+cudaError_t launch_kvf_meta(const KvfMetaArgs &a, int meta_dtype, int head_dim, int num_sms, cudaStream_t stream) {
     const bool bf16 = meta_dtype == kDtypeBf16;
     const int per_cta = kMetaThreads / (head_dim / 4);
-    const int64_t tiles = int64_t(a.n_list) * a.num_kv_heads;
-    const dim3 grid(unsigned((tiles + per_cta - 1) / per_cta)), block(kMetaThreads);
+    const int64_t tiles = int64_t(a.n_list) * a.num_kv_heads, ctas = (tiles + per_cta - 1) / per_cta;
+    const dim3 grid(unsigned(ctas < kMetaCtas * num_sms ? ctas : kMetaCtas * num_sms)), block(kMetaThreads);
     if (head_dim == 128)
         return bf16 ? launch_pdl(kvf_meta_kernel<true, 128>, grid, block, 0, stream, a)
                     : launch_pdl(kvf_meta_kernel<false, 128>, grid, block, 0, stream, a);

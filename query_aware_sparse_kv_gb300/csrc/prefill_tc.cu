@@ -654,24 +654,6 @@ __device__ __forceinline__ void fetch_role(const PrefillArgs &a, Shared &s, uint
     __syncwarp();
 }
 
-// Two e4m3 codes, in the upper bytes of x's halves (what else is in x says nothing), as bf16 numbers less 2^120: sign,
-// exponent and fraction moved to their places.  Times 2^(120 + e) they are the cached values, exactly; a code's subnormals
-// are bf16's, which a product takes as they are.
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t x, uint32_t x_up4) {
-    return (x & 0x80008000u) | (x_up4 & 0x07f007f0u);
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-// 2^(120 + e) in both halves, as far as bf16 goes; powers above (values from 2^16 on) leave the rest in `more`.
-__device__ __forceinline__ uint32_t power_bf16x2(uint32_t stored, uint32_t &more) {
-    const uint32_t f = min(stored + 120u, 254u);
-    more = stored + 120u - f;
-    return f << 7 | f << 23;
-}
-
 // Codes to bf16 numbers, K and V in turn.  A part has D chunks of 16 bytes of keys and as many of values, a thread each;
 // of a K or V its chunks are STEPS parts at the same places.
 template <int D>
@@ -713,18 +695,18 @@ __device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, ui
             for (int i = 0; i < STEPS; i++) {
                 const uint4 w = *reinterpret_cast<const uint4 *>(codes + i * FROM);
                 uint32_t more;
-                const uint32_t power = power_bf16x2(powers[i * FROM + kt], more);
+                const uint32_t power = kvf_power_bf16x2(powers[i * FROM + kt], more);
                 const uint32_t u[4] = {w.x, w.y, w.z, w.w};
                 uint32_t y[8];
 #pragma unroll
                 for (int k = 0; k < 8; k++) {
                     const uint32_t z = __byte_perm(u[k / 2], 0, k & 1 ? 0x3424 : 0x1404);
-                    y[k] = mul_bf16x2(codes_bf16(z, z >> 4), power);
+                    y[k] = kvf_mul_bf16x2(kvf_bf16x2(z, z >> 4), power);
                 }
                 if (more) {
                     const uint32_t p = (127u + more) << 7 | (127u + more) << 23;
 #pragma unroll
-                    for (int k = 0; k < 8; k++) y[k] = mul_bf16x2(y[k], p);
+                    for (int k = 0; k < 8; k++) y[k] = kvf_mul_bf16x2(y[k], p);
                 }
                 const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
                 *reinterpret_cast<uint4 *>(to + k_first + i * TO) = swap ? hi : lo;
@@ -747,18 +729,18 @@ __device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, ui
                     w.x &= keep, w.y &= keep, w.z &= keep, w.w &= keep, e &= keep;
                 }
                 uint32_t more0, more1;
-                const uint32_t p0 = power_bf16x2(e & 255, more0), p1 = power_bf16x2(e >> 8, more1);
+                const uint32_t p0 = kvf_power_bf16x2(e & 255, more0), p1 = kvf_power_bf16x2(e >> 8, more1);
                 const uint32_t u[4] = {w.x, w.y, w.z, w.w};
                 uint32_t y0[4], y1[4];
 #pragma unroll
                 for (int k = 0; k < 4; k++) {  // bytes in turn of both tokens
-                    y0[k] = mul_bf16x2(codes_bf16(u[k] << 8, u[k] << 4), p0);
-                    y1[k] = mul_bf16x2(codes_bf16(u[k], u[k] >> 4), p1);
+                    y0[k] = kvf_mul_bf16x2(kvf_bf16x2(u[k] << 8, u[k] << 4), p0);
+                    y1[k] = kvf_mul_bf16x2(kvf_bf16x2(u[k], u[k] >> 4), p1);
                 }
                 if (more0 | more1) {
                     const uint32_t q0 = (127u + more0) << 7 | (127u + more0) << 23, q1 = (127u + more1) << 7 | (127u + more1) << 23;
 #pragma unroll
-                    for (int k = 0; k < 4; k++) y0[k] = mul_bf16x2(y0[k], q0), y1[k] = mul_bf16x2(y1[k], q1);
+                    for (int k = 0; k < 4; k++) y0[k] = kvf_mul_bf16x2(y0[k], q0), y1[k] = kvf_mul_bf16x2(y1[k], q1);
                 }
                 *reinterpret_cast<uint4 *>(to + v_first + i * TO) = make_uint4(y0[0], y0[1], y0[2], y0[3]);
                 *reinterpret_cast<uint4 *>(to + v_second + i * TO) = make_uint4(y1[0], y1[1], y1[2], y1[3]);
