@@ -69,59 +69,80 @@ __device__ __forceinline__ uint32_t kvf_codes(const float *x, float up) {
 // First byte of the part that a slot lies in, for one head.
 template <int D>
 __device__ __forceinline__ int64_t part_at(int slot, int page_size, int num_kv_heads, int head) {
-    const int shift = page_size == 16 ? 4 : 5, parts = page_size >> 4;
-    return ((int64_t(slot >> shift) * num_kv_heads + head) * parts + ((slot & (page_size - 1)) >> 4)) * kvf_part_bytes(D);
+    const int shift = page_size == 16 ? 4 : 5, parts = page_size >> 4;  // (parts of a pool are fewer than 2^27)
+    return int64_t(((slot >> shift) * num_kv_heads + head) * parts + ((slot & (page_size - 1)) >> 4)) * kvf_part_bytes(D);
 }
 
-// A thread takes its 8 dims of ITEMS tokens that follow one another: where two
-// of them are a pair of the cache (a run of tokens goes to slots in order) the
-// value codes of both leave as one 16-byte store; a token without its other
-// one in the same thread is stored byte by byte.
+// A thread takes 8 dims, of the key and of the value, of ITEMS tokens that
+// follow one another.  A run of tokens goes to slots in order, so that two of
+// them are a pair of the cache, whose value codes leave as one 16-byte store:
+// a pair's second token is taken with its first, by whichever thread that is
+// (so a thread may have one token more, or one less).  A token alone in its
+// pair is stored byte by byte.
 template <bool BF16, int D, int ITEMS>
 __global__ void __launch_bounds__(kCacheThreads) kvf_append_kernel(KvfStoreArgs a) {
-    constexpr int W = D / 8, TPB = kCacheThreads / W;
+    constexpr int W = D / 8, TPB = kCacheThreads / W, N = ITEMS + 1;
     pdl_trigger();
     pdl_wait();
-    const int per_chunk = 2 * a.num_kv_heads;
-    const int chunk = blockIdx.x / per_chunk, y = blockIdx.x % per_chunk;
-    const int which = y >= a.num_kv_heads, head = which ? y - a.num_kv_heads : y;
+    const int chunk = blockIdx.x / a.num_kv_heads, head = blockIdx.x % a.num_kv_heads;
     const int w = threadIdx.x % W, token0 = (chunk * TPB + threadIdx.x / W) * ITEMS;
-    const void *src = which ? a.v : a.k;
-    const int64_t stride = which ? a.v_stride : a.k_stride, col = head * D + w * 8;
-    Raw8<BF16> raw[ITEMS];
-    int slot[ITEMS];
+    const int64_t col = head * D + w * 8;
+    const int slots = a.num_pool_pages * a.page_size;  // below 2^31
+    Raw8<BF16> k[N], v[N];
+    int slot[N];
 #pragma unroll
-    for (int i = 0; i < ITEMS; i++) {
-        const int t = token0 + i, in = min(t, a.n_tokens - 1);
-        slot[i] = t < a.n_tokens ? __ldg(a.slots + in) : -1;
-        raw[i].load(src, in * stride + col);
+    for (int i = 0; i < N; i++) {
+        const int t = min(token0 + i, a.n_tokens - 1);
+        slot[i] = token0 + i < a.n_tokens ? __ldg(a.slots + t) : -1;
+        if (i < ITEMS) k[i].load(a.k, t * a.k_stride + col), v[i].load(a.v, t * a.v_stride + col);
     }
-    uint2 codes[ITEMS];
+    const int before = token0 > 0 && token0 < a.n_tokens ? __ldg(a.slots + token0 - 1) : -1;
+    const bool second = (slot[0] & 1) && before >= 0 && before + 1 == slot[0];  // taken with the token before
+    const bool more = slot[ITEMS - 1] >= 0 && (slot[ITEMS] & 1) && slot[ITEMS - 1] + 1 == slot[ITEMS];
+    if (more) {
+        k[ITEMS].load(a.k, (token0 + ITEMS) * a.k_stride + col);
+        v[ITEMS].load(a.v, (token0 + ITEMS) * a.v_stride + col);
+    } else {
+        slot[ITEMS] = -1;
+        k[ITEMS] = k[0], v[ITEMS] = v[0];
+    }
+    if (second) slot[0] = -1;
+    uint2 codes[N];
 #pragma unroll
-    for (int i = 0; i < ITEMS; i++) {
-        uint32_t top = raw[i].top();
+    for (int i = 0; i < N; i++) {
+        uint32_t top_k = k[i].top(), top_v = v[i].top();
+        if constexpr (BF16) {  // both in one word: magnitudes of 16 bits
+            uint32_t r = (top_k & 0xffff0000u) | top_v >> 16;
 #pragma unroll
-        for (int o = 1; o < W; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int e = kvf_exponent(top);
-        const float up = kvf_power(254 - e);
+            for (int o = 1; o < W; o <<= 1) r = __vmaxu2(r, __shfl_xor_sync(0xffffffffu, r, o));
+            top_k = r & 0xffff0000u, top_v = r << 16;
+        } else {
+#pragma unroll
+            for (int o = 1; o < W; o <<= 1) {
+                top_k = max(top_k, __shfl_xor_sync(0xffffffffu, top_k, o));
+                top_v = max(top_v, __shfl_xor_sync(0xffffffffu, top_v, o));
+            }
+        }
+        const int ek = kvf_exponent(top_k), ev = kvf_exponent(top_v);
         float x[8];
-        raw[i].floats(x);
-        codes[i] = make_uint2(kvf_codes(x, up), kvf_codes(x + 4, up));
-        if (slot[i] >= a.num_pool_pages * int64_t(a.page_size)) {
+        k[i].floats(x);
+        const float up_k = kvf_power(254 - ek), up_v = kvf_power(254 - ev);
+        const uint2 key = make_uint2(kvf_codes(x, up_k), kvf_codes(x + 4, up_k));
+        v[i].floats(x);
+        codes[i] = make_uint2(kvf_codes(x, up_v), kvf_codes(x + 4, up_v));
+        if (slot[i] >= slots) {
             if (w == 0) raise_error(a.flags, kErrPageId);
             slot[i] = -1;
         }
         if (slot[i] < 0) continue;
         uint8_t *part = a.pool + part_at<D>(slot[i], a.page_size, a.num_kv_heads, head);
         const int t = slot[i] & 15;
-        if (w == 0) part[32 * D + 16 * which + t] = uint8_t(e);
-        if (!which)
-            *reinterpret_cast<uint2 *>(part + t * D + kvf_key_chunk<D>(w >> 1, t) * 16 + (w & 1) * 8) = codes[i];
+        if (w == 0) part[32 * D + t] = uint8_t(ek), part[32 * D + 16 + t] = uint8_t(ev);
+        *reinterpret_cast<uint2 *>(part + t * D + kvf_key_chunk<D>(w >> 1, t) * 16 + (w & 1) * 8) = key;
     }
-    if (!which) return;
     bool taken = false;  // the token before this one was stored together with it
 #pragma unroll
-    for (int i = 0; i < ITEMS; i++) {
+    for (int i = 0; i < N; i++) {
         if (slot[i] < 0 || taken) {
             taken = false;
             continue;
@@ -129,16 +150,16 @@ __global__ void __launch_bounds__(kCacheThreads) kvf_append_kernel(KvfStoreArgs 
         const int t = slot[i] & 15, p = t >> 1;
         uint8_t *to = a.pool + part_at<D>(slot[i], a.page_size, a.num_kv_heads, head) + 16 * D + p * 2 * D +
                       kvf_value_chunk<D>(w, p) * 16;
-        if (i + 1 < ITEMS && !(t & 1) && slot[i + 1 < ITEMS ? i + 1 : i] == slot[i] + 1) {
-            const uint2 x = codes[i], y = codes[i + 1 < ITEMS ? i + 1 : i];
+        if (i + 1 < N && !(t & 1) && slot[i + 1 < N ? i + 1 : i] == slot[i] + 1) {
+            const uint2 x = codes[i], y = codes[i + 1 < N ? i + 1 : i];
             *reinterpret_cast<uint4 *>(to) = make_uint4(__byte_perm(x.x, y.x, 0x5140), __byte_perm(x.x, y.x, 0x7362),
                                                         __byte_perm(x.y, y.y, 0x5140), __byte_perm(x.y, y.y, 0x7362));
             taken = true;
         } else {
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                to[2 * k + (t & 1)] = uint8_t(codes[i].x >> (8 * k));
-                to[8 + 2 * k + (t & 1)] = uint8_t(codes[i].y >> (8 * k));
+            for (int b = 0; b < 4; b++) {
+                to[2 * b + (t & 1)] = uint8_t(codes[i].x >> (8 * b));
+                to[8 + 2 * b + (t & 1)] = uint8_t(codes[i].y >> (8 * b));
             }
         }
     }
@@ -154,56 +175,57 @@ __device__ __forceinline__ void kvf_values(uint2 codes, float power, float (&x)[
     }
 }
 
+template <bool BF16>
+__device__ __forceinline__ void write_values(void *out, int64_t at, uint2 codes, float power) {
+    float x[8];
+    kvf_values(codes, power, x);
+    if constexpr (BF16) {
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) =
+            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    } else {
+        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
+        o[0] = make_float4(x[0], x[1], x[2], x[3]);
+        o[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+}
+
+// A thread 8 dims of the key and of the value of ITEMS tokens that follow one another.
 template <bool BF16, int D, int ITEMS>
 __global__ void __launch_bounds__(kCacheThreads) kvf_gather_kernel(KvfStoreArgs a) {
     constexpr int W = D / 8, TPB = kCacheThreads / W;
     pdl_trigger();
     pdl_wait();
-    const int per_chunk = 2 * a.num_kv_heads;
-    const int chunk = blockIdx.x / per_chunk, y = blockIdx.x % per_chunk;
-    const int which = y >= a.num_kv_heads, head = which ? y - a.num_kv_heads : y;
+    const int chunk = blockIdx.x / a.num_kv_heads, head = blockIdx.x % a.num_kv_heads;
     const int w = threadIdx.x % W, token0 = (chunk * TPB + threadIdx.x / W) * ITEMS;
+    const int slots = a.num_pool_pages * a.page_size;  // below 2^31
     int slot[ITEMS];
-    uint2 codes[ITEMS];
-    uint32_t e[ITEMS];
+    uint2 keys[ITEMS];
+    uint4 pairs[ITEMS];
+    uint32_t ek[ITEMS], ev[ITEMS];
 #pragma unroll
     for (int i = 0; i < ITEMS; i++) slot[i] = token0 + i < a.n_tokens ? __ldg(a.slots + token0 + i) : -1;
 #pragma unroll
     for (int i = 0; i < ITEMS; i++) {
-        codes[i] = make_uint2(0, 0), e[i] = 127;
-        if (slot[i] >= a.num_pool_pages * int64_t(a.page_size)) {
+        keys[i] = make_uint2(0, 0), pairs[i] = make_uint4(0, 0, 0, 0), ek[i] = ev[i] = 127;
+        if (slot[i] >= slots) {
             if (w == 0) raise_error(a.flags, kErrPageId);
             continue;
         }
         if (slot[i] < 0) continue;
         const uint8_t *part = a.pool + part_at<D>(slot[i], a.page_size, a.num_kv_heads, head);
         const int t = slot[i] & 15, p = t >> 1;
-        e[i] = __ldg(part + 32 * D + 16 * which + t);
-        if (which) {
-            const uint4 x =
-                __ldg(reinterpret_cast<const uint4 *>(part + 16 * D + p * 2 * D + kvf_value_chunk<D>(w, p) * 16));
-            const uint32_t pick = t & 1 ? 0x7531 : 0x6420;
-            codes[i] = make_uint2(__byte_perm(x.x, x.y, pick), __byte_perm(x.z, x.w, pick));
-        } else {
-            codes[i] = __ldg(reinterpret_cast<const uint2 *>(part + t * D + kvf_key_chunk<D>(w >> 1, t) * 16 + (w & 1) * 8));
-        }
+        ek[i] = __ldg(part + 32 * D + t), ev[i] = __ldg(part + 32 * D + 16 + t);
+        keys[i] = __ldg(reinterpret_cast<const uint2 *>(part + t * D + kvf_key_chunk<D>(w >> 1, t) * 16 + (w & 1) * 8));
+        pairs[i] = __ldg(reinterpret_cast<const uint4 *>(part + 16 * D + p * 2 * D + kvf_value_chunk<D>(w, p) * 16));
     }
-    void *out = which ? a.v_out : a.k_out;
 #pragma unroll
     for (int i = 0; i < ITEMS; i++) {
         if (token0 + i >= a.n_tokens) break;
-        float x[8];
-        kvf_values(codes[i], kvf_power(e[i]), x);
         const int64_t at = (int64_t(token0 + i) * a.num_kv_heads + head) * D + w * 8;
-        if constexpr (BF16) {
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) =
-                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                           pack_bf16x2(x[6], x[7]));
-        } else {
-            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
-            o[0] = make_float4(x[0], x[1], x[2], x[3]);
-            o[1] = make_float4(x[4], x[5], x[6], x[7]);
-        }
+        const uint32_t pick = slot[i] & 1 ? 0x7531 : 0x6420;
+        write_values<BF16>(a.k_out, at, keys[i], kvf_power(ek[i]));
+        write_values<BF16>(a.v_out, at, make_uint2(__byte_perm(pairs[i].x, pairs[i].y, pick), __byte_perm(pairs[i].z, pairs[i].w, pick)),
+                           kvf_power(ev[i]));
     }
 }
 
@@ -331,14 +353,14 @@ __global__ void __launch_bounds__(kMetaThreads, kMetaCtas) kvf_meta_kernel(KvfMe
 // CTAs of `items` tokens a thread.
 int64_t token_ctas(const KvfStoreArgs &a, int head_dim, int items) {
     const int per_cta = kCacheThreads / (head_dim / 8) * items;
-    return (int64_t(a.n_tokens) + per_cta - 1) / per_cta * 2 * a.num_kv_heads;
+    return (int64_t(a.n_tokens) + per_cta - 1) / per_cta * a.num_kv_heads;
 }
-constexpr int kItems = 8;
-constexpr int64_t kManyCtas = 608;
+constexpr int kAppendItems = 4, kGatherItems = 2;
+constexpr int64_t kManyCtas = 152;
 
 }  // namespace
 
-#define KVF_TOKENS(kernel)                                                                                      \
+#define KVF_TOKENS(kernel, kItems)                                                                                  \
     const bool bf16 = dtype == kDtypeBf16, many = token_ctas(a, head_dim, kItems) >= kManyCtas;                 \
     const dim3 grid(unsigned(token_ctas(a, head_dim, many ? kItems : 1))), block(kCacheThreads);                \
     if (head_dim == 128) {                                                                                      \
@@ -353,11 +375,11 @@ constexpr int64_t kManyCtas = 608;
                 : launch_pdl(kernel<false, 64, 1>, grid, block, 0, stream, a);
 
 cudaError_t launch_kvf_append(const KvfStoreArgs &a, int dtype, int head_dim, cudaStream_t stream) {
-    KVF_TOKENS(kvf_append_kernel)
+    KVF_TOKENS(kvf_append_kernel, kAppendItems)
 }
 
 cudaError_t launch_kvf_gather(const KvfStoreArgs &a, int dtype, int head_dim, cudaStream_t stream) {
-    KVF_TOKENS(kvf_gather_kernel)
+    KVF_TOKENS(kvf_gather_kernel, kGatherItems)
 }
 
 cudaError_t launch_kvf_meta(const KvfMetaArgs &a, int meta_dtype, int head_dim, int num_sms, cudaStream_t stream) {
