@@ -55,8 +55,8 @@ struct Cfg {
     static constexpr int NB = D / 64;            // 64-dim (128-byte) column groups
     static constexpr int ATOM = 128 * 128;       // 128 rows x 128 bytes
     static constexpr int TILE = NB * ATOM;       // 128 rows of Q, K or V
-    static constexpr int STAGES = D == 128 ? (KVF ? 4 : 5) : 8;
-    static constexpr int PARTS = KVF ? 8 * kvf_part_bytes(D) : 0;  // codes of a block
+    static constexpr int STAGES = D == 128 ? (KVF ? 3 : 5) : 8;
+    static constexpr int PARTS = KVF ? 2 * 8 * kvf_part_bytes(D) : 0;  // codes of two blocks
     static constexpr int SMEM = 2 * TILE + STAGES * TILE + PARTS + 1024;
     static constexpr uint32_t S_COL = 0, O_COL = 256;  // half h: S (and P) at 128 h, O at 256 + 128 h
 };
@@ -69,7 +69,7 @@ struct Slot {
 struct Shared {
     uint64_t item_full[2], item_empty[2], q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2];
     uint64_t parts_done, last_known, drain;
-    uint64_t part_full, part_empty[8];  // of the 8-bit codes: a block's are there, a part's place is free
+    uint64_t part_full[2], part_empty[2];  // of the 8-bit codes of a block (even, odd ones): there, and no longer needed
     Slot slot[2];
     uint32_t good[kGoodRing];  // pages of a block that are there
     uint32_t tmem;
@@ -602,7 +602,7 @@ __device__ __forceinline__ void load_role(const PrefillArgs &a, Shared &s, uint8
         mbar_wait_bounded(&s.kv_full[i % C::STAGES], i / C::STAGES & 1, kWaitLimitNs);
 }
 
-// The codes of an 8-bit cache, parts of 16 tokens: a block's 8 into a ring of as many.
+// The codes of an 8-bit cache, parts of 16 tokens, a block ahead of the one that is converted.
 template <int D>
 __device__ __forceinline__ void fetch_role(const PrefillArgs &a, Shared &s, uint8_t *parts) {
     constexpr uint32_t BYTES = kvf_part_bytes(D);
@@ -633,24 +633,24 @@ __device__ __forceinline__ void fetch_role(const PrefillArgs &a, Shared &s, uint
             const uint32_t good = __ballot_sync(0xffffffffu, lane < ppb && first >= 0);
             if (lane == 0) s.good[block % kGoodRing] = good;
             __syncwarp();
-            // a lane a part, as soon as its place is free
-            if (lane < 8) {
-                ok = block == 0 || wait_phase(s, &s.part_empty[lane], (block - 1) & 1, a.flags);
-                if (ok && id >= 0) {
-                    mbar_arrive_expect_tx(&s.part_full, BYTES);
-                    bulk_load(parts + lane * BYTES,
-                              a.pool + ((int64_t(id) * a.num_kv_heads + x.head) * per + (lane & (per - 1))) * BYTES, BYTES,
-                              &s.part_full);
-                } else if (ok) {
-                    mbar_arrive(&s.part_full);
+            if (block >= 2) ok = warp_wait(s, &s.part_empty[block & 1], (block / 2 - 1) & 1, a.flags);
+            if (!ok) break;
+            if (lane < 8) {  // a lane a part
+                uint64_t *full = &s.part_full[block & 1];
+                if (id >= 0) {
+                    mbar_arrive_expect_tx(full, BYTES);
+                    bulk_load(parts + ((block & 1) * 8 + lane) * BYTES,
+                              a.pool + ((int64_t(id) * a.num_kv_heads + x.head) * per + (lane & (per - 1))) * BYTES, BYTES, full);
+                } else {
+                    mbar_arrive(full);
                 }
             }
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            __syncwarp();
         }
     }
     // copies under way land before the CTA's memory is released
-    if (block > 0) mbar_wait_bounded(&s.part_full, (block - 1) & 1, kWaitLimitNs);
+    for (uint32_t b = block > 2 ? block - 2 : 0; b < block; b++)
+        mbar_wait_bounded(&s.part_full[b & 1], b / 2 & 1, kWaitLimitNs);
     __syncwarp();
 }
 
@@ -661,7 +661,7 @@ __device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, ui
     using C = Cfg<D, true>;
     constexpr int TOGETHER = 128 / D, STEPS = 8 / TOGETHER;  // parts the threads cover at once, and how often they do
     constexpr int FROM = TOGETHER * kvf_part_bytes(D), TO = TOGETHER * 16 * 128;  // bytes from one to the next
-    const int tid = threadIdx.x - 32 * kConvertWarp, c = tid % D, part0 = tid / D, lane = tid & 31;
+    const int tid = threadIdx.x - 32 * kConvertWarp, c = tid % D, part0 = tid / D;
     const int page_shift = a.page_size == 16 ? 4 : 5;
     const uint32_t whole = a.page_size == 16 ? 0xff : 0xf;
     // keys: token and first 16-byte chunk (16 dims); values: pair of tokens and chunk (8 dims)
@@ -688,14 +688,15 @@ __device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, ui
         const int n = it.block1 - it.block0, end = it.pos + it.tokens;
         for (int j = 0; j < n; j++, block++) {
             const int left = end - (it.block0 + j) * 128;  // tokens of the row from the block on
-            ok = warp_wait(s, &s.part_full, block & 1, a.flags) && (!filled || warp_wait(s, &s.kv_empty[stage], phase ^ 1, a.flags));
+            ok = warp_wait(s, &s.part_full[block & 1], block / 2 & 1, a.flags) && (!filled || warp_wait(s, &s.kv_empty[stage], phase ^ 1, a.flags));
             if (!ok) break;
             uint8_t *to = ring + stage * C::TILE;
+            const int half = (block & 1) * 8 * kvf_part_bytes(D);
 #pragma unroll 4
             for (int i = 0; i < STEPS; i++) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(codes + i * FROM);
+                const uint4 w = *reinterpret_cast<const uint4 *>(codes + half + i * FROM);
                 uint32_t more;
-                const uint32_t power = kvf_power_bf16x2(powers[i * FROM + kt], more);
+                const uint32_t power = kvf_power_bf16x2(powers[half + i * FROM + kt], more);
                 const uint32_t u[4] = {w.x, w.y, w.z, w.w};
                 uint32_t y[8];
 #pragma unroll
@@ -720,8 +721,8 @@ __device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, ui
             const bool full = good == whole && left >= 128;
 #pragma unroll 4
             for (int i = 0; i < STEPS; i++) {
-                uint4 w = *reinterpret_cast<const uint4 *>(codes + 16 * D + i * FROM);
-                uint32_t e = *reinterpret_cast<const uint16_t *>(powers + 16 + 2 * vp + i * FROM);
+                uint4 w = *reinterpret_cast<const uint4 *>(codes + half + 16 * D + i * FROM);
+                uint32_t e = *reinterpret_cast<const uint16_t *>(powers + half + 16 + 2 * vp + i * FROM);
                 const int part = i * TOGETHER + part0, row = part * 16 + 2 * vp;
                 if (!full) {  // what lies past the end may be no number
                     const bool there = good >> (part * 16 >> page_shift) & 1;
@@ -744,10 +745,9 @@ __device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, ui
                 }
                 *reinterpret_cast<uint4 *>(to + v_first + i * TO) = make_uint4(y0[0], y0[1], y0[2], y0[3]);
                 *reinterpret_cast<uint4 *>(to + v_second + i * TO) = make_uint4(y1[0], y1[1], y1[2], y1[3]);
-                __syncwarp();  // the part's place is free
-                if (lane == 0) mbar_arrive(&s.part_empty[part]);
             }
             advance();
+            mbar_arrive(&s.part_empty[block & 1]);
         }
     }
 }
@@ -816,9 +816,9 @@ __global__ void __launch_bounds__(kThreads<KVF>, 1)
             mbar_init(&s.kv_full[i], KVF ? 128 : 1);
             mbar_init(&s.kv_empty[i], 1);
         }
-        for (int i = 0; i < 8 && KVF; i++) {
-            if (i == 0) mbar_init(&s.part_full, 8);
-            mbar_init(&s.part_empty[i], D / 32);  // the warps that convert a part
+        for (int i = 0; i < 2 && KVF; i++) {
+            mbar_init(&s.part_full[i], 8);
+            mbar_init(&s.part_empty[i], 128);
         }
         mbar_init(&s.parts_done, 32 * kSoftmaxWarps);
         mbar_init(&s.last_known, 1);
