@@ -14,6 +14,7 @@ namespace qskv {
 namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32, kBuckets = 256;
+constexpr int kSharedRows = 4096;
 constexpr int kMinBlocks = 8;  // a part has at least as many key blocks
 
 struct Shared {
@@ -22,6 +23,7 @@ struct Shared {
     int longest;                // blocks of the longest part
     int begin[kBuckets];        // items of a bucket, then its first place in the list
     int slots;
+    int tile_begin[kSharedRows + 1];  // a row's first tile, of as many rows (more: in the workspace)
 };
 
 // Sum of x over the threads before this one, and over all of them.
@@ -51,18 +53,18 @@ struct Tile {
     int row, token, tokens, pos, blocks;
 };
 
-__device__ Tile tile_at(const PrefillArgs &a, int tile) {
+__device__ Tile tile_at(const PrefillArgs &a, const int *tile_begin, int tile) {
     int lo = 0, hi = a.batch;  // the last row whose first tile is at or before this one
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.tile_begin[mid] <= tile)
+        if (tile_begin[mid] <= tile)
             lo = mid;
         else
             hi = mid;
     }
     int first, n, len;
     prefill_row(a, lo, first, n, len);
-    const int per = a.tile_rows / a.group, at = (tile - a.tile_begin[lo]) * per;
+    const int per = a.tile_rows / a.group, at = (tile - tile_begin[lo]) * per;
     Tile t;
     t.row = lo, t.token = first + at, t.tokens = min(per, n - at), t.pos = len - n + at;
     t.blocks = (max(t.pos + t.tokens, 0) + a.block_keys - 1) / a.block_keys;
@@ -78,6 +80,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(PrefillArgs a) {
     if (tid < kBuckets) s.begin[tid] = 0;
     for (int i = tid; i < a.max_slots * a.num_kv_heads; i += kThreads) a.tickets[i] = 0;
     // ---- tiles a row, and their prefix
+    int *tile_begin = a.batch <= kSharedRows ? s.tile_begin : a.tile_begin;
     int tiles = 0;
     for (int base = 0; base < a.batch; base += kThreads) {
         const int b = base + tid;
@@ -89,15 +92,17 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(PrefillArgs a) {
         }
         int total;
         const int before = exclusive_sum(s, count, total);
-        if (b < a.batch) a.tile_begin[b] = tiles + before;
+        if (b < a.batch) tile_begin[b] = tiles + before;
         tiles += total;
     }
-    if (tid == 0) a.tile_begin[a.batch] = tiles;
     tiles = min(tiles, a.max_items - a.max_slots);  // sequences that overlap in q may have more: those are cut off
     __syncthreads();
     // ---- all blocks
+    Tile own = {};  // the thread's first tile, looked up once
+    if (tid < tiles) own = tile_at(a, tile_begin, tid);
+    auto tile_of = [&](int i) { return i == tid ? own : tile_at(a, tile_begin, i); };
     unsigned long long sum = 0;
-    for (int i = tid; i < tiles; i += kThreads) sum += tile_at(a, i).blocks;
+    for (int i = tid; i < tiles; i += kThreads) sum += tile_of(i).blocks;
     if (sum) atomicAdd(&s.blocks, sum);
     __syncthreads();
     int cap = 0x7fffffff;  // blocks a part has at most
@@ -108,14 +113,14 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(PrefillArgs a) {
     auto parts_of = [&](int blocks) { return blocks > cap ? (blocks + cap - 1) / cap : 1; };
     // ---- lengths
     for (int i = tid; i < tiles; i += kThreads) {
-        const int blocks = tile_at(a, i).blocks, parts = parts_of(blocks);
+        const int blocks = tile_of(i).blocks, parts = parts_of(blocks);
         atomicMax(&s.longest, (blocks + parts - 1) / parts);
     }
     __syncthreads();
     const int longest = s.longest;
     auto bucket_of = [&](int blocks) { return kBuckets - 1 - int(int64_t(blocks) * (kBuckets - 1) / max(longest, 1)); };
     for (int i = tid; i < tiles; i += kThreads) {
-        const int blocks = tile_at(a, i).blocks, parts = parts_of(blocks);
+        const int blocks = tile_of(i).blocks, parts = parts_of(blocks);
         atomicAdd(&s.begin[bucket_of((blocks + parts - 1) / parts)], parts);
     }
     __syncthreads();
@@ -126,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(PrefillArgs a) {
     __syncthreads();
     // ---- the list
     for (int i = tid; i < tiles; i += kThreads) {
-        const Tile t = tile_at(a, i);
+        const Tile t = tile_of(i);
         const int parts = parts_of(t.blocks);
         const int at = atomicAdd(&s.begin[bucket_of((t.blocks + parts - 1) / parts)], parts);
         const int slot = parts > 1 ? atomicAdd(&s.slots, parts) : 0;
