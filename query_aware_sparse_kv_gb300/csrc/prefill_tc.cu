@@ -55,8 +55,10 @@ struct Cfg {
     static constexpr int NB = D / 64;            // 64-dim (128-byte) column groups
     static constexpr int ATOM = 128 * 128;       // 128 rows x 128 bytes
     static constexpr int TILE = NB * ATOM;       // 128 rows of Q, K or V
-    static constexpr int STAGES = D == 128 ? (KVF ? 3 : 5) : 8;
-    static constexpr int PARTS = KVF ? 2 * 8 * kvf_part_bytes(D) : 0;  // codes of two blocks
+    static constexpr int STAGES = D == 128 ? (KVF ? 4 : 5) : 8;
+    // a block's codes: of each of 8 parts the keys and their powers, the values and all powers
+    static constexpr int KEYS = 16 * D + 16, VALUES = 16 * D + 32;
+    static constexpr int PARTS = KVF ? 8 * (KEYS + VALUES) : 0;
     static constexpr int SMEM = 2 * TILE + STAGES * TILE + PARTS + 1024;
     static constexpr uint32_t S_COL = 0, O_COL = 256;  // half h: S (and P) at 128 h, O at 256 + 128 h
 };
@@ -69,7 +71,7 @@ struct Slot {
 struct Shared {
     uint64_t item_full[2], item_empty[2], q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2];
     uint64_t parts_done, last_known, drain;
-    uint64_t part_full[2], part_empty[2];  // of the 8-bit codes of a block (even, odd ones): there, and no longer needed
+    uint64_t part_full[2], part_empty[2];  // of a block's 8-bit codes (keys, values): there, and no longer needed
     Slot slot[2];
     uint32_t good[kGoodRing];  // pages of a block that are there
     uint32_t tmem;
@@ -602,15 +604,15 @@ __device__ __forceinline__ void load_role(const PrefillArgs &a, Shared &s, uint8
         mbar_wait_bounded(&s.kv_full[i % C::STAGES], i / C::STAGES & 1, kWaitLimitNs);
 }
 
-// The codes of an 8-bit cache, parts of 16 tokens, a block ahead of the one that is converted.
+// The codes of an 8-bit cache: the next block's keys while values are converted, its values while keys are.
 template <int D>
-__device__ __forceinline__ void fetch_role(const PrefillArgs &a, Shared &s, uint8_t *parts) {
-    constexpr uint32_t BYTES = kvf_part_bytes(D);
+__device__ __forceinline__ void fetch_role(const PrefillArgs &a, Shared &s, uint8_t *codes) {
+    using C = Cfg<D, true>;
     const int lane = threadIdx.x & 31, page_shift = a.page_size == 16 ? 4 : 5, ppb = a.page_size == 16 ? 8 : 4;
     const int per = a.page_size >> 4;
     ItemReader items;
     Slot x;
-    uint32_t block = 0;
+    uint32_t block = 0, issued = 0;
     bool ok = true;
     while (ok && items.next(s, x, a.flags)) {
         const PrefillItem &it = x.item;
@@ -633,24 +635,32 @@ __device__ __forceinline__ void fetch_role(const PrefillArgs &a, Shared &s, uint
             const uint32_t good = __ballot_sync(0xffffffffu, lane < ppb && first >= 0);
             if (lane == 0) s.good[block % kGoodRing] = good;
             __syncwarp();
-            if (block >= 2) ok = warp_wait(s, &s.part_empty[block & 1], (block / 2 - 1) & 1, a.flags);
-            if (!ok) break;
-            if (lane < 8) {  // a lane a part
-                uint64_t *full = &s.part_full[block & 1];
-                if (id >= 0) {
-                    mbar_arrive_expect_tx(full, BYTES);
-                    bulk_load(parts + ((block & 1) * 8 + lane) * BYTES,
-                              a.pool + ((int64_t(id) * a.num_kv_heads + x.head) * per + (lane & (per - 1))) * BYTES, BYTES, full);
-                } else {
+            const uint8_t *from =
+                a.pool + ((int64_t(max(id, 0)) * a.num_kv_heads + x.head) * per + (lane & (per - 1))) * kvf_part_bytes(D);
+            for (int which = 0; which < 2; which++) {
+                if (block >= 1) ok = warp_wait(s, &s.part_empty[which], (block - 1) & 1, a.flags);
+                if (!ok) break;
+                uint64_t *full = &s.part_full[which];
+                if (lane < 8 && id >= 0) {  // a lane a part
+                    mbar_arrive_expect_tx(full, which ? C::VALUES : C::KEYS);
+                    if (which) {
+                        bulk_load(codes + 8 * C::KEYS + lane * C::VALUES, from + 16 * D, C::VALUES, full);
+                    } else {
+                        bulk_load(codes + lane * C::KEYS, from, 16 * D, full);
+                        bulk_load(codes + lane * C::KEYS + 16 * D, from + 32 * D, 16, full);
+                    }
+                } else if (lane < 8) {
                     mbar_arrive(full);
                 }
+                __syncwarp();
+                issued++;
             }
-            __syncwarp();
+            if (!ok) break;
         }
     }
     // copies under way land before the CTA's memory is released
-    for (uint32_t b = block > 2 ? block - 2 : 0; b < block; b++)
-        mbar_wait_bounded(&s.part_full[b & 1], b / 2 & 1, kWaitLimitNs);
+    for (uint32_t i = issued > 2 ? issued - 2 : 0; i < issued; i++)
+        mbar_wait_bounded(&s.part_full[i & 1], i / 2 & 1, kWaitLimitNs);
     __syncwarp();
 }
 
@@ -660,18 +670,19 @@ template <int D>
 __device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, uint8_t *ring, const uint8_t *parts) {
     using C = Cfg<D, true>;
     constexpr int TOGETHER = 128 / D, STEPS = 8 / TOGETHER;  // parts the threads cover at once, and how often they do
-    constexpr int FROM = TOGETHER * kvf_part_bytes(D), TO = TOGETHER * 16 * 128;  // bytes from one to the next
+    constexpr int K_FROM = TOGETHER * C::KEYS, V_FROM = TOGETHER * C::VALUES, TO = TOGETHER * 16 * 128;  // from one to the next
     const int tid = threadIdx.x - 32 * kConvertWarp, c = tid % D, part0 = tid / D;
     const int page_shift = a.page_size == 16 ? 4 : 5;
     const uint32_t whole = a.page_size == 16 ? 0xff : 0xf;
-    // keys: token and first 16-byte chunk (16 dims); values: pair of tokens and chunk (8 dims)
-    const int kt = c / (D / 16), kc = kvf_key_chunk<D>(c % (D / 16), kt);
+    // keys: a token's 16-byte chunk (16 dims); eight lanes have four chunks of two tokens, which meet all banks at their
+    // places here and, as two chunks of bf16 numbers each, in the ring
+    const int kt = D == 128 ? (c >> 2 & 1) + (c >> 4 << 1) : c >> 2, kc = D == 128 ? (c & 3) + (c >> 3 & 1) * 4 : c & 3;
+    // values: pair of tokens and chunk (8 dims)
     const int vp = c / (D / 8), vc = kvf_value_chunk<D>(c % (D / 8), vp);
-    const uint8_t *codes = parts + part0 * kvf_part_bytes(D) + c * 16, *powers = parts + part0 * kvf_part_bytes(D) + 32 * D;
-    // the lanes of the upper half of the dims store theirs the other way round: all banks are met
-    const int swap = D == 128 ? kc >> 2 & 1 : 0;
+    const uint8_t *k_from = parts + part0 * C::KEYS, *v_from = parts + 8 * C::KEYS + part0 * C::VALUES;
+    const uint8_t *k_codes = k_from + kt * D + kvf_key_chunk<D>(kc, kt) * 16, *v_codes = v_from + c * 16;
     const int k_to = kc / 4 * C::ATOM + (part0 * 16 + kt) * 128;
-    const int k_first = k_to + ((((kc & 3) * 2 + swap) ^ (kt & 7)) << 4), k_second = k_to + ((((kc & 3) * 2 + (swap ^ 1)) ^ (kt & 7)) << 4);
+    const int k_first = k_to + (((kc & 3) * 2 ^ (kt & 7)) << 4), k_second = k_to + ((((kc & 3) * 2 + 1) ^ (kt & 7)) << 4);
     const int v_to = vc / 8 * C::ATOM + (part0 * 16 + 2 * vp) * 128;
     const int v_first = v_to + (((vc & 7) ^ (2 * vp & 7)) << 4), v_second = v_to + 128 + (((vc & 7) ^ ((2 * vp + 1) & 7)) << 4);
     ItemReader items;
@@ -688,15 +699,14 @@ __device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, ui
         const int n = it.block1 - it.block0, end = it.pos + it.tokens;
         for (int j = 0; j < n; j++, block++) {
             const int left = end - (it.block0 + j) * 128;  // tokens of the row from the block on
-            ok = warp_wait(s, &s.part_full[block & 1], block / 2 & 1, a.flags) && (!filled || warp_wait(s, &s.kv_empty[stage], phase ^ 1, a.flags));
+            ok = warp_wait(s, &s.part_full[0], block & 1, a.flags) && (!filled || warp_wait(s, &s.kv_empty[stage], phase ^ 1, a.flags));
             if (!ok) break;
             uint8_t *to = ring + stage * C::TILE;
-            const int half = (block & 1) * 8 * kvf_part_bytes(D);
 #pragma unroll 4
             for (int i = 0; i < STEPS; i++) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(codes + half + i * FROM);
+                const uint4 w = *reinterpret_cast<const uint4 *>(k_codes + i * K_FROM);
                 uint32_t more;
-                const uint32_t power = kvf_power_bf16x2(powers[half + i * FROM + kt], more);
+                const uint32_t power = kvf_power_bf16x2(k_from[i * K_FROM + 16 * D + kt], more);
                 const uint32_t u[4] = {w.x, w.y, w.z, w.w};
                 uint32_t y[8];
 #pragma unroll
@@ -709,20 +719,20 @@ __device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, ui
 #pragma unroll
                     for (int k = 0; k < 8; k++) y[k] = kvf_mul_bf16x2(y[k], p);
                 }
-                const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-                *reinterpret_cast<uint4 *>(to + k_first + i * TO) = swap ? hi : lo;
-                *reinterpret_cast<uint4 *>(to + k_second + i * TO) = swap ? lo : hi;
+                *reinterpret_cast<uint4 *>(to + k_first + i * TO) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4 *>(to + k_second + i * TO) = make_uint4(y[4], y[5], y[6], y[7]);
             }
             advance();
-            if (filled) ok = warp_wait(s, &s.kv_empty[stage], phase ^ 1, a.flags);
+            mbar_arrive(&s.part_empty[0]);
+            ok = warp_wait(s, &s.part_full[1], block & 1, a.flags) && (!filled || warp_wait(s, &s.kv_empty[stage], phase ^ 1, a.flags));
             if (!ok) break;
             to = ring + stage * C::TILE;
             const uint32_t good = s.good[block % kGoodRing];
             const bool full = good == whole && left >= 128;
 #pragma unroll 4
             for (int i = 0; i < STEPS; i++) {
-                uint4 w = *reinterpret_cast<const uint4 *>(codes + half + 16 * D + i * FROM);
-                uint32_t e = *reinterpret_cast<const uint16_t *>(powers + half + 16 + 2 * vp + i * FROM);
+                uint4 w = *reinterpret_cast<const uint4 *>(v_codes + i * V_FROM);
+                uint32_t e = *reinterpret_cast<const uint16_t *>(v_from + i * V_FROM + 16 * D + 16 + 2 * vp);
                 const int part = i * TOGETHER + part0, row = part * 16 + 2 * vp;
                 if (!full) {  // what lies past the end may be no number
                     const bool there = good >> (part * 16 >> page_shift) & 1;
@@ -747,7 +757,7 @@ __device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, ui
                 *reinterpret_cast<uint4 *>(to + v_second + i * TO) = make_uint4(y1[0], y1[1], y1[2], y1[3]);
             }
             advance();
-            mbar_arrive(&s.part_empty[block & 1]);
+            mbar_arrive(&s.part_empty[1]);
         }
     }
 }
