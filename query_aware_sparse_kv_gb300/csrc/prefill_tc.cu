@@ -664,6 +664,13 @@ __device__ __forceinline__ void fetch_role(const PrefillArgs &a, Shared &s, uint
     __syncwarp();
 }
 
+// The values of two codes (the low half of w), which bf16 holds exactly.
+__device__ __forceinline__ uint32_t bf16_values(uint32_t w, float power) {
+    const uint32_t f = kvf_half2(w);
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f));
+    return pack_bf16x2(v.x * power, v.y * power);
+}
+
 // Codes to bf16 numbers, K and V in turn.  A part has D chunks of 16 bytes of keys and as many of values, a thread each;
 // of a K or V its chunks are STEPS parts at the same places.
 template <int D>
@@ -702,25 +709,14 @@ __device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, ui
             ok = warp_wait(s, &s.part_full[0], block & 1, a.flags) && (!filled || warp_wait(s, &s.kv_empty[stage], phase ^ 1, a.flags));
             if (!ok) break;
             uint8_t *to = ring + stage * C::TILE;
-#pragma unroll 4
+#pragma unroll 2
             for (int i = 0; i < STEPS; i++) {
                 const uint4 w = *reinterpret_cast<const uint4 *>(k_codes + i * K_FROM);
-                uint32_t more;
-                const uint32_t power = kvf_power_bf16x2(k_from[i * K_FROM + 16 * D + kt], more);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                uint32_t y[8];
-#pragma unroll
-                for (int k = 0; k < 8; k++) {
-                    const uint32_t z = __byte_perm(u[k / 2], 0, k & 1 ? 0x3424 : 0x1404);
-                    y[k] = kvf_mul_bf16x2(kvf_bf16x2(z, z >> 4), power);
-                }
-                if (more) {
-                    const uint32_t p = (127u + more) << 7 | (127u + more) << 23;
-#pragma unroll
-                    for (int k = 0; k < 8; k++) y[k] = kvf_mul_bf16x2(y[k], p);
-                }
-                *reinterpret_cast<uint4 *>(to + k_first + i * TO) = make_uint4(y[0], y[1], y[2], y[3]);
-                *reinterpret_cast<uint4 *>(to + k_second + i * TO) = make_uint4(y[4], y[5], y[6], y[7]);
+                const float power = kvf_power(k_from[i * K_FROM + 16 * D + kt]);
+                *reinterpret_cast<uint4 *>(to + k_first + i * TO) =
+                    make_uint4(bf16_values(w.x, power), bf16_values(w.x >> 16, power), bf16_values(w.y, power), bf16_values(w.y >> 16, power));
+                *reinterpret_cast<uint4 *>(to + k_second + i * TO) =
+                    make_uint4(bf16_values(w.z, power), bf16_values(w.z >> 16, power), bf16_values(w.w, power), bf16_values(w.w >> 16, power));
             }
             advance();
             mbar_arrive(&s.part_empty[0]);
@@ -728,33 +724,32 @@ __device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, ui
             if (!ok) break;
             to = ring + stage * C::TILE;
             const uint32_t good = s.good[block % kGoodRing];
-            const bool full = good == whole && left >= 128;
-#pragma unroll 4
-            for (int i = 0; i < STEPS; i++) {
+            auto values = [&](int i, bool all) {
                 uint4 w = *reinterpret_cast<const uint4 *>(v_codes + i * V_FROM);
                 uint32_t e = *reinterpret_cast<const uint16_t *>(v_from + i * V_FROM + 16 * D + 16 + 2 * vp);
-                const int part = i * TOGETHER + part0, row = part * 16 + 2 * vp;
-                if (!full) {  // what lies past the end may be no number
+                if (!all) {  // what lies past the end may be no number
+                    const int part = i * TOGETHER + part0, row = part * 16 + 2 * vp;
                     const bool there = good >> (part * 16 >> page_shift) & 1;
                     const uint32_t keep = (there && row < left ? 0x00ff00ffu : 0u) | (there && row + 1 < left ? 0xff00ff00u : 0u);
                     w.x &= keep, w.y &= keep, w.z &= keep, w.w &= keep, e &= keep;
                 }
-                uint32_t more0, more1;
-                const uint32_t p0 = kvf_power_bf16x2(e & 255, more0), p1 = kvf_power_bf16x2(e >> 8, more1);
                 const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                const float p0 = kvf_power(e & 255), p1 = kvf_power(e >> 8);
                 uint32_t y0[4], y1[4];
 #pragma unroll
                 for (int k = 0; k < 4; k++) {  // bytes in turn of both tokens
-                    y0[k] = kvf_mul_bf16x2(kvf_bf16x2(u[k] << 8, u[k] << 4), p0);
-                    y1[k] = kvf_mul_bf16x2(kvf_bf16x2(u[k], u[k] >> 4), p1);
-                }
-                if (more0 | more1) {
-                    const uint32_t q0 = (127u + more0) << 7 | (127u + more0) << 23, q1 = (127u + more1) << 7 | (127u + more1) << 23;
-#pragma unroll
-                    for (int k = 0; k < 4; k++) y0[k] = kvf_mul_bf16x2(y0[k], q0), y1[k] = kvf_mul_bf16x2(y1[k], q1);
+                    y0[k] = bf16_values(__byte_perm(u[k], 0, 0x0020), p0);
+                    y1[k] = bf16_values(__byte_perm(u[k], 0, 0x0031), p1);
                 }
                 *reinterpret_cast<uint4 *>(to + v_first + i * TO) = make_uint4(y0[0], y0[1], y0[2], y0[3]);
                 *reinterpret_cast<uint4 *>(to + v_second + i * TO) = make_uint4(y1[0], y1[1], y1[2], y1[3]);
+            };
+            if (good == whole && left >= 128) {
+#pragma unroll 2
+                for (int i = 0; i < STEPS; i++) values(i, true);
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < STEPS; i++) values(i, false);
             }
             advance();
             mbar_arrive(&s.part_empty[1]);

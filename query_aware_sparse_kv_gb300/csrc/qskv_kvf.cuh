@@ -53,24 +53,6 @@ __device__ __forceinline__ uint32_t kvf_half2(uint32_t w) {
     return r;
 }
 
-// Two e4m3 codes, in the upper bytes of x's halves (what else is in x says nothing), as bf16 numbers less 2^120: sign,
-// exponent and fraction moved to their places.  Times 2^(120 + e) they are the cached values, exactly; a code's subnormals
-// are bf16's, which a product takes as they are.
-__device__ __forceinline__ uint32_t kvf_bf16x2(uint32_t x, uint32_t x_up4) {
-    return (x & 0x80008000u) | (x_up4 & 0x07f007f0u);
-}
-__device__ __forceinline__ uint32_t kvf_mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-// 2^(120 + e) in both halves, as far as bf16 goes; powers above (values from 2^16 on) leave the rest in `more`.
-__device__ __forceinline__ uint32_t kvf_power_bf16x2(uint32_t stored, uint32_t &more) {
-    const uint32_t f = min(stored + 120u, 254u);
-    more = stored + 120u - f;
-    return f << 7 | f << 23;
-}
-
 struct KvfStoreArgs {
     const void *k, *v;     // append: [n][Hkv][d], rows k_stride / v_stride elements apart
     void *k_out, *v_out;   // gather: [n][Hkv][d]
