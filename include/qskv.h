@@ -556,8 +556,8 @@ qskv_status qskv_kvf_paged_decode(const void *q, qskv_dtype q_dtype, const void 
  *   out       [n_tokens][num_q_heads][head_dim], contiguous, q's type; must not
  *             overlap an input
  *   lse       [n_tokens][num_q_heads] fp32, or NULL
- *   n_tokens  rows of q and out; rows behind cu_new[batch] (padding) are not
- *             read, and out and lse there are left as they were.
+ *   n_tokens  rows of q and out; rows behind cu_new[batch] (padding) may hold
+ *             anything, and out and lse there are left as they were.
  *             n_tokens * num_q_heads must be below 2^31.
  *   sm_scale  0 means 1/sqrt(d)
  * Here q, out and lse are device memory.  The caches are those of
@@ -565,7 +565,8 @@ qskv_status qskv_kvf_paged_decode(const void *q, qskv_dtype q_dtype, const void 
  * qskv_kvf_paged_decode (pool); what lies in slots past seq_len may be anything.
  * With fp32 queries, and with an fp32 cache, everything is computed in fp32.
  * With bf16 queries over a bf16 or 8-bit cache the products take bf16 operands
- * (softmax weights are rounded to bf16) and sum in fp32.
+ * (softmax weights are rounded to bf16) and sum in fp32; every logit must then
+ * be below 2^30 in magnitude, in fp32 below 2^126.
  * Nothing is read before the previous kernel in the stream has completed.
  * Device errors: cu_new out of order or range, seq_len outside
  * [0, max_pages * page_size] or below n_b: clamped to what there is (a query

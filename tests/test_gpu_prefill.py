@@ -193,6 +193,88 @@ def test_bad_packing_touches_nothing_else(dtype, cache, cu):
     b.check()
 
 
+@pytest.mark.parametrize("dtype,cache", [(BF16, "bf16"), (BF16, "kvf"), (F32, "fp32")])
+def test_more_rows_than_the_plan_keeps_at_hand(dtype, cache):
+    """5000 sequences, most without new tokens, some with none at all; a long one among them, cut into parts."""
+    rows = [(i % 23, 0 if i % 25 else 1 + i // 25 % 3) for i in range(5000)]
+    rows[4321] = (6000, 2)
+    b = Batch(15, rows, 4, 1, 64, 16, dtype, cache)
+    b.run()
+    b.check()
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF16, "bf16"), (BF16, "kvf"), (F32, "fp32")])
+def test_a_captured_step_from_lengths_to_outputs(dtype, cache):
+    """Tables, store and prefill in one graph, replayed over steps of other lengths: chunks of prompts and single tokens
+    mixed, fewer tokens than the buffers hold, tables and workspace shared."""
+    g = torch.Generator().manual_seed(21)
+    B, hq, hkv, d, P, mp, N, T = 4, 8, 2, 64, 16, 40, 120, 300
+    shape = qskv.make_shape(B, hq, hkv, d, P, mp, N)
+    size = max(qskv.prefill_workspace_size(shape, T), qskv.tables_workspace_size(shape))
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    lens, grown, new, cu, slots, table, counts = i32(B), i32(B), i32(B), i32(B + 1), i32(T), i32(B, mp) - 1, i32(4)
+    free = torch.randperm(N, generator=g).int().cuda()
+    k, v = (torch.zeros((T, hkv, d), dtype=dtype, device="cuda") for _ in range(2))
+    q, out = (torch.zeros((T, hq, d), dtype=dtype, device="cuda") for _ in range(2))
+    if cache == "kvf":
+        pools = [torch.zeros((N, hkv, qskv.kvf_block_bytes(shape)), dtype=torch.uint8, device="cuda")]
+    else:
+        pools = [torch.zeros((N, hkv, P, d), dtype=dtype, device="cuda") for _ in range(2)]
+
+    def body():
+        qskv.extend_tables(lens, new, free, table, grown, cu, slots, shape, ws, counts=counts)
+        if cache == "kvf":
+            qskv.kvf_append(k, v, slots, pools[0], shape, ws)
+            qskv.kvf_paged_prefill(q, pools[0], table, grown, cu, out, shape, ws)
+        else:  # the framework stores into its own caches only; a bf16 or fp32 pool is the caller's
+            at = slots.long().clamp_min(0)
+            live = (slots >= 0)[:, None, None]
+            for pool, x in zip(pools, (k, v)):
+                old = pool[at // P, :, at % P]
+                pool[at // P, :, at % P] = torch.where(live, x, old)
+            qskv.paged_prefill(q, *pools, table, grown, cu, out, shape, ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        body()  # no new tokens yet
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        body()
+    seen = [[torch.empty((0, hkv, d), dtype=torch.float64)] * 2 for _ in range(B)]
+    # a padded place writes to slot 0's old values above, so slot 0's page is never handed out
+    free.copy_(torch.cat([free[free != 0], free[free == 0]]))
+    for step in ([120, 0, 33, 1], [1, 1, 1, 1], [150, 2, 1, 100], [0, 0, 0, 0], [1, 200, 1, 0]):
+        n = sum(step)
+        x = [torch.randn(t.shape, generator=g).to(dtype) for t in (k, v, q)]
+        for t, y in zip((k, v, q), x):
+            t.copy_(y)
+        new.copy_(_i32(step))
+        out.fill_(7.0)
+        graph.replay()
+        taken = int(counts[1])
+        free.copy_(torch.roll(free, -taken))
+        lens.copy_(grown)
+        assert qskv.get_error(ws) == 0
+        got, at = out.cpu(), 0
+        assert bool((got[n:] == 7).all())
+        for b, m in enumerate(step):
+            for i in range(2):
+                y = x[i][at:at + m].double()
+                y = F.values(*F.quantise(y)) if cache == "kvf" and m else y
+                seen[b][i] = torch.cat([seen[b][i], y])
+            if m:
+                kk, vv = seen[b]
+                for h in range(hkv):
+                    hs, pos = slice(4 * h, 4 * h + 4), len(kk) - m + torch.arange(m)
+                    o, _, pabs, A = R.attend_rows(x[2][at:at + m, hs], kk[:, h], vv[:, h], pos, d ** -0.5)
+                    tol, _ = R.bounds(o, pabs, float(vv.abs().max()), A, len(kk), d, dtype == BF16)
+                    assert bool(((got[at:at + m, hs].double() - o).abs() <= tol).all()), (step, b, h)
+            at += m
+
+
 def test_refused_arguments():
     b = Batch(9, [(4, 30)], 4, 2, 64, 16, BF16, "bf16")
     for over, match in ((dict(out=b.out.float()), "out"), (dict(lse=b.lse[:-1]), "lse"), (dict(cu_new=b.gpu["cu_new"][:-1]), "cu_new"),
