@@ -1235,7 +1235,7 @@ struct PrefillWorkspace {
 };
 
 size_t prefill_workspace(const qskv_shape *s, int64_t n_tokens, int num_sms) {
-    const size_t x = PrefillWorkspace(s, n_tokens, num_sms, kPrefillSimtRows, 0).total;
+    const size_t x = PrefillWorkspace(s, n_tokens, num_sms, kPrefillFp32Rows, 0).total;
     const size_t y = PrefillWorkspace(s, n_tokens, num_sms, kPrefillTcRows, kPrefillWaves).total;
     return x > y ? x : y;
 }
@@ -1274,8 +1274,8 @@ qskv_status prefill(const void *q, qskv_dtype q_dtype, int64_t q_stride, const v
     QSKV_TRY(check_workspace(workspace, workspace_bytes, prefill_workspace(shape, n_tokens, sms)));
     PrefillArgs a = {};
     const bool tensor_cores = q_dtype == QSKV_BF16 && kv_dtype == QSKV_BF16;
-    a.tile_rows = tensor_cores ? kPrefillTcRows : kPrefillSimtRows;
-    a.block_keys = tensor_cores ? kPrefillTcKeys : kPrefillSimtKeys;
+    a.tile_rows = tensor_cores ? kPrefillTcRows : kPrefillFp32Rows;
+    a.block_keys = tensor_cores ? kPrefillTcKeys : prefill_fp32_keys(shape->head_dim);
     a.waves = tensor_cores ? kPrefillWaves : 0;
     const PrefillWorkspace L(shape, n_tokens, sms, a.tile_rows, a.waves);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -1324,7 +1324,7 @@ qskv_status prefill(const void *q, qskv_dtype q_dtype, int64_t q_stride, const v
     cudaError_t e = launch_prefill_plan(a, st);
     if (e == cudaSuccess)
         e = tensor_cores ? launch_prefill_tc(a, &tq, &tk, &tv, shape->head_dim, st)
-                         : launch_prefill_simt(a, q_dtype, kv_dtype, shape->head_dim, st);
+                         : launch_prefill_fp32(a, q_dtype, kv_dtype, shape->head_dim, st);
     return launched(e, what);
 }
 }  // namespace

@@ -1,6 +1,6 @@
 // Causal attention of the newest tokens of every row of a batch (a prompt, or
 // a chunk of one behind what is cached) over the row's pages: argument block,
-// work items and launchers (prefill_plan.cu, prefill_simt.cu, prefill_tc.cu).
+// work items and launchers (prefill_plan.cu, prefill_fp32.cu, prefill_tc.cu).
 //
 // Row b holds seq_lens[b] tokens; the last n_b = cu_new[b + 1] - cu_new[b] of
 // them are the queries cu_new[b].. of q.  Query i stands at pos = seq_len -
@@ -74,15 +74,17 @@ __device__ __forceinline__ void prefill_row(const PrefillArgs &a, int b, int &fi
 }
 
 // Which kernel a call takes, and the sizes of its work: tiles of kPrefillTcRows rows on the tensor cores (bf16 queries
-// over bf16 or 8-bit caches), of kPrefillSimtRows in fp32 arithmetic.
+// over bf16 or 8-bit caches), of kPrefillFp32Rows where
+// fp32 is kept.
 constexpr int kPrefillTcRows = 256, kPrefillTcKeys = 128;
 constexpr int kPrefillWaves = 2;
-constexpr int kPrefillSimtRows = 64, kPrefillSimtKeys = 64;
+constexpr int kPrefillFp32Rows = 64;
+constexpr int prefill_fp32_keys(int head_dim) { return head_dim == 64 ? 64 : 32; }
 
 cudaError_t launch_prefill_plan(const PrefillArgs &a, cudaStream_t stream);
 // q: the queries as [n_tokens][Hq][D], boxes of 64 dims x G heads x 128 / G tokens; k, v: the pools' 16 x 64 boxes.
 cudaError_t launch_prefill_tc(const PrefillArgs &a, const CUtensorMap *q, const CUtensorMap *k, const CUtensorMap *v,
                               int head_dim, cudaStream_t stream);
-cudaError_t launch_prefill_simt(const PrefillArgs &a, int q_dtype, int kv_dtype, int head_dim, cudaStream_t stream);
+cudaError_t launch_prefill_fp32(const PrefillArgs &a, int q_dtype, int kv_dtype, int head_dim, cudaStream_t stream);
 
 }  // namespace qskv

@@ -3,6 +3,8 @@
 Codes are bytes, numbers come from their bits; packing moves them to their
 places by the rules stated in include/qskv.h.  Nothing here calls the library.
 """
+import functools
+
 import torch
 
 NAN = 0x7F  # e4m3's not-a-number
@@ -12,6 +14,7 @@ def part_bytes(d):
     return 16 * (2 * d + 2)
 
 
+@functools.lru_cache
 def places(d, P):
     """Bytes within a block of [P][d] key codes, [P][d] value codes, [P] key and [P] value powers, written out."""
     key, val = torch.empty((P, d), dtype=torch.long), torch.empty((P, d), dtype=torch.long)
