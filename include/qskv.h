@@ -564,7 +564,7 @@ qskv_status qskv_kvf_paged_decode(const void *q, qskv_dtype q_dtype, const void 
  * qskv_sparse_paged_decode (k_pool, v_pool in kv_dtype) and of
  * qskv_kvf_paged_decode (pool); what lies in slots past seq_len may be anything.
  * With fp32 queries, and with an fp32 cache, everything is kept in fp32 (the
- * products are sums of products of three bf16 parts each, within 2^-23).
+ * products are sums of products of three bf16 parts each, within 2^-22).
  * With bf16 queries over a bf16 or 8-bit cache the products take bf16 operands
  * (softmax weights are rounded to bf16) and sum in fp32; every logit must then
  * be below 2^30 in magnitude, in fp32 below 2^126.

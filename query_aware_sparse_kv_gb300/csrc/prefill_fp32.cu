@@ -3,8 +3,8 @@
 //
 // Products go through mma.sync as sums of products of bf16 parts: an fp32
 // number is x0 + x1 + x2, each part the next 8 bits, over fp32's whole range,
-// and x y = x0 y0 + (x0 y1 + x1 y0) + (x0 y2 + x1 y1 + x2 y0) within 2^-23 of
-// itself; a cached value that is a bf16 number is one part, of three products.
+// and x y = x0 y0 + (x0 y1 + x1 y0) + (x0 y2 + x1 y1 + x2 y0) within 2^-22 of
+// itself (x1 y2 < 2^-23, x2 y1 < 2^-24); a cached value that is a bf16 number is one part, of three products.
 // x0 y0 and the rest are summed apart and joined in fp32, a block's outputs
 // likewise, so that the products' own summation runs over few terms.  Keys and
 // values are cut (hi bits as they are, which is exact and cannot overflow),

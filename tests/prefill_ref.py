@@ -28,7 +28,9 @@ def bounds(o, pabs, vmax, A, T, d, bf16):
     fp32 arithmetic: logits within (d + 16) roundings of 2^-24 on A, the
     largest sum of absolute products; a change of every logit by at most e
     changes an output by at most 2 e max|v|, the lse by e; exp2 within 2^-22;
-    sums of T terms.  With bf16 operands in addition each weight is rounded
+    sums of T terms.  Where fp32 products are sums of products of bf16 parts
+    each is within 4 roundings, and their sum in steps of 16 within d / 8 of
+    them, T / 8 for the outputs: less.  With bf16 operands in addition each weight is rounded
     (2^-8 of it, so 2^-8 sum p|v|) and the output (2^-8 of it); the weights'
     sum is taken before their rounding.
     """
