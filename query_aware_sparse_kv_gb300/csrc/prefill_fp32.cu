@@ -38,7 +38,7 @@ constexpr int kRows = kPrefillFp32Rows, kThreads = 128;
 // among more warps, and short prompts are as long as their longest tile.  128 dims leave room for 32 keys.
 template <int D>
 constexpr int kKeys = prefill_fp32_keys(D);
-constexpr int kCtas = 2;  // an SM
+constexpr int kCtas = prefill_fp32_ctas(1);  // an SM
 
 enum Cache { kF32 = 0, kBf16 = 1, kKvf = 2 };
 template <int CACHE>
@@ -181,13 +181,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) prefill_fp32_kernel(PrefillAr
     constexpr uint32_t kRow = (D + 8) * 2, kQPart = kRows * kRow, kPart = KEYS * kRow;
     pdl_trigger();
     pdl_wait();
-    const int total = int(__ldcg(&a.plan->items)) * a.num_kv_heads;
-    while (true) {
-        if (tid == 0) s.next = int(atomicAdd(&a.plan->next, 1u));
+    const int total = (a.direct ? a.batch : int(__ldcg(&a.plan->items))) * a.num_kv_heads;
+    for (int round = 0;; round++) {
+        if (tid == 0) s.next = a.direct ? round ? total : int(blockIdx.x) : int(atomicAdd(&a.plan->next, 1u));
         __syncthreads();
         const int next = s.next;
         if (next >= total) return;
-        if (tid == 0) s.item = a.items[next / a.num_kv_heads];
+        if (tid == 0 && !a.direct) s.item = a.items[next / a.num_kv_heads];
+        if (tid == 0 && a.direct) {  // a row's only tile
+            int len;
+            s.item.row = next / a.num_kv_heads;
+            prefill_row(a, next / a.num_kv_heads, s.item.token, s.item.tokens, len);
+            s.item.pos = len - s.item.tokens, s.item.block0 = 0;
+            s.item.block1 = s.item.tokens ? (len + KEYS - 1) / KEYS : 0;
+        }
         __syncthreads();
         const PrefillItem it = s.item;
         const int g = next % a.num_kv_heads, rows = it.tokens * G, last = it.pos + it.tokens;  // keys the tile sees
@@ -348,7 +355,7 @@ cudaError_t launch_one(const PrefillArgs &a, cudaStream_t stream) {
     constexpr size_t bytes = sizeof(Smem<D, QBF16 ? 1 : 3, kCacheParts<CACHE>>);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     if (e != cudaSuccess) return e;
-    const int64_t most = int64_t(a.max_items) * a.num_kv_heads, ctas = kCtas * a.num_sms;
+    const int64_t most = int64_t(a.direct ? a.batch : a.max_items) * a.num_kv_heads, ctas = prefill_fp32_ctas(a.num_sms);
     return launch_pdl(kernel, dim3(unsigned(most < ctas ? most : ctas)), dim3(kThreads), bytes, stream, a);
 }
 

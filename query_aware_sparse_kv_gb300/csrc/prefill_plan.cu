@@ -16,7 +16,6 @@ namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32, kBuckets = 256;
 constexpr int kSharedRows = 4096;
-constexpr int kMinBlocks = 8;  // a part has at least as many key blocks
 
 struct Shared {
     int warp_sum[kWarps];
@@ -109,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(PrefillArgs a) {
     int cap = 0x7fffffff;  // blocks a part has at most
     if (a.waves > 0) {
         const unsigned long long share = s.blocks * a.num_kv_heads / (unsigned(a.num_sms) * unsigned(a.waves)) + 1;
-        cap = int(min(max(share, (unsigned long long)kMinBlocks), 0x7fffffffull));
+        cap = int(min(max(share, (unsigned long long)kPrefillMinBlocks), 0x7fffffffull));
     }
     auto parts_of = [&](int blocks) { return blocks > cap ? (blocks + cap - 1) / cap : 1; };
     // ---- lengths

@@ -71,16 +71,103 @@ struct Cfg {
     static constexpr uint32_t S_COL = 0, O_COL = 256;  // half h: S (and P) at 128 h, O at 256 + 128 h
 };
 
+// (max_slots Hkv is below 2^18, tickets without a list are fewer than SMs)
+constexpr int kPlaceBits = 20, kPlaceMask = (1 << kPlaceBits) - 1;
+
 struct Slot {
     PrefillItem item;
-    int head;  // KV head; -1: no more items
+    int head;   // KV head; -1: no more items
+    int place;  // of a tile in parts: where their results lie; direct: its ticket above that
+};
+
+// A row's tile, where there is no list: its queries and key blocks, and the units of work that they count as (of one KV
+// head, after `before` of the rows ahead).
+struct RowWork {
+    int first, n, pos, blocks;
+    uint32_t units, before;
+};
+
+// Items without a list.  The tiles' key blocks, row by row and head by head, are units on a line that is cut into ranges:
+// one a CTA, all as long (within one), where that gives a CTA kPrefillMinBlocks or more; else as many as tiles have parts of
+// kPrefillMinBlocks blocks, the last part's rest counted in.
+struct Line {
+    uint32_t units, ranges, least, more;  // the first `more` ranges have least + 1 units, the others least
+    uint32_t range, at, end;              // this CTA's range, and what of it is still to do
+
+    __device__ __forceinline__ uint32_t begin(uint32_t r) const { return r * least + min(r, more); }
+    __device__ __forceinline__ uint32_t range_of(uint32_t x) const {
+        const uint32_t first = more * (least + 1);
+        return x < first ? x / (least + 1) : more + (x - first) / least;
+    }
+    // (the whole list warp, a lane a row; what follows is its first lane's)
+    __device__ void make(const PrefillArgs &a, RowWork *rows) {
+        const int lane = threadIdx.x & 31;
+        RowWork w = {};
+        if (lane < a.batch) {
+            int len;
+            prefill_row(a, lane, w.first, w.n, len);
+            w.pos = len - w.n;
+            w.blocks = w.n > 0 ? (len + a.block_keys - 1) / a.block_keys : 0;
+            w.units = w.n > 0 ? max(w.blocks, 1) : 0;
+        }
+        const uint32_t heads = a.num_kv_heads;
+        const uint64_t all = uint64_t(__reduce_add_sync(0xffffffffu, w.units)) * heads;
+        const bool even = all >= uint64_t(kPrefillMinBlocks) * gridDim.x;
+        if (!even) w.units = (w.units + kPrefillMinBlocks - 1) / kPrefillMinBlocks * kPrefillMinBlocks;
+        w.before = w.units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, w.before, o);
+            if (lane >= o) w.before += up;
+        }
+        const uint32_t tiles = __shfl_sync(0xffffffffu, w.before, 31);
+        w.before -= w.units;
+        rows[lane] = w;
+        if (lane == 0) {
+            units = tiles * heads;
+            ranges = even ? gridDim.x : units / kPrefillMinBlocks;
+            least = ranges ? units / ranges : 0, more = ranges ? units % ranges : 0;
+            range = blockIdx.x, at = end = 0;
+            if (range < ranges) at = begin(range), end = begin(range + 1);
+        }
+        __syncwarp();
+    }
+    // The next item; leaves x as it is where there is none.
+    __device__ void next(const PrefillArgs &a, const RowWork *rows, Slot &x) {
+        if (at == end) {
+            range += gridDim.x;
+            if (range >= ranges) return;
+            at = begin(range), end = begin(range + 1);
+        }
+        const uint32_t heads = a.num_kv_heads;
+        int r = 0;  // the row that the unit is in
+#pragma unroll
+        for (int step = kPrefillDirectRows / 2; step; step >>= 1) {
+            const RowWork &w = rows[r + step - 1];
+            if ((w.before + w.units) * heads <= at) r += step;
+        }
+        const RowWork w = rows[r];
+        const uint32_t off = at - w.before * heads, head = off / w.units, block = off - head * w.units;
+        const uint32_t take = min(w.units - block, end - at), tile = at - block;
+        const uint32_t first = range_of(tile), last = range_of(tile + w.units - 1);
+        at += take;
+        x.item = {};
+        x.item.row = r, x.item.token = w.first, x.item.tokens = w.n, x.item.pos = w.pos;
+        x.item.block0 = min(int(block), w.blocks), x.item.block1 = min(int(block + take), w.blocks);
+        x.item.part = range - first, x.item.parts = last - first + 1;
+        // parts are numbered by range and tile: the next tile's first is in this one's last range or behind it
+        const uint32_t ticket = r * heads + head;
+        x.head = head, x.place = int(ticket << kPlaceBits | (ticket + first));
+    }
 };
 
 struct Shared {
     uint64_t item_full[2], item_empty[2], q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2];
     uint64_t parts_done, last_known, drain;
     uint64_t part_full[2], part_empty[2];  // of a block's 8-bit codes (keys, values): there, and no longer needed
-    Slot slot[2];
+    Slot slot[4];
+    RowWork rows[kPrefillDirectRows];
+    Line line;
     uint32_t good[kGoodRing];  // pages of a block that are there
     uint32_t tmem;
     uint32_t last;
@@ -214,17 +301,19 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
-// The next item, copied out of its slot.
+// The next item, copied out of its slot.  A role is at most two items behind the list warp, so of four slots the one that it
+// works on is still as it was.
 struct ItemReader {
-    int slot = 0, phase = 0;
+    uint32_t n = 0;  // items so far
     __device__ __forceinline__ bool next(Shared &s, Slot &x, uint32_t *flags) {
-        if (!warp_wait(s, &s.item_full[slot], phase, flags)) return false;
-        x = s.slot[slot];
+        if (!warp_wait(s, &s.item_full[n & 1], n >> 1 & 1, flags)) return false;
+        x = s.slot[n & 3];
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(&s.item_empty[slot]);
-        if ((slot ^= 1) == 0) phase ^= 1;
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&s.item_empty[n & 1]);
+        n++;
         return x.head >= 0;
     }
+    __device__ __forceinline__ const Slot &current(const Shared &s) const { return s.slot[(n - 1) & 3]; }
 };
 
 // ------------------------------------------------------------- softmax --
@@ -341,9 +430,11 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
         }
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
-        const int64_t head = (int64_t(it.token + token) * a.num_q_heads) + x.head * G + (tile_row & (G - 1));
+        const Slot &now = items.current(s);  // (read here: the softmax has no registers to keep it in)
+        const int64_t head = int64_t(now.item.token + token) * a.num_q_heads + now.head * G + (tile_row & (G - 1));
         uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + head * D);
-        const int64_t slot0 = int64_t(it.slot) * a.num_kv_heads + x.head;  // part p: + p Hkv
+        const int parts = now.item.parts, part = now.item.part;
+        const int64_t place = now.place & kPlaceMask;  // part p's results: p behind it
         // of a part: its row's outputs, 4 dims at [dim / 4][row]
         float4 *part_o = reinterpret_cast<float4 *>(a.part_o) + tile_row;
         constexpr int64_t kPart = int64_t(D / 4) * kPrefillTcRows;
@@ -361,14 +452,14 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
                     float f[32];
 #pragma unroll
                     for (int k = 0; k < 32; k++) f[k] = l > 0.f ? __uint_as_float(o[k]) * inv : 0.f;
-                    if (it.parts == 1) {
+                    if (parts == 1) {
 #pragma unroll
                         for (int k = 0; k < 4; k++)
                             out[c / 8 + k] =
                                 make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]), pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
                                            pack_bf16x2(f[8 * k + 4], f[8 * k + 5]), pack_bf16x2(f[8 * k + 6], f[8 * k + 7]));
                     } else {
-                        float4 *to = part_o + (slot0 + int64_t(it.part) * a.num_kv_heads) * kPart + c / 4 * kPrefillTcRows;
+                        float4 *to = part_o + (place + part) * kPart + c / 4 * kPrefillTcRows;
 #pragma unroll
                         for (int k = 0; k < 8; k++)
                             to[k * kPrefillTcRows] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
@@ -378,18 +469,20 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
             }
         }
         tc_fence_before();
-        if (it.parts == 1) {
+        if (parts == 1) {
             if (mine && a.lse) a.lse[head] = lse2 * 0.6931471805599453f;
             continue;
         }
         // ---- a part: the last one that is done joins them, in their order
-        if (mine) a.part_lse[(slot0 + int64_t(it.part) * a.num_kv_heads) * kPrefillTcRows + tile_row] = lse2;
+        if (mine) a.part_lse[(place + part) * kPrefillTcRows + tile_row] = lse2;
         __threadfence();
         mbar_arrive(&s.parts_done);
         if (threadIdx.x == 0) {
             if (wait_phase(s, &s.parts_done, parts_phase, a.flags)) {
-                const uint32_t done = atomicAdd(a.tickets + slot0, 1u);
-                s.last = done == uint32_t(it.parts) - 1;
+                uint32_t *ticket = a.tickets + (a.direct ? now.place >> kPlaceBits : int(place));
+                const uint32_t done = atomicAdd(ticket, 1u);
+                s.last = done == uint32_t(parts) - 1;
+                if (s.last && a.direct) *ticket = 0;
                 __threadfence();
                 mbar_arrive(&s.last_known);
             }
@@ -400,12 +493,11 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
         if (!s.last) continue;
         __threadfence();
         if (!mine) continue;
-        const float *part_lse = a.part_lse + slot0 * kPrefillTcRows + tile_row;
-        const int64_t step = int64_t(a.num_kv_heads) * kPrefillTcRows;
+        auto lse_of = [&](int p) { return __ldcg(a.part_lse + (place + p) * kPrefillTcRows + tile_row); };
         float most = -INFINITY, total = 0.f;
-        for (int p = 0; p < it.parts; p++) most = fmaxf(most, __ldcg(part_lse + p * step));
+        for (int p = 0; p < parts; p++) most = fmaxf(most, lse_of(p));
         if (most > -INFINITY)
-            for (int p = 0; p < it.parts; p++) total += ex2(__ldcg(part_lse + p * step) - most);
+            for (int p = 0; p < parts; p++) total += ex2(lse_of(p) - most);
         const float share = total > 0.f ? 1.f / total : 0.f;
         if (a.lse) a.lse[head] = total > 0.f ? (most + log2f(total)) * 0.6931471805599453f : -INFINITY;
 #pragma unroll 1
@@ -413,9 +505,9 @@ __device__ void softmax_role(const PrefillArgs &a, Shared &s, uint8_t *ring, uin
             float4 f[8];
 #pragma unroll
             for (int k = 0; k < 8; k++) f[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int p = 0; p < it.parts; p++) {
-                const float w = most > -INFINITY ? ex2(__ldcg(part_lse + p * step) - most) * share : 0.f;
-                const float4 *from = part_o + (slot0 + int64_t(p) * a.num_kv_heads) * kPart + c * 2 * kPrefillTcRows;
+            for (int p = 0; p < parts; p++) {
+                const float w = most > -INFINITY ? ex2(lse_of(p) - most) * share : 0.f;
+                const float4 *from = part_o + (place + p) * kPart + c * 2 * kPrefillTcRows;
 #pragma unroll
                 for (int k = 0; k < 8; k++) {
                     const float4 o = __ldcg(from + k * kPrefillTcRows);
@@ -765,30 +857,32 @@ __device__ __forceinline__ void convert_role(const PrefillArgs &a, Shared &s, ui
     }
 }
 
-// Takes items from the list, one ahead of the CTA's other roles, and loads their queries.
+// Takes items from the list, or its share of the line, one ahead of the CTA's other roles, and loads their queries.
 template <int D>
 __device__ void list_role(const PrefillArgs &a, Shared &s, uint8_t *q, const CUtensorMap *map_q) {
     using C = Cfg<D, false>;  // its tiles are as large for both caches
+    if (a.direct) s.line.make(a, s.rows);
     if ((threadIdx.x & 31) != 0) return;
-    const int total = int(__ldcg(&a.plan->items)) * a.num_kv_heads, per = 128 / a.group;
-    int slot = 0, phase = 0, q_phase = 0;
+    const int total = a.direct ? 0 : int(__ldcg(&a.plan->items)) * a.num_kv_heads, per = 128 / a.group;
+    int q_phase = 0;
     bool q_used = false;
     for (int i = 0;; i++) {
-        const int next = int(atomicAdd(&a.plan->next, 1u));
-        if (i >= 2 && !wait_phase(s, &s.item_empty[slot], phase ^ 1, a.flags)) break;
-        Slot x;
+        const int next = a.direct ? 0 : int(atomicAdd(&a.plan->next, 1u));
+        if (i >= 2 && !wait_phase(s, &s.item_empty[i & 1], (i >> 1 & 1) ^ 1, a.flags)) break;
+        Slot &x = s.slot[i & 3];
         x.head = -1;
-        if (next < total) {
+        if (a.direct) {
+            s.line.next(a, s.rows, x);
+        } else if (next < total) {
             const int4 *from = reinterpret_cast<const int4 *>(a.items + next / a.num_kv_heads);
             int4 *to = reinterpret_cast<int4 *>(&x.item);
 #pragma unroll
             for (int k = 0; k < int(sizeof(PrefillItem) / 16); k++) to[k] = __ldcg(from + k);
             x.head = next % a.num_kv_heads;
+            x.place = x.head * a.max_slots + x.item.slot;
         }
-        s.slot[slot] = x;
-        mbar_arrive(&s.item_full[slot]);
+        mbar_arrive(&s.item_full[i & 1]);
         if (x.head < 0) break;
-        if ((slot ^= 1) == 0) phase ^= 1;
         if (x.item.block1 == x.item.block0) continue;
         if (q_used) {
             if (!wait_phase(s, &s.q_empty, q_phase, a.flags)) break;

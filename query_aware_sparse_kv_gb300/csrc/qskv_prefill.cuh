@@ -14,7 +14,9 @@
 // their heads go.  A work item is one tile, one KV head and a range of
 // key blocks.  The lengths are on the device, so a kernel of one CTA
 // (prefill_plan_kernel) makes the list of items; the CTAs of the attention
-// take them by a counter, the longest first.
+// take them by a counter, the longest first.  Where every row's queries fit one
+// tile for sure (few tokens of few rows), there is no list: a CTA finds its own
+// share from the lengths.
 #pragma once
 
 #include "qskv_device.cuh"
@@ -51,15 +53,17 @@ struct PrefillArgs {
     PrefillPlan *plan;
     int32_t *tile_begin;       // [batch + 1]: a sequence's first tile
     PrefillItem *items;
-    uint32_t *tickets;         // [max_slots][Hkv]: parts of a tile that are done (counted at the slot of part 0)
-    float *part_o;             // [max_slots][Hkv][tile_rows][D]: a part's outputs
-    float *part_lse;           // [max_slots][Hkv][tile_rows], log2 domain
+    uint32_t *tickets;         // [Hkv][max_slots]: parts of a tile that are done (counted at the slot of part 0);
+                               // direct: [batch][Hkv], zero between calls
+    float *part_o;             // [Hkv][max_slots][tile_rows][D]: a part's outputs
+    float *part_lse;           // [Hkv][max_slots][tile_rows], log2 domain
     int64_t q_stride;
     int32_t n_tokens, batch, num_q_heads, num_kv_heads, group, page_size, max_pages, num_pool_pages;
     int32_t tile_rows, block_keys;  // rows of a tile, keys of a block
     int32_t max_items, max_slots;   // room of the lists
     int32_t waves;             // parts are made so that an SM has about this many (0: no tile is cut)
     int32_t num_sms;
+    int32_t direct;            // no list: every row has one tile at most
     float scale_log2;          // sm_scale * log2(e)
 };
 
@@ -78,8 +82,11 @@ __device__ __forceinline__ void prefill_row(const PrefillArgs &a, int b, int &fi
 // fp32 is kept.
 constexpr int kPrefillTcRows = 256, kPrefillTcKeys = 128;
 constexpr int kPrefillWaves = 2;
+constexpr int kPrefillMinBlocks = 8;   // a part has at least as many key blocks
+constexpr int kPrefillDirectRows = 32; // rows of a batch that needs no list
 constexpr int kPrefillFp32Rows = 64;
 constexpr int prefill_fp32_keys(int head_dim) { return head_dim == 64 ? 64 : 32; }
+constexpr int prefill_fp32_ctas(int num_sms) { return 2 * num_sms; }
 
 cudaError_t launch_prefill_plan(const PrefillArgs &a, cudaStream_t stream);
 // q: the queries as [n_tokens][Hq][D], boxes of 64 dims x G heads x 128 / G tokens; k, v: the pools' 16 x 64 boxes.

@@ -146,6 +146,34 @@ def test_work_splits(dtype, cache, rows, hq, hkv, d, P):
     assert torch.equal(b.out, first[0]) and torch.equal(b.lse, first[1])
 
 
+FEW = [
+    ([(0, 1)], 2, 1, 64, 16),
+    ([(0, 3), (200, 0), (255, 1), (0, 0), (131, 5)], 4, 2, 128, 16),
+    ([(1000 + 100 * i, i % 3) for i in range(19)], 8, 4, 64, 16),           # each tile in parts, some rows without one
+    ([(9000, 5), (1, 2), (20000, 1)], 8, 2, 128, 32),                       # a CTA has a range of one tile
+    ([(3000 + 500 * (i % 5), 1) for i in range(32)], 4, 4, 64, 16),         # and of several
+    ([(0, 1 + i % 2) for i in range(32)], 4, 4, 64, 32),
+    ([(30000, 17)], 16, 2, 64, 16),
+]
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("rows,hq,hkv,d,P", FEW)
+def test_few_tokens_of_few_rows(dtype, cache, rows, hq, hkv, d, P):
+    """No list is made for these; the counters that they share with other calls are as they were after each."""
+    b = Batch(len(rows) + d + P, rows, hq, hkv, d, P, dtype, cache, pad=1)
+    b.run(scale=0.2)
+    first = b.out.clone(), b.lse.clone()
+    b.check(scale=0.2)
+    assert not bool(b.ws[:256 + 4 * len(rows) * hkv].any())
+    for _ in range(3):  # equal inputs, equal bits
+        b.run(scale=0.2)
+        assert torch.equal(b.out, first[0]) and torch.equal(b.lse, first[1])
+    lens = [max(x - 7, 0) if i % 2 else x for i, x in enumerate(b.lens)]  # some shorter than what is new
+    b.run(scale=0.2, seq_lens=_i32(lens))
+    b.check(scale=0.2, lens=lens, error=5 if any(n > x for n, x in zip(b.new, lens)) else 0)
+
+
 @pytest.mark.parametrize("dtype,cache", KINDS)
 def test_unusual_values(dtype, cache):
     """Logits far apart, growing along the row, all equal; large values."""
