@@ -575,6 +575,8 @@ qskv_status qskv_kvf_paged_decode(const void *q, qskv_dtype q_dtype, const void 
  * pool: its tokens are skipped; both flag QSKV_ERR_DEVICE_INDEX.
  * Workspace: qskv_prefill_workspace_size bytes, 256-byte aligned, zeroed once;
  * it may be shared with the other calls (of the same batch and num_kv_heads).
+ * After QSKV_ERR_DEVICE_TIMEOUT it must be zeroed again: the call that gave up
+ * may have left its counters behind.
  */
 size_t qskv_prefill_workspace_size(const qskv_shape *shape, int32_t n_tokens);
 

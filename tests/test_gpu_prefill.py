@@ -174,6 +174,54 @@ def test_few_tokens_of_few_rows(dtype, cache, rows, hq, hkv, d, P):
     b.check(scale=0.2, lens=lens, error=5 if any(n > x for n, x in zip(b.new, lens)) else 0)
 
 
+@pytest.mark.parametrize("cache", ["bf16", "kvf"])
+def test_graphs_with_and_without_a_list_share_a_workspace(cache):
+    """Few queries, the same ones within a longer buffer (a list is made then), and a decode over the same pages and counters,
+    each captured; replayed in turn while the lengths change."""
+    b = Batch(11, [(2000, 4), (40, 0), (0, 3), (9000, 5)], 8, 2, 128, 16, BF16, cache, pad=0, room=100)
+    T, long_q = b.T, torch.zeros((b.T + 100, 8, 128), dtype=BF16, device="cuda")
+    long_q[:T] = b.gpu["q"]
+    long_out, long_lse = torch.full_like(long_q, 7.0), torch.full((T + 100, 8), 7.0, device="cuda")
+    size = max(b.ws.numel(), qskv.kvf_workspace_size(b.shape), qskv.workspace_size(b.shape))
+    b.ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    one = torch.randn((4, 8, 128), device="cuda").to(BF16)
+    dec = torch.empty((4, 8, 128), device="cuda")
+
+    def decode():
+        if cache == "kvf":
+            qskv.kvf_paged_decode(one, b.pools["pool"], b.gpu["page_table"], b.gpu["seq_lens"], dec, b.shape, b.ws)
+        else:
+            qskv.sparse_paged_decode(one, b.pools["k_pool"], b.pools["v_pool"], b.gpu["page_table"], b.gpu["seq_lens"], dec,
+                                     b.shape, b.ws)
+
+    calls = [b.run, lambda: b.run(q=long_q, out=long_out, lse=long_lse), decode]
+    graphs = []
+    for call in calls:
+        call()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    lens = list(b.lens)
+    for cut in (0, 5, 900, 0):
+        now = [max(x - cut, n) for x, n in zip(lens, b.new)]
+        b.gpu["seq_lens"].copy_(_i32(now))
+        decode()
+        want = dec.clone()
+        for order in ((0, 1, 2), (2, 0, 0), (1, 0, 2), (0, 2, 1)):
+            b.out.fill_(7.0), b.lse.fill_(7.0), dec.fill_(7.0)
+            for i in order:
+                graphs[i].replay()
+            if 0 in order:
+                b.check(lens=now)
+            if 2 in order:
+                assert torch.equal(dec, want)
+            if 1 in order:
+                assert bool((long_out[T:] == 7).all())
+                # two bf16 evaluations, each within 2^-8 (1 + 2^-7) of the weighted values and of the output, and little more
+                assert float((long_out[:T].float() - b.out.float()).abs().max()) <= 2.1 * 2.0 ** -7 * float(b.v.abs().max())
+
+
 @pytest.mark.parametrize("dtype,cache", KINDS)
 def test_unusual_values(dtype, cache):
     """Logits far apart, growing along the row, all equal; large values."""
