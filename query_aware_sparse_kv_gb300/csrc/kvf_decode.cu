@@ -19,10 +19,13 @@
 //   * The order of dims within a product is free: a lane's operands of a key
 //     are 16-byte chunks of its row, those of a value pair's row likewise.
 //
-// Softmax.  One running reference M a head, such that no weight w = 2^(x + f - M)
-// passes 2^15 (fp16) and no p = 2^(x - M) passes 2^104 (their fp32 sum): it
-// moves only when one would, to where the largest weight is 2^8, or the
-// largest p 2^100.  Sums of p stay per lane until the row ends.
+// Softmax.  Two running references a head, whole numbers: M of the logits,
+// p = 2^(x - M), and R of the values' powers on top of it, w = 2^(x - M + f - R).
+// They move only when a p or a w would pass 2^15 (fp16): M to the largest
+// logit, R to where the largest w is above 2^8, but never so far down that
+// outputs would grow.  A sum of both, as one number, would lose the powers
+// beside large logits; and moves by powers of two are exact.  Sums of p stay
+// per lane until the row ends.
 //
 // One GB300, GPU time: 32 sequences x 8 KV heads x 128 pages of 16 tokens, 4
 // heads a group: 32.0 us (4.3 TB/s; the start and the fold are 6 us of it);
@@ -52,7 +55,8 @@ struct KvfState {
     uint32_t q[KS][4];
     float scale;      // logits, in units of log2, of the products
     float m, l;
-    float o[ND][2];   // head g, dims (2 t) ND + i and (2 t + 1) ND + i
+    float r;          // R + 127, of stored powers
+    float o[ND][2];   // head g, dims (2 t) ND + i and (2 t + 1) ND + i; times 2^(M + R)
 
     __device__ __forceinline__ void attach(uint8_t *, int) {}
 
@@ -106,7 +110,7 @@ struct KvfState {
     }
 
     __device__ __forceinline__ void clear() {
-        m = kNoRef, l = 0.f;
+        m = kNoRef, l = 0.f, r = 127.f;
 #pragma unroll
         for (int i = 0; i < ND; i++) o[i][0] = o[i][1] = 0.f;
     }
@@ -148,12 +152,12 @@ struct KvfState {
             for (int k = 0; k < 2; k++) {
                 const float s = (c[j][k] + c2[j][k]) + (c[j][2 + k] + c2[j][2 + k]);
                 x[j][k] = s * (kvf_power(pk >> (8 * k) & 255) * scale);
-                f[j][k] = float(int(pv >> (8 * k) & 255) - 127);
+                f[j][k] = float(pv >> (8 * k) & 255) - r;
                 if (8 * j + 2 * t + k >= nv) x[j][k] = -INFINITY, f[j][k] = 0.f;
             }
         }
         // ---- weights
-        float p[2][2], w[2][2], most_p = 0.f, most_w = 0.f;
+        float p[2][2], w[2][2], most = 0.f;
         auto weigh = [&] {
 #pragma unroll
             for (int j = 0; j < 2; j++)
@@ -161,22 +165,34 @@ struct KvfState {
                 for (int k = 0; k < 2; k++) {
                     const float y = x[j][k] - m;
                     p[j][k] = ex2(y), w[j][k] = ex2(y + f[j][k]);
-                    most_p = fmaxf(most_p, p[j][k]), most_w = fmaxf(most_w, w[j][k]);
+                    most = fmaxf(most, fmaxf(p[j][k], w[j][k]));
                 }
         };
         weigh();
-        if (!__all_sync(0xffffffffu, most_p <= 2.028240960365167e31f && most_w <= 32768.f)) {  // 2^104
-            float mn = m;
+        if (!__all_sync(0xffffffffu, most <= 32768.f)) {
+            float mn = -INFINITY, top = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 2; j++)
 #pragma unroll
-                for (int k = 0; k < 2; k++) mn = fmaxf(mn, fmaxf(x[j][k] + f[j][k] - 8.f, x[j][k] - 100.f));
+                for (int k = 0; k < 2; k++) mn = fmaxf(mn, x[j][k]);
             mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 1));
-            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
-            const float down = ex2(m - mn);
-            m = mn, l *= down;
+            mn = fmaxf(m, ceilf(fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2))));
 #pragma unroll
-            for (int i = 0; i < ND; i++) o[i][0] *= down, o[i][1] *= down;
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int k = 0; k < 2; k++) top = fmaxf(top, x[j][k] - mn + f[j][k]);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // sums go down by 2^down, outputs by 2^(down - more)
+            const float down = fmaxf(m - mn, -1000.f), more = fmaxf(ceilf(top) - 9.f, down);
+            const float power = kvf_power(max(int(down - more) + 127, 0));
+            m = mn, r += more, l *= kvf_power(max(int(down) + 127, 0));
+#pragma unroll
+            for (int i = 0; i < ND; i++) o[i][0] *= power, o[i][1] *= power;
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int k = 0; k < 2; k++) f[j][k] -= more;
             weigh();
         }
         l += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
@@ -194,9 +210,9 @@ struct KvfState {
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 const int pair = t + 4 * j;
-                const uint4 r = *reinterpret_cast<const uint4 *>(part + 16 * D + pair * 2 * D +
+                const uint4 u = *reinterpret_cast<const uint4 *>(part + 16 * D + pair * 2 * D +
                                                                  kvf_value_chunk<D>(VC * g + v, pair) * 16);
-                y[j][0] = r.x, y[j][1] = r.y, y[j][2] = r.z, y[j][3] = r.w;
+                y[j][0] = u.x, y[j][1] = u.y, y[j][2] = u.z, y[j][3] = u.w;
                 if (nv < 16) {  // what lies past the end may be no number
                     const uint32_t keep = (2 * pair < nv ? 0x00ff00ffu : 0u) | (2 * pair + 1 < nv ? 0xff00ff00u : 0u);
 #pragma unroll
@@ -222,14 +238,15 @@ struct KvfState {
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         if (g >= a.group) return;
         const int64_t head0 = int64_t(row / a.num_kv_heads) * a.num_q_heads + int64_t(row % a.num_kv_heads) * a.group;
-        const float inv = !final ? 1.f : l > 0.f ? 1.f / l : 0.f;
+        const float inv = !final ? 1.f : l > 0.f ? 1.f / l : 0.f, power = kvf_power(uint32_t(r));
         float *dst = (final ? a.out + (head0 + g) * D : piece_o + g * D) + t * (D / 4);
 #pragma unroll
         for (int k = 0; k < 2; k++)
 #pragma unroll
             for (int i = 0; i < ND; i += 4)
                 *reinterpret_cast<float4 *>(dst + k * ND + i) =
-                    make_float4(o[i][k] * inv, o[i + 1][k] * inv, o[i + 2][k] * inv, o[i + 3][k] * inv);
+                    make_float4(o[i][k] * inv * power, o[i + 1][k] * inv * power, o[i + 2][k] * inv * power,
+                                o[i + 3][k] * inv * power);
         if (t == 0) {
             if (final) {
                 if (a.lse) a.lse[head0 + g] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
