@@ -565,9 +565,15 @@ qskv_status qskv_kvf_paged_decode(const void *q, qskv_dtype q_dtype, const void 
  * qskv_kvf_paged_decode (pool); what lies in slots past seq_len may be anything.
  * With fp32 queries, and with an fp32 cache, everything is kept in fp32 (the
  * products are sums of products of three bf16 parts each, within 2^-22).
+ * Every logit must then be below 2^126 in magnitude, and every sum over the
+ * dims of |q_i k_i| below 2^127.
  * With bf16 queries over a bf16 or 8-bit cache the products take bf16 operands
  * (softmax weights are rounded to bf16) and sum in fp32; every logit must then
- * be below 2^30 in magnitude, in fp32 below 2^126.
+ * be below 2^28 in magnitude (a weight is off by up to half of fp32's step at
+ * its logit, as a power of two: from there on weights beside large values
+ * would leave fp32's range).
+ * Queries, keys and values of tokens that count must be finite; values below
+ * 2^72 in magnitude (2^60 in the 8-bit cache).
  * Nothing is read before the previous kernel in the stream has completed.
  * Device errors: cu_new out of order or range, seq_len outside
  * [0, max_pages * page_size] or below n_b: clamped to what there is (a query
