@@ -383,21 +383,24 @@ class QuantizedPagedDecoder:
         that is refused (ValueError, TypeError, QskvError) leaves lengths,
         pages and cache as they were."""
         self._check_query(q)
-        self._extend_and_append(k, v, [1] * self.shape.batch if new_lens is None else new_lens, stream)
-        if self.top_k is not None:
-            self.select(q, stream)
-        self.decode(q, stream=stream)
-
-    def _extend_and_append(self, k, v, new_lens, stream):
-        """Both, or neither: lengths, pages and cache stay as they were if either is refused."""
-        lengths, taken = self.lengths, self._taken
-        self.extend(new_lens, stream)
-        try:
+        with self._undone_if_refused():
+            self.extend([1] * self.shape.batch if new_lens is None else new_lens, stream)
             self.append(k, v, stream)
+            if self.top_k is not None:
+                self.select(q, stream)
+            self.decode(q, stream=stream)
+
+    @contextlib.contextmanager
+    def _undone_if_refused(self):
+        """Lengths and pages as they were if a call within raises: of the table and the pool only places past a row's end
+        are new then, and the metadata of a row's last page still bounds its keys."""
+        names = ("lengths", "_taken", "_new", "seq_lens", "_lens_out")
+        before = [getattr(self, name) for name in names]
+        try:
+            yield
         except Exception:
-            # nothing is stored: the lengths as before, of the table only entries past them are new
-            self.seq_lens, self._lens_out = self._lens_out, self.seq_lens
-            self.lengths, self._taken, self._new = lengths, taken, 0
+            for name, value in zip(names, before):
+                setattr(self, name, value)
             raise
 
     def prefill(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, new_lens, out: Optional[torch.Tensor] = None,
@@ -415,6 +418,8 @@ class QuantizedPagedDecoder:
         B._rows("q", q, q.dtype, n, s.num_q_heads, s.head_dim, self.pool.get_device())
         if q.data_ptr() % 16 or (n > 1 and q.stride(0) * q.element_size() % 16):
             raise ValueError("the rows of q must be 16-byte aligned")
+        if n > 1 and q.stride(0) < s.num_q_heads * s.head_dim:
+            raise ValueError(f"the rows of q must not overlap (strides {q.stride()})")
         for name, t, want in (("out", out, (q.dtype, q.shape)), ("lse", lse, (torch.float32, q.shape[:2]))):
             if t is not None and ((t.dtype, t.shape) != want or t.get_device() != self.pool.get_device()
                                   or not t.is_contiguous() or t.data_ptr() % 16):
@@ -423,9 +428,11 @@ class QuantizedPagedDecoder:
         if out is None:
             with self._on(stream):
                 out = torch.empty(q.shape, dtype=q.dtype, device=self.pool.device)
-        self._extend_and_append(k, v, new_lens, stream)
-        B.kvf_paged_prefill(q, self.pool, self.page_table, self.seq_lens, self.cu_new, out, s, self.workspace, lse=lse,
-                            sm_scale=self.sm_scale, stream=stream)
+        with self._undone_if_refused():
+            self.extend(new_lens, stream)
+            self.append(k, v, stream)
+            B.kvf_paged_prefill(q, self.pool, self.page_table, self.seq_lens, self.cu_new, out, s, self.workspace, lse=lse,
+                                sm_scale=self.sm_scale, stream=stream)
         return out
 
     def gather(self, row: int, dtype=torch.float32, stream=None):
