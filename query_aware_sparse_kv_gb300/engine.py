@@ -422,9 +422,10 @@ class QuantizedPagedDecoder:
             raise ValueError(f"the rows of q must not overlap (strides {q.stride()})")
         for name, t, want in (("out", out, (q.dtype, q.shape)), ("lse", lse, (torch.float32, q.shape[:2]))):
             if t is not None and ((t.dtype, t.shape) != want or t.get_device() != self.pool.get_device()
-                                  or not t.is_contiguous() or t.data_ptr() % 16):
-                raise ValueError(f"{name} must be {want[0]} {tuple(want[1])}, contiguous, 16-byte aligned and on the "
-                                 f"decoder's device")
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name} must be {want[0]} {tuple(want[1])}, contiguous and on the decoder's device")
+        if out is not None and out.data_ptr() % 16:
+            raise ValueError("out must be 16-byte aligned")
         if out is None:
             with self._on(stream):
                 out = torch.empty(q.shape, dtype=q.dtype, device=self.pool.device)

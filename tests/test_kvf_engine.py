@@ -92,6 +92,17 @@ def test_tokens_that_extend_made_room_for_are_still_awaited_after_a_refusal(call
     assert dec.lengths == dec.seq_lens.tolist() == [2, 0, 1]
 
 
+def test_sums_at_any_place_of_a_longer_buffer(calls):
+    """lse of the prefill needs no more than its type's alignment, as the library's call has it."""
+    dec = _decoder(num_q_heads=2, num_kv_heads=2)
+    sums = torch.zeros((9, 2))
+    for at, n in ((0, 3), (3, 2)):
+        dec.prefill(torch.zeros((n, 2, D)), _tokens(n), _tokens(n), [n, 0, 0], lse=sums[at:at + n])
+        assert calls[-1][0] == "kvf_paged_prefill" and calls[-1][2]["lse"].data_ptr() == sums[at:].data_ptr()
+    with pytest.raises(ValueError, match="out"):
+        dec.prefill(torch.zeros((2, 2, D)), _tokens(2), _tokens(2), [2, 0, 0], out=torch.zeros(2 * 2 * D + 1)[1:].view(2, 2, D))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_a_refused_prefill_stores_nothing_on_the_gpu(dtype):
@@ -120,5 +131,3 @@ def test_a_refused_prefill_stores_nothing_on_the_gpu(dtype):
         ends.append((*outs, dec.out, dec.selected, *dec.gather(0), *dec.gather(1), *dec.gather(2)))
     for x, y in zip(*ends):
         assert torch.equal(x, y)
-
-
