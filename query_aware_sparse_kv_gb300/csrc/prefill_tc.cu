@@ -864,8 +864,7 @@ __device__ void list_role(const PrefillArgs &a, Shared &s, uint8_t *q, const CUt
     if (a.direct) s.line.make(a, s.rows);
     if ((threadIdx.x & 31) != 0) return;
     const int total = a.direct ? 0 : int(__ldcg(&a.plan->items)) * a.num_kv_heads, per = 128 / a.group;
-    int q_phase = 0;
-    bool q_used = false;
+    uint32_t loads = 0;  // of queries
     for (int i = 0;; i++) {
         const int next = a.direct ? 0 : int(atomicAdd(&a.plan->next, 1u));
         if (i >= 2 && !wait_phase(s, &s.item_empty[i & 1], (i >> 1 & 1) ^ 1, a.flags)) break;
@@ -884,11 +883,8 @@ __device__ void list_role(const PrefillArgs &a, Shared &s, uint8_t *q, const CUt
         mbar_arrive(&s.item_full[i & 1]);
         if (x.head < 0) break;
         if (x.item.block1 == x.item.block0) continue;
-        if (q_used) {
-            if (!wait_phase(s, &s.q_empty, q_phase, a.flags)) break;
-            q_phase ^= 1;
-        }
-        q_used = true;
+        if (loads && !wait_phase(s, &s.q_empty, (loads - 1) & 1, a.flags)) break;
+        loads++;
         const int halves = x.item.tokens > per ? 2 : 1;
         mbar_arrive_expect_tx(&s.q_full, halves * C::TILE);
         for (int h = 0; h < halves; h++)
@@ -896,6 +892,8 @@ __device__ void list_role(const PrefillArgs &a, Shared &s, uint8_t *q, const CUt
             for (int c = 0; c < C::NB; c++)
                 tma_load_3d(q + h * C::TILE + c * C::ATOM, map_q, c * 64, x.head * a.group, x.item.token + h * per, &s.q_full);
     }
+    // the last queries have landed before the CTA's memory is released, also where nobody waits for them any more
+    if (loads) mbar_wait_bounded(&s.q_full, (loads - 1) & 1, kWaitLimitNs);
 }
 
 template <int D, bool KVF>
