@@ -359,15 +359,14 @@ int64_t token_ctas(const KvfStoreArgs &a, int head_dim, int items) {
     return (int64_t(a.n_tokens) + per_cta - 1) / per_cta * a.num_kv_heads;
 }
 // Tokens a thread: with 2, 4 and 8 32768 tokens stored and read back take 70.8, 70.7 and 82.7 us, 131072 read back 119.8,
-// 132.4 and 142.1.  One a thread where that leaves fewer CTAs than SMs: 1200 tokens stored and read back in 5.9 us, with
-// one a thread 7.0; 600 in 5.2 and 4.9.
+// 132.4 and 142.1.  One a thread where several would leave SMs without a CTA: with one and with several, 32 tokens x 8 heads
+// stored and read back take 4.4 and 6.1 us, 600 4.9 and 5.3, 1200 7.2 and 6.1.
 constexpr int kAppendItems = 4, kGatherItems = 2;
-constexpr int64_t kManyCtas = 152;
 
 }  // namespace
 
-#define KVF_TOKENS(kernel, kItems)                                                                                  \
-    const bool bf16 = dtype == kDtypeBf16, many = token_ctas(a, head_dim, kItems) >= kManyCtas;                 \
+#define KVF_TOKENS(kernel, kItems)                                                                              \
+    const bool bf16 = dtype == kDtypeBf16, many = token_ctas(a, head_dim, kItems) >= num_sms;                   \
     const dim3 grid(unsigned(token_ctas(a, head_dim, many ? kItems : 1))), block(kCacheThreads);                \
     if (head_dim == 128) {                                                                                      \
         if (many) return bf16 ? launch_pdl(kernel<true, 128, kItems>, grid, block, 0, stream, a)                \
@@ -380,11 +379,11 @@ constexpr int64_t kManyCtas = 152;
     return bf16 ? launch_pdl(kernel<true, 64, 1>, grid, block, 0, stream, a)                                    \
                 : launch_pdl(kernel<false, 64, 1>, grid, block, 0, stream, a);
 
-cudaError_t launch_kvf_append(const KvfStoreArgs &a, int dtype, int head_dim, cudaStream_t stream) {
+cudaError_t launch_kvf_append(const KvfStoreArgs &a, int dtype, int head_dim, int num_sms, cudaStream_t stream) {
     KVF_TOKENS(kvf_append_kernel, kAppendItems)
 }
 
-cudaError_t launch_kvf_gather(const KvfStoreArgs &a, int dtype, int head_dim, cudaStream_t stream) {
+cudaError_t launch_kvf_gather(const KvfStoreArgs &a, int dtype, int head_dim, int num_sms, cudaStream_t stream) {
     KVF_TOKENS(kvf_gather_kernel, kGatherItems)
 }
 

@@ -1122,6 +1122,8 @@ qskv_status qskv_kvf_append(const void *k, const void *v, qskv_dtype kv_dtype, i
     if (n_tokens > 1 && (k_stride < row || v_stride < row || k_stride % vec || v_stride % vec))
         return fail(QSKV_ERR_INVALID_ARG,
                     "k_stride and v_stride must be at least num_kv_heads * head_dim and multiples of 16 bytes");
+    const int sms = current_sm_count(nullptr);
+    if (sms <= 0) return fail(QSKV_ERR_CUDA, "cannot query the current CUDA device");
     KvfStoreArgs a = {};
     a.k = k;
     a.v = v;
@@ -1134,7 +1136,7 @@ qskv_status qskv_kvf_append(const void *k, const void *v, qskv_dtype kv_dtype, i
     a.num_kv_heads = shape->num_kv_heads;
     a.page_size = shape->page_size;
     a.num_pool_pages = shape->num_pool_pages;
-    return launched(launch_kvf_append(a, kv_dtype, shape->head_dim, static_cast<cudaStream_t>(stream)),
+    return launched(launch_kvf_append(a, kv_dtype, shape->head_dim, sms, static_cast<cudaStream_t>(stream)),
                     "kvf_append launch");
 }
 
@@ -1151,6 +1153,8 @@ qskv_status qskv_kvf_gather(const void *pool, const int32_t *slots, int32_t n_to
     if (!aligned(pool, 16) || !aligned(k_out, 16) || !aligned(v_out, 16))
         return fail(QSKV_ERR_INVALID_ARG, "pool, k_out and v_out must be 16-byte aligned");
     if (!aligned(slots, 4)) return fail(QSKV_ERR_INVALID_ARG, "slots must be 4-byte aligned");
+    const int sms = current_sm_count(nullptr);
+    if (sms <= 0) return fail(QSKV_ERR_CUDA, "cannot query the current CUDA device");
     KvfStoreArgs a = {};
     a.k_out = k_out;
     a.v_out = v_out;
@@ -1161,7 +1165,7 @@ qskv_status qskv_kvf_gather(const void *pool, const int32_t *slots, int32_t n_to
     a.num_kv_heads = shape->num_kv_heads;
     a.page_size = shape->page_size;
     a.num_pool_pages = shape->num_pool_pages;
-    return launched(launch_kvf_gather(a, out_dtype, shape->head_dim, static_cast<cudaStream_t>(stream)),
+    return launched(launch_kvf_gather(a, out_dtype, shape->head_dim, sms, static_cast<cudaStream_t>(stream)),
                     "kvf_gather launch");
 }
 

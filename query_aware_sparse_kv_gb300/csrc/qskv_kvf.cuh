@@ -28,7 +28,6 @@
 namespace qskv {
 
 constexpr int kKvfPartTokens = 16;
-constexpr float kKvfTop = 448.f;
 constexpr int kKvfLowExp = -100, kKvfHighExp = 119;
 
 __host__ __device__ constexpr int kvf_part_bytes(int head_dim) { return kKvfPartTokens * (2 * head_dim + 2); }
@@ -71,8 +70,8 @@ struct KvfMetaArgs {
     int32_t n_list, num_kv_heads, page_size, num_pool_pages;
 };
 
-cudaError_t launch_kvf_append(const KvfStoreArgs &a, int dtype, int head_dim, cudaStream_t stream);
-cudaError_t launch_kvf_gather(const KvfStoreArgs &a, int dtype, int head_dim, cudaStream_t stream);
+cudaError_t launch_kvf_append(const KvfStoreArgs &a, int dtype, int head_dim, int num_sms, cudaStream_t stream);
+cudaError_t launch_kvf_gather(const KvfStoreArgs &a, int dtype, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_kvf_meta(const KvfMetaArgs &a, int meta_dtype, int head_dim, int num_sms, cudaStream_t stream);
 // The decode takes the argument block, the workspace and the grid of the 4-bit one; group_size is not used.
 cudaError_t launch_kvf_decode(KvqDecodeArgs a, int head_dim, int num_sms, cudaStream_t stream);
