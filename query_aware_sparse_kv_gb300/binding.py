@@ -581,7 +581,13 @@ def paged_prefill(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, p
     queries are q[cu_new[b]:cu_new[b + 1]] ([T][Hq][d] packed, bf16 or fp32,
     any token stride of whole 16 bytes), the last of its seq_lens[b] tokens.
     out [T][Hq][d] has q's type; rows behind cu_new[-1] stay as they were.
-    The workspace must hold prefill_workspace_size(shape, T) bytes."""
+    The workspace must hold prefill_workspace_size(shape, T) bytes.
+
+    fp32 queries, or an fp32 cache, keep everything in fp32.  With bf16
+    queries over a bf16 cache the softmax weights are rounded to bf16 before
+    they meet the values (their sum is not): outputs are then within 2^-8 of
+    the weighted sum of |v|, besides their own rounding, and not as exact as
+    a decode's of the same token."""
     lib = _lib or load()
     dev = _device("k_pool", k_pool)
     full = (shape.num_pool_pages, shape.num_kv_heads, shape.page_size, shape.head_dim)
@@ -594,7 +600,8 @@ def paged_prefill(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, p
 def kvf_paged_prefill(q: torch.Tensor, pool: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
                       cu_new: torch.Tensor, out: torch.Tensor, shape: Shape, workspace: torch.Tensor,
                       lse: Optional[torch.Tensor] = None, sm_scale: float = 0.0, stream=None):
-    """paged_prefill over the 8-bit cache."""
+    """paged_prefill over the 8-bit cache, with the same precision by q's type:
+    with fp32 queries as exact as kvf_paged_decode, with bf16 ones less so."""
     lib = _lib or load()
     dev = _device("pool", pool)
     _prefill(lib.qskv_kvf_paged_prefill, q, (_pool8_ptr(pool, shape, dev),), page_table, seq_lens, cu_new, out, shape,

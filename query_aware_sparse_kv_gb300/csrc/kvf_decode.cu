@@ -28,9 +28,10 @@
 // per lane until the row ends.
 //
 // One GB300, GPU time: 32 sequences x 8 KV heads x 128 pages of 16 tokens, 4
-// heads a group: 32.0 us (4.3 TB/s; the start and the fold are 6 us of it);
-// 4 x 65536..131072 tokens, 8 heads a group: 139 us (5.8 TB/s, 86 % of the copy
-// rate); two short rows: 6.5 us.
+// heads a group: 32.2 us (4.2 TB/s; the start and the fold are 6 us of it, and
+// of 152 SMs 104 have two rows, which they read at 91 % of an SM's share of the
+// copy rate, the others one); 4 x 65536..131072 tokens, 8 heads a group: 138 us
+// (5.9 TB/s, 87 % of the copy rate); two short rows: 6.5 us.
 #include "kvq_decode.cuh"
 #include "qskv_kvf.cuh"
 
@@ -269,6 +270,12 @@ struct KvfFormat {
 
 }  // namespace
 
+// The rules by which rows are split count units, here parts of 16 tokens, with the constants of the 4-bit decode.  What they
+// take over this cache (pages of 16 tokens, 4 heads a group), and what other splits do: 256 rows of 128 selected pages, a CTA
+// each, 32.2 us, evenly 37.0; 2048 rows of 7 pages, to warps, 17.2, evenly 29.0; 2560 rows of 1 to 32 pages, to warps, 78.6,
+// evenly 61.5 (there the rule costs); 8 rows of 32, 64, 128 pages, a CTA for every 32 places, 10.3, 13.3, 13.6, for every 16
+// 11.2, 11.5, 11.8, for every 64 10.3, 14.1, 17.3; 8 rows of 1024, 2048 selected pages, at most 16 CTAs each, 21.0, 30.2, at
+// most 8 26.0, 42.3, at most 64 19.0, 24.0.
 cudaError_t launch_kvf_decode(KvqDecodeArgs a, int head_dim, int num_sms, cudaStream_t stream) {
     if (head_dim == 128)
         return a.page_size == 16 ? launch_one<KvfFormat<128, 16>>(a, num_sms, stream)

@@ -23,7 +23,10 @@
 // heads of 64 dims, in 52 us (82 with fp32 FMAs); 6 of 2048 tokens, the same
 // heads, 0.96 ms (1.52), 32 heads of 128 dims over 8 3.5 ms (5.28; 59 TFLOP/s),
 // over an 8-bit cache 2.6 ms.  Outputs of the first are off by 1.1e-7 from
-// fp64, 2.4e-7 with fp32 FMAs.
+// fp64, 2.4e-7 with fp32 FMAs.  A tile's keys are one CTA's, one block after the
+// other, so few tokens over a long cache leave the GPU nearly idle: 4 rows of 1
+// to 4 tokens over 65536, 32 heads of 128 dims over 8, 6.9 ms over fp32 pages
+// (the bf16 kernel over bf16 pages, which cuts rows into parts: 0.17 ms).
 #include <cuda_fp16.h>
 
 #include "qskv_kvf.cuh"

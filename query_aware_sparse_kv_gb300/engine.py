@@ -42,7 +42,9 @@ class PagedDecoder:
     approx_epsilon  None: exact top-K; else the lossy top-K stops refining
                 once at most floor(epsilon * top_k) pages are undecided and
                 samples them from the threshold bucket (seed approx_seed)
-    prefill_tokens  queries that a ``prefill`` may bring (0: none)
+    prefill_tokens  queries that a ``prefill`` may bring (0: none); the
+                workspace then grows by room for parts of tiles, about 80 MB
+                with 128 dims
     """
 
     def __init__(self, q, k_pool, v_pool, page_table, seq_lens, top_k: Optional[int], sm_scale: float = 0.0,
@@ -90,7 +92,8 @@ class PagedDecoder:
         """Causal attention of the rows' newest tokens, whose keys and values
         are in the pools and counted by ``seq_lens``: row b's queries are
         q[cu_new[b]:cu_new[b + 1]] of q [T][Hq][d].  Into ``out`` (q's shape
-        and type; zeros to begin with if none is given), which is returned."""
+        and type; zeros to begin with if none is given), which is returned.
+        Precision goes by the types, as binding.paged_prefill says."""
         if q.shape[0] > self.prefill_tokens:
             raise ValueError(f"{q.shape[0]} queries, at most {self.prefill_tokens} a prefill (prefill_tokens)")
         if out is None:
@@ -255,7 +258,8 @@ class QuantizedPagedDecoder:
     max_pages   pages a row may hold
     max_tokens  new tokens a step may bring, all rows together
     top_k       pages kept per (row, KV head); None = all
-    bits        4 or 8 (group_size says nothing for 8)
+    bits        4 or 8 (group_size says nothing for 8; ``prefill`` needs 8,
+                whose workspace has about 80 MB for it with 128 dims)
     """
 
     def __init__(self, batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int, max_pages: int,
@@ -408,8 +412,10 @@ class QuantizedPagedDecoder:
         """Prompts, or chunks of them: the rows' new tokens stored, then the
         causal attention of all of them, q [sum(new_lens)][Hq][d], over what
         the rows hold (8-bit caches; all pages, whatever top_k).  Into ``out``
-        (q's shape and type), which is returned.  A call that is refused
-        leaves lengths, pages and cache as they were."""
+        (q's shape and type), which is returned.  With bf16 queries softmax
+        weights are rounded to bf16, which ``step`` does not do; fp32 queries
+        give ``step``'s precision.  A call that is refused leaves lengths,
+        pages and cache as they were."""
         if self.bits != 8:
             raise ValueError("prefill attends to 8-bit caches (bits=8)")
         new_lens = [int(x) for x in new_lens]
